@@ -142,6 +142,47 @@ FA_API fa_status fa_bwd_varlen(const void* q, const void* k, const void* v, cons
                         int causal, void* stream);
 
 /*
+ * Grouped heads over a packed batch: H query heads share Hk key/value heads
+ * (H a multiple of Hk), query head h reading key/value head h / (H / Hk).
+ * Forward and backward over whole prompts of different lengths, as
+ * fa_fwd_varlen and fa_bwd_varlen, with these differences:
+ *   q, o, dout, dq  bf16 [total, H, d];  k, v, dk, dv  bf16 [total, Hk, d]
+ *   lse        fp32 [H, total]: one value for each packed row
+ *   ldq, ldk, ldv   elements between consecutive rows of q, k and v (at least
+ *              heads·d, a multiple of 8), so that all three may be slices of
+ *              one projection's output; every other tensor is contiguous
+ *   cu_seqlens device int32 [nseq + 1], cu_seqlens[0] = 0, non-decreasing,
+ *              cu_seqlens[nseq] <= total: rows may be left behind the last
+ *              sequence (a buffer of fixed size).  Empty sequences are
+ *              allowed.  The library does not read it on the host.  Offsets
+ *              outside [0, total] and rows of a sequence past max_seqlen are
+ *              ignored: their results are unspecified, but no call reads or
+ *              writes outside its tensors.
+ *   zero_tail  rows behind the last sequence: 0 leaves every output as it was
+ *              there; otherwise o, dq, dk, dv become 0 and lse -infinity.
+ *   scale      finite and positive, else FA_ERR_SCALE.
+ * What stands in rows behind the last sequence or in another sequence
+ * (infinities, NaN) does not reach a sequence's results.  Within a sequence a
+ * key that the causal mask hides must be finite.  fa_bwd_grouped sums dK and
+ * dV over the query heads of a key/value head in a fixed order; dQ is summed
+ * by fp32 adds in memory whose order varies, so that two runs can differ in
+ * its last bits.  The current device of the calling thread is left as it was.
+ */
+FA_API fa_status fa_fwd_grouped(const void* q, const void* k, const void* v, void* o, float* lse,
+                                const int* cu_seqlens, int nseq, int max_seqlen, int total, int H, int Hk, int d,
+                                long long ldq, long long ldk, long long ldv, float scale, int causal, int zero_tail,
+                                void* stream);
+/* Workspace of fa_bwd_grouped: D [H, total], the fp32 dQ accumulator, and,
+ * where few long sequences would leave SMs idle, fp32 parts of dK and dV.
+ * 0 for arguments that fa_bwd_grouped rejects. */
+FA_API size_t fa_bwd_grouped_workspace_bytes(int nseq, int max_seqlen, int total, int H, int Hk, int d, int causal);
+FA_API fa_status fa_bwd_grouped(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                                const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                                size_t workspace_bytes, const int* cu_seqlens, int nseq, int max_seqlen, int total,
+                                int H, int Hk, int d, long long ldq, long long ldk, long long ldv, float scale,
+                                int causal, int zero_tail, void* stream);
+
+/*
  * Decode forward against a key/value cache, split along the cache ("LLM
  * Systems 22: Flash Attention", sections 5.1 and 5.2: Split-KV /
  * Flash-Decoding).  q, o: bf16 [B, Nq, H, d], the Nq (1 .. 8) newest tokens;

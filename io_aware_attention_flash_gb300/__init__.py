@@ -12,6 +12,8 @@ module allocates outputs and workspace and calls the binding.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _binding
@@ -20,11 +22,14 @@ from ._binding import (  # noqa: F401  (C-ABI names)
     fa_decode_workspace_bytes,
     fa_fwd_decode,
     fa_bwd,
+    fa_bwd_grouped,
+    fa_bwd_grouped_workspace_bytes,
     fa_bwd_varlen,
     fa_bwd_varlen_workspace_bytes,
     fa_bwd_workspace_bytes,
     fa_cta_order,
     fa_fwd,
+    fa_fwd_grouped,
     fa_fwd_varlen,
     fa_get_device_error,
     fa_selftest_wait_timeout,
@@ -36,6 +41,8 @@ __all__ = [
     "flash_attention", "FaError", "fa_fwd", "fa_bwd", "fa_fwd_varlen", "fa_bwd_varlen",
     "fa_bwd_workspace_bytes", "fa_bwd_varlen_workspace_bytes", "fa_get_device_error", "load_library",
     "attention_decode", "fa_fwd_decode", "fa_decode_workspace_bytes",
+    "attention_forward_grouped", "attention_backward_grouped", "flash_attention_grouped", "fa_fwd_grouped",
+    "fa_bwd_grouped", "fa_bwd_grouped_workspace_bytes",
 ]
 
 
@@ -118,3 +125,64 @@ class _FlashAttention(torch.autograd.Function):
 def flash_attention(q, k, v, causal: bool = False, scale=None):
     """Autograd-aware attention over bf16 [B,N,H,d] CUDA tensors."""
     return _FlashAttention.apply(q, k, v, causal, scale)
+
+
+# ---------------------------------------------------------------------------
+# Grouped heads over packed batches: H query heads share Hk key/value heads.
+# ---------------------------------------------------------------------------
+def _allocating_on(stream):
+    """What a call on `stream` allocates belongs to that stream, so that its
+    memory is not handed to another one while the kernels still use it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None, stream=None):
+    """Packed batch with grouped heads: q [T,H,d], k and v [T,Hk,d] (H a
+    multiple of Hk; slices of one wider projection are taken as they are).
+    Returns (o [T,H,d] bf16, lse [H,T] fp32); rows behind the last sequence
+    get o = 0, lse = -inf."""
+    with _allocating_on(stream):
+        o = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
+        lse = torch.empty((q.shape[1], q.shape[0]), device=q.device, dtype=torch.float32)
+    fa_fwd_grouped(q, k, v, o, lse, cu_seqlens, max_seqlen, causal, scale, stream, zero_tail=True)
+    return o, lse
+
+
+def attention_backward_grouped(q, k, v, o, dout, lse, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None,
+                               stream=None, workspace=None):
+    """Returns (dq [T,H,d], dk, dv [T,Hk,d]), zero in rows behind the last
+    sequence.  dk and dv are summed over the query heads that share them."""
+    T, H, d = q.shape
+    Hk = k.shape[1]
+    with _allocating_on(stream):
+        if workspace is None:
+            n = fa_bwd_grouped_workspace_bytes(cu_seqlens.numel() - 1, max_seqlen, T, H, Hk, d, causal)
+            workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
+        dq = torch.empty((T, H, d), device=q.device, dtype=torch.bfloat16)
+        dk, dv = (torch.empty((T, Hk, d), device=q.device, dtype=torch.bfloat16) for _ in range(2))
+    fa_bwd_grouped(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max_seqlen, causal, scale, stream,
+                   zero_tail=True)
+    return dq, dk, dv
+
+
+class _FlashAttentionGrouped(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens, max_seqlen, causal, scale):
+        o, lse = attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
+        ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
+        ctx.args = max_seqlen, causal, scale
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
+        grads = attention_backward_grouped(q, k, v, o, do.contiguous(), lse, cu_seqlens, *ctx.args)
+        return (*grads, None, None, None, None)
+
+
+def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None):
+    """Autograd-aware attention with grouped heads over a packed batch:
+    q [T,H,d], k and v [T,Hk,d], cu_seqlens int32 [nseq+1] on the device,
+    max_seqlen the longest sequence.  Returns o [T,H,d]."""
+    return _FlashAttentionGrouped.apply(q, k, v, cu_seqlens, max_seqlen, causal, scale)

@@ -26,6 +26,7 @@ STATUS_NAMES = {
 
 # Exported symbols and their C signatures (include/fa.h).
 _P, _I, _F, _Z, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64
+_L = ctypes.c_longlong
 SIGNATURES = {
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
@@ -41,6 +42,10 @@ SIGNATURES = {
     "fa_last_error_detail": (ctypes.c_char_p, []),
     "fa_bwd_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
     "fa_microbench": (_I, [_I, _I, ctypes.POINTER(ctypes.c_double), _P]),
+    "fa_fwd_grouped": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _L, _L, _L, _F, _I, _I, _P]),
+    "fa_bwd_grouped_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
+    "fa_bwd_grouped": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P, _I, _I, _I, _I, _I, _I, _L, _L, _L, _F, _I,
+                            _I, _P]),
     "fa_decode_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
     "fa_fwd_decode": (_I, [_P, _P, _P, _P, _P, _P, _Z, _I, _I, _I, _I, _I, _F, _I, _P]),
 }
@@ -126,6 +131,44 @@ def _scale(scale, d):
     return float(d) ** -0.5 if scale is None else float(scale)
 
 
+def _stream_of(stream, device) -> int:
+    """The given stream, or the current one of the tensors' device."""
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _on(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _int32(name: str, t: torch.Tensor, shape, device) -> None:
+    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+
+
+def _rows(name: str, t: torch.Tensor, rows: int, heads: int, d: int, device) -> int:
+    """Checks a bf16 [rows, heads, d] tensor whose rows may be further apart
+    than heads·d elements (a slice of a wider projection); returns the row
+    stride in elements."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16 (got {t.dtype}); fp32 and other types are not supported")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if tuple(t.shape) != (rows, heads, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, d)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    s0, s1, s2 = t.stride()
+    if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}: each row of {heads} heads of {d} must be contiguous (strides {t.stride()})")
+    if rows <= 1:
+        return heads * d
+    if s0 < heads * d or s0 % 8:
+        raise ValueError(f"{name}: rows must be a multiple of 8 elements and at least {heads * d} apart (stride {s0})")
+    return s0
+
+
 # ---------------------------------------------------------------------------
 # Entry points (same names as the C ABI)
 # ---------------------------------------------------------------------------
@@ -193,6 +236,50 @@ def fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max_
         _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _ptr(cu_seqlens), nseq, max_seqlen, T, H, d,
         _scale(scale, d), int(bool(causal)), _stream(stream)))
+
+
+def _grouped(q, k, v, cu_seqlens):
+    """Checks of q, k, v and cu_seqlens: (T, H, Hk, d, nseq, row strides)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T, H, d] and [T, Hk, d]")
+    T, H, d = q.shape
+    Hk = k.shape[1]
+    ld = _rows("q", q, T, H, d, q.device), _rows("k", k, T, Hk, d, q.device), _rows("v", v, T, Hk, d, q.device)
+    nseq = cu_seqlens.numel() - 1
+    _int32("cu_seqlens", cu_seqlens, (nseq + 1,), q.device)
+    return T, H, Hk, d, nseq, ld
+
+
+def fa_fwd_grouped(q, k, v, o, lse, cu_seqlens, max_seqlen: int, causal: bool, scale=None, stream=None,
+                   zero_tail: bool = False) -> None:
+    """q, o [T, H, d], k, v [T, Hk, d] (rows of q, k, v may be slices of wider
+    ones), lse fp32 [H, T]; query head h reads key/value head h // (H // Hk)."""
+    T, H, Hk, d, nseq, ld = _grouped(q, k, v, cu_seqlens)
+    _bf16("o", o, (T, H, d))
+    _f32("lse", lse, (H, T))
+    _on(q.device, o=o, lse=lse)
+    _check("fa_fwd_grouped", lib().fa_fwd_grouped(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), nseq,
+        max_seqlen, T, H, Hk, d, *ld, _scale(scale, d), bool(causal), bool(zero_tail), _stream_of(stream, q.device)))
+
+
+def fa_bwd_grouped_workspace_bytes(nseq: int, max_seqlen: int, total: int, H: int, Hk: int, d: int,
+                                   causal: bool) -> int:
+    return int(lib().fa_bwd_grouped_workspace_bytes(nseq, max_seqlen, total, H, Hk, d, bool(causal)))
+
+
+def fa_bwd_grouped(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max_seqlen: int, causal: bool,
+                   scale=None, stream=None, zero_tail: bool = False) -> None:
+    T, H, Hk, d, nseq, ld = _grouped(q, k, v, cu_seqlens)
+    for n, t, heads in (("o", o, H), ("dout", dout, H), ("dq", dq, H), ("dk", dk, Hk), ("dv", dv, Hk)):
+        _bf16(n, t, (T, heads, d))
+    _f32("lse", lse, (H, T))
+    _on(q.device, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, workspace=workspace)
+    _check("fa_bwd_grouped", lib().fa_bwd_grouped(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        cu_seqlens.data_ptr(), nseq, max_seqlen, T, H, Hk, d, *ld, _scale(scale, d), bool(causal), bool(zero_tail),
+        _stream_of(stream, q.device)))
 
 
 def fa_decode_workspace_bytes(B: int, H: int, Nq: int, Nk: int, d: int) -> int:

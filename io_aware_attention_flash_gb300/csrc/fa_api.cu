@@ -263,6 +263,122 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
   return e == cudaSuccess ? FA_OK : cuda_fail("backward launch", e);
 }
 
+// ----------------------------------------------------------------------------
+// Grouped heads over a packed batch
+// ----------------------------------------------------------------------------
+// The calling thread's current device as it was, whatever the call made current.
+class DeviceGuard {
+ public:
+  DeviceGuard() { ok_ = cudaGetDevice(&prev_) == cudaSuccess; }
+  ~DeviceGuard() {
+    if (ok_) cudaSetDevice(prev_);
+  }
+
+ private:
+  int prev_ = 0;
+  bool ok_ = false;
+};
+
+// bf16 tensor [rows, heads, d] whose rows are ld elements apart, as the 4-D
+// map of make_map (outer extent 1).
+fa_status make_map_ld(CUtensorMap* map, const void* ptr, int d, int heads, long long rows, long long ld) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cuda_fail("cuTensorMapEncodeTiled entry point not found", cudaErrorSymbolNotFound);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows), 1};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(ld) * 2,
+                                 static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[4] = {64, 1, static_cast<cuuint32_t>(fa::kTile), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    snprintf(t_detail, sizeof(t_detail), "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+// fp32 parts of dK and dV, [slabs, rows, heads, d], stored in boxes of 32
+// columns x 32 rows.
+fa_status make_map_parts(CUtensorMap* map, const void* ptr, int d, int heads, long long rows, int slabs) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cuda_fail("cuTensorMapEncodeTiled entry point not found", cudaErrorSymbolNotFound);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(slabs)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 4, static_cast<cuuint64_t>(heads) * d * 4,
+                                 static_cast<cuuint64_t>(rows) * heads * d * 4};
+  const cuuint32_t box[4] = {32, 1, 32, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    snprintf(t_detail, sizeof(t_detail), "cuTensorMapEncodeTiled (dK, dV parts) failed (CUresult %d)",
+             static_cast<int>(r));
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
+fa_status check_grouped(int nseq, int max_seqlen, int total, int H, int Hk, int d, float scale) {
+  FA_TRY(check_common(H, d, scale));
+  if (!(scale > 0.f)) return FA_ERR_SCALE;
+  if (Hk <= 0 || H % Hk != 0) return FA_ERR_SHAPE;
+  return check_rows(nseq, total, max_seqlen, H, d);
+}
+
+// Row strides: whole rows of `heads` heads, 16-byte multiples.
+bool stride_ok(long long ld, int heads, int d) {
+  return ld >= static_cast<long long>(heads) * d && ld % 8 == 0 && ld < (1LL << 36);
+}
+
+// Parts that the query heads of a key/value head are split into in the
+// backward: the smallest divisor of the group at which the heaviest CTA (key
+// tile 0 of the longest sequence: all its query tiles, for each head of the
+// part) takes at most half of one SM's share of the whole work, estimated as
+// total / max_seqlen sequences of max_seqlen rows on 152 SMs.  Each part costs
+// an fp32 dK, dV written and read again.
+int grouped_splits(int total, int max_seqlen, int H, int Hk, int causal) {
+  const int G = H / Hk;
+  const double nt = (max_seqlen + fa::kTile - 1) / fa::kTile;
+  const double nseq = total > max_seqlen ? static_cast<double>(total) / max_seqlen : 1.0;
+  const double share = nseq * H * (causal ? nt * (nt + 1) / 2 : nt * nt) / 152.0;
+  int s = 1;
+  while (s < G && (G % s != 0 || G / s * nt > 0.5 * share)) ++s;
+  return s;
+}
+
+struct GroupedWs {
+  size_t dq_off, part_off, bytes;
+  int splits;
+};
+
+GroupedWs grouped_ws(int total, int max_seqlen, int H, int Hk, int d, int causal) {
+  GroupedWs w{};
+  w.splits = grouped_splits(total, max_seqlen, H, Hk, causal);
+  const size_t rows128 = static_cast<size_t>((total + 127LL) / 128) * 128;
+  w.dq_off = pad256(static_cast<size_t>(total) * H * 4);
+  w.part_off = w.dq_off + rows128 * H * d * 4;
+  w.bytes = w.part_off + (w.splits > 1 ? static_cast<size_t>(2) * w.splits * total * Hk * d * 4 : 0);
+  return w;
+}
+
+fa::SeqView grouped_view(const int* cu, int nseq, int max_seqlen, int total, int H, int Hk, int zero_tail) {
+  fa::SeqView sv{};
+  sv.cu_seqlens = cu;
+  sv.H = H;
+  sv.N = total;
+  sv.G = H / Hk;
+  sv.Hk = Hk;
+  sv.nseq = nseq;
+  sv.max_seqlen = max_seqlen;
+  sv.splits = 1;
+  sv.zero_tail = zero_tail ? 1 : 0;
+  return sv;
+}
+
 // One CTA waits on an mbarrier that nothing arrives on, with a short limit.
 __global__ void fa_wait_timeout_selftest_kernel(uint32_t* err, uint64_t limit_ns) {
   __shared__ __align__(8) uint64_t barrier;
@@ -385,6 +501,91 @@ FA_API fa_status fa_bwd_varlen(const void* q, const void* k, const void* v, cons
   FA_TRY(check_rows(nseq, total, max_seqlen, H, d));
   return bwd_impl(q, k, v, o, dout, lse, dq, dk, dv, workspace, workspace_bytes, cu_seqlens, nseq, max_seqlen, total,
                   1, H, d, scale, causal, stream);
+}
+
+FA_API fa_status fa_fwd_grouped(const void* q, const void* k, const void* v, void* o, float* lse,
+                                const int* cu_seqlens, int nseq, int max_seqlen, int total, int H, int Hk, int d,
+                                long long ldq, long long ldk, long long ldv, float scale, int causal, int zero_tail,
+                                void* stream) {
+  FA_TRY(check_grouped(nseq, max_seqlen, total, H, Hk, d, scale));
+  if (!q || !k || !v || !o || !lse || !cu_seqlens) return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return FA_ERR_ALIGN;
+  if (!stride_ok(ldq, H, d) || !stride_ok(ldk, Hk, d) || !stride_ok(ldv, Hk, d)) return FA_ERR_SHAPE;
+  DeviceGuard guard;
+  FA_TRY(bind_device(q));
+  fa::FwdParams p{};
+  FA_TRY(error_word(&p.err));
+  CUtensorMap tq, tk, tv, to;
+  FA_TRY(make_map_ld(&tq, q, d, H, total, ldq));
+  FA_TRY(make_map_ld(&tk, k, d, Hk, total, ldk));
+  FA_TRY(make_map_ld(&tv, v, d, Hk, total, ldv));
+  FA_TRY(make_map(&to, o, d, H, total, 1, 32));
+  p.sv = grouped_view(cu_seqlens, nseq, max_seqlen, total, H, Hk, zero_tail);
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.causal = causal ? 1 : 0;
+  p.timeout_ns = kWaitLimitNs;
+  const cudaError_t e = fa::launch_fwd_grouped(d, tq, tk, tv, to, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail("grouped forward launch", e);
+}
+
+FA_API size_t fa_bwd_grouped_workspace_bytes(int nseq, int max_seqlen, int total, int H, int Hk, int d, int causal) {
+  if (check_grouped(nseq, max_seqlen, total, H, Hk, d, 1.0f) != FA_OK) return 0;
+  return grouped_ws(total, max_seqlen, H, Hk, d, causal).bytes;
+}
+
+FA_API fa_status fa_bwd_grouped(const void* q, const void* k, const void* v, const void* o, const void* dout,
+                                const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                                size_t workspace_bytes, const int* cu_seqlens, int nseq, int max_seqlen, int total,
+                                int H, int Hk, int d, long long ldq, long long ldk, long long ldv, float scale,
+                                int causal, int zero_tail, void* stream) {
+  FA_TRY(check_grouped(nseq, max_seqlen, total, H, Hk, d, scale));
+  if (!q || !k || !v || !o || !dout || !lse || !dq || !dk || !dv || !cu_seqlens) return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dout) || !aligned16(lse) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return FA_ERR_ALIGN;
+  if (!stride_ok(ldq, H, d) || !stride_ok(ldk, Hk, d) || !stride_ok(ldv, Hk, d)) return FA_ERR_SHAPE;
+  const GroupedWs w = grouped_ws(total, max_seqlen, H, Hk, d, causal);
+  if (!workspace || workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FA_ERR_ALIGN;
+  DeviceGuard guard;
+  FA_TRY(bind_device(q));
+  fa::BwdParams p{};
+  FA_TRY(error_word(&p.err));
+  p.sv = grouped_view(cu_seqlens, nseq, max_seqlen, total, H, Hk, zero_tail);
+  p.sv.splits = w.splits;
+  p.o = static_cast<const uint16_t*>(o);
+  p.dout = static_cast<const uint16_t*>(dout);
+  p.lse = lse;
+  p.dpsum = static_cast<float*>(workspace);
+  p.dq_accum = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.dq_off);
+  p.dkv_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_off);
+  p.dq = static_cast<uint16_t*>(dq);
+  p.dk = static_cast<uint16_t*>(dk);
+  p.dv = static_cast<uint16_t*>(dv);
+  p.scale = scale;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.causal = causal ? 1 : 0;
+  p.rows = total;
+  p.nseq = nseq;
+  p.timeout_ns = kWaitLimitNs;
+  CUtensorMap tq, tk, tv, tdo, tdq, tdk, tdv;
+  FA_TRY(make_map_ld(&tq, q, d, H, total, ldq));
+  FA_TRY(make_map_ld(&tk, k, d, Hk, total, ldk));
+  FA_TRY(make_map_ld(&tv, v, d, Hk, total, ldv));
+  FA_TRY(make_map(&tdo, dout, d, H, total, 1));
+  FA_TRY(make_map_dq(&tdq, p.dq_accum, d, H, total));
+  if (w.splits > 1) {
+    FA_TRY(make_map_parts(&tdk, p.dkv_part, d, Hk, total, 2 * w.splits));
+    tdv = tdk;
+  } else {
+    FA_TRY(make_map(&tdk, dk, d, Hk, total, 1, 32));
+    FA_TRY(make_map(&tdv, dv, d, Hk, total, 1, 32));
+  }
+  const cudaError_t e =
+      fa::launch_bwd_grouped(d, tq, tk, tv, tdo, tdq, tdk, tdv, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail("grouped backward launch", e);
 }
 
 FA_API size_t fa_decode_workspace_bytes(int B, int H, int Nq, int Nk, int d) {

@@ -64,7 +64,7 @@ __device__ __forceinline__ void locate_row(const SeqView& sv, int nseq, int g, i
 // 16-byte loads in flight per thread, enough to keep HBM busy at one load
 // round trip per thread).
 // ----------------------------------------------------------------------------
-template <int D>
+template <int D, bool GRP = false>
 __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdParams p) {
   grid_launch_dependents();  // the main kernel's prologue and first MMAs need nothing from here
   constexpr int TPR = D / 8;  // threads per (row, head); rows do not straddle warps (TPR divides 32)
@@ -93,6 +93,10 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdParams p) {
   for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
   if (live && part == 0) {
     const int g = static_cast<int>(rh / H), h = static_cast<int>(rh - (rh / H) * H);
+    if constexpr (GRP) {  // D [H, rows]
+      p.dpsum[static_cast<size_t>(h) * p.sv.N + g] = acc;
+      return;
+    }
     int bs, local;
     locate_row(p.sv, p.nseq, g, bs, local);
     p.dpsum[(static_cast<size_t>(bs) * H + h) * p.sv.lse_stride + local] = acc;
@@ -115,6 +119,54 @@ __global__ void __launch_bounds__(256) fa_bwd_post_kernel(const BwdParams p, siz
   w.z = pack_bf16x2(b.x * s, b.y * s);
   w.w = pack_bf16x2(b.z * s, b.w * s);
   reinterpret_cast<uint4*>(p.dq)[i] = w;
+}
+
+// ----------------------------------------------------------------------------
+// fa_bwd_post_grouped: the same for grouped heads, dK and dV as the sums of
+// their parts in the parts' order (threads past dQ's n8; no atomics, so the
+// sum does not depend on which CTA finished first), and the rows behind the
+// last sequence, which no main-kernel CTA writes.
+// ----------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_post_grouped_kernel(const BwdParams p, size_t n8) {
+  grid_dependency_wait();
+  const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  constexpr int C8 = D / 8;
+  const int end = packed_end(p.sv);
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  auto pack8 = [](const float4& a, const float4& b, float s) {
+    return make_uint4(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(a.z * s, a.w * s), pack_bf16x2(b.x * s, b.y * s),
+                      pack_bf16x2(b.z * s, b.w * s));
+  };
+  if (i < n8) {
+    const size_t row = i / (static_cast<size_t>(p.sv.H) * C8);
+    if (row < static_cast<size_t>(end)) {
+      const float4* acc = reinterpret_cast<const float4*>(p.dq_accum) + 2 * i;
+      reinterpret_cast<uint4*>(p.dq)[i] = pack8(acc[0], acc[1], p.scale);
+    } else if (p.sv.zero_tail) {
+      reinterpret_cast<uint4*>(p.dq)[i] = zero;
+      const size_t in_row = i - row * p.sv.H * C8;
+      if (in_row < static_cast<size_t>(p.sv.Hk) * C8) {
+        reinterpret_cast<uint4*>(p.dk)[row * p.sv.Hk * C8 + in_row] = zero;
+        reinterpret_cast<uint4*>(p.dv)[row * p.sv.Hk * C8 + in_row] = zero;
+      }
+    }
+    return;
+  }
+  const size_t n8kv = static_cast<size_t>(p.rows) * p.sv.Hk * C8;
+  const size_t j = i - n8;
+  if (p.sv.splits == 1 || j >= 2 * n8kv) return;  // past the last thread with work
+  const bool is_v = j >= n8kv;
+  const size_t e = is_v ? j - n8kv : j;
+  if (e / (static_cast<size_t>(p.sv.Hk) * C8) >= static_cast<size_t>(end)) return;
+  const float4* part = reinterpret_cast<const float4*>(p.dkv_part) + 2 * (n8kv * p.sv.splits * (is_v ? 1 : 0) + e);
+  float4 a = part[0], b = part[1];
+  for (int k = 1; k < p.sv.splits; ++k) {
+    const float4 x = part[2 * n8kv * k], y = part[2 * n8kv * k + 1];
+    a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+    b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+  }
+  reinterpret_cast<uint4*>(is_v ? p.dv : p.dk)[e] = pack8(a, b, is_v ? 1.0f : p.scale);
 }
 
 // ----------------------------------------------------------------------------
@@ -184,7 +236,19 @@ struct BwdCfg {
   static constexpr int B_DKDV = B_DQDRAINED + 1;
   static constexpr int B_DRAIN = B_DKDV + 1;
   static constexpr int B_STAT = B_DRAIN + 1;           // [2]: row statistics of a query tile staged
-  static constexpr int NBAR = B_STAT + 2;
+  // Grouped heads: rows past the sequence's end zeroed in K and V, and in the
+  // Q and dO of a ring slot.
+  static constexpr int B_CLEANKV = B_STAT + 2;
+  static constexpr int B_CLEANQ = B_CLEANKV + 1;       // [NSQ]
+  static constexpr int B_CLEANDO = B_CLEANQ + NSQ;     // [NSQ]
+  // [NSQ] each: the producer has issued the load of a ragged Q or dO tile into
+  // the slot.  The cleaner must not wait on the slot's own barrier before: it
+  // does not follow the slot's other tiles, and a parity that is one phase off
+  // reads as complete.  A slot's next ragged load comes only after the MMAs of
+  // this one, hence after its cleaning, so these never run a phase ahead.
+  static constexpr int B_RAGQ = B_CLEANDO + NSQ;
+  static constexpr int B_RAGDO = B_RAGQ + NSQ;
+  static constexpr int NBAR = B_RAGDO + NSQ;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_USED = OFF_MISC + 16;
   // Whatever is left of the 227 KB opt-in limit is alignment slack.
@@ -229,7 +293,17 @@ struct BwdCfg {
   static_assert(!DS_IN_DO || (NCHT - NCH_STG) * 4 * 4096 <= TILE_BYTES, "dQ half fits over a dO tile");
 };
 
-template <int D>
+// GRP: grouped heads over a packed batch.  A CTA owns one key tile of one
+// key/value head and loops over the query tiles of all query heads of its part
+// of the group (heads outer, query tiles inner, one ring and one TMEM dK, dV
+// throughout), so a key/value head's gradient is summed on chip.  With few
+// sequences the heaviest such CTA outlasts the rest, so the group's heads may
+// be split into parts (BwdParams::sv.splits), each writing an fp32 dK, dV of
+// its own that the conversion sums.  Tiles that run past the sequence's end
+// hold other rows, whose infinities or NaNs would reach the products of the
+// sequence's own rows (0 · NaN): warp 14, which has no role otherwise, zeroes
+// those rows in shared memory before the first MMA reads them.
+template <int D, bool GRP = false>
 __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -256,30 +330,63 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
   int pair, j;                        // j: key tile; heavy (small j) tiles first under a causal mask
   cta_item(p.sv, pair, j);
   if (pair >= p.sv.npairs) return;
-  const SeqPos sp = seq_pos(p.sv, pair);
+  SeqPos sp;
+  int hk, part = 0, nh = 1;           // key/value head; part of its query heads and how many those are
+  if constexpr (GRP) {
+    const int per_seq = p.sv.Hk * p.sv.splits;
+    clamp_seq(p.sv, pair / per_seq, sp);
+    const int rem = pair % per_seq;
+    hk = rem / p.sv.splits;
+    part = rem - hk * p.sv.splits;
+    nh = p.sv.G / p.sv.splits;
+    sp.h = hk * p.sv.G + part * nh;   // first query head
+  } else {
+    sp = seq_pos(p.sv, pair);
+    hk = sp.h;
+  }
   const int kv0 = j * kTile;
   if (kv0 >= sp.seqlen) return;
   const int nq_total = (sp.seqlen + kTile - 1) / kTile;
   const int i_first = p.causal ? j : 0;
-  const int nq = nq_total - i_first;
+  const int nq_h = nq_total - i_first;  // query tiles of one head
+  const int nq = GRP ? nq_h * nh : nq_h;
+  // Query head and query tile of loop index ii.
+  auto item = [&](int ii, int& h, int& qi) {
+    if constexpr (GRP) {
+      const int hh = static_cast<int>(static_cast<uint32_t>(ii) / static_cast<uint32_t>(nq_h));
+      h = sp.h + hh;
+      qi = i_first + ii - hh * nq_h;
+    } else {
+      h = sp.h;
+      qi = i_first + ii;
+    }
+  };
+  const bool kv_ragged = GRP && kv0 + kTile > sp.seqlen;          // this key tile runs past the end
+  const bool q_ragged = GRP && nq_total * kTile > sp.seqlen;      // the last query tile does
 
   // TMA issue of query tile ii's Q and dO into ring slot ii % NSQ (producer
   // thread).
   auto load_q = [&](int ii) {
     const int qs = ii % C::NSQ;
-    const int qrow = sp.tma_row0 + (i_first + ii) * kTile;
+    int h, qi;
+    item(ii, h, qi);
+    const int qrow = sp.tma_row0 + qi * kTile;
     mbar_arrive_expect_tx(bar(C::B_QFULL + qs), C::TILE_BYTES);
     for (int kb = 0; kb < C::KB; ++kb)
-      tma_load_4d(sb + C::OFF_Q + qs * C::TILE_BYTES + kb * C::BLK_BYTES, &tmQ, bar(C::B_QFULL + qs), kb * 64, sp.h,
+      tma_load_4d(sb + C::OFF_Q + qs * C::TILE_BYTES + kb * C::BLK_BYTES, &tmQ, bar(C::B_QFULL + qs), kb * 64, h,
                   qrow, sp.tma_b);
+    if (q_ragged && qi == nq_total - 1) mbar_arrive(bar(C::B_RAGQ + qs));
   };
   auto load_do = [&](int ii) {
     const int qs = ii % C::NSQ;
-    const int qrow = sp.tma_row0 + (i_first + ii) * kTile;
+    int h, qi;
+    item(ii, h, qi);
+    const int qrow = sp.tma_row0 + qi * kTile;
     mbar_arrive_expect_tx(bar(C::B_DOFULL + qs), C::TILE_BYTES);
     for (int kb = 0; kb < C::KB; ++kb)
       tma_load_4d(sb + C::OFF_DO + qs * C::TILE_BYTES + kb * C::BLK_BYTES, &tmdO, bar(C::B_DOFULL + qs), kb * 64,
-                  sp.h, qrow, sp.tma_b);
+                  h, qrow, sp.tma_b);
+    if (q_ragged && qi == nq_total - 1) mbar_arrive(bar(C::B_RAGDO + qs));
   };
   // K, V and the query tiles whose ring slots start empty are loaded by the
   // producer as soon as it has initialised the barriers, so the first loads
@@ -308,6 +415,15 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
     mbar_init(bar(C::B_DRAIN), 1);
     mbar_init(bar(C::B_STAT + 0), C::NUM_COMPUTE);
     mbar_init(bar(C::B_STAT + 1), C::NUM_COMPUTE);
+    if constexpr (GRP) {
+      mbar_init(bar(C::B_CLEANKV), 32);
+      for (int s = 0; s < C::NSQ; ++s) {
+        mbar_init(bar(C::B_CLEANQ + s), 32);
+        mbar_init(bar(C::B_CLEANDO + s), 32);
+        mbar_init(bar(C::B_RAGQ + s), 1);
+        mbar_init(bar(C::B_RAGDO + s), 1);
+      }
+    }
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
@@ -321,11 +437,11 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
     // dO_0 (dPᵀ_0), then the rest of the ring.
     mbar_arrive_expect_tx(bar(C::B_K), C::TILE_BYTES);
     for (int kb = 0; kb < C::KB; ++kb)
-      tma_load_4d(sb + C::OFF_K + kb * C::BLK_BYTES, &tmK, bar(C::B_K), kb * 64, sp.h, sp.tma_row0 + kv0, sp.tma_b);
+      tma_load_4d(sb + C::OFF_K + kb * C::BLK_BYTES, &tmK, bar(C::B_K), kb * 64, hk, sp.tma_row0 + kv0, sp.tma_b);
     if (preloaded > 0) load_q(0);
     mbar_arrive_expect_tx(bar(C::B_V), C::TILE_BYTES);
     for (int kb = 0; kb < C::KB; ++kb)
-      tma_load_4d(sb + C::OFF_V + kb * C::BLK_BYTES, &tmV, bar(C::B_V), kb * 64, sp.h, sp.tma_row0 + kv0, sp.tma_b);
+      tma_load_4d(sb + C::OFF_V + kb * C::BLK_BYTES, &tmV, bar(C::B_V), kb * 64, hk, sp.tma_row0 + kv0, sp.tma_b);
     if (preloaded > 0) load_do(0);
     for (int ii = 1; ii < preloaded; ++ii) {
       load_q(ii);
@@ -340,8 +456,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const size_t stat_base = (static_cast<size_t>(sp.bs) * p.sv.H + sp.h) * p.sv.lse_stride;
-  const size_t row_stride = static_cast<size_t>(p.sv.H) * D;  // elements between consecutive rows
+  const size_t stat_base = GRP ? static_cast<size_t>(sp.row_base)
+                               : (static_cast<size_t>(sp.bs) * p.sv.H + sp.h) * p.sv.lse_stride;
+  const size_t row_stride = static_cast<size_t>(GRP ? p.sv.Hk : p.sv.H) * D;  // elements between dK, dV rows
 
   if (warp == C::PRODUCER_WARP) {
     // ---------------------------------------------------------------- TMA
@@ -355,12 +472,14 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
       // read; d = 64: dV_t has read dO_t).
       auto reduce_chunks = [&](int t, int c_lo, int c_hi) {
         const int qs = t % C::NSQ;
-        const int q0 = (i_first + t) * kTile;
+        int h, qi;
+        item(t, h, qi);
+        const int q0 = qi * kTile;
 #pragma unroll 1
         for (int wq = 0; wq < 4; ++wq) {
 #pragma unroll
           for (int c = c_lo; c < c_hi; ++c)
-            tma_reduce_add_3d(&tmDQ, sb + C::dq_slice(qs, c, wq), 32 * c, sp.h, sp.row_base + q0 + 32 * wq);
+            tma_reduce_add_3d(&tmDQ, sb + C::dq_slice(qs, c, wq), 32 * c, h, sp.row_base + q0 + 32 * wq);
         }
         bulk_commit_group();
       };
@@ -431,14 +550,26 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
           mma_ss(dst, sdesc_add(a, koff), sdesc_add(b, koff), idesc_sp, kk > 0);
         }
       };
+      // Grouped heads: the zeroed rows of ragged tiles (one phase of a slot's
+      // barrier for each ragged tile in it; phases counted in the masks).
+      uint32_t clean_q = 0, clean_do = 0;
+      int to_last = nq_h - 1;  // query tiles until the head's last
+      auto wait_clean = [&](int b0, uint32_t& phases, int slot) -> bool {
+        const uint32_t ph = (phases >> slot) & 1u;
+        phases ^= 1u << slot;
+        return wait_bounded(bar(b0 + slot), ph, abort_flag, p.err, p.timeout_ns);
+      };
       bool ok = wait_bounded(bar(C::B_K), 0, abort_flag, p.err, p.timeout_ns) &&
                 wait_bounded(bar(C::B_QFULL + 0), 0, abort_flag, p.err, p.timeout_ns);
+      if (GRP && ok && kv_ragged) ok = wait_bounded(bar(C::B_CLEANKV), 0, abort_flag, p.err, p.timeout_ns);
+      if (GRP && ok && q_ragged && to_last == 0) ok = wait_clean(C::B_CLEANQ, clean_q, 0);
       if (ok) {
         tc_fence_after();
         issue_sp(region(0), kmK, kmQ);                                     // Sᵀ_0 -> X
         tc_commit(bar(C::B_SFULL));
         ok = wait_bounded(bar(C::B_V), 0, abort_flag, p.err, p.timeout_ns) &&
              wait_bounded(bar(C::B_DOFULL + 0), 0, abort_flag, p.err, p.timeout_ns);
+        if (GRP && ok && q_ragged && to_last == 0) ok = wait_clean(C::B_CLEANDO, clean_do, 0);
       }
       if (ok) {
         tc_fence_after();
@@ -452,6 +583,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
         const uint64_t aDS = sdesc_sw128(sb + C::ds_base(qs), C::BLK_BYTES, 1024);  // dS, MN-major
         const uint64_t kDS = sdesc_sw128(sb + C::ds_base(qs), 16, 1024);            // dSᵀ, K-major
         const bool next = ii + 1 < nq;
+        if (GRP) to_last = to_last == 0 ? nq_h - 1 : to_last - 1;  // of tile ii + 1
         const int qs1 = (ii + 1) % C::NSQ;
         const uint32_t ph1 = ((ii + 1) / C::NSQ) & 1;
         ok = wait_bounded(bar(C::B_PREADY), ii & 1, abort_flag, p.err, p.timeout_ns);
@@ -464,6 +596,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
         tc_commit(bar(C::DS_IN_DO ? C::B_DVDONE : C::B_DOFREE + qs));  // dO_i read: dS (or the next dO) may go there
         if (next) {
           ok = wait_bounded(bar(C::B_QFULL + qs1), ph1, abort_flag, p.err, p.timeout_ns);
+          if (GRP && ok && q_ragged && to_last == 0) ok = wait_clean(C::B_CLEANQ, clean_q, qs1);
           if (!ok) break;
           tc_fence_after();
           issue_sp(tX, kmK, sdesc_add(kmQ, qs1 * C::TILE_BYTES));               // Sᵀ_{i+1} -> X (after dV_i)
@@ -487,6 +620,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
           ok = wait_bounded(bar(C::B_DQDRAINED), ii & 1, abort_flag, p.err, p.timeout_ns);
           if (!ok) break;
           ok = wait_bounded(bar(C::B_DOFULL + qs1), ph1, abort_flag, p.err, p.timeout_ns);
+          if (GRP && ok && q_ragged && to_last == 0) ok = wait_clean(C::B_CLEANDO, clean_do, qs1);
           if (!ok) break;
           tc_fence_after();
           issue_sp(tY, kmV, sdesc_add(kmDO, qs1 * C::TILE_BYTES));              // dPᵀ_{i+1} -> Y
@@ -498,7 +632,48 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
       wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
     }
   } else if (warp >= C::DRAIN_WARP0 + 4) {
-    setmaxnreg_dec<C::REG_OTHER>();        // warps 14-15: no role
+    setmaxnreg_dec<C::REG_OTHER>();        // warps 14-15: no role, but for warp 14 under grouped heads
+    if (GRP && warp == C::DRAIN_WARP0 + 4) {
+      // Zeroes rows n .. 127 of a 128-row tile (whole 128-byte rows of each
+      // 64-column block, so the swizzle does not matter).
+      auto zero_rows = [&](uint32_t off, int n) {
+        for (int i = n * 8 + lane; i < kTile * 8; i += 32)
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+            reinterpret_cast<uint4*>(smem + off + kb * C::BLK_BYTES)[i] = make_uint4(0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+      };
+      bool ok = true;
+      if (kv_ragged) {
+        ok = wait_bounded(bar(C::B_K), 0, abort_flag, p.err, p.timeout_ns) &&
+             wait_bounded(bar(C::B_V), 0, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          zero_rows(C::OFF_K, sp.seqlen - kv0);
+          zero_rows(C::OFF_V, sp.seqlen - kv0);
+          mbar_arrive(bar(C::B_CLEANKV));
+        }
+      }
+      const int n_last = sp.seqlen - (nq_total - 1) * kTile;  // rows of the last query tile
+      uint32_t ragged_phases = 0;  // of a slot's B_RAGQ and B_RAGDO alike
+      for (int hh = 0; q_ragged && ok && hh < nh; ++hh) {
+        const int ii = hh * nq_h + nq_h - 1, qs = ii % C::NSQ;
+        const uint32_t ph = (ii / C::NSQ) & 1, ph_rag = (ragged_phases >> qs) & 1;
+        ragged_phases ^= 1u << qs;
+        ok = wait_bounded(bar(C::B_RAGQ + qs), ph_rag, abort_flag, p.err, p.timeout_ns) &&
+             wait_bounded(bar(C::B_QFULL + qs), ph, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        zero_rows(C::OFF_Q + qs * C::TILE_BYTES, n_last);
+        mbar_arrive(bar(C::B_CLEANQ + qs));
+        ok = wait_bounded(bar(C::B_RAGDO + qs), ph_rag, abort_flag, p.err, p.timeout_ns) &&
+             wait_bounded(bar(C::B_DOFULL + qs), ph, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        zero_rows(C::OFF_DO + qs * C::TILE_BYTES, n_last);
+        mbar_arrive(bar(C::B_CLEANDO + qs));
+      }
+    }
   } else if (warp >= C::DRAIN_WARP0) {
     // ---------------------------------------------------------------- dQ drain
     setmaxnreg_dec<C::REG_OTHER>();
@@ -538,15 +713,32 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
       const int qs = ii % C::NSQ;
       if (ii > 0 && !wait_bounded(bar(C::B_STGFREE), (ii - 1) & 1, abort_flag, p.err, p.timeout_ns)) break;
       uint32_t a[2][32];
+      // Grouped heads: a row past the sequence's end is dS = 0 times this
+      // sequence's K, NaN where that has one, and it is added to a row of the
+      // next sequence: written as zeros.
+      bool dead = false;
+      if (GRP && q_ragged) {
+        int h, qi;
+        item(ii, h, qi);
+        dead = qi * kTile + 32 * wq + lane >= sp.seqlen;
+      }
+      auto drop_dead = [&]() {
+        if (GRP && dead) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[0][e] = a[1][e] = 0u;
+        }
+      };
 #pragma unroll
       for (int c0 = 0; c0 < C::NCH_STG; c0 += 2) {
         load_pair(rs, c0, a);
+        drop_dead();
         stage_chunk(a[0], sb + C::dq_slice(qs, c0, wq));
         stage_chunk(a[1], sb + C::dq_slice(qs, c0 + 1, wq));
       }
       if constexpr (C::NCHT > C::NCH_STG) {
         if (!wait_bounded(bar(C::B_QFREE + qs), (ii / C::NSQ) & 1, abort_flag, p.err, p.timeout_ns)) break;
         load_pair(rs, C::NCH_STG, a);
+        drop_dead();
         stage_chunk(a[0], sb + C::dq_slice(qs, C::NCH_STG, wq));
         stage_chunk(a[1], sb + C::dq_slice(qs, C::NCH_STG + 1, wq));
       }
@@ -576,9 +768,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
     // load before then (scaling it by log2 e here would stall the warp for
     // the load's latency on every tile).
     auto load_stat = [&](int ii) -> float {
-      const int q = (i_first + ii) * kTile + r;
+      int h, qi;
+      item(ii, h, qi);
+      const int q = qi * kTile + r;
       if (q >= sp.seqlen) return g == 0 ? CUDART_INF_F : 0.f;
-      return __ldg((g == 0 ? p.lse : p.dpsum) + stat_base + q);
+      const size_t at = GRP ? static_cast<size_t>(h) * p.sv.N + stat_base + q : stat_base + q;
+      return __ldg((g == 0 ? p.lse : p.dpsum) + at);
     };
     // Both warpgroups read all 128 entries of a tile (log2e·LSE and D):
     // publish them through an mbarrier (a bounded wait, unlike a named
@@ -600,7 +795,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
     bool ok = true;
     for (int ii = 0; ii < nq; ++ii) {
       const float stat_after = ii + 2 < nq ? load_stat(ii + 2) : 0.f;
-      const int qi = i_first + ii;
+      int h_unused, qi;
+      item(ii, h_unused, qi);
       const int q0 = qi * kTile;
       const uint32_t rs = lane_addr + C::R_COL;        // region X: Sᵀ, Pᵀ
       const uint32_t rp = lane_addr + C::R_COL + 128;  // region Y: dPᵀ
@@ -709,11 +905,52 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
       // its sequence's end is written row by row (a box would overwrite the
       // next sequence's rows).
       tc_fence_after();
+      if (GRP && p.sv.splits > 1) {
+        // One of several parts: fp32 rows, unscaled, 32 columns at a time
+        // through the same stage (4 KB a warp), stored as above.
+        const bool via_tma = kv0 + 32 * wq + 32 <= sp.seqlen;
+        const uint32_t stage = sb + (g == 0 ? C::OFF_K : C::OFF_V) + wq * 4096;
+        const size_t slab = (static_cast<size_t>(g) * p.sv.splits + part) * p.rows;
+        float* dst = p.dkv_part + (slab + sp.row_base + kv_row) * row_stride + static_cast<size_t>(hk) * D;
+        const uint32_t src = lane_addr + (g == 0 ? C::DK_COL : C::DV_COL);
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t v[32];
+          tmem_ld32(src + cb * 32, v);
+          tmem_wait_ld();
+          reg_fence(v);
+          if (via_tma) {
+            if (cb > 0) {
+              if (lane == 0) bulk_wait_group_read0();
+              __syncwarp();
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const uint32_t chunk = u ^ (lane & 7);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + chunk * 16),
+                           "r"(v[4 * u]), "r"(v[4 * u + 1]), "r"(v[4 * u + 2]), "r"(v[4 * u + 3])
+                           : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              // (column, head, row of the part's slab, dK or dV and part)
+              tma_store_4d(&tmDK, stage, cb * 32, hk, sp.row_base + kv0 + 32 * wq, g * p.sv.splits + part);
+              bulk_commit_group();
+            }
+          } else if (!row_dead) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              reinterpret_cast<uint4*>(dst + cb * 32)[u] = make_uint4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+          }
+        }
+        if (via_tma && lane == 0) bulk_wait_group_read0();
+      } else {
       const float mul = g == 0 ? p.scale : 1.0f;
       const bool via_tma = !p.sv.cu_seqlens || kv0 + 32 * wq + 32 <= sp.seqlen;
       const uint32_t stage = sb + (g == 0 ? C::OFF_K : C::OFF_V);
       uint16_t* dst = (g == 0 ? p.dk : p.dv) + (static_cast<size_t>(sp.row_base) + kv_row) * row_stride +
-                      static_cast<size_t>(sp.h) * D;
+                      static_cast<size_t>(hk) * D;
       const uint32_t src = lane_addr + (g == 0 ? C::DK_COL : C::DV_COL);
 #pragma unroll 1
       for (int cb = 0; cb < D / 64; ++cb) {  // 64 columns (one 128-byte swizzle block) per TMEM round trip
@@ -752,11 +989,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
         if (lane == 0 && kv0 + 32 * wq < sp.seqlen) {
 #pragma unroll
           for (int kb = 0; kb < C::KB; ++kb)
-            tma_store_4d(g == 0 ? &tmDK : &tmDV, stage + kb * C::BLK_BYTES + wq * 4096, kb * 64, sp.h,
+            tma_store_4d(g == 0 ? &tmDK : &tmDV, stage + kb * C::BLK_BYTES + wq * 4096, kb * 64, hk,
                          sp.tma_row0 + kv0 + 32 * wq, sp.tma_b);
           bulk_commit_group();
           bulk_wait_group_read0();  // the stage may be released once the copies have read it
         }
+      }
       }
     }
   }
@@ -768,20 +1006,20 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
   }
 }
 
-template <int D>
+template <int D, bool GRP = false>
 cudaError_t launch_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                          const CUtensorMap& tdq, const CUtensorMap& tdk, const CUtensorMap& tdv, const BwdParams& p,
                          int max_seqlen, cudaStream_t s, cudaEvent_t ev0, cudaEvent_t ev1) {
   using C = BwdCfg<D>;
   static SmemLimit smem_limit;
-  cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_bwd_main_kernel<D>), C::SMEM_BYTES);
+  cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_bwd_main_kernel<D, GRP>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   // The compute warpgroups' setmaxnreg increase is served from the registers
   // the CTA launched with; if the compiler gave the kernel fewer than the
   // split assumes, the increase would never be granted, so refuse to launch.
   static const int launch_regs = [] {
     cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, fa_bwd_main_kernel<D>) == cudaSuccess ? fa.numRegs : -1;
+    return cudaFuncGetAttributes(&fa, fa_bwd_main_kernel<D, GRP>) == cudaSuccess ? fa.numRegs : -1;
   }();
   if (launch_regs * C::NUM_THREADS <
       C::NUM_COMPUTE * C::REG_COMPUTE + (C::NUM_THREADS - C::NUM_COMPUTE) * C::REG_OTHER)
@@ -790,14 +1028,14 @@ cudaError_t launch_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   e = current_sm_count(sms);
   if (e != cudaSuccess) return e;
   BwdParams pm = p;
-  pm.sv.npairs = p.nseq * p.sv.H;
+  pm.sv.npairs = p.nseq * (GRP ? p.sv.Hk * p.sv.splits : p.sv.H);
   pm.sv.ntiles = (max_seqlen + kTile - 1) / kTile;
   pm.sv.pair_group = pair_group_size(pm.sv.npairs, pm.sv.ntiles, sms);  // one CTA per SM
   const long long ctas = grid_ctas(pm.sv.npairs, pm.sv.ntiles, pm.sv.pair_group);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(ctas));
   const long long pairs = static_cast<long long>(p.rows) * p.sv.H;
-  fa_bwd_pre_kernel<D><<<static_cast<unsigned>((pairs * (D / 8) + 255) / 256), 256, 0, s>>>(p);
+  fa_bwd_pre_kernel<D, GRP><<<static_cast<unsigned>((pairs * (D / 8) + 255) / 256), 256, 0, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (ev0 && (e = cudaEventRecord(ev0, s)) != cudaSuccess) return e;
@@ -805,16 +1043,29 @@ cudaError_t launch_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   // while the main kernel's last CTAs run (each waits for its predecessor
   // before reading what it wrote).  An event recorded between two kernels
   // (timing the main kernel alone) keeps them apart.
-  e = launch_kernel(fa_bwd_main_kernel<D>, grid, dim3(C::NUM_THREADS), C::SMEM_BYTES, s, ev0 == nullptr, tq, tk, tv,
+  e = launch_kernel(fa_bwd_main_kernel<D, GRP>, grid, dim3(C::NUM_THREADS), C::SMEM_BYTES, s, ev0 == nullptr, tq, tk, tv,
                     tdo, tdq, tdk, tdv, pm);
   if (e != cudaSuccess) return e;
   if (ev1 && (e = cudaEventRecord(ev1, s)) != cudaSuccess) return e;
   const size_t n8 = static_cast<size_t>(pairs) * D / 8;
+  if constexpr (GRP) {
+    const size_t n8kv = p.sv.splits > 1 ? static_cast<size_t>(p.rows) * p.sv.Hk * (D / 8) * 2 : 0;
+    return launch_kernel(fa_bwd_post_grouped_kernel<D>, dim3(static_cast<unsigned>((n8 + n8kv + 255) / 256)), dim3(256),
+                         0, s, ev1 == nullptr, p, n8);
+  }
   return launch_kernel(fa_bwd_post_kernel, dim3(static_cast<unsigned>((n8 + 255) / 256)), dim3(256), 0, s,
                        ev1 == nullptr, p, n8);
 }
 
 }  // namespace
+
+cudaError_t launch_bwd_grouped(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& tdo, const CUtensorMap& tdq, const CUtensorMap& tdk,
+                               const CUtensorMap& tdv, const BwdParams& p, cudaStream_t s) {
+  if (d == 64)
+    return launch_bwd_d<64, true>(tq, tk, tv, tdo, tdq, tdk, tdv, p, p.sv.max_seqlen, s, nullptr, nullptr);
+  return launch_bwd_d<128, true>(tq, tk, tv, tdo, tdq, tdk, tdv, p, p.sv.max_seqlen, s, nullptr, nullptr);
+}
 
 cudaError_t launch_bwd(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& tdo, const CUtensorMap& tdq, const CUtensorMap& tdk,

@@ -83,7 +83,25 @@ struct FwdCfg {
   static_assert(MIN_BLOCKS * (SMEM_BYTES + 1024) <= 233472, "shared memory for the CTAs of one SM");
 };
 
-template <int D, int NQT_>
+// Rows behind the last packed sequence: O = 0, LSE = -inf, shared out over the
+// grid's CTAs row by row (grouped heads; thread tid of nthreads).
+template <int D>
+__device__ __forceinline__ void zero_tail_rows(const FwdParams& p, int tid, int nthreads) {
+  const int end = packed_end(p.sv);
+  for (int row = end + blockIdx.x; row < p.sv.N; row += gridDim.x) {
+    uint4* o = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(row) * p.sv.H * D);
+    for (int i = tid; i < p.sv.H * (D / 8); i += nthreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int h = tid; h < p.sv.H; h += nthreads) p.lse[static_cast<size_t>(h) * p.sv.N + row] = -CUDART_INF_F;
+  }
+}
+
+// GRP: grouped heads over a packed batch.  K and V come from key/value head
+// h / G (the CTAs of a group's heads run next to one another and share the
+// K/V tiles in L2).  A tile that runs past its sequence's end holds the next
+// sequence's rows, or what lies behind the last one: its scores are masked,
+// and its V rows are zeroed in shared memory, since a probability of 0 times
+// an infinity or NaN there would not be 0.
+template <int D, int NQT_, bool GRP = false>
 __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>::MIN_BLOCKS)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -103,12 +121,19 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
   const int lane = threadIdx.x & 31;
   int pair, tile;
   cta_item(p.sv, pair, tile);
-  if (pair >= p.sv.npairs) return;
-  const SeqPos sp = seq_pos(p.sv, pair);
+  if (pair >= p.sv.npairs) {
+    if (GRP && p.sv.zero_tail) zero_tail_rows<D>(p, threadIdx.x, C::NUM_THREADS);
+    return;
+  }
+  const SeqPos sp = GRP ? seq_pos_grouped(p.sv, pair) : seq_pos(p.sv, pair);
+  const int hk = GRP ? sp.h / p.sv.G : sp.h;  // key/value head
   // Causal: the last query tiles see the most keys, so they go first.
   const int ctile = p.causal ? p.sv.ntiles - 1 - tile : tile;
   const int q0 = ctile * kTile * NQT;
-  if (q0 >= sp.seqlen) return;  // whole CTA past the end of a short packed sequence
+  if (q0 >= sp.seqlen) {  // whole CTA past the end of a short packed sequence
+    if (GRP && p.sv.zero_tail) zero_tail_rows<D>(p, threadIdx.x, C::NUM_THREADS);
+    return;
+  }
 
   const int nkv_total = (sp.seqlen + kTile - 1) / kTile;
   int nkv[NQT];
@@ -132,14 +157,14 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
     mbar_arrive_expect_tx(bar(C::B_KFULL + ks), C::TILE_BYTES);
     for (int kb = 0; kb < C::KB; ++kb)
       tma_load_4d(sb + C::OFF_K + ks * C::TILE_BYTES + kb * C::BLK_BYTES, &tmK, bar(C::B_KFULL + ks), kb * 64,
-                  sp.h, sp.tma_row0 + j * kTile, sp.tma_b);
+                  hk, sp.tma_row0 + j * kTile, sp.tma_b);
   };
   auto load_v = [&](int j) {
     const int vs = j % C::NSV;
     mbar_arrive_expect_tx(bar(C::B_VFULL + vs), C::TILE_BYTES);
     for (int kb = 0; kb < C::KB; ++kb)
       tma_load_4d(sb + C::OFF_V + vs * C::TILE_BYTES + kb * C::BLK_BYTES, &tmV, bar(C::B_VFULL + vs), kb * 64,
-                  sp.h, sp.tma_row0 + j * kTile, sp.tma_b);
+                  hk, sp.tma_row0 + j * kTile, sp.tma_b);
   };
   // K/V tiles whose ring slots start empty: loaded by the producer as soon as
   // it has initialised the barriers, so the first loads overlap the TMEM
@@ -308,6 +333,10 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
     // This warp's tile's key count, computed rather than read from nkv[] with
     // a run-time index (which would put the array in local memory).
     const int nkv_t = qt >= sp.seqlen ? 0 : (p.causal ? min(nkv_total, qt / kTile + 1) : nkv_total);
+    if (GRP && p.sv.zero_tail) zero_tail_rows<D>(p, threadIdx.x, 128 * NQT);  // while the first tiles arrive
+    // Grouped heads: one warpgroup zeroes the last key tile's V rows past the
+    // sequence's end, the one whose O += P V comes first on that tile.
+    const bool zero_v = GRP && (t == 0 || (p.causal && q0 / kTile + 1 < nkv_total));
     if (nkv_t > 0) {
       const float c = p.scale_log2;
       const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -392,7 +421,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
         // below 2^40 and O in fp32 range.
         if (j == 0) m_ref = row_max();
         float lt = p_pass();
-        if (__any_sync(0xffffffffu, !(lt < 0x1p40f))) {
+        if (__any_sync(0xffffffffu, !(lt < 0x1p40f) && (!GRP || q_row < sp.seqlen))) {
           const float m_new = fmaxf(m_ref, row_max());
           const float alpha = (m_ref == -CUDART_INF_F) ? 0.f : ex2_approx((m_ref - m_new) * c);
           m_ref = m_new;
@@ -412,6 +441,22 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
           lt = p_pass();
         }
         l += lt;
+        if (GRP && zero_v && kv0 + kTile > sp.seqlen) {
+          const int vs = j % C::NSV;
+          if (!wait_bounded(bar(C::B_VFULL + vs), (j / C::NSV) & 1, abort_flag, p.err, p.timeout_ns)) {
+            ok = false;
+            break;
+          }
+          if (kv0 + r >= sp.seqlen) {
+            uint8_t* vrow = smem + C::OFF_V + vs * C::TILE_BYTES + r * 128;
+#pragma unroll
+            for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                reinterpret_cast<uint4*>(vrow + kb * C::BLK_BYTES)[u] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(bar(C::B_PFULL + t));
@@ -463,7 +508,9 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
         }
         if (store) {
           const float lse = l > 0.f ? (m_ref * c + log2f(l)) * kLn2 : -CUDART_INF_F;
-          p.lse[(static_cast<size_t>(sp.bs) * p.sv.H + sp.h) * p.sv.lse_stride + q_row] = lse;
+          const size_t at = GRP ? static_cast<size_t>(sp.h) * p.sv.N + sp.row_base + q_row
+                                : (static_cast<size_t>(sp.bs) * p.sv.H + sp.h) * p.sv.lse_stride + q_row;
+          p.lse[at] = lse;
         }
         if (via_tma) {
           // Each warp stores its own 32 rows (a 32-row box whose 1024-byte
@@ -494,12 +541,12 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
   }
 }
 
-template <int D, int NQT>
+template <int D, int NQT, bool GRP = false>
 cudaError_t launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                          const FwdParams& p, int nseq, int max_seqlen, cudaStream_t s) {
   using C = FwdCfg<D, NQT>;
   static SmemLimit smem_limit;
-  cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_fwd_kernel<D, NQT>), C::SMEM_BYTES);
+  cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_fwd_kernel<D, NQT, GRP>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   int sms = 0;
   e = current_sm_count(sms);
@@ -510,7 +557,7 @@ cudaError_t launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   pl.sv.pair_group = pair_group_size(pl.sv.npairs, pl.sv.ntiles, sms * C::MIN_BLOCKS);
   const long long ctas = grid_ctas(pl.sv.npairs, pl.sv.ntiles, pl.sv.pair_group);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  fa_fwd_kernel<D, NQT><<<static_cast<unsigned>(ctas), C::NUM_THREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, to, pl);
+  fa_fwd_kernel<D, NQT, GRP><<<static_cast<unsigned>(ctas), C::NUM_THREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, to, pl);
   return cudaGetLastError();
 }
 
@@ -520,6 +567,12 @@ cudaError_t launch_fwd(int d, const CUtensorMap& tq, const CUtensorMap& tk, cons
                        const CUtensorMap& to, const FwdParams& p, int nseq, int max_seqlen, cudaStream_t s) {
   if (d == 64) return launch_fwd_d<64, 1>(tq, tk, tv, to, p, nseq, max_seqlen, s);
   return launch_fwd_d<128, 2>(tq, tk, tv, to, p, nseq, max_seqlen, s);
+}
+
+cudaError_t launch_fwd_grouped(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& to, const FwdParams& p, cudaStream_t s) {
+  if (d == 64) return launch_fwd_d<64, 1, true>(tq, tk, tv, to, p, p.sv.nseq, p.sv.max_seqlen, s);
+  return launch_fwd_d<128, 2, true>(tq, tk, tv, to, p, p.sv.nseq, p.sv.max_seqlen, s);
 }
 
 }  // namespace fa

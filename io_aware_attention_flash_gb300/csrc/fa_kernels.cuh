@@ -25,6 +25,13 @@ struct SeqView {
   int npairs;             // (sequence, head) pairs: nseq·H
   int ntiles;             // tiles of the launch's kind along the longest sequence
   int pair_group;         // pairs per launch group (pair_group_size)
+  // Grouped heads (packed batches only; lse and D are then [H, N] over the N packed rows):
+  int G;                  // query heads per key/value head
+  int Hk;                 // key/value heads, H / G
+  int nseq;
+  int max_seqlen;         // rows of a sequence past it are ignored
+  int splits;             // backward: parts that a key/value head's query heads are split into
+  int zero_tail;          // rows behind the last sequence: 1 writes zeros (LSE: -inf), 0 leaves them
 };
 
 // CTA order.  A CTA's work item is a (sequence·head pair, tile), and CTAs
@@ -140,6 +147,7 @@ struct BwdParams {
   int causal;
   int rows;               // B*N (dense) or total (packed): rows of the [rows, H, d] view
   int nseq;               // B (dense) or nseq (packed)
+  float* dkv_part;        // grouped heads in several parts: fp32 [2 (dK, dV), splits, rows, Hk, d]
   uint32_t* err;
   uint64_t timeout_ns;
 };
@@ -185,6 +193,30 @@ __device__ __forceinline__ SeqPos seq_pos(const SeqView& sv, int pair) {
   return s;
 }
 
+// Position of a (sequence, query head) pair under grouped heads.  Offsets that
+// do not fit the buffers are clamped to them, so that no cu_seqlens makes a
+// kernel leave its tensors; query head h reads key/value head h / G.
+__device__ __forceinline__ void clamp_seq(const SeqView& sv, int bs, SeqPos& s) {
+  s.bs = bs;
+  const int a = min(max(__ldg(sv.cu_seqlens + bs), 0), sv.N);
+  const int b = min(max(__ldg(sv.cu_seqlens + bs + 1), a), sv.N);
+  s.seq_start = s.row_base = s.tma_row0 = a;
+  s.seqlen = min(b - a, sv.max_seqlen);
+  s.tma_b = 0;
+}
+
+__device__ __forceinline__ SeqPos seq_pos_grouped(const SeqView& sv, int pair) {
+  SeqPos s;
+  clamp_seq(sv, pair / sv.H, s);
+  s.h = pair % sv.H;
+  return s;
+}
+
+// First row behind the last sequence.
+__device__ __forceinline__ int packed_end(const SeqView& sv) {
+  return min(max(__ldg(sv.cu_seqlens + sv.nseq), 0), sv.N);
+}
+
 // Launch with or without programmatic stream serialisation (the kernel may
 // start before the previous kernel in the stream has finished; it orders its
 // dependent reads with grid_dependency_wait).
@@ -207,6 +239,11 @@ inline cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, 
 // Grid sizes / launches (defined next to the kernels).
 cudaError_t launch_fwd(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& to, const FwdParams& p, int nseq, int max_seqlen, cudaStream_t s);
+cudaError_t launch_fwd_grouped(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& to, const FwdParams& p, cudaStream_t s);
+cudaError_t launch_bwd_grouped(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                               const CUtensorMap& tdo, const CUtensorMap& tdq, const CUtensorMap& tdk,
+                               const CUtensorMap& tdv, const BwdParams& p, cudaStream_t s);
 cudaError_t launch_bwd(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                        const CUtensorMap& tdo, const CUtensorMap& tdq, const CUtensorMap& tdk,
                        const CUtensorMap& tdv, const BwdParams& p, int max_seqlen,
