@@ -76,6 +76,7 @@ enum {
   FA_ERR_WORKSPACE = 8,     /* workspace missing or smaller than required */
   FA_ERR_SCALE = 9,         /* scale not finite */
   FA_ERR_NOT_DEVICE = 10,   /* q is not device memory (its device is the one launched on) */
+  FA_ERR_PAGE = 12,         /* a page table entry, length or start position out of range (device side) */
   FA_ERR_SCRATCH_LIMIT = 11 /* fa_bwd_noalloc: problem needs more than FA_NOALLOC_SCRATCH_BYTES */
 };
 
@@ -203,11 +204,73 @@ FA_API fa_status fa_fwd_decode(const void* q, const void* k, const void* v, void
                                void* stream);
 
 /*
+ * Paged key/value cache in 8 bits.  K and V are two pools of pages,
+ *   k_codes, v_codes  e4m3 (1 byte) [num_blocks, Hk, block, d], block one of
+ *                     16, 32, 64, 128 tokens
+ *   k_scale, v_scale  fp32 [num_blocks, Hk]: the value of a code is
+ *                     code · scale; scales are powers of two
+ *   block_table       int32 [B, table_cols]: the page of each run of `block`
+ *                     tokens of a sequence (token t is slot t mod block of
+ *                     page block_table[b][t / block])
+ * A page's scale for a head is the smallest power of two s, at least 2^-64,
+ * with |x| <= 448 s for every finite value stored in it, and never less than
+ * what the page's earlier tokens needed.  Values are rounded to the nearest
+ * e4m3 value of x / s (ties to even); infinities become ±448 s, NaN stays NaN.
+ * Pages may be shared for reading (a common beginning); a page that is written
+ * belongs to one sequence.
+ *
+ * fa_cache8_store appends new tokens: rows cu_seqlens[b] .. cu_seqlens[b+1]−1
+ * of k and v (bf16 [total, Hk, d], rows ldk and ldv elements apart as in
+ * fa_fwd_grouped) become tokens start[b], start[b] + 1, … of sequence b.
+ *   cu_seqlens  device int32 [B + 1], non-decreasing, within [0, total]
+ *   start       device int32 [B]: tokens cached before
+ *   max_new     largest number of new tokens of a sequence (further ones are
+ *               dropped)
+ * Where a page's earlier tokens (slots below start[b] mod block) were stored
+ * at a smaller scale than the new ones need, they are rounded again at the new
+ * scale; where start[b] is the page's first token, nothing that the page held
+ * before counts.  Slots behind the last new token are left as they were.
+ * A page index outside [0, num_blocks), a block past table_cols or a negative
+ * start is skipped and reported by fa_get_device_error as FA_ERR_PAGE.
+ */
+FA_API fa_status fa_cache8_store(const void* k, const void* v, void* k_codes, void* v_codes, float* k_scale,
+                                 float* v_scale, const int* block_table, const int* cu_seqlens, const int* start,
+                                 int B, int max_new, int total, int num_blocks, int table_cols, int Hk, int block,
+                                 int d, long long ldk, long long ldv, void* stream);
+
+/*
+ * Attention of the Nq (1 .. 8) newest tokens of each sequence over the cache,
+ * H query heads over Hk key/value heads (query head h reads h / (H / Hk)).
+ *   q, o     bf16 [B, Nq, H, d];  lse fp32 [B, H, Nq]
+ *   seqlens  device int32 [B]: cached tokens, the new ones among them; 0 for
+ *            a slot without a sequence (o = 0, lse = -infinity there)
+ *   max_seqlen  at least every length
+ * causal as in fa_fwd_decode: query i sees keys j <= seqlens[b] − Nq + i.
+ * Scores and sums are fp32 (each query and each probability is split into two
+ * e4m3 factors, whose product with the codes is exact to about 2^-9 of a
+ * probability and 2^-24 of the largest query element).  What cache slots
+ * behind a sequence's last token hold does not matter; stored tokens must be
+ * finite.  A page index out of range reads as a page of zeros, a length
+ * outside [0, min(max_seqlen, table_cols · block)] as the nearer end of that
+ * range, and both are reported by fa_get_device_error as FA_ERR_PAGE.  Results
+ * do not depend on the order in which CTAs run.  `workspace`: at least
+ * fa_decode_cache8_workspace_bytes(B, Nq, H, Hk, max_seqlen, d) bytes, contents
+ * ignored; calls that may overlap need one each.
+ */
+FA_API size_t fa_decode_cache8_workspace_bytes(int B, int Nq, int H, int Hk, int max_seqlen, int d);
+FA_API fa_status fa_fwd_decode_cache8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                                      const float* v_scale, const int* block_table, const int* seqlens, void* o,
+                                      float* lse, void* workspace, size_t workspace_bytes, int B, int Nq, int H,
+                                      int Hk, int num_blocks, int table_cols, int block, int max_seqlen, int d,
+                                      float scale, int causal, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the error word of the device
  * the stream belongs to (NULL, the legacy default stream: the current
  * device); the calling thread's current device is left as it was.  Returns
  * FA_OK, FA_ERR_TIMEOUT (some kernel's bounded mbarrier wait ran out and the
- * kernel returned early: its outputs are invalid) or FA_ERR_CUDA (the
+ * kernel returned early: its outputs are invalid), FA_ERR_PAGE (the 8-bit
+ * cache's entry points met an index out of range) or FA_ERR_CUDA (the
  * synchronisation or the read itself failed).
  */
 FA_API fa_status fa_get_device_error(void* stream);

@@ -13,6 +13,7 @@ module allocates outputs and workspace and calls the binding.
 from __future__ import annotations
 
 import contextlib
+from typing import NamedTuple
 
 import torch
 
@@ -27,8 +28,11 @@ from ._binding import (  # noqa: F401  (C-ABI names)
     fa_bwd_varlen,
     fa_bwd_varlen_workspace_bytes,
     fa_bwd_workspace_bytes,
+    fa_cache8_store,
     fa_cta_order,
+    fa_decode_cache8_workspace_bytes,
     fa_fwd,
+    fa_fwd_decode_cache8,
     fa_fwd_grouped,
     fa_fwd_varlen,
     fa_get_device_error,
@@ -42,7 +46,8 @@ __all__ = [
     "fa_bwd_workspace_bytes", "fa_bwd_varlen_workspace_bytes", "fa_get_device_error", "load_library",
     "attention_decode", "fa_fwd_decode", "fa_decode_workspace_bytes",
     "attention_forward_grouped", "attention_backward_grouped", "flash_attention_grouped", "fa_fwd_grouped",
-    "fa_bwd_grouped", "fa_bwd_grouped_workspace_bytes",
+    "fa_bwd_grouped", "fa_bwd_grouped_workspace_bytes", "Cache8", "cache8_alloc", "cache8_store",
+    "attention_decode_cache8", "fa_cache8_store", "fa_fwd_decode_cache8", "fa_decode_cache8_workspace_bytes",
 ]
 
 
@@ -186,3 +191,47 @@ def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool =
     q [T,H,d], k and v [T,Hk,d], cu_seqlens int32 [nseq+1] on the device,
     max_seqlen the longest sequence.  Returns o [T,H,d]."""
     return _FlashAttentionGrouped.apply(q, k, v, cu_seqlens, max_seqlen, causal, scale)
+
+
+# ---------------------------------------------------------------------------
+# Paged key/value cache in 8 bits.
+# ---------------------------------------------------------------------------
+class Cache8(NamedTuple):
+    """Pools of e4m3 pages [num_blocks, Hk, block, d] and their scales fp32
+    [num_blocks, Hk] (powers of two; the value of a code is code · scale)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def cache8_alloc(num_blocks: int, Hk: int, block: int, d: int, device="cuda") -> Cache8:
+    """An empty cache of num_blocks pages of `block` tokens (16, 32, 64 or 128)."""
+    pages = [torch.zeros((num_blocks, Hk, block, d), device=device, dtype=torch.uint8).view(torch.float8_e4m3fn)
+             for _ in range(2)]
+    return Cache8(*pages, *(torch.ones((num_blocks, Hk), device=device) for _ in range(2)))
+
+
+def cache8_store(k, v, cache: Cache8, block_table, cu_seqlens, start, max_new: int, stream=None) -> None:
+    """Appends new tokens to the cache: rows cu_seqlens[b] .. cu_seqlens[b+1]-1
+    of k, v [T,Hk,d] become tokens start[b], start[b]+1, ... of sequence b,
+    in the pages block_table [B,cols] names (int32, as cu_seqlens [B+1] and
+    start [B]); max_new is the largest number of new tokens of a sequence."""
+    fa_cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new, stream)
+
+
+def attention_decode_cache8(q, cache: Cache8, block_table, seqlens, max_seqlen: int, causal: bool = False, scale=None,
+                            stream=None, workspace=None):
+    """Decode over the 8-bit paged cache: q [B,Nq,H,d] (Nq <= 8 newest tokens),
+    seqlens int32 [B] cached tokens (the new ones among them; 0 for an empty
+    slot), max_seqlen at least every length.  Returns (o [B,Nq,H,d] bf16, lse
+    [B,H,Nq] fp32).  causal as in attention_decode."""
+    B, Nq, H, d = q.shape
+    with _allocating_on(stream):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            n = fa_decode_cache8_workspace_bytes(B, Nq, H, cache.k.shape[1], max_seqlen, d)
+            workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
+    fa_fwd_decode_cache8(q, cache, block_table, seqlens, o, lse, workspace, max_seqlen, causal, scale, stream)
+    return o, lse

@@ -22,6 +22,7 @@ STATUS_NAMES = {
     0: "FA_OK", 1: "FA_ERR_NULL", 2: "FA_ERR_ALIGN", 3: "FA_ERR_HEAD_DIM", 4: "FA_ERR_SHAPE",
     5: "FA_ERR_ARCH", 6: "FA_ERR_CUDA", 7: "FA_ERR_TIMEOUT", 8: "FA_ERR_WORKSPACE", 9: "FA_ERR_SCALE",
     10: "FA_ERR_NOT_DEVICE", 11: "FA_ERR_SCRATCH_LIMIT",
+    12: "FA_ERR_PAGE",
 }
 
 # Exported symbols and their C signatures (include/fa.h).
@@ -46,6 +47,9 @@ SIGNATURES = {
     "fa_bwd_grouped_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I, _I]),
     "fa_bwd_grouped": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P, _I, _I, _I, _I, _I, _I, _L, _L, _L, _F, _I,
                             _I, _P]),
+    "fa_cache8_store": (_I, [_P] * 9 + [_I] * 8 + [_L, _L, _P]),
+    "fa_decode_cache8_workspace_bytes": (_Z, [_I] * 6),
+    "fa_fwd_decode_cache8": (_I, [_P] * 10 + [_Z] + [_I] * 9 + [_F, _I, _P]),
     "fa_decode_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
     "fa_fwd_decode": (_I, [_P, _P, _P, _P, _P, _P, _Z, _I, _I, _I, _I, _I, _F, _I, _P]),
 }
@@ -280,6 +284,73 @@ def fa_bwd_grouped(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max
         dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         cu_seqlens.data_ptr(), nseq, max_seqlen, T, H, Hk, d, *ld, _scale(scale, d), bool(causal), bool(zero_tail),
         _stream_of(stream, q.device)))
+
+
+def _cache8(cache, device):
+    """Checks of a cache's four tensors: (num_blocks, Hk, block, d)."""
+    k, v, k_scale, v_scale = cache
+    if k.dim() != 4:
+        raise ValueError("cache pages must be [num_blocks, Hk, block, d]")
+    shape = k.shape
+    for name, t in (("cache.k", k), ("cache.v", v)):
+        if t.dtype != torch.float8_e4m3fn:
+            raise TypeError(f"{name} must be float8_e4m3fn (got {t.dtype})")
+        if t.device != device or not t.is_contiguous() or t.shape != shape:
+            raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
+    for name, t in (("cache.k_scale", k_scale), ("cache.v_scale", v_scale)):
+        if t.dtype != torch.float32 or t.device != device or not t.is_contiguous() or t.shape != shape[:2]:
+            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape[:2])} on {device}")
+    return shape
+
+
+def fa_cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new: int, stream=None) -> None:
+    """Appends k, v [T, Hk, d] (rows may be slices of wider ones) to the cache
+    (k, v, k_scale, v_scale): rows cu_seqlens[b] .. of sequence b become its
+    tokens start[b], start[b] + 1, ..."""
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hk, d]")
+    device = k.device
+    T, Hk, d = k.shape
+    ldk, ldv = _rows("k", k, T, Hk, d, device), _rows("v", v, T, Hk, d, device)
+    num_blocks, heads, block, dim = _cache8(cache, device)
+    if (heads, dim) != (Hk, d):
+        raise ValueError(f"the cache holds {heads} heads of {dim}, k and v have {Hk} of {d}")
+    B, cols = block_table.shape
+    _int32("block_table", block_table, (B, cols), device)
+    _int32("cu_seqlens", cu_seqlens, (B + 1,), device)
+    _int32("start", start, (B,), device)
+    ck, cv, sk, sv = cache
+    _check("fa_cache8_store", lib().fa_cache8_store(
+        k.data_ptr(), v.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(), sv.data_ptr(), block_table.data_ptr(),
+        cu_seqlens.data_ptr(), start.data_ptr(), B, max_new, T, num_blocks, cols, Hk, block, d, ldk, ldv,
+        _stream_of(stream, device)))
+
+
+def fa_decode_cache8_workspace_bytes(B: int, Nq: int, H: int, Hk: int, max_seqlen: int, d: int) -> int:
+    return int(lib().fa_decode_cache8_workspace_bytes(B, Nq, H, Hk, max_seqlen, d))
+
+
+def fa_fwd_decode_cache8(q, cache, block_table, seqlens, o, lse, workspace, max_seqlen: int, causal: bool, scale=None,
+                         stream=None) -> None:
+    """q, o [B, Nq, H, d] over the cache (k, v, k_scale, v_scale); lse fp32 [B, H, Nq]."""
+    B, Nq, H, d = q.shape
+    device = q.device
+    _bf16("q", q, (B, Nq, H, d))
+    _bf16("o", o, (B, Nq, H, d))
+    _f32("lse", lse, (B, H, Nq))
+    num_blocks, Hk, block, dim = _cache8(cache, device)
+    if dim != d:
+        raise ValueError(f"the cache holds heads of {dim}, q has {d}")
+    cols = block_table.shape[1]
+    _int32("block_table", block_table, (B, cols), device)
+    _int32("seqlens", seqlens, (B,), device)
+    _on(device, o=o, lse=lse, workspace=workspace)
+    ck, cv, sk, sv = cache
+    _check("fa_fwd_decode_cache8", lib().fa_fwd_decode_cache8(
+        q.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(), sv.data_ptr(), block_table.data_ptr(),
+        seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), B, Nq, H, Hk, num_blocks, cols, block, max_seqlen, d,
+        _scale(scale, d), bool(causal), _stream_of(stream, device)))
 
 
 def fa_decode_workspace_bytes(B: int, H: int, Nq: int, Nk: int, d: int) -> int:

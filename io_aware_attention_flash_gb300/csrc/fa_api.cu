@@ -379,6 +379,52 @@ fa::SeqView grouped_view(const int* cu, int nseq, int max_seqlen, int total, int
   return sv;
 }
 
+// ----------------------------------------------------------------------------
+// 8-bit paged cache
+// ----------------------------------------------------------------------------
+fa_status check_cache8(int B, int num_blocks, int table_cols, int Hk, int block, int d) {
+  if (d != 64 && d != 128) return FA_ERR_HEAD_DIM;
+  if (block != 16 && block != 32 && block != 64 && block != 128) return FA_ERR_SHAPE;
+  if (B <= 0 || num_blocks <= 0 || table_cols <= 0 || Hk <= 0 || Hk > 65535) return FA_ERR_SHAPE;
+  if (static_cast<long long>(num_blocks) * Hk * block > 0x7fffffffLL * 16) return FA_ERR_SHAPE;
+  return FA_OK;
+}
+
+// CTAs of the cache attention: two on each of 152 SMs (fixed, so that the
+// workspace does not depend on the device), or one for each possible tile.
+constexpr int kDecode8Ctas = 304;
+
+fa_status check_decode8(int B, int Nq, int H, int Hk, int num_blocks, int table_cols, int block, int max_seqlen,
+                        int d, float scale) {
+  FA_TRY(check_common(H, d, scale));
+  FA_TRY(check_cache8(B, num_blocks, table_cols, Hk, block, d));
+  if (!(scale > 0.f)) return FA_ERR_SCALE;
+  if (Nq <= 0 || Nq > 8 || H % Hk != 0 || max_seqlen <= 0) return FA_ERR_SHAPE;
+  const long long tiles = (static_cast<long long>(max_seqlen) + fa::kTile - 1) / fa::kTile;
+  const long long rows = static_cast<long long>(B) * Nq * H;
+  if (rows > (1LL << 31) / 32 || B * tiles * Nq * H > 0x7fffffffLL) return FA_ERR_SHAPE;
+  return FA_OK;
+}
+
+struct Decode8Plan {
+  int row_groups, ctas;
+  size_t ml_off, start_off, bytes;
+};
+
+Decode8Plan decode8_plan(int B, int Nq, int H, int Hk, int max_seqlen, int d) {
+  Decode8Plan w{};
+  const int rows = fa::cache8_rows();
+  w.row_groups = (Nq * (H / Hk) + rows - 1) / rows;
+  const long long tiles =
+      (static_cast<long long>(max_seqlen) + fa::kTile - 1) / fa::kTile * B * Hk * w.row_groups;
+  w.ctas = static_cast<int>(tiles < kDecode8Ctas ? tiles : kDecode8Ctas);
+  const size_t parts = static_cast<size_t>(2) * w.ctas * rows;
+  w.ml_off = pad256(parts * d * 4);
+  w.start_off = w.ml_off + pad256(parts * 2 * 4);
+  w.bytes = w.start_off + pad256((static_cast<size_t>(B) + 1) * 4);
+  return w;
+}
+
 // One CTA waits on an mbarrier that nothing arrives on, with a short limit.
 __global__ void fa_wait_timeout_selftest_kernel(uint32_t* err, uint64_t limit_ns) {
   __shared__ __align__(8) uint64_t barrier;
@@ -450,6 +496,7 @@ FA_API const char* fa_status_string(fa_status status) {
     case FA_ERR_WORKSPACE: return "workspace missing or too small";
     case FA_ERR_SCALE: return "scale is not finite";
     case FA_ERR_NOT_DEVICE: return "q is not a device pointer";
+    case FA_ERR_PAGE: return "page table entry, sequence length or start position out of range; outputs invalid";
     case FA_ERR_SCRATCH_LIMIT: return "problem needs more scratch than the static no-alloc array holds";
     default: return "unknown status";
   }
@@ -588,6 +635,92 @@ FA_API fa_status fa_bwd_grouped(const void* q, const void* k, const void* v, con
   return e == cudaSuccess ? FA_OK : cuda_fail("grouped backward launch", e);
 }
 
+FA_API fa_status fa_cache8_store(const void* k, const void* v, void* k_codes, void* v_codes, float* k_scale,
+                                 float* v_scale, const int* block_table, const int* cu_seqlens, const int* start,
+                                 int B, int max_new, int total, int num_blocks, int table_cols, int Hk, int block,
+                                 int d, long long ldk, long long ldv, void* stream) {
+  FA_TRY(check_cache8(B, num_blocks, table_cols, Hk, block, d));
+  if (max_new <= 0 || total <= 0) return FA_ERR_SHAPE;
+  if (!k || !v || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !cu_seqlens || !start)
+    return FA_ERR_NULL;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes)) return FA_ERR_ALIGN;
+  if (!stride_ok(ldk, Hk, d) || !stride_ok(ldv, Hk, d)) return FA_ERR_SHAPE;
+  DeviceGuard guard;
+  FA_TRY(bind_device(k));
+  fa::Cache8StoreParams p{};
+  FA_TRY(error_word(&p.err));
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.ldk = ldk;
+  p.ldv = ldv;
+  p.k_codes = static_cast<uint8_t*>(k_codes);
+  p.v_codes = static_cast<uint8_t*>(v_codes);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.cu_seqlens = cu_seqlens;
+  p.start = start;
+  p.B = B;
+  p.total = total;
+  p.max_new = max_new;
+  p.num_blocks = num_blocks;
+  p.table_cols = table_cols;
+  p.Hk = Hk;
+  p.blocks = static_cast<int>((static_cast<long long>(max_new) + block - 2) / block + 1);
+  const cudaError_t e = fa::launch_cache8_store(d, block, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail("cache store launch", e);
+}
+
+FA_API size_t fa_decode_cache8_workspace_bytes(int B, int Nq, int H, int Hk, int max_seqlen, int d) {
+  if (check_decode8(B, Nq, H, Hk, 1, 1, 16, max_seqlen, d, 1.0f) != FA_OK) return 0;
+  return decode8_plan(B, Nq, H, Hk, max_seqlen, d).bytes;
+}
+
+FA_API fa_status fa_fwd_decode_cache8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                                      const float* v_scale, const int* block_table, const int* seqlens, void* o,
+                                      float* lse, void* workspace, size_t workspace_bytes, int B, int Nq, int H,
+                                      int Hk, int num_blocks, int table_cols, int block, int max_seqlen, int d,
+                                      float scale, int causal, void* stream) {
+  FA_TRY(check_decode8(B, Nq, H, Hk, num_blocks, table_cols, block, max_seqlen, d, scale));
+  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !seqlens || !o || !lse || !workspace)
+    return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(o) || !aligned16(workspace))
+    return FA_ERR_ALIGN;
+  const Decode8Plan w = decode8_plan(B, Nq, H, Hk, max_seqlen, d);
+  if (workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
+  DeviceGuard guard;
+  FA_TRY(bind_device(q));
+  fa::Cache8DecodeParams p{};
+  FA_TRY(error_word(&p.err));
+  p.q = static_cast<const uint16_t*>(q);
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.k_codes = static_cast<const uint8_t*>(k_codes);
+  p.v_codes = static_cast<const uint8_t*>(v_codes);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.seqlens = seqlens;
+  p.o_part = static_cast<float*>(workspace);
+  p.ml_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml_off);
+  p.tile_start = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.start_off);
+  p.B = B;
+  p.Nq = Nq;
+  p.H = H;
+  p.Hk = Hk;
+  p.G = H / Hk;
+  p.num_blocks = num_blocks;
+  p.table_cols = table_cols;
+  p.block = block;
+  p.max_seqlen = max_seqlen;
+  p.row_groups = w.row_groups;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.timeout_ns = kWaitLimitNs;
+  const cudaError_t e = fa::launch_cache8_decode(d, p, w.ctas, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail("cache attention launch", e);
+}
+
 FA_API size_t fa_decode_workspace_bytes(int B, int H, int Nq, int Nk, int d) {
   if (check_decode(B, H, Nq, Nk, d, 1.0f) != FA_OK) return 0;
   return decode_ws_bytes(B, H, Nq, Nk, d);
@@ -654,6 +787,8 @@ FA_API fa_status fa_get_device_error(void* stream) {
       st = cuda_fail("clear error word", e);
     } else if (word & fa::kDevErrTimeout) {
       st = FA_ERR_TIMEOUT;
+    } else if (word & fa::kDevErrPage) {
+      st = FA_ERR_PAGE;
     } else {
       snprintf(t_detail, sizeof(t_detail), "device error word 0x%x", word);
       st = FA_ERR_CUDA;

@@ -168,6 +168,45 @@ struct DecodeParams {
   uint64_t timeout_ns;
 };
 
+// 8-bit paged cache (fa_cache8.cu): pages [num_blocks, Hk, block, d] of e4m3
+// codes, one power-of-two scale for each (page, head).
+struct Cache8StoreParams {
+  const uint16_t* k;      // bf16 [total, Hk, d], rows ldk elements apart
+  const uint16_t* v;
+  long long ldk, ldv;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scale;         // [num_blocks, Hk]
+  float* v_scale;
+  const int* table;       // [B, table_cols] page of each block of tokens
+  const int* cu_seqlens;  // [B + 1] new tokens' rows
+  const int* start;       // [B] tokens cached before
+  int B, total, max_new, num_blocks, table_cols, Hk;
+  int blocks;             // pages that one sequence's new tokens can touch
+  uint32_t* err;
+};
+
+struct Cache8DecodeParams {
+  const uint16_t* q;      // bf16 [B, Nq, H, d]
+  uint16_t* o;
+  float* lse;             // fp32 [B, H, Nq]
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const float* k_scale;
+  const float* v_scale;
+  const int* table;
+  const int* seqlens;     // [B] cached tokens, the new ones among them
+  float* o_part;          // fp32 [2 · CTAs, rows of a group, d]
+  float* ml_part;         // fp32 [2 · CTAs, rows of a group, 2]
+  int* tile_start;        // [B + 1] first tile of each sequence in the launch's order, and the total
+  int B, Nq, H, Hk, G, num_blocks, table_cols, block, max_seqlen;
+  int row_groups;
+  int causal;
+  float scale_log2;
+  uint32_t* err;
+  uint64_t timeout_ns;
+};
+
 // Position of a (sequence, head) pair: pair = sequence * H + head.
 struct SeqPos {
   int bs, h, seq_start, seqlen, row_base, tma_row0, tma_b;
@@ -251,6 +290,9 @@ cudaError_t launch_bwd(int d, const CUtensorMap& tq, const CUtensorMap& tk, cons
                        cudaEvent_t main_start = nullptr, cudaEvent_t main_end = nullptr);
 cudaError_t launch_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int grid,
                           cudaStream_t s);
+cudaError_t launch_cache8_store(int d, int block, const Cache8StoreParams& p, cudaStream_t s);
+int cache8_rows();  // (new token, query head) rows of a decode work item
+cudaError_t launch_cache8_decode(int d, const Cache8DecodeParams& p, int ctas, cudaStream_t s);
 cudaError_t launch_wait_timeout_selftest(uint32_t* err, uint64_t limit_ns, cudaStream_t s);
 cudaError_t run_microbench(int which, int iters, uint32_t* err, double* result, cudaStream_t s);
 

@@ -17,6 +17,7 @@ namespace fa {
 enum : uint32_t {
   kDevErrTimeout = 1u,        // an mbarrier wait ran past its limit
   kDevErrSmemAlign = 2u,      // dynamic shared memory not 1024-byte aligned
+  kDevErrPage = 4u,           // a page table entry, a length or a start position out of range
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

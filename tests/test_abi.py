@@ -137,3 +137,61 @@ def test_decode_validation(lib):
     assert dec(ws_ptr=NUL) == 1
     assert dec(ws_ptr=FAKE + 8) == 2
     assert dec(ws_bytes=ws - 1) == 8
+
+
+def _grouped(lib, q=FAKE, cu=FAKE, nseq=3, max_seqlen=500, total=1000, H=8, Hk=2, d=128, ldq=1024, ldk=256, scale=0.1):
+    return lib.fa_fwd_grouped(q, FAKE, FAKE, FAKE, FAKE, cu, nseq, max_seqlen, total, H, Hk, d, ldq, ldk, ldk, scale, 1,
+                              0, None)
+
+
+def test_grouped_validation(lib):
+    assert _grouped(lib, d=96) == 3
+    assert _grouped(lib, Hk=3) == 4 and _grouped(lib, Hk=0) == 4 and _grouped(lib, H=0) == 4
+    assert _grouped(lib, nseq=0) == 4 and _grouped(lib, max_seqlen=0) == 4 and _grouped(lib, total=0) == 4
+    assert _grouped(lib, q=NUL) == 1 and _grouped(lib, cu=NUL) == 1
+    assert _grouped(lib, q=FAKE + 8) == 2
+    assert _grouped(lib, ldq=1016) == 4 and _grouped(lib, ldk=260) == 4
+    for scale in (0.0, -0.1, float("nan"), float("inf")):
+        assert _grouped(lib, scale=scale) == 9
+    ws = lib.fa_bwd_grouped_workspace_bytes(3, 500, 1000, 8, 2, 128, 1)
+    # D [8, 1000] and the dQ accumulator of 1024 rows, then parts of dK and dV
+    assert ws >= 8 * 1000 * 4 + 1024 * 8 * 128 * 4
+    assert lib.fa_bwd_grouped_workspace_bytes(3, 500, 1000, 8, 3, 128, 1) == 0
+
+    def bwd(ws_ptr=FAKE, ws_bytes=ws, dk=FAKE):
+        return lib.fa_bwd_grouped(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, dk, FAKE, ws_ptr, ws_bytes, FAKE, 3, 500,
+                                  1000, 8, 2, 128, 1024, 256, 256, 0.1, 1, 0, None)
+
+    assert bwd(ws_bytes=ws - 1) == 8 and bwd(ws_ptr=NUL) == 8 and bwd(ws_ptr=FAKE + 8) == 2
+    assert bwd(dk=NUL) == 1 and bwd(dk=FAKE + 4) == 2
+
+
+def test_cache8_validation(lib):
+    def store(k=FAKE, codes=FAKE, table=FAKE, B=2, max_new=5, total=9, blocks=10, cols=4, Hk=2, block=16, d=64, ld=128):
+        return lib.fa_cache8_store(k, FAKE, codes, FAKE, FAKE, FAKE, table, FAKE, FAKE, B, max_new, total, blocks, cols, Hk,
+                                   block, d, ld, ld, None)
+
+    assert store(d=32) == 3
+    assert store(block=24) == 4 and store(block=256) == 4 and store(B=0) == 4 and store(max_new=0) == 4
+    assert store(total=0) == 4 and store(blocks=0) == 4 and store(cols=0) == 4 and store(Hk=0) == 4
+    assert store(ld=120) == 4 and store(ld=132) == 4
+    assert store(k=NUL) == 1 and store(table=NUL) == 1
+    assert store(k=FAKE + 2) == 2 and store(codes=FAKE + 8) == 2
+
+    ws = lib.fa_decode_cache8_workspace_bytes(2, 1, 8, 2, 1000, 128)
+    assert ws > 0 and ws % 256 == 0
+    assert lib.fa_decode_cache8_workspace_bytes(2, 9, 8, 2, 1000, 128) == 0
+    assert lib.fa_decode_cache8_workspace_bytes(2, 1, 8, 3, 1000, 128) == 0
+    assert lib.fa_decode_cache8_workspace_bytes(2, 1, 8, 2, 0, 128) == 0
+
+    def dec(q=FAKE, codes=FAKE, ws_ptr=FAKE, ws_bytes=ws, Nq=1, H=8, Hk=2, block=16, d=128, max_seqlen=1000, scale=0.1):
+        return lib.fa_fwd_decode_cache8(q, codes, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, ws_ptr, ws_bytes, 2, Nq, H, Hk, 100,
+                                        63, block, max_seqlen, d, scale, 1, None)
+
+    assert dec(d=96) == 3
+    assert dec(Nq=0) == 4 and dec(Nq=9) == 4 and dec(Hk=3) == 4 and dec(block=8) == 4 and dec(max_seqlen=0) == 4
+    assert dec(scale=0.0) == 9 and dec(scale=float("nan")) == 9
+    assert dec(q=NUL) == 1 and dec(ws_ptr=NUL) == 1
+    assert dec(codes=FAKE + 1) == 2 and dec(ws_ptr=FAKE + 8) == 2
+    assert dec(ws_bytes=ws - 1) == 8
+    assert lib.fa_status_string(12)
