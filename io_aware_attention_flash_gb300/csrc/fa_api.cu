@@ -390,6 +390,28 @@ fa_status check_cache8(int B, int num_blocks, int table_cols, int Hk, int block,
   return FA_OK;
 }
 
+// Pages [num_blocks, Hk, block, d] of 1-byte codes, one (page, head) a copy,
+// rows swizzled over their d bytes.
+fa_status make_map_codes(CUtensorMap* map, const void* ptr, int d, int block, int Hk, int num_blocks) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return cuda_fail("cuTensorMapEncodeTiled entry point not found", cudaErrorSymbolNotFound);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(block), static_cast<cuuint64_t>(Hk),
+                              static_cast<cuuint64_t>(num_blocks)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(block) * d,
+                                 static_cast<cuuint64_t>(Hk) * block * d};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(block), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    snprintf(t_detail, sizeof(t_detail), "cuTensorMapEncodeTiled (cache pages) failed (CUresult %d)",
+             static_cast<int>(r));
+    return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}
+
 // CTAs of the cache attention: two on each of 152 SMs (fixed, so that the
 // workspace does not depend on the device), or one for each possible tile.
 constexpr int kDecode8Ctas = 304;
@@ -407,18 +429,17 @@ fa_status check_decode8(int B, int Nq, int H, int Hk, int num_blocks, int table_
 }
 
 struct Decode8Plan {
-  int row_groups, ctas;
+  int row_groups, rows, ctas;
   size_t ml_off, start_off, bytes;
 };
 
 Decode8Plan decode8_plan(int B, int Nq, int H, int Hk, int max_seqlen, int d) {
   Decode8Plan w{};
-  const int rows = fa::cache8_rows();
-  w.row_groups = (Nq * (H / Hk) + rows - 1) / rows;
+  fa::cache8_row_groups(Nq * (H / Hk), &w.row_groups, &w.rows);
   const long long tiles =
       (static_cast<long long>(max_seqlen) + fa::kTile - 1) / fa::kTile * B * Hk * w.row_groups;
   w.ctas = static_cast<int>(tiles < kDecode8Ctas ? tiles : kDecode8Ctas);
-  const size_t parts = static_cast<size_t>(2) * w.ctas * rows;
+  const size_t parts = static_cast<size_t>(2) * w.ctas * w.rows;
   w.ml_off = pad256(parts * d * 4);
   w.start_off = w.ml_off + pad256(parts * 2 * 4);
   w.bytes = w.start_off + pad256((static_cast<size_t>(B) + 1) * 4);
@@ -714,10 +735,14 @@ FA_API fa_status fa_fwd_decode_cache8(const void* q, const void* k_codes, const 
   p.block = block;
   p.max_seqlen = max_seqlen;
   p.row_groups = w.row_groups;
+  p.rows = w.rows;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * fa::kLog2e;
   p.timeout_ns = kWaitLimitNs;
-  const cudaError_t e = fa::launch_cache8_decode(d, p, w.ctas, static_cast<cudaStream_t>(stream));
+  CUtensorMap tk, tv;
+  FA_TRY(make_map_codes(&tk, k_codes, d, block, Hk, num_blocks));
+  FA_TRY(make_map_codes(&tv, v_codes, d, block, Hk, num_blocks));
+  const cudaError_t e = fa::launch_cache8_decode(d, tk, tv, p, w.ctas, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail("cache attention launch", e);
 }
 

@@ -171,28 +171,35 @@ cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
 // ----------------------------------------------------------------------------
 // Work: the 128-key tiles of every (sequence, key/value head, row group), in
 // that order, are shared out in equal runs over the launch's CTAs, whatever
-// the sequences' lengths; a row group is up to kRows of the (new token, query
+// the sequences' lengths; a row group is up to 16 of the (new token, query
 // head) rows that attend to one key/value head.  A CTA that has all tiles of
 // an item writes its output; an item that several CTAs share leaves partials
 // (m, l, O) that the merge kernel combines in the order of the tiles.
-constexpr int kRows = 8;
-
-struct Work {
-  int* start;     // [B + 1] shared memory: first tile of each sequence, then the total
-  int total;
-};
-
-// Cached tokens of sequence b: a length below 0 counts as 0, one past the page
-// table as the table's end.
-__device__ __forceinline__ int cached_len(const Cache8DecodeParams& p, int b) {
-  const long long cap = static_cast<long long>(p.table_cols) * p.block;
-  int n = __ldg(p.seqlens + b);
-  if (n < 0 || n > cap || n > p.max_seqlen) {
-    atomicOr(p.err, kDevErrPage);
-    n = n < 0 ? 0 : static_cast<int>(min(cap, static_cast<long long>(p.max_seqlen)));
-  }
-  return n;
-}
+//
+// Both products run on the tensor core straight from the codes, keys (or, for
+// P V, head dimensions) as the 128 rows of A and the queries as B:
+//   S^T = K Q^T     A = K tile, K-major;   B = Q,  K-major
+//   O^T = V^T P^T   A = V tile, MN-major;  B = P,  K-major
+// with B in e4m3 as well, split into two factors so that nothing is lost to 8
+// bits: q / s_q = hi + lo / 16 (s_q a power of two for each row; exact for
+// elements above 2^-13 of the row's largest, else off by 2^-22 of that) and
+// p = hi + lo / 32 (off by at most 2^-8 p, as much as rounding to bf16 would
+// be, for p above 2^-13 of the tile's largest).  The factors are separate
+// columns of B, so each product stays one MMA chain.  K's scale (times softmax
+// scale and s_q) multiplies the scores; V's goes into P: with
+// y = s c + log2 s_V the tile's largest y of each row is the tile's reference,
+// P = 2^(y - y_max) 256, so that a tile of small probabilities (all but the
+// first, where one early key takes most of the weight) keeps its relative
+// accuracy, and O is rescaled in registers from tile to tile as in the usual
+// online softmax.
+//
+// Warps 0-3 (thread r: key r for scores and P, head dimension r for O), warp 4
+// loads (lane i: page i of the tile, its TMA copies and its two scales), warp
+// 5 issues the MMAs.  d = 64: A needs 128 rows, so V is read as two blocks of
+// 64 dimensions, keys 0-63 and 64-127 of the tile, each against P's own half
+// of the keys as columns of their own: thread r keeps dimension r mod 64 of
+// half r / 64, and the halves are added once for each item.
+constexpr int kRowsMax = 16;
 
 __device__ __forceinline__ int run_start(long long c, int total, int ctas) { return static_cast<int>(c * total / ctas); }
 // The CTA whose run holds tile t.
@@ -200,181 +207,495 @@ __device__ __forceinline__ int run_of(long long t, int total, int ctas) {
   return static_cast<int>(((t + 1) * ctas + total - 1) / total - 1);
 }
 
-// Sum of the tiles of the sequences before b0 .. (whole block; NT threads).
-// Returns this CTA's first sequence and the tiles before it through `scan`.
-template <int NT>
-__device__ __forceinline__ int block_scan_tiles(const Cache8DecodeParams& p, int* warp_sums, bool store) {
-  // inclusive scans of NT sequences at a time
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += NT) {
-    const int b = b0 + threadIdx.x;
-    int n = b < p.B ? (cached_len(p, b) + kTile - 1) / kTile * p.Hk * p.row_groups : 0;
-    const int own = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, n, off);
-      if (lane >= off) n += y;
-    }
-    if (lane == 31) warp_sums[warp] = n;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < NT / 32; ++w) {
-      before += w < warp ? warp_sums[w] : 0;
-      all += warp_sums[w];
-    }
-    __syncthreads();
-    if (store && b < p.B) p.tile_start[b] = base + before + n - own;
-    base += all;
-  }
-  return base;
+// Cached tokens of sequence b: a length below 0 counts as 0, one past
+// max_seqlen or the page table as the nearer of the two.
+__device__ __forceinline__ int cached_len(const Cache8DecodeParams& p, int b) {
+  const long long cap = min(static_cast<long long>(p.table_cols) * p.block, static_cast<long long>(p.max_seqlen));
+  const int n = __ldg(p.seqlens + b);
+  return static_cast<int>(min(max(static_cast<long long>(n), 0LL), cap));
+}
+__device__ __forceinline__ int seq_tiles(const Cache8DecodeParams& p, int b) {
+  return (cached_len(p, b) + kTile - 1) / kTile;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) fa_cache8_decode_kernel(const Cache8DecodeParams p) {
-  __shared__ int warp_sums[4];
-  __shared__ float qs[kRows][D];
-  __shared__ float ps[kRows][kTile];
-  __shared__ float red[4][kRows];
-  __shared__ float m_s[kRows], l_s[kRows], a_s[kRows];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // Every CTA finds its place by itself: the tiles before each sequence.
-  const int total = block_scan_tiles<128>(p, warp_sums, blockIdx.x == 0);
-  if (blockIdx.x == 0 && tid == 0) p.tile_start[p.B] = total;
-  const int ctas = min(static_cast<int>(gridDim.x), total);  // every one of them has a tile
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const int t_lo = run_start(blockIdx.x, total, ctas), t_hi = run_start(blockIdx.x + 1LL, total, ctas);
-  int b = 0, seq0 = 0;  // sequence of tile t and its first tile
-  for (int t = t_lo; t < t_hi;) {
-    int nt;
-    while (true) {
-      nt = (cached_len(p, b) + kTile - 1) / kTile;
-      if (t < seq0 + nt * p.Hk * p.row_groups) break;
-      seq0 += nt * p.Hk * p.row_groups;
-      ++b;
+// A CTA's walk through its run: the tiles [k0, k1) of one item after another.
+struct Walk {
+  int t, t_hi, b, seq0;              // next tile, end of the run, sequence and its first tile
+  int hk, rg, nt, k0, k1, len;
+  // WARP: called by a whole warp, which takes lane 0's lengths, so that it
+  // stays together even if a caller changes the lengths meanwhile.
+  template <bool WARP>
+  __device__ __forceinline__ bool next(const Cache8DecodeParams& p) {
+    if (t >= t_hi) return false;
+    const int per = p.Hk * p.row_groups;
+    auto read = [&]() {
+      len = cached_len(p, b);
+      if (WARP) len = __shfl_sync(0xffffffffu, len, 0);
+      nt = (len + kTile - 1) / kTile;
+    };
+    read();
+    while (t >= seq0 + nt * per) {
+      seq0 += nt * per;
+      if (++b >= p.B) return false;
+      read();
     }
-    const int len = cached_len(p, b);
-    const int item = (t - seq0) / nt;           // (head, row group)
-    const int k0 = (t - seq0) - item * nt;      // first tile of the item in this run
-    const int k1 = min(nt, k0 + (t_hi - t));
-    const int hk = item / p.row_groups, rg = item - hk * p.row_groups;
-    const int rows = min(kRows, p.Nq * p.G - rg * kRows);
-    __syncthreads();
-    for (int i = tid; i < kRows * D; i += 128) {
-      const int r = i / D, f = rg * kRows + r;
-      float v = 0.f;
-      if (r < rows)
-        v = __uint_as_float(static_cast<uint32_t>(
-                p.q[((static_cast<size_t>(b) * p.Nq + f / p.G) * p.H + hk * p.G + f % p.G) * D + i % D]) << 16);
-      qs[r][i % D] = v;
-    }
-    if (tid < kRows) {
-      m_s[tid] = -CUDART_INF_F;
-      l_s[tid] = 0.f;
-    }
-    float acc[kRows];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) acc[r] = 0.f;
-    for (int kt = k0; kt < k1; ++kt) {
-      __syncthreads();
-      const int key = kt * kTile + tid;
-      float s[kRows];
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) s[r] = 0.f;
-      int page = -1;
-      if (key < len) {
-        page = __ldg(p.table + static_cast<size_t>(b) * p.table_cols + key / p.block);
-        if (page < 0 || page >= p.num_blocks) {
-          atomicOr(p.err, kDevErrPage);
-          page = -1;
-        }
-      }
-      if (page >= 0) {
-        const uint32_t* row = reinterpret_cast<const uint32_t*>(
-            p.k_codes + ((static_cast<size_t>(page) * p.Hk + hk) * p.block + key % p.block) * D);
-        for (int c = 0; c < D / 4; ++c) {
-          const uint32_t w = row[c];
-          float x[4];
-          unpack_e4m3x2(w, x[0], x[1]);
-          unpack_e4m3x2(w >> 16, x[2], x[3]);
-#pragma unroll
-          for (int r = 0; r < kRows; ++r)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[r] = fmaf(qs[r][4 * c + e], x[e], s[r]);
-        }
-        const float ks = p.k_scale[static_cast<size_t>(page) * p.Hk + hk] * p.scale_log2;
-#pragma unroll
-        for (int r = 0; r < kRows; ++r) s[r] *= ks;
-      }
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const int last = p.causal ? len - p.Nq + (rg * kRows + r) / p.G : len - 1;
-        if (key > last || key >= len) s[r] = -CUDART_INF_F;
-        float mx = s[r];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        if (lane == 0) red[warp][r] = mx;
-      }
-      __syncthreads();
-      if (tid < kRows) {
-        const float m_new = fmaxf(fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid])), m_s[tid]);
-        a_s[tid] = m_s[tid] == -CUDART_INF_F ? 0.f : ex2_approx(m_s[tid] - m_new);
-        m_s[tid] = m_new;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const float e = s[r] == -CUDART_INF_F ? 0.f : ex2_approx(s[r] - m_s[r]);
-        ps[r][tid] = e;
-        float sum = e;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) red[warp][r] = sum;
-        acc[r] *= a_s[r];
-      }
-      __syncthreads();
-      if (tid < kRows) l_s[tid] = l_s[tid] * a_s[tid] + ((red[0][tid] + red[1][tid]) + (red[2][tid] + red[3][tid]));
-      if (tid < D) {
-        const int n = min(kTile, len - kt * kTile);
-        for (int j = 0; j < n; ++j) {
-          const int kj = kt * kTile + j;
-          const int pj = __ldg(p.table + static_cast<size_t>(b) * p.table_cols + kj / p.block);
-          if (pj < 0 || pj >= p.num_blocks) continue;
-          const size_t ph = static_cast<size_t>(pj) * p.Hk + hk;
-          float v, unused;
-          unpack_e4m3x2(p.v_codes[(ph * p.block + kj % p.block) * D + tid], v, unused);
-          v *= p.v_scale[ph];
-#pragma unroll
-          for (int r = 0; r < kRows; ++r) acc[r] = fmaf(ps[r][j], v, acc[r]);
-        }
-      }
-    }
-    __syncthreads();
-    const bool whole = k0 == 0 && k1 == nt;
-    for (int r = 0; r < rows; ++r) {
-      const int f = rg * kRows + r;
-      const size_t qrow = static_cast<size_t>(b) * p.Nq + f / p.G;
-      const int h = hk * p.G + f % p.G;
-      float a = 0.f;
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) a = i == r ? acc[i] : a;
-      if (whole) {
-        const float l = l_s[r];
-        if (tid < D) p.o[(qrow * p.H + h) * D + tid] = static_cast<uint16_t>(pack_bf16x2(l > 0.f ? a / l : 0.f, 0.f));
-        if (tid == 0)
-          p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + f / p.G] =
-              l > 0.f ? (m_s[r] + log2f(l)) * kLn2 : -CUDART_INF_F;
-      } else {
-        const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (k0 == 0 ? 1 : 0)) * kRows + r;
-        if (tid < D) p.o_part[slot * D + tid] = a;
-        if (tid == 0) {
-          p.ml_part[slot * 2] = m_s[r];
-          p.ml_part[slot * 2 + 1] = l_s[r];
-        }
-      }
-    }
+    const int item = (t - seq0) / nt;
+    k0 = t - seq0 - item * nt;
+    k1 = min(nt, k0 + (t_hi - t));
+    hk = item / p.row_groups;
+    rg = item - hk * p.row_groups;
     t += k1 - k0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// D(tmem) (+)= A(smem) B(smem), e4m3 inputs, fp32 accumulate, K = 32 a step.
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (formats 0), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+template <int D, int RP>
+struct Dec8Cfg {
+  static constexpr int TILE_BYTES = kTile * D;               // 128 keys
+  static constexpr int NST = D == 128 ? 3 : 6;               // ring stages (K and V tile each)
+  static constexpr int NS = 2 * RP < 16 ? 16 : 2 * RP;       // columns of S: the rows' hi, then lo factors
+  static constexpr int HALVES = 128 / D;
+  static constexpr int NO = 2 * RP * HALVES < 16 ? 16 : 2 * RP * HALVES;
+  static constexpr int Q_BYTES = NS * D;
+  static constexpr int P_BYTES = NO * (kTile / HALVES);
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
+  static constexpr int OFF_Q = OFF_V + NST * TILE_BYTES;
+  static constexpr int OFF_P = OFF_Q + Q_BYTES;
+  static constexpr int OFF_SC = OFF_P + P_BYTES;             // [NST][8 pages][2] scales of K, V
+  static constexpr int OFF_QS = OFF_SC + NST * 8 * 2 * 4;    // [RP] score factor of each row
+  static constexpr int OFF_XCH = OFF_QS + kRowsMax * 4;      // [2][4 warps][RP]
+  static constexpr int OFF_HALF = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [RP][64] O of the second half (d = 64)
+  static constexpr int OFF_SCAN = OFF_HALF + (D == 64 ? RP * 64 * 4 : 0);  // [6] warp sums, [2] first sequence and its tile
+  static constexpr int OFF_BAR = (OFF_SCAN + 8 * 4 + 7) / 8 * 8;
+  static constexpr int B_FULL = 0, B_EMPTY = NST, B_SFULL = 2 * NST, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 1,
+                       B_XCH = B_PVDONE + 1, B_QREADY = B_XCH + 1, B_DRAIN = B_QREADY + 1, NBAR = B_DRAIN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;    // slack to align the base to 1024
+  static constexpr int NUM_THREADS = 6 * 32;
+  static constexpr uint32_t COLS = 2 * NS + NO;
+  static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : 128;
+  static constexpr uint32_t O_COL = 2 * NS;
+  static_assert(COLS <= 128, "tensor memory budget");
+  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs on an SM");
+  static_assert(OFF_Q % 1024 == 0 && OFF_P % 512 == 0 && (D == 64 || OFF_P % 1024 == 0), "swizzle atoms");
+};
+
+// Byte `byte` of row `row` in a tile of W-byte rows swizzled over W bytes (the
+// 16-byte chunk's index exclusive-or the address bits above the 128-byte line).
+template <int W>
+__device__ __forceinline__ uint32_t swz(int row, int byte) {
+  constexpr int MASK = W / 16 - 1;
+  const int line = W == 128 ? row : row >> 1;
+  return row * W + ((((byte >> 4) ^ line) & MASK) << 4) + (byte & 15);
+}
+// Descriptor of an operand in W-byte swizzled rows, 8 rows an atom.
+template <int W>
+__device__ __forceinline__ uint64_t sdesc8(uint32_t saddr, uint32_t lbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((8 * W) >> 4) << 32) | (1ull << 46) | ((W == 128 ? 2ull : 4ull) << 61);
+}
+
+template <int D, int RP>
+__global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
+    fa_cache8_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                            const Cache8DecodeParams p) {
+  using C = Dec8Cfg<D, RP>;
+  grid_launch_dependents();
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sb = raw_base + pad;
+  auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // ---- this CTA's place: all tiles counted, then the sequence of its first one
+  const int per = p.Hk * p.row_groups;
+  int mine = 0;
+  for (int b = threadIdx.x; b < p.B; b += C::NUM_THREADS) mine += seq_tiles(p, b);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) scan[warp] = mine;
+  if (warp == 4 && lane == 0) {
+    for (int s = 0; s < C::NST; ++s) {
+      mbar_init(bar(C::B_FULL + s), 32);
+      mbar_init(bar(C::B_EMPTY + s), 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_SFULL + i), 1);
+    mbar_init(bar(C::B_PFULL), 128);
+    mbar_init(bar(C::B_PVDONE), 1);
+    mbar_init(bar(C::B_XCH), 128);
+    mbar_init(bar(C::B_QREADY), 128);
+    mbar_init(bar(C::B_DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  __syncthreads();
+  const int total = (scan[0] + scan[1] + scan[2] + scan[3] + scan[4] + scan[5]) * per;
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.tile_start[p.B] = total;
+  const int ctas = min(static_cast<int>(gridDim.x), total);  // every one of them has a tile
+  const bool idle = static_cast<int>(blockIdx.x) >= ctas;
+  if (idle && blockIdx.x != 0) return;
+  Walk w{};
+  w.t = idle ? 0 : run_start(blockIdx.x, total, ctas);
+  w.t_hi = idle ? 0 : run_start(blockIdx.x + 1LL, total, ctas);
+  if (warp == 0) {  // CTA 0 writes down every sequence's first tile for the merge
+    int base = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      const int n = b < p.B ? seq_tiles(p, b) * per : 0;
+      int sum = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, off);
+        if (lane >= off) sum += y;
+      }
+      const int first = base + sum - n;
+      if (blockIdx.x == 0) {
+        if (b < p.B) {
+          p.tile_start[b] = first;
+          const int raw = __ldg(p.seqlens + b);
+          if (raw != cached_len(p, b)) atomicOr(p.err, kDevErrPage);
+        }
+      }
+      if (n > 0 && w.t >= first && w.t < first + n) {
+        scan[6] = b;
+        scan[7] = first;
+      }
+      base += __shfl_sync(0xffffffffu, sum, 31);
+      if (blockIdx.x != 0 && base > w.t) break;
+    }
+    if (!idle) {
+      tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  } else if (warp < 4) {  // factors of rows that do not exist stay zero for good
+    for (int i = threadIdx.x - 32; i < (C::Q_BYTES + C::P_BYTES) / 16; i += 96)
+      reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (idle) return;
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  w.b = scan[6];
+  w.seq0 = scan[7];
+
+  if (warp == 4) {
+    // ---------------------------------------------------------------- TMA
+    const int ppt = kTile / p.block;  // pages of a tile
+    int t = 0;
+    bool ok = true;
+    while (ok && w.next<true>(p)) {
+      const int* row = p.table + static_cast<size_t>(w.b) * p.table_cols;
+      for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
+        const int st = t % C::NST;
+        const int n_pages = min(ppt, (w.len - kt * kTile + p.block - 1) / p.block);
+        int page = p.num_blocks;  // a page out of range reads as zeros
+        float ks = 0.f, vs = 0.f;
+        if (lane < n_pages) {
+          const int e = __ldg(row + kt * ppt + lane);
+          if (e >= 0 && e < p.num_blocks) {
+            page = e;
+            ks = __ldg(p.k_scale + static_cast<size_t>(e) * p.Hk + w.hk);
+            vs = __ldg(p.v_scale + static_cast<size_t>(e) * p.Hk + w.hk);
+          } else {
+            atomicOr(p.err, kDevErrPage);
+          }
+        }
+        if (t >= C::NST) ok = wait_bounded(bar(C::B_EMPTY + st), ((t / C::NST) - 1) & 1, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(bar(C::B_FULL + st), n_pages * p.block * D * 2);
+        __syncwarp();
+        if (lane < n_pages) {
+          const uint32_t off = st * C::TILE_BYTES + lane * p.block * D;
+          tma_load_4d(sb + C::OFF_K + off, &tmK, bar(C::B_FULL + st), 0, 0, w.hk, page);
+          tma_load_4d(sb + C::OFF_V + off, &tmV, bar(C::B_FULL + st), 0, 0, w.hk, page);
+        }
+        if (lane < 8) {
+          float* sc = reinterpret_cast<float*>(smem + C::OFF_SC) + (st * 8 + lane) * 2;
+          sc[0] = ks;
+          sc[1] = vs;
+        }
+        mbar_arrive(bar(C::B_FULL + st));
+      }
+    }
+    // Every copy issued lands before the CTA may exit, whoever aborted.
+    for (int s = 0; s < C::NST && s < t; ++s) {
+      const int last = s + ((t - 1 - s) / C::NST) * C::NST;
+      wait_drain(bar(C::B_FULL + s), (last / C::NST) & 1, p.err, p.timeout_ns);
+    }
+  } else if (warp == 5) {
+    // ---------------------------------------------------------------- MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_e4m3(128, C::NS, false), idesc_o = idesc_e4m3(128, C::NO, true);
+      constexpr int KW = kTile / C::HALVES;  // P row in bytes: keys of a half
+      const uint64_t dK0 = sdesc8<D>(sb + C::OFF_K, 16);
+      const uint64_t dV0 = sdesc8<D>(sb + C::OFF_V, 64 * D);  // MN-major; second block of 64 dimensions (d = 64): keys 64..
+      const uint64_t dQ = sdesc8<D>(sb + C::OFF_Q, 16);
+      const uint64_t dP = sdesc8<KW>(sb + C::OFF_P, 16);
+      auto issue_s = [&](int u) -> bool {
+        const int st = u % C::NST;
+        if (!wait_bounded(bar(C::B_FULL + st), (u / C::NST) & 1, abort_flag, p.err, p.timeout_ns)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D / 32; ++kk)
+          mma_e4m3(tmem + C::NS * (u & 1), sdesc_add(dK0, st * C::TILE_BYTES + kk * 32), sdesc_add(dQ, kk * 32), idesc_s,
+                   kk > 0);
+        tc_commit(bar(C::B_SFULL + (u & 1)));
+        return true;
+      };
+      int t = 0, n_item = 0;
+      bool ok = true;
+      for (; ok && w.next<false>(p); ++n_item) {
+        ok = wait_bounded(bar(C::B_QREADY), n_item & 1, abort_flag, p.err, p.timeout_ns) && issue_s(t);
+        for (int kt = w.k0; ok && kt < w.k1; ++kt, ++t) {
+          // the next tile's scores run while this tile's P is formed (across
+          // items they cannot: the next Q is staged after this item's last S)
+          if (kt + 1 < w.k1) ok = issue_s(t + 1);
+          ok = ok && wait_bounded(bar(C::B_PFULL), t & 1, abort_flag, p.err, p.timeout_ns);
+          if (!ok) break;
+          tc_fence_after();
+          const int st = t % C::NST;
+#pragma unroll
+          for (int kk = 0; kk < KW / 32; ++kk)
+            mma_e4m3(tmem + C::O_COL, sdesc_add(dV0, st * C::TILE_BYTES + kk * 32 * D), sdesc_add(dP, kk * 32), idesc_o,
+                     kk > 0);
+          tc_commit(bar(C::B_PVDONE));
+          tc_commit(bar(C::B_EMPTY + st));
+        }
+      }
+      tc_commit(bar(C::B_DRAIN));
+      wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax, P, running O
+    const int r = threadIdx.x;  // key of the tile; head dimension (and half) of O
+    const int half = r / D;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    float* xch = reinterpret_cast<float*>(smem + C::OFF_XCH);
+    float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+    constexpr int KW = kTile / C::HALVES;
+    int t = 0, nx = 0, n_item = 0;
+    bool ok = true;
+    auto wait = [&](int i, uint32_t ph) {
+      ok = ok && wait_bounded(bar(i), ph, abort_flag, p.err, p.timeout_ns);
+    };
+    for (; __all_sync(0xffffffffu, ok) && w.next<true>(p); ++n_item) {
+      const int rows = min(p.rows, p.Nq * p.G - w.rg * p.rows);
+      // ---- the item's queries as two factors (their last reader, the S of the
+      // item before, has completed)
+      for (int q = warp; q < RP; q += 4) {
+        constexpr int E = D / 32;
+        float x[E];
+        float mx = 0.f;
+        const int f = w.rg * p.rows + q;
+        const uint16_t* src =
+            p.q + ((static_cast<size_t>(w.b) * p.Nq + f / p.G) * p.H + w.hk * p.G + f % p.G) * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          x[e] = q < rows ? __uint_as_float(static_cast<uint32_t>(src[e]) << 16) : 0.f;
+          mx = fmaxf(mx, fabsf(x[e]));
+        }
+        mx = redux_max(mx);
+        // smallest power of two s with mx <= 448 s (within the exponents whose inverse is a float)
+        const int e2 = min(max(scale_exponent(__float_as_uint(mx) >> 16), -100), 100);
+        const float inv = exp2_int(-e2);
+        uint32_t hi = 0, lo = 0;
+        float h[E];
+        if constexpr (E == 4) {
+          hi = pack_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+          unpack_e4m3x2(hi, h[0], h[1]);
+          unpack_e4m3x2(hi >> 16, h[2], h[3]);
+          lo = pack_e4m3x4((x[0] * inv - h[0]) * 16.f, (x[1] * inv - h[1]) * 16.f, (x[2] * inv - h[2]) * 16.f,
+                           (x[3] * inv - h[3]) * 16.f);
+          *reinterpret_cast<uint32_t*>(smem + C::OFF_Q + swz<D>(q, E * lane)) = hi;
+          *reinterpret_cast<uint32_t*>(smem + C::OFF_Q + swz<D>(RP + q, E * lane)) = lo;
+        } else {
+          hi = pack_e4m3x4(x[0] * inv, x[1] * inv, 0.f, 0.f);
+          unpack_e4m3x2(hi, h[0], h[1]);
+          lo = pack_e4m3x4((x[0] * inv - h[0]) * 16.f, (x[1] * inv - h[1]) * 16.f, 0.f, 0.f);
+          *reinterpret_cast<uint16_t*>(smem + C::OFF_Q + swz<D>(q, E * lane)) = static_cast<uint16_t>(hi);
+          *reinterpret_cast<uint16_t*>(smem + C::OFF_Q + swz<D>(RP + q, E * lane)) = static_cast<uint16_t>(lo);
+        }
+        if (lane == 0) qs[q] = exp2_int(e2) * p.scale_log2;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(C::B_QREADY));
+      wait(C::B_QREADY, n_item & 1);
+      float qf[RP], m[RP], lsum[RP], ov[RP];
+#pragma unroll
+      for (int q = 0; q < RP; ++q) {
+        qf[q] = qs[q];
+        m[q] = -CUDART_INF_F;
+        lsum[q] = ov[q] = 0.f;
+      }
+      for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
+        const int st = t % C::NST;
+        wait(C::B_FULL + st, (t / C::NST) & 1);
+        const int key = kt * kTile + r;
+        const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (st * 8 + r / p.block) * 2;
+        const float ks = sc[0], vs = sc[1];
+        // log2 of V's scale: 0 for a page of zeros, whatever its scale
+        const int ve = vs > 0.f ? static_cast<int>(__float_as_uint(vs) >> 23) - 127 : 0;
+        wait(C::B_SFULL + (t & 1), (t >> 1) & 1);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t sv[C::NS];
+#pragma unroll
+        for (int c = 0; c < C::NS / 16; ++c) tmem_ld16(lane_addr + C::NS * (t & 1) + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < C::NS / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
+        float y[RP];
+        float wm = 0.f;
+#pragma unroll
+        for (int q = 0; q < RP; ++q) {
+          const int f = w.rg * p.rows + q;
+          const int last = p.causal ? w.len - p.Nq + f / p.G : w.len - 1;
+          const float s = fmaf(__uint_as_float(sv[RP + q]), 0.0625f, __uint_as_float(sv[q])) * ks * qf[q];
+          y[q] = (q < rows && key <= last && key < w.len) ? s + static_cast<float>(ve) : -CUDART_INF_F;
+          const float mx = redux_max(y[q]);
+          if (lane == q) wm = mx;
+        }
+        // ---- the tile's largest y of each row, over the four warps
+        float* slot = xch + (nx & 1) * 4 * kRowsMax;
+        if (lane < RP) slot[warp * kRowsMax + lane] = wm;
+        mbar_arrive(bar(C::B_XCH));
+        wait(C::B_XCH, nx & 1);
+        ++nx;
+        const float inv_vs = exp2_int(-ve);
+        float alpha[RP], wt[RP];
+#pragma unroll
+        for (int q = 0; q < RP; ++q) {
+          const float mt = fmaxf(fmaxf(slot[q], slot[kRowsMax + q]), fmaxf(slot[2 * kRowsMax + q], slot[3 * kRowsMax + q]));
+          const float m_new = fmaxf(m[q], mt);
+          const bool none = mt == -CUDART_INF_F;
+          alpha[q] = m[q] == -CUDART_INF_F ? 0.f : ex2_approx(m[q] - m_new);
+          wt[q] = none ? 0.f : ex2_approx(mt - m_new - 8.f);
+          m[q] = m_new;
+          const float pq = ex2_approx(y[q] - (none ? 0.f : mt - 8.f));  // at most 256
+          lsum[q] = fmaf(lsum[q], alpha[q], pq * inv_vs * wt[q]);
+          uint16_t hi, lo;
+          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(0.f), "f"(pq));
+          float h, unused;
+          unpack_e4m3x2(hi, h, unused);
+          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(0.f), "f"((pq - h) * 32.f));
+          const int col = 2 * RP * half + q;
+          smem[C::OFF_P + swz<KW>(col, r % KW)] = static_cast<uint8_t>(hi);
+          smem[C::OFF_P + swz<KW>(col + RP, r % KW)] = static_cast<uint8_t>(lo);
+        }
+        if (key >= w.len) {  // slots without a token may hold NaN, and 0 · NaN is not 0
+          uint4* vrow = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::TILE_BYTES + r * D);
+#pragma unroll
+          for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(bar(C::B_PFULL));
+        wait(C::B_PVDONE, t & 1);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t o[C::NS];
+#pragma unroll
+        for (int c = 0; c < (2 * RP + 15) / 16; ++c)
+          tmem_ld16(lane_addr + C::O_COL + (2 * RP >= 16 ? 2 * RP * half : 0) + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < (2 * RP + 15) / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
+#pragma unroll
+        for (int q = 0; q < RP; ++q) {
+          // fewer than 16 columns in all: both halves are in the one load
+          float hi = __uint_as_float(o[q]), lo = __uint_as_float(o[q + RP]);
+          if (C::HALVES == 2 && 2 * RP < 16) {
+            hi = half ? __uint_as_float(o[(q + 2 * RP) & 15]) : hi;
+            lo = half ? __uint_as_float(o[(q + 3 * RP) & 15]) : lo;
+          }
+          ov[q] = fmaf(ov[q], alpha[q], fmaf(lo, 0.03125f, hi) * wt[q]);
+        }
+      }
+      // ---- the item's sums: l over the keys, O over the halves
+      float* slot = xch + (nx & 1) * 4 * kRowsMax;
+#pragma unroll
+      for (int q = 0; q < RP; ++q) {
+        float l = lsum[q];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (lane == q) slot[warp * kRowsMax + q] = l;
+      }
+      float* other = reinterpret_cast<float*>(smem + C::OFF_HALF);
+      if (D == 64 && half) {
+#pragma unroll
+        for (int q = 0; q < RP; ++q) other[q * 64 + r % 64] = ov[q];
+      }
+      tc_fence_before();
+      mbar_arrive(bar(C::B_XCH));
+      wait(C::B_XCH, nx & 1);
+      ++nx;
+      const bool whole = w.k0 == 0 && w.k1 == w.nt;
+#pragma unroll
+      for (int q = 0; q < RP; ++q) {
+        if (q >= rows) break;
+        const float l = (slot[q] + slot[kRowsMax + q]) + (slot[2 * kRowsMax + q] + slot[3 * kRowsMax + q]);
+        const float o = D == 64 && r < 64 ? ov[q] + other[q * 64 + r % 64] : ov[q];
+        const int f = w.rg * p.rows + q;
+        const size_t qrow = static_cast<size_t>(w.b) * p.Nq + f / p.G;
+        const int h = w.hk * p.G + f % p.G;
+        if (whole) {
+          if (r < D) p.o[(qrow * p.H + h) * D + r] = static_cast<uint16_t>(pack_bf16x2(l > 0.f ? o / l : 0.f, 0.f));
+          if (r == 0)
+            p.lse[(static_cast<size_t>(w.b) * p.H + h) * p.Nq + f / p.G] =
+                l > 0.f ? (m[q] + log2f(l)) * kLn2 : -CUDART_INF_F;
+        } else {
+          const size_t part = (2 * static_cast<size_t>(blockIdx.x) + (w.k0 == 0 ? 1 : 0)) * p.rows + q;
+          if (r < D) p.o_part[part * D + r] = o;
+          if (r == 0) {
+            p.ml_part[part * 2] = m[q];
+            p.ml_part[part * 2 + 1] = l;
+          }
+        }
+      }
+      if (D == 64) {  // the second half's buffer has been read
+        mbar_arrive(bar(C::B_XCH));
+        wait(C::B_XCH, nx & 1);
+        ++nx;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -393,7 +714,7 @@ __global__ void __launch_bounds__(128) fa_cache8_merge_kernel(const Cache8Decode
   const int total = p.tile_start[p.B];
   ctas = min(ctas, total);
   const int s0 = p.tile_start[b], s1 = p.tile_start[b + 1];
-  const int hk = h / p.G, f = i * p.G + h % p.G, rg = f / kRows, r = f - rg * kRows;
+  const int hk = h / p.G, f = i * p.G + h % p.G, rg = f / p.rows, r = f - rg * p.rows;
   const int nt = (s1 - s0) / (p.Hk * p.row_groups);
   const long long t0 = s0 + static_cast<long long>(hk * p.row_groups + rg) * nt;
   const int c0 = nt ? run_of(t0, total, ctas) : 0, c1 = nt ? run_of(t0 + nt - 1, total, ctas) : -1;
@@ -402,7 +723,7 @@ __global__ void __launch_bounds__(128) fa_cache8_merge_kernel(const Cache8Decode
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int c = c0; c <= c1; ++c) {
-    const size_t slot = (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * kRows + r;
+    const size_t slot = (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * p.rows + r;
     const float mc = p.ml_part[slot * 2], lc = p.ml_part[slot * 2 + 1];
     if (mc == -CUDART_INF_F) continue;
     const float m_new = fmaxf(m, mc);
@@ -420,19 +741,35 @@ __global__ void __launch_bounds__(128) fa_cache8_merge_kernel(const Cache8Decode
     p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
 }
 
-template <int D>
-cudaError_t launch_decode8(const Cache8DecodeParams& p, int ctas, cudaStream_t s) {
-  fa_cache8_decode_kernel<D><<<ctas, 128, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+template <int D, int RP>
+cudaError_t launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const Cache8DecodeParams& p, int ctas,
+                           cudaStream_t s) {
+  using C = Dec8Cfg<D, RP>;
+  static SmemLimit smem_limit;
+  cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_cache8_decode_kernel<D, RP>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
+  fa_cache8_decode_kernel<D, RP><<<ctas, C::NUM_THREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long warps = static_cast<long long>(p.B) * p.Nq * p.H;
-  fa_cache8_merge_kernel<D><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, s>>>(p, ctas);
-  return cudaGetLastError();
+  return launch_kernel(fa_cache8_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, s, true, p,
+                       ctas);
+}
+
+template <int D>
+cudaError_t launch_decode8_rows(const CUtensorMap& tk, const CUtensorMap& tv, const Cache8DecodeParams& p, int ctas,
+                                cudaStream_t s) {
+  if (p.rows <= 1) return launch_decode8<D, 1>(tk, tv, p, ctas, s);
+  if (p.rows <= 4) return launch_decode8<D, 4>(tk, tv, p, ctas, s);
+  if (p.rows <= 8) return launch_decode8<D, 8>(tk, tv, p, ctas, s);
+  return launch_decode8<D, 16>(tk, tv, p, ctas, s);
 }
 
 }  // namespace
 
-int cache8_rows() { return kRows; }
+void cache8_row_groups(int rows_total, int* groups, int* rows) {
+  *groups = (rows_total + kRowsMax - 1) / kRowsMax;
+  *rows = (rows_total + *groups - 1) / *groups;
+}
 
 cudaError_t launch_cache8_store(int d, int block, const Cache8StoreParams& p, cudaStream_t s) {
   if (d == 64) {
@@ -447,8 +784,9 @@ cudaError_t launch_cache8_store(int d, int block, const Cache8StoreParams& p, cu
   return launch_store<128, 128>(p, s);
 }
 
-cudaError_t launch_cache8_decode(int d, const Cache8DecodeParams& p, int ctas, cudaStream_t s) {
-  return d == 64 ? launch_decode8<64>(p, ctas, s) : launch_decode8<128>(p, ctas, s);
+cudaError_t launch_cache8_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv, const Cache8DecodeParams& p,
+                                 int ctas, cudaStream_t s) {
+  return d == 64 ? launch_decode8_rows<64>(tk, tv, p, ctas, s) : launch_decode8_rows<128>(tk, tv, p, ctas, s);
 }
 
 }  // namespace fa

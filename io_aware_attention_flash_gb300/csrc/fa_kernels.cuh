@@ -200,7 +200,7 @@ struct Cache8DecodeParams {
   float* ml_part;         // fp32 [2 · CTAs, rows of a group, 2]
   int* tile_start;        // [B + 1] first tile of each sequence in the launch's order, and the total
   int B, Nq, H, Hk, G, num_blocks, table_cols, block, max_seqlen;
-  int row_groups;
+  int row_groups, rows;   // groups of (new token, query head) rows, rows of a group
   int causal;
   float scale_log2;
   uint32_t* err;
@@ -291,8 +291,11 @@ cudaError_t launch_bwd(int d, const CUtensorMap& tq, const CUtensorMap& tk, cons
 cudaError_t launch_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p, int grid,
                           cudaStream_t s);
 cudaError_t launch_cache8_store(int d, int block, const Cache8StoreParams& p, cudaStream_t s);
-int cache8_rows();  // (new token, query head) rows of a decode work item
-cudaError_t launch_cache8_decode(int d, const Cache8DecodeParams& p, int ctas, cudaStream_t s);
+// Row groups that the rows_total (new token, query head) rows over one
+// key/value head are split into, and the rows of each.
+void cache8_row_groups(int rows_total, int* groups, int* rows);
+cudaError_t launch_cache8_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv, const Cache8DecodeParams& p,
+                                 int ctas, cudaStream_t s);
 cudaError_t launch_wait_timeout_selftest(uint32_t* err, uint64_t limit_ns, cudaStream_t s);
 cudaError_t run_microbench(int which, int iters, uint32_t* err, double* result, cudaStream_t s);
 
