@@ -733,6 +733,7 @@ FA_API fa_status fa_fwd_decode_cache8(const void* q, const void* k_codes, const 
   p.num_blocks = num_blocks;
   p.table_cols = table_cols;
   p.block = block;
+  p.block_shift = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
   p.max_seqlen = max_seqlen;
   p.row_groups = w.row_groups;
   p.rows = w.rows;

@@ -33,12 +33,15 @@ __device__ __forceinline__ int scale_exponent(uint32_t amax_bits) {
   return max(biased - 127 - 8 + (mant > 96 ? 1 : 0), kScaleFloor);
 }
 
-// Four floats to four e4m3 codes (nearest even, saturating; NaN stays NaN).
+// Floats to e4m3 codes, the first in the lowest byte (nearest even,
+// saturating; NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+  return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
 }
 // Two e4m3 codes to two floats (exact).
 __device__ __forceinline__ void unpack_e4m3x2(uint32_t code2, float& a, float& b) {
@@ -179,13 +182,13 @@ cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
 // Both products run on the tensor core straight from the codes, keys (or, for
 // P V, head dimensions) as the 128 rows of A and the queries as B:
 //   S^T = K Q^T     A = K tile, K-major;   B = Q,  K-major
-//   O^T = V^T P^T   A = V tile, MN-major;  B = P,  K-major
-// with B in e4m3 as well, split into two factors so that nothing is lost to 8
-// bits: q / s_q = hi + lo / 16 (s_q a power of two for each row; exact for
-// elements above 2^-13 of the row's largest, else off by 2^-22 of that) and
-// p = hi + lo / 32 (off by at most 2^-8 p, as much as rounding to bf16 would
-// be, for p above 2^-13 of the tile's largest).  The factors are separate
-// columns of B, so each product stays one MMA chain.  K's scale (times softmax
+//   O^T = V^T P^T   A = V tile, MN-major;  B = P,  MN-major
+// with B in e4m3 as well, split into two terms so that nothing is lost to 8
+// bits: q / s_q = hi + lo (s_q a power of two for each row; exact for elements
+// above 2^-10 of the row's largest, else off by 2^-18 of that) and p = hi + lo
+// (off by at most 2^-8 p, as much as rounding to bf16 would be, or by 2^-18 of
+// the tile's largest p where that is more).  The terms are separate columns
+// of B: one MMA reads A once for both.  K's scale (times softmax
 // scale and s_q) multiplies the scores; V's goes into P: with
 // y = s c + log2 s_V the tile's largest y of each row is the tile's reference,
 // P = 2^(y - y_max) 256, so that a tile of small probabilities (all but the
@@ -249,10 +252,32 @@ struct Walk {
   }
 };
 
-__device__ __forceinline__ float redux_max(float v) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
+// Maxima (or sums) over the warp of RP values a lane: value i of all lanes ends
+// in lanes 32/RP · i .. +32/RP - 1.  Each step sends half of the values that are
+// left to the lane that keeps them (RP - 1 + log2(32/RP) shuffles in all).
+template <int RP, bool SUM>
+__device__ __forceinline__ float rows_reduce(const float (&y)[RP], int lane) {
+  auto join = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
+  float v[RP];
+#pragma unroll
+  for (int i = 0; i < RP; ++i) v[i] = y[i];
+  int n = RP;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    if (n > 1) {
+      n /= 2;
+      const bool upper = (lane & off) != 0;
+#pragma unroll
+      for (int i = 0; i < RP / 2; ++i)
+        if (i < n) {
+          const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+          v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, off));
+        }
+    } else {
+      v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
+    }
+  }
+  return v[0];
 }
 
 // D(tmem) (+)= A(smem) B(smem), e4m3 inputs, fp32 accumulate, K = 32 a step.
@@ -265,9 +290,10 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint6
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor, kind::f8f6f4: e4m3 A and B (formats 0), fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B (formats 0), both of them
+// K-major or both MN-major, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool mn_major) {
+  return (1u << 4) | ((mn_major ? 3u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
@@ -287,7 +313,8 @@ struct Dec8Cfg {
   static constexpr int OFF_SC = OFF_P + P_BYTES;             // [NST][8 pages][2] scales of K, V
   static constexpr int OFF_QS = OFF_SC + NST * 8 * 2 * 4;    // [RP] score factor of each row
   static constexpr int OFF_XCH = OFF_QS + kRowsMax * 4;      // [2][4 warps][RP]
-  static constexpr int OFF_HALF = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [RP][64] O of the second half (d = 64)
+  static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [4 warps][3: reference, alpha, weight][RP]
+  static constexpr int OFF_HALF = OFF_STAT + 4 * 3 * kRowsMax * 4;  // [RP][64] O of the second half (d = 64)
   static constexpr int OFF_SCAN = OFF_HALF + (D == 64 ? RP * 64 * 4 : 0);  // [6] warp sums, [2] first sequence and its tile
   static constexpr int OFF_BAR = (OFF_SCAN + 8 * 4 + 7) / 8 * 8;
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_SFULL = 2 * NST, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 1,
@@ -308,14 +335,35 @@ struct Dec8Cfg {
 template <int W>
 __device__ __forceinline__ uint32_t swz(int row, int byte) {
   constexpr int MASK = W / 16 - 1;
-  const int line = W == 128 ? row : row >> 1;
+  const int line = row / (128 / W);
   return row * W + ((((byte >> 4) ^ line) & MASK) << 4) + (byte & 15);
 }
-// Descriptor of an operand in W-byte swizzled rows, 8 rows an atom.
+// Descriptor of an operand in W-byte rows swizzled over W bytes (16: not
+// swizzled), 8 rows an atom.  K-major: rows are M or N.  MN-major: rows are K,
+// lbo the distance to the next W bytes of M.
 template <int W>
 __device__ __forceinline__ uint64_t sdesc8(uint32_t saddr, uint32_t lbo) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((8 * W) >> 4) << 32) | (1ull << 46) | ((W == 128 ? 2ull : 4ull) << 61);
+  constexpr uint64_t mode = W == 128 ? 2 : W == 64 ? 4 : W == 32 ? 6 : 0;
+  // Without a swizzle the two distances change places in MN-major.
+  constexpr uint32_t next8 = 8 * W;
+  const uint32_t lead = W == 16 ? next8 : lbo, stride = W == 16 ? lbo : next8;
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (mode << 61);
+}
+
+// N floats of shared memory, four at a time.
+template <int N>
+__device__ __forceinline__ void load_row(const float* src, float (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(src)[i];
+      v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = src[i];
+  }
 }
 
 template <int D, int RP>
@@ -411,26 +459,50 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
 
   if (warp == 4) {
     // ---------------------------------------------------------------- TMA
+    // The run in units of up to 32 pages (32 / ppt tiles) of one item, a page a
+    // lane.  A unit's table entries are read two units ahead and its scales
+    // one unit ahead, so that the copies wait for neither (read where they
+    // were used, the two dependent loads took about 2 us a tile).
     const int ppt = kTile / p.block;  // pages of a tile
+    struct Unit {
+      int kt0, tiles, len, hk, page;  // first tile, tiles; page of this lane (num_blocks: none, reads as zeros)
+      float ks, vs;
+    };
+    int left = 0;  // tiles of the current item not yet in a unit
+    auto next_unit = [&](Unit& u) {
+      if (left == 0) left = w.next<true>(p) ? w.k1 - w.k0 : 0;
+      u.kt0 = w.k1 - left;
+      u.tiles = min(left, 32 / ppt);
+      u.len = w.len;
+      u.hk = w.hk;
+      left -= u.tiles;
+      u.page = p.num_blocks;
+      if (lane < u.tiles * ppt && (u.kt0 * ppt + lane) * p.block < u.len)
+        u.page = __ldg(p.table + static_cast<size_t>(w.b) * p.table_cols + u.kt0 * ppt + lane);
+    };
+    auto load_scales = [&](Unit& u) {
+      const bool token = lane < u.tiles * ppt && (u.kt0 * ppt + lane) * p.block < u.len;
+      u.ks = u.vs = 0.f;
+      if (token && u.page >= 0 && u.page < p.num_blocks) {
+        u.ks = __ldg(p.k_scale + static_cast<size_t>(u.page) * p.Hk + u.hk);
+        u.vs = __ldg(p.v_scale + static_cast<size_t>(u.page) * p.Hk + u.hk);
+      } else {
+        if (token) atomicOr(p.err, kDevErrPage);
+        u.page = p.num_blocks;
+      }
+    };
+    Unit cur, near, far;
+    next_unit(cur);
+    next_unit(near);
+    load_scales(cur);
     int t = 0;
     bool ok = true;
-    while (ok && w.next<true>(p)) {
-      const int* row = p.table + static_cast<size_t>(w.b) * p.table_cols;
-      for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
-        const int st = t % C::NST;
-        const int n_pages = min(ppt, (w.len - kt * kTile + p.block - 1) / p.block);
-        int page = p.num_blocks;  // a page out of range reads as zeros
-        float ks = 0.f, vs = 0.f;
-        if (lane < n_pages) {
-          const int e = __ldg(row + kt * ppt + lane);
-          if (e >= 0 && e < p.num_blocks) {
-            page = e;
-            ks = __ldg(p.k_scale + static_cast<size_t>(e) * p.Hk + w.hk);
-            vs = __ldg(p.v_scale + static_cast<size_t>(e) * p.Hk + w.hk);
-          } else {
-            atomicOr(p.err, kDevErrPage);
-          }
-        }
+    while (ok && cur.tiles > 0) {
+      for (int i = 0; i < cur.tiles; ++i, ++t) {
+        const int st = t % C::NST, kt = cur.kt0 + i;
+        const int n_pages = min(ppt, (cur.len - kt * kTile + p.block - 1) / p.block);
+        const int from = i * ppt + lane;  // this lane's page of the tile
+        const int page = __shfl_sync(0xffffffffu, cur.page, from & 31);
         if (t >= C::NST) ok = wait_bounded(bar(C::B_EMPTY + st), ((t / C::NST) - 1) & 1, abort_flag, p.err, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -438,16 +510,23 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         __syncwarp();
         if (lane < n_pages) {
           const uint32_t off = st * C::TILE_BYTES + lane * p.block * D;
-          tma_load_4d(sb + C::OFF_K + off, &tmK, bar(C::B_FULL + st), 0, 0, w.hk, page);
-          tma_load_4d(sb + C::OFF_V + off, &tmV, bar(C::B_FULL + st), 0, 0, w.hk, page);
+          tma_load_4d(sb + C::OFF_K + off, &tmK, bar(C::B_FULL + st), 0, 0, cur.hk, page);
+          tma_load_4d(sb + C::OFF_V + off, &tmV, bar(C::B_FULL + st), 0, 0, cur.hk, page);
         }
-        if (lane < 8) {
+        if (i == 0) {
+          next_unit(far);
+          load_scales(near);
+        }
+        const float ks = __shfl_sync(0xffffffffu, cur.ks, from & 31), vs = __shfl_sync(0xffffffffu, cur.vs, from & 31);
+        if (lane < ppt) {
           float* sc = reinterpret_cast<float*>(smem + C::OFF_SC) + (st * 8 + lane) * 2;
-          sc[0] = ks;
-          sc[1] = vs;
+          sc[0] = lane < n_pages ? ks : 0.f;
+          sc[1] = lane < n_pages ? vs : 0.f;
         }
         mbar_arrive(bar(C::B_FULL + st));
       }
+      cur = near;
+      near = far;
     }
     // Every copy issued lands before the CTA may exit, whoever aborted.
     for (int s = 0; s < C::NST && s < t; ++s) {
@@ -462,7 +541,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       const uint64_t dK0 = sdesc8<D>(sb + C::OFF_K, 16);
       const uint64_t dV0 = sdesc8<D>(sb + C::OFF_V, 64 * D);  // MN-major; second block of 64 dimensions (d = 64): keys 64..
       const uint64_t dQ = sdesc8<D>(sb + C::OFF_Q, 16);
-      const uint64_t dP = sdesc8<KW>(sb + C::OFF_P, 16);
+      const uint64_t dP = sdesc8<C::NO>(sb + C::OFF_P, 16);  // MN-major: a key's columns are a row
       auto issue_s = [&](int u) -> bool {
         const int st = u % C::NST;
         if (!wait_bounded(bar(C::B_FULL + st), (u / C::NST) & 1, abort_flag, p.err, p.timeout_ns)) return false;
@@ -488,7 +567,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           const int st = t % C::NST;
 #pragma unroll
           for (int kk = 0; kk < KW / 32; ++kk)
-            mma_e4m3(tmem + C::O_COL, sdesc_add(dV0, st * C::TILE_BYTES + kk * 32 * D), sdesc_add(dP, kk * 32), idesc_o,
+            mma_e4m3(tmem + C::O_COL, sdesc_add(dV0, st * C::TILE_BYTES + kk * 32 * D), sdesc_add(dP, kk * 32 * C::NO), idesc_o,
                      kk > 0);
           tc_commit(bar(C::B_PVDONE));
           tc_commit(bar(C::B_EMPTY + st));
@@ -505,6 +584,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     float* xch = reinterpret_cast<float*>(smem + C::OFF_XCH);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
     constexpr int KW = kTile / C::HALVES;
+    constexpr int LPR = 32 / RP;  // lanes that keep one row's statistics
+    const int my_row = lane / LPR;
     int t = 0, nx = 0, n_item = 0;
     bool ok = true;
     auto wait = [&](int i, uint32_t ph) {
@@ -512,107 +593,174 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     };
     for (; __all_sync(0xffffffffu, ok) && w.next<true>(p); ++n_item) {
       const int rows = min(p.rows, p.Nq * p.G - w.rg * p.rows);
-      // ---- the item's queries as two factors (their last reader, the S of the
-      // item before, has completed)
-      for (int q = warp; q < RP; q += 4) {
-        constexpr int E = D / 32;
-        float x[E];
-        float mx = 0.f;
-        const int f = w.rg * p.rows + q;
-        const uint16_t* src =
-            p.q + ((static_cast<size_t>(w.b) * p.Nq + f / p.G) * p.H + w.hk * p.G + f % p.G) * D + E * lane;
+      // Row my_row: its row of q and o, its place in lse, and how many of the
+      // last keys it does not see.
+      int row_q, row_lse, row_hidden;
+      {
+        const int f = min(w.rg * p.rows + my_row, p.Nq * p.G - 1);
+        const int i = f / p.G, h = w.hk * p.G + f - i * p.G;
+        row_q = (w.b * p.Nq + i) * p.H + h;
+        row_lse = (w.b * p.H + h) * p.Nq + i;
+        row_hidden = p.causal ? p.Nq - 1 - i : 0;
+      }
+      // ---- the item's queries as two terms (their last reader, the S of the
+      // item before, has completed); warp w takes rows w, w + 4, ..
+      {
+        constexpr int E = D / 32, NR = (RP + 3) / 4;
+        uint32_t raw[NR][E / 2];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          x[e] = q < rows ? __uint_as_float(static_cast<uint32_t>(src[e]) << 16) : 0.f;
-          mx = fmaxf(mx, fabsf(x[e]));
+        for (int j = 0; j < NR; ++j) {
+          const int q = warp + 4 * j;
+          const uint16_t* src = p.q + static_cast<size_t>(__shfl_sync(0xffffffffu, row_q, (q * LPR) & 31)) * D + E * lane;
+          const bool live = q < rows;
+          if constexpr (E == 4) {
+            const uint2 x = live ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0u, 0u);
+            raw[j][0] = x.x, raw[j][1] = x.y;
+          } else {
+            raw[j][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(src)) : 0u;
+          }
         }
-        mx = redux_max(mx);
-        // smallest power of two s with mx <= 448 s (within the exponents whose inverse is a float)
-        const int e2 = min(max(scale_exponent(__float_as_uint(mx) >> 16), -100), 100);
-        const float inv = exp2_int(-e2);
-        uint32_t hi = 0, lo = 0;
-        float h[E];
-        if constexpr (E == 4) {
-          hi = pack_e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-          unpack_e4m3x2(hi, h[0], h[1]);
-          unpack_e4m3x2(hi >> 16, h[2], h[3]);
-          lo = pack_e4m3x4((x[0] * inv - h[0]) * 16.f, (x[1] * inv - h[1]) * 16.f, (x[2] * inv - h[2]) * 16.f,
-                           (x[3] * inv - h[3]) * 16.f);
-          *reinterpret_cast<uint32_t*>(smem + C::OFF_Q + swz<D>(q, E * lane)) = hi;
-          *reinterpret_cast<uint32_t*>(smem + C::OFF_Q + swz<D>(RP + q, E * lane)) = lo;
-        } else {
-          hi = pack_e4m3x4(x[0] * inv, x[1] * inv, 0.f, 0.f);
-          unpack_e4m3x2(hi, h[0], h[1]);
-          lo = pack_e4m3x4((x[0] * inv - h[0]) * 16.f, (x[1] * inv - h[1]) * 16.f, 0.f, 0.f);
-          *reinterpret_cast<uint16_t*>(smem + C::OFF_Q + swz<D>(q, E * lane)) = static_cast<uint16_t>(hi);
-          *reinterpret_cast<uint16_t*>(smem + C::OFF_Q + swz<D>(RP + q, E * lane)) = static_cast<uint16_t>(lo);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+          const int q = warp + 4 * j;
+          if (q >= RP) break;
+          uint32_t top = 0;
+#pragma unroll
+          for (int u = 0; u < E / 2; ++u) top = __vmaxu2(top, raw[j][u] & 0x7fff7fffu);
+          const uint32_t mx = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+          // smallest power of two s with max <= 448 s (within the exponents whose inverse is a float)
+          const int e2 = min(max(scale_exponent(mx), -100), 100);
+          const float inv = exp2_int(-e2);
+          float x[E], h[E];
+#pragma unroll
+          for (int u = 0; u < E / 2; ++u) {
+            x[2 * u] = bf16lo_to_f32(raw[j][u]) * inv;
+            x[2 * u + 1] = bf16hi_to_f32(raw[j][u]) * inv;
+          }
+          uint32_t hi[2] = {}, lo[2] = {};
+#pragma unroll
+          for (int u = 0; u < E / 2; ++u) {
+            hi[u] = pack_e4m3x2(x[2 * u], x[2 * u + 1]);
+            unpack_e4m3x2(hi[u], h[2 * u], h[2 * u + 1]);
+            lo[u] = pack_e4m3x2(x[2 * u] - h[2 * u], x[2 * u + 1] - h[2 * u + 1]);
+          }
+          uint8_t* at_hi = smem + C::OFF_Q + swz<D>(q, E * lane);
+          uint8_t* at_lo = smem + C::OFF_Q + swz<D>(RP + q, E * lane);
+          if constexpr (E == 4) {
+            *reinterpret_cast<uint32_t*>(at_hi) = hi[0] | (hi[1] << 16);
+            *reinterpret_cast<uint32_t*>(at_lo) = lo[0] | (lo[1] << 16);
+          } else {
+            *reinterpret_cast<uint16_t*>(at_hi) = static_cast<uint16_t>(hi[0]);
+            *reinterpret_cast<uint16_t*>(at_lo) = static_cast<uint16_t>(lo[0]);
+          }
+          if (lane == 0) qs[q] = exp2_int(e2) * p.scale_log2;
         }
-        if (lane == 0) qs[q] = exp2_int(e2) * p.scale_log2;
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(C::B_QREADY));
       wait(C::B_QREADY, n_item & 1);
-      float qf[RP], m[RP], lsum[RP], ov[RP];
+      float qf[RP], lsum[RP], ov[RP];
+      load_row<RP>(qs, qf);
 #pragma unroll
-      for (int q = 0; q < RP; ++q) {
-        qf[q] = qs[q];
-        m[q] = -CUDART_INF_F;
-        lsum[q] = ov[q] = 0.f;
-      }
+      for (int q = 0; q < RP; ++q) lsum[q] = ov[q] = 0.f;
+      float m = -CUDART_INF_F;  // running reference of row my_row
       for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
         const int st = t % C::NST;
         wait(C::B_FULL + st, (t / C::NST) & 1);
         const int key = kt * kTile + r;
-        const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (st * 8 + r / p.block) * 2;
+        const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (st * 8 + (r >> p.block_shift)) * 2;
         const float ks = sc[0], vs = sc[1];
         // log2 of V's scale: 0 for a page of zeros, whatever its scale
         const int ve = vs > 0.f ? static_cast<int>(__float_as_uint(vs) >> 23) - 127 : 0;
+        const float vef = static_cast<float>(ve);
         wait(C::B_SFULL + (t & 1), (t >> 1) & 1);
         __syncwarp();
         tc_fence_after();
         uint32_t sv[C::NS];
 #pragma unroll
-        for (int c = 0; c < C::NS / 16; ++c) tmem_ld16(lane_addr + C::NS * (t & 1) + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
+        for (int c = 0; c < C::NS / 16; ++c)
+          tmem_ld16(lane_addr + C::NS * (t & 1) + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < C::NS / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
         float y[RP];
-        float wm = 0.f;
 #pragma unroll
-        for (int q = 0; q < RP; ++q) {
-          const int f = w.rg * p.rows + q;
-          const int last = p.causal ? w.len - p.Nq + f / p.G : w.len - 1;
-          const float s = fmaf(__uint_as_float(sv[RP + q]), 0.0625f, __uint_as_float(sv[q])) * ks * qf[q];
-          y[q] = (q < rows && key <= last && key < w.len) ? s + static_cast<float>(ve) : -CUDART_INF_F;
-          const float mx = redux_max(y[q]);
-          if (lane == q) wm = mx;
+        for (int q = 0; q < RP; ++q)
+          y[q] = fmaf(__uint_as_float(sv[q]) + __uint_as_float(sv[RP + q]), ks * qf[q], vef);
+        if (kt * kTile + kTile > w.len - (p.causal ? p.Nq - 1 : 0)) {  // some row does not see all of the tile
+#pragma unroll
+          for (int q = 0; q < RP; ++q)
+            if (key >= w.len - __shfl_sync(0xffffffffu, row_hidden, q * LPR)) y[q] = -CUDART_INF_F;
         }
-        // ---- the tile's largest y of each row, over the four warps
+        // ---- the tile's largest y of each row: over the warp, then over the
+        // four warps; lane q does the rest of row q's statistics and leaves
+        // them for its warp
         float* slot = xch + (nx & 1) * 4 * kRowsMax;
-        if (lane < RP) slot[warp * kRowsMax + lane] = wm;
+        {
+          const float wm = rows_reduce<RP, false>(y, lane);
+          if (lane % LPR == 0) slot[warp * kRowsMax + my_row] = wm;
+        }
         mbar_arrive(bar(C::B_XCH));
         wait(C::B_XCH, nx & 1);
         ++nx;
-        const float inv_vs = exp2_int(-ve);
-        float alpha[RP], wt[RP];
-#pragma unroll
-        for (int q = 0; q < RP; ++q) {
-          const float mt = fmaxf(fmaxf(slot[q], slot[kRowsMax + q]), fmaxf(slot[2 * kRowsMax + q], slot[3 * kRowsMax + q]));
-          const float m_new = fmaxf(m[q], mt);
+        float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT) + warp * 3 * kRowsMax;
+        {
+          const int q = my_row;
+          const float mt = fmaxf(fmax3(slot[q], slot[kRowsMax + q], slot[2 * kRowsMax + q]), slot[3 * kRowsMax + q]);
+          const float m_new = fmaxf(m, mt);
           const bool none = mt == -CUDART_INF_F;
-          alpha[q] = m[q] == -CUDART_INF_F ? 0.f : ex2_approx(m[q] - m_new);
-          wt[q] = none ? 0.f : ex2_approx(mt - m_new - 8.f);
-          m[q] = m_new;
-          const float pq = ex2_approx(y[q] - (none ? 0.f : mt - 8.f));  // at most 256
-          lsum[q] = fmaf(lsum[q], alpha[q], pq * inv_vs * wt[q]);
-          uint16_t hi, lo;
-          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(0.f), "f"(pq));
-          float h, unused;
-          unpack_e4m3x2(hi, h, unused);
-          asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(0.f), "f"((pq - h) * 32.f));
-          const int col = 2 * RP * half + q;
-          smem[C::OFF_P + swz<KW>(col, r % KW)] = static_cast<uint8_t>(hi);
-          smem[C::OFF_P + swz<KW>(col + RP, r % KW)] = static_cast<uint8_t>(lo);
+          if (lane % LPR == 0) {
+            stat[q] = none ? 0.f : mt - 8.f;
+            stat[kRowsMax + q] = m == -CUDART_INF_F ? 0.f : ex2_approx(m - m_new);
+            stat[2 * kRowsMax + q] = none ? 0.f : ex2_approx(mt - m_new - 8.f);
+          }
+          m = m_new;
+          __syncwarp();
+        }
+        const float inv_vs = exp2_int(-ve);
+        {
+          float ref[RP], alpha[RP], wt[RP];
+          load_row<RP>(stat, ref);
+          load_row<RP>(stat + kRowsMax, alpha);
+          load_row<RP>(stat + 2 * kRowsMax, wt);
+          uint32_t hi[(RP + 3) / 4], lo[(RP + 3) / 4];
+#pragma unroll
+          for (int q = 0; q < RP; ++q) {
+            y[q] = ex2_approx(y[q] - ref[q]);  // P, at most 256
+            lsum[q] = fmaf(lsum[q], alpha[q], y[q] * (inv_vs * wt[q]));
+          }
+#pragma unroll
+          for (int q = 0; q < RP; q += 2) {
+            const float p1 = q + 1 < RP ? y[q + 1 < RP ? q + 1 : q] : 0.f;
+            float h0, h1;
+            const uint32_t c = pack_e4m3x2(y[q], p1);
+            unpack_e4m3x2(c, h0, h1);
+            const uint32_t e = pack_e4m3x2(y[q] - h0, p1 - h1);
+            if (q % 4 == 0) {
+              hi[q / 4] = c;
+              lo[q / 4] = e;
+            } else {
+              hi[q / 4] |= c << 16;
+              lo[q / 4] |= e << 16;
+            }
+          }
+          // the key's columns: hi terms of the rows, then lo terms (d = 64: of
+          // its half of the keys)
+          const int k = r % KW;
+          if constexpr (RP == 16) {
+            uint4* row0 = reinterpret_cast<uint4*>(smem + C::OFF_P + swz<C::NO>(k, 32 * half));
+            uint4* row1 = reinterpret_cast<uint4*>(smem + C::OFF_P + swz<C::NO>(k, 32 * half + 16));
+            *row0 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *row1 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else if constexpr (RP == 8) {
+            *reinterpret_cast<uint4*>(smem + C::OFF_P + swz<C::NO>(k, 16 * half)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+          } else if constexpr (RP == 4) {
+            *reinterpret_cast<uint2*>(smem + C::OFF_P + k * 16 + 8 * half) = make_uint2(hi[0], lo[0]);
+          } else {
+            static_assert(RP == 1 || RP >= 4, "row counts that the P layout has");
+            *reinterpret_cast<uint16_t*>(smem + C::OFF_P + k * 16 + 2 * half) =
+                static_cast<uint16_t>((hi[0] & 0xffu) | (lo[0] << 8));
+          }
         }
         if (key >= w.len) {  // slots without a token may hold NaN, and 0 · NaN is not 0
           uint4* vrow = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::TILE_BYTES + r * D);
@@ -625,32 +773,31 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         wait(C::B_PVDONE, t & 1);
         __syncwarp();
         tc_fence_after();
-        uint32_t o[C::NS];
+        constexpr int NL = 2 * RP >= 16 ? 2 * RP : 16;  // columns of one half, or all of them
+        uint32_t o[NL];
 #pragma unroll
-        for (int c = 0; c < (2 * RP + 15) / 16; ++c)
-          tmem_ld16(lane_addr + C::O_COL + (2 * RP >= 16 ? 2 * RP * half : 0) + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
+        for (int c = 0; c < NL / 16; ++c)
+          tmem_ld16(lane_addr + C::O_COL + (2 * RP >= 16 ? 2 * RP * half : 0) + 16 * c,
+                    *reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < (2 * RP + 15) / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
+        for (int c = 0; c < NL / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
+        float alpha[RP], wt[RP];
+        load_row<RP>(stat + kRowsMax, alpha);
+        load_row<RP>(stat + 2 * kRowsMax, wt);
 #pragma unroll
         for (int q = 0; q < RP; ++q) {
-          // fewer than 16 columns in all: both halves are in the one load
-          float hi = __uint_as_float(o[q]), lo = __uint_as_float(o[q + RP]);
-          if (C::HALVES == 2 && 2 * RP < 16) {
-            hi = half ? __uint_as_float(o[(q + 2 * RP) & 15]) : hi;
-            lo = half ? __uint_as_float(o[(q + 3 * RP) & 15]) : lo;
-          }
-          ov[q] = fmaf(ov[q], alpha[q], fmaf(lo, 0.03125f, hi) * wt[q]);
+          float sum = __uint_as_float(o[q]) + __uint_as_float(o[q + RP]);
+          if (C::HALVES == 2 && 2 * RP < 16)  // both halves are in the one load
+            sum = half ? __uint_as_float(o[(q + 2 * RP) % NL]) + __uint_as_float(o[(q + 3 * RP) % NL]) : sum;
+          ov[q] = fmaf(ov[q], alpha[q], sum * wt[q]);
         }
       }
       // ---- the item's sums: l over the keys, O over the halves
       float* slot = xch + (nx & 1) * 4 * kRowsMax;
-#pragma unroll
-      for (int q = 0; q < RP; ++q) {
-        float l = lsum[q];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-        if (lane == q) slot[warp * kRowsMax + q] = l;
+      {
+        const float l = rows_reduce<RP, true>(lsum, lane);
+        if (lane % LPR == 0) slot[warp * kRowsMax + my_row] = l;
       }
       float* other = reinterpret_cast<float*>(smem + C::OFF_HALF);
       if (D == 64 && half) {
@@ -661,29 +808,39 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       mbar_arrive(bar(C::B_XCH));
       wait(C::B_XCH, nx & 1);
       ++nx;
+      // the tile loop's statistics of this warp make room for the rows' factors
+      float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT) + warp * 3 * kRowsMax;
       const bool whole = w.k0 == 0 && w.k1 == w.nt;
-#pragma unroll
-      for (int q = 0; q < RP; ++q) {
-        if (q >= rows) break;
-        const float l = (slot[q] + slot[kRowsMax + q]) + (slot[2 * kRowsMax + q] + slot[3 * kRowsMax + q]);
-        const float o = D == 64 && r < 64 ? ov[q] + other[q * 64 + r % 64] : ov[q];
-        const int f = w.rg * p.rows + q;
-        const size_t qrow = static_cast<size_t>(w.b) * p.Nq + f / p.G;
-        const int h = w.hk * p.G + f % p.G;
-        if (whole) {
-          if (r < D) p.o[(qrow * p.H + h) * D + r] = static_cast<uint16_t>(pack_bf16x2(l > 0.f ? o / l : 0.f, 0.f));
-          if (r == 0)
-            p.lse[(static_cast<size_t>(w.b) * p.H + h) * p.Nq + f / p.G] =
-                l > 0.f ? (m[q] + log2f(l)) * kLn2 : -CUDART_INF_F;
-        } else {
-          const size_t part = (2 * static_cast<size_t>(blockIdx.x) + (w.k0 == 0 ? 1 : 0)) * p.rows + q;
-          if (r < D) p.o_part[part * D + r] = o;
-          if (r == 0) {
-            p.ml_part[part * 2] = m[q];
-            p.ml_part[part * 2 + 1] = l;
+      const float l = (slot[my_row] + slot[kRowsMax + my_row]) + (slot[2 * kRowsMax + my_row] + slot[3 * kRowsMax + my_row]);
+      const size_t part0 = (2 * static_cast<size_t>(blockIdx.x) + (w.k0 == 0 ? 1 : 0)) * p.rows;
+      if (lane % LPR == 0) {
+        stat[my_row] = l > 0.f ? 1.f / l : 0.f;
+        reinterpret_cast<int*>(stat)[kRowsMax + my_row] = row_q;
+        if (warp == 0 && my_row < rows) {
+          if (whole) {
+            p.lse[row_lse] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+          } else {
+            p.ml_part[(part0 + my_row) * 2] = m;
+            p.ml_part[(part0 + my_row) * 2 + 1] = l;
           }
         }
       }
+      __syncwarp();
+      if (r < D) {
+        float inv[RP];
+        load_row<RP>(stat, inv);
+#pragma unroll
+        for (int q = 0; q < RP; ++q) {
+          if (q >= rows) break;
+          const float o = D == 64 ? ov[q] + other[q * 64 + r % 64] : ov[q];
+          if (whole)
+            p.o[static_cast<size_t>(reinterpret_cast<int*>(stat)[kRowsMax + q]) * D + r] =
+                static_cast<uint16_t>(pack_bf16x2(o * inv[q], 0.f));
+          else
+            p.o_part[(part0 + q) * D + r] = o;
+        }
+      }
+      __syncwarp();
       if (D == 64) {  // the second half's buffer has been read
         mbar_arrive(bar(C::B_XCH));
         wait(C::B_XCH, nx & 1);

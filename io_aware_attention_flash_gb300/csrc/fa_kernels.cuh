@@ -199,7 +199,7 @@ struct Cache8DecodeParams {
   float* o_part;          // fp32 [2 · CTAs, rows of a group, d]
   float* ml_part;         // fp32 [2 · CTAs, rows of a group, 2]
   int* tile_start;        // [B + 1] first tile of each sequence in the launch's order, and the total
-  int B, Nq, H, Hk, G, num_blocks, table_cols, block, max_seqlen;
+  int B, Nq, H, Hk, G, num_blocks, table_cols, block, block_shift, max_seqlen;  // block = 1 << block_shift
   int row_groups, rows;   // groups of (new token, query head) rows, rows of a group
   int causal;
   float scale_log2;
