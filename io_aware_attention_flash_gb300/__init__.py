@@ -12,7 +12,7 @@ module allocates outputs and workspace and calls the binding.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 from typing import NamedTuple
 
 import torch
@@ -135,38 +135,53 @@ def flash_attention(q, k, v, causal: bool = False, scale=None):
 # ---------------------------------------------------------------------------
 # Grouped heads over packed batches: H query heads share Hk key/value heads.
 # ---------------------------------------------------------------------------
-def _allocating_on(stream):
-    """What a call on `stream` allocates belongs to that stream, so that its
-    memory is not handed to another one while the kernels still use it."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _on_stream(fn):
+    """A call on a stream of its own runs with that stream current: what it
+    allocates belongs to that stream, so that its memory is not handed to
+    another one while the kernels still use it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return fn(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kwargs)
+    return call
 
 
-def attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None, stream=None):
+@_on_stream
+def attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None):
     """Packed batch with grouped heads: q [T,H,d], k and v [T,Hk,d] (H a
     multiple of Hk; slices of one wider projection are taken as they are).
     Returns (o [T,H,d] bf16, lse [H,T] fp32); rows behind the last sequence
-    get o = 0, lse = -inf."""
-    with _allocating_on(stream):
-        o = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
-        lse = torch.empty((q.shape[1], q.shape[0]), device=q.device, dtype=torch.float32)
-    fa_fwd_grouped(q, k, v, o, lse, cu_seqlens, max_seqlen, causal, scale, stream, zero_tail=True)
+    get o = 0, lse = -inf.  stream: the stream to run on (default: the
+    current one)."""
+    checked = _binding._grouped(q, k, v, cu_seqlens)
+    T, H, d = q.shape
+    o = torch.empty((T, H, d), device=q.device, dtype=torch.bfloat16)
+    lse = torch.empty((H, T), device=q.device, dtype=torch.float32)
+    _binding._launch_fwd_grouped(checked, q, k, v, o, lse, cu_seqlens, max_seqlen, causal, scale, None, True)
     return o, lse
 
 
+@_on_stream
 def attention_backward_grouped(q, k, v, o, dout, lse, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None,
-                               stream=None, workspace=None):
+                               workspace=None):
     """Returns (dq [T,H,d], dk, dv [T,Hk,d]), zero in rows behind the last
-    sequence.  dk and dv are summed over the query heads that share them."""
-    T, H, d = q.shape
-    Hk = k.shape[1]
-    with _allocating_on(stream):
-        if workspace is None:
-            n = fa_bwd_grouped_workspace_bytes(cu_seqlens.numel() - 1, max_seqlen, T, H, Hk, d, causal)
-            workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
-        dq = torch.empty((T, H, d), device=q.device, dtype=torch.bfloat16)
-        dk, dv = (torch.empty((T, Hk, d), device=q.device, dtype=torch.bfloat16) for _ in range(2))
-    fa_bwd_grouped(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max_seqlen, causal, scale, stream,
-                   zero_tail=True)
+    sequence.  dk and dv are summed over the query heads that share them.
+    stream: the stream to run on (default: the current one)."""
+    checked = _binding._grouped(q, k, v, cu_seqlens)
+    dev, T, H, Hk, d, nseq = checked[:6]
+    device = q.device
+    if workspace is None:
+        n = fa_bwd_grouped_workspace_bytes(nseq, max_seqlen, T, H, Hk, d, causal)
+        workspace = torch.empty(n, device=device, dtype=torch.uint8)
+    else:
+        n = _binding._nbytes(workspace, dev)
+    dq = torch.empty((T, H, d), device=device, dtype=torch.bfloat16)
+    dk = torch.empty((T, Hk, d), device=device, dtype=torch.bfloat16)
+    dv = torch.empty((T, Hk, d), device=device, dtype=torch.bfloat16)
+    _binding._launch_bwd_grouped(checked, q, k, v, o, dout, lse, dq, dk, dv, workspace, n, cu_seqlens, max_seqlen, causal,
+                                 scale, None, True)
     return dq, dk, dv
 
 
@@ -220,18 +235,23 @@ def cache8_store(k, v, cache: Cache8, block_table, cu_seqlens, start, max_new: i
     fa_cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new, stream)
 
 
+@_on_stream
 def attention_decode_cache8(q, cache: Cache8, block_table, seqlens, max_seqlen: int, causal: bool = False, scale=None,
-                            stream=None, workspace=None):
+                            workspace=None):
     """Decode over the 8-bit paged cache: q [B,Nq,H,d] (Nq <= 8 newest tokens),
     seqlens int32 [B] cached tokens (the new ones among them; 0 for an empty
     slot), max_seqlen at least every length.  Returns (o [B,Nq,H,d] bf16, lse
-    [B,H,Nq] fp32).  causal as in attention_decode."""
-    B, Nq, H, d = q.shape
-    with _allocating_on(stream):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, H, Nq), device=q.device, dtype=torch.float32)
-        if workspace is None:
-            n = fa_decode_cache8_workspace_bytes(B, Nq, H, cache.k.shape[1], max_seqlen, d)
-            workspace = torch.empty(max(n, 16), device=q.device, dtype=torch.uint8)
-    fa_fwd_decode_cache8(q, cache, block_table, seqlens, o, lse, workspace, max_seqlen, causal, scale, stream)
+    [B,H,Nq] fp32).  causal as in attention_decode.  stream: the stream to run
+    on (default: the current one)."""
+    checked = _binding._decode_cache8(q, cache, block_table, seqlens)
+    dev, B, Nq, H, d, _, Hk = checked[:7]
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, Nq), device=q.device, dtype=torch.float32)
+    if workspace is None:
+        n = fa_decode_cache8_workspace_bytes(B, Nq, H, Hk, max_seqlen, d)
+        workspace = torch.empty(n, device=q.device, dtype=torch.uint8)
+    else:
+        n = _binding._nbytes(workspace, dev)
+    _binding._launch_decode_cache8(checked, q, cache, block_table, seqlens, o, lse, workspace, n, max_seqlen, causal, scale,
+                                   None)
     return o, lse

@@ -135,42 +135,55 @@ def _scale(scale, d):
     return float(d) ** -0.5 if scale is None else float(scale)
 
 
-def _stream_of(stream, device) -> int:
+# The checks of the entry points below run on every call of a decoding step, so
+# each is one expression where all is well; what is wrong is found out after.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream_of(stream, dev: int) -> int:
     """The given stream, or the current one of the tensors' device."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _on(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _device_of(name: str, t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return dev
 
 
-def _int32(name: str, t: torch.Tensor, shape, device) -> None:
-    if t.dtype != torch.int32 or t.device != device or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+def _dense(name: str, t: torch.Tensor, dtype, shape, dev: int) -> None:
+    """Checks a contiguous tensor of the given type and shape on device dev."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return
+    if t.dtype is not dtype and dtype in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"{name} must be {str(dtype)[6:]} (got {t.dtype}); other types are not supported")
+    raise ValueError(f"{name} must be a contiguous {str(dtype)[6:]} tensor of shape {tuple(shape)} on cuda:{dev} (got "
+                     f"{t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device})")
 
 
-def _rows(name: str, t: torch.Tensor, rows: int, heads: int, d: int, device) -> int:
+def _rows(name: str, t: torch.Tensor, rows: int, heads: int, d: int, dev: int) -> int:
     """Checks a bf16 [rows, heads, d] tensor whose rows may be further apart
     than heads·d elements (a slice of a wider projection); returns the row
     stride in elements."""
-    if t.dtype != torch.bfloat16:
+    n = heads * d
+    if t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == (rows, heads, d):
+        if t.is_contiguous() or rows <= 1 and t[0].is_contiguous():
+            return n
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (s1 == d or heads == 1) and s0 >= n and s0 % 8 == 0:
+            return s0
+        raise ValueError(f"{name}: each row of {heads} heads of {d} must be contiguous, and rows a multiple of 8 "
+                         f"elements and at least {n} apart (strides {t.stride()})")
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16 (got {t.dtype}); fp32 and other types are not supported")
-    if not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (rows, heads, d):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, heads, d)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    s0, s1, s2 = t.stride()
-    if (d > 1 and s2 != 1) or (heads > 1 and s1 != d):
-        raise ValueError(f"{name}: each row of {heads} heads of {d} must be contiguous (strides {t.stride()})")
-    if rows <= 1:
-        return heads * d
-    if s0 < heads * d or s0 % 8:
-        raise ValueError(f"{name}: rows must be a multiple of 8 elements and at least {heads * d} apart (stride {s0})")
-    return s0
+    raise ValueError(f"{name} must be a tensor of shape {(rows, heads, d)} on cuda:{dev} (got {tuple(t.shape)}, {t.device})")
+
+
+def _nbytes(workspace: torch.Tensor, dev: int) -> int:
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace.numel() * workspace.element_size()
 
 
 # ---------------------------------------------------------------------------
@@ -243,114 +256,146 @@ def fa_bwd_varlen(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max_
 
 
 def _grouped(q, k, v, cu_seqlens):
-    """Checks of q, k, v and cu_seqlens: (T, H, Hk, d, nseq, row strides)."""
+    """Checks of q, k, v and cu_seqlens: (device, T, H, Hk, d, nseq, row strides)."""
+    dev = _device_of("q", q)
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [T, H, d] and [T, Hk, d]")
     T, H, d = q.shape
     Hk = k.shape[1]
-    ld = _rows("q", q, T, H, d, q.device), _rows("k", k, T, Hk, d, q.device), _rows("v", v, T, Hk, d, q.device)
+    ldq, ldk, ldv = _rows("q", q, T, H, d, dev), _rows("k", k, T, Hk, d, dev), _rows("v", v, T, Hk, d, dev)
     nseq = cu_seqlens.numel() - 1
-    _int32("cu_seqlens", cu_seqlens, (nseq + 1,), q.device)
-    return T, H, Hk, d, nseq, ld
+    _dense("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), dev)
+    return dev, T, H, Hk, d, nseq, ldq, ldk, ldv
+
+
+def _launch_fwd_grouped(checked, q, k, v, o, lse, cu_seqlens, max_seqlen, causal, scale, stream, zero_tail) -> None:
+    dev, T, H, Hk, d, nseq, ldq, ldk, ldv = checked
+    _check("fa_fwd_grouped", lib().fa_fwd_grouped(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), nseq,
+        max_seqlen, T, H, Hk, d, ldq, ldk, ldv, _scale(scale, d), bool(causal), zero_tail, _stream_of(stream, dev)))
 
 
 def fa_fwd_grouped(q, k, v, o, lse, cu_seqlens, max_seqlen: int, causal: bool, scale=None, stream=None,
                    zero_tail: bool = False) -> None:
     """q, o [T, H, d], k, v [T, Hk, d] (rows of q, k, v may be slices of wider
     ones), lse fp32 [H, T]; query head h reads key/value head h // (H // Hk)."""
-    T, H, Hk, d, nseq, ld = _grouped(q, k, v, cu_seqlens)
-    _bf16("o", o, (T, H, d))
-    _f32("lse", lse, (H, T))
-    _on(q.device, o=o, lse=lse)
-    _check("fa_fwd_grouped", lib().fa_fwd_grouped(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), nseq,
-        max_seqlen, T, H, Hk, d, *ld, _scale(scale, d), bool(causal), bool(zero_tail), _stream_of(stream, q.device)))
+    checked = _grouped(q, k, v, cu_seqlens)
+    dev, T, H, _, d = checked[:5]
+    _dense("o", o, torch.bfloat16, (T, H, d), dev)
+    _dense("lse", lse, torch.float32, (H, T), dev)
+    _launch_fwd_grouped(checked, q, k, v, o, lse, cu_seqlens, max_seqlen, causal, scale, stream, bool(zero_tail))
 
 
 def fa_bwd_grouped_workspace_bytes(nseq: int, max_seqlen: int, total: int, H: int, Hk: int, d: int,
                                    causal: bool) -> int:
-    return int(lib().fa_bwd_grouped_workspace_bytes(nseq, max_seqlen, total, H, Hk, d, bool(causal)))
+    return lib().fa_bwd_grouped_workspace_bytes(nseq, max_seqlen, total, H, Hk, d, bool(causal))
+
+
+def _launch_bwd_grouped(checked, q, k, v, o, dout, lse, dq, dk, dv, workspace, nbytes, cu_seqlens, max_seqlen, causal,
+                        scale, stream, zero_tail) -> None:
+    dev, T, H, Hk, d, nseq, ldq, ldk, ldv = checked
+    _dense("o", o, torch.bfloat16, (T, H, d), dev)
+    _dense("dout", dout, torch.bfloat16, (T, H, d), dev)
+    _dense("lse", lse, torch.float32, (H, T), dev)
+    _check("fa_bwd_grouped", lib().fa_bwd_grouped(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), nbytes, cu_seqlens.data_ptr(), nseq, max_seqlen, T, H, Hk, d,
+        ldq, ldk, ldv, _scale(scale, d), bool(causal), zero_tail, _stream_of(stream, dev)))
 
 
 def fa_bwd_grouped(q, k, v, o, dout, lse, dq, dk, dv, workspace, cu_seqlens, max_seqlen: int, causal: bool,
                    scale=None, stream=None, zero_tail: bool = False) -> None:
-    T, H, Hk, d, nseq, ld = _grouped(q, k, v, cu_seqlens)
-    for n, t, heads in (("o", o, H), ("dout", dout, H), ("dq", dq, H), ("dk", dk, Hk), ("dv", dv, Hk)):
-        _bf16(n, t, (T, heads, d))
-    _f32("lse", lse, (H, T))
-    _on(q.device, o=o, dout=dout, lse=lse, dq=dq, dk=dk, dv=dv, workspace=workspace)
-    _check("fa_bwd_grouped", lib().fa_bwd_grouped(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(), dq.data_ptr(),
-        dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        cu_seqlens.data_ptr(), nseq, max_seqlen, T, H, Hk, d, *ld, _scale(scale, d), bool(causal), bool(zero_tail),
-        _stream_of(stream, q.device)))
+    checked = _grouped(q, k, v, cu_seqlens)
+    dev, T, H, Hk, d = checked[:5]
+    _dense("dq", dq, torch.bfloat16, (T, H, d), dev)
+    _dense("dk", dk, torch.bfloat16, (T, Hk, d), dev)
+    _dense("dv", dv, torch.bfloat16, (T, Hk, d), dev)
+    _launch_bwd_grouped(checked, q, k, v, o, dout, lse, dq, dk, dv, workspace, _nbytes(workspace, dev), cu_seqlens,
+                        max_seqlen, causal, scale, stream, bool(zero_tail))
 
 
-def _cache8(cache, device):
-    """Checks of a cache's four tensors: (num_blocks, Hk, block, d)."""
+def _cache8(cache, dev: int):
+    """Checks of a cache's four tensors: its page shape (num_blocks, Hk, block, d)."""
     k, v, k_scale, v_scale = cache
-    if k.dim() != 4:
-        raise ValueError("cache pages must be [num_blocks, Hk, block, d]")
     shape = k.shape
-    for name, t in (("cache.k", k), ("cache.v", v)):
-        if t.dtype != torch.float8_e4m3fn:
-            raise TypeError(f"{name} must be float8_e4m3fn (got {t.dtype})")
-        if t.device != device or not t.is_contiguous() or t.shape != shape:
-            raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}")
-    for name, t in (("cache.k_scale", k_scale), ("cache.v_scale", v_scale)):
-        if t.dtype != torch.float32 or t.device != device or not t.is_contiguous() or t.shape != shape[:2]:
-            raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(shape[:2])} on {device}")
+    if len(shape) != 4:
+        raise ValueError("cache pages must be [num_blocks, Hk, block, d]")
+    _dense("cache.k", k, torch.float8_e4m3fn, shape, dev)
+    _dense("cache.v", v, torch.float8_e4m3fn, shape, dev)
+    _dense("cache.k_scale", k_scale, torch.float32, shape[:2], dev)
+    _dense("cache.v_scale", v_scale, torch.float32, shape[:2], dev)
     return shape
+
+
+def _block_table(t: torch.Tensor, rows: int, dev: int) -> int:
+    if t.dim() != 2:
+        raise ValueError("block_table must be [B, cols]")
+    cols = t.shape[1]
+    _dense("block_table", t, torch.int32, (rows, cols), dev)
+    return cols
 
 
 def fa_cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new: int, stream=None) -> None:
     """Appends k, v [T, Hk, d] (rows may be slices of wider ones) to the cache
     (k, v, k_scale, v_scale): rows cu_seqlens[b] .. of sequence b become its
     tokens start[b], start[b] + 1, ..."""
+    dev = _device_of("k", k)
     if k.dim() != 3:
         raise ValueError("k must be [T, Hk, d]")
-    device = k.device
     T, Hk, d = k.shape
-    ldk, ldv = _rows("k", k, T, Hk, d, device), _rows("v", v, T, Hk, d, device)
-    num_blocks, heads, block, dim = _cache8(cache, device)
-    if (heads, dim) != (Hk, d):
+    ldk, ldv = _rows("k", k, T, Hk, d, dev), _rows("v", v, T, Hk, d, dev)
+    num_blocks, heads, block, dim = _cache8(cache, dev)
+    if heads != Hk or dim != d:
         raise ValueError(f"the cache holds {heads} heads of {dim}, k and v have {Hk} of {d}")
-    B, cols = block_table.shape
-    _int32("block_table", block_table, (B, cols), device)
-    _int32("cu_seqlens", cu_seqlens, (B + 1,), device)
-    _int32("start", start, (B,), device)
+    B = start.numel()
+    cols = _block_table(block_table, B, dev)
+    _dense("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev)
+    _dense("start", start, torch.int32, (B,), dev)
     ck, cv, sk, sv = cache
     _check("fa_cache8_store", lib().fa_cache8_store(
         k.data_ptr(), v.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(), sv.data_ptr(), block_table.data_ptr(),
         cu_seqlens.data_ptr(), start.data_ptr(), B, max_new, T, num_blocks, cols, Hk, block, d, ldk, ldv,
-        _stream_of(stream, device)))
+        _stream_of(stream, dev)))
 
 
 def fa_decode_cache8_workspace_bytes(B: int, Nq: int, H: int, Hk: int, max_seqlen: int, d: int) -> int:
-    return int(lib().fa_decode_cache8_workspace_bytes(B, Nq, H, Hk, max_seqlen, d))
+    return lib().fa_decode_cache8_workspace_bytes(B, Nq, H, Hk, max_seqlen, d)
+
+
+def _decode_cache8(q, cache, block_table, seqlens):
+    """Checks of the inputs: (device, B, Nq, H, d, num_blocks, Hk, block, table columns)."""
+    dev = _device_of("q", q)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Nq, H, d]")
+    B, Nq, H, d = q.shape
+    _dense("q", q, torch.bfloat16, q.shape, dev)
+    num_blocks, Hk, block, dim = _cache8(cache, dev)
+    if dim != d:
+        raise ValueError(f"the cache holds heads of {dim}, q has {d}")
+    cols = _block_table(block_table, B, dev)
+    _dense("seqlens", seqlens, torch.int32, (B,), dev)
+    return dev, B, Nq, H, d, num_blocks, Hk, block, cols
+
+
+def _launch_decode_cache8(checked, q, cache, block_table, seqlens, o, lse, workspace, nbytes, max_seqlen, causal, scale,
+                          stream) -> None:
+    dev, B, Nq, H, d, num_blocks, Hk, block, cols = checked
+    ck, cv, sk, sv = cache
+    _check("fa_fwd_decode_cache8", lib().fa_fwd_decode_cache8(
+        q.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(), sv.data_ptr(), block_table.data_ptr(),
+        seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, B, Nq, H, Hk, num_blocks, cols,
+        block, max_seqlen, d, _scale(scale, d), bool(causal), _stream_of(stream, dev)))
 
 
 def fa_fwd_decode_cache8(q, cache, block_table, seqlens, o, lse, workspace, max_seqlen: int, causal: bool, scale=None,
                          stream=None) -> None:
     """q, o [B, Nq, H, d] over the cache (k, v, k_scale, v_scale); lse fp32 [B, H, Nq]."""
-    B, Nq, H, d = q.shape
-    device = q.device
-    _bf16("q", q, (B, Nq, H, d))
-    _bf16("o", o, (B, Nq, H, d))
-    _f32("lse", lse, (B, H, Nq))
-    num_blocks, Hk, block, dim = _cache8(cache, device)
-    if dim != d:
-        raise ValueError(f"the cache holds heads of {dim}, q has {d}")
-    cols = block_table.shape[1]
-    _int32("block_table", block_table, (B, cols), device)
-    _int32("seqlens", seqlens, (B,), device)
-    _on(device, o=o, lse=lse, workspace=workspace)
-    ck, cv, sk, sv = cache
-    _check("fa_fwd_decode_cache8", lib().fa_fwd_decode_cache8(
-        q.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(), sv.data_ptr(), block_table.data_ptr(),
-        seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), B, Nq, H, Hk, num_blocks, cols, block, max_seqlen, d,
-        _scale(scale, d), bool(causal), _stream_of(stream, device)))
+    checked = _decode_cache8(q, cache, block_table, seqlens)
+    dev, B, Nq, H = checked[:4]
+    _dense("o", o, torch.bfloat16, q.shape, dev)
+    _dense("lse", lse, torch.float32, (B, H, Nq), dev)
+    _launch_decode_cache8(checked, q, cache, block_table, seqlens, o, lse, workspace, _nbytes(workspace, dev), max_seqlen,
+                          causal, scale, stream)
 
 
 def fa_decode_workspace_bytes(B: int, H: int, Nq: int, Nk: int, d: int) -> int:
