@@ -385,7 +385,7 @@ fa::SeqView grouped_view(const int* cu, int nseq, int max_seqlen, int total, int
 fa_status check_cache8(int B, int num_blocks, int table_cols, int Hk, int block, int d) {
   if (d != 64 && d != 128) return FA_ERR_HEAD_DIM;
   if (block != 16 && block != 32 && block != 64 && block != 128) return FA_ERR_SHAPE;
-  if (B <= 0 || num_blocks <= 0 || table_cols <= 0 || Hk <= 0 || Hk > 65535) return FA_ERR_SHAPE;
+  if (B <= 0 || num_blocks <= 0 || table_cols <= 0 || Hk <= 0 || Hk > 16384) return FA_ERR_SHAPE;
   if (static_cast<long long>(num_blocks) * Hk * block > 0x7fffffffLL * 16) return FA_ERR_SHAPE;
   return FA_OK;
 }
@@ -662,6 +662,7 @@ FA_API fa_status fa_cache8_store(const void* k, const void* v, void* k_codes, vo
                                  int d, long long ldk, long long ldv, void* stream) {
   FA_TRY(check_cache8(B, num_blocks, table_cols, Hk, block, d));
   if (max_new <= 0 || total <= 0) return FA_ERR_SHAPE;
+  if (static_cast<long long>(B) * ((static_cast<long long>(max_new) + block - 2) / block + 1) > 0x7fffffffLL) return FA_ERR_SHAPE;
   if (!k || !v || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !cu_seqlens || !start)
     return FA_ERR_NULL;
   if (!aligned16(k) || !aligned16(v) || !aligned16(k_codes) || !aligned16(v_codes)) return FA_ERR_ALIGN;

@@ -51,42 +51,44 @@ __device__ __forceinline__ void unpack_e4m3x2(uint32_t code2, float& a, float& b
   asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}" : "=f"(a), "=f"(b) : "r"(h2));
 }
 
+// The larger of two bf16 in each half; of a NaN and a number the number.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // One group of TG threads quantises the new tokens of one (page, head) of K or
 // V: each thread keeps CH 16-byte chunks of them in registers between the
-// maximum and the rounding, so the input is read once.  A page that already
-// holds tokens keeps its scale if that suffices; otherwise they are rounded
-// again to the larger one.  Groups of consecutive heads are consecutive, so a
-// warp's loads cover whole rows of the token-major input.
-template <int CH, int TG, int D, int BLOCK>
-__global__ void __launch_bounds__(256) fa_cache8_store_kernel(const Cache8StoreParams p) {
+// maximum and the rounding, so the input is read once, and its loads do not
+// wait for the page table's.  A page that already holds tokens keeps its scale
+// if that suffices; otherwise they are rounded again to the larger one.
+// Groups of consecutive heads are consecutive, so a block's loads cover whole
+// rows of the token-major input.
+template <int CH, int TG, int D, int BLOCK, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) fa_cache8_store_kernel(const Cache8StoreParams p) {
   static_assert(CH * TG * 8 == D * BLOCK, "a group's chunks cover a page and head");
-  constexpr int GPB = 256 / TG;  // groups per block
-  constexpr int C8 = D / 8;      // chunks per token
-  __shared__ uint32_t warp_max[8];
+  constexpr int GPB = NT / TG;  // groups per block
+  constexpr int C8 = D / 8;     // chunks per token
+  __shared__ uint32_t warp_max[NT / 32];
   const int group = threadIdx.x / TG, tid = threadIdx.x % TG;
-  const long long item = static_cast<long long>(blockIdx.x) * GPB + group;
-  // item = ((sequence · blocks + block) · 2 + V) · Hk + head
-  const int head = static_cast<int>(item % p.Hk);
-  const long long rest = item / p.Hk;
-  const bool is_v = rest & 1;
-  const int nth = static_cast<int>((rest >> 1) % p.blocks);
-  const int b = static_cast<int>((rest >> 1) / p.blocks);
+  // blockIdx.x: (sequence, block of tokens); the groups run over K's heads, then V's
+  const int b = blockIdx.x / p.blocks, nth = blockIdx.x - b * p.blocks;
+  const int which = blockIdx.y * GPB + group;
+  const bool is_v = which >= p.Hk;
+  const int head = is_v ? which - p.Hk : which;
   int page = -1, old = 0, lo = 0, hi = 0;  // the page; its tokens [0, old) are held, [lo, hi) are new
   int src = 0;                             // input row of slot 0
-  if (b < p.B) {
+  if (which < 2 * p.Hk) {
     const int first = min(max(__ldg(p.cu_seqlens + b), 0), p.total);
     const int count = min(max(__ldg(p.cu_seqlens + b + 1), first), p.total) - first;
     const int start = __ldg(p.start + b);
     const long long end = static_cast<long long>(start) + min(count, p.max_new);
     const long long blk = static_cast<long long>(start) / BLOCK + nth;
     if (start < 0) {
-      if (count > 0 && nth == 0 && tid == 0) atomicOr(p.err, kDevErrPage);
+      if (count > 0 && tid == 0) atomicOr(p.err, kDevErrPage);
     } else if (count > 0 && blk * BLOCK < end) {
-      page = blk < p.table_cols ? __ldg(p.table + static_cast<size_t>(b) * p.table_cols + blk) : -1;
-      if (page < 0 || page >= p.num_blocks) {
-        if (tid == 0) atomicOr(p.err, kDevErrPage);
-        page = -1;
-      }
+      if (blk < p.table_cols) page = __ldg(p.table + static_cast<size_t>(b) * p.table_cols + blk);
       const long long base = blk * BLOCK;
       old = static_cast<int>(max(0LL, start - base));
       lo = old;
@@ -94,78 +96,92 @@ __global__ void __launch_bounds__(256) fa_cache8_store_kernel(const Cache8StoreP
       src = first + static_cast<int>(base - start);
     }
   }
-  const uint16_t* x = is_v ? p.v : p.k;
+  const bool touched = hi > lo;
+  if (TG == NT ? !touched : __syncthreads_or(touched) == 0) return;
+  // Chunk c of a thread: token t0 + c · STEP of the page, the same 8 elements.
+  static_assert(TG % C8 == 0, "a thread's chunks lie below one another");
+  constexpr int STEP = TG / C8;
+  const int t0 = tid / C8;
   const long long ld = is_v ? p.ldv : p.ldk;
+  const uint16_t* x = (is_v ? p.v : p.k) + (static_cast<long long>(src) + t0) * ld + head * D + (tid % C8) * 8;
   uint4 val[CH];
-  uint32_t amax2 = 0;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int chunk = c * TG + tid, t = chunk / C8;
     val[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (page >= 0 && t >= lo && t < hi)
-      val[c] = *reinterpret_cast<const uint4*>(x + (static_cast<long long>(src) + t) * ld + head * D + (chunk % C8) * 8);
+    if (t0 + c * STEP >= lo && t0 + c * STEP < hi) val[c] = *reinterpret_cast<const uint4*>(x + c * (STEP * ld));
   }
+  const bool live = touched && page >= 0 && page < p.num_blocks;
+  if (touched && !live && tid == 0) atomicOr(p.err, kDevErrPage);
+  const size_t ph = live ? static_cast<size_t>(page) * p.Hk + head : 0;
+  float* scale = (is_v ? p.v_scale : p.k_scale) + ph;
+  const float held = live && old > 0 ? *scale : 0.f;
+  // Largest magnitude as bf16 bits.  Infinities and NaN do not set the scale
+  // (the maximum passes over NaN; where it is infinite, once more without).
+  auto largest = [&](bool finite) {
+    uint32_t top = 0;
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const uint32_t w[4] = {val[c].x, val[c].y, val[c].z, val[c].w};
+    for (int c = 0; c < CH; ++c) {
+      const uint32_t w[4] = {val[c].x, val[c].y, val[c].z, val[c].w};
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t m = w[u] & 0x7fff7fffu;
-      amax2 = __vmaxu2(amax2, m & ~__vcmpgeu2(m, 0x7f807f80u));  // infinities and NaN do not set the scale
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t m = w[u] & 0x7fff7fffu;
+        top = max_bf16x2(top, finite ? m & ~__vcmpgeu2(m, 0x7f807f80u) : m);
+      }
     }
-  }
-  uint32_t amax = max(amax2 & 0xffffu, amax2 >> 16);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-  if (TG > 32) {
+    return max(top & 0xffffu, top >> 16);
+  };
+  uint32_t amax = largest(false);
+  if (amax >= 0x7f80u) amax = largest(true);
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if (TG > 32) {  // (and every thread has read the scale held before one of them writes the new one)
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = amax;
     __syncthreads();
     const int w0 = group * (TG / 32);
 #pragma unroll
     for (int w = 0; w < TG / 32; ++w) amax = max(amax, warp_max[w0 + w]);
   }
-  if (page < 0) return;
-  const size_t ph = static_cast<size_t>(page) * p.Hk + head;
-  float* scale = (is_v ? p.v_scale : p.k_scale) + ph;
-  const float held = old > 0 ? *scale : 0.f;
+  if (!live) return;
   const float s = fmaxf(exp2_int(scale_exponent(amax)), held);
   // 1 / s of a power of two, by its exponent
   const float inv = exp2_int(127 - static_cast<int>((__float_as_uint(s) >> 23) & 255u));
-  uint2* out = reinterpret_cast<uint2*>((is_v ? p.v_codes : p.k_codes) + ph * (BLOCK * D));
+  const bool again = s > held;
+  if (tid == 0 && again) *scale = s;
+  const uint64_t inv2 = f2_pack(inv, inv);
+  auto codes = [&](uint32_t a, uint32_t b) {  // four values, two a word
+    float v[4];
+    f2_unpack(fmul2(f2_pack(bf16lo_to_f32(a), bf16hi_to_f32(a)), inv2), v[0], v[1]);
+    f2_unpack(fmul2(f2_pack(bf16lo_to_f32(b), bf16hi_to_f32(b)), inv2), v[2], v[3]);
+    return pack_e4m3x4(v[0], v[1], v[2], v[3]);
+  };
+  uint2* out = reinterpret_cast<uint2*>((is_v ? p.v_codes : p.k_codes) + ph * (BLOCK * D)) + tid;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    const int chunk = c * TG + tid, t = chunk / C8;
+    const int t = t0 + c * STEP;
     if (t >= lo && t < hi) {
-      out[chunk] = make_uint2(
-          pack_e4m3x4(bf16lo_to_f32(val[c].x) * inv, bf16hi_to_f32(val[c].x) * inv, bf16lo_to_f32(val[c].y) * inv,
-                      bf16hi_to_f32(val[c].y) * inv),
-          pack_e4m3x4(bf16lo_to_f32(val[c].z) * inv, bf16hi_to_f32(val[c].z) * inv, bf16lo_to_f32(val[c].w) * inv,
-                      bf16hi_to_f32(val[c].w) * inv));
-    } else if (t < old && s > held) {
-      const uint2 code = out[chunk];
+      out[c * TG] = make_uint2(codes(val[c].x, val[c].y), codes(val[c].z, val[c].w));
+    } else if (t < old && again) {
+      const uint2 code = out[c * TG];
       const float f = held * inv;
       float v[8];
       unpack_e4m3x2(code.x, v[0], v[1]);
       unpack_e4m3x2(code.x >> 16, v[2], v[3]);
       unpack_e4m3x2(code.y, v[4], v[5]);
       unpack_e4m3x2(code.y >> 16, v[6], v[7]);
-      out[chunk] = make_uint2(pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
-                              pack_e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+      out[c * TG] = make_uint2(pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
+                               pack_e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
     }
   }
-  if (TG > 32) __syncthreads();  // every thread has read the scale held
-  else __syncwarp();
-  if (tid == 0) *scale = s;
 }
 
 template <int D, int BLOCK>
 cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
   constexpr int CHUNKS = D * BLOCK / 8;
   constexpr int TG = CHUNKS <= 256 ? 32 : CHUNKS / 8;
-  const long long items = static_cast<long long>(p.B) * p.blocks * 2 * p.Hk;
-  const long long ctas = (items * TG + 255) / 256;
-  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  fa_cache8_store_kernel<CHUNKS / TG, TG, D, BLOCK><<<static_cast<unsigned>(ctas), 256, 0, s>>>(p);
+  constexpr int NT = TG > 128 ? TG : 128;
+  const long long x = static_cast<long long>(p.B) * p.blocks, y = (2LL * p.Hk * TG + NT - 1) / NT;
+  if (x > 0x7fffffffLL || y > 65535) return cudaErrorInvalidConfiguration;
+  const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
+  fa_cache8_store_kernel<CHUNKS / TG, TG, D, BLOCK, NT><<<grid, NT, 0, s>>>(p);
   return cudaGetLastError();
 }
 
