@@ -316,7 +316,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool mn_major) {
 template <int D, int RP>
 struct Dec8Cfg {
   static constexpr int TILE_BYTES = kTile * D;               // 128 keys
-  static constexpr int NST = D == 128 ? 3 : 6;               // ring stages (K and V tile each)
+  static constexpr int NST = D == 128 ? 3 : 5;               // ring stages (K and V tile each)
   static constexpr int NS = 2 * RP < 16 ? 16 : 2 * RP;       // columns of S: the rows' hi, then lo factors
   static constexpr int HALVES = 128 / D;
   static constexpr int NO = 2 * RP * HALVES < 16 ? 16 : 2 * RP * HALVES;
@@ -326,22 +326,22 @@ struct Dec8Cfg {
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
   static constexpr int OFF_Q = OFF_V + NST * TILE_BYTES;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_SC = OFF_P + P_BYTES;             // [NST][8 pages][2] scales of K, V
+  static constexpr int OFF_SC = OFF_P + 2 * P_BYTES;         // (two P buffers) [NST][8 pages][2] scales of K, V
   static constexpr int OFF_QS = OFF_SC + NST * 8 * 2 * 4;    // [RP] score factor of each row
   static constexpr int OFF_XCH = OFF_QS + kRowsMax * 4;      // [2][4 warps][RP]
-  static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [4 warps][3: reference, alpha, weight][RP]
-  static constexpr int OFF_HALF = OFF_STAT + 4 * 3 * kRowsMax * 4;  // [RP][64] O of the second half (d = 64)
+  static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [2 tiles][4 warps][3: reference, alpha, weight][RP]
+  static constexpr int OFF_HALF = OFF_STAT + 2 * 4 * 3 * kRowsMax * 4;  // [RP][64] O of the second half (d = 64)
   static constexpr int OFF_SCAN = OFF_HALF + (D == 64 ? RP * 64 * 4 : 0);  // [6] warp sums, [2] first sequence and its tile
   static constexpr int OFF_BAR = (OFF_SCAN + 8 * 4 + 7) / 8 * 8;
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_SFULL = 2 * NST, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 1,
-                       B_XCH = B_PVDONE + 1, B_QREADY = B_XCH + 1, B_DRAIN = B_QREADY + 1, NBAR = B_DRAIN + 1;
+                       B_XCH = B_PVDONE + 2, B_QREADY = B_XCH + 1, B_DRAIN = B_QREADY + 1, NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;    // slack to align the base to 1024
   static constexpr int NUM_THREADS = 6 * 32;
-  static constexpr uint32_t COLS = 2 * NS + NO;
-  static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : 128;
+  static constexpr uint32_t COLS = 2 * NS + 2 * NO;
+  static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
   static constexpr uint32_t O_COL = 2 * NS;
-  static_assert(COLS <= 128, "tensor memory budget");
+  static_assert(COLS <= 256, "tensor memory for two CTAs on an SM");
   static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs on an SM");
   static_assert(OFF_Q % 1024 == 0 && OFF_P % 512 == 0 && (D == 64 || OFF_P % 1024 == 0), "swizzle atoms");
 };
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     }
     for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_SFULL + i), 1);
     mbar_init(bar(C::B_PFULL), 128);
-    mbar_init(bar(C::B_PVDONE), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_PVDONE + i), 1);
     mbar_init(bar(C::B_XCH), 128);
     mbar_init(bar(C::B_QREADY), 128);
     mbar_init(bar(C::B_DRAIN), 1);
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       tmem_relinquish();
     }
   } else if (warp < 4) {  // factors of rows that do not exist stay zero for good
-    for (int i = threadIdx.x - 32; i < (C::Q_BYTES + C::P_BYTES) / 16; i += 96)
+    for (int i = threadIdx.x - 32; i < (C::Q_BYTES + 2 * C::P_BYTES) / 16; i += 96)
       reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   if (idle) return;
@@ -583,9 +583,9 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           const int st = t % C::NST;
 #pragma unroll
           for (int kk = 0; kk < KW / 32; ++kk)
-            mma_e4m3(tmem + C::O_COL, sdesc_add(dV0, st * C::TILE_BYTES + kk * 32 * D), sdesc_add(dP, kk * 32 * C::NO), idesc_o,
-                     kk > 0);
-          tc_commit(bar(C::B_PVDONE));
+            mma_e4m3(tmem + C::O_COL + C::NO * (t & 1), sdesc_add(dV0, st * C::TILE_BYTES + kk * 32 * D),
+                     sdesc_add(dP, (t & 1) * C::P_BYTES + kk * 32 * C::NO), idesc_o, kk > 0);
+          tc_commit(bar(C::B_PVDONE + (t & 1)));
           tc_commit(bar(C::B_EMPTY + st));
         }
       }
@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float* xch = reinterpret_cast<float*>(smem + C::OFF_XCH);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+    float* stats = reinterpret_cast<float*>(smem + C::OFF_STAT) + warp * 3 * kRowsMax;
     constexpr int KW = kTile / C::HALVES;
     constexpr int LPR = 32 / RP;  // lanes that keep one row's statistics
     const int my_row = lane / LPR;
@@ -680,6 +681,33 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
 #pragma unroll
       for (int q = 0; q < RP; ++q) lsum[q] = ov[q] = 0.f;
       float m = -CUDART_INF_F;  // running reference of row my_row
+      // O of tile u (its statistics are still in their buffer) into the running one.
+      auto add_o = [&](int u) {
+        const float* stat = stats + (u & 1) * 4 * 3 * kRowsMax;
+        wait(C::B_PVDONE + (u & 1), (u >> 1) & 1);
+        __syncwarp();
+        tc_fence_after();
+        constexpr int NL = 2 * RP >= 16 ? 2 * RP : 16;  // columns of one half, or all of them
+        uint32_t o[NL];
+#pragma unroll
+        for (int c = 0; c < NL / 16; ++c)
+          tmem_ld16(lane_addr + C::O_COL + C::NO * (u & 1) + (2 * RP >= 16 ? 2 * RP * half : 0) + 16 * c,
+                    *reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < NL / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
+        float alpha[RP], wt[RP];
+        load_row<RP>(stat + kRowsMax, alpha);
+        load_row<RP>(stat + 2 * kRowsMax, wt);
+#pragma unroll
+        for (int q = 0; q < RP; ++q) {
+          float sum = __uint_as_float(o[q]) + __uint_as_float(o[q + RP]);
+          if (C::HALVES == 2 && 2 * RP < 16)  // both halves are in the one load
+            sum = half ? __uint_as_float(o[(q + 2 * RP) % NL]) + __uint_as_float(o[(q + 3 * RP) % NL]) : sum;
+          ov[q] = fmaf(ov[q], alpha[q], sum * wt[q]);
+        }
+        tc_fence_before();
+      };
       for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
         const int st = t % C::NST;
         wait(C::B_FULL + st, (t / C::NST) & 1);
@@ -719,7 +747,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         mbar_arrive(bar(C::B_XCH));
         wait(C::B_XCH, nx & 1);
         ++nx;
-        float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT) + warp * 3 * kRowsMax;
+        float* stat = stats + (t & 1) * 4 * 3 * kRowsMax;
         {
           const int q = my_row;
           const float mt = fmaxf(fmax3(slot[q], slot[kRowsMax + q], slot[2 * kRowsMax + q]), slot[3 * kRowsMax + q]);
@@ -763,18 +791,19 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           // the key's columns: hi terms of the rows, then lo terms (d = 64: of
           // its half of the keys)
           const int k = r % KW;
+          const uint32_t pbuf = C::OFF_P + (t & 1) * C::P_BYTES;
           if constexpr (RP == 16) {
-            uint4* row0 = reinterpret_cast<uint4*>(smem + C::OFF_P + swz<C::NO>(k, 32 * half));
-            uint4* row1 = reinterpret_cast<uint4*>(smem + C::OFF_P + swz<C::NO>(k, 32 * half + 16));
+            uint4* row0 = reinterpret_cast<uint4*>(smem + pbuf + swz<C::NO>(k, 32 * half));
+            uint4* row1 = reinterpret_cast<uint4*>(smem + pbuf + swz<C::NO>(k, 32 * half + 16));
             *row0 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *row1 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           } else if constexpr (RP == 8) {
-            *reinterpret_cast<uint4*>(smem + C::OFF_P + swz<C::NO>(k, 16 * half)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+            *reinterpret_cast<uint4*>(smem + pbuf + swz<C::NO>(k, 16 * half)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
           } else if constexpr (RP == 4) {
-            *reinterpret_cast<uint2*>(smem + C::OFF_P + k * 16 + 8 * half) = make_uint2(hi[0], lo[0]);
+            *reinterpret_cast<uint2*>(smem + pbuf + k * 16 + 8 * half) = make_uint2(hi[0], lo[0]);
           } else {
             static_assert(RP == 1 || RP >= 4, "row counts that the P layout has");
-            *reinterpret_cast<uint16_t*>(smem + C::OFF_P + k * 16 + 2 * half) =
+            *reinterpret_cast<uint16_t*>(smem + pbuf + k * 16 + 2 * half) =
                 static_cast<uint16_t>((hi[0] & 0xffu) | (lo[0] << 8));
           }
         }
@@ -786,29 +815,11 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         fence_proxy_async_smem();
         tc_fence_before();
         mbar_arrive(bar(C::B_PFULL));
-        wait(C::B_PVDONE, t & 1);
-        __syncwarp();
-        tc_fence_after();
-        constexpr int NL = 2 * RP >= 16 ? 2 * RP : 16;  // columns of one half, or all of them
-        uint32_t o[NL];
-#pragma unroll
-        for (int c = 0; c < NL / 16; ++c)
-          tmem_ld16(lane_addr + C::O_COL + (2 * RP >= 16 ? 2 * RP * half : 0) + 16 * c,
-                    *reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < NL / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
-        float alpha[RP], wt[RP];
-        load_row<RP>(stat + kRowsMax, alpha);
-        load_row<RP>(stat + 2 * kRowsMax, wt);
-#pragma unroll
-        for (int q = 0; q < RP; ++q) {
-          float sum = __uint_as_float(o[q]) + __uint_as_float(o[q + RP]);
-          if (C::HALVES == 2 && 2 * RP < 16)  // both halves are in the one load
-            sum = half ? __uint_as_float(o[(q + 2 * RP) % NL]) + __uint_as_float(o[(q + 3 * RP) % NL]) : sum;
-          ov[q] = fmaf(ov[q], alpha[q], sum * wt[q]);
-        }
+        // The product of the tile before is ready by now: waiting for this one's
+        // would leave the warps idle for its whole latency.
+        if (kt > w.k0) add_o(t - 1);
       }
+      add_o(t - 1);
       // ---- the item's sums: l over the keys, O over the halves
       float* slot = xch + (nx & 1) * 4 * kRowsMax;
       {
@@ -824,8 +835,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       mbar_arrive(bar(C::B_XCH));
       wait(C::B_XCH, nx & 1);
       ++nx;
-      // the tile loop's statistics of this warp make room for the rows' factors
-      float* stat = reinterpret_cast<float*>(smem + C::OFF_STAT) + warp * 3 * kRowsMax;
+      float* stat = stats;  // the tile loop's statistics of this warp make room for the rows' factors
       const bool whole = w.k0 == 0 && w.k1 == w.nt;
       const float l = (slot[my_row] + slot[kRowsMax + my_row]) + (slot[2 * kRowsMax + my_row] + slot[3 * kRowsMax + my_row]);
       const size_t part0 = (2 * static_cast<size_t>(blockIdx.x) + (w.k0 == 0 ? 1 : 0)) * p.rows;
