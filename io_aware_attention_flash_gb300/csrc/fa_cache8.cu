@@ -212,9 +212,10 @@ cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
 // accuracy, and O is rescaled in registers from tile to tile as in the usual
 // online softmax.
 //
-// Warps 0-3 (thread r: key r for scores and P, head dimension r for O), warp 4
-// loads (lane i: page i of the tile, its TMA copies and its two scales), warp
-// 5 issues the MMAs.  d = 64: A needs 128 rows, so V is read as two blocks of
+// One or two warpgroups (thread r: key r for scores and P, head dimension r for
+// O; two share the rows from 8 on, as a tile's time is the length of one warp's
+// instruction chain), a warp that loads (lane i: page i of the tile, its TMA
+// copies and its two scales) and one that issues the MMAs.  d = 64: A needs 128 rows, so V is read as two blocks of
 // 64 dimensions, keys 0-63 and 64-127 of the tile, each against P's own half
 // of the keys as columns of their own: thread r keeps dimension r mod 64 of
 // half r / 64, and the halves are added once for each item.
@@ -315,9 +316,14 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool mn_major) {
 
 template <int D, int RP>
 struct Dec8Cfg {
+  static constexpr int WG = RP >= 8 ? 2 : 1;                 // warpgroups that share the rows
+  static constexpr int RW = RP / WG;                         // rows of one
+  static constexpr int NCW = 4 * WG;                         // compute warps; then the TMA and the MMA warp
+  static constexpr int NUM_WARPS = NCW + 2;
+  static constexpr int NUM_THREADS = 32 * NUM_WARPS;
   static constexpr int TILE_BYTES = kTile * D;               // 128 keys
   static constexpr int NST = D == 128 ? 3 : 5;               // ring stages (K and V tile each)
-  static constexpr int NS = 2 * RP < 16 ? 16 : 2 * RP;       // columns of S: the rows' hi, then lo factors
+  static constexpr int NS = 2 * RP < 16 ? 16 : 2 * RP;       // columns of S: a warpgroup's rows' hi, then lo terms
   static constexpr int HALVES = 128 / D;
   static constexpr int NO = 2 * RP * HALVES < 16 ? 16 : 2 * RP * HALVES;
   static constexpr int Q_BYTES = NS * D;
@@ -329,15 +335,15 @@ struct Dec8Cfg {
   static constexpr int OFF_SC = OFF_P + 2 * P_BYTES;         // (two P buffers) [NST][8 pages][2] scales of K, V
   static constexpr int OFF_QS = OFF_SC + NST * 8 * 2 * 4;    // [RP] score factor of each row
   static constexpr int OFF_XCH = OFF_QS + kRowsMax * 4;      // [2][4 warps][RP]
-  static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [2 tiles][4 warps][3: reference, alpha, weight][RP]
-  static constexpr int OFF_HALF = OFF_STAT + 2 * 4 * 3 * kRowsMax * 4;  // [RP][64] O of the second half (d = 64)
-  static constexpr int OFF_SCAN = OFF_HALF + (D == 64 ? RP * 64 * 4 : 0);  // [6] warp sums, [2] first sequence and its tile
-  static constexpr int OFF_BAR = (OFF_SCAN + 8 * 4 + 7) / 8 * 8;
+  static constexpr int STAT_WARP = 3 * RW < 4 ? 4 : 3 * RW;  // reference, alpha, weight of each row
+  static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [2 tiles][NCW][STAT_WARP]
+  static constexpr int OFF_HALF = OFF_STAT + 2 * NCW * STAT_WARP * 4;  // [RP][64] O of the second half (d = 64)
+  static constexpr int OFF_SCAN = OFF_HALF + (D == 64 ? RP * 64 * 4 : 0);  // [2] first sequence, its tile; [warps] sums
+  static constexpr int OFF_BAR = (OFF_SCAN + (2 + NUM_WARPS) * 4 + 7) / 8 * 8;
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_SFULL = 2 * NST, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 1,
-                       B_XCH = B_PVDONE + 2, B_QREADY = B_XCH + 1, B_DRAIN = B_QREADY + 1, NBAR = B_DRAIN + 1;
+                       B_XCH = B_PVDONE + 2, B_QREADY = B_XCH + 2, B_DRAIN = B_QREADY + 1, NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;    // slack to align the base to 1024
-  static constexpr int NUM_THREADS = 6 * 32;
   static constexpr uint32_t COLS = 2 * NS + 2 * NO;
   static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
   static constexpr uint32_t O_COL = 2 * NS;
@@ -365,6 +371,16 @@ __device__ __forceinline__ uint64_t sdesc8(uint32_t saddr, uint32_t lbo) {
   const uint32_t lead = W == 16 ? next8 : lbo, stride = W == 16 ? lbo : next8;
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (mode << 61);
+}
+
+// 8 or 16 columns of this warp's TMEM lanes.
+template <int N>
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, uint32_t (&v)[N]) {
+  static_assert(N == 8 || N == 16, "shapes in use");
+  if constexpr (N == 8) tmem_ld8(taddr, v);
+  else tmem_ld16(taddr, v);
+  tmem_wait_ld();
+  reg_fence(v);
 }
 
 // N floats of shared memory, four at a time.
@@ -404,17 +420,17 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
   int mine = 0;
   for (int b = threadIdx.x; b < p.B; b += C::NUM_THREADS) mine += seq_tiles(p, b);
   mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) scan[warp] = mine;
-  if (warp == 4 && lane == 0) {
+  if (lane == 0) scan[2 + warp] = mine;
+  if (warp == C::NCW && lane == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(bar(C::B_FULL + s), 32);
       mbar_init(bar(C::B_EMPTY + s), 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_SFULL + i), 1);
-    mbar_init(bar(C::B_PFULL), 128);
+    mbar_init(bar(C::B_PFULL), 32 * C::NCW);
     for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_PVDONE + i), 1);
-    mbar_init(bar(C::B_XCH), 128);
-    mbar_init(bar(C::B_QREADY), 128);
+    for (int i = 0; i < C::WG; ++i) mbar_init(bar(C::B_XCH + i), 128);
+    mbar_init(bar(C::B_QREADY), 32 * C::NCW);
     mbar_init(bar(C::B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -422,7 +438,10 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     tma_prefetch_desc(&tmV);
   }
   __syncthreads();
-  const int total = (scan[0] + scan[1] + scan[2] + scan[3] + scan[4] + scan[5]) * per;
+  int total = 0;
+#pragma unroll
+  for (int i = 0; i < C::NUM_WARPS; ++i) total += scan[2 + i];
+  total *= per;
   if (blockIdx.x == 0 && threadIdx.x == 0) p.tile_start[p.B] = total;
   const int ctas = min(static_cast<int>(gridDim.x), total);  // every one of them has a tile
   const bool idle = static_cast<int>(blockIdx.x) >= ctas;
@@ -450,8 +469,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         }
       }
       if (n > 0 && w.t >= first && w.t < first + n) {
-        scan[6] = b;
-        scan[7] = first;
+        scan[0] = b;
+        scan[1] = first;
       }
       base += __shfl_sync(0xffffffffu, sum, 31);
       if (blockIdx.x != 0 && base > w.t) break;
@@ -460,8 +479,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
       tmem_relinquish();
     }
-  } else if (warp < 4) {  // factors of rows that do not exist stay zero for good
-    for (int i = threadIdx.x - 32; i < (C::Q_BYTES + 2 * C::P_BYTES) / 16; i += 96)
+  } else if (warp < C::NCW) {  // terms of rows that do not exist stay zero for good
+    for (int i = threadIdx.x - 32; i < (C::Q_BYTES + 2 * C::P_BYTES) / 16; i += 32 * (C::NCW - 1))
       reinterpret_cast<uint4*>(smem + C::OFF_Q)[i] = make_uint4(0u, 0u, 0u, 0u);
   }
   if (idle) return;
@@ -470,10 +489,10 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  w.b = scan[6];
-  w.seq0 = scan[7];
+  w.b = scan[0];
+  w.seq0 = scan[1];
 
-  if (warp == 4) {
+  if (warp == C::NCW) {
     // ---------------------------------------------------------------- TMA
     // The run in units of up to 32 pages (32 / ppt tiles) of one item, a page a
     // lane.  A unit's table entries are read two units ahead and its scales
@@ -549,7 +568,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       const int last = s + ((t - 1 - s) / C::NST) * C::NST;
       wait_drain(bar(C::B_FULL + s), (last / C::NST) & 1, p.err, p.timeout_ns);
     }
-  } else if (warp == 5) {
+  } else if (warp == C::NCW + 1) {
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_e4m3(128, C::NS, false), idesc_o = idesc_e4m3(128, C::NO, true);
@@ -594,15 +613,19 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     }
   } else {
     // ---------------------------------------------------------------- softmax, P, running O
-    const int r = threadIdx.x;  // key of the tile; head dimension (and half) of O
+    constexpr int RW = C::RW;
+    const int wg = C::WG == 2 ? warp >> 2 : 0, quarter = warp & 3;
+    const int row0 = wg * RW;            // first of this warpgroup's rows
+    const int r = quarter * 32 + lane;   // TMEM lane: key of the tile; head dimension (and half) of O
     const int half = r / D;
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     float* xch = reinterpret_cast<float*>(smem + C::OFF_XCH);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
-    float* stats = reinterpret_cast<float*>(smem + C::OFF_STAT) + warp * 3 * kRowsMax;
+    float* stats = reinterpret_cast<float*>(smem + C::OFF_STAT) + warp * C::STAT_WARP;
+    const int xbar = C::B_XCH + wg;
     constexpr int KW = kTile / C::HALVES;
-    constexpr int LPR = 32 / RP;  // lanes that keep one row's statistics
-    const int my_row = lane / LPR;
+    constexpr int LPR = 32 / RW;  // lanes that keep one row's statistics
+    const int my_row = lane / LPR;  // within the warpgroup's rows
     int t = 0, nx = 0, n_item = 0;
     bool ok = true;
     auto wait = [&](int i, uint32_t ph) {
@@ -610,26 +633,26 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     };
     for (; __all_sync(0xffffffffu, ok) && w.next<true>(p); ++n_item) {
       const int rows = min(p.rows, p.Nq * p.G - w.rg * p.rows);
-      // Row my_row: its row of q and o, its place in lse, and how many of the
-      // last keys it does not see.
+      // Row row0 + my_row: its row of q and o, its place in lse, and how many of
+      // the last keys it does not see.
       int row_q, row_lse, row_hidden;
       {
-        const int f = min(w.rg * p.rows + my_row, p.Nq * p.G - 1);
+        const int f = min(w.rg * p.rows + row0 + my_row, p.Nq * p.G - 1);
         const int i = f / p.G, h = w.hk * p.G + f - i * p.G;
         row_q = (w.b * p.Nq + i) * p.H + h;
         row_lse = (w.b * p.H + h) * p.Nq + i;
         row_hidden = p.causal ? p.Nq - 1 - i : 0;
       }
       // ---- the item's queries as two terms (their last reader, the S of the
-      // item before, has completed); warp w takes rows w, w + 4, ..
+      // item before, has completed); a warpgroup's warps take turns at its rows
       {
-        constexpr int E = D / 32, NR = (RP + 3) / 4;
+        constexpr int E = D / 32, NR = (RW + 3) / 4;
         uint32_t raw[NR][E / 2];
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
-          const int q = warp + 4 * j;
+          const int q = quarter + 4 * j;
           const uint16_t* src = p.q + static_cast<size_t>(__shfl_sync(0xffffffffu, row_q, (q * LPR) & 31)) * D + E * lane;
-          const bool live = q < rows;
+          const bool live = q < RW && row0 + q < rows;
           if constexpr (E == 4) {
             const uint2 x = live ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0u, 0u);
             raw[j][0] = x.x, raw[j][1] = x.y;
@@ -639,8 +662,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         }
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
-          const int q = warp + 4 * j;
-          if (q >= RP) break;
+          const int q = quarter + 4 * j;
+          if (q >= RW) break;
           uint32_t top = 0;
 #pragma unroll
           for (int u = 0; u < E / 2; ++u) top = __vmaxu2(top, raw[j][u] & 0x7fff7fffu);
@@ -661,8 +684,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
             unpack_e4m3x2(hi[u], h[2 * u], h[2 * u + 1]);
             lo[u] = pack_e4m3x2(x[2 * u] - h[2 * u], x[2 * u + 1] - h[2 * u + 1]);
           }
-          uint8_t* at_hi = smem + C::OFF_Q + swz<D>(q, E * lane);
-          uint8_t* at_lo = smem + C::OFF_Q + swz<D>(RP + q, E * lane);
+          uint8_t* at_hi = smem + C::OFF_Q + swz<D>(2 * row0 + q, E * lane);
+          uint8_t* at_lo = smem + C::OFF_Q + swz<D>(2 * row0 + RW + q, E * lane);
           if constexpr (E == 4) {
             *reinterpret_cast<uint32_t*>(at_hi) = hi[0] | (hi[1] << 16);
             *reinterpret_cast<uint32_t*>(at_lo) = lo[0] | (lo[1] << 16);
@@ -670,40 +693,33 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
             *reinterpret_cast<uint16_t*>(at_hi) = static_cast<uint16_t>(hi[0]);
             *reinterpret_cast<uint16_t*>(at_lo) = static_cast<uint16_t>(lo[0]);
           }
-          if (lane == 0) qs[q] = exp2_int(e2) * p.scale_log2;
+          if (lane == 0) qs[row0 + q] = exp2_int(e2) * p.scale_log2;
         }
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(C::B_QREADY));
       wait(C::B_QREADY, n_item & 1);
-      float qf[RP], lsum[RP], ov[RP];
-      load_row<RP>(qs, qf);
+      float qf[RW], lsum[RW], ov[RW];
+      load_row<RW>(qs + row0, qf);
 #pragma unroll
-      for (int q = 0; q < RP; ++q) lsum[q] = ov[q] = 0.f;
+      for (int q = 0; q < RW; ++q) lsum[q] = ov[q] = 0.f;
       float m = -CUDART_INF_F;  // running reference of row my_row
+      constexpr int NL = RP == 1 ? 8 : 2 * RW;  // columns of the warpgroup's rows
       // O of tile u (its statistics are still in their buffer) into the running one.
       auto add_o = [&](int u) {
-        const float* stat = stats + (u & 1) * 4 * 3 * kRowsMax;
+        const float* stat = stats + (u & 1) * C::NCW * C::STAT_WARP;
         wait(C::B_PVDONE + (u & 1), (u >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        constexpr int NL = 2 * RP >= 16 ? 2 * RP : 16;  // columns of one half, or all of them
         uint32_t o[NL];
+        tmem_cols(lane_addr + C::O_COL + C::NO * (u & 1) + (RP == 1 ? 0 : 2 * RP * half + 2 * row0), o);
+        float alpha[RW], wt[RW];
+        load_row<RW>(stat + RW, alpha);
+        load_row<RW>(stat + 2 * RW, wt);
 #pragma unroll
-        for (int c = 0; c < NL / 16; ++c)
-          tmem_ld16(lane_addr + C::O_COL + C::NO * (u & 1) + (2 * RP >= 16 ? 2 * RP * half : 0) + 16 * c,
-                    *reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < NL / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(o + 16 * c));
-        float alpha[RP], wt[RP];
-        load_row<RP>(stat + kRowsMax, alpha);
-        load_row<RP>(stat + 2 * kRowsMax, wt);
-#pragma unroll
-        for (int q = 0; q < RP; ++q) {
-          float sum = __uint_as_float(o[q]) + __uint_as_float(o[q + RP]);
-          if (C::HALVES == 2 && 2 * RP < 16)  // both halves are in the one load
-            sum = half ? __uint_as_float(o[(q + 2 * RP) % NL]) + __uint_as_float(o[(q + 3 * RP) % NL]) : sum;
+        for (int q = 0; q < RW; ++q) {
+          float sum = __uint_as_float(o[q]) + __uint_as_float(o[q + RW]);
+          if (RP == 1 && D == 64) sum = half ? __uint_as_float(o[2]) + __uint_as_float(o[3]) : sum;
           ov[q] = fmaf(ov[q], alpha[q], sum * wt[q]);
         }
         tc_fence_before();
@@ -720,34 +736,29 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         wait(C::B_SFULL + (t & 1), (t >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        uint32_t sv[C::NS];
+        uint32_t sv[NL];
+        tmem_cols(lane_addr + C::NS * (t & 1) + 2 * row0, sv);
+        float y[RW];
 #pragma unroll
-        for (int c = 0; c < C::NS / 16; ++c)
-          tmem_ld16(lane_addr + C::NS * (t & 1) + 16 * c, *reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
-        tmem_wait_ld();
-#pragma unroll
-        for (int c = 0; c < C::NS / 16; ++c) reg_fence(*reinterpret_cast<uint32_t(*)[16]>(sv + 16 * c));
-        float y[RP];
-#pragma unroll
-        for (int q = 0; q < RP; ++q)
-          y[q] = fmaf(__uint_as_float(sv[q]) + __uint_as_float(sv[RP + q]), ks * qf[q], vef);
+        for (int q = 0; q < RW; ++q)
+          y[q] = fmaf(__uint_as_float(sv[q]) + __uint_as_float(sv[RW + q]), ks * qf[q], vef);
         if (kt * kTile + kTile > w.len - (p.causal ? p.Nq - 1 : 0)) {  // some row does not see all of the tile
 #pragma unroll
-          for (int q = 0; q < RP; ++q)
+          for (int q = 0; q < RW; ++q)
             if (key >= w.len - __shfl_sync(0xffffffffu, row_hidden, q * LPR)) y[q] = -CUDART_INF_F;
         }
         // ---- the tile's largest y of each row: over the warp, then over the
         // four warps; lane q does the rest of row q's statistics and leaves
         // them for its warp
-        float* slot = xch + (nx & 1) * 4 * kRowsMax;
+        float* slot = xch + (nx & 1) * 4 * kRowsMax + row0;
         {
-          const float wm = rows_reduce<RP, false>(y, lane);
-          if (lane % LPR == 0) slot[warp * kRowsMax + my_row] = wm;
+          const float wm = rows_reduce<RW, false>(y, lane);
+          if (lane % LPR == 0) slot[quarter * kRowsMax + my_row] = wm;
         }
-        mbar_arrive(bar(C::B_XCH));
-        wait(C::B_XCH, nx & 1);
+        mbar_arrive(bar(xbar));
+        wait(xbar, nx & 1);
         ++nx;
-        float* stat = stats + (t & 1) * 4 * 3 * kRowsMax;
+        float* stat = stats + (t & 1) * C::NCW * C::STAT_WARP;
         {
           const int q = my_row;
           const float mt = fmaxf(fmax3(slot[q], slot[kRowsMax + q], slot[2 * kRowsMax + q]), slot[3 * kRowsMax + q]);
@@ -755,27 +766,27 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           const bool none = mt == -CUDART_INF_F;
           if (lane % LPR == 0) {
             stat[q] = none ? 0.f : mt - 8.f;
-            stat[kRowsMax + q] = m == -CUDART_INF_F ? 0.f : ex2_approx(m - m_new);
-            stat[2 * kRowsMax + q] = none ? 0.f : ex2_approx(mt - m_new - 8.f);
+            stat[RW + q] = m == -CUDART_INF_F ? 0.f : ex2_approx(m - m_new);
+            stat[2 * RW + q] = none ? 0.f : ex2_approx(mt - m_new - 8.f);
           }
           m = m_new;
           __syncwarp();
         }
         const float inv_vs = exp2_int(-ve);
         {
-          float ref[RP], alpha[RP], wt[RP];
-          load_row<RP>(stat, ref);
-          load_row<RP>(stat + kRowsMax, alpha);
-          load_row<RP>(stat + 2 * kRowsMax, wt);
-          uint32_t hi[(RP + 3) / 4], lo[(RP + 3) / 4];
+          float ref[RW], alpha[RW], wt[RW];
+          load_row<RW>(stat, ref);
+          load_row<RW>(stat + RW, alpha);
+          load_row<RW>(stat + 2 * RW, wt);
+          uint32_t hi[(RW + 3) / 4], lo[(RW + 3) / 4];
 #pragma unroll
-          for (int q = 0; q < RP; ++q) {
+          for (int q = 0; q < RW; ++q) {
             y[q] = ex2_approx(y[q] - ref[q]);  // P, at most 256
             lsum[q] = fmaf(lsum[q], alpha[q], y[q] * (inv_vs * wt[q]));
           }
 #pragma unroll
-          for (int q = 0; q < RP; q += 2) {
-            const float p1 = q + 1 < RP ? y[q + 1 < RP ? q + 1 : q] : 0.f;
+          for (int q = 0; q < RW; q += 2) {
+            const float p1 = q + 1 < RW ? y[q + 1 < RW ? q + 1 : q] : 0.f;
             float h0, h1;
             const uint32_t c = pack_e4m3x2(y[q], p1);
             unpack_e4m3x2(c, h0, h1);
@@ -788,26 +799,18 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
               lo[q / 4] |= e << 16;
             }
           }
-          // the key's columns: hi terms of the rows, then lo terms (d = 64: of
-          // its half of the keys)
-          const int k = r % KW;
-          const uint32_t pbuf = C::OFF_P + (t & 1) * C::P_BYTES;
-          if constexpr (RP == 16) {
-            uint4* row0 = reinterpret_cast<uint4*>(smem + pbuf + swz<C::NO>(k, 32 * half));
-            uint4* row1 = reinterpret_cast<uint4*>(smem + pbuf + swz<C::NO>(k, 32 * half + 16));
-            *row0 = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *row1 = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else if constexpr (RP == 8) {
-            *reinterpret_cast<uint4*>(smem + pbuf + swz<C::NO>(k, 16 * half)) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-          } else if constexpr (RP == 4) {
-            *reinterpret_cast<uint2*>(smem + pbuf + k * 16 + 8 * half) = make_uint2(hi[0], lo[0]);
-          } else {
-            static_assert(RP == 1 || RP >= 4, "row counts that the P layout has");
-            *reinterpret_cast<uint16_t*>(smem + pbuf + k * 16 + 2 * half) =
-                static_cast<uint16_t>((hi[0] & 0xffu) | (lo[0] << 8));
-          }
+          // the key's columns (d = 64: of its half of the keys): a warpgroup's
+          // rows' hi terms, then their lo terms
+          uint8_t* at = smem + C::OFF_P + (t & 1) * C::P_BYTES + swz<C::NO>(r % KW, 2 * RP * half + 2 * row0);
+          static_assert(RW == 8 || RW == 4 || RW == 1, "row counts that the P layout has");
+          if constexpr (RW == 8)
+            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+          else if constexpr (RW == 4)
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], lo[0]);
+          else
+            *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>((hi[0] & 0xffu) | (lo[0] << 8));
         }
-        if (key >= w.len) {  // slots without a token may hold NaN, and 0 · NaN is not 0
+        if (wg == 0 && key >= w.len) {  // slots without a token may hold NaN, and 0 · NaN is not 0
           uint4* vrow = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::TILE_BYTES + r * D);
 #pragma unroll
           for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -821,28 +824,27 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       }
       add_o(t - 1);
       // ---- the item's sums: l over the keys, O over the halves
-      float* slot = xch + (nx & 1) * 4 * kRowsMax;
+      float* slot = xch + (nx & 1) * 4 * kRowsMax + row0;
       {
-        const float l = rows_reduce<RP, true>(lsum, lane);
-        if (lane % LPR == 0) slot[warp * kRowsMax + my_row] = l;
+        const float l = rows_reduce<RW, true>(lsum, lane);
+        if (lane % LPR == 0) slot[quarter * kRowsMax + my_row] = l;
       }
-      float* other = reinterpret_cast<float*>(smem + C::OFF_HALF);
+      float* other = reinterpret_cast<float*>(smem + C::OFF_HALF) + row0 * 64 + r % 64;
       if (D == 64 && half) {
 #pragma unroll
-        for (int q = 0; q < RP; ++q) other[q * 64 + r % 64] = ov[q];
+        for (int q = 0; q < RW; ++q) other[q * 64] = ov[q];
       }
-      tc_fence_before();
-      mbar_arrive(bar(C::B_XCH));
-      wait(C::B_XCH, nx & 1);
+      mbar_arrive(bar(xbar));
+      wait(xbar, nx & 1);
       ++nx;
       float* stat = stats;  // the tile loop's statistics of this warp make room for the rows' factors
       const bool whole = w.k0 == 0 && w.k1 == w.nt;
       const float l = (slot[my_row] + slot[kRowsMax + my_row]) + (slot[2 * kRowsMax + my_row] + slot[3 * kRowsMax + my_row]);
-      const size_t part0 = (2 * static_cast<size_t>(blockIdx.x) + (w.k0 == 0 ? 1 : 0)) * p.rows;
+      const size_t part0 = (2 * static_cast<size_t>(blockIdx.x) + (w.k0 == 0 ? 1 : 0)) * p.rows + row0;
       if (lane % LPR == 0) {
         stat[my_row] = l > 0.f ? 1.f / l : 0.f;
-        reinterpret_cast<int*>(stat)[kRowsMax + my_row] = row_q;
-        if (warp == 0 && my_row < rows) {
+        reinterpret_cast<int*>(stat)[RW + my_row] = row_q;
+        if (quarter == 0 && row0 + my_row < rows) {
           if (whole) {
             p.lse[row_lse] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
           } else {
@@ -853,14 +855,14 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       }
       __syncwarp();
       if (r < D) {
-        float inv[RP];
-        load_row<RP>(stat, inv);
+        float inv[RW];
+        load_row<RW>(stat, inv);
 #pragma unroll
-        for (int q = 0; q < RP; ++q) {
-          if (q >= rows) break;
-          const float o = D == 64 ? ov[q] + other[q * 64 + r % 64] : ov[q];
+        for (int q = 0; q < RW; ++q) {
+          if (row0 + q >= rows) break;
+          const float o = D == 64 ? ov[q] + other[q * 64] : ov[q];
           if (whole)
-            p.o[static_cast<size_t>(reinterpret_cast<int*>(stat)[kRowsMax + q]) * D + r] =
+            p.o[static_cast<size_t>(reinterpret_cast<int*>(stat)[RW + q]) * D + r] =
                 static_cast<uint16_t>(pack_bf16x2(o * inv[q], 0.f));
           else
             p.o_part[(part0 + q) * D + r] = o;
@@ -868,8 +870,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       }
       __syncwarp();
       if (D == 64) {  // the second half's buffer has been read
-        mbar_arrive(bar(C::B_XCH));
-        wait(C::B_XCH, nx & 1);
+        mbar_arrive(bar(xbar));
+        wait(xbar, nx & 1);
         ++nx;
       }
     }

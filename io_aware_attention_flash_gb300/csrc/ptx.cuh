@@ -318,6 +318,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : FA_R8(0) : "r"(taddr));
+}
+
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -327,6 +331,7 @@ __device__ __forceinline__ void reg_fence(uint32_t (&r)[32]) {
   asm volatile("" : FA_F8(0), FA_F8(8), FA_F8(16), FA_F8(24));
 }
 __device__ __forceinline__ void reg_fence(uint32_t (&r)[16]) { asm volatile("" : FA_F8(0), FA_F8(8)); }
+__device__ __forceinline__ void reg_fence(uint32_t (&r)[8]) { asm volatile("" : FA_F8(0)); }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
