@@ -412,9 +412,9 @@ fa_status make_map_codes(CUtensorMap* map, const void* ptr, int d, int block, in
   return FA_OK;
 }
 
-// CTAs of the cache attention: two on each of 152 SMs (fixed, so that the
+// CTAs of the cache attention: as many as 152 SMs hold (fixed, so that the
 // workspace does not depend on the device), or one for each possible tile.
-constexpr int kDecode8Ctas = 304;
+constexpr int kDecode8Sms = 152;
 
 fa_status check_decode8(int B, int Nq, int H, int Hk, int num_blocks, int table_cols, int block, int max_seqlen,
                         int d, float scale) {
@@ -435,10 +435,11 @@ struct Decode8Plan {
 
 Decode8Plan decode8_plan(int B, int Nq, int H, int Hk, int max_seqlen, int d) {
   Decode8Plan w{};
-  fa::cache8_row_groups(Nq * (H / Hk), &w.row_groups, &w.rows);
+  int per_sm = 0;
+  fa::cache8_plan(d, Nq * (H / Hk), &w.row_groups, &w.rows, &per_sm);
   const long long tiles =
       (static_cast<long long>(max_seqlen) + fa::kTile - 1) / fa::kTile * B * Hk * w.row_groups;
-  w.ctas = static_cast<int>(tiles < kDecode8Ctas ? tiles : kDecode8Ctas);
+  w.ctas = static_cast<int>(tiles < kDecode8Sms * per_sm ? tiles : kDecode8Sms * per_sm);
   const size_t parts = static_cast<size_t>(2) * w.ctas * w.rows;
   w.ml_off = pad256(parts * d * 4);
   w.start_off = w.ml_off + pad256(parts * 2 * 4);

@@ -269,12 +269,18 @@ struct Walk {
   }
 };
 
-// Maxima (or sums) over the warp of RP values a lane: value i of all lanes ends
-// in lanes 32/RP · i .. +32/RP - 1.  Each step sends half of the values that are
+// The largest value of the warp, in every lane.
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// Sums over the warp of RP values a lane: value i of all lanes ends in lanes
+// 32/RP · i .. +32/RP - 1.  Each step sends half of the values that are
 // left to the lane that keeps them (RP - 1 + log2(32/RP) shuffles in all).
-template <int RP, bool SUM>
-__device__ __forceinline__ float rows_reduce(const float (&y)[RP], int lane) {
-  auto join = [](float a, float b) { return SUM ? a + b : fmaxf(a, b); };
+template <int RP>
+__device__ __forceinline__ float rows_sum(const float (&y)[RP], int lane) {
   float v[RP];
 #pragma unroll
   for (int i = 0; i < RP; ++i) v[i] = y[i];
@@ -288,10 +294,10 @@ __device__ __forceinline__ float rows_reduce(const float (&y)[RP], int lane) {
       for (int i = 0; i < RP / 2; ++i)
         if (i < n) {
           const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
-          v[i] = join(keep, __shfl_xor_sync(0xffffffffu, send, off));
+          v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
         }
     } else {
-      v[0] = join(v[0], __shfl_xor_sync(0xffffffffu, v[0], off));
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
     }
   }
   return v[0];
@@ -322,7 +328,12 @@ struct Dec8Cfg {
   static constexpr int NUM_WARPS = NCW + 2;
   static constexpr int NUM_THREADS = 32 * NUM_WARPS;
   static constexpr int TILE_BYTES = kTile * D;               // 128 keys
-  static constexpr int NST = D == 128 ? 3 : 5;               // ring stages (K and V tile each)
+  // CTAs on an SM.  A tile's chain of waits and short steps takes some 1350
+  // cycles; at d = 64 a tile is 16 KB, which the memory delivers to an SM in
+  // less than half of that, so four small CTAs overlap (8 rows and more: two,
+  // by their registers).
+  static constexpr int CTAS = D == 64 && RP <= 4 ? 4 : 2;
+  static constexpr int NST = D == 128 || CTAS == 4 ? 3 : 5;  // ring stages (K and V tile each)
   static constexpr int NS = 2 * RP < 16 ? 16 : 2 * RP;       // columns of S: a warpgroup's rows' hi, then lo terms
   static constexpr int HALVES = 128 / D;
   static constexpr int NO = 2 * RP * HALVES < 16 ? 16 : 2 * RP * HALVES;
@@ -347,8 +358,8 @@ struct Dec8Cfg {
   static constexpr uint32_t COLS = 2 * NS + 2 * NO;
   static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
   static constexpr uint32_t O_COL = 2 * NS;
-  static_assert(COLS <= 256, "tensor memory for two CTAs on an SM");
-  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "two CTAs on an SM");
+  static_assert(CTAS * TMEM_COLS <= 512, "tensor memory for the CTAs of an SM");
+  static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "shared memory for the CTAs of an SM");
   static_assert(OFF_Q % 1024 == 0 && OFF_P % 512 == 0 && (D == 64 || OFF_P % 1024 == 0), "swizzle atoms");
 };
 
@@ -398,8 +409,29 @@ __device__ __forceinline__ void load_row(const float* src, float (&v)[N]) {
   }
 }
 
+template <int N>
+__device__ __forceinline__ void store_row(float* dst, const float (&v)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i)
+      reinterpret_cast<float4*>(dst)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) dst[i] = v[i];
+  }
+}
+
+// Element-wise arithmetic on rows' values, two at a time (the paired fp32
+// instructions halve the issue slots, which bound a tile of 8 rows and more).
+template <int N, typename F2, typename F1>
+__device__ __forceinline__ void each_pair(F2 two, F1 one) {
+#pragma unroll
+  for (int q = 0; q + 1 < N; q += 2) two(q);
+  if constexpr (N % 2 == 1) one(N - 1);
+}
+
 template <int D, int RP>
-__global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
+__global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::CTAS)
     fa_cache8_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const Cache8DecodeParams p) {
   using C = Dec8Cfg<D, RP>;
@@ -716,12 +748,19 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         float alpha[RW], wt[RW];
         load_row<RW>(stat + RW, alpha);
         load_row<RW>(stat + 2 * RW, wt);
-#pragma unroll
-        for (int q = 0; q < RW; ++q) {
-          float sum = __uint_as_float(o[q]) + __uint_as_float(o[q + RW]);
-          if (RP == 1 && D == 64) sum = half ? __uint_as_float(o[2]) + __uint_as_float(o[3]) : sum;
-          ov[q] = fmaf(ov[q], alpha[q], sum * wt[q]);
-        }
+        each_pair<RW>(
+            [&](int q) {
+              const uint64_t sum = fadd2(f2_pack(__uint_as_float(o[q]), __uint_as_float(o[q + 1])),
+                                         f2_pack(__uint_as_float(o[RW + q]), __uint_as_float(o[RW + q + 1])));
+              f2_unpack(ffma2(sum, f2_pack(wt[q], wt[q + 1]),
+                              fmul2(f2_pack(ov[q], ov[q + 1]), f2_pack(alpha[q], alpha[q + 1]))),
+                        ov[q], ov[q + 1]);
+            },
+            [&](int q) {
+              float sum = __uint_as_float(o[q]) + __uint_as_float(o[q + RW]);
+              if (RP == 1 && D == 64) sum = half ? __uint_as_float(o[2]) + __uint_as_float(o[3]) : sum;
+              ov[q] = fmaf(sum, wt[q], ov[q] * alpha[q]);
+            });
         tc_fence_before();
       };
       for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
@@ -739,9 +778,13 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         uint32_t sv[NL];
         tmem_cols(lane_addr + C::NS * (t & 1) + 2 * row0, sv);
         float y[RW];
-#pragma unroll
-        for (int q = 0; q < RW; ++q)
-          y[q] = fmaf(__uint_as_float(sv[q]) + __uint_as_float(sv[RW + q]), ks * qf[q], vef);
+        each_pair<RW>(
+            [&](int q) {
+              const uint64_t s = fadd2(f2_pack(__uint_as_float(sv[q]), __uint_as_float(sv[q + 1])),
+                                       f2_pack(__uint_as_float(sv[RW + q]), __uint_as_float(sv[RW + q + 1])));
+              f2_unpack(ffma2(s, fmul2(f2_pack(ks, ks), f2_pack(qf[q], qf[q + 1])), f2_pack(vef, vef)), y[q], y[q + 1]);
+            },
+            [&](int q) { y[q] = fmaf(__uint_as_float(sv[q]) + __uint_as_float(sv[RW + q]), ks * qf[q], vef); });
         if (kt * kTile + kTile > w.len - (p.causal ? p.Nq - 1 : 0)) {  // some row does not see all of the tile
 #pragma unroll
           for (int q = 0; q < RW; ++q)
@@ -752,8 +795,10 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         // them for its warp
         float* slot = xch + (nx & 1) * 4 * kRowsMax + row0;
         {
-          const float wm = rows_reduce<RW, false>(y, lane);
-          if (lane % LPR == 0) slot[quarter * kRowsMax + my_row] = wm;
+          float wm[RW];
+#pragma unroll
+          for (int q = 0; q < RW; ++q) wm[q] = warp_max(y[q]);
+          if (lane == 0) store_row<RW>(slot + quarter * kRowsMax, wm);
         }
         mbar_arrive(bar(xbar));
         wait(xbar, nx & 1);
@@ -779,18 +824,29 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           load_row<RW>(stat + RW, alpha);
           load_row<RW>(stat + 2 * RW, wt);
           uint32_t hi[(RW + 3) / 4], lo[(RW + 3) / 4];
-#pragma unroll
-          for (int q = 0; q < RW; ++q) {
-            y[q] = ex2_approx(y[q] - ref[q]);  // P, at most 256
-            lsum[q] = fmaf(lsum[q], alpha[q], y[q] * (inv_vs * wt[q]));
-          }
+          // P = 2^(y - reference), at most 256, and its share of l
+          each_pair<RW>(
+              [&](int q) {
+                f2_unpack(fsub2(f2_pack(y[q], y[q + 1]), f2_pack(ref[q], ref[q + 1])), y[q], y[q + 1]);
+                y[q] = ex2_approx(y[q]);
+                y[q + 1] = ex2_approx(y[q + 1]);
+                const uint64_t c = fmul2(f2_pack(inv_vs, inv_vs), f2_pack(wt[q], wt[q + 1]));
+                f2_unpack(ffma2(f2_pack(y[q], y[q + 1]), c,
+                                fmul2(f2_pack(lsum[q], lsum[q + 1]), f2_pack(alpha[q], alpha[q + 1]))),
+                          lsum[q], lsum[q + 1]);
+              },
+              [&](int q) {
+                y[q] = ex2_approx(y[q] - ref[q]);
+                lsum[q] = fmaf(y[q], inv_vs * wt[q], lsum[q] * alpha[q]);
+              });
 #pragma unroll
           for (int q = 0; q < RW; q += 2) {
             const float p1 = q + 1 < RW ? y[q + 1 < RW ? q + 1 : q] : 0.f;
-            float h0, h1;
+            float h0, h1, e0, e1;
             const uint32_t c = pack_e4m3x2(y[q], p1);
             unpack_e4m3x2(c, h0, h1);
-            const uint32_t e = pack_e4m3x2(y[q] - h0, p1 - h1);
+            f2_unpack(fsub2(f2_pack(y[q], p1), f2_pack(h0, h1)), e0, e1);
+            const uint32_t e = pack_e4m3x2(e0, e1);
             if (q % 4 == 0) {
               hi[q / 4] = c;
               lo[q / 4] = e;
@@ -826,7 +882,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       // ---- the item's sums: l over the keys, O over the halves
       float* slot = xch + (nx & 1) * 4 * kRowsMax + row0;
       {
-        const float l = rows_reduce<RW, true>(lsum, lane);
+        const float l = rows_sum<RW>(lsum, lane);
         if (lane % LPR == 0) slot[quarter * kRowsMax + my_row] = l;
       }
       float* other = reinterpret_cast<float*>(smem + C::OFF_HALF) + row0 * 64 + r % 64;
@@ -951,9 +1007,10 @@ cudaError_t launch_decode8_rows(const CUtensorMap& tk, const CUtensorMap& tv, co
 
 }  // namespace
 
-void cache8_row_groups(int rows_total, int* groups, int* rows) {
+void cache8_plan(int d, int rows_total, int* groups, int* rows, int* ctas_per_sm) {
   *groups = (rows_total + kRowsMax - 1) / kRowsMax;
   *rows = (rows_total + *groups - 1) / *groups;
+  *ctas_per_sm = d == 64 && *rows <= 4 ? Dec8Cfg<64, 4>::CTAS : Dec8Cfg<128, 16>::CTAS;
 }
 
 cudaError_t launch_cache8_store(int d, int block, const Cache8StoreParams& p, cudaStream_t s) {
