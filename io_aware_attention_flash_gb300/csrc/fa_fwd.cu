@@ -101,7 +101,13 @@ __device__ __forceinline__ void zero_tail_rows(const FwdParams& p, int tid, int 
 // sequence's rows, or what lies behind the last one: its scores are masked,
 // and its V rows are zeroed in shared memory, since a probability of 0 times
 // an infinity or NaN there would not be 0.
-template <int D, int NQT_, bool GRP = false>
+// HP: a CTA's two query tiles are the same 128 rows of two query heads of one
+// group instead of 256 rows of one head.  They see the same keys, so under a
+// causal mask neither tile waits out the other's last step, and short
+// sequences waste no half-empty 256-row tiles: a sequence of n rows takes
+// half of the sum of its 128-row tiles' steps a head, against the sum over
+// pairs of tiles of the larger one.
+template <int D, int NQT_, bool GRP = false, bool HP = false>
 __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>::MIN_BLOCKS)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -125,11 +131,14 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
     if (GRP && p.sv.zero_tail) zero_tail_rows<D>(p, threadIdx.x, C::NUM_THREADS);
     return;
   }
-  const SeqPos sp = GRP ? seq_pos_grouped(p.sv, pair) : seq_pos(p.sv, pair);
+  static_assert(!HP || (GRP && NQT == 2), "head pairs: two query tiles of grouped heads");
+  const SeqPos sp = GRP ? seq_pos_grouped(p.sv, pair, HP ? 2 : 1) : seq_pos(p.sv, pair);
   const int hk = GRP ? sp.h / p.sv.G : sp.h;  // key/value head
   // Causal: the last query tiles see the most keys, so they go first.
   const int ctile = p.causal ? p.sv.ntiles - 1 - tile : tile;
-  const int q0 = ctile * kTile * NQT;
+  constexpr int QSTEP = HP ? 0 : kTile;  // rows from one query tile to the next
+  constexpr int HSTEP = HP ? 1 : 0;      // heads from one to the next
+  const int q0 = ctile * kTile * (HP ? 1 : NQT);
   if (q0 >= sp.seqlen) {  // whole CTA past the end of a short packed sequence
     if (GRP && p.sv.zero_tail) zero_tail_rows<D>(p, threadIdx.x, C::NUM_THREADS);
     return;
@@ -140,7 +149,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
   int nkv_max = 0;
 #pragma unroll
   for (int t = 0; t < NQT; ++t) {
-    const int qt = q0 + t * kTile;
+    const int qt = q0 + t * QSTEP;
     nkv[t] = qt >= sp.seqlen ? 0 : (p.causal ? min(nkv_total, qt / kTile + 1) : nkv_total);
     nkv_max = max(nkv_max, nkv[t]);
   }
@@ -149,8 +158,8 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
   auto load_q = [&](int t) {
     mbar_arrive_expect_tx(bar(C::B_Q + t), C::TILE_BYTES);
     for (int kb = 0; kb < C::KB; ++kb)
-      tma_load_4d(sb + C::OFF_Q + t * C::TILE_BYTES + kb * C::BLK_BYTES, &tmQ, bar(C::B_Q + t), kb * 64, sp.h,
-                  sp.tma_row0 + q0 + t * kTile, sp.tma_b);
+      tma_load_4d(sb + C::OFF_Q + t * C::TILE_BYTES + kb * C::BLK_BYTES, &tmQ, bar(C::B_Q + t), kb * 64,
+                  sp.h + t * HSTEP, sp.tma_row0 + q0 + t * QSTEP, sp.tma_b);
   };
   auto load_k = [&](int j) {
     const int ks = j % C::NSK;
@@ -328,7 +337,8 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
     const int t = warp / 4;
     const int wq = warp % 4;
     const int r = wq * 32 + lane;
-    const int qt = q0 + t * kTile;
+    const int qt = q0 + t * QSTEP;
+    const int head = sp.h + t * HSTEP;
     const int q_row = qt + r;  // row within the sequence
     // This warp's tile's key count, computed rather than read from nkv[] with
     // a run-time index (which would put the array in local memory).
@@ -336,7 +346,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
     if (GRP && p.sv.zero_tail) zero_tail_rows<D>(p, threadIdx.x, 128 * NQT);  // while the first tiles arrive
     // Grouped heads: one warpgroup zeroes the last key tile's V rows past the
     // sequence's end, the one whose O += P V comes first on that tile.
-    const bool zero_v = GRP && (t == 0 || (p.causal && q0 / kTile + 1 < nkv_total));
+    const bool zero_v = GRP && (t == 0 || (!HP && p.causal && q0 / kTile + 1 < nkv_total));
     if (nkv_t > 0) {
       const float c = p.scale_log2;
       const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
         const bool store = q_row < sp.seqlen;
         const bool via_tma = !p.sv.cu_seqlens || qt + 32 * wq + 32 <= sp.seqlen;
         const uint32_t stage = sb + C::OFF_Q + t * C::TILE_BYTES;
-        uint16_t* orow = p.o + (static_cast<size_t>(sp.row_base + q_row) * p.sv.H + sp.h) * D;
+        uint16_t* orow = p.o + (static_cast<size_t>(sp.row_base + q_row) * p.sv.H + head) * D;
 #pragma unroll 1
         for (int cb = 0; cb < D / 64; ++cb) {  // 64 columns (one 128-byte swizzle block) per TMEM round trip
           uint32_t o[2][32];
@@ -508,8 +518,8 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
         }
         if (store) {
           const float lse = l > 0.f ? (m_ref * c + log2f(l)) * kLn2 : -CUDART_INF_F;
-          const size_t at = GRP ? static_cast<size_t>(sp.h) * p.sv.N + sp.row_base + q_row
-                                : (static_cast<size_t>(sp.bs) * p.sv.H + sp.h) * p.sv.lse_stride + q_row;
+          const size_t at = GRP ? static_cast<size_t>(head) * p.sv.N + sp.row_base + q_row
+                                : (static_cast<size_t>(sp.bs) * p.sv.H + head) * p.sv.lse_stride + q_row;
           p.lse[at] = lse;
         }
         if (via_tma) {
@@ -521,7 +531,7 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
           if (lane == 0 && qt + 32 * wq < sp.seqlen) {
 #pragma unroll
             for (int kb = 0; kb < C::KB; ++kb)
-              tma_store_4d(&tmO, stage + kb * C::BLK_BYTES + wq * 4096, kb * 64, sp.h, sp.tma_row0 + qt + 32 * wq,
+              tma_store_4d(&tmO, stage + kb * C::BLK_BYTES + wq * 4096, kb * 64, head, sp.tma_row0 + qt + 32 * wq,
                            sp.tma_b);
             bulk_commit_group();
             // The stage may be released once the copies have read it; their
@@ -541,23 +551,24 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
   }
 }
 
-template <int D, int NQT, bool GRP = false>
+template <int D, int NQT, bool GRP = false, bool HP = false>
 cudaError_t launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to,
                          const FwdParams& p, int nseq, int max_seqlen, cudaStream_t s) {
   using C = FwdCfg<D, NQT>;
   static SmemLimit smem_limit;
-  cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_fwd_kernel<D, NQT, GRP>), C::SMEM_BYTES);
+  cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_fwd_kernel<D, NQT, GRP, HP>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   int sms = 0;
   e = current_sm_count(sms);
   if (e != cudaSuccess) return e;
   FwdParams pl = p;
-  pl.sv.npairs = nseq * p.sv.H;
-  pl.sv.ntiles = (max_seqlen + kTile * C::NQT - 1) / (kTile * C::NQT);
+  constexpr int ROWS = kTile * (HP ? 1 : C::NQT);  // of a CTA
+  pl.sv.npairs = nseq * (p.sv.H / (HP ? 2 : 1));
+  pl.sv.ntiles = (max_seqlen + ROWS - 1) / ROWS;
   pl.sv.pair_group = pair_group_size(pl.sv.npairs, pl.sv.ntiles, sms * C::MIN_BLOCKS);
   const long long ctas = grid_ctas(pl.sv.npairs, pl.sv.ntiles, pl.sv.pair_group);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  fa_fwd_kernel<D, NQT, GRP><<<static_cast<unsigned>(ctas), C::NUM_THREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, to, pl);
+  fa_fwd_kernel<D, NQT, GRP, HP><<<static_cast<unsigned>(ctas), C::NUM_THREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, to, pl);
   return cudaGetLastError();
 }
 
@@ -572,6 +583,7 @@ cudaError_t launch_fwd(int d, const CUtensorMap& tq, const CUtensorMap& tk, cons
 cudaError_t launch_fwd_grouped(int d, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                const CUtensorMap& to, const FwdParams& p, cudaStream_t s) {
   if (d == 64) return launch_fwd_d<64, 1, true>(tq, tk, tv, to, p, p.sv.nseq, p.sv.max_seqlen, s);
+  if (p.sv.G % 2 == 0) return launch_fwd_d<128, 2, true, true>(tq, tk, tv, to, p, p.sv.nseq, p.sv.max_seqlen, s);
   return launch_fwd_d<128, 2, true>(tq, tk, tv, to, p, p.sv.nseq, p.sv.max_seqlen, s);
 }
 

@@ -244,10 +244,12 @@ __device__ __forceinline__ void clamp_seq(const SeqView& sv, int bs, SeqPos& s) 
   s.tma_b = 0;
 }
 
-__device__ __forceinline__ SeqPos seq_pos_grouped(const SeqView& sv, int pair) {
+// heads: query heads of a work item (h is the first of them).
+__device__ __forceinline__ SeqPos seq_pos_grouped(const SeqView& sv, int pair, int heads) {
   SeqPos s;
-  clamp_seq(sv, pair / sv.H, s);
-  s.h = pair % sv.H;
+  const int per_seq = sv.H / heads;
+  clamp_seq(sv, pair / per_seq, s);
+  s.h = pair % per_seq * heads;
   return s;
 }
 
