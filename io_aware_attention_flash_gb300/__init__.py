@@ -155,7 +155,10 @@ def attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool
     Returns (o [T,H,d] bf16, lse [H,T] fp32); rows behind the last sequence
     get o = 0, lse = -inf.  stream: the stream to run on (default: the
     current one)."""
-    checked = _binding._grouped(q, k, v, cu_seqlens)
+    return _forward_grouped(_binding._grouped(q, k, v, cu_seqlens), q, k, v, cu_seqlens, max_seqlen, causal, scale)
+
+
+def _forward_grouped(checked, q, k, v, cu_seqlens, max_seqlen, causal, scale):
     T, H, d = q.shape
     o = torch.empty((T, H, d), device=q.device, dtype=torch.bfloat16)
     lse = torch.empty((H, T), device=q.device, dtype=torch.float32)
@@ -170,6 +173,10 @@ def attention_backward_grouped(q, k, v, o, dout, lse, cu_seqlens, max_seqlen: in
     sequence.  dk and dv are summed over the query heads that share them.
     stream: the stream to run on (default: the current one)."""
     checked = _binding._grouped(q, k, v, cu_seqlens)
+    return _backward_grouped(checked, q, k, v, o, dout, lse, cu_seqlens, max_seqlen, causal, scale, workspace)
+
+
+def _backward_grouped(checked, q, k, v, o, dout, lse, cu_seqlens, max_seqlen, causal, scale, workspace):
     dev, T, H, Hk, d, nseq = checked[:6]
     device = q.device
     if workspace is None:
@@ -188,17 +195,19 @@ def attention_backward_grouped(q, k, v, o, dout, lse, cu_seqlens, max_seqlen: in
 class _FlashAttentionGrouped(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, max_seqlen, causal, scale):
-        o, lse = attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
+        checked = _binding._grouped(q, k, v, cu_seqlens)
+        o, lse = _forward_grouped(checked, q, k, v, cu_seqlens, max_seqlen, causal, scale)
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
-        ctx.args = max_seqlen, causal, scale
+        ctx.args = checked, max_seqlen, causal, scale
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
-        grads = attention_backward_grouped(q, k, v, o, do.contiguous(), lse, cu_seqlens, *ctx.args)
-        return (*grads, None, None, None, None)
+        checked, max_seqlen, causal, scale = ctx.args
+        dq, dk, dv = _backward_grouped(checked, q, k, v, o, do.contiguous(), lse, cu_seqlens, max_seqlen, causal, scale, None)
+        return dq, dk, dv, None, None, None, None
 
 
 def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None):
