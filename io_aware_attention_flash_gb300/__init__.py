@@ -140,11 +140,12 @@ def _on_stream(fn):
     allocates belongs to that stream, so that its memory is not handed to
     another one while the kernels still use it."""
     @functools.wraps(fn)
-    def call(*args, stream=None, **kwargs):
+    def call(q, *args, stream=None, **kwargs):
         if stream is None:
-            return fn(*args, **kwargs)
+            return fn(q, *args, **kwargs)
+        _binding._stream_of(stream, q.get_device())  # refuses another device's
         with torch.cuda.stream(stream):
-            return fn(*args, **kwargs)
+            return fn(q, *args, **kwargs)
     return call
 
 
@@ -213,7 +214,11 @@ class _FlashAttentionGrouped(torch.autograd.Function):
 def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None):
     """Autograd-aware attention with grouped heads over a packed batch:
     q [T,H,d], k and v [T,Hk,d], cu_seqlens int32 [nseq+1] on the device,
-    max_seqlen the longest sequence.  Returns o [T,H,d]."""
+    max_seqlen the longest sequence.  Returns o [T,H,d], zeros in rows behind
+    the last sequence.  Differentiable once.  To capture a training step into
+    a CUDA graph, run it outside first and let go of that run's graph (its
+    outputs and losses): PyTorch cannot capture a backward pass into leaves
+    that a graph recorded outside still holds."""
     return _FlashAttentionGrouped.apply(q, k, v, cu_seqlens, max_seqlen, causal, scale)
 
 

@@ -142,7 +142,11 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _stream_of(stream, dev: int) -> int:
     """The given stream, or the current one of the tensors' device."""
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
+    if stream is None:
+        return _raw_stream(dev)
+    if stream.device_index != dev:
+        raise ValueError(f"the stream belongs to cuda:{stream.device_index}, the tensors are on cuda:{dev}")
+    return stream.cuda_stream
 
 
 def _device_of(name: str, t: torch.Tensor) -> int:

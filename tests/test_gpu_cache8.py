@@ -434,6 +434,31 @@ def test_attend_repeatable_streams_and_graph(d):
         assert all(torch.equal(a, b) for a, b in zip(want, cap))
 
 
+def test_cache_past_four_gigabytes():
+    """Pages whose bytes lie past 2^32 in the pool, stored and attended to."""
+    fa = require_gpu()
+    Hk, block, d, n = 8, 128, 128, 300
+    pages = 2 ** 32 // (Hk * block * d) + 40
+    cache = fa.cache8_alloc(pages, Hk, block, d)
+    table = torch.tensor([[pages - 1, 5, pages - 7]], dtype=torch.int32)
+    gen = torch.Generator().manual_seed(28)
+    k, v = (torch.randn(n, Hk, d, generator=gen).bfloat16() for _ in range(2))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    fa.cache8_store(k.cuda(), v.cuda(), cache, table.cuda(), i32([0, n]), i32([0]), n)
+    q = torch.randn(1, 1, 16, d, generator=gen).bfloat16()
+    o, lse = fa.attention_decode_cache8(q.cuda(), cache, table.cuda(), i32([n]), n)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    used = table[0].long()
+    ref = [np.zeros((3, Hk, block, d)), np.zeros((3, Hk, block, d)), np.ones((3, Hk)), np.ones((3, Hk))]
+    for x, c, s in ((k, 0, 2), (v, 1, 3)):
+        store_formula(f64(x), ref[c], ref[s], [[0, 1, 2]], [0, n], [0])
+    for t, want in zip(cache, ref):
+        assert np.array_equal(f64(t.view(torch.uint8)[used.cuda()].view(t.dtype) if t.dtype != torch.float32 else t[used.cuda()]), want)
+    O, L, vmax = attend_formula(f64(q), ref, np.array([[0, 1, 2]]), [n], d ** -0.5, False)
+    assert np.abs(f64(o) - O).max() <= 2.0 ** -7 * vmax and np.abs(f64(lse) - L).max() <= LSE_TOL
+
+
 # ---------------------------------------------------------------- together
 @pytest.mark.parametrize("d,block", [(64, 16), (128, 64)])
 def test_prompt_store_and_decoding_steps(d, block):
