@@ -41,7 +41,12 @@ __device__ __forceinline__ uint32_t pack_e4m3x2(float a, float b) {
   return r;
 }
 __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
-  return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
+  uint32_t r;
+  asm("{.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+      "mov.b32 %0, {l, h};}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 // Two e4m3 codes to two floats (exact).
 __device__ __forceinline__ void unpack_e4m3x2(uint32_t code2, float& a, float& b) {
@@ -56,6 +61,16 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+// Four e4m3 codes to four floats (exact).
+__device__ __forceinline__ void unpack_e4m3x4(uint32_t code4, float (&v)[4]) {
+  uint32_t a, b;
+  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
+      : "=r"(a), "=r"(b)
+      : "r"(code4));
+  asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}" : "=f"(v[0]), "=f"(v[1]) : "r"(a));
+  asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}" : "=f"(v[2]), "=f"(v[3]) : "r"(b));
 }
 
 // One group of TG threads quantises the new tokens of one (page, head) of K or
@@ -162,13 +177,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) fa_cache8_store_kernel(const Ca
     } else if (t < old && again) {
       const uint2 code = out[c * TG];
       const float f = held * inv;
-      float v[8];
-      unpack_e4m3x2(code.x, v[0], v[1]);
-      unpack_e4m3x2(code.x >> 16, v[2], v[3]);
-      unpack_e4m3x2(code.y, v[4], v[5]);
-      unpack_e4m3x2(code.y >> 16, v[6], v[7]);
+      float v[4], w[4];
+      unpack_e4m3x4(code.x, v);
+      unpack_e4m3x4(code.y, w);
       out[c * TG] = make_uint2(pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
-                               pack_e4m3x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f));
+                               pack_e4m3x4(w[0] * f, w[1] * f, w[2] * f, w[3] * f));
     }
   }
 }
@@ -272,7 +285,7 @@ struct Walk {
 // The largest value of the warp, in every lane.
 __device__ __forceinline__ float warp_max(float v) {
   float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -343,8 +356,8 @@ struct Dec8Cfg {
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
   static constexpr int OFF_Q = OFF_V + NST * TILE_BYTES;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_SC = OFF_P + 2 * P_BYTES;         // (two P buffers) [NST][8 pages][2] scales of K, V
-  static constexpr int OFF_QS = OFF_SC + NST * 8 * 2 * 4;    // [RP] score factor of each row
+  static constexpr int OFF_SC = OFF_P + 2 * P_BYTES;         // (two P buffers) [NST][8 pages][4]: K's scale, 1 / V's, its log2
+  static constexpr int OFF_QS = OFF_SC + NST * 8 * 16;    // [RP] score factor of each row
   static constexpr int OFF_XCH = OFF_QS + kRowsMax * 4;      // [2][4 warps][RP]
   static constexpr int STAT_WARP = 3 * RW < 4 ? 4 : 3 * RW;  // reference, alpha, weight of each row
   static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [2 tiles][NCW][STAT_WARP]
@@ -586,9 +599,10 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
         }
         const float ks = __shfl_sync(0xffffffffu, cur.ks, from & 31), vs = __shfl_sync(0xffffffffu, cur.vs, from & 31);
         if (lane < ppt) {
-          float* sc = reinterpret_cast<float*>(smem + C::OFF_SC) + (st * 8 + lane) * 2;
-          sc[0] = lane < n_pages ? ks : 0.f;
-          sc[1] = lane < n_pages ? vs : 0.f;
+          // V's scale by its exponent, a power of two; 1 for a page of zeros and for none
+          const int ve = vs > 0.f ? static_cast<int>(__float_as_uint(vs) >> 23) - 127 : 0;
+          reinterpret_cast<float4*>(smem + C::OFF_SC)[st * 8 + lane] =
+              lane < n_pages ? make_float4(ks, exp2_int(-ve), static_cast<float>(ve), 0.f) : make_float4(0.f, 1.f, 0.f, 0.f);
         }
         mbar_arrive(bar(C::B_FULL + st));
       }
@@ -659,6 +673,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
     constexpr int LPR = 32 / RW;  // lanes that keep one row's statistics
     const int my_row = lane / LPR;  // within the warpgroup's rows
     int t = 0, nx = 0, n_item = 0;
+    int st = 0;             // tile t's ring stage, and its phase there
+    uint32_t st_phase = 0;
     bool ok = true;
     auto wait = [&](int i, uint32_t ph) {
       ok = ok && wait_bounded(bar(i), ph, abort_flag, p.err, p.timeout_ns);
@@ -763,15 +779,13 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
             });
         tc_fence_before();
       };
+      // tiles of which some row does not see all keys: from this one on
+      const int kt_mask = max(0, w.len - (p.causal ? p.Nq - 1 : 0)) / kTile;
       for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
-        const int st = t % C::NST;
-        wait(C::B_FULL + st, (t / C::NST) & 1);
-        const int key = kt * kTile + r;
-        const float* sc = reinterpret_cast<const float*>(smem + C::OFF_SC) + (st * 8 + (r >> p.block_shift)) * 2;
-        const float ks = sc[0], vs = sc[1];
-        // log2 of V's scale: 0 for a page of zeros, whatever its scale
-        const int ve = vs > 0.f ? static_cast<int>(__float_as_uint(vs) >> 23) - 127 : 0;
-        const float vef = static_cast<float>(ve);
+        wait(C::B_FULL + st, st_phase);
+        // K's scale, 1 / V's scale and its log2 for this thread's key
+        const float4 sc = reinterpret_cast<const float4*>(smem + C::OFF_SC)[st * 8 + (r >> p.block_shift)];
+        const float ks = sc.x, inv_vs = sc.y, vef = sc.z;
         wait(C::B_SFULL + (t & 1), (t >> 1) & 1);
         __syncwarp();
         tc_fence_after();
@@ -785,10 +799,10 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
               f2_unpack(ffma2(s, fmul2(f2_pack(ks, ks), f2_pack(qf[q], qf[q + 1])), f2_pack(vef, vef)), y[q], y[q + 1]);
             },
             [&](int q) { y[q] = fmaf(__uint_as_float(sv[q]) + __uint_as_float(sv[RW + q]), ks * qf[q], vef); });
-        if (kt * kTile + kTile > w.len - (p.causal ? p.Nq - 1 : 0)) {  // some row does not see all of the tile
+        if (kt >= kt_mask) {
 #pragma unroll
           for (int q = 0; q < RW; ++q)
-            if (key >= w.len - __shfl_sync(0xffffffffu, row_hidden, q * LPR)) y[q] = -CUDART_INF_F;
+            if (kt * kTile + r >= w.len - __shfl_sync(0xffffffffu, row_hidden, q * LPR)) y[q] = -CUDART_INF_F;
         }
         // ---- the tile's largest y of each row: over the warp, then over the
         // four warps; lane q does the rest of row q's statistics and leaves
@@ -817,7 +831,6 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
           m = m_new;
           __syncwarp();
         }
-        const float inv_vs = exp2_int(-ve);
         {
           float ref[RW], alpha[RW], wt[RW];
           load_row<RW>(stat, ref);
@@ -839,21 +852,21 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
                 y[q] = ex2_approx(y[q] - ref[q]);
                 lsum[q] = fmaf(y[q], inv_vs * wt[q], lsum[q] * alpha[q]);
               });
+          if constexpr (RW % 4 == 0) {
 #pragma unroll
-          for (int q = 0; q < RW; q += 2) {
-            const float p1 = q + 1 < RW ? y[q + 1 < RW ? q + 1 : q] : 0.f;
-            float h0, h1, e0, e1;
-            const uint32_t c = pack_e4m3x2(y[q], p1);
-            unpack_e4m3x2(c, h0, h1);
-            f2_unpack(fsub2(f2_pack(y[q], p1), f2_pack(h0, h1)), e0, e1);
-            const uint32_t e = pack_e4m3x2(e0, e1);
-            if (q % 4 == 0) {
-              hi[q / 4] = c;
-              lo[q / 4] = e;
-            } else {
-              hi[q / 4] |= c << 16;
-              lo[q / 4] |= e << 16;
+            for (int q = 0; q < RW; q += 4) {
+              float h[4], e[4];
+              hi[q / 4] = pack_e4m3x4(y[q], y[q + 1], y[q + 2], y[q + 3]);
+              unpack_e4m3x4(hi[q / 4], h);
+              f2_unpack(fsub2(f2_pack(y[q], y[q + 1]), f2_pack(h[0], h[1])), e[0], e[1]);
+              f2_unpack(fsub2(f2_pack(y[q + 2], y[q + 3]), f2_pack(h[2], h[3])), e[2], e[3]);
+              lo[q / 4] = pack_e4m3x4(e[0], e[1], e[2], e[3]);
             }
+          } else {
+            float h, unused;
+            hi[0] = pack_e4m3x2(y[0], 0.f);
+            unpack_e4m3x2(hi[0], h, unused);
+            lo[0] = pack_e4m3x2(y[0] - h, 0.f);
           }
           // the key's columns (d = 64: of its half of the keys): a warpgroup's
           // rows' hi terms, then their lo terms
@@ -866,7 +879,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
           else
             *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>((hi[0] & 0xffu) | (lo[0] << 8));
         }
-        if (wg == 0 && key >= w.len) {  // slots without a token may hold NaN, and 0 · NaN is not 0
+        // slots without a token may hold NaN, and 0 · NaN is not 0
+        if (wg == 0 && kt >= kt_mask && kt * kTile + r >= w.len) {
           uint4* vrow = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::TILE_BYTES + r * D);
 #pragma unroll
           for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -877,6 +891,10 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
         // The product of the tile before is ready by now: waiting for this one's
         // would leave the warps idle for its whole latency.
         if (kt > w.k0) add_o(t - 1);
+        if (++st == C::NST) {
+          st = 0;
+          st_phase ^= 1u;
+        }
       }
       add_o(t - 1);
       // ---- the item's sums: l over the keys, O over the halves
