@@ -12,7 +12,7 @@ module allocates outputs and workspace and calls the binding.
 """
 from __future__ import annotations
 
-import functools
+import contextlib
 from typing import NamedTuple
 
 import torch
@@ -135,28 +135,29 @@ def flash_attention(q, k, v, causal: bool = False, scale=None):
 # ---------------------------------------------------------------------------
 # Grouped heads over packed batches: H query heads share Hk key/value heads.
 # ---------------------------------------------------------------------------
-def _on_stream(fn):
-    """A call on a stream of its own runs with that stream current: what it
-    allocates belongs to that stream, so that its memory is not handed to
-    another one while the kernels still use it."""
-    @functools.wraps(fn)
-    def call(q, *args, stream=None, **kwargs):
-        if stream is None:
-            return fn(q, *args, **kwargs)
-        _binding._stream_of(stream, q.get_device())  # refuses another device's
-        with torch.cuda.stream(stream):
-            return fn(q, *args, **kwargs)
-    return call
+# Each call first goes to its compiled counterpart, which returns None where
+# something is not in order; the Python path then runs or says what is wrong.
+def _on_stream(stream, t):
+    """What a call on a stream of its own allocates belongs to that stream, so
+    that its memory is not handed to another one while the kernels still use
+    it.  Refuses a stream of another device than the tensor's."""
+    if stream is None:
+        return contextlib.nullcontext()
+    _binding._stream_of(stream, t.get_device())
+    return torch.cuda.stream(stream)
 
 
-@_on_stream
-def attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None):
+def attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None, stream=None):
     """Packed batch with grouped heads: q [T,H,d], k and v [T,Hk,d] (H a
     multiple of Hk; slices of one wider projection are taken as they are).
     Returns (o [T,H,d] bf16, lse [H,T] fp32); rows behind the last sequence
-    get o = 0, lse = -inf.  stream: the stream to run on (default: the
-    current one)."""
-    return _forward_grouped(_binding._grouped(q, k, v, cu_seqlens), q, k, v, cu_seqlens, max_seqlen, causal, scale)
+    get o = 0, lse = -inf."""
+    if stream is None:
+        out = _binding.native().forward_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
+        if out is not None:
+            return out
+    with _on_stream(stream, q):
+        return _forward_grouped(_binding._grouped(q, k, v, cu_seqlens), q, k, v, cu_seqlens, max_seqlen, causal, scale)
 
 
 def _forward_grouped(checked, q, k, v, cu_seqlens, max_seqlen, causal, scale):
@@ -167,14 +168,17 @@ def _forward_grouped(checked, q, k, v, cu_seqlens, max_seqlen, causal, scale):
     return o, lse
 
 
-@_on_stream
 def attention_backward_grouped(q, k, v, o, dout, lse, cu_seqlens, max_seqlen: int, causal: bool = False, scale=None,
-                               workspace=None):
+                               stream=None, workspace=None):
     """Returns (dq [T,H,d], dk, dv [T,Hk,d]), zero in rows behind the last
-    sequence.  dk and dv are summed over the query heads that share them.
-    stream: the stream to run on (default: the current one)."""
-    checked = _binding._grouped(q, k, v, cu_seqlens)
-    return _backward_grouped(checked, q, k, v, o, dout, lse, cu_seqlens, max_seqlen, causal, scale, workspace)
+    sequence.  dk and dv are summed over the query heads that share them."""
+    if stream is None and workspace is None:
+        out = _binding.native().backward_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale, o, dout, lse)
+        if out is not None:
+            return out
+    with _on_stream(stream, q):
+        return _backward_grouped(_binding._grouped(q, k, v, cu_seqlens), q, k, v, o, dout, lse, cu_seqlens, max_seqlen,
+                                 causal, scale, workspace)
 
 
 def _backward_grouped(checked, q, k, v, o, dout, lse, cu_seqlens, max_seqlen, causal, scale, workspace):
@@ -219,6 +223,9 @@ def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool =
     a CUDA graph, run it outside first and let go of that run's graph (its
     outputs and losses): PyTorch cannot capture a backward pass into leaves
     that a graph recorded outside still holds."""
+    o = _binding.native().flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
+    if o is not None:
+        return o
     return _FlashAttentionGrouped.apply(q, k, v, cu_seqlens, max_seqlen, causal, scale)
 
 
@@ -246,26 +253,29 @@ def cache8_store(k, v, cache: Cache8, block_table, cu_seqlens, start, max_new: i
     of k, v [T,Hk,d] become tokens start[b], start[b]+1, ... of sequence b,
     in the pages block_table [B,cols] names (int32, as cu_seqlens [B+1] and
     start [B]); max_new is the largest number of new tokens of a sequence."""
+    if stream is None and _binding.native().cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new):
+        return
     fa_cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new, stream)
 
 
-@_on_stream
 def attention_decode_cache8(q, cache: Cache8, block_table, seqlens, max_seqlen: int, causal: bool = False, scale=None,
-                            workspace=None):
+                            stream=None, workspace=None):
     """Decode over the 8-bit paged cache: q [B,Nq,H,d] (Nq <= 8 newest tokens),
     seqlens int32 [B] cached tokens (the new ones among them; 0 for an empty
     slot), max_seqlen at least every length.  Returns (o [B,Nq,H,d] bf16, lse
-    [B,H,Nq] fp32).  causal as in attention_decode.  stream: the stream to run
-    on (default: the current one)."""
+    [B,H,Nq] fp32).  causal as in attention_decode."""
+    if stream is None and workspace is None:
+        out = _binding.native().decode_cache8(q, cache, block_table, seqlens, max_seqlen, causal, scale)
+        if out is not None:
+            return out
     checked = _binding._decode_cache8(q, cache, block_table, seqlens)
     dev, B, Nq, H, d, _, Hk = checked[:7]
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, Nq), device=q.device, dtype=torch.float32)
-    if workspace is None:
-        n = fa_decode_cache8_workspace_bytes(B, Nq, H, Hk, max_seqlen, d)
-        workspace = torch.empty(n, device=q.device, dtype=torch.uint8)
-    else:
-        n = _binding._nbytes(workspace, dev)
-    _binding._launch_decode_cache8(checked, q, cache, block_table, seqlens, o, lse, workspace, n, max_seqlen, causal, scale,
-                                   None)
+    with _on_stream(stream, q):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            n = fa_decode_cache8_workspace_bytes(B, Nq, H, Hk, max_seqlen, d)
+            workspace = torch.empty(n, device=q.device, dtype=torch.uint8)
+        _binding._launch_decode_cache8(checked, q, cache, block_table, seqlens, o, lse, workspace,
+                                       _binding._nbytes(workspace, dev), max_seqlen, causal, scale, None)
     return o, lse

@@ -9,6 +9,7 @@ with an error instead of falling back to anything.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -16,6 +17,7 @@ import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libfa_gb300.so")
+TORCH_LIB_PATH = os.path.join(_PKG, "lib", "_fa_torch.so")
 
 FA_OK = 0
 STATUS_NAMES = {
@@ -70,6 +72,7 @@ MICROBENCH = {"ex2_per_sm_clk": 0, "cvt_bf16x2_per_sm_clk": 1, "ffma_per_sm_clk"
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 _lib = None
+_native = None
 _lock = threading.Lock()
 
 
@@ -98,6 +101,26 @@ def lib() -> ctypes.CDLL:
                     fn.argtypes = args
                 _lib = handle
     return _lib
+
+
+def native():
+    """The compiled calls of the grouped-head and cache entry points (once
+    loaded).  Each does what the Python helper of its name does and returns
+    None where anything is not in order; the helper then takes the Python path,
+    which says what.  Raises if the library has not been built."""
+    global _native
+    if _native is None:
+        lib()
+        with _lock:
+            if _native is None:
+                if not os.path.exists(TORCH_LIB_PATH):
+                    raise RuntimeError(
+                        f"{TORCH_LIB_PATH} is missing: build it with `python -m io_aware_attention_flash_gb300.build`")
+                spec = importlib.util.spec_from_file_location("_fa_torch", TORCH_LIB_PATH)
+                module = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(module)
+                _native = module
+    return _native
 
 
 def _check(fn: str, status: int) -> None:
@@ -272,8 +295,15 @@ def _grouped(q, k, v, cu_seqlens):
     return dev, T, H, Hk, d, nseq, ldq, ldk, ldv
 
 
+def _count(name: str, n: int) -> int:
+    if not 0 <= n < 2 ** 31:
+        raise ValueError(f"{name} must be an int32 count (got {n})")
+    return n
+
+
 def _launch_fwd_grouped(checked, q, k, v, o, lse, cu_seqlens, max_seqlen, causal, scale, stream, zero_tail) -> None:
     dev, T, H, Hk, d, nseq, ldq, ldk, ldv = checked
+    _count("max_seqlen", max_seqlen)
     _check("fa_fwd_grouped", lib().fa_fwd_grouped(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), cu_seqlens.data_ptr(), nseq,
         max_seqlen, T, H, Hk, d, ldq, ldk, ldv, _scale(scale, d), bool(causal), zero_tail, _stream_of(stream, dev)))
@@ -298,6 +328,7 @@ def fa_bwd_grouped_workspace_bytes(nseq: int, max_seqlen: int, total: int, H: in
 def _launch_bwd_grouped(checked, q, k, v, o, dout, lse, dq, dk, dv, workspace, nbytes, cu_seqlens, max_seqlen, causal,
                         scale, stream, zero_tail) -> None:
     dev, T, H, Hk, d, nseq, ldq, ldk, ldv = checked
+    _count("max_seqlen", max_seqlen)
     _dense("o", o, torch.bfloat16, (T, H, d), dev)
     _dense("dout", dout, torch.bfloat16, (T, H, d), dev)
     _dense("lse", lse, torch.float32, (H, T), dev)
@@ -355,6 +386,7 @@ def fa_cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new: int, s
     cols = _block_table(block_table, B, dev)
     _dense("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev)
     _dense("start", start, torch.int32, (B,), dev)
+    _count("max_new", max_new)
     ck, cv, sk, sv = cache
     _check("fa_cache8_store", lib().fa_cache8_store(
         k.data_ptr(), v.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(), sv.data_ptr(), block_table.data_ptr(),
@@ -384,6 +416,7 @@ def _decode_cache8(q, cache, block_table, seqlens):
 def _launch_decode_cache8(checked, q, cache, block_table, seqlens, o, lse, workspace, nbytes, max_seqlen, causal, scale,
                           stream) -> None:
     dev, B, Nq, H, d, num_blocks, Hk, block, cols = checked
+    _count("max_seqlen", max_seqlen)
     ck, cv, sk, sv = cache
     _check("fa_fwd_decode_cache8", lib().fa_fwd_decode_cache8(
         q.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(), sv.data_ptr(), block_table.data_ptr(),

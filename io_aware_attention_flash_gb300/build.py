@@ -2,8 +2,10 @@
 
 Each translation unit is compiled in its own nvcc process (in parallel), then
 linked into ``io_aware_attention_flash_gb300/lib/libfa_gb300.so`` with the
-CUDA runtime linked statically.  A rebuild happens only when a source or
-header is newer than the library.
+CUDA runtime linked statically.  Beside it, the host compiler builds
+``lib/_fa_torch.so``, the calls from PyTorch that do without the interpreter
+(linked against libfa_gb300.so next to it).  A rebuild happens only when a
+source or header is newer than the libraries.
 
     python -m io_aware_attention_flash_gb300.build [--force] [--verbose]
 """
@@ -23,6 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa_gb300.so")
+TORCH_LIB_PATH = os.path.join(LIB_DIR, "_fa_torch.so")
+TORCH_SOURCE = "fa_torch.cpp"
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_cache8.cu", "fa_microbench.cu"]
 HEADERS = ["ptx.cuh", "fa_kernels.cuh"]
@@ -39,16 +43,16 @@ def _nvcc() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS + [TORCH_SOURCE]]
     files.append(os.path.join(INCLUDE, "fa.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_LIB_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_LIB_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -64,6 +68,39 @@ def _compile(nvcc: str, src: str, verbose: bool) -> tuple[str, str]:
     return obj, log
 
 
+def _compile_torch(verbose: bool) -> str:
+    """The PyTorch calls' object file, with the compiler ABI PyTorch has."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    obj = os.path.join(BUILD_DIR, "fa_torch.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    for inc in (root, os.path.join(root, "torch", "csrc", "api", "include"), cuda, sysconfig.get_paths()["include"]):
+        cmd += ["-isystem", inc]
+    cmd += ["-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {TORCH_SOURCE}:\n{' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    return obj
+
+
+def _link_torch(obj: str) -> None:
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_LIB_PATH + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", LIB_DIR, "-l:libfa_gb300.so", "-L", libs, "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    os.replace(tmp, TORCH_LIB_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link the library if needed; returns its path."""
     if not force and up_to_date():
@@ -71,8 +108,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        torch_obj = ex.submit(_compile_torch, verbose)
         results = list(ex.map(lambda s: _compile(nvcc, s, verbose), SOURCES))
+        torch_obj = torch_obj.result()
     objs = [o for o, _ in results]
     with open(os.path.join(BUILD_DIR, "ptxas.log"), "w") as f:
         for _, log in results:
@@ -83,6 +122,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_torch(torch_obj)
     return LIB_PATH
 
 

@@ -535,3 +535,30 @@ def test_refusals():
         s(k, k, cache, table, cu, start, 0)
     torch.cuda.synchronize()
     assert_no_device_error(fa)
+
+
+def test_compiled_and_python_calls_agree():
+    fa = require_gpu()
+    from io_aware_attention_flash_gb300 import _binding
+    n = _binding.native()
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    caches = [random_cache(fa, 6, 2, 16, 64, seed=29) for _ in range(2)]
+    k, v = (torch.randn(20, 2, 64).bfloat16().cuda() for _ in range(2))
+    table, cu, start = i32([[0, 1, 2], [3, 4, 5]]), i32([0, 5, 20]), i32([7, 2])
+    assert n.cache8_store(k, v, caches[0], table, cu, start, 15) is True
+    fa.fa_cache8_store(k, v, caches[1], table, cu, start, 15)
+    assert all(torch.equal(bits(a), bits(b)) for a, b in zip(*caches))
+    q, lens = torch.randn(2, 1, 6, 64).bfloat16().cuda(), i32([12, 17])
+    got = n.decode_cache8(q, caches[0], table, lens, 48, True, None)
+    ws = torch.empty(fa.fa_decode_cache8_workspace_bytes(2, 1, 6, 2, 48, 64), dtype=torch.uint8, device="cuda")
+    want = fa.attention_decode_cache8(q, caches[0], table, lens, 48, True, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    for bad in ((q.float(), caches[0], table, lens, 48, True, None), (q, caches[0][:3], table, lens, 48, True, None),
+                (q, caches[0], table[:1], lens, 48, True, None), (q, caches[0], table, lens, -1, True, None),
+                (q, caches[0], table, lens.long(), 48, True, None), (q, caches[0], table, lens, 48, True, 0.0)):
+        assert n.decode_cache8(*bad) is None
+    assert n.cache8_store(k, v[:3], caches[0], table, cu, start, 15) is None
+    with pytest.raises(ValueError):
+        fa.cache8_store(k, v, caches[0], table, cu, start, 2 ** 32 + 1)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)

@@ -324,3 +324,37 @@ def test_refusals():
         fa.attention_backward_grouped(q, k, v, o, do, lse, cu, 40, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     assert_no_device_error(fa)
+
+
+def test_compiled_and_python_calls_agree():
+    """The helpers' compiled calls do what their Python paths do, and hand over
+    what is not in order."""
+    fa = require_gpu()
+    from io_aware_attention_flash_gb300 import _binding
+    n = _binding.native()
+    cu, q, k, v, do = (t.cuda() for t in make([40, 200], 4, 2, 64, seed=14, pad=5))
+    o, lse = n.forward_grouped(q, k, v, cu, 200, True, None)
+    checked = _binding._grouped(q, k, v, cu)
+    o1, lse1 = fa._forward_grouped(checked, q, k, v, cu, 200, True, None)
+    assert torch.equal(o, o1) and torch.equal(lse, lse1)
+    _, dk, dv = n.backward_grouped(q, k, v, cu, 200, True, 0.3, o, do, lse)
+    _, dk1, dv1 = fa._backward_grouped(checked, q, k, v, o, do, lse, cu, 200, True, 0.3, None)
+    assert torch.equal(dk, dk1) and torch.equal(dv, dv1)
+    leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+    o2 = n.flash_attention_grouped(*leaves, cu, 200, True, None)
+    o3 = fa._FlashAttentionGrouped.apply(*leaves, cu, 200, True, None)
+    assert torch.equal(o2, o3) and o2.requires_grad
+    for a, b in zip(torch.autograd.grad(o2, leaves[1:], do), torch.autograd.grad(o3, leaves[1:], do)):
+        assert torch.equal(a, b)
+    with pytest.raises(RuntimeError):
+        o2 = n.flash_attention_grouped(*leaves, cu, 200, True, None)
+        (g,) = torch.autograd.grad(o2, leaves[0], do, create_graph=True)
+        g.sum().backward()
+    for bad in ((q.float(), k, v, cu, 200, True, None), (q, k, v, cu.cpu(), 200, True, None), (q, k, v, cu, 0, True, None),
+                (q, k, v, cu, 2 ** 32 + 200, True, None), (q, k, v, cu, 200, True, -1.0), (q, k, v, cu, 200, True, "1"),
+                (q, k, 3, cu, 200, True, None), (q, k, v, cu)):
+        assert n.forward_grouped(*bad) is None and n.flash_attention_grouped(*bad) is None
+    with pytest.raises(ValueError):
+        fa.attention_forward_grouped(q, k, v, cu, 2 ** 32 + 200)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
