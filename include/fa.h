@@ -173,8 +173,8 @@ FA_API fa_status fa_fwd_grouped(const void* q, const void* k, const void* v, voi
                                 const int* cu_seqlens, int nseq, int max_seqlen, int total, int H, int Hk, int d,
                                 long long ldq, long long ldk, long long ldv, float scale, int causal, int zero_tail,
                                 void* stream);
-/* Workspace of fa_bwd_grouped: D [H, total], the fp32 dQ accumulator, and,
- * where few long sequences would leave SMs idle, fp32 parts of dK and dV.
+/* Workspace of fa_bwd_grouped: D [H, total], and [nseq, H, 16] for each
+ * sequence's first rows, the fp32 dQ accumulator, and, where few long sequences would leave SMs idle, fp32 parts of dK and dV.
  * 0 for arguments that fa_bwd_grouped rejects. */
 FA_API size_t fa_bwd_grouped_workspace_bytes(int nseq, int max_seqlen, int total, int H, int Hk, int d, int causal);
 FA_API fa_status fa_bwd_grouped(const void* q, const void* k, const void* v, const void* o, const void* dout,

@@ -351,15 +351,16 @@ int grouped_splits(int total, int max_seqlen, int H, int Hk, int causal) {
 }
 
 struct GroupedWs {
-  size_t dq_off, part_off, bytes;
+  size_t short_off, dq_off, part_off, bytes;
   int splits;
 };
 
-GroupedWs grouped_ws(int total, int max_seqlen, int H, int Hk, int d, int causal) {
+GroupedWs grouped_ws(int nseq, int total, int max_seqlen, int H, int Hk, int d, int causal) {
   GroupedWs w{};
   w.splits = grouped_splits(total, max_seqlen, H, Hk, causal);
   const size_t rows128 = static_cast<size_t>((total + 127LL) / 128) * 128;
-  w.dq_off = pad256(static_cast<size_t>(total) * H * 4);
+  w.short_off = pad256(static_cast<size_t>(total) * H * 4);
+  w.dq_off = w.short_off + pad256(static_cast<size_t>(nseq) * H * fa::kExactRows * 4);
   w.part_off = w.dq_off + rows128 * H * d * 4;
   w.bytes = w.part_off + (w.splits > 1 ? static_cast<size_t>(2) * w.splits * total * Hk * d * 4 : 0);
   return w;
@@ -601,7 +602,7 @@ FA_API fa_status fa_fwd_grouped(const void* q, const void* k, const void* v, voi
 
 FA_API size_t fa_bwd_grouped_workspace_bytes(int nseq, int max_seqlen, int total, int H, int Hk, int d, int causal) {
   if (check_grouped(nseq, max_seqlen, total, H, Hk, d, 1.0f) != FA_OK) return 0;
-  return grouped_ws(total, max_seqlen, H, Hk, d, causal).bytes;
+  return grouped_ws(nseq, total, max_seqlen, H, Hk, d, causal).bytes;
 }
 
 FA_API fa_status fa_bwd_grouped(const void* q, const void* k, const void* v, const void* o, const void* dout,
@@ -615,7 +616,7 @@ FA_API fa_status fa_bwd_grouped(const void* q, const void* k, const void* v, con
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
     return FA_ERR_ALIGN;
   if (!stride_ok(ldq, H, d) || !stride_ok(ldk, Hk, d) || !stride_ok(ldv, Hk, d)) return FA_ERR_SHAPE;
-  const GroupedWs w = grouped_ws(total, max_seqlen, H, Hk, d, causal);
+  const GroupedWs w = grouped_ws(nseq, total, max_seqlen, H, Hk, d, causal);
   if (!workspace || workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FA_ERR_ALIGN;
   DeviceGuard guard;
@@ -624,10 +625,17 @@ FA_API fa_status fa_bwd_grouped(const void* q, const void* k, const void* v, con
   FA_TRY(error_word(&p.err));
   p.sv = grouped_view(cu_seqlens, nseq, max_seqlen, total, H, Hk, zero_tail);
   p.sv.splits = w.splits;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.ldv = ldv;
   p.o = static_cast<const uint16_t*>(o);
   p.dout = static_cast<const uint16_t*>(dout);
   p.lse = lse;
   p.dpsum = static_cast<float*>(workspace);
+  p.d_short = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.short_off);
   p.dq_accum = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.dq_off);
   p.dkv_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part_off);
   p.dq = static_cast<uint16_t*>(dq);

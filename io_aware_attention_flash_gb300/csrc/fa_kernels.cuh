@@ -132,6 +132,8 @@ struct FwdParams {
   uint64_t timeout_ns;
 };
 
+constexpr int kExactRows = 16;  // grouped backward: rows of a sequence whose D is formed from P and dP
+
 struct BwdParams {
   SeqView sv;
   const uint16_t* o;
@@ -147,6 +149,11 @@ struct BwdParams {
   int causal;
   int rows;               // B*N (dense) or total (packed): rows of the [rows, H, d] view
   int nseq;               // B (dense) or nseq (packed)
+  const uint16_t* q;      // grouped heads: bf16 rows ldq, ldk, ldv elements apart
+  const uint16_t* k;
+  const uint16_t* v;
+  long long ldq, ldk, ldv;
+  float* d_short;         // D of the first rows of each sequence, fp32 [nseq, H, kExactRows]
   float* dkv_part;        // grouped heads in several parts: fp32 [2 (dK, dV), splits, rows, Hk, d]
   uint32_t* err;
   uint64_t timeout_ns;

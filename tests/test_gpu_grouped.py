@@ -285,7 +285,9 @@ def test_own_stream_and_captured_training_step():
 
 
 def test_single_heads_match_the_packed_entry_points():
-    """H = Hk: the outputs of the existing packed entry points."""
+    """H = Hk: the outputs of the packed entry points; dK (and dQ) up to the
+    rows that see few keys, whose row statistic is exact here: each side's own
+    error is at most GRAD_TOL."""
     fa = require_gpu()
     lengths = [100, 257]
     cu, q, k, v, do = (t.cuda() for t in make(lengths, 3, 3, 128, seed=12))
@@ -295,7 +297,30 @@ def test_single_heads_match_the_packed_entry_points():
     assert torch.equal(lse[:, :100], lse1[0, :, :100]) and torch.equal(lse[:, 100:], lse1[1])
     _, dk, dv = fa.attention_backward_grouped(q, k, v, o, do, lse, cu, 257, True)
     _, dk1, dv1 = fa.attention_backward_varlen(q, k, v, o1, do, lse1, cu, 257, True)
-    assert torch.equal(dk, dk1) and torch.equal(dv, dv1)
+    assert torch.equal(dv, dv1) and rel_fro(f64(dk), f64(dk1)) <= 2 * GRAD_TOL
+    assert torch.equal(dk[16:100], dk1[16:100]) or rel_fro(f64(dk[16:100]), f64(dk1[16:100])) <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 7, 16, 17, 30])
+def test_gradients_of_short_sequences(n, d, causal):
+    """Rows that see few keys, where dP - D is a small difference of large
+    numbers: dS = 0 exactly for one key; else the roundings of dS and of the
+    output (each at most 2^-8 of a value, as independent errors 2.3e-3 in the
+    norm, 3.3e-3 together) are all that is left: held to 5e-3."""
+    fa = require_gpu()
+    cu, q, k, v, do = make([n] * 12, 6, 2, d, seed=20 + n)
+    dev = [t.cuda() for t in (q, k, v, do, cu)]
+    o, lse = fa.attention_forward_grouped(*dev[:3], dev[4], n, causal)
+    grads = fa.attention_backward_grouped(*dev[:3], o, dev[3], lse, dev[4], n, causal)
+    _, _, *ref = formula(cu, q, k, v, do, d ** -0.5, causal)
+    for g, r in zip(grads, ref):
+        if n == 1 and not r.any():
+            assert not g.float().any()
+        else:
+            assert rel_fro(f64(g), r) <= 5e-3
+    assert_no_device_error(fa)
 
 
 def test_refusals():
