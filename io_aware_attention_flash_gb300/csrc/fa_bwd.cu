@@ -68,7 +68,7 @@ __device__ __forceinline__ void locate_row(const SeqView& sv, int nseq, int g, i
 // definition Σ_j P_ij dP_ij instead.  There dP − D is a small difference (none
 // at all for one key), in which O's rounding to bf16 shows: relative errors of
 // dQ and dK of 4e-3 to 8e-3 at two keys and 3.0e-3 at sixteen, against
-// 2.4e-3 to 2.6e-3 for long rows.  Blocks of their own behind the others form
+// 2.4e-3 to 2.6e-3 for long rows.  Blocks of their own before the others form
 // them, so that no other row has to find out which sequence it is in: d_short
 // [nseq, H, kExactRows], read by the main kernel in D's place.
 __device__ __forceinline__ bool exact_row(const BwdParams& p, int seqlen, int q) {
@@ -111,10 +111,11 @@ __device__ __forceinline__ void short_rows(const BwdParams& p, long long tid) {
     return v;
   };
   float sum = 0.f;
-  for (int j0 = 0; j0 < steps; j0 += 4) {  // four keys' loads in flight
-    uint4 k[4], v[4];
+#pragma unroll 1
+  for (int j0 = 0; j0 < steps; j0 += 2) {  // two keys' loads in flight: more would cost the other rows' occupancy
+    uint4 k[2], v[2];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       k[u] = v[u] = zero;
       if (j0 + u < seen) {
         const size_t row = static_cast<size_t>(sp.row_base) + j0 + u;
@@ -123,7 +124,7 @@ __device__ __forceinline__ void short_rows(const BwdParams& p, long long tid) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < 2; ++u) {
       const float s = dot(q, k[u]), dp = dot(dout, v[u]);
       if (j0 + u < seen) sum = fmaf(ex2_approx(fmaf(s, p.scale_log2, -lse2)), dp, sum);
     }
@@ -132,19 +133,19 @@ __device__ __forceinline__ void short_rows(const BwdParams& p, long long tid) {
 }
 
 template <int D, bool GRP = false>
-__global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(256, GRP ? 6 : 1) fa_bwd_pre_kernel(const BwdParams p) {
   grid_launch_dependents();  // the main kernel's prologue and first MMAs need nothing from here
   constexpr int TPR = D / 8;  // threads per (row, head); rows do not straddle warps (TPR divides 32)
   static_assert(32 % TPR == 0, "a (row, head) lies within one warp");
   const int H = p.sv.H;
   const long long total = static_cast<long long>(p.rows) * H;
-  const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if constexpr (GRP) {
-    const long long blocks = (total * TPR + 255) / 256;
-    if (blockIdx.x >= blocks) {
-      short_rows<D>(p, tid - blocks * 256);
+  long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if constexpr (GRP) {  // the few rows with a long chain of loads first
+    if (blockIdx.x < p.short_blocks) {
+      short_rows<D>(p, tid);
       return;
     }
+    tid -= static_cast<long long>(p.short_blocks) * 256;
   }
   const long long rh = tid / TPR;  // (row, head) = row·H + head
   const int part = static_cast<int>(tid % TPR);
@@ -1114,10 +1115,15 @@ cudaError_t launch_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(ctas));
   const long long pairs = static_cast<long long>(p.rows) * p.sv.H;
+  BwdParams pp = p;
   long long pre_blocks = (pairs * (D / 8) + 255) / 256;
-  if (GRP) pre_blocks += (static_cast<long long>(p.nseq) * p.sv.H * kExactRows * (D / 8) + 255) / 256;
-  if (pre_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  fa_bwd_pre_kernel<D, GRP><<<static_cast<unsigned>(pre_blocks), 256, 0, s>>>(p);
+  if (GRP) {
+    const long long n = (static_cast<long long>(p.nseq) * p.sv.H * kExactRows * (D / 8) + 255) / 256;
+    pre_blocks += n;
+    if (pre_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    pp.short_blocks = static_cast<unsigned>(n);
+  }
+  fa_bwd_pre_kernel<D, GRP><<<static_cast<unsigned>(pre_blocks), 256, 0, s>>>(pp);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (ev0 && (e = cudaEventRecord(ev0, s)) != cudaSuccess) return e;

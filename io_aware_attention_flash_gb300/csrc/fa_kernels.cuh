@@ -153,6 +153,7 @@ struct BwdParams {
   const uint16_t* k;
   const uint16_t* v;
   long long ldq, ldk, ldv;
+  unsigned short_blocks;  // blocks of the pre-pass that form d_short
   float* d_short;         // D of the first rows of each sequence, fp32 [nseq, H, kExactRows]
   float* dkv_part;        // grouped heads in several parts: fp32 [2 (dK, dV), splits, rows, Hk, d]
   uint32_t* err;
