@@ -335,19 +335,39 @@ bool stride_ok(long long ld, int heads, int d) {
 }
 
 // Parts that the query heads of a key/value head are split into in the
-// backward: the smallest divisor of the group at which the heaviest CTA (key
-// tile 0 of the longest sequence: all its query tiles, for each head of the
-// part) takes at most half of one SM's share of the whole work, estimated as
-// total / max_seqlen sequences of max_seqlen rows on 152 SMs.  Each part costs
-// an fp32 dK, dV written and read again.
-int grouped_splits(int total, int max_seqlen, int H, int Hk, int causal) {
+// backward.  One part per head balances few long sequences over the SMs, but
+// every CTA costs some five query tiles' time to start and to write out, and
+// the fp32 dK, dV of each part are written and read again (through DRAM beyond
+// what L2 holds of them).  In units of a query tile's time, with the work taken as total / max_seqlen sequences of
+// max_seqlen rows: the launch lasts as long as its longest CTA if all run at
+// once, else the SMs' share of the work plus, measured, three tenths of the
+// longest CTA.  The divisor of the group with the least of that.  Measured, d =
+// 128, 32 heads: one sequence of 1024, Hk = 8: 96 / 63 / 53 us for 1 / 2 / 4
+// parts (4 taken); two of 1000: 107 / 85 / 107 (2); eight of 64 .. 2048: 409 /
+// 448 / 531 (1), with Hk = 4: 461 / 429 / 446 (2); two of 4000, Hk = 8: 695 /
+// 737 / 812 (1).
+int grouped_splits(int total, int max_seqlen, int H, int Hk, int d, int causal) {
+  constexpr double kSms = 152.0, kCtaCost = 5.0, kTail = 0.3, kL2Bytes = 64e6, kBytesPerUs = 6.8e6;
+  const double tile_us = d == 64 ? 1.4 : 2.2;
   const int G = H / Hk;
   const double nt = (max_seqlen + fa::kTile - 1) / fa::kTile;
   const double nseq = total > max_seqlen ? static_cast<double>(total) / max_seqlen : 1.0;
-  const double share = nseq * H * (causal ? nt * (nt + 1) / 2 : nt * nt) / 152.0;
-  int s = 1;
-  while (s < G && (G % s != 0 || G / s * nt > 0.5 * share)) ++s;
-  return s;
+  const double work = nseq * H * (causal ? nt * (nt + 1) / 2 : nt * nt);
+  int best = 1;
+  double best_cost = 0.0;
+  for (int s = 1; s <= G; ++s) {
+    if (G % s != 0) continue;
+    const double longest = G / s * nt + kCtaCost, ctas = nseq * Hk * s * nt;
+    const double share = (work + ctas * kCtaCost) / kSms;
+    const double spilled = s > 1 ? 2.0 * s * total * Hk * d * 8 - kL2Bytes : 0.0;
+    const double cost = (ctas <= kSms ? longest : (share > longest ? share : longest) + kTail * longest) +
+                        (spilled > 0.0 ? spilled / kBytesPerUs / tile_us : 0.0);
+    if (s == 1 || cost < best_cost) {
+      best = s;
+      best_cost = cost;
+    }
+  }
+  return best;
 }
 
 struct GroupedWs {
@@ -357,7 +377,7 @@ struct GroupedWs {
 
 GroupedWs grouped_ws(int nseq, int total, int max_seqlen, int H, int Hk, int d, int causal) {
   GroupedWs w{};
-  w.splits = grouped_splits(total, max_seqlen, H, Hk, causal);
+  w.splits = grouped_splits(total, max_seqlen, H, Hk, d, causal);
   const size_t rows128 = static_cast<size_t>((total + 127LL) / 128) * 128;
   w.short_off = pad256(static_cast<size_t>(total) * H * 4);
   w.dq_off = w.short_off + pad256(static_cast<size_t>(nseq) * H * fa::kExactRows * 4);

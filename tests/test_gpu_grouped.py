@@ -119,7 +119,8 @@ def test_longer_sequences(d):
     check(fa, *make([1000, 1100], 4, 2, d, seed=3), True, 1100)
     check(fa, *make([300] * 40, 4, 2, d, seed=4), False, 300)
     check(fa, *make([300] * 80, 4, 2, d, seed=5), False, 300)
-    sizes = [fa.fa_bwd_grouped_workspace_bytes(n, 300, 300 * n, 4, 2, d, False) / (300 * n) for n in (40, 80)]
+    check(fa, *make([300] * 2, 4, 2, d, seed=6), False, 300)
+    sizes = [fa.fa_bwd_grouped_workspace_bytes(n, 300, 300 * n, 4, 2, d, False) / (300 * n) for n in (2, 80)]
     assert sizes[0] > sizes[1] + 2 * 2 * 2 * d * 4 - 64, "the two calls were meant to split and not to split the group"
 
 
