@@ -246,11 +246,12 @@ FA_API fa_status fa_cache8_store(const void* k, const void* v, void* k_codes, vo
  *            a slot without a sequence (o = 0, lse = -infinity there)
  *   max_seqlen  at least every length
  * causal as in fa_fwd_decode: query i sees keys j <= seqlens[b] − Nq + i.
- * Scores and sums are fp32 (each query and each probability is split into two
- * e4m3 factors, whose product with the codes is exact to about 2^-9 of a
- * probability and 2^-24 of the largest query element).  What cache slots
- * behind a sequence's last token hold does not matter; stored tokens must be
- * finite.  A page index out of range reads as a page of zeros, a length
+ * Scores and sums are fp32; each query and each probability enters its product
+ * with the codes as the sum of two e4m3 terms, off by at most 2^-18 of the
+ * row's largest query element, and by 2^-8 of the probability or 2^-18 of the
+ * largest one among its 128 keys.  What cache slots behind a sequence's last
+ * token hold does not matter; queries and stored tokens must be finite, and
+ * scales powers of two (as fa_cache8_store writes them).  A page index out of range reads as a page of zeros, a length
  * outside [0, min(max_seqlen, table_cols · block)] as the nearer end of that
  * range, and both are reported by fa_get_device_error as FA_ERR_PAGE.  Results
  * do not depend on the order in which CTAs run.  `workspace`: at least
