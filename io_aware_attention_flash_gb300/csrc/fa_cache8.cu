@@ -968,44 +968,84 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
 
 // One warp per (sequence, new token, query head): the partials of an item that
 // several CTAs shared, in the order of its tiles; zeros where no key is cached.
+// The kernel is scheduled while the attention still runs and finds its item's
+// place from the lengths meanwhile (few sequences; else from what CTA 0 of the
+// attention wrote); a lane takes each partial's statistics, and the partials
+// are then read with several loads in flight.
 template <int D>
 __global__ void __launch_bounds__(128) fa_cache8_merge_kernel(const Cache8DecodeParams p, int ctas) {
   constexpr int E = D / 32;
-  grid_dependency_wait();
+  constexpr int kScanSeqs = 512;  // 16 lengths a lane
   const int lane = threadIdx.x & 31;
   const long long wid = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (wid >= static_cast<long long>(p.B) * p.Nq * p.H) return;
-  const int h = static_cast<int>(wid % p.H);
-  const long long qrow = wid / p.H;
+  const bool live = wid < static_cast<long long>(p.B) * p.Nq * p.H;
+  const int h = live ? static_cast<int>(wid % p.H) : 0;
+  const long long qrow = live ? wid / p.H : 0;
   const int i = static_cast<int>(qrow % p.Nq), b = static_cast<int>(qrow / p.Nq);
-  const int total = p.tile_start[p.B];
+  const int per = p.Hk * p.row_groups;
+  int s0 = 0, nt = 0, total = 0;
+  const bool scan = p.B <= kScanSeqs;
+  if (scan) {
+    for (int j = lane; j < p.B; j += 32) {
+      const int n = seq_tiles(p, j);
+      total += n;
+      s0 += j < b ? n : 0;
+    }
+    s0 = __reduce_add_sync(0xffffffffu, s0) * per;
+    total = __reduce_add_sync(0xffffffffu, total) * per;
+    nt = seq_tiles(p, b);
+  }
+  grid_dependency_wait();
+  if (!live) return;
+  if (!scan) {
+    s0 = p.tile_start[b];
+    nt = (p.tile_start[b + 1] - s0) / per;
+    total = p.tile_start[p.B];
+  }
   ctas = min(ctas, total);
-  const int s0 = p.tile_start[b], s1 = p.tile_start[b + 1];
   const int hk = h / p.G, f = i * p.G + h % p.G, rg = f / p.rows, r = f - rg * p.rows;
-  const int nt = (s1 - s0) / (p.Hk * p.row_groups);
   const long long t0 = s0 + static_cast<long long>(hk * p.row_groups + rg) * nt;
   const int c0 = nt ? run_of(t0, total, ctas) : 0, c1 = nt ? run_of(t0 + nt - 1, total, ctas) : -1;
   if (c0 == c1) return;  // written by that CTA
-  float m = -CUDART_INF_F, l = 0.f, acc[E];
+  auto slot = [&](int c) { return (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * p.rows + r; };
+  float mmax = -CUDART_INF_F, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int c = c0; c <= c1; ++c) {
-    const size_t slot = (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * p.rows + r;
-    const float mc = p.ml_part[slot * 2], lc = p.ml_part[slot * 2 + 1];
-    if (mc == -CUDART_INF_F) continue;
-    const float m_new = fmaxf(m, mc);
-    const float a = m == -CUDART_INF_F ? 0.f : ex2_approx(m - m_new), w = ex2_approx(mc - m_new);
-    m = m_new;
-    l = l * a + w * lc;
+  for (int c = c0 + lane; c <= c1; c += 32) mmax = fmaxf(mmax, p.ml_part[slot(c) * 2]);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * p.o_part[slot * D + E * lane + e];
+  for (int off = 16; off > 0; off >>= 1) mmax = fmaxf(mmax, __shfl_xor_sync(0xffffffffu, mmax, off));
+  if (mmax != -CUDART_INF_F) {
+    for (int cb = c0; cb <= c1; cb += 32) {
+      float w = 0.f;  // of partial cb + lane
+      if (cb + lane <= c1) {
+        const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + slot(cb + lane) * 2);
+        w = ml.x == -CUDART_INF_F ? 0.f : ex2_approx(ml.x - mmax);
+        l = fmaf(w, ml.y, l);
+      }
+      const int n = min(32, c1 - cb + 1);
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) {
+        const float wj = __shfl_sync(0xffffffffu, w, j);
+        const float* op = p.o_part + slot(cb + j) * D + E * lane;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(op);
+          acc[0] = fmaf(wj, v.x, acc[0]), acc[1] = fmaf(wj, v.y, acc[1]);
+          acc[2] = fmaf(wj, v.z, acc[2]), acc[3] = fmaf(wj, v.w, acc[3]);
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(op);
+          acc[0] = fmaf(wj, v.x, acc[0]), acc[1] = fmaf(wj, v.y, acc[1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
   }
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint16_t* o = p.o + (qrow * p.H + h) * D + E * lane;
 #pragma unroll
   for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   if (lane == 0)
-    p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = l > 0.f ? (m + log2f(l)) * kLn2 : -CUDART_INF_F;
+    p.lse[(static_cast<size_t>(b) * p.H + h) * p.Nq + i] = l > 0.f ? (mmax + log2f(l)) * kLn2 : -CUDART_INF_F;
 }
 
 template <int D, int RP>
