@@ -411,20 +411,19 @@ fa_status check_cache8(int B, int num_blocks, int table_cols, int Hk, int block,
   return FA_OK;
 }
 
-// Pages [num_blocks, Hk, block, d] of 1-byte codes, one (page, head) a copy,
-// rows swizzled over their d bytes.
+// Pages [num_blocks, Hk, block, d] of 1-byte codes, one (page, head) a copy, as
+// rows of 128 bytes (d = 64: two tokens a row), swizzled.
 fa_status make_map_codes(CUtensorMap* map, const void* ptr, int d, int block, int Hk, int num_blocks) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cuda_fail("cuTensorMapEncodeTiled entry point not found", cudaErrorSymbolNotFound);
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(block), static_cast<cuuint64_t>(Hk),
+  const int rows = block * d / 128;
+  const cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(Hk),
                               static_cast<cuuint64_t>(num_blocks)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(block) * d,
-                                 static_cast<cuuint64_t>(Hk) * block * d};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(block), 1, 1};
+  const cuuint64_t strides[3] = {128, static_cast<cuuint64_t>(block) * d, static_cast<cuuint64_t>(Hk) * block * d};
+  const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(rows), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     snprintf(t_detail, sizeof(t_detail), "cuTensorMapEncodeTiled (cache pages) failed (CUresult %d)",
              static_cast<int>(r));
@@ -433,9 +432,9 @@ fa_status make_map_codes(CUtensorMap* map, const void* ptr, int d, int block, in
   return FA_OK;
 }
 
-// CTAs of the cache attention: as many as 152 SMs hold (fixed, so that the
+// CTAs of the cache attention: two on each of 152 SMs (fixed, so that the
 // workspace does not depend on the device), or one for each possible tile.
-constexpr int kDecode8Sms = 152;
+constexpr int kDecode8Ctas = 304;
 
 fa_status check_decode8(int B, int Nq, int H, int Hk, int num_blocks, int table_cols, int block, int max_seqlen,
                         int d, float scale) {
@@ -456,11 +455,10 @@ struct Decode8Plan {
 
 Decode8Plan decode8_plan(int B, int Nq, int H, int Hk, int max_seqlen, int d) {
   Decode8Plan w{};
-  int per_sm = 0;
-  fa::cache8_plan(d, Nq * (H / Hk), &w.row_groups, &w.rows, &per_sm);
-  const long long tiles =
-      (static_cast<long long>(max_seqlen) + fa::kTile - 1) / fa::kTile * B * Hk * w.row_groups;
-  w.ctas = static_cast<int>(tiles < kDecode8Sms * per_sm ? tiles : kDecode8Sms * per_sm);
+  int tokens = 0;
+  fa::cache8_plan(d, Nq * (H / Hk), &w.row_groups, &w.rows, &tokens);
+  const long long tiles = (static_cast<long long>(max_seqlen) + tokens - 1) / tokens * B * Hk * w.row_groups;
+  w.ctas = static_cast<int>(tiles < kDecode8Ctas ? tiles : kDecode8Ctas);
   const size_t parts = static_cast<size_t>(2) * w.ctas * w.rows;
   w.ml_off = pad256(parts * d * 4);
   w.start_off = w.ml_off + pad256(parts * 2 * 4);

@@ -236,10 +236,14 @@ cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
 // One or two warpgroups (thread r: key r for scores and P, head dimension r for
 // O; two share the rows from 8 on, as a tile's time is the length of one warp's
 // instruction chain), a warp that loads (lane i: page i of the tile, its TMA
-// copies and its two scales) and one that issues the MMAs.  d = 64: A needs 128 rows, so V is read as two blocks of
-// 64 dimensions, keys 0-63 and 64-127 of the tile, each against P's own half
-// of the keys as columns of their own: thread r keeps dimension r mod 64 of
-// half r / 64, and the halves are added once for each item.
+// copies and its two scales) and one that issues the MMAs.
+//
+// d = 64: a tile's 128 rows of 128 bytes hold two tokens each, 256 in all, so
+// that a tile, its copies and its fixed costs are those of d = 128.  S^T is two
+// products, of the rows' first and second 64 bytes; in V^T P^T the rows' 128
+// bytes are M, so P's columns come once for the first tokens (read in lanes
+// 0-63) and once for the second ones (lanes 64-127), and the two O are added
+// once for each item.
 constexpr int kRowsMax = 16;
 
 __device__ __forceinline__ int run_start(long long c, int total, int ctas) { return static_cast<int>(c * total / ctas); }
@@ -255,11 +259,17 @@ __device__ __forceinline__ int cached_len(const Cache8DecodeParams& p, int b) {
   const int n = __ldg(p.seqlens + b);
   return static_cast<int>(min(max(static_cast<long long>(n), 0LL), cap));
 }
+// Tokens of a tile: 128 rows of 128 bytes.
+template <int D>
+constexpr int kTokens = kTile * 128 / D;
+
+template <int D>
 __device__ __forceinline__ int seq_tiles(const Cache8DecodeParams& p, int b) {
-  return (cached_len(p, b) + kTile - 1) / kTile;
+  return (cached_len(p, b) + kTokens<D> - 1) / kTokens<D>;
 }
 
 // A CTA's walk through its run: the tiles [k0, k1) of one item after another.
+template <int D>
 struct Walk {
   int t, t_hi, b, seq0;              // next tile, end of the run, sequence and its first tile
   int hk, rg, nt, k0, k1, len;
@@ -272,7 +282,7 @@ struct Walk {
     auto read = [&]() {
       len = cached_len(p, b);
       if (WARP) len = __shfl_sync(0xffffffffu, len, 0);
-      nt = (len + kTile - 1) / kTile;
+      nt = (len + kTokens<D> - 1) / kTokens<D>;
     };
     read();
     while (t >= seq0 + nt * per) {
@@ -348,40 +358,37 @@ struct Dec8Cfg {
   static constexpr int NCW = 4 * WG;                         // compute warps; then the TMA and the MMA warp
   static constexpr int NUM_WARPS = NCW + 2;
   static constexpr int NUM_THREADS = 32 * NUM_WARPS;
-  static constexpr int TILE_BYTES = kTile * D;               // 128 keys
-  // CTAs on an SM.  A tile's chain of waits and short steps takes some 1350
-  // cycles; at d = 64 a tile is 16 KB, which the memory delivers to an SM in
-  // less than half of that, so four small CTAs overlap (8 rows and more: two,
-  // by their registers).
-  static constexpr int CTAS = D == 64 && RP <= 4 ? 4 : 2;
-  static constexpr int NST = D == 128 || CTAS == 4 ? 3 : 5;  // ring stages (K and V tile each)
+  static constexpr int NP = 128 / D;                         // tokens of a tile's row
+  static constexpr int TILE_BYTES = kTile * 128;
+  static constexpr int NST = D == 64 && RP == 16 ? 2 : 3;    // ring stages (K and V tile each)
   static constexpr int NS = 2 * RP < 16 ? 16 : 2 * RP;       // columns of S: a warpgroup's rows' hi, then lo terms
-  static constexpr int HALVES = 128 / D;
-  static constexpr int NO = 2 * RP * HALVES < 16 ? 16 : 2 * RP * HALVES;
+  static constexpr int NO = 2 * RP * NP < 16 ? 16 : 2 * RP * NP;
   static constexpr int Q_BYTES = NS * D;
-  static constexpr int P_BYTES = NO * (kTile / HALVES);
+  static constexpr int P_BYTES = NO * kTile;
+  static constexpr int MAX_PPT = 8 * NP;                     // pages of a tile, at most
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
   static constexpr int OFF_Q = OFF_V + NST * TILE_BYTES;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_SC = OFF_P + 2 * P_BYTES;         // (two P buffers) [NST][8 pages][4]: K's scale, 1 / V's, its log2
-  static constexpr int OFF_QS = OFF_SC + NST * 8 * 16;    // [RP] score factor of each row
+  static constexpr int OFF_HALF = OFF_P;                     // between items: [RP][64] O of the second tokens (d = 64)
+  static constexpr int OFF_SC = OFF_P + 2 * P_BYTES;         // (two P buffers) [NST][pages][4]: K's scale, 1 / V's, its log2
+  static constexpr int OFF_QS = OFF_SC + NST * MAX_PPT * 16;    // [RP] score factor of each row
   static constexpr int OFF_XCH = OFF_QS + kRowsMax * 4;      // [2][4 warps][RP]
   static constexpr int STAT_WARP = 3 * RW < 4 ? 4 : 3 * RW;  // reference, alpha, weight of each row
   static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [2 tiles][NCW][STAT_WARP]
-  static constexpr int OFF_HALF = OFF_STAT + 2 * NCW * STAT_WARP * 4;  // [RP][64] O of the second half (d = 64)
-  static constexpr int OFF_SCAN = OFF_HALF + (D == 64 ? RP * 64 * 4 : 0);  // [2] first sequence, its tile; [warps] sums
+  static constexpr int OFF_SCAN = OFF_STAT + 2 * NCW * STAT_WARP * 4;  // [2] first sequence, its tile; [warps] sums
   static constexpr int OFF_BAR = (OFF_SCAN + (2 + NUM_WARPS) * 4 + 7) / 8 * 8;
   static constexpr int B_FULL = 0, B_EMPTY = NST, B_SFULL = 2 * NST, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 1,
                        B_XCH = B_PVDONE + 2, B_QREADY = B_XCH + 2, B_DRAIN = B_QREADY + 1, NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;    // slack to align the base to 1024
-  static constexpr uint32_t COLS = 2 * NS + 2 * NO;
+  static constexpr uint32_t COLS = 2 * NP * NS + 2 * NO;
   static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
-  static constexpr uint32_t O_COL = 2 * NS;
-  static_assert(CTAS * TMEM_COLS <= 512, "tensor memory for the CTAs of an SM");
-  static_assert(CTAS * (SMEM_BYTES + 1024) <= 233472, "shared memory for the CTAs of an SM");
-  static_assert(OFF_Q % 1024 == 0 && OFF_P % 512 == 0 && (D == 64 || OFF_P % 1024 == 0), "swizzle atoms");
+  static constexpr uint32_t O_COL = 2 * NP * NS;
+  static_assert(2 * TMEM_COLS <= 512, "tensor memory for two CTAs on an SM");
+  static_assert(2 * (SMEM_BYTES + 1024) <= 233472, "shared memory for two CTAs on an SM");
+  static_assert(OFF_Q % 1024 == 0 && OFF_P % 512 == 0, "swizzle atoms");
+  static_assert(D == 128 || RP * 64 * 4 <= 2 * P_BYTES, "O of the second tokens fits over P");
 };
 
 // Byte `byte` of row `row` in a tile of W-byte rows swizzled over W bytes (the
@@ -452,7 +459,7 @@ __device__ __forceinline__ void each_pair(F2 two, F1 one) {
 }
 
 template <int D, int RP>
-__global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::CTAS)
+__global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     fa_cache8_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const Cache8DecodeParams p) {
   using C = Dec8Cfg<D, RP>;
@@ -471,7 +478,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
   // ---- this CTA's place: all tiles counted, then the sequence of its first one
   const int per = p.Hk * p.row_groups;
   int mine = 0;
-  for (int b = threadIdx.x; b < p.B; b += C::NUM_THREADS) mine += seq_tiles(p, b);
+  for (int b = threadIdx.x; b < p.B; b += C::NUM_THREADS) mine += seq_tiles<D>(p, b);
   mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) scan[2 + warp] = mine;
   if (warp == C::NCW && lane == 0) {
@@ -499,14 +506,14 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
   const int ctas = min(static_cast<int>(gridDim.x), total);  // every one of them has a tile
   const bool idle = static_cast<int>(blockIdx.x) >= ctas;
   if (idle && blockIdx.x != 0) return;
-  Walk w{};
+  Walk<D> w{};
   w.t = idle ? 0 : run_start(blockIdx.x, total, ctas);
   w.t_hi = idle ? 0 : run_start(blockIdx.x + 1LL, total, ctas);
   if (warp == 0) {  // CTA 0 writes down every sequence's first tile for the merge
     int base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int b = b0 + lane;
-      const int n = b < p.B ? seq_tiles(p, b) * per : 0;
+      const int n = b < p.B ? seq_tiles<D>(p, b) * per : 0;
       int sum = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -551,14 +558,14 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
     // lane.  A unit's table entries are read two units ahead and its scales
     // one unit ahead, so that the copies wait for neither (read where they
     // were used, the two dependent loads took about 2 us a tile).
-    const int ppt = kTile / p.block;  // pages of a tile
+    const int ppt = kTokens<D> >> p.block_shift;  // pages of a tile
     struct Unit {
       int kt0, tiles, len, hk, page;  // first tile, tiles; page of this lane (num_blocks: none, reads as zeros)
       float ks, vs;
     };
     int left = 0;  // tiles of the current item not yet in a unit
     auto next_unit = [&](Unit& u) {
-      if (left == 0) left = w.next<true>(p) ? w.k1 - w.k0 : 0;
+      if (left == 0) left = w.template next<true>(p) ? w.k1 - w.k0 : 0;
       u.kt0 = w.k1 - left;
       u.tiles = min(left, 32 / ppt);
       u.len = w.len;
@@ -588,7 +595,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
     while (ok && cur.tiles > 0) {
       for (int i = 0; i < cur.tiles; ++i, ++t) {
         const int st = t % C::NST, kt = cur.kt0 + i;
-        const int n_pages = min(ppt, (cur.len - kt * kTile + p.block - 1) / p.block);
+        const int n_pages = min(ppt, (cur.len - kt * kTokens<D> + p.block - 1) >> p.block_shift);
         const int from = i * ppt + lane;  // this lane's page of the tile
         const int page = __shfl_sync(0xffffffffu, cur.page, from & 31);
         if (t >= C::NST) ok = wait_bounded(bar(C::B_EMPTY + st), ((t / C::NST) - 1) & 1, abort_flag, p.err, p.timeout_ns);
@@ -609,7 +616,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
         if (lane < ppt) {
           // V's scale by its exponent, a power of two; 1 for a page of zeros and for none
           const int ve = vs > 0.f ? static_cast<int>(__float_as_uint(vs) >> 23) - 127 : 0;
-          reinterpret_cast<float4*>(smem + C::OFF_SC)[st * 8 + lane] =
+          reinterpret_cast<float4*>(smem + C::OFF_SC)[st * C::MAX_PPT + lane] =
               lane < n_pages ? make_float4(ks, exp2_int(-ve), static_cast<float>(ve), 0.f) : make_float4(0.f, 1.f, 0.f, 0.f);
         }
         mbar_arrive(bar(C::B_FULL + st));
@@ -626,9 +633,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
     // ---------------------------------------------------------------- MMA
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_e4m3(128, C::NS, false), idesc_o = idesc_e4m3(128, C::NO, true);
-      constexpr int KW = kTile / C::HALVES;  // P row in bytes: keys of a half
-      const uint64_t dK0 = sdesc8<D>(sb + C::OFF_K, 16);
-      const uint64_t dV0 = sdesc8<D>(sb + C::OFF_V, 64 * D);  // MN-major; second block of 64 dimensions (d = 64): keys 64..
+      const uint64_t dK0 = sdesc8<128>(sb + C::OFF_K, 16);
+      const uint64_t dV0 = sdesc8<128>(sb + C::OFF_V, 16);  // MN-major: the rows' 128 bytes are M
       const uint64_t dQ = sdesc8<D>(sb + C::OFF_Q, 16);
       const uint64_t dP = sdesc8<C::NO>(sb + C::OFF_P, 16);  // MN-major: a key's columns are a row
       auto issue_s = [&](int u) -> bool {
@@ -636,15 +642,17 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
         if (!wait_bounded(bar(C::B_FULL + st), (u / C::NST) & 1, abort_flag, p.err, p.timeout_ns)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < D / 32; ++kk)
-          mma_e4m3(tmem + C::NS * (u & 1), sdesc_add(dK0, st * C::TILE_BYTES + kk * 32), sdesc_add(dQ, kk * 32), idesc_s,
-                   kk > 0);
+        for (int pos = 0; pos < C::NP; ++pos)  // d = 64: the rows' first tokens, then their second ones
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_e4m3(tmem + C::NS * (C::NP * (u & 1) + pos), sdesc_add(dK0, st * C::TILE_BYTES + pos * D + kk * 32),
+                     sdesc_add(dQ, kk * 32), idesc_s, kk > 0);
         tc_commit(bar(C::B_SFULL + (u & 1)));
         return true;
       };
       int t = 0, n_item = 0;
       bool ok = true;
-      for (; ok && w.next<false>(p); ++n_item) {
+      for (; ok && w.template next<false>(p); ++n_item) {
         ok = wait_bounded(bar(C::B_QREADY), n_item & 1, abort_flag, p.err, p.timeout_ns) && issue_s(t);
         for (int kt = w.k0; ok && kt < w.k1; ++kt, ++t) {
           // the next tile's scores run while this tile's P is formed (across
@@ -655,8 +663,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
           tc_fence_after();
           const int st = t % C::NST;
 #pragma unroll
-          for (int kk = 0; kk < KW / 32; ++kk)
-            mma_e4m3(tmem + C::O_COL + C::NO * (t & 1), sdesc_add(dV0, st * C::TILE_BYTES + kk * 32 * D),
+          for (int kk = 0; kk < kTile / 32; ++kk)
+            mma_e4m3(tmem + C::O_COL + C::NO * (t & 1), sdesc_add(dV0, st * C::TILE_BYTES + kk * 32 * 128),
                      sdesc_add(dP, (t & 1) * C::P_BYTES + kk * 32 * C::NO), idesc_o, kk > 0);
           tc_commit(bar(C::B_PVDONE + (t & 1)));
           tc_commit(bar(C::B_EMPTY + st));
@@ -670,14 +678,14 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
     constexpr int RW = C::RW;
     const int wg = C::WG == 2 ? warp >> 2 : 0, quarter = warp & 3;
     const int row0 = wg * RW;            // first of this warpgroup's rows
-    const int r = quarter * 32 + lane;   // TMEM lane: key of the tile; head dimension (and half) of O
+    const int r = quarter * 32 + lane;   // TMEM lane: row of the tile (its tokens); head dimension of O (and which token)
     const int half = r / D;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     float* xch = reinterpret_cast<float*>(smem + C::OFF_XCH);
     float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
     float* stats = reinterpret_cast<float*>(smem + C::OFF_STAT) + warp * C::STAT_WARP;
     const int xbar = C::B_XCH + wg;
-    constexpr int KW = kTile / C::HALVES;
+    constexpr int NP = C::NP, TOK = kTokens<D>;
     constexpr int LPR = 32 / RW;  // lanes that keep one row's statistics
     const int my_row = lane / LPR;  // within the warpgroup's rows
     int t = 0, nx = 0, n_item = 0;
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
     auto wait = [&](int i, uint32_t ph) {
       ok = ok && wait_bounded(bar(i), ph, abort_flag, p.err, p.timeout_ns);
     };
-    for (; __all_sync(0xffffffffu, ok) && w.next<true>(p); ++n_item) {
+    for (; __all_sync(0xffffffffu, ok) && w.template next<true>(p); ++n_item) {
       const int rows = min(p.rows, p.Nq * p.G - w.rg * p.rows);
       // Row row0 + my_row: its row of q and o, its place in lse, and how many of
       // the last keys it does not see.
@@ -788,29 +796,39 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
         tc_fence_before();
       };
       // tiles of which some row does not see all keys: from this one on
-      const int kt_mask = max(0, w.len - (p.causal ? p.Nq - 1 : 0)) / kTile;
+      const int kt_mask = max(0, w.len - (p.causal ? p.Nq - 1 : 0)) / TOK;
       for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
         wait(C::B_FULL + st, st_phase);
-        // K's scale, 1 / V's scale and its log2 for this thread's key
-        const float4 sc = reinterpret_cast<const float4*>(smem + C::OFF_SC)[st * 8 + (r >> p.block_shift)];
+        // K's scale, 1 / V's scale and its log2 of the page of this thread's tokens
+        const float4 sc = reinterpret_cast<const float4*>(smem + C::OFF_SC)[st * C::MAX_PPT + ((NP * r) >> p.block_shift)];
         const float ks = sc.x, inv_vs = sc.y, vef = sc.z;
         wait(C::B_SFULL + (t & 1), (t >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        uint32_t sv[NL];
-        tmem_cols(lane_addr + C::NS * (t & 1) + 2 * row0, sv);
-        float y[RW];
-        each_pair<RW>(
-            [&](int q) {
-              const uint64_t s = fadd2(f2_pack(__uint_as_float(sv[q]), __uint_as_float(sv[q + 1])),
-                                       f2_pack(__uint_as_float(sv[RW + q]), __uint_as_float(sv[RW + q + 1])));
-              f2_unpack(ffma2(s, fmul2(f2_pack(ks, ks), f2_pack(qf[q], qf[q + 1])), f2_pack(vef, vef)), y[q], y[q + 1]);
-            },
-            [&](int q) { y[q] = fmaf(__uint_as_float(sv[q]) + __uint_as_float(sv[RW + q]), ks * qf[q], vef); });
+        float y[NP][RW];
+#pragma unroll
+        for (int pos = 0; pos < NP; ++pos) {
+          uint32_t sv[NL];
+          tmem_cols(lane_addr + C::NS * (NP * (t & 1) + pos) + 2 * row0, sv);
+          each_pair<RW>(
+              [&](int q) {
+                const uint64_t s = fadd2(f2_pack(__uint_as_float(sv[q]), __uint_as_float(sv[q + 1])),
+                                         f2_pack(__uint_as_float(sv[RW + q]), __uint_as_float(sv[RW + q + 1])));
+                f2_unpack(ffma2(s, fmul2(f2_pack(ks, ks), f2_pack(qf[q], qf[q + 1])), f2_pack(vef, vef)), y[pos][q],
+                          y[pos][q + 1]);
+              },
+              [&](int q) {
+                y[pos][q] = fmaf(__uint_as_float(sv[q]) + __uint_as_float(sv[RW + q]), ks * qf[q], vef);
+              });
+        }
         if (kt >= kt_mask) {
 #pragma unroll
-          for (int q = 0; q < RW; ++q)
-            if (kt * kTile + r >= w.len - __shfl_sync(0xffffffffu, row_hidden, q * LPR)) y[q] = -CUDART_INF_F;
+          for (int q = 0; q < RW; ++q) {
+            const int end = w.len - __shfl_sync(0xffffffffu, row_hidden, q * LPR) - (kt * TOK + NP * r);
+#pragma unroll
+            for (int pos = 0; pos < NP; ++pos)
+              if (pos >= end) y[pos][q] = -CUDART_INF_F;
+          }
         }
         // ---- the tile's largest y of each row: over the warp, then over the
         // four warps; lane q does the rest of row q's statistics and leaves
@@ -819,7 +837,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
         {
           float wm[RW];
 #pragma unroll
-          for (int q = 0; q < RW; ++q) wm[q] = warp_max(y[q]);
+          for (int q = 0; q < RW; ++q) wm[q] = warp_max(NP == 2 ? fmaxf(y[0][q], y[NP - 1][q]) : y[0][q]);
           if (lane == 0) store_row<RW>(slot + quarter * kRowsMax, wm);
         }
         mbar_arrive(bar(xbar));
@@ -844,54 +862,60 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
           load_row<RW>(stat, ref);
           load_row<RW>(stat + RW, alpha);
           load_row<RW>(stat + 2 * RW, wt);
-          uint32_t hi[(RW + 3) / 4], lo[(RW + 3) / 4];
-          // P = 2^(y - reference), at most 256, and its share of l
-          each_pair<RW>(
-              [&](int q) {
-                f2_unpack(fsub2(f2_pack(y[q], y[q + 1]), f2_pack(ref[q], ref[q + 1])), y[q], y[q + 1]);
-                y[q] = ex2_approx(y[q]);
-                y[q + 1] = ex2_approx(y[q + 1]);
-                const uint64_t c = fmul2(f2_pack(inv_vs, inv_vs), f2_pack(wt[q], wt[q + 1]));
-                f2_unpack(ffma2(f2_pack(y[q], y[q + 1]), c,
-                                fmul2(f2_pack(lsum[q], lsum[q + 1]), f2_pack(alpha[q], alpha[q + 1]))),
-                          lsum[q], lsum[q + 1]);
-              },
-              [&](int q) {
-                y[q] = ex2_approx(y[q] - ref[q]);
-                lsum[q] = fmaf(y[q], inv_vs * wt[q], lsum[q] * alpha[q]);
-              });
-          if constexpr (RW % 4 == 0) {
 #pragma unroll
-            for (int q = 0; q < RW; q += 4) {
-              float h[4], e[4];
-              hi[q / 4] = pack_e4m3x4(y[q], y[q + 1], y[q + 2], y[q + 3]);
-              unpack_e4m3x4(hi[q / 4], h);
-              f2_unpack(fsub2(f2_pack(y[q], y[q + 1]), f2_pack(h[0], h[1])), e[0], e[1]);
-              f2_unpack(fsub2(f2_pack(y[q + 2], y[q + 3]), f2_pack(h[2], h[3])), e[2], e[3]);
-              lo[q / 4] = pack_e4m3x4(e[0], e[1], e[2], e[3]);
+          for (int q = 0; q < RW; ++q) lsum[q] *= alpha[q];
+#pragma unroll
+          for (int pos = 0; pos < NP; ++pos) {
+            uint32_t hi[(RW + 3) / 4], lo[(RW + 3) / 4];
+            float(&x)[RW] = y[pos];
+            // P = 2^(y - reference), at most 256, and its share of l
+            each_pair<RW>(
+                [&](int q) {
+                  f2_unpack(fsub2(f2_pack(x[q], x[q + 1]), f2_pack(ref[q], ref[q + 1])), x[q], x[q + 1]);
+                  x[q] = ex2_approx(x[q]);
+                  x[q + 1] = ex2_approx(x[q + 1]);
+                  const uint64_t c = fmul2(f2_pack(inv_vs, inv_vs), f2_pack(wt[q], wt[q + 1]));
+                  f2_unpack(ffma2(f2_pack(x[q], x[q + 1]), c, f2_pack(lsum[q], lsum[q + 1])), lsum[q], lsum[q + 1]);
+                },
+                [&](int q) {
+                  x[q] = ex2_approx(x[q] - ref[q]);
+                  lsum[q] = fmaf(x[q], inv_vs * wt[q], lsum[q]);
+                });
+            if constexpr (RW % 4 == 0) {
+#pragma unroll
+              for (int q = 0; q < RW; q += 4) {
+                float h[4], e[4];
+                hi[q / 4] = pack_e4m3x4(x[q], x[q + 1], x[q + 2], x[q + 3]);
+                unpack_e4m3x4(hi[q / 4], h);
+                f2_unpack(fsub2(f2_pack(x[q], x[q + 1]), f2_pack(h[0], h[1])), e[0], e[1]);
+                f2_unpack(fsub2(f2_pack(x[q + 2], x[q + 3]), f2_pack(h[2], h[3])), e[2], e[3]);
+                lo[q / 4] = pack_e4m3x4(e[0], e[1], e[2], e[3]);
+              }
+            } else {
+              float h, unused;
+              hi[0] = pack_e4m3x2(x[0], 0.f);
+              unpack_e4m3x2(hi[0], h, unused);
+              lo[0] = pack_e4m3x2(x[0] - h, 0.f);
             }
-          } else {
-            float h, unused;
-            hi[0] = pack_e4m3x2(y[0], 0.f);
-            unpack_e4m3x2(hi[0], h, unused);
-            lo[0] = pack_e4m3x2(y[0] - h, 0.f);
+            // the token's columns: a warpgroup's rows' hi terms, then their lo
+            // terms (d = 64: of the rows' second tokens behind the first ones')
+            uint8_t* at = smem + C::OFF_P + (t & 1) * C::P_BYTES + swz<C::NO>(r, 2 * RP * pos + 2 * row0);
+            static_assert(RW == 8 || RW == 4 || RW == 1, "row counts that the P layout has");
+            if constexpr (RW == 8)
+              *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
+            else if constexpr (RW == 4)
+              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], lo[0]);
+            else
+              *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>((hi[0] & 0xffu) | (lo[0] << 8));
           }
-          // the key's columns (d = 64: of its half of the keys): a warpgroup's
-          // rows' hi terms, then their lo terms
-          uint8_t* at = smem + C::OFF_P + (t & 1) * C::P_BYTES + swz<C::NO>(r % KW, 2 * RP * half + 2 * row0);
-          static_assert(RW == 8 || RW == 4 || RW == 1, "row counts that the P layout has");
-          if constexpr (RW == 8)
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-          else if constexpr (RW == 4)
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], lo[0]);
-          else
-            *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>((hi[0] & 0xffu) | (lo[0] << 8));
         }
         // slots without a token may hold NaN, and 0 · NaN is not 0
-        if (wg == 0 && kt >= kt_mask && kt * kTile + r >= w.len) {
-          uint4* vrow = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::TILE_BYTES + r * D);
+        if (wg == 0 && kt >= kt_mask) {
+          const int held = w.len - (kt * TOK + NP * r);  // tokens of this row
+          uint4* vrow = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::TILE_BYTES + r * 128);
 #pragma unroll
-          for (int u = 0; u < D / 16; ++u) vrow[u] = make_uint4(0u, 0u, 0u, 0u);
+          for (int u = 0; u < 8; ++u)  // 16-byte chunks, swizzled
+            if (u * 16 / D >= held) vrow[u ^ (r & 7)] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -951,11 +975,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, Dec8Cfg<D, RP>::C
         }
       }
       __syncwarp();
-      if (D == 64) {  // the second half's buffer has been read
-        mbar_arrive(bar(xbar));
-        wait(xbar, nx & 1);
-        ++nx;
-      }
+      // (what the next item writes over, it writes after all have arrived on
+      // its B_QREADY)
     }
   }
   tc_fence_before();
@@ -987,13 +1008,13 @@ __global__ void __launch_bounds__(128) fa_cache8_merge_kernel(const Cache8Decode
   const bool scan = p.B <= kScanSeqs;
   if (scan) {
     for (int j = lane; j < p.B; j += 32) {
-      const int n = seq_tiles(p, j);
+      const int n = seq_tiles<D>(p, j);
       total += n;
       s0 += j < b ? n : 0;
     }
     s0 = __reduce_add_sync(0xffffffffu, s0) * per;
     total = __reduce_add_sync(0xffffffffu, total) * per;
-    nt = seq_tiles(p, b);
+    nt = seq_tiles<D>(p, b);
   }
   grid_dependency_wait();
   if (!live) return;
@@ -1073,10 +1094,10 @@ cudaError_t launch_decode8_rows(const CUtensorMap& tk, const CUtensorMap& tv, co
 
 }  // namespace
 
-void cache8_plan(int d, int rows_total, int* groups, int* rows, int* ctas_per_sm) {
+void cache8_plan(int d, int rows_total, int* groups, int* rows, int* tokens) {
   *groups = (rows_total + kRowsMax - 1) / kRowsMax;
   *rows = (rows_total + *groups - 1) / *groups;
-  *ctas_per_sm = d == 64 && *rows <= 4 ? Dec8Cfg<64, 4>::CTAS : Dec8Cfg<128, 16>::CTAS;
+  *tokens = d == 64 ? kTokens<64> : kTokens<128>;
 }
 
 cudaError_t launch_cache8_store(int d, int block, const Cache8StoreParams& p, cudaStream_t s) {

@@ -302,8 +302,8 @@ cudaError_t launch_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv, c
                           cudaStream_t s);
 cudaError_t launch_cache8_store(int d, int block, const Cache8StoreParams& p, cudaStream_t s);
 // Row groups that the rows_total (new token, query head) rows over one
-// key/value head are split into, the rows of each, and the CTAs an SM holds.
-void cache8_plan(int d, int rows_total, int* groups, int* rows, int* ctas_per_sm);
+// key/value head are split into, the rows of each, and the tokens of a tile.
+void cache8_plan(int d, int rows_total, int* groups, int* rows, int* tokens);
 cudaError_t launch_cache8_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv, const Cache8DecodeParams& p,
                                  int ctas, cudaStream_t s);
 cudaError_t launch_wait_timeout_selftest(uint32_t* err, uint64_t limit_ns, cudaStream_t s);
