@@ -134,6 +134,9 @@ __device__ __forceinline__ void short_rows(const BwdParams& p, long long tid) {
 
 template <int D, bool GRP = false>
 __global__ void __launch_bounds__(256, GRP ? 6 : 1) fa_bwd_pre_kernel(const BwdParams p) {
+  // Grouped: scheduled while the kernel before finishes.  The main kernel loads
+  // Q, K, V and dO without waiting for this one, so it may start only after.
+  if (GRP) grid_dependency_wait();
   grid_launch_dependents();  // the main kernel's prologue and first MMAs need nothing from here
   constexpr int TPR = D / 8;  // threads per (row, head); rows do not straddle warps (TPR divides 32)
   static_assert(32 % TPR == 0, "a (row, head) lies within one warp");
@@ -404,7 +407,12 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
   const int lane = threadIdx.x & 31;
   int pair, j;                        // j: key tile; heavy (small j) tiles first under a causal mask
   cta_item(p.sv, pair, j);
-  if (pair >= p.sv.npairs) return;
+  // A grouped grid of which no CTA has work must not finish before the pre-pass
+  // either: what follows in the stream waits for this kernel alone.
+  if (pair >= p.sv.npairs) {
+    if (GRP) grid_dependency_wait();
+    return;
+  }
   SeqPos sp;
   int hk, part = 0, nh = 1;           // key/value head; part of its query heads and how many those are
   if constexpr (GRP) {
@@ -420,7 +428,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
     hk = sp.h;
   }
   const int kv0 = j * kTile;
-  if (kv0 >= sp.seqlen) return;
+  if (kv0 >= sp.seqlen) {
+    if (GRP) grid_dependency_wait();
+    return;
+  }
   const int nq_total = (sp.seqlen + kTile - 1) / kTile;
   const int i_first = p.causal ? j : 0;
   const int nq_h = nq_total - i_first;  // query tiles of one head
@@ -1123,8 +1134,12 @@ cudaError_t launch_bwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
     if (pre_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     pp.short_blocks = static_cast<unsigned>(n);
   }
-  fa_bwd_pre_kernel<D, GRP><<<static_cast<unsigned>(pre_blocks), 256, 0, s>>>(pp);
-  e = cudaGetLastError();
+  if (GRP) {
+    e = launch_kernel(fa_bwd_pre_kernel<D, GRP>, dim3(static_cast<unsigned>(pre_blocks)), dim3(256), 0, s, true, pp);
+  } else {
+    fa_bwd_pre_kernel<D, GRP><<<static_cast<unsigned>(pre_blocks), 256, 0, s>>>(pp);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return e;
   if (ev0 && (e = cudaEventRecord(ev0, s)) != cudaSuccess) return e;
   // The main kernel starts while the pre-pass finishes, and the conversion

@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) fa_cache8_store_kernel(const Ca
   const int which = blockIdx.y * GPB + group;
   const bool is_v = which >= p.Hk;
   const int head = is_v ? which - p.Hk : which;
+  grid_dependency_wait();  // scheduled while the kernel before it in the stream finishes
   int page = -1, old = 0, lo = 0, hi = 0;  // the page; its tokens [0, old) are held, [lo, hi) are new
   int src = 0;                             // input row of slot 0
   if (which < 2 * p.Hk) {
@@ -202,8 +203,7 @@ cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
   const long long x = static_cast<long long>(p.B) * p.blocks, y = (2LL * p.Hk * TG + NT - 1) / NT;
   if (x > 0x7fffffffLL || y > 65535) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(x), static_cast<unsigned>(y));
-  fa_cache8_store_kernel<CHUNKS / TG, TG, D, BLOCK, NT><<<grid, NT, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(fa_cache8_store_kernel<CHUNKS / TG, TG, D, BLOCK, NT>, grid, dim3(NT), 0, s, true, p);
 }
 
 // ----------------------------------------------------------------------------
@@ -463,7 +463,6 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     fa_cache8_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                             const Cache8DecodeParams p) {
   using C = Dec8Cfg<D, RP>;
-  grid_launch_dependents();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
@@ -475,12 +474,6 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
   int* scan = reinterpret_cast<int*>(smem + C::OFF_SCAN);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  // ---- this CTA's place: all tiles counted, then the sequence of its first one
-  const int per = p.Hk * p.row_groups;
-  int mine = 0;
-  for (int b = threadIdx.x; b < p.B; b += C::NUM_THREADS) mine += seq_tiles<D>(p, b);
-  mine = __reduce_add_sync(0xffffffffu, mine);
-  if (lane == 0) scan[2 + warp] = mine;
   if (warp == C::NCW && lane == 0) {
     for (int s = 0; s < C::NST; ++s) {
       mbar_init(bar(C::B_FULL + s), 32);
@@ -497,6 +490,17 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  // The kernel may start while the one before it in the stream finishes: what
+  // that one wrote is read from here on, and only now may the merge start,
+  // which reads the lengths.
+  grid_dependency_wait();
+  grid_launch_dependents();
+  // ---- this CTA's place: all tiles counted, then the sequence of its first one
+  const int per = p.Hk * p.row_groups;
+  int mine = 0;
+  for (int b = threadIdx.x; b < p.B; b += C::NUM_THREADS) mine += seq_tiles<D>(p, b);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if (lane == 0) scan[2 + warp] = mine;
   __syncthreads();
   int total = 0;
 #pragma unroll
@@ -1076,8 +1080,9 @@ cudaError_t launch_decode8(const CUtensorMap& tk, const CUtensorMap& tv, const C
   static SmemLimit smem_limit;
   cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_cache8_decode_kernel<D, RP>), C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  fa_cache8_decode_kernel<D, RP><<<ctas, C::NUM_THREADS, C::SMEM_BYTES, s>>>(tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_kernel(fa_cache8_decode_kernel<D, RP>, dim3(static_cast<unsigned>(ctas)), dim3(C::NUM_THREADS),
+                    C::SMEM_BYTES, s, true, tk, tv, p);
+  if (e != cudaSuccess) return e;
   const long long warps = static_cast<long long>(p.B) * p.Nq * p.H;
   return launch_kernel(fa_cache8_merge_kernel<D>, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, s, true, p,
                        ctas);

@@ -125,6 +125,9 @@ __global__ void __launch_bounds__(FwdCfg<D, NQT_>::NUM_THREADS, FwdCfg<D, NQT_>:
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  // Grouped: the kernel may be scheduled while the one before it in the stream
+  // finishes; nothing that one wrote is read before this.
+  if (GRP) grid_dependency_wait();
   int pair, tile;
   cta_item(p.sv, pair, tile);
   if (pair >= p.sv.npairs) {
@@ -568,6 +571,9 @@ cudaError_t launch_fwd_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUt
   pl.sv.pair_group = pair_group_size(pl.sv.npairs, pl.sv.ntiles, sms * C::MIN_BLOCKS);
   const long long ctas = grid_ctas(pl.sv.npairs, pl.sv.ntiles, pl.sv.pair_group);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (GRP)
+    return launch_kernel(fa_fwd_kernel<D, NQT, GRP, HP>, dim3(static_cast<unsigned>(ctas)), dim3(C::NUM_THREADS),
+                         C::SMEM_BYTES, s, true, tq, tk, tv, to, pl);
   fa_fwd_kernel<D, NQT, GRP, HP><<<static_cast<unsigned>(ctas), C::NUM_THREADS, C::SMEM_BYTES, s>>>(tq, tk, tv, to, pl);
   return cudaGetLastError();
 }

@@ -124,6 +124,24 @@ def test_longer_sequences(d):
     assert sizes[0] > sizes[1] + 2 * 2 * 2 * d * 4 - 64, "the two calls were meant to split and not to split the group"
 
 
+def test_only_empty_sequences():
+    """No row belongs to a sequence: zeros, -infinity, and nothing left running
+    that later calls on the same memory would meet."""
+    fa = require_gpu()
+    for d in (64, 128):
+        _, q, k, v, do = (t.cuda() for t in make([0, 0], 4, 2, d, seed=1, pad=300))
+        cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+        for _ in range(20):
+            o, lse = fa.attention_forward_grouped(q, k, v, cu, 50, True)
+            grads = fa.attention_backward_grouped(q, k, v, o, do, lse, cu, 50, True)
+            filled = [torch.full_like(t, 3.0) for t in (q, k, v, o)]
+            torch.cuda.synchronize()
+            assert not o.any() and (lse == -np.inf).all() and not any(g.any() for g in grads)
+            assert all((t == 3.0).all() for t in filled)
+            del o, lse, grads, filled
+        assert_no_device_error(fa)
+
+
 def test_max_seqlen_above_the_longest_and_large_scores():
     fa = require_gpu()
     cu, q, k, v, do = make([200, 77], 4, 2, 128, seed=8)
