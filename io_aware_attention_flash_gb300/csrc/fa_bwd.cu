@@ -216,27 +216,27 @@ __global__ void __launch_bounds__(256) fa_bwd_post_grouped_kernel(const BwdParam
     return make_uint4(pack_bf16x2(a.x * s, a.y * s), pack_bf16x2(a.z * s, a.w * s), pack_bf16x2(b.x * s, b.y * s),
                       pack_bf16x2(b.z * s, b.w * s));
   };
+  const size_t row8 = static_cast<size_t>(p.sv.H) * C8, row8kv = static_cast<size_t>(p.sv.Hk) * C8;  // chunks of a row
   if (i < n8) {
-    const size_t row = i / (static_cast<size_t>(p.sv.H) * C8);
-    if (row < static_cast<size_t>(end)) {
+    if (i < end * row8) {
       const float4* acc = reinterpret_cast<const float4*>(p.dq_accum) + 2 * i;
       reinterpret_cast<uint4*>(p.dq)[i] = pack8(acc[0], acc[1], p.scale);
     } else if (p.sv.zero_tail) {
       reinterpret_cast<uint4*>(p.dq)[i] = zero;
-      const size_t in_row = i - row * p.sv.H * C8;
-      if (in_row < static_cast<size_t>(p.sv.Hk) * C8) {
-        reinterpret_cast<uint4*>(p.dk)[row * p.sv.Hk * C8 + in_row] = zero;
-        reinterpret_cast<uint4*>(p.dv)[row * p.sv.Hk * C8 + in_row] = zero;
+      const size_t row = i / row8, in_row = i - row * row8;
+      if (in_row < row8kv) {
+        reinterpret_cast<uint4*>(p.dk)[row * row8kv + in_row] = zero;
+        reinterpret_cast<uint4*>(p.dv)[row * row8kv + in_row] = zero;
       }
     }
     return;
   }
-  const size_t n8kv = static_cast<size_t>(p.rows) * p.sv.Hk * C8;
+  const size_t n8kv = static_cast<size_t>(p.rows) * row8kv;
   const size_t j = i - n8;
   if (p.sv.splits == 1 || j >= 2 * n8kv) return;  // past the last thread with work
   const bool is_v = j >= n8kv;
   const size_t e = is_v ? j - n8kv : j;
-  if (e / (static_cast<size_t>(p.sv.Hk) * C8) >= static_cast<size_t>(end)) return;
+  if (e >= end * row8kv) return;
   const float4* part = reinterpret_cast<const float4*>(p.dkv_part) + 2 * (n8kv * p.sv.splits * (is_v ? 1 : 0) + e);
   float4 a = part[0], b = part[1];
   for (int k = 1; k < p.sv.splits; ++k) {

@@ -209,7 +209,8 @@ cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
 // ----------------------------------------------------------------------------
 // Attention over the cache
 // ----------------------------------------------------------------------------
-// Work: the 128-key tiles of every (sequence, key/value head, row group), in
+// Work: the tiles (128 rows of 128 bytes of K and of V: 128 tokens, at d = 64
+// 256) of every (sequence, key/value head, row group), in
 // that order, are shared out in equal runs over the launch's CTAs, whatever
 // the sequences' lengths; a row group is up to 16 of the (new token, query
 // head) rows that attend to one key/value head.  A CTA that has all tiles of

@@ -7,7 +7,7 @@
 //
 // Every function returns its tensors, or None if anything is not as the C ABI
 // wants it (or an allocation or the call failed): the caller then takes the
-// Python path, which names what is wrong.  No exception leaves a function.
+// Python path, which names what is wrong.  No C++ exception leaves a function.
 #include <Python.h>
 
 #include <cmath>
@@ -158,6 +158,7 @@ PyObject* py_forward_grouped(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (grouped_args(args, n, t, &g) && forward_grouped(g, *t[0], *t[1], *t[2], *t[3], &o, &lse) == FA_OK)
       return pair(std::move(o), std::move(lse));
   } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
   }
   Py_RETURN_NONE;
 }
@@ -220,6 +221,7 @@ PyObject* py_flash_attention_grouped(PyObject*, PyObject* const* args, Py_ssize_
       return THPVariable_Wrap(std::move(o));
     }
   } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
   }
   Py_RETURN_NONE;
 }
@@ -248,6 +250,7 @@ PyObject* py_backward_grouped(PyObject*, PyObject* const* args, Py_ssize_t n) {
       }
     }
   } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
   }
   Py_RETURN_NONE;
 }
@@ -301,6 +304,7 @@ PyObject* py_cache8_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
         stream_of(dev));
     if (st == FA_OK) Py_RETURN_TRUE;
   } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
   }
   Py_RETURN_NONE;
 }
@@ -337,6 +341,7 @@ PyObject* py_decode_cache8(PyObject*, PyObject* const* args, Py_ssize_t n) {
         stream_of(dev));
     if (st == FA_OK) return pair(std::move(o), std::move(lse));
   } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
   }
   Py_RETURN_NONE;
 }

@@ -303,6 +303,33 @@ def test_own_stream_and_captured_training_step():
     assert torch.equal(o, cap[0]) and torch.equal(lse, cap[1])
 
 
+def test_two_calls_at_once():
+    """Two training steps of different shapes on two streams, queued in turn,
+    each with a workspace of its own."""
+    fa = require_gpu()
+    jobs = []
+    for lengths, H, Hk, d, seed in (([700, 90, 300], 8, 2, 128, 31), ([513, 40], 4, 4, 64, 32)):
+        cu, q, k, v, do = (t.cuda() for t in make(lengths, H, Hk, d, seed=seed, pad=7))
+        n = max(lengths)
+        o, lse = fa.attention_forward_grouped(q, k, v, cu, n, True)
+        want = (o, lse, *fa.attention_backward_grouped(q, k, v, o, do, lse, cu, n, True))
+        ws = torch.empty(fa.fa_bwd_grouped_workspace_bytes(len(lengths), n, q.shape[0], H, Hk, d, True), dtype=torch.uint8,
+                         device="cuda")
+        jobs.append((torch.cuda.Stream(), (q, k, v, cu, n), do, ws, want))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for side, (q, k, v, cu, n), do, ws, want in jobs:
+            o, lse = fa.attention_forward_grouped(q, k, v, cu, n, True, stream=side)
+            got.append(((o, lse, *fa.attention_backward_grouped(q, k, v, o, do, lse, cu, n, True, stream=side, workspace=ws)),
+                        want))
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    for a, b in got:
+        for i, (x, y) in enumerate(zip(a, b)):
+            assert rel_fro(f64(x), f64(y)) < 2.0 ** -8 if i == 2 else torch.equal(x, y), i
+
+
 def test_single_heads_match_the_packed_entry_points():
     """H = Hk: the outputs of the packed entry points; dK (and dQ) up to the
     rows that see few keys, whose row statistic is exact here: each side's own
