@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(256, GRP ? 6 : 1) fa_bwd_pre_kernel(const BwdP
       short_rows<D>(p, tid);
       return;
     }
-    tid -= static_cast<long long>(p.short_blocks) * 256;
+    // The rows from the last to the first: the main kernel begins with the first
+    // ones, whose dO and zeroed accumulators then still are in L2.
+    tid = static_cast<long long>(gridDim.x - 1 - blockIdx.x) * blockDim.x + threadIdx.x;
   }
   const long long rh = tid / TPR;  // (row, head) = row·H + head
   const int part = static_cast<int>(tid % TPR);
@@ -200,15 +202,16 @@ __global__ void __launch_bounds__(256) fa_bwd_post_kernel(const BwdParams p, siz
 }
 
 // ----------------------------------------------------------------------------
-// fa_bwd_post_grouped: the same for grouped heads, dK and dV as the sums of
+// fa_bwd_post_grouped: the same for grouped heads, from the last row to the
+// first (the main kernel's last sums still are in L2), dK and dV as the sums of
 // their parts in the parts' order (threads past dQ's n8; no atomics, so the
 // sum does not depend on which CTA finished first), and the rows behind the
 // last sequence, which no main-kernel CTA writes.
 // ----------------------------------------------------------------------------
 template <int D>
-__global__ void __launch_bounds__(256) fa_bwd_post_grouped_kernel(const BwdParams p, size_t n8) {
+__global__ void __launch_bounds__(256, 5) fa_bwd_post_grouped_kernel(const BwdParams p, size_t n8) {
   grid_dependency_wait();
-  const size_t i = static_cast<size_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const size_t i = static_cast<size_t>(gridDim.x - 1 - blockIdx.x) * blockDim.x + threadIdx.x;
   constexpr int C8 = D / 8;
   const int end = packed_end(p.sv);
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
