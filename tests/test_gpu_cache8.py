@@ -333,6 +333,32 @@ def test_attend_long_sequences(d):
     check_attend(fa, 2, 1, d, 64, [9000, 130, 40, 5000, 77], 1, True, seed=15, max_seqlen=10000)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_attend_very_long_sequence(d):
+    """300,001 tokens whose weight lies on the first one and, as small parts, on
+    all others: what a running maximum would lose must still count."""
+    fa = require_gpu()
+    n, block = 300001, 128
+    pages = -(-n // block)
+    g = torch.Generator(device="cuda").manual_seed(34)
+    cache = fa.cache8_alloc(pages, 1, block, d)
+    cache.k.copy_(torch.randn(pages, 1, block, d, device="cuda", generator=g) * 0.02)
+    cache.v.copy_(torch.randn(pages, 1, block, d, device="cuda", generator=g) + 1.0)
+    q = torch.randn(1, 1, 4, d, device="cuda", generator=g).bfloat16()
+    scale = d ** -0.5
+    first = q[0, 0, 0].double() / (q[0, 0, 0].double().square().sum() * scale)
+    cache.k[0, 0, 0] = (first * 12.0).to(torch.float8_e4m3fn)  # a score near 12: e^12 against 300,000
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    o, lse = fa.attention_decode_cache8(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n, True)
+    k, v = (t.reshape(-1, d)[:n].double() for t in cache[:2])
+    s = scale * q[0, 0].double() @ k.T
+    want = torch.softmax(s, 1) @ v
+    assert_no_device_error(fa)
+    # values near 1 of one sign: what of the tail's weight is lost shows in full
+    assert (o[0, 0].double() - want).abs().max() <= 2.0 ** -7 * want.abs().max()
+    assert (lse[0, :, 0].double() - torch.logsumexp(s, 1)).abs().max() <= LSE_TOL * 15
+
+
 def test_attend_uneven_scales_and_peaked_scores():
     """V scales 2^40 apart from page to page; scores of which one key takes all,
     found late; scores that fall and rise by hundreds."""

@@ -303,6 +303,30 @@ def test_own_stream_and_captured_training_step():
     assert torch.equal(o, cap[0]) and torch.equal(lse, cap[1])
 
 
+def test_more_than_two_to_the_31_elements():
+    """1200 sequences of 500 tokens, 32 heads of 128: q holds 2.4e9 elements.
+    The first and the last sequence against the formula, one head of each group."""
+    fa = require_gpu()
+    n, nseq, H, Hk, d = 500, 1200, 32, 2, 128
+    T = n * nseq
+    assert T * H * d > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(33)
+    q, do = (torch.empty(T, H, d, device="cuda", dtype=torch.bfloat16).normal_(generator=g) for _ in range(2))
+    k, v = (torch.empty(T, Hk, d, device="cuda", dtype=torch.bfloat16).normal_(generator=g) for _ in range(2))
+    cu = torch.arange(0, T + 1, n, dtype=torch.int32, device="cuda")
+    o, lse = fa.attention_forward_grouped(q, k, v, cu, n, True)
+    grads = fa.attention_backward_grouped(q, k, v, o, do, lse, cu, n, True)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    for a in (0, T - n):
+        rows = [t[a:a + n].cpu() for t in (q, k, v, do)]
+        O, L, *ref = formula(torch.tensor([0, n]), *rows, d ** -0.5, True)
+        assert np.abs(f64(o[a:a + n]) - O).max() <= 2.0 ** -7 * np.abs(f64(rows[2])).max()
+        assert np.abs(f64(lse[:, a:a + n]) - L).max() <= LSE_TOL
+        for t, r in zip(grads, ref):
+            assert rel_fro(f64(t[a:a + n]), r) <= GRAD_TOL
+
+
 def test_two_calls_at_once():
     """Two training steps of different shapes on two streams, queued in turn,
     each with a workspace of its own."""
