@@ -10,12 +10,12 @@
 // be more accurate, since e4m3 keeps the same relative step at any size.
 //
 // Both kernels are bound by DRAM.  Measured on a GB300 (a plain copy moves 6.78
-// TB/s): the store of 34,700 tokens of 8 heads, d = 128, 33 us, 6.2 TB/s; the
-// attention of one token over 4 x 32768 tokens, 32 heads, d = 128, 158 us, 6.8
-// TB/s, and over 64 sequences of 100 .. 8192 tokens, 32 query over 8 heads, 91
-// us, 6.2 TB/s.  At d = 64 a tile is half the bytes for the same instructions:
-// 4.7 TB/s for up to 4 rows; from 16 rows on (4 tokens of 8 heads a group: two
-// row groups, 31 us for 39 MB) the tile's instructions bound it.
+// TB/s), whole calls: the store of 34,700 tokens of 8 heads, d = 128, 32 us, 6.5
+// TB/s; the attention of one token over 4 x 32768 tokens, 32 heads, d = 128, 164
+// us, 6.5 TB/s, and over 64 sequences of 100 .. 8192 tokens, 32 query over 8
+// heads, 94 us, 5.9 TB/s.  At d = 64 there are twice as many scores to a byte: 5.1
+// TB/s for up to 4 rows; from 16 rows on (4 tokens of 8 heads a group: two row
+// groups, 30 us for 39 MB) the instructions of a tile bound it.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
