@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 #include <math_constants.h>
 
+#include "cache8_phases.h"
 #include "fa_kernels.cuh"
 #include "ptx.cuh"
 
@@ -380,8 +381,8 @@ struct Dec8Cfg {
   static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [2 tiles][NCW][STAT_WARP]
   static constexpr int OFF_SCAN = OFF_STAT + 2 * NCW * STAT_WARP * 4;  // [warps] sums of tiles
   static constexpr int OFF_BAR = (OFF_SCAN + NUM_WARPS * 4 + 7) / 8 * 8;
-  static constexpr int B_FULL = 0, B_EMPTY = NST, B_SFULL = 2 * NST, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 1,
-                       B_XCH = B_PVDONE + 2, B_QREADY = B_XCH + 2, B_DRAIN = B_QREADY + 1, NBAR = B_DRAIN + 1;
+  static constexpr int B_FULL = 0, B_EMPTY = NST, B_SFULL = 2 * NST, B_PFULL = B_SFULL + cache8::kSBars,
+                       B_PVDONE = B_PFULL + cache8::kPBars, B_XCH = B_PVDONE + cache8::kPvBars, B_QREADY = B_XCH + 2, B_DRAIN = B_QREADY + 1, NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;    // slack to align the base to 1024
   static constexpr uint32_t COLS = 2 * NP * NS + 2 * NO;
@@ -481,9 +482,9 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       mbar_init(bar(C::B_FULL + s), 32);
       mbar_init(bar(C::B_EMPTY + s), 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_SFULL + i), 1);
-    mbar_init(bar(C::B_PFULL), 32 * C::NCW);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(C::B_PVDONE + i), 1);
+    for (int i = 0; i < cache8::kSBars; ++i) mbar_init(bar(C::B_SFULL + i), 1);
+    for (int i = 0; i < cache8::kPBars; ++i) mbar_init(bar(C::B_PFULL + i), 32 * C::NCW);
+    for (int i = 0; i < cache8::kPvBars; ++i) mbar_init(bar(C::B_PVDONE + i), 1);
     for (int i = 0; i < C::WG; ++i) mbar_init(bar(C::B_XCH + i), 128);
     mbar_init(bar(C::B_QREADY), 32 * C::NCW);
     mbar_init(bar(C::B_DRAIN), 1);
@@ -610,7 +611,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         const int n_pages = min(ppt, (cur.len - kt * kTokens<D> + p.block - 1) >> p.block_shift);
         const int from = i * ppt + lane;  // this lane's page of the tile
         const int page = __shfl_sync(0xffffffffu, cur.page, from & 31);
-        if (t >= C::NST) ok = wait_bounded(bar(C::B_EMPTY + st), ((t / C::NST) - 1) & 1, abort_flag, p.err, p.timeout_ns);
+        if (t >= C::NST) ok = wait_bounded(bar(C::B_EMPTY + st), cache8::ring(t - C::NST, C::NST).parity, abort_flag, p.err, p.timeout_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(bar(C::B_FULL + st), n_pages * p.block * D * 2);
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     // Every copy issued lands before the CTA may exit, whoever aborted.
     for (int s = 0; s < C::NST && s < t; ++s) {
       const int last = s + ((t - 1 - s) / C::NST) * C::NST;
-      wait_drain(bar(C::B_FULL + s), (last / C::NST) & 1, p.err, p.timeout_ns);
+      wait_drain(bar(C::B_FULL + s), cache8::ring(last, C::NST).parity, p.err, p.timeout_ns);
     }
   } else if (warp == C::NCW + 1) {
     // ---------------------------------------------------------------- MMA
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       const uint64_t dP = sdesc8<C::NO>(sb + C::OFF_P, 16);  // MN-major: a key's columns are a row
       auto issue_s = [&](int u) -> bool {
         const int st = u % C::NST;
-        if (!wait_bounded(bar(C::B_FULL + st), (u / C::NST) & 1, abort_flag, p.err, p.timeout_ns)) return false;
+        if (!wait_bounded(bar(C::B_FULL + st), cache8::ring(u, C::NST).parity, abort_flag, p.err, p.timeout_ns)) return false;
         tc_fence_after();
 #pragma unroll
         for (int pos = 0; pos < C::NP; ++pos)  // d = 64: the rows' first tokens, then their second ones
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           for (int kk = 0; kk < D / 32; ++kk)
             mma_e4m3(tmem + C::NS * (C::NP * (u & 1) + pos), sdesc_add(dK0, st * C::TILE_BYTES + pos * D + kk * 32),
                      sdesc_add(dQ, kk * 32), idesc_s, kk > 0);
-        tc_commit(bar(C::B_SFULL + (u & 1)));
+        tc_commit(bar(C::B_SFULL + cache8::s_full(u).index));
         return true;
       };
       int t = 0, n_item = 0;
@@ -670,7 +671,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           // the next tile's scores run while this tile's P is formed (across
           // items they cannot: the next Q is staged after this item's last S)
           if (kt + 1 < w.k1) ok = issue_s(t + 1);
-          ok = ok && wait_bounded(bar(C::B_PFULL), t & 1, abort_flag, p.err, p.timeout_ns);
+          const cache8::Phase pf = cache8::p_full(t);
+          ok = ok && wait_bounded(bar(C::B_PFULL + pf.index), pf.parity, abort_flag, p.err, p.timeout_ns);
           if (!ok) break;
           tc_fence_after();
           const int st = t % C::NST;
@@ -678,7 +680,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           for (int kk = 0; kk < kTile / 32; ++kk)
             mma_e4m3(tmem + C::O_COL + C::NO * (t & 1), sdesc_add(dV0, st * C::TILE_BYTES + kk * 32 * 128),
                      sdesc_add(dP, (t & 1) * C::P_BYTES + kk * 32 * C::NO), idesc_o, kk > 0);
-          tc_commit(bar(C::B_PVDONE + (t & 1)));
+          tc_commit(bar(C::B_PVDONE + cache8::pv_done(t).index));
           tc_commit(bar(C::B_EMPTY + st));
         }
       }
@@ -784,7 +786,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       // O of tile u (its statistics are still in their buffer) into the running one.
       auto add_o = [&](int u) {
         const float* stat = stats + (u & 1) * C::NCW * C::STAT_WARP;
-        wait(C::B_PVDONE + (u & 1), (u >> 1) & 1);
+        wait(C::B_PVDONE + cache8::pv_done(u).index, cache8::pv_done(u).parity);
         __syncwarp();
         tc_fence_after();
         uint32_t o[NL];
@@ -814,7 +816,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         // K's scale, 1 / V's scale and its log2 of the page of this thread's tokens
         const float4 sc = reinterpret_cast<const float4*>(smem + C::OFF_SC)[st * C::MAX_PPT + ((NP * r) >> p.block_shift)];
         const float ks = sc.x, inv_vs = sc.y, vef = sc.z;
-        wait(C::B_SFULL + (t & 1), (t >> 1) & 1);
+        wait(C::B_SFULL + cache8::s_full(t).index, cache8::s_full(t).parity);
         __syncwarp();
         tc_fence_after();
         float y[NP][RW];
@@ -931,7 +933,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(bar(C::B_PFULL));
+        mbar_arrive(bar(C::B_PFULL + cache8::p_full(t).index));
         // The product of the tile before is ready by now: waiting for this one's
         // would leave the warps idle for its whole latency.
         if (kt > w.k0) add_o(t - 1);
