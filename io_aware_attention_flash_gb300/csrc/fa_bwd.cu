@@ -53,10 +53,10 @@ __device__ __forceinline__ void locate_row(const SeqView& sv, int nseq, int g, i
   int lo = 0, hi = nseq - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(sv.cu_seqlens + mid) <= g) lo = mid; else hi = mid - 1;
+    if (sv.cu_seqlens[mid] <= g) lo = mid; else hi = mid - 1;
   }
   bs = lo;
-  local = g - __ldg(sv.cu_seqlens + lo);
+  local = g - sv.cu_seqlens[lo];
 }
 
 // ----------------------------------------------------------------------------
@@ -99,7 +99,7 @@ __device__ __forceinline__ void short_rows(const BwdParams& p, long long tid) {
   if (seen > 0) {
     q = *reinterpret_cast<const uint4*>(p.q + g * p.ldq + h * D + part * 8);
     dout = *reinterpret_cast<const uint4*>(p.dout + (g * p.sv.H + h) * D + part * 8);
-    lse2 = __ldg(p.lse + static_cast<size_t>(h) * p.sv.N + g) * kLog2e;
+    lse2 = p.lse[static_cast<size_t>(h) * p.sv.N + g] * kLog2e;
   }
   auto dot = [](const uint4& a, const uint4& b) {  // over the row's TPR threads
     float v = bf16lo_to_f32(a.x) * bf16lo_to_f32(b.x) + bf16hi_to_f32(a.x) * bf16hi_to_f32(b.x) +
@@ -862,9 +862,9 @@ __global__ void __launch_bounds__(BwdCfg<D>::NUM_THREADS, 1)
       const int q = qi * kTile + r;
       if (q >= sp.seqlen) return g == 0 ? CUDART_INF_F : 0.f;
       if (GRP && g == 1 && exact_row(p, sp.seqlen, q))
-        return __ldg(p.d_short + (static_cast<size_t>(sp.bs) * p.sv.H + h) * kExactRows + q);
+        return p.d_short[(static_cast<size_t>(sp.bs) * p.sv.H + h) * kExactRows + q];
       const size_t at = GRP ? static_cast<size_t>(h) * p.sv.N + stat_base + q : stat_base + q;
-      return __ldg((g == 0 ? p.lse : p.dpsum) + at);
+      return (g == 0 ? p.lse : p.dpsum)[at];
     };
     // Both warpgroups read all 128 entries of a tile (log2e·LSE and D):
     // publish them through an mbarrier (a bounded wait, unlike a named

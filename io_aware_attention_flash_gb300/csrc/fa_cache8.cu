@@ -105,15 +105,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) fa_cache8_store_kernel(const Ca
   int page = -1, old = 0, lo = 0, hi = 0;  // the page; its tokens [0, old) are held, [lo, hi) are new
   int src = 0;                             // input row of slot 0
   if (which < 2 * p.Hk) {
-    const int first = min(max(__ldg(p.cu_seqlens + b), 0), p.total);
-    const int count = min(max(__ldg(p.cu_seqlens + b + 1), first), p.total) - first;
-    const int start = __ldg(p.start + b);
+    const int first = min(max(p.cu_seqlens[b], 0), p.total);
+    const int count = min(max(p.cu_seqlens[b + 1], first), p.total) - first;
+    const int start = p.start[b];
     const long long end = static_cast<long long>(start) + min(count, p.max_new);
     const long long blk = static_cast<long long>(start) / BLOCK + nth;
     if (start < 0) {
       if (count > 0 && tid == 0) atomicOr(p.err, kDevErrPage);
     } else if (count > 0 && blk * BLOCK < end) {
-      if (blk < p.table_cols) page = __ldg(p.table + static_cast<size_t>(b) * p.table_cols + blk);
+      if (blk < p.table_cols) page = p.table[static_cast<size_t>(b) * p.table_cols + blk];
       const long long base = blk * BLOCK;
       old = static_cast<int>(max(0LL, start - base));
       lo = old;
@@ -257,18 +257,22 @@ __device__ __forceinline__ int run_of(long long t, int total, int ctas) {
 
 // Cached tokens of sequence b: a length below 0 counts as 0, one past
 // max_seqlen or the page table as the nearer of the two.
-__device__ __forceinline__ int cached_len(const Cache8DecodeParams& p, int b) {
+__device__ __forceinline__ int clamp_len(const Cache8DecodeParams& p, int n) {
   const long long cap = min(static_cast<long long>(p.table_cols) * p.block, static_cast<long long>(p.max_seqlen));
-  const int n = __ldg(p.seqlens + b);
   return static_cast<int>(min(max(static_cast<long long>(n), 0LL), cap));
 }
+__device__ __forceinline__ int cached_len(const Cache8DecodeParams& p, int b) { return clamp_len(p, p.seqlens[b]); }
 // Tokens of a tile: 128 rows of 128 bytes.
 template <int D>
 constexpr int kTokens = kTile * 128 / D;
 
 template <int D>
+__device__ __forceinline__ int len_tiles(int len) {
+  return (len + kTokens<D> - 1) / kTokens<D>;
+}
+template <int D>
 __device__ __forceinline__ int seq_tiles(const Cache8DecodeParams& p, int b) {
-  return (cached_len(p, b) + kTokens<D> - 1) / kTokens<D>;
+  return len_tiles<D>(cached_len(p, b));
 }
 
 // A CTA's walk through its run: the tiles [k0, k1) of one item after another.
@@ -550,7 +554,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     const int first = base + sum - n;
     if (writes && b < p.B) {
       if (p.B > kScanSeqs) p.tile_start[b] = first;
-      if (__ldg(p.seqlens + b) != cached_len(p, b)) atomicOr(p.err, kDevErrPage);
+      if (p.seqlens[b] != cached_len(p, b)) atomicOr(p.err, kDevErrPage);
     }
     const uint32_t here = __ballot_sync(0xffffffffu, n > 0 && w.t >= first && w.t < first + n);
     if (here != 0) {
@@ -586,14 +590,14 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       left -= u.tiles;
       u.page = p.num_blocks;
       if (lane < u.tiles * ppt && (u.kt0 * ppt + lane) * p.block < u.len)
-        u.page = __ldg(p.table + static_cast<size_t>(w.b) * p.table_cols + u.kt0 * ppt + lane);
+        u.page = p.table[static_cast<size_t>(w.b) * p.table_cols + u.kt0 * ppt + lane];
     };
     auto load_scales = [&](Unit& u) {
       const bool token = lane < u.tiles * ppt && (u.kt0 * ppt + lane) * p.block < u.len;
       u.ks = u.vs = 0.f;
       if (token && u.page >= 0 && u.page < p.num_blocks) {
-        u.ks = __ldg(p.k_scale + static_cast<size_t>(u.page) * p.Hk + u.hk);
-        u.vs = __ldg(p.v_scale + static_cast<size_t>(u.page) * p.Hk + u.hk);
+        u.ks = p.k_scale[static_cast<size_t>(u.page) * p.Hk + u.hk];
+        u.vs = p.v_scale[static_cast<size_t>(u.page) * p.Hk + u.hk];
       } else {
         if (token) atomicOr(p.err, kDevErrPage);
         u.page = p.num_blocks;
@@ -732,10 +736,10 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           const uint16_t* src = p.q + static_cast<size_t>(__shfl_sync(0xffffffffu, row_q, (q * LPR) & 31)) * D + E * lane;
           const bool live = q < RW && row0 + q < rows;
           if constexpr (E == 4) {
-            const uint2 x = live ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0u, 0u);
+            const uint2 x = live ? *reinterpret_cast<const uint2*>(src) : make_uint2(0u, 0u);
             raw[j][0] = x.x, raw[j][1] = x.y;
           } else {
-            raw[j][0] = live ? __ldg(reinterpret_cast<const uint32_t*>(src)) : 0u;
+            raw[j][0] = live ? *reinterpret_cast<const uint32_t*>(src) : 0u;
           }
         }
 #pragma unroll
@@ -1020,14 +1024,17 @@ __global__ void __launch_bounds__(128) fa_cache8_merge_kernel(const Cache8Decode
   int s0 = 0, nt = 0, total = 0;
   const bool scan = p.B <= kScanSeqs;
   if (scan) {
+    // Before the wait, yet complete: the attention lets this kernel start only
+    // behind its own wait for whatever wrote the lengths.  Read from L2.
+    auto tiles = [&](int j) { return len_tiles<D>(clamp_len(p, ld_relaxed_gpu(p.seqlens + j))); };
     for (int j = lane; j < p.B; j += 32) {
-      const int n = seq_tiles<D>(p, j);
+      const int n = tiles(j);
       total += n;
       s0 += j < b ? n : 0;
     }
     s0 = __reduce_add_sync(0xffffffffu, s0) * per;
     total = __reduce_add_sync(0xffffffffu, total) * per;
-    nt = seq_tiles<D>(p, b);
+    nt = tiles(b);
   }
   grid_dependency_wait();
   if (!live) return;

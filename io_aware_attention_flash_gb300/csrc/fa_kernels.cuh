@@ -225,8 +225,8 @@ __device__ __forceinline__ SeqPos seq_pos(const SeqView& sv, int pair) {
   s.bs = pair / sv.H;
   s.h = pair % sv.H;
   if (sv.cu_seqlens) {
-    s.seq_start = __ldg(sv.cu_seqlens + s.bs);
-    s.seqlen = __ldg(sv.cu_seqlens + s.bs + 1) - s.seq_start;
+    s.seq_start = sv.cu_seqlens[s.bs];
+    s.seqlen = sv.cu_seqlens[s.bs + 1] - s.seq_start;
     s.row_base = s.seq_start;
     s.tma_row0 = s.seq_start;
     s.tma_b = 0;
@@ -245,8 +245,8 @@ __device__ __forceinline__ SeqPos seq_pos(const SeqView& sv, int pair) {
 // kernel leave its tensors; query head h reads key/value head h / G.
 __device__ __forceinline__ void clamp_seq(const SeqView& sv, int bs, SeqPos& s) {
   s.bs = bs;
-  const int a = min(max(__ldg(sv.cu_seqlens + bs), 0), sv.N);
-  const int b = min(max(__ldg(sv.cu_seqlens + bs + 1), a), sv.N);
+  const int a = min(max(sv.cu_seqlens[bs], 0), sv.N);
+  const int b = min(max(sv.cu_seqlens[bs + 1], a), sv.N);
   s.seq_start = s.row_base = s.tma_row0 = a;
   s.seqlen = min(b - a, sv.max_seqlen);
   s.tma_b = 0;
@@ -263,7 +263,7 @@ __device__ __forceinline__ SeqPos seq_pos_grouped(const SeqView& sv, int pair, i
 
 // First row behind the last sequence.
 __device__ __forceinline__ int packed_end(const SeqView& sv) {
-  return min(max(__ldg(sv.cu_seqlens + sv.nseq), 0), sv.N);
+  return min(max(sv.cu_seqlens[sv.nseq], 0), sv.N);
 }
 
 // Launch with or without programmatic stream serialisation (the kernel may

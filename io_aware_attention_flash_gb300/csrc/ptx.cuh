@@ -115,8 +115,18 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // running (once every CTA of that kernel has issued launch_dependents or
 // exited); wait blocks until that kernel has completed and its memory
 // operations are visible.  Without the launch attribute both are no-ops.
+// What is visible is so to ordinary loads: non-coherent ones (ld.global.nc) are
+// for data that nothing writes during the whole life of the kernel, which here
+// overlaps the kernel before it.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// An int of global memory as L2 has it.
+__device__ __forceinline__ int ld_relaxed_gpu(const int* p) {
+  int v;
+  asm("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
 
 // Generic-proxy writes to global memory made visible to the async proxy
 // (TMA reduce-adds into bytes that another kernel wrote with plain stores).
