@@ -29,7 +29,7 @@ TORCH_LIB_PATH = os.path.join(LIB_DIR, "_fa_torch.so")
 TORCH_SOURCE = "fa_torch.cpp"
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_cache8.cu", "fa_microbench.cu"]
-HEADERS = ["ptx.cuh", "fa_kernels.cuh", "cache8_phases.h"]
+HEADERS = ["ptx.cuh", "fa_kernels.cuh", "cache8_phases.h", "cache8_tiles.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
           "-Xptxas", "-v"]

@@ -22,6 +22,7 @@
 #include <math_constants.h>
 
 #include "cache8_phases.h"
+#include "cache8_tiles.h"
 #include "fa_kernels.cuh"
 #include "ptx.cuh"
 
@@ -267,12 +268,8 @@ template <int D>
 constexpr int kTokens = kTile * 128 / D;
 
 template <int D>
-__device__ __forceinline__ int len_tiles(int len) {
-  return (len + kTokens<D> - 1) / kTokens<D>;
-}
-template <int D>
 __device__ __forceinline__ int seq_tiles(const Cache8DecodeParams& p, int b) {
-  return len_tiles<D>(cached_len(p, b));
+  return cache8::tiles_of(cached_len(p, b), kTokens<D>);
 }
 
 // A CTA's walk through its run: the tiles [k0, k1) of one item after another.
@@ -289,7 +286,7 @@ struct Walk {
     auto read = [&]() {
       len = cached_len(p, b);
       if (WARP) len = __shfl_sync(0xffffffffu, len, 0);
-      nt = (len + kTokens<D> - 1) / kTokens<D>;
+      nt = cache8::tiles_of(len, kTokens<D>);
     };
     read();
     while (t >= seq0 + nt * per) {
@@ -589,11 +586,11 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       u.hk = w.hk;
       left -= u.tiles;
       u.page = p.num_blocks;
-      if (lane < u.tiles * ppt && (u.kt0 * ppt + lane) * p.block < u.len)
+      if (lane < u.tiles * ppt && u.kt0 * ppt + lane < cache8::pages_of(u.len, p.block_shift))
         u.page = p.table[static_cast<size_t>(w.b) * p.table_cols + u.kt0 * ppt + lane];
     };
     auto load_scales = [&](Unit& u) {
-      const bool token = lane < u.tiles * ppt && (u.kt0 * ppt + lane) * p.block < u.len;
+      const bool token = lane < u.tiles * ppt && u.kt0 * ppt + lane < cache8::pages_of(u.len, p.block_shift);
       u.ks = u.vs = 0.f;
       if (token && u.page >= 0 && u.page < p.num_blocks) {
         u.ks = p.k_scale[static_cast<size_t>(u.page) * p.Hk + u.hk];
@@ -612,7 +609,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     while (ok && cur.tiles > 0) {
       for (int i = 0; i < cur.tiles; ++i, ++t) {
         const int st = t % C::NST, kt = cur.kt0 + i;
-        const int n_pages = min(ppt, (cur.len - kt * kTokens<D> + p.block - 1) >> p.block_shift);
+        const int n_pages = min(ppt, cache8::pages_of(cur.len, p.block_shift) - kt * ppt);
         const int from = i * ppt + lane;  // this lane's page of the tile
         const int page = __shfl_sync(0xffffffffu, cur.page, from & 31);
         if (t >= C::NST) ok = wait_bounded(bar(C::B_EMPTY + st), cache8::ring(t - C::NST, C::NST).parity, abort_flag, p.err, p.timeout_ns);
@@ -842,7 +839,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         if (kt >= kt_mask) {
 #pragma unroll
           for (int q = 0; q < RW; ++q) {
-            const int end = w.len - __shfl_sync(0xffffffffu, row_hidden, q * LPR) - (kt * TOK + NP * r);
+            const int end = cache8::tokens_from(w.len, kt, TOK, NP * r) - __shfl_sync(0xffffffffu, row_hidden, q * LPR);
 #pragma unroll
             for (int pos = 0; pos < NP; ++pos)
               if (pos >= end) y[pos][q] = -CUDART_INF_F;
@@ -929,7 +926,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
         }
         // slots without a token may hold NaN, and 0 · NaN is not 0
         if (wg == 0 && kt >= kt_mask) {
-          const int held = w.len - (kt * TOK + NP * r);  // tokens of this row
+          const int held = cache8::tokens_from(w.len, kt, TOK, NP * r);  // tokens of this row
           uint4* vrow = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::TILE_BYTES + r * 128);
 #pragma unroll
           for (int u = 0; u < 8; ++u)  // 16-byte chunks, swizzled
@@ -1026,7 +1023,7 @@ __global__ void __launch_bounds__(128) fa_cache8_merge_kernel(const Cache8Decode
   if (scan) {
     // Before the wait, yet complete: the attention lets this kernel start only
     // behind its own wait for whatever wrote the lengths.  Read from L2.
-    auto tiles = [&](int j) { return len_tiles<D>(clamp_len(p, ld_relaxed_gpu(p.seqlens + j))); };
+    auto tiles = [&](int j) { return cache8::tiles_of(clamp_len(p, ld_relaxed_gpu(p.seqlens + j)), kTokens<D>); };
     for (int j = lane; j < p.B; j += 32) {
       const int n = tiles(j);
       total += n;
