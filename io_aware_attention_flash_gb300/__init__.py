@@ -137,6 +137,15 @@ def flash_attention(q, k, v, causal: bool = False, scale=None):
 # ---------------------------------------------------------------------------
 # Each call first goes to its compiled counterpart, which returns None where
 # something is not in order; the Python path then runs or says what is wrong.
+_tracing = torch._C._get_tracing_state
+
+
+def _refuse_trace(name: str) -> None:
+    """torch.jit.trace would record the outputs' allocation and not the kernel."""
+    if _tracing() is not None:
+        raise RuntimeError(f"{name} cannot be recorded by torch.jit.trace (flash_attention_grouped can)")
+
+
 def _on_stream(stream, t):
     """What a call on a stream of its own allocates belongs to that stream, so
     that its memory is not handed to another one while the kernels still use
@@ -152,6 +161,7 @@ def attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool
     multiple of Hk; slices of one wider projection are taken as they are).
     Returns (o [T,H,d] bf16, lse [H,T] fp32); rows behind the last sequence
     get o = 0, lse = -inf."""
+    _refuse_trace("attention_forward_grouped")
     if stream is None:
         out = _binding.native().forward_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
         if out is not None:
@@ -172,6 +182,7 @@ def attention_backward_grouped(q, k, v, o, dout, lse, cu_seqlens, max_seqlen: in
                                stream=None, workspace=None):
     """Returns (dq [T,H,d], dk, dv [T,Hk,d]), zero in rows behind the last
     sequence.  dk and dv are summed over the query heads that share them."""
+    _refuse_trace("attention_backward_grouped")
     if stream is None and workspace is None:
         out = _binding.native().backward_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale, o, dout, lse)
         if out is not None:
@@ -223,9 +234,10 @@ def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool =
     a CUDA graph, run it outside first and let go of that run's graph (its
     outputs and losses): PyTorch cannot capture a backward pass into leaves
     that a graph recorded outside still holds."""
-    o = _binding.native().flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
-    if o is not None:
-        return o
+    if _tracing() is None:  # a trace records the Python function as one operation, the compiled one not at all
+        o = _binding.native().flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
+        if o is not None:
+            return o
     return _FlashAttentionGrouped.apply(q, k, v, cu_seqlens, max_seqlen, causal, scale)
 
 
@@ -253,6 +265,7 @@ def cache8_store(k, v, cache: Cache8, block_table, cu_seqlens, start, max_new: i
     of k, v [T,Hk,d] become tokens start[b], start[b]+1, ... of sequence b,
     in the pages block_table [B,cols] names (int32, as cu_seqlens [B+1] and
     start [B]); max_new is the largest number of new tokens of a sequence."""
+    _refuse_trace("cache8_store")
     if stream is None and _binding.native().cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new):
         return
     fa_cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new, stream)
@@ -264,6 +277,7 @@ def attention_decode_cache8(q, cache: Cache8, block_table, seqlens, max_seqlen: 
     seqlens int32 [B] cached tokens (the new ones among them; 0 for an empty
     slot), max_seqlen at least every length.  Returns (o [B,Nq,H,d] bf16, lse
     [B,H,Nq] fp32).  causal as in attention_decode."""
+    _refuse_trace("attention_decode_cache8")
     if stream is None and workspace is None:
         out = _binding.native().decode_cache8(q, cache, block_table, seqlens, max_seqlen, causal, scale)
         if out is not None:
