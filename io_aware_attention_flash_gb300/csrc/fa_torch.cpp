@@ -8,6 +8,8 @@
 // Every function returns its tensors, or None if anything is not as the C ABI
 // wants it (or an allocation or the call failed): the caller then takes the
 // Python path, which names what is wrong.  No C++ exception leaves a function.
+// Allocations and launches, which may have to wait (for memory, for room in the
+// launch queue), run without the interpreter lock.
 #include <Python.h>
 
 #include <cmath>
@@ -26,6 +28,18 @@
 namespace {
 
 using at::Tensor;
+
+// Lets other Python threads run while in scope (also left by an exception).
+class WithoutLock {
+ public:
+  WithoutLock() : state_(PyEval_SaveThread()) {}
+  ~WithoutLock() { PyEval_RestoreThread(state_); }
+  WithoutLock(const WithoutLock&) = delete;
+  WithoutLock& operator=(const WithoutLock&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
 
 // A tensor argument; nullptr if it is something else.
 const Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -155,8 +169,14 @@ PyObject* py_forward_grouped(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const Tensor* t[4];
     Grouped g;
     Tensor o, lse;
-    if (grouped_args(args, n, t, &g) && forward_grouped(g, *t[0], *t[1], *t[2], *t[3], &o, &lse) == FA_OK)
-      return pair(std::move(o), std::move(lse));
+    if (grouped_args(args, n, t, &g)) {
+      fa_status st;
+      {
+        WithoutLock unlocked;
+        st = forward_grouped(g, *t[0], *t[1], *t[2], *t[3], &o, &lse);
+      }
+      if (st == FA_OK) return pair(std::move(o), std::move(lse));
+    }
   } catch (...) {
     PyErr_Clear();  // an exception that came out of Python
   }
@@ -216,8 +236,12 @@ PyObject* py_flash_attention_grouped(PyObject*, PyObject* const* args, Py_ssize_
     const Tensor* t[4];
     Grouped g;
     if (grouped_args(args, n, t, &g)) {
-      Tensor o = FlashAttentionGrouped::apply(*t[0], *t[1], *t[2], *t[3], static_cast<int64_t>(g.max_seqlen), g.causal,
-                                              static_cast<double>(g.scale));
+      Tensor o;
+      {
+        WithoutLock unlocked;
+        o = FlashAttentionGrouped::apply(*t[0], *t[1], *t[2], *t[3], static_cast<int64_t>(g.max_seqlen), g.causal,
+                                         static_cast<double>(g.scale));
+      }
       return THPVariable_Wrap(std::move(o));
     }
   } catch (...) {
@@ -235,7 +259,12 @@ PyObject* py_backward_grouped(PyObject*, PyObject* const* args, Py_ssize_t n) {
       if (o && dout && lse && dense(*o, at::kBFloat16, {g.T, g.H, g.d}, g.dev) &&
           dense(*dout, at::kBFloat16, {g.T, g.H, g.d}, g.dev) && dense(*lse, at::kFloat, {g.H, g.T}, g.dev)) {
         Tensor d[3];
-        if (backward_grouped(g, *t[0], *t[1], *t[2], *o, *dout, *lse, *t[3], &d[0], &d[1], &d[2]) == FA_OK) {
+        fa_status st;
+        {
+          WithoutLock unlocked;
+          st = backward_grouped(g, *t[0], *t[1], *t[2], *o, *dout, *lse, *t[3], &d[0], &d[1], &d[2]);
+        }
+        if (st == FA_OK) {
           PyObject* r = PyTuple_New(3);
           for (int i = 0; r && i < 3; ++i) {
             PyObject* x = THPVariable_Wrap(std::move(d[i]));
@@ -296,12 +325,16 @@ PyObject* py_cache8_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
         !dense(*table, at::kInt, {B, table->size(1)}, dev) || !dense(*cu, at::kInt, {B + 1}, dev) ||
         !dense(*start, at::kInt, {B}, dev))
       Py_RETURN_NONE;
-    const fa_status st = fa_cache8_store(
-        k->data_ptr(), v->data_ptr(), c.t[0]->data_ptr(), c.t[1]->data_ptr(), static_cast<float*>(c.t[2]->data_ptr()),
-        static_cast<float*>(c.t[3]->data_ptr()), static_cast<const int*>(table->data_ptr()),
-        static_cast<const int*>(cu->data_ptr()), static_cast<const int*>(start->data_ptr()), static_cast<int>(B), max_new,
-        static_cast<int>(T), c.num_blocks, static_cast<int>(table->size(1)), c.Hk, c.block, c.d, ldk, ldv,
-        stream_of(dev));
+    fa_status st;
+    {
+      WithoutLock unlocked;
+      st = fa_cache8_store(
+          k->data_ptr(), v->data_ptr(), c.t[0]->data_ptr(), c.t[1]->data_ptr(), static_cast<float*>(c.t[2]->data_ptr()),
+          static_cast<float*>(c.t[3]->data_ptr()), static_cast<const int*>(table->data_ptr()),
+          static_cast<const int*>(cu->data_ptr()), static_cast<const int*>(start->data_ptr()), static_cast<int>(B), max_new,
+          static_cast<int>(T), c.num_blocks, static_cast<int>(table->size(1)), c.Hk, c.block, c.d, ldk, ldv,
+          stream_of(dev));
+    }
     if (st == FA_OK) Py_RETURN_TRUE;
   } catch (...) {
     PyErr_Clear();  // an exception that came out of Python
@@ -330,15 +363,21 @@ PyObject* py_decode_cache8(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int b = static_cast<int>(B), nq = static_cast<int>(Nq), h = static_cast<int>(H);
     const size_t bytes = fa_decode_cache8_workspace_bytes(b, nq, h, c.Hk, max_seqlen, c.d);
     if (bytes == 0) Py_RETURN_NONE;
-    const auto opt = q->options().requires_grad(false);
-    Tensor o = at::empty(q->sizes(), opt), lse = at::empty({B, H, Nq}, opt.dtype(at::kFloat));
-    Tensor ws = at::empty({static_cast<int64_t>(bytes)}, opt.dtype(at::kByte));
-    const fa_status st = fa_fwd_decode_cache8(
-        q->data_ptr(), c.t[0]->data_ptr(), c.t[1]->data_ptr(), static_cast<const float*>(c.t[2]->data_ptr()),
-        static_cast<const float*>(c.t[3]->data_ptr()), static_cast<const int*>(table->data_ptr()),
-        static_cast<const int*>(lens->data_ptr()), o.data_ptr(), static_cast<float*>(lse.data_ptr()), ws.data_ptr(), bytes,
-        b, nq, h, c.Hk, c.num_blocks, static_cast<int>(table->size(1)), c.block, max_seqlen, c.d, scale, causal,
-        stream_of(dev));
+    Tensor o, lse;
+    fa_status st;
+    {
+      WithoutLock unlocked;
+      const auto opt = q->options().requires_grad(false);
+      o = at::empty(q->sizes(), opt);
+      lse = at::empty({B, H, Nq}, opt.dtype(at::kFloat));
+      Tensor ws = at::empty({static_cast<int64_t>(bytes)}, opt.dtype(at::kByte));
+      st = fa_fwd_decode_cache8(
+          q->data_ptr(), c.t[0]->data_ptr(), c.t[1]->data_ptr(), static_cast<const float*>(c.t[2]->data_ptr()),
+          static_cast<const float*>(c.t[3]->data_ptr()), static_cast<const int*>(table->data_ptr()),
+          static_cast<const int*>(lens->data_ptr()), o.data_ptr(), static_cast<float*>(lse.data_ptr()), ws.data_ptr(), bytes,
+          b, nq, h, c.Hk, c.num_blocks, static_cast<int>(table->size(1)), c.block, max_seqlen, c.d, scale, causal,
+          stream_of(dev));
+    }
     if (st == FA_OK) return pair(std::move(o), std::move(lse));
   } catch (...) {
     PyErr_Clear();  // an exception that came out of Python
