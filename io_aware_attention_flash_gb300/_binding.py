@@ -116,6 +116,12 @@ def native():
                 if not os.path.exists(TORCH_LIB_PATH):
                     raise RuntimeError(
                         f"{TORCH_LIB_PATH} is missing: build it with `python -m io_aware_attention_flash_gb300.build`")
+                from . import build
+
+                if build.torch_built_for() != build.torch_stamp():
+                    raise RuntimeError(
+                        f"{TORCH_LIB_PATH} was built for another PyTorch or Python ({build.torch_built_for() or 'unknown'}; "
+                        f"here {build.torch_stamp()}): rebuild it with `python -m io_aware_attention_flash_gb300.build`")
                 spec = importlib.util.spec_from_file_location("_fa_torch", TORCH_LIB_PATH)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)

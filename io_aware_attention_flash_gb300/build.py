@@ -4,8 +4,9 @@ Each translation unit is compiled in its own nvcc process (in parallel), then
 linked into ``io_aware_attention_flash_gb300/lib/libfa_gb300.so`` with the
 CUDA runtime linked statically.  Beside it, the host compiler builds
 ``lib/_fa_torch.so``, the calls from PyTorch that do without the interpreter
-(linked against libfa_gb300.so next to it).  A rebuild happens only when a
-source or header is newer than the libraries.
+(linked against libfa_gb300.so next to it); ``lib/_fa_torch.txt`` names the
+PyTorch and Python it is for.  A rebuild happens only when a source or header is
+newer than the libraries, or PyTorch or Python is another one.
 
     python -m io_aware_attention_flash_gb300.build [--force] [--verbose]
 """
@@ -26,6 +27,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa_gb300.so")
 TORCH_LIB_PATH = os.path.join(LIB_DIR, "_fa_torch.so")
+TORCH_STAMP_PATH = os.path.join(LIB_DIR, "_fa_torch.txt")
 TORCH_SOURCE = "fa_torch.cpp"
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_decode.cu", "fa_cache8.cu", "fa_microbench.cu"]
@@ -49,8 +51,28 @@ def _inputs():
     return files
 
 
+def torch_stamp() -> str:
+    """What _fa_torch.so depends on beside the sources: the layout of PyTorch's
+    C++ objects, the compiler's ABI and the Python."""
+    import sysconfig
+
+    import torch
+
+    return (f"torch {torch.__version__} {torch.version.git_version} cxx11abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)} "
+            f"python {sysconfig.get_config_var('SOABI')}")
+
+
+def torch_built_for() -> str:
+    """The stamp of the _fa_torch.so that is there; empty if it has none."""
+    try:
+        with open(TORCH_STAMP_PATH) as f:
+            return f.read()
+    except FileNotFoundError:
+        return ""
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(TORCH_LIB_PATH) or torch_built_for() != torch_stamp():
         return False
     t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(TORCH_LIB_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -98,7 +120,12 @@ def _link_torch(obj: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    if os.path.exists(TORCH_STAMP_PATH):  # at no time beside a library that it is not of
+        os.remove(TORCH_STAMP_PATH)
     os.replace(tmp, TORCH_LIB_PATH)
+    with open(TORCH_STAMP_PATH + ".tmp", "w") as f:
+        f.write(torch_stamp())
+    os.replace(TORCH_STAMP_PATH + ".tmp", TORCH_STAMP_PATH)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
