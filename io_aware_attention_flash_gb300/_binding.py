@@ -12,6 +12,7 @@ import ctypes
 import importlib.util
 import os
 import threading
+import warnings
 
 import torch
 
@@ -103,25 +104,43 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+class _NoNative:
+    """Stands for the compiled calls where they cannot be loaded: hands every call
+    to the helper's Python path, which launches the same kernels."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    forward_grouped = backward_grouped = flash_attention_grouped = cache8_store = decode_cache8 = _none
+
+
 def native():
     """The compiled calls of the grouped-head and cache entry points (once
     loaded).  Each does what the Python helper of its name does and returns
     None where anything is not in order; the helper then takes the Python path,
-    which says what.  Raises if the library has not been built."""
+    which says what.  Where they are not built, or for another PyTorch, the
+    Python paths take every call (and more host time: a warning says so).  Raises
+    if libfa_gb300.so has not been built."""
     global _native
     if _native is None:
         lib()
         with _lock:
             if _native is None:
-                if not os.path.exists(TORCH_LIB_PATH):
-                    raise RuntimeError(
-                        f"{TORCH_LIB_PATH} is missing: build it with `python -m io_aware_attention_flash_gb300.build`")
                 from . import build
 
+                rebuild = ("calls take more host time until it is rebuilt with "
+                           "`python -m io_aware_attention_flash_gb300.build`")
+                if not os.path.exists(TORCH_LIB_PATH):
+                    warnings.warn(f"{TORCH_LIB_PATH} is missing: {rebuild}", RuntimeWarning, stacklevel=3)
+                    _native = _NoNative()
+                    return _native
                 if build.torch_built_for() != build.torch_stamp():
-                    raise RuntimeError(
-                        f"{TORCH_LIB_PATH} was built for another PyTorch or Python ({build.torch_built_for() or 'unknown'}; "
-                        f"here {build.torch_stamp()}): rebuild it with `python -m io_aware_attention_flash_gb300.build`")
+                    warnings.warn(f"{TORCH_LIB_PATH} was built for another PyTorch or Python "
+                                  f"({build.torch_built_for() or 'unknown'}; here {build.torch_stamp()}): {rebuild}",
+                                  RuntimeWarning, stacklevel=3)
+                    _native = _NoNative()
+                    return _native
                 spec = importlib.util.spec_from_file_location("_fa_torch", TORCH_LIB_PATH)
                 module = importlib.util.module_from_spec(spec)
                 spec.loader.exec_module(module)
