@@ -37,10 +37,10 @@ constexpr int kScaleFloor = -64;  // exponent of the smallest scale
 __device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
 
 // Scale exponent of a maximum magnitude given as bf16 bits: amax = 1.m · 2^E is
-// at most 448 · 2^e = 1.75 · 2^(8+e).
-__device__ __forceinline__ int scale_exponent(uint32_t amax_bits) {
+// at most 448 · 2^e = 1.75 · 2^(8+e); not below `least`.
+__device__ __forceinline__ int scale_exponent(uint32_t amax_bits, int least) {
   const int biased = static_cast<int>(amax_bits >> 7), mant = static_cast<int>(amax_bits & 127u);
-  return max(biased - 127 - 8 + (mant > 96 ? 1 : 0), kScaleFloor);
+  return max(biased - 127 - 8 + (mant > 96 ? 1 : 0), least);
 }
 
 // Floats to e4m3 codes, the first in the lowest byte (nearest even,
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) fa_cache8_store_kernel(const Ca
     for (int w = 0; w < TG / 32; ++w) amax = max(amax, warp_max[w0 + w]);
   }
   if (!live) return;
-  const float s = fmaxf(exp2_int(scale_exponent(amax)), held);
+  const float s = fmaxf(exp2_int(scale_exponent(amax, kScaleFloor)), held);
   // 1 / s of a power of two, by its exponent
   const float inv = exp2_int(127 - static_cast<int>((__float_as_uint(s) >> 23) & 255u));
   const bool again = s > held;
@@ -747,8 +747,9 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
 #pragma unroll
           for (int u = 0; u < E / 2; ++u) top = __vmaxu2(top, raw[j][u] & 0x7fff7fffu);
           const uint32_t mx = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-          // smallest power of two s with max <= 448 s (within the exponents whose inverse is a float)
-          const int e2 = min(max(scale_exponent(mx), -100), 100);
+          // smallest power of two s with max <= 448 s, for any finite row: 2^120 at
+          // most, at least 2^-126 (fp32's smallest that is not subnormal)
+          const int e2 = min(scale_exponent(mx, -126), 120);
           const float inv = exp2_int(-e2);
           float x[E], h[E];
 #pragma unroll

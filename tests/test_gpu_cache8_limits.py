@@ -42,3 +42,43 @@ def test_lengths_up_to_the_largest_int(d, block, n):
     assert abs(f64(lse)[0, 0, 0] - np.log(p.sum())) <= 4e-3
     p /= p.sum()
     assert (np.abs(f64(o)[0, 0, 0] - p @ v) <= (2.0 ** -7 + 7e-3) * (p @ np.abs(v))).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_exp,k_exp", [(110, -60), (125, -70), (-100, 60), (-115, 90), (-60, 30), (0, 0)])
+def test_queries_of_any_size(q_exp, k_exp, d):
+    """Queries up to bf16's largest and down to its smallest normal numbers, over
+    keys (by their scales) and a softmax scale that make the scores of order 1.  A
+    query element is off by at most 2^-18 of its row's largest, so a score by
+    e = scale 2^-18 max|q| max_j Σ|k_j|, the LSE by e and P by 2e of itself; the
+    rest as everywhere: 2^-7 Σ P |v| for O, 1e-4 for the LSE."""
+    fa = require_gpu()
+    H, Hk, block, n = 8, 2, 16, 300
+    pages = -(-n // block)
+    g = torch.Generator(device="cuda").manual_seed(q_exp + 200)
+    cache = fa.cache8_alloc(pages, Hk, block, d)
+    cache.k.copy_(torch.randn(pages, Hk, block, d, device="cuda", generator=g))
+    cache.v.copy_(torch.randn(pages, Hk, block, d, device="cuda", generator=g))
+    cache.k_scale.fill_(2.0 ** k_exp)
+    table = torch.arange(pages, device="cuda", dtype=torch.int32)[None]
+    # (2^q_exp in two steps: neither factor leaves fp32)
+    q = (torch.randn(1, 2, H, d, device="cuda", generator=g) * 2.0 ** (q_exp // 2) * 2.0 ** (q_exp - q_exp // 2)).bfloat16()
+    scale = d ** -0.5 * 2.0 ** -(q_exp + k_exp)
+    o, lse = fa.attention_decode_cache8(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n, True, scale)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    Q = f64(q)
+    assert np.isfinite(Q).all() and np.abs(Q).max() > 2.0 ** q_exp
+    for h in range(H):
+        k, v = ((f64(c)[:, h // (H // Hk)] * f64(s)[:, h // (H // Hk), None, None]).reshape(-1, d)[:n]
+                for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+        for i in range(2):
+            seen = slice(0, n - 1 + i)
+            s = scale * (k[seen] @ Q[0, i, h])
+            e = scale * 2.0 ** -18 * np.abs(Q[0, i, h]).max() * np.abs(k).sum(1).max()
+            assert e < 1e-3
+            p = np.exp(s - s.max())
+            assert abs(f64(lse)[0, h, i] - (s.max() + np.log(p.sum()))) <= 1e-4 + e
+            p /= p.sum()
+            bound = p @ np.abs(v[seen])
+            assert (np.abs(f64(o)[0, i, h] - p @ v[seen]) <= (2.0 ** -7 + 2 * e) * bound).all()
