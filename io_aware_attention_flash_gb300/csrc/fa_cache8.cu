@@ -248,6 +248,11 @@ cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
 // 0-63) and once for the second ones (lanes 64-127), and the two O are added
 // once for each item.
 constexpr int kRowsMax = 16;
+// V's scales further apart than 2^kWide within an item, or above it, take the sum l
+// by another way.  Up to there a factor of the usual one leaves fp32 (2^-126) only
+// for keys whose weight is below 2^(kWide - 118) of the largest, 2^31 of which are
+// nothing.  (A page of zeros, scale 2^-64, beside values up to 28 does not get there.)
+constexpr float kWide = 60.f;
 constexpr int kScanSeqs = 512;  // up to here a warp finds a tile's sequence by itself (16 lengths a lane)
 
 __device__ __forceinline__ int run_start(long long c, int total, int ctas) { return static_cast<int>(c * total / ctas); }
@@ -375,10 +380,10 @@ struct Dec8Cfg {
   static constexpr int OFF_Q = OFF_V + NST * TILE_BYTES;
   static constexpr int OFF_P = OFF_Q + Q_BYTES;
   static constexpr int OFF_HALF = OFF_P;                     // between items: [RP][64] O of the second tokens (d = 64)
-  static constexpr int OFF_SC = OFF_P + 2 * P_BYTES;         // (two P buffers) [NST][pages][4]: K's scale, 1 / V's, its log2
+  static constexpr int OFF_SC = OFF_P + 2 * P_BYTES;         // (two P buffers) [NST][pages][4]: K's scale, 1 / V's, its log2, the tile's largest
   static constexpr int OFF_QS = OFF_SC + NST * MAX_PPT * 16;    // [RP] score factor of each row
   static constexpr int OFF_XCH = OFF_QS + kRowsMax * 4;      // [2][4 warps][RP]
-  static constexpr int STAT_WARP = 3 * RW < 4 ? 4 : 3 * RW;  // reference, alpha, weight of each row
+  static constexpr int STAT_WARP = 4 * RW;                   // reference, alpha, weight, step of the running reference of each row
   static constexpr int OFF_STAT = OFF_XCH + 2 * 4 * kRowsMax * 4;  // [2 tiles][NCW][STAT_WARP]
   static constexpr int OFF_SCAN = OFF_STAT + 2 * NCW * STAT_WARP * 4;  // [warps] sums of tiles
   static constexpr int OFF_BAR = (OFF_SCAN + NUM_WARPS * 4 + 7) / 8 * 8;
@@ -627,12 +632,12 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
           load_scales(near);
         }
         const float ks = __shfl_sync(0xffffffffu, cur.ks, from & 31), vs = __shfl_sync(0xffffffffu, cur.vs, from & 31);
-        if (lane < ppt) {
-          // V's scale by its exponent, a power of two; 1 for a page of zeros and for none
-          const int ve = vs > 0.f ? static_cast<int>(__float_as_uint(vs) >> 23) - 127 : 0;
+        // V's scale by its exponent, a power of two; 1 for a page of zeros and for none
+        const int ve = lane < n_pages && vs > 0.f ? static_cast<int>(__float_as_uint(vs) >> 23) - 127 : 0;
+        const float ve_max = warp_max(lane < n_pages ? static_cast<float>(ve) : -CUDART_INF_F);
+        if (lane < ppt)
           reinterpret_cast<float4*>(smem + C::OFF_SC)[st * C::MAX_PPT + lane] =
-              lane < n_pages ? make_float4(ks, exp2_int(-ve), static_cast<float>(ve), 0.f) : make_float4(0.f, 1.f, 0.f, 0.f);
-        }
+              make_float4(lane < n_pages ? ks : 0.f, exp2_int(-ve), static_cast<float>(ve), ve_max);
         mbar_arrive(bar(C::B_FULL + st));
       }
       cur = near;
@@ -784,6 +789,7 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
 #pragma unroll
       for (int q = 0; q < RW; ++q) lsum[q] = ov[q] = 0.f;
       float m = -CUDART_INF_F;  // running reference of row my_row
+      float ve_hi = -CUDART_INF_F, ve_lo = 0.f;  // log2 of V's scales: the largest; the least of this thread's tokens, and of 1
       constexpr int NL = RP == 1 ? 8 : 2 * RW;  // columns of the warpgroup's rows
       // O of tile u (its statistics are still in their buffer) into the running one.
       auto add_o = [&](int u) {
@@ -815,7 +821,8 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
       const int kt_mask = max(0, w.len - (p.causal ? p.Nq - 1 : 0)) / TOK;
       for (int kt = w.k0; kt < w.k1; ++kt, ++t) {
         wait(C::B_FULL + st, st_phase);
-        // K's scale, 1 / V's scale and its log2 of the page of this thread's tokens
+        // K's scale, 1 / V's scale and its log2 of the page of this thread's tokens (and the
+        // largest such log2 of the tile's pages)
         const float4 sc = reinterpret_cast<const float4*>(smem + C::OFF_SC)[st * C::MAX_PPT + ((NP * r) >> p.block_shift)];
         const float ks = sc.x, inv_vs = sc.y, vef = sc.z;
         wait(C::B_SFULL + cache8::s_full(t).index, cache8::s_full(t).parity);
@@ -869,17 +876,38 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
             stat[q] = none ? 0.f : mt - 8.f;
             stat[RW + q] = m == -CUDART_INF_F ? 0.f : ex2_approx(m - m_new);
             stat[2 * RW + q] = none ? 0.f : ex2_approx(mt - m_new - 8.f);
+            stat[3 * RW + q] = m == -CUDART_INF_F ? -CUDART_INF_F : m - m_new;
           }
           m = m_new;
           __syncwarp();
         }
         {
+          ve_hi = fmaxf(ve_hi, sc.w);
+          ve_lo = fminf(ve_lo, vef);
+          const bool wide = __any_sync(0xffffffffu, ve_hi - ve_lo > kWide);
+          if (wide) {
+            // V's scales so far apart that a factor of a key's share of l, 2^(s - m),
+            // would leave fp32 though the share does not: as squares of its root
+#pragma unroll
+            for (int q = 0; q < RW; ++q) {
+              const float to = __shfl_sync(0xffffffffu, m, q * LPR), root = ex2_approx(0.5f * stat[3 * RW + q]);
+              lsum[q] = lsum[q] * root * root;
+#pragma unroll
+              for (int pos = 0; pos < NP; ++pos) {
+                const float h = y[pos][q] == -CUDART_INF_F ? 0.f : ex2_approx(0.5f * (y[pos][q] - vef - to));
+                lsum[q] = fmaf(h, h, lsum[q]);
+              }
+            }
+          }
+          const float inv_l = wide ? 0.f : inv_vs;
           float ref[RW], alpha[RW], wt[RW];
           load_row<RW>(stat, ref);
           load_row<RW>(stat + RW, alpha);
           load_row<RW>(stat + 2 * RW, wt);
+          if (!wide) {
 #pragma unroll
-          for (int q = 0; q < RW; ++q) lsum[q] *= alpha[q];
+            for (int q = 0; q < RW; ++q) lsum[q] *= alpha[q];
+          }
 #pragma unroll
           for (int pos = 0; pos < NP; ++pos) {
             uint32_t hi[(RW + 3) / 4], lo[(RW + 3) / 4];
@@ -890,12 +918,12 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
                   f2_unpack(fsub2(f2_pack(x[q], x[q + 1]), f2_pack(ref[q], ref[q + 1])), x[q], x[q + 1]);
                   x[q] = ex2_approx(x[q]);
                   x[q + 1] = ex2_approx(x[q + 1]);
-                  const uint64_t c = fmul2(f2_pack(inv_vs, inv_vs), f2_pack(wt[q], wt[q + 1]));
+                  const uint64_t c = fmul2(f2_pack(inv_l, inv_l), f2_pack(wt[q], wt[q + 1]));
                   f2_unpack(ffma2(f2_pack(x[q], x[q + 1]), c, f2_pack(lsum[q], lsum[q + 1])), lsum[q], lsum[q + 1]);
                 },
                 [&](int q) {
                   x[q] = ex2_approx(x[q] - ref[q]);
-                  lsum[q] = fmaf(x[q], inv_vs * wt[q], lsum[q]);
+                  lsum[q] = fmaf(x[q], inv_l * wt[q], lsum[q]);
                 });
             if constexpr (RW % 4 == 0) {
 #pragma unroll
@@ -1058,8 +1086,9 @@ __global__ void __launch_bounds__(128) fa_cache8_merge_kernel(const Cache8Decode
       float w = 0.f;  // of partial cb + lane
       if (cb + lane <= c1) {
         const float2 ml = *reinterpret_cast<const float2*>(p.ml_part + slot(cb + lane) * 2);
-        w = ml.x == -CUDART_INF_F ? 0.f : ex2_approx(ml.x - mmax);
-        l = fmaf(w, ml.y, l);
+        const float root = ml.x == -CUDART_INF_F ? 0.f : ex2_approx(0.5f * (ml.x - mmax));
+        w = root * root;
+        l = fmaf(root, root * ml.y, l);  // (w may be below fp32's range where w · l is not)
       }
       const int n = min(32, c1 - cb + 1);
 #pragma unroll 8

@@ -82,3 +82,45 @@ def test_queries_of_any_size(q_exp, k_exp, d):
             p /= p.sum()
             bound = p @ np.abs(v[seen])
             assert (np.abs(f64(o)[0, i, h] - p @ v[seen]) <= (2.0 ** -7 + 2 * e) * bound).all()
+
+
+@pytest.mark.parametrize("spread", [0, 40, 90, 130, 184])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [200, 700, 5000])
+def test_values_of_very_different_sizes(n, d, spread):
+    """V's scales up to the 2^184 apart that a store can write (pages of zeros beside
+    bf16's largest values) from page to page, within tiles, from tile to
+    tile and from CTA to CTA.  All values are positive, so that O is Σ P |v| and a
+    relative bound on it can be held: 2^-7 of it, and what the two e4m3 terms of
+    P s_V lose where P s_V is below its tile's largest, M: at most 2^-18 M a key,
+    times the key's code.  A dropped page's weight, or the folding of a scale left
+    out, changes every element by far more: the bound is asserted to be a small
+    part of O."""
+    fa = require_gpu()
+    H, Hk, block = 6, 2, 16
+    pages = -(-n // block)
+    g = torch.Generator(device="cuda").manual_seed(n + spread)
+    cache = fa.cache8_alloc(pages, Hk, block, d)
+    cache.k.copy_(torch.randn(pages, Hk, block, d, device="cuda", generator=g))
+    cache.v.copy_(64.0 + 128.0 * torch.rand(pages, Hk, block, d, device="cuda", generator=g))
+    at = torch.arange(pages * Hk, device="cuda").reshape(pages, Hk)
+    cache.v_scale.copy_(2.0 ** (torch.floor(spread * ((at * 7) % 5) / 4.0) - min(spread // 2, 64)))
+    table = torch.arange(pages, device="cuda", dtype=torch.int32)[None]
+    q = torch.randn(1, 1, H, d, device="cuda", generator=g).bfloat16()
+    o, lse = fa.attention_decode_cache8(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), n)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    tile = 128 * 128 // d
+    for h in range(H):
+        hk = h // (H // Hk)
+        k, codes = (f64(c)[:, hk].reshape(-1, d)[:n] for c in (cache.k, cache.v))
+        sv = f64(cache.v_scale)[:, hk].repeat(block)[:n]
+        s = d ** -0.5 * k @ f64(q)[0, 0, h]
+        p = np.exp(s - s.max())
+        assert abs(f64(lse)[0, h, 0] - (s.max() + np.log(p.sum()))) <= 1e-4
+        p = p / p.sum() * sv
+        want = p @ codes
+        lost = sum(2.0 ** -18 * p[a:a + tile].max() * codes[a:a + tile].sum(0) for a in range(0, n, tile))
+        bound = 2.0 ** -7 * want + lost
+        assert (bound <= 2.0 ** -5 * want).all()
+        assert (np.abs(f64(o)[0, 0, h] - want) <= bound).all()
