@@ -214,14 +214,15 @@ class _FlashAttentionGrouped(torch.autograd.Function):
         checked = _binding._grouped(q, k, v, cu_seqlens)
         o, lse = _forward_grouped(checked, q, k, v, cu_seqlens, max_seqlen, causal, scale)
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens)
-        ctx.args = checked, max_seqlen, causal, scale
+        ctx.args = max_seqlen, causal, scale
         return o
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, do):
         q, k, v, o, lse, cu_seqlens = ctx.saved_tensors
-        checked, max_seqlen, causal, scale = ctx.args
+        max_seqlen, causal, scale = ctx.args
+        checked = _binding._grouped(q, k, v, cu_seqlens)  # saved tensors may come back with other strides
         dq, dk, dv = _backward_grouped(checked, q, k, v, o, do.contiguous(), lse, cu_seqlens, max_seqlen, causal, scale, None)
         return dq, dk, dv, None, None, None, None
 

@@ -206,7 +206,10 @@ struct FlashAttentionGrouped : torch::autograd::Function<FlashAttentionGrouped> 
                                                  torch::autograd::variable_list grads) {
     const auto s = ctx->get_saved_variables();
     Grouped g;
-    TORCH_CHECK(check_grouped(s[0], s[1], s[2], s[5], &g), "flash_attention_grouped: saved tensors out of order");
+    // (what was saved comes back through hooks that the user may have set)
+    TORCH_CHECK(check_grouped(s[0], s[1], s[2], s[5], &g) && dense(s[3], at::kBFloat16, {g.T, g.H, g.d}, g.dev) &&
+                    dense(s[4], at::kFloat, {g.H, g.T}, g.dev),
+                "flash_attention_grouped: saved tensors out of order");
     g.max_seqlen = static_cast<int>(ctx->saved_data["max_seqlen"].toInt());
     g.causal = ctx->saved_data["causal"].toBool();
     g.scale = static_cast<float>(ctx->saved_data["scale"].toDouble());
