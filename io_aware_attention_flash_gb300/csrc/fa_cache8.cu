@@ -253,7 +253,15 @@ constexpr int kRowsMax = 16;
 // for keys whose weight is below 2^(kWide - 118) of the largest, 2^31 of which are
 // nothing.  (A page of zeros, scale 2^-64, beside values up to 28 does not get there.)
 constexpr float kWide = 60.f;
-constexpr int kScanSeqs = 512;  // up to here a warp finds a tile's sequence by itself (16 lengths a lane)
+// Up to here every warp finds its CTA's first tile by itself, from all lengths, while
+// warp 0 allocates: one barrier before the roles part instead of two, and the merge
+// finds its place while the attention runs.  With more sequences the lengths are
+// summed by all warps together and CTA 0 writes each one's first tile down.
+// Measured in a graph, 32 query heads on 8, d = 128, us by itself / together: 1
+// sequence of 40 tokens 6.2 / 6.6, 16 7.1 / 7.2, 64 11.1 / 10.7, 128 17.0 / 16.5, 512
+// 56 / 48, 4096 630 / 371; of 1000 tokens 8.5 / 8.7, 13.6 / 13.9, 32.4 / 32.7, 51.7 /
+// 51.8, 177 / 170, 1532 / 1271.
+constexpr int kScanSeqs = 64;
 
 __device__ __forceinline__ int run_start(long long c, int total, int ctas) { return static_cast<int>(c * total / ctas); }
 // The CTA whose run holds tile t.
@@ -517,9 +525,6 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
   // ---- this CTA's place: all tiles counted, then the sequence of its first one
   const int per = p.Hk * p.row_groups;
   int total = 0;
-  // Few sequences: every warp finds the place by itself while warp 0 allocates,
-  // with one barrier before the roles part instead of two (one sequence of 777
-  // tokens, 32 query heads on 8, d = 128: 13.0 -> 10.7 us a call).
   if (p.B <= kScanSeqs) {
     for (int b = lane; b < p.B; b += 32) total += seq_tiles<D>(p, b);
     total = __reduce_add_sync(0xffffffffu, total);

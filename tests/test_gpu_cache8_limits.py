@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from tests.gpu_util import assert_no_device_error, f64, gpu, require_gpu
+from tests.test_gpu_cache8 import check_attend
 
 pytestmark = gpu
 
@@ -124,3 +125,12 @@ def test_values_of_very_different_sizes(n, d, spread):
         bound = 2.0 ** -7 * want + lost
         assert (bound <= 2.0 ** -5 * want).all()
         assert (np.abs(f64(o)[0, 0, h] - want) <= bound).all()
+
+
+@pytest.mark.parametrize("B", [63, 64, 65, 128, 129])
+def test_batches_on_both_sides_of_the_scan(B):
+    """Few sequences are found by every warp by itself, more by all together: ragged
+    lengths, empty sequences among them, first, last and in between."""
+    fa = require_gpu()
+    check_attend(fa, 4, 2, 64, 16, [0] + [(i * 53) % 300 for i in range(1, B - 1)] + [0], 1, True, seed=B)
+    check_attend(fa, 2, 1, 128, 32, [(i * 29) % 400 for i in range(B)], 2, True, seed=B + 1)
