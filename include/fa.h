@@ -74,7 +74,7 @@ enum {
   FA_ERR_CUDA = 6,          /* a CUDA runtime/driver call or launch failed */
   FA_ERR_TIMEOUT = 7,       /* a kernel's bounded wait expired (device side) */
   FA_ERR_WORKSPACE = 8,     /* workspace missing or smaller than required */
-  FA_ERR_SCALE = 9,         /* scale not finite */
+  FA_ERR_SCALE = 9,         /* scale not finite, or not positive where that is asked for */
   FA_ERR_NOT_DEVICE = 10,   /* q is not device memory (its device is the one launched on) */
   FA_ERR_PAGE = 12,         /* a page table entry, length or start position out of range (device side) */
   FA_ERR_SCRATCH_LIMIT = 11 /* fa_bwd_noalloc: problem needs more than FA_NOALLOC_SCRATCH_BYTES */
@@ -246,12 +246,16 @@ FA_API fa_status fa_cache8_store(const void* k, const void* v, void* k_codes, vo
  *            a slot without a sequence (o = 0, lse = -infinity there)
  *   max_seqlen  at least every length
  * causal as in fa_fwd_decode: query i sees keys j <= seqlens[b] − Nq + i.
- * Scores and sums are fp32; each query and each probability enters its product
- * with the codes as the sum of two e4m3 terms, off by at most 2^-18 of the
- * row's largest query element, and by 2^-8 of the probability or 2^-18 of the
- * largest one among its 128 keys.  What cache slots behind a sequence's last
- * token hold does not matter; queries and stored tokens must be finite, and
- * scales powers of two (as fa_cache8_store writes them).  A page index out of range reads as a page of zeros, a length
+ * Scores and sums are fp32, which the scores have to fit.  A query element enters
+ * its product with the codes as the sum of two e4m3 terms, off by at most 2^-17 of
+ * its row's largest (rows below 2^-118: of 2^-118).  A probability P_j enters the
+ * product with V's codes as two such terms of P_j s_j, s_j the V scale of the
+ * key's page, together off by at most 2^-8 of it or by 2^-18 of the largest P s of
+ * the key's tile (128 keys, at d = 64 256), whichever is more: beside values of
+ * larger scale a key's share of O, not its weight in the sum, may lose bits.  What
+ * cache slots behind a sequence's last token hold does not matter; queries and
+ * stored tokens must be finite, and scales powers of two (as fa_cache8_store
+ * writes them).  A page index out of range reads as a page of zeros, a length
  * outside [0, min(max_seqlen, table_cols · block)] as the nearer end of that
  * range, and both are reported by fa_get_device_error as FA_ERR_PAGE.  Results
  * do not depend on the order in which CTAs run.  `workspace`: at least

@@ -535,7 +535,7 @@ FA_API const char* fa_status_string(fa_status status) {
     case FA_ERR_CUDA: return "CUDA runtime or launch failure";
     case FA_ERR_TIMEOUT: return "device wait timed out; outputs invalid";
     case FA_ERR_WORKSPACE: return "workspace missing or too small";
-    case FA_ERR_SCALE: return "scale is not finite";
+    case FA_ERR_SCALE: return "scale is not finite, or not positive where it has to be";
     case FA_ERR_NOT_DEVICE: return "q is not a device pointer";
     case FA_ERR_PAGE: return "page table entry, sequence length or start position out of range; outputs invalid";
     case FA_ERR_SCRATCH_LIMIT: return "problem needs more scratch than the static no-alloc array holds";

@@ -195,3 +195,9 @@ def test_cache8_validation(lib):
     assert dec(codes=FAKE + 1) == 2 and dec(ws_ptr=FAKE + 8) == 2
     assert dec(ws_bytes=ws - 1) == 8
     assert lib.fa_status_string(12)
+
+
+def test_the_scale_error_names_both_of_its_causes(lib):
+    """0 and negative scales are refused with it as well, by the grouped and cache entry points."""
+    text = lib.fa_status_string(9).decode()
+    assert "finite" in text and "positive" in text

@@ -50,8 +50,9 @@ def test_lengths_up_to_the_largest_int(d, block, n):
 def test_queries_of_any_size(q_exp, k_exp, d):
     """Queries up to bf16's largest and down to its smallest normal numbers, over
     keys (by their scales) and a softmax scale that make the scores of order 1.  A
-    query element is off by at most 2^-18 of its row's largest, so a score by
-    e = scale 2^-18 max|q| max_j Σ|k_j|, the LSE by e and P by 2e of itself; the
+    query element is off by at most 2^-17 of its row's largest (half of e4m3's least
+    step, 2^-10, where the largest is at least 224), so a score by
+    e = scale 2^-17 max|q| max_j Σ|k_j|, the LSE by e and P by 2e of itself; the
     rest as everywhere: 2^-7 Σ P |v| for O, 1e-4 for the LSE."""
     fa = require_gpu()
     H, Hk, block, n = 8, 2, 16, 300
@@ -76,7 +77,7 @@ def test_queries_of_any_size(q_exp, k_exp, d):
         for i in range(2):
             seen = slice(0, n - 1 + i)
             s = scale * (k[seen] @ Q[0, i, h])
-            e = scale * 2.0 ** -18 * np.abs(Q[0, i, h]).max() * np.abs(k).sum(1).max()
+            e = scale * 2.0 ** -17 * np.abs(Q[0, i, h]).max() * np.abs(k).sum(1).max()
             assert e < 1e-3
             p = np.exp(s - s.max())
             assert abs(f64(lse)[0, h, i] - (s.max() + np.log(p.sum()))) <= 1e-4 + e
