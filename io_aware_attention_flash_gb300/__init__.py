@@ -138,12 +138,16 @@ def flash_attention(q, k, v, causal: bool = False, scale=None):
 # Each call first goes to its compiled counterpart, which returns None where
 # something is not in order; the Python path then runs or says what is wrong.
 _tracing = torch._C._get_tracing_state
+_dispatch_mode, _PROXY = torch._C._get_dispatch_mode, torch._C._TorchDispatchModeKey.PROXY
 
 
-def _refuse_trace(name: str) -> None:
-    """torch.jit.trace would record the outputs' allocation and not the kernel."""
-    if _tracing() is not None:
-        raise RuntimeError(f"{name} cannot be recorded by torch.jit.trace (flash_attention_grouped can)")
+def _refuse_trace(name: str, recordable: bool = False) -> None:
+    """A recorder of PyTorch's operations (torch.jit.trace; torch.fx's make_fx)
+    would take down the outputs' allocation and not the kernel: refused, but for
+    a call that torch.jit.trace can record as a Python function."""
+    if _dispatch_mode(_PROXY) is not None or _tracing() is not None and not recordable:
+        raise RuntimeError(f"{name} cannot be recorded by torch.jit.trace or make_fx (torch.jit.trace can record "
+                           "flash_attention_grouped)")
 
 
 def _on_stream(stream, t):
@@ -235,6 +239,7 @@ def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool =
     a CUDA graph, run it outside first and let go of that run's graph (its
     outputs and losses): PyTorch cannot capture a backward pass into leaves
     that a graph recorded outside still holds."""
+    _refuse_trace("flash_attention_grouped", recordable=True)
     if _tracing() is None:  # a trace records the Python function as one operation, the compiled one not at all
         o = _binding.native().flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
         if o is not None:

@@ -70,3 +70,22 @@ def test_traced_on_the_gpu():
     a, b = (torch.autograd.grad(o, (q, k, v), do) for o in (got, want))
     assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
     assert rel_fro(f64(a[0]), f64(b[0])) < 2.0 ** -8  # dQ: fp32 sums in another order
+
+
+def test_a_proxy_graph_is_refused(monkeypatch):
+    """torch.fx's make_fx records operations below the autograd function: none of the
+    calls has one to record."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+
+    monkeypatch.setattr(fa._binding, "native", lambda: CompiledCalls())
+    x = torch.randn(5, 4, 64)
+    cu = torch.tensor([0, 5], dtype=torch.int32)
+    cache = fa.Cache8(x, x, x, x)
+    for f in (lambda x: fa.flash_attention_grouped(x, x, x, cu, 5),
+              lambda x: fa.attention_forward_grouped(x, x, x, cu, 5)[0],
+              lambda x: fa.attention_backward_grouped(x, x, x, x, x, x, cu, 5)[0],
+              lambda x: fa.attention_decode_cache8(x, cache, cu, cu, 5)[0],
+              lambda x: fa.cache8_store(x, x, cache, cu, cu, cu, 5) or x):
+        with pytest.raises(RuntimeError, match="make_fx"):
+            make_fx(f)(x)
+    assert (fa.flash_attention_grouped(x, x, x, cu, 5) == 3.0).all()
