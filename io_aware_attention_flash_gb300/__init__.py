@@ -136,7 +136,8 @@ def flash_attention(q, k, v, causal: bool = False, scale=None):
 # Grouped heads over packed batches: H query heads share Hk key/value heads.
 # ---------------------------------------------------------------------------
 # Each call first goes to its compiled counterpart, which returns None where
-# something is not in order; the Python path then runs or says what is wrong.
+# something is not in order, or where PyTorch's operations are being recorded; the
+# Python path then runs or says what is wrong.
 _tracing = torch._C._get_tracing_state
 _dispatch_mode, _PROXY = torch._C._get_dispatch_mode, torch._C._TorchDispatchModeKey.PROXY
 
@@ -165,11 +166,11 @@ def attention_forward_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool
     multiple of Hk; slices of one wider projection are taken as they are).
     Returns (o [T,H,d] bf16, lse [H,T] fp32); rows behind the last sequence
     get o = 0, lse = -inf."""
-    _refuse_trace("attention_forward_grouped")
     if stream is None:
         out = _binding.native().forward_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
         if out is not None:
             return out
+    _refuse_trace("attention_forward_grouped")
     with _on_stream(stream, q):
         return _forward_grouped(_binding._grouped(q, k, v, cu_seqlens), q, k, v, cu_seqlens, max_seqlen, causal, scale)
 
@@ -186,11 +187,11 @@ def attention_backward_grouped(q, k, v, o, dout, lse, cu_seqlens, max_seqlen: in
                                stream=None, workspace=None):
     """Returns (dq [T,H,d], dk, dv [T,Hk,d]), zero in rows behind the last
     sequence.  dk and dv are summed over the query heads that share them."""
-    _refuse_trace("attention_backward_grouped")
     if stream is None and workspace is None:
         out = _binding.native().backward_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale, o, dout, lse)
         if out is not None:
             return out
+    _refuse_trace("attention_backward_grouped")
     with _on_stream(stream, q):
         return _backward_grouped(_binding._grouped(q, k, v, cu_seqlens), q, k, v, o, dout, lse, cu_seqlens, max_seqlen,
                                  causal, scale, workspace)
@@ -239,11 +240,10 @@ def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool =
     a CUDA graph, run it outside first and let go of that run's graph (its
     outputs and losses): PyTorch cannot capture a backward pass into leaves
     that a graph recorded outside still holds."""
+    o = _binding.native().flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
+    if o is not None:
+        return o
     _refuse_trace("flash_attention_grouped", recordable=True)
-    if _tracing() is None:  # a trace records the Python function as one operation, the compiled one not at all
-        o = _binding.native().flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
-        if o is not None:
-            return o
     return _FlashAttentionGrouped.apply(q, k, v, cu_seqlens, max_seqlen, causal, scale)
 
 
@@ -271,9 +271,9 @@ def cache8_store(k, v, cache: Cache8, block_table, cu_seqlens, start, max_new: i
     of k, v [T,Hk,d] become tokens start[b], start[b]+1, ... of sequence b,
     in the pages block_table [B,cols] names (int32, as cu_seqlens [B+1] and
     start [B]); max_new is the largest number of new tokens of a sequence."""
-    _refuse_trace("cache8_store")
     if stream is None and _binding.native().cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new):
         return
+    _refuse_trace("cache8_store")
     fa_cache8_store(k, v, cache, block_table, cu_seqlens, start, max_new, stream)
 
 
@@ -283,11 +283,11 @@ def attention_decode_cache8(q, cache: Cache8, block_table, seqlens, max_seqlen: 
     seqlens int32 [B] cached tokens (the new ones among them; 0 for an empty
     slot), max_seqlen at least every length.  Returns (o [B,Nq,H,d] bf16, lse
     [B,H,Nq] fp32).  causal as in attention_decode."""
-    _refuse_trace("attention_decode_cache8")
     if stream is None and workspace is None:
         out = _binding.native().decode_cache8(q, cache, block_table, seqlens, max_seqlen, causal, scale)
         if out is not None:
             return out
+    _refuse_trace("attention_decode_cache8")
     checked = _binding._decode_cache8(q, cache, block_table, seqlens)
     dev, B, Nq, H, d, _, Hk = checked[:7]
     with _on_stream(stream, q):

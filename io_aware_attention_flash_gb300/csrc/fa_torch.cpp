@@ -6,8 +6,9 @@
 // and ctypes 24 us for a token's attention whose kernels run 7 us.
 //
 // Every function returns its tensors, or None if anything is not as the C ABI
-// wants it (or an allocation or the call failed): the caller then takes the
-// Python path, which names what is wrong.  No C++ exception leaves a function.
+// wants it (or an allocation or the call failed), or while PyTorch's operations
+// are recorded, which none of these is: the caller then takes the Python path,
+// which names what is wrong.  No C++ exception leaves a function.
 // Allocations and launches, which may have to wait (for memory, for room in the
 // launch queue), run without the interpreter lock.
 #include <Python.h>
@@ -18,10 +19,12 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/jit/frontend/tracer.h>
 
 #include "fa.h"
 
@@ -40,6 +43,14 @@ class WithoutLock {
  private:
   PyThreadState* state_;
 };
+
+// torch.jit.trace or make_fx is at work on this thread.
+bool recording() {
+  using c10::impl::TorchDispatchModeKey;
+  using c10::impl::TorchDispatchModeTLS;
+  return torch::jit::tracer::isTracing() ||
+         (TorchDispatchModeTLS::any_modes_set() && TorchDispatchModeTLS::get_mode(TorchDispatchModeKey::PROXY).has_value());
+}
 
 // A tensor argument; nullptr if it is something else.
 const Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
@@ -151,7 +162,7 @@ fa_status backward_grouped(const Grouped& g, const Tensor& q, const Tensor& k, c
 
 // (q, k, v, cu_seqlens, max_seqlen, causal, scale) of `args`.
 bool grouped_args(PyObject* const* args, Py_ssize_t n, const Tensor* (&t)[4], Grouped* g) {
-  if (n != 7) return false;
+  if (n != 7 || recording()) return false;
   for (int i = 0; i < 4; ++i)
     if (!(t[i] = tensor(args[i]))) return false;
   if (!check_grouped(*t[0], *t[1], *t[2], *t[3], g)) return false;
@@ -314,7 +325,7 @@ bool cache_args(PyObject* cache, int dev, Cache* c) {
 // (k, v, cache, block_table, cu_seqlens, start, max_new) -> True
 PyObject* py_cache8_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
-    if (n != 7) Py_RETURN_NONE;
+    if (n != 7 || recording()) Py_RETURN_NONE;
     const Tensor *k = tensor(args[0]), *v = tensor(args[1]), *table = tensor(args[3]), *cu = tensor(args[4]),
                  *start = tensor(args[5]);
     Cache c;
@@ -348,7 +359,7 @@ PyObject* py_cache8_store(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // (q, cache, block_table, seqlens, max_seqlen, causal, scale) -> (o, lse)
 PyObject* py_decode_cache8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
-    if (n != 7) Py_RETURN_NONE;
+    if (n != 7 || recording()) Py_RETURN_NONE;
     const Tensor *q = tensor(args[0]), *table = tensor(args[2]), *lens = tensor(args[3]);
     Cache c;
     int max_seqlen = 0;
