@@ -9,13 +9,17 @@
 // 2^-10 s for values below 2^-6 s) is the only one; a general scale would not
 // be more accurate, since e4m3 keeps the same relative step at any size.
 //
-// Both kernels are bound by DRAM.  Measured on a GB300 (a plain copy moves 6.78
-// TB/s), whole calls: the store of 34,700 tokens of 8 heads, d = 128, 32 us, 6.5
-// TB/s; the attention of one token over 4 x 32768 tokens, 32 heads, d = 128, 164
-// us, 6.5 TB/s, and over 64 sequences of 100 .. 8192 tokens, 32 query over 8
-// heads, 94 us, 5.9 TB/s.  At d = 64 there are twice as many scores to a byte: 5.1
-// TB/s for up to 4 rows; from 16 rows on (4 tokens of 8 heads a group: two row
-// groups, 30 us for 39 MB) the instructions of a tile bound it.
+// The store, and the attention of one new token, are bound by DRAM.  Measured on a
+// GB300 (a plain copy moves 6.78 TB/s), whole calls: the store of 34,700 tokens of 8
+// heads, d = 128, 32 us, 6.5 TB/s; the attention of one token over 4 x 32768 tokens,
+// 32 heads, d = 128, 163 us, 6.6 TB/s, over 64 sequences of 100 .. 8192 tokens, 32
+// query over 8 heads, 94 us, 5.9 TB/s, and over 16 x 16384 tokens of 8 heads, one
+// call behind another, 6.0 TB/s at d = 128 and 4.8 (pages of 16) to 5.3 TB/s (of 64)
+// at d = 64, with 1 or 4 query heads a key/value head.  Several new tokens are held
+// by the latency of a tile's chain (scores, the exchange of the row maxima, P, the
+// product): 4 of 16 sequences, 64 query over 8 heads of 64, take 30 us for 39 MB
+// with the issue slots 47 % busy, the tensor pipe 7 % and DRAM 18 %; each of the two
+// groups of 16 rows walks the key/value head's tiles for itself.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -225,10 +229,10 @@ cudaError_t launch_store(const Cache8StoreParams& p, cudaStream_t s) {
 //   O^T = V^T P^T   A = V tile, MN-major;  B = P,  MN-major
 // with B in e4m3 as well, split into two terms so that nothing is lost to 8
 // bits: q / s_q = hi + lo (s_q a power of two for each row; exact for elements
-// above 2^-10 of the row's largest, else off by 2^-18 of that) and p = hi + lo
-// (off by at most 2^-8 p, as much as rounding to bf16 would be, or by 2^-18 of
-// the tile's largest p where that is more).  The terms are separate columns
-// of B: one MMA reads A once for both.  K's scale (times softmax
+// above 2^-10 of the row's largest, else off by 2^-17 of that) and p = hi + lo, p
+// the probability times its page's V scale (off by at most 2^-8 p, as much as
+// rounding to bf16 would be, or by 2^-18 of the tile's largest p where that is
+// more).  The terms are separate columns of B: one MMA reads A once for both.  K's scale (times softmax
 // scale and s_q) multiplies the scores; V's goes into P: with
 // y = s c + log2 s_V the tile's largest y of each row is the tile's reference,
 // P = 2^(y - y_max) 256, so that a tile of small probabilities (all but the
@@ -580,8 +584,9 @@ __global__ void __launch_bounds__(Dec8Cfg<D, RP>::NUM_THREADS, 2)
     // ---------------------------------------------------------------- TMA
     // The run in units of up to 32 pages (32 / ppt tiles) of one item, a page a
     // lane.  A unit's table entries are read two units ahead and its scales
-    // one unit ahead, so that the copies wait for neither (read where they
-    // were used, the two dependent loads took about 2 us a tile).
+    // one unit ahead, so that the copies wait for neither.  (Against reading both
+    // where a unit begins: pages of 16 tokens, d = 128, of which a unit is 4 tiles,
+    // 2 % faster with up to 16 rows and 4 % with 32; pages of 64 and 128 alike.)
     const int ppt = kTokens<D> >> p.block_shift;  // pages of a tile
     struct Unit {
       int kt0, tiles, len, hk, page;  // first tile, tiles; page of this lane (num_blocks: none, reads as zeros)
