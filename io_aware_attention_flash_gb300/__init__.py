@@ -239,9 +239,9 @@ def flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen: int, causal: bool =
     the last sequence.  Differentiable once.  To capture a training step into
     a CUDA graph, run it outside first and let go of that run's graph (its
     outputs and losses): PyTorch cannot capture a backward pass into leaves
-    that a graph recorded outside still holds.  torch.jit.trace records it as one
-    operation; make_fx is refused, and so are
-    both by the calls that are not autograd functions."""
+    that a graph recorded outside still holds.  torch.jit.trace records it as
+    one operation (make_fx is refused; the calls that are not autograd functions
+    refuse both)."""
     o = _binding.native().flash_attention_grouped(q, k, v, cu_seqlens, max_seqlen, causal, scale)
     if o is not None:
         return o

@@ -64,3 +64,41 @@ def test_a_full_launch_queue_stops_no_other_thread(name):
     assert_no_device_error(fa)
     assert blocked > 0.5, "the queue was meant to fill"
     assert gap[0] < 0.25, f"another thread stood still for {gap[0]:.2f} s of {blocked:.2f} s"
+
+
+@pytest.mark.parametrize("mode", ["anomaly", "dispatch", "hooks", "inference"])
+def test_modes_that_call_python_while_the_lock_is_free(mode):
+    """What PyTorch calls back into Python for during a compiled call takes the
+    interpreter's lock itself: the call's outputs and gradients are the plain ones."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    fa = require_gpu()
+    seen = []
+
+    class Log(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            seen.append(str(func))
+            return func(*args, **(kwargs or {}))
+
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    q, k, v, do = (torch.randn(150, h, 64, device="cuda", generator=gen).bfloat16() for h in (4, 2, 2, 4))
+    cu = torch.tensor([0, 100, 150], dtype=torch.int32, device="cuda")
+
+    def step():
+        leaves = [t.clone().requires_grad_() for t in (q, k, v)]
+        o = fa.flash_attention_grouped(*leaves, cu, 100, causal=True)
+        if torch.is_inference_mode_enabled():
+            return [o]
+        return [o, *torch.autograd.grad(o, leaves[1:], do)]
+
+    want = step()
+    scope = {"anomaly": lambda: torch.autograd.detect_anomaly(check_nan=True), "dispatch": Log,
+             "hooks": lambda: torch.autograd.graph.saved_tensors_hooks(lambda t: seen.append(1) or t.clone(), lambda t: t),
+             "inference": torch.inference_mode}[mode]
+    with scope():
+        got = step()
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    assert mode not in ("dispatch", "hooks") or seen
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
