@@ -270,6 +270,83 @@ FA_API fa_status fa_fwd_decode_cache8(const void* q, const void* k_codes, const 
                                       float scale, int causal, void* stream);
 
 /*
+ * Rotary positions.  Each head's first 2·pairs dimensions are taken in pairs (a,
+ * b), and pair j becomes (a cos t − b sin t, b cos t + a sin t) with t = position ·
+ * frequency_j; the other dimensions pass as they are.
+ *   pairs        a multiple of 8, 2·pairs <= d
+ *   interleaved  0: pair j is dimensions j and j + pairs; otherwise 2j and 2j + 1
+ *   turns        device uint64 [pairs]: each frequency (radians a position) as a
+ *                fraction of a turn, frequency / 2π · 2^64 modulo 2^64, rounded
+ *   axes, axis   a token's number of positions (1 .. pairs: time, height, width),
+ *                and device int32 [pairs]: the one that each pair is turned by
+ *                (may be NULL with one axis; entries outside [0, axes) count as the
+ *                nearer end)
+ *   positions    device int32 [axes, total]; any value, negative ones too
+ * The angle is formed exactly (position · turns modulo 2^64) and its sine and cosine
+ * in fp32, as is the turn; results are rounded once.  A pair that holds an infinity
+ * or NaN follows the arithmetic of the formula.
+ *
+ * fa_rotary turns the rows of q [total, H, d] and k [total, Hk, d] (bf16, rows ldq
+ * and ldk elements apart as in fa_fwd_grouped) into q_out, k_out (contiguous, not
+ * overlapping the inputs).  inverse != 0 turns back, by −t: the inverse, and the
+ * gradient of the turn.
+ */
+FA_API fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                           const uint64_t* turns, const int* axis, int total, int H, int Hk, int d, int pairs, int axes,
+                           int interleaved, int inverse, long long ldq, long long ldk, void* stream);
+
+/*
+ * fa_cache8_store with the positions on the way: the new tokens' keys are turned as
+ * in fa_rotary and stored (in fp32 up to their one rounding, to e4m3), the values
+ * are stored as they are, and the queries q [total, H, d] turned into q_out (bf16,
+ * contiguous).  Arguments, pages and errors as fa_cache8_store; in addition
+ *   positions   device int32 [axes, total], or NULL: a token's place in its
+ *               sequence, start[b] + i, on every axis
+ *   zero_tail   rows of q_out behind the last sequence: 0 leaves them as they were,
+ *               otherwise they become 0
+ * Queries are turned whether or not their token could be stored.
+ */
+FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void* v, void* q_out, void* k_codes,
+                                        void* v_codes, float* k_scale, float* v_scale, const int* block_table,
+                                        const int* cu_seqlens, const int* start, const int* positions,
+                                        const uint64_t* turns, const int* axis, int B, int max_new, int total,
+                                        int num_blocks, int table_cols, int H, int Hk, int block, int d, int pairs,
+                                        int axes, int interleaved, long long ldq, long long ldk, long long ldv,
+                                        int zero_tail, void* stream);
+
+/*
+ * Attention of a chunk of new tokens over the cache: any number of them a sequence,
+ * a different one for each (a prompt's next piece beside another sequence's single
+ * token), H query heads over Hk key/value heads (query head h reads h / (H / Hk)).
+ *   q, o        bf16 [total, H, d] (rows of q ldq elements apart as in
+ *               fa_fwd_grouped);  lse fp32 [H, total]
+ *   cu_seqlens  device int32 [B + 1], non-decreasing, within [0, total]: sequence b's
+ *               new tokens are rows cu_seqlens[b] .. cu_seqlens[b+1]−1
+ *   seqlens     device int32 [B]: cached tokens, the new ones the last of them
+ *   max_new     at least every number of new tokens (rows past it are not computed,
+ *               their results unspecified);  max_seqlen  at least every length
+ * causal != 0: new token i of n sees the keys j <= seqlens[b] − n + i; otherwise all.
+ * A row that sees no key gets o = 0, lse = −infinity.  zero_tail as in
+ * fa_fwd_grouped.  Keys and values are code · scale exactly; products, sums and
+ * rounding of the probabilities (to bf16) are those of fa_fwd_grouped.  What slots
+ * behind a sequence's last token hold does not matter; queries and stored tokens
+ * must be finite (a stored NaN reads as ±480 scales), scales powers of two.  A page
+ * index out of range reads as a page of zeros, a length outside [0, min(max_seqlen,
+ * table_cols · block)] as the nearer end of that range, and both are reported by
+ * fa_get_device_error as FA_ERR_PAGE.  Results do not depend on the order in which
+ * CTAs run.  `workspace`: at least fa_chunk_cache8_workspace_bytes() bytes (0 for
+ * arguments that the call rejects), contents ignored; calls that may overlap need
+ * one each.
+ */
+FA_API size_t fa_chunk_cache8_workspace_bytes(int B, int max_new, int total, int H, int Hk, int max_seqlen, int d);
+FA_API fa_status fa_fwd_chunk_cache8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                                     const float* v_scale, const int* block_table, const int* cu_seqlens,
+                                     const int* seqlens, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                     int B, int max_new, int total, int H, int Hk, int num_blocks, int table_cols,
+                                     int block, int max_seqlen, int d, long long ldq, float scale, int causal,
+                                     int zero_tail, void* stream);
+
+/*
  * Synchronises `stream`, then reads and clears the error word of the device
  * the stream belongs to (NULL, the legacy default stream: the current
  * device); the calling thread's current device is left as it was.  Returns

@@ -13,6 +13,8 @@ module allocates outputs and workspace and calls the binding.
 from __future__ import annotations
 
 import contextlib
+import math
+from fractions import Fraction
 from typing import NamedTuple
 
 import torch
@@ -29,13 +31,17 @@ from ._binding import (  # noqa: F401  (C-ABI names)
     fa_bwd_varlen_workspace_bytes,
     fa_bwd_workspace_bytes,
     fa_cache8_store,
+    fa_cache8_store_rotary,
+    fa_chunk_cache8_workspace_bytes,
     fa_cta_order,
     fa_decode_cache8_workspace_bytes,
     fa_fwd,
+    fa_fwd_chunk_cache8,
     fa_fwd_decode_cache8,
     fa_fwd_grouped,
     fa_fwd_varlen,
     fa_get_device_error,
+    fa_rotary,
     fa_selftest_wait_timeout,
     fa_set_kernel_events,
 )
@@ -48,6 +54,8 @@ __all__ = [
     "attention_forward_grouped", "attention_backward_grouped", "flash_attention_grouped", "fa_fwd_grouped",
     "fa_bwd_grouped", "fa_bwd_grouped_workspace_bytes", "Cache8", "cache8_alloc", "cache8_store",
     "attention_decode_cache8", "fa_cache8_store", "fa_fwd_decode_cache8", "fa_decode_cache8_workspace_bytes",
+    "Rotary", "rotary_plan", "rotary_forward", "rotary_backward", "rotary_embedding", "fa_rotary", "cache8_store_rotary",
+    "fa_cache8_store_rotary", "attention_chunk_cache8", "fa_fwd_chunk_cache8", "fa_chunk_cache8_workspace_bytes",
 ]
 
 
@@ -301,3 +309,134 @@ def attention_decode_cache8(q, cache: Cache8, block_table, seqlens, max_seqlen: 
         _binding._launch_decode_cache8(checked, q, cache, block_table, seqlens, o, lse, workspace,
                                        _binding._nbytes(workspace, dev), max_seqlen, causal, scale, None)
     return o, lse
+
+
+def attention_chunk_cache8(q, cache: Cache8, block_table, cu_seqlens, seqlens, max_new: int, max_seqlen: int,
+                           causal: bool = False, scale=None, stream=None, workspace=None):
+    """Attention of a chunk of new tokens over the 8-bit paged cache: rows
+    cu_seqlens[b] .. cu_seqlens[b+1]-1 of q [T,H,d] are sequence b's newest
+    tokens, any number of them (a prompt's next piece, a single token), seqlens
+    int32 [B] its cached tokens with the new ones; max_new and max_seqlen at
+    least every number of new and of cached tokens.  causal: new token i of n
+    sees keys j <= seqlens[b] - n + i.  Returns (o [T,H,d] bf16, lse [H,T]
+    fp32); rows that see no key, and rows behind the last sequence, get o = 0,
+    lse = -inf."""
+    if stream is None and workspace is None:
+        out = _binding.native().chunk_cache8(q, cache, block_table, cu_seqlens, seqlens, max_new, max_seqlen, causal, scale)
+        if out is not None:
+            return out
+    _refuse_trace("attention_chunk_cache8")
+    checked = _binding._chunk_cache8(q, cache, block_table, cu_seqlens, seqlens)
+    dev, T, H, d, _, _, Hk, _, B, _ = checked
+    with _on_stream(stream, q):
+        o = torch.empty((T, H, d), device=q.device, dtype=torch.bfloat16)
+        lse = torch.empty((H, T), device=q.device, dtype=torch.float32)
+        if workspace is None:
+            n = fa_chunk_cache8_workspace_bytes(B, max_new, T, H, Hk, max_seqlen, d)
+            workspace = torch.empty(n, device=q.device, dtype=torch.uint8)
+        _binding._launch_chunk_cache8(checked, q, cache, block_table, cu_seqlens, seqlens, o, lse, workspace,
+                                      _binding._nbytes(workspace, dev), max_new, max_seqlen, causal, scale, None, True)
+    return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions.
+# ---------------------------------------------------------------------------
+class Rotary(NamedTuple):
+    """Frequencies of rotary positions: turns int64 [pairs] (each one as a fraction
+    of a turn, its 64 bits the multiple of 2^-64), axis int32 [pairs] (the position
+    that a pair is turned by), the number of axes, and whether a pair is two
+    neighbouring dimensions (otherwise dimensions j and j + pairs)."""
+    turns: torch.Tensor
+    axis: torch.Tensor
+    axes: int
+    interleaved: bool
+
+
+_PI = Fraction(3141592653589793238462643383279502884197, 10 ** 39)
+
+
+def rotary_plan(inv_freq, axis=None, interleaved: bool = False, device="cuda") -> Rotary:
+    """The frequencies inv_freq (radians a position, one for each pair of a head's
+    dimensions; a multiple of 8 of them) as the kernels take them.  The pairs are the
+    first 2 * len(inv_freq) dimensions, the others are not turned.  axis: the
+    position axis of each pair (0, 1, ...; None: one axis)."""
+    freq = [float(f) for f in inv_freq]
+    if not freq or len(freq) % 8 or not all(map(math.isfinite, freq)):
+        raise ValueError("inv_freq must be finite, a multiple of 8 frequencies")
+    axis = [0] * len(freq) if axis is None else [int(a) for a in axis]
+    if len(axis) != len(freq) or min(axis) < 0 or max(axis) >= len(freq):
+        raise ValueError(f"axis must name an axis (from 0) for each of {len(freq)} pairs")
+    turns = [round(Fraction(f) / (2 * _PI) * 2 ** 64) % 2 ** 64 for f in freq]
+    turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+    return Rotary(torch.tensor(turns, dtype=torch.int64, device=device),
+                  torch.tensor(axis, dtype=torch.int32, device=device), max(axis) + 1, bool(interleaved))
+
+
+def _turned(q, k, positions, rotary, inverse, stream):
+    if stream is None:
+        out = _binding.native().rotary(q, k, positions, rotary, inverse)
+        if out is not None:
+            return out
+    _refuse_trace("rotary_backward" if inverse else "rotary_forward")
+    checked = _binding._turn(q, k, positions, rotary)
+    with _on_stream(stream, q):
+        out = tuple(torch.empty(t.shape, device=t.device, dtype=torch.bfloat16) for t in (q, k))
+        _binding._launch_rotary(checked, q, k, *out, positions, rotary, inverse, None)
+    return out
+
+
+def rotary_forward(q, k, positions, rotary: Rotary, stream=None):
+    """q [T,H,d] and k [T,Hk,d] (slices of one projection are taken as they are)
+    turned by positions, int32 [T] or [axes,T].  Returns (q', k')."""
+    return _turned(q, k, positions, rotary, False, stream)
+
+
+def rotary_backward(dq, dk, positions, rotary: Rotary, stream=None):
+    """The gradients of rotary_forward's inputs from those of its outputs: the turn
+    back, which is also its inverse."""
+    return _turned(dq, dk, positions, rotary, True, stream)
+
+
+class _RotaryEmbedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, rotary):
+        _binding._turn(q, k, positions, rotary)  # names what is wrong before anything is saved
+        ctx.save_for_backward(positions, rotary[0], rotary[1])
+        ctx.plan = rotary[2:]
+        return _turned(q, k, positions, rotary, False, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq, dk):
+        positions, *plan = ctx.saved_tensors
+        dq, dk = _turned(dq.contiguous(), dk.contiguous(), positions, (*plan, *ctx.plan), True, None)
+        return dq, dk, None, None
+
+
+def rotary_embedding(q, k, positions, rotary: Rotary):
+    """Autograd-aware rotary_forward, differentiable once."""
+    out = _binding.native().rotary_embedding(q, k, positions, rotary)
+    if out is not None:
+        return out
+    _refuse_trace("rotary_embedding")
+    return _RotaryEmbedding.apply(q, k, positions, rotary)
+
+
+def cache8_store_rotary(q, k, v, cache: Cache8, block_table, cu_seqlens, start, max_new: int, rotary: Rotary,
+                        positions=None, stream=None):
+    """cache8_store with the positions on the way: the new tokens' keys [T,Hk,d]
+    are turned and stored with the values, and the queries q [T,H,d] turned.
+    positions: int32 [T] or [axes,T]; None: each token's place in its sequence,
+    start[b] + i, on every axis.  Returns q', zero in rows behind the last
+    sequence."""
+    if stream is None:
+        out = _binding.native().cache8_store_rotary(q, k, v, cache, block_table, cu_seqlens, start, max_new, rotary,
+                                                    positions)
+        if out is not None:
+            return out
+    _refuse_trace("cache8_store_rotary")
+    with _on_stream(stream, q):
+        q_out = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16)
+        fa_cache8_store_rotary(q, k, v, q_out, cache, block_table, cu_seqlens, start, max_new, rotary, positions, None, True)
+    return q_out

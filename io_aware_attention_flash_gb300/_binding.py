@@ -53,6 +53,10 @@ SIGNATURES = {
     "fa_cache8_store": (_I, [_P] * 9 + [_I] * 8 + [_L, _L, _P]),
     "fa_decode_cache8_workspace_bytes": (_Z, [_I] * 6),
     "fa_fwd_decode_cache8": (_I, [_P] * 10 + [_Z] + [_I] * 9 + [_F, _I, _P]),
+    "fa_rotary": (_I, [_P] * 7 + [_I] * 8 + [_L, _L, _P]),
+    "fa_cache8_store_rotary": (_I, [_P] * 14 + [_I] * 12 + [_L, _L, _L, _I, _P]),
+    "fa_chunk_cache8_workspace_bytes": (_Z, [_I] * 7),
+    "fa_fwd_chunk_cache8": (_I, [_P] * 11 + [_Z] + [_I] * 10 + [_L, _F, _I, _I, _P]),
     "fa_decode_workspace_bytes": (_Z, [_I, _I, _I, _I, _I]),
     "fa_fwd_decode": (_I, [_P, _P, _P, _P, _P, _P, _Z, _I, _I, _I, _I, _I, _F, _I, _P]),
 }
@@ -113,6 +117,7 @@ class _NoNative:
         return None
 
     forward_grouped = backward_grouped = flash_attention_grouped = cache8_store = decode_cache8 = _none
+    rotary = rotary_embedding = cache8_store_rotary = chunk_cache8 = _none
 
 
 def native():
@@ -458,6 +463,129 @@ def fa_fwd_decode_cache8(q, cache, block_table, seqlens, o, lse, workspace, max_
     _dense("lse", lse, torch.float32, (B, H, Nq), dev)
     _launch_decode_cache8(checked, q, cache, block_table, seqlens, o, lse, workspace, _nbytes(workspace, dev), max_seqlen,
                           causal, scale, stream)
+
+
+def _rotary(rotary, total: int, d: int, positions, dev: int):
+    """Checks of a Rotary and its positions ([total] or [axes, total]; None where
+    the call allows it): (pairs, axes, interleaved)."""
+    turns, axis, axes, interleaved = rotary
+    if turns.dim() != 1:
+        raise ValueError("rotary.turns must be [pairs]")
+    pairs = turns.numel()
+    _dense("rotary.turns", turns, torch.int64, (pairs,), dev)
+    _dense("rotary.axis", axis, torch.int32, (pairs,), dev)
+    if pairs == 0 or pairs % 8 or 2 * pairs > d:
+        raise ValueError(f"rotary: {pairs} pairs must be a multiple of 8 and at most half of a head's {d} dimensions")
+    if not 1 <= axes <= pairs:
+        raise ValueError(f"rotary: {axes} axes for {pairs} pairs")
+    if positions is not None:
+        _dense("positions", positions, torch.int32,
+               (total,) if axes == 1 and positions.dim() == 1 else (axes, total), dev)
+    return pairs, axes, bool(interleaved)
+
+
+def _turn(q, k, positions, rotary):
+    """Checks of fa_rotary's inputs: (device, T, H, Hk, d, pairs, axes, interleaved, row strides)."""
+    dev = _device_of("q", q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T, H, d] and [T, Hk, d]")
+    T, H, d = q.shape
+    Hk = k.shape[1]
+    ldq, ldk = _rows("q", q, T, H, d, dev), _rows("k", k, T, Hk, d, dev)
+    if positions is None:
+        raise TypeError("positions must be an int32 tensor")
+    return (dev, T, H, Hk, d, *_rotary(rotary, T, d, positions, dev), ldq, ldk)
+
+
+def _launch_rotary(checked, q, k, q_out, k_out, positions, rotary, inverse, stream) -> None:
+    dev, T, H, Hk, d, pairs, axes, interleaved, ldq, ldk = checked
+    _check("fa_rotary", lib().fa_rotary(
+        q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), positions.data_ptr(), rotary[0].data_ptr(),
+        rotary[1].data_ptr(), T, H, Hk, d, pairs, axes, interleaved, inverse, ldq, ldk, _stream_of(stream, dev)))
+
+
+def fa_rotary(q, k, q_out, k_out, positions, rotary, inverse: bool = False, stream=None) -> None:
+    """q, q_out [T, H, d], k, k_out [T, Hk, d] (rows of q and k may be slices of
+    wider ones); positions int32 [T] or [axes, T]."""
+    checked = _turn(q, k, positions, rotary)
+    dev, T, H, Hk, d = checked[:5]
+    _dense("q_out", q_out, torch.bfloat16, (T, H, d), dev)
+    _dense("k_out", k_out, torch.bfloat16, (T, Hk, d), dev)
+    _launch_rotary(checked, q, k, q_out, k_out, positions, rotary, bool(inverse), stream)
+
+
+def fa_cache8_store_rotary(q, k, v, q_out, cache, block_table, cu_seqlens, start, max_new: int, rotary, positions=None,
+                           stream=None, zero_tail: bool = False) -> None:
+    """fa_cache8_store of turned keys; q [T, H, d] turned into q_out."""
+    dev = _device_of("q", q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T, H, d] and [T, Hk, d]")
+    T, H, d = q.shape
+    Hk = k.shape[1]
+    ldq, ldk, ldv = _rows("q", q, T, H, d, dev), _rows("k", k, T, Hk, d, dev), _rows("v", v, T, Hk, d, dev)
+    _dense("q_out", q_out, torch.bfloat16, (T, H, d), dev)
+    num_blocks, heads, block, dim = _cache8(cache, dev)
+    if heads != Hk or dim != d:
+        raise ValueError(f"the cache holds {heads} heads of {dim}, k and v have {Hk} of {d}")
+    pairs, axes, interleaved = _rotary(rotary, T, d, positions, dev)
+    B = start.numel()
+    cols = _block_table(block_table, B, dev)
+    _dense("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev)
+    _dense("start", start, torch.int32, (B,), dev)
+    _count("max_new", max_new)
+    ck, cv, sk, sv = cache
+    _check("fa_cache8_store_rotary", lib().fa_cache8_store_rotary(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(),
+        sv.data_ptr(), block_table.data_ptr(), cu_seqlens.data_ptr(), start.data_ptr(),
+        None if positions is None else positions.data_ptr(), rotary[0].data_ptr(), rotary[1].data_ptr(), B, max_new, T,
+        num_blocks, cols, H, Hk, block, d, pairs, axes, interleaved, ldq, ldk, ldv, bool(zero_tail),
+        _stream_of(stream, dev)))
+
+
+def fa_chunk_cache8_workspace_bytes(B: int, max_new: int, total: int, H: int, Hk: int, max_seqlen: int, d: int) -> int:
+    return lib().fa_chunk_cache8_workspace_bytes(B, max_new, total, H, Hk, max_seqlen, d)
+
+
+def _chunk_cache8(q, cache, block_table, cu_seqlens, seqlens):
+    """Checks of the inputs: (device, T, H, d, row stride, num_blocks, Hk, block, B, table columns)."""
+    dev = _device_of("q", q)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, H, d]")
+    T, H, d = q.shape
+    ldq = _rows("q", q, T, H, d, dev)
+    num_blocks, Hk, block, dim = _cache8(cache, dev)
+    if dim != d:
+        raise ValueError(f"the cache holds heads of {dim}, q has {d}")
+    B = seqlens.numel()
+    cols = _block_table(block_table, B, dev)
+    _dense("cu_seqlens", cu_seqlens, torch.int32, (B + 1,), dev)
+    _dense("seqlens", seqlens, torch.int32, (B,), dev)
+    return dev, T, H, d, ldq, num_blocks, Hk, block, B, cols
+
+
+def _launch_chunk_cache8(checked, q, cache, block_table, cu_seqlens, seqlens, o, lse, workspace, nbytes, max_new,
+                         max_seqlen, causal, scale, stream, zero_tail) -> None:
+    dev, T, H, d, ldq, num_blocks, Hk, block, B, cols = checked
+    _count("max_new", max_new)
+    _count("max_seqlen", max_seqlen)
+    ck, cv, sk, sv = cache
+    _check("fa_fwd_chunk_cache8", lib().fa_fwd_chunk_cache8(
+        q.data_ptr(), ck.data_ptr(), cv.data_ptr(), sk.data_ptr(), sv.data_ptr(), block_table.data_ptr(),
+        cu_seqlens.data_ptr(), seqlens.data_ptr(), o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, B, max_new,
+        T, H, Hk, num_blocks, cols, block, max_seqlen, d, ldq, _scale(scale, d), bool(causal), zero_tail,
+        _stream_of(stream, dev)))
+
+
+def fa_fwd_chunk_cache8(q, cache, block_table, cu_seqlens, seqlens, o, lse, workspace, max_new: int, max_seqlen: int,
+                        causal: bool, scale=None, stream=None, zero_tail: bool = False) -> None:
+    """q, o [T, H, d] (rows of q may be slices of wider ones) over the cache (k, v,
+    k_scale, v_scale); lse fp32 [H, T]."""
+    checked = _chunk_cache8(q, cache, block_table, cu_seqlens, seqlens)
+    dev, T, H, d = checked[:4]
+    _dense("o", o, torch.bfloat16, (T, H, d), dev)
+    _dense("lse", lse, torch.float32, (H, T), dev)
+    _launch_chunk_cache8(checked, q, cache, block_table, cu_seqlens, seqlens, o, lse, workspace, _nbytes(workspace, dev),
+                         max_new, max_seqlen, causal, scale, stream, bool(zero_tail))
 
 
 def fa_decode_workspace_bytes(B: int, H: int, Nq: int, Nk: int, d: int) -> int:

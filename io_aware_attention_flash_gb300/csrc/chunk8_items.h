@@ -1,0 +1,48 @@
+// The work items of the chunk attention: which query rows, which key tiles, and how
+// they are shared out over the launch's CTAs.  Plain C++, so that it can be checked
+// on the host.
+//
+// A sequence's n new tokens and the G query heads of a key/value head make n · G
+// rows, token by token (row f: token f / G, head f mod G of the group).  An item is
+// kRows of them over one key/value head; its tiles are the runs of kKeys keys that
+// its last row sees, at least one.  The items in the order (sequence, row block,
+// key/value head), tile after tile, are cut into runs of equal length, one a CTA.
+#pragma once
+
+#ifdef __CUDACC__
+#define FA_CHUNK_FN __host__ __device__ __forceinline__ constexpr
+#else
+#define FA_CHUNK_FN constexpr
+#endif
+
+namespace fa {
+namespace chunk8 {
+
+constexpr int kRows = 256, kHalf = 128, kKeys = 128;
+
+// Keys that new token i of n sees, of `len` cached ones (the new tokens are the last of them).
+FA_CHUNK_FN int visible(int len, int n, int i, bool causal) {
+  if (!causal) return len;
+  const long long v = static_cast<long long>(len) - n + i + 1;
+  return v < 0 ? 0 : v > len ? len : static_cast<int>(v);
+}
+FA_CHUNK_FN int tiles(int keys) {
+  const int t = static_cast<int>((static_cast<unsigned>(keys) + kKeys - 1u) / kKeys);
+  return t < 1 ? 1 : t;
+}
+// Tiles that the rows [first, first + count) take, 0 if none of them exists (rows = n · G).
+FA_CHUNK_FN int row_tiles(int len, int n, int G, int first, int count, bool causal) {
+  const int rows = n * G;
+  if (first >= rows) return 0;
+  const int last = (rows - first < count ? rows : first + count) - 1;
+  return tiles(visible(len, n, last / G, causal));
+}
+
+// Run c of `ctas` over `total` tiles begins at run_start(c); tile t lies in run run_of(t).
+FA_CHUNK_FN long long run_start(long long c, long long total, long long ctas) { return c * total / ctas; }
+FA_CHUNK_FN int run_of(long long t, long long total, long long ctas) {
+  return static_cast<int>(((t + 1) * ctas + total - 1) / total - 1);
+}
+
+}  // namespace chunk8
+}  // namespace fa

@@ -9,6 +9,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "chunk8_items.h"
 #include "fa.h"
 #include "fa_kernels.cuh"
 #include "ptx.cuh"
@@ -466,6 +467,59 @@ Decode8Plan decode8_plan(int B, int Nq, int H, int Hk, int max_seqlen, int d) {
   return w;
 }
 
+// Rotary positions.
+fa_status check_rotary(const uint64_t* turns, const int* axis, int pairs, int axes, int d) {
+  if (d != 64 && d != 128) return FA_ERR_HEAD_DIM;
+  if (pairs <= 0 || pairs % 8 != 0 || 2 * pairs > d) return FA_ERR_SHAPE;
+  if (axes <= 0 || axes > pairs) return FA_ERR_SHAPE;
+  if (!turns || (axes > 1 && !axis)) return FA_ERR_NULL;
+  return FA_OK;
+}
+
+fa_status check_heads(int total, int H, int d) {
+  if (H <= 0 || H > 65535 || total <= 0) return FA_ERR_SHAPE;
+  return static_cast<long long>(total) * H * d > (1LL << 40) ? FA_ERR_SHAPE : FA_OK;
+}
+
+fa::RotaryParams rotary_params(const int* positions, const uint64_t* turns, const int* axis, int pairs, int axes,
+                               int interleaved, int inverse) {
+  fa::RotaryParams r{};
+  r.turns = turns;
+  r.axis = axis;
+  r.positions = positions;
+  r.pairs = pairs;
+  r.axes = axes;
+  r.interleaved = interleaved ? 1 : 0;
+  r.inverse = inverse ? 1 : 0;
+  return r;
+}
+
+// Attention of a chunk over the cache: a CTA an SM, or a tile, and two partials of each.
+constexpr int kChunkCtas = 152;
+
+struct ChunkPlan {
+  int row_blocks, ctas;
+  size_t ml_off, merge_off, bytes;
+};
+
+fa_status chunk_plan(int B, int max_new, int total, int H, int Hk, int max_seqlen, int d, ChunkPlan* w) {
+  FA_TRY(check_common(H, d, 1.0f));
+  if (B <= 0 || max_new <= 0 || total <= 0 || max_seqlen <= 0 || Hk <= 0 || H % Hk != 0) return FA_ERR_SHAPE;
+  if (static_cast<long long>(total) * H > 0x7fffffffLL) return FA_ERR_SHAPE;
+  const long long rows = static_cast<long long>(max_new < total ? max_new : total) * (H / Hk);
+  const long long blocks = (rows + fa::chunk8::kRows - 1) / fa::chunk8::kRows;
+  if (blocks * B > 0x7fffffffLL) return FA_ERR_SHAPE;
+  const long long tiles = (static_cast<long long>(max_seqlen) + fa::chunk8::kKeys - 1) / fa::chunk8::kKeys;
+  const long long most = kChunkCtas / tiles / Hk < blocks * B ? kChunkCtas : blocks * B * Hk * tiles;
+  w->row_blocks = static_cast<int>(blocks);
+  w->ctas = static_cast<int>(most < kChunkCtas ? most : kChunkCtas);
+  const size_t parts = static_cast<size_t>(2) * w->ctas * fa::chunk8::kRows;
+  w->ml_off = pad256(parts * d * 4);
+  w->merge_off = w->ml_off + pad256(parts * 2 * 4);
+  w->bytes = w->merge_off + pad256(static_cast<size_t>(w->ctas) * 8 * 4);
+  return FA_OK;
+}
+
 // One CTA waits on an mbarrier that nothing arrives on, with a short limit.
 __global__ void fa_wait_timeout_selftest_kernel(uint32_t* err, uint64_t limit_ns) {
   __shared__ __align__(8) uint64_t barrier;
@@ -773,6 +827,132 @@ FA_API fa_status fa_fwd_decode_cache8(const void* q, const void* k_codes, const 
   FA_TRY(make_map_codes(&tv, v_codes, d, block, Hk, num_blocks));
   const cudaError_t e = fa::launch_cache8_decode(d, tk, tv, p, w.ctas, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail("cache attention launch", e);
+}
+
+FA_API fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+                           const uint64_t* turns, const int* axis, int total, int H, int Hk, int d, int pairs, int axes,
+                           int interleaved, int inverse, long long ldq, long long ldk, void* stream) {
+  FA_TRY(check_rotary(turns, axis, pairs, axes, d));
+  FA_TRY(check_heads(total, H, d));
+  FA_TRY(check_heads(total, Hk, d));
+  if (!q || !k || !q_out || !k_out || !positions) return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return FA_ERR_ALIGN;
+  if (!stride_ok(ldq, H, d) || !stride_ok(ldk, Hk, d)) return FA_ERR_SHAPE;
+  DeviceGuard guard;
+  FA_TRY(bind_device(q));
+  const fa::RotaryParams r = rotary_params(positions, turns, axis, pairs, axes, interleaved, inverse);
+  const fa::TurnRows x{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k), ldq, ldk,
+                       static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_out), H, Hk};
+  const cudaError_t e = fa::launch_rotary(d, r, x, total, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail("rotary launch", e);
+}
+
+FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void* v, void* q_out, void* k_codes,
+                                        void* v_codes, float* k_scale, float* v_scale, const int* block_table,
+                                        const int* cu_seqlens, const int* start, const int* positions,
+                                        const uint64_t* turns, const int* axis, int B, int max_new, int total,
+                                        int num_blocks, int table_cols, int H, int Hk, int block, int d, int pairs,
+                                        int axes, int interleaved, long long ldq, long long ldk, long long ldv,
+                                        int zero_tail, void* stream) {
+  FA_TRY(check_cache8(B, num_blocks, table_cols, Hk, block, d));
+  FA_TRY(check_rotary(turns, axis, pairs, axes, d));
+  FA_TRY(check_heads(total, H, d));
+  if (max_new <= 0) return FA_ERR_SHAPE;
+  if (static_cast<long long>(B) * ((static_cast<long long>(max_new) + block - 2) / block + 1) > 0x7fffffffLL) return FA_ERR_SHAPE;
+  if (!q || !k || !v || !q_out || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !cu_seqlens || !start)
+    return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_codes) || !aligned16(v_codes))
+    return FA_ERR_ALIGN;
+  if (!stride_ok(ldq, H, d) || !stride_ok(ldk, Hk, d) || !stride_ok(ldv, Hk, d)) return FA_ERR_SHAPE;
+  DeviceGuard guard;
+  FA_TRY(bind_device(q));
+  fa::Cache8StoreParams p{};
+  FA_TRY(error_word(&p.err));
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.ldk = ldk;
+  p.ldv = ldv;
+  p.k_codes = static_cast<uint8_t*>(k_codes);
+  p.v_codes = static_cast<uint8_t*>(v_codes);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.cu_seqlens = cu_seqlens;
+  p.start = start;
+  p.B = B;
+  p.total = total;
+  p.max_new = max_new;
+  p.num_blocks = num_blocks;
+  p.table_cols = table_cols;
+  p.Hk = Hk;
+  p.blocks = static_cast<int>((static_cast<long long>(max_new) + block - 2) / block + 1);
+  const fa::RotaryParams r = rotary_params(positions, turns, axis, pairs, axes, interleaved, 0);
+  const fa::TurnRows x{static_cast<const uint16_t*>(q), nullptr, ldq, 0, static_cast<uint16_t*>(q_out), nullptr, H, 0};
+  const cudaError_t e =
+      fa::launch_cache8_append(d, block, p, r, x, zero_tail ? 1 : 0, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail("cache append launch", e);
+}
+
+FA_API size_t fa_chunk_cache8_workspace_bytes(int B, int max_new, int total, int H, int Hk, int max_seqlen, int d) {
+  ChunkPlan w{};
+  return chunk_plan(B, max_new, total, H, Hk, max_seqlen, d, &w) == FA_OK ? w.bytes : 0;
+}
+
+FA_API fa_status fa_fwd_chunk_cache8(const void* q, const void* k_codes, const void* v_codes, const float* k_scale,
+                                     const float* v_scale, const int* block_table, const int* cu_seqlens,
+                                     const int* seqlens, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                                     int B, int max_new, int total, int H, int Hk, int num_blocks, int table_cols,
+                                     int block, int max_seqlen, int d, long long ldq, float scale, int causal,
+                                     int zero_tail, void* stream) {
+  FA_TRY(check_common(H, d, scale));
+  FA_TRY(check_cache8(B, num_blocks, table_cols, Hk, block, d));
+  if (!(scale > 0.f)) return FA_ERR_SCALE;
+  ChunkPlan w{};
+  FA_TRY(chunk_plan(B, max_new, total, H, Hk, max_seqlen, d, &w));
+  if (!stride_ok(ldq, H, d)) return FA_ERR_SHAPE;
+  if (!q || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !cu_seqlens || !seqlens || !o || !lse ||
+      !workspace)
+    return FA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned16(o) || !aligned16(workspace))
+    return FA_ERR_ALIGN;
+  if (workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
+  DeviceGuard guard;
+  FA_TRY(bind_device(q));
+  fa::Chunk8Params p{};
+  FA_TRY(error_word(&p.err));
+  p.q = static_cast<const uint16_t*>(q);
+  p.ldq = ldq;
+  p.o = static_cast<uint16_t*>(o);
+  p.lse = lse;
+  p.k_codes = static_cast<const uint8_t*>(k_codes);
+  p.v_codes = static_cast<const uint8_t*>(v_codes);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.cu_seqlens = cu_seqlens;
+  p.seqlens = seqlens;
+  p.o_part = static_cast<float*>(workspace);
+  p.ml_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.ml_off);
+  p.merge = reinterpret_cast<int*>(static_cast<char*>(workspace) + w.merge_off);
+  p.B = B;
+  p.total = total;
+  p.H = H;
+  p.Hk = Hk;
+  p.G = H / Hk;
+  p.num_blocks = num_blocks;
+  p.table_cols = table_cols;
+  p.block_shift = block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7;
+  p.max_new = max_new;
+  p.max_seqlen = max_seqlen;
+  p.row_blocks = w.row_blocks;
+  p.causal = causal ? 1 : 0;
+  p.zero_tail = zero_tail ? 1 : 0;
+  p.scale_log2 = scale * fa::kLog2e;
+  p.timeout_ns = kWaitLimitNs;
+  // An item of one tile is whole: nothing to join.
+  const bool merge = max_seqlen > fa::chunk8::kKeys;
+  const cudaError_t e = fa::launch_cache8_chunk(d, p, w.ctas, merge, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail("chunk attention launch", e);
 }
 
 FA_API size_t fa_decode_workspace_bytes(int B, int H, int Nq, int Nk, int d) {

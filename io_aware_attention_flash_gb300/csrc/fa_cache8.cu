@@ -27,6 +27,7 @@
 
 #include "cache8_phases.h"
 #include "cache8_tiles.h"
+#include "e4m3.cuh"
 #include "fa_kernels.cuh"
 #include "ptx.cuh"
 
@@ -36,57 +37,6 @@ namespace {
 // ----------------------------------------------------------------------------
 // Store
 // ----------------------------------------------------------------------------
-constexpr int kScaleFloor = -64;  // exponent of the smallest scale
-
-__device__ __forceinline__ float exp2_int(int e) { return __int_as_float((e + 127) << 23); }
-
-// Scale exponent of a maximum magnitude given as bf16 bits: amax = 1.m · 2^E is
-// at most 448 · 2^e = 1.75 · 2^(8+e); not below `least`.
-__device__ __forceinline__ int scale_exponent(uint32_t amax_bits, int least) {
-  const int biased = static_cast<int>(amax_bits >> 7), mant = static_cast<int>(amax_bits & 127u);
-  return max(biased - 127 - 8 + (mant > 96 ? 1 : 0), least);
-}
-
-// Floats to e4m3 codes, the first in the lowest byte (nearest even,
-// saturating; NaN stays NaN).
-__device__ __forceinline__ uint32_t pack_e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
-      "mov.b32 %0, {l, h};}"
-      : "=r"(r)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-// Two e4m3 codes to two floats (exact).
-__device__ __forceinline__ void unpack_e4m3x2(uint32_t code2, float& a, float& b) {
-  uint32_t h2;
-  const uint16_t c = static_cast<uint16_t>(code2);
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(c));
-  asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}" : "=f"(a), "=f"(b) : "r"(h2));
-}
-
-// The larger of two bf16 in each half; of a NaN and a number the number.
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Four e4m3 codes to four floats (exact).
-__device__ __forceinline__ void unpack_e4m3x4(uint32_t code4, float (&v)[4]) {
-  uint32_t a, b;
-  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
-      : "=r"(a), "=r"(b)
-      : "r"(code4));
-  asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}" : "=f"(v[0]), "=f"(v[1]) : "r"(a));
-  asm("{.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;}" : "=f"(v[2]), "=f"(v[3]) : "r"(b));
-}
-
 // One group of TG threads quantises the new tokens of one (page, head) of K or
 // V: each thread keeps CH 16-byte chunks of them in registers between the
 // maximum and the rounding, so the input is read once, and its loads do not

@@ -1,0 +1,859 @@
+// Attention of a chunk of new tokens over the 8-bit paged cache, for sm_103a.
+//
+//   O = softmax(scale Q K^T) V over the tokens a sequence has in the cache, its new
+//   ones the last of them (causal: new token i of n sees keys up to len - n + i).
+//
+// The rows of a product are the new tokens times the G query heads of one key/value
+// head, so a tile of keys is read once for all of them, and a chunk of a few tokens
+// still fills the tensor core's 128 rows.  A CTA takes 256 rows (two tiles of 128)
+// over a run of key tiles; chunk8_items.h says which.  An item that several CTAs
+// share leaves partials (m, l, O), which a second kernel joins in the order of the
+// keys, so results do not depend on timing.
+//
+// Keys and values leave the cache as codes (half the bytes of bf16 through L2 and
+// shared memory) and are made bf16 in shared memory on the way to the tensor core:
+// an e4m3 value times its page's power of two is a bf16 number, so nothing is
+// rounded, and the products are those of the forward kernel.  (Straight from the
+// codes, as the cache's decode does it, Q and P need two e4m3 terms each: as many
+// tensor operations, and the second term of P costs the softmax as many instructions
+// as this conversion costs warps of its own.)
+//
+// Warp roles (16 warps):
+//   0-3, 4-7   softmax, one warpgroup a row tile; thread r owns row r of it
+//   8-11       conversion of a K, then a V tile
+//   12         tcgen05.mma issue
+//   13         items and copies: publishes the CTA's next item, copies the codes of
+//              its pages (lane i: page i of the tile) with their scales
+// The softmax is the forward kernel's: the reference of a row is the maximum of its
+// first tile and moves only where a tile's row sum reaches 2^40.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "cache8_tiles.h"
+#include "chunk8_items.h"
+#include "fa_kernels.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+using chunk8::kHalf;
+using chunk8::kKeys;
+using chunk8::kRows;
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int KB = D / 64;                     // 128-byte swizzle blocks per row
+  static constexpr int BLK_BYTES = kTile * 128;         // one 128-row x 64-col block
+  static constexpr int TILE_BYTES = KB * BLK_BYTES;     // one 128 x D tile of bf16
+  static constexpr int CODE_BYTES = kKeys * D;          // the same of codes
+  static constexpr int NK = D == 128 ? 2 : 3;           // K, V ring depth
+  static constexpr int NV = NK;
+  static constexpr int NST = D == 128 ? 2 : 6;          // code ring: K, V, K, V, ...
+  static constexpr int NI = 4;                          // published items
+  static constexpr int MAX_PPT = kKeys / 16;            // pages of a tile, at most
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + NK * TILE_BYTES;
+  static constexpr int OFF_C = OFF_V + NV * TILE_BYTES;
+  static constexpr int OFF_SC = OFF_C + NST * CODE_BYTES;          // [NST][pages] two factors, bf16 pairs
+  static constexpr int ITEM_INTS = 12;
+  static constexpr int OFF_ITEM = OFF_SC + NST * MAX_PPT * 8;
+  static constexpr int OFF_SCAN = OFF_ITEM + NI * ITEM_INTS * 4;   // [16] sums of a scan, then its find
+  static constexpr int OFF_BAR = OFF_SCAN + 18 * 8;
+  static constexpr int B_IFULL = 0;
+  static constexpr int B_IEMPTY = B_IFULL + NI;
+  static constexpr int B_CFULL = B_IEMPTY + NI;
+  static constexpr int B_CEMPTY = B_CFULL + NST;
+  static constexpr int B_KFULL = B_CEMPTY + NST;
+  static constexpr int B_KEMPTY = B_KFULL + NK;
+  static constexpr int B_VFULL = B_KEMPTY + NK;
+  static constexpr int B_VEMPTY = B_VFULL + NV;
+  static constexpr int B_Q = B_VEMPTY + NV;
+  static constexpr int B_SFULL = B_Q + 2;
+  static constexpr int B_PFULL = B_SFULL + 2;
+  static constexpr int B_ODONE = B_PFULL + 2;
+  static constexpr int B_DRAIN = B_ODONE + 2;
+  static constexpr int NBAR = B_DRAIN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // slack to align the base to 1024
+  static constexpr int CONVERT_WARP = 8, MMA_WARP = 12, COPY_WARP = 13;
+  static constexpr int NUM_THREADS = 512;
+  static constexpr int READERS = 13;                    // warps that take an item: all but the copying one and two idle
+  // Registers a thread after the split; launched with 128.
+  static constexpr int REG_SOFTMAX = 192, REG_CONVERT = 72, REG_OTHER = 56;
+  static_assert(2 * REG_SOFTMAX + REG_CONVERT + REG_OTHER == 4 * 128, "the split takes what the launch gives");
+  static constexpr uint32_t TMEM_COLS = 512;
+  __host__ __device__ static constexpr uint32_t S_COL(int t) { return t * 128; }
+  __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256 + t * D; }
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+// What the roles know of an item.
+struct Item {
+  int b, hk, rb, k0, tiles, n, len, tok0, cnt0, cnt1, slot;  // slot: of the partial, -1: the item is whole
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// New tokens and cached tokens of sequence b, within what the buffers hold.
+__device__ __forceinline__ void chunk_seq(const Chunk8Params& p, int b, int& tok0, int& n, int& len) {
+  tok0 = min(max(p.cu_seqlens[b], 0), p.total);
+  n = min(min(max(p.cu_seqlens[b + 1], tok0), p.total) - tok0, p.max_new);
+  const long long cap = min(static_cast<long long>(p.table_cols) << p.block_shift, static_cast<long long>(p.max_seqlen));
+  len = static_cast<int>(min(max(static_cast<long long>(p.seqlens[b]), 0LL), cap));
+}
+
+// Four codes to bf16 by their bits: sign, and exponent and mantissa four places
+// down, which reads as the value times 2^-120 (a subnormal code as a subnormal).
+// The first word holds elements 0 and 2, the second 1 and 3: Q's and O's dimensions
+// change places to match, which costs nothing.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& even, uint32_t& odd) {
+  odd = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+  even = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+constexpr uint32_t kOne2 = 0x3f803f80u;
+// 2^(e + 120) as two bf16 factors, each a pair; e the exponent of a page's scale.
+__device__ __forceinline__ uint2 scale_factors(float scale) {
+  const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127;
+  const int a = max(min(e + 120, 127), -126), b = max(e - 7, 0);
+  return make_uint2(static_cast<uint32_t>(a + 127) * 0x00800080u, static_cast<uint32_t>(b + 127) * 0x00800080u);
+}
+
+template <int D>
+__global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(const Chunk8Params p) {
+  using C = ChunkCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_base = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw_base & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sb = raw_base + pad;
+  auto bar = [&](int i) -> uint32_t { return sb + C::OFF_BAR + 8 * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (warp == C::COPY_WARP && lane == 0) {
+    for (int i = 0; i < C::NI; ++i) {
+      mbar_init(bar(C::B_IFULL + i), 1);
+      mbar_init(bar(C::B_IEMPTY + i), C::READERS);
+    }
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(bar(C::B_CFULL + i), 1);
+      mbar_init(bar(C::B_CEMPTY + i), 4);
+    }
+    for (int i = 0; i < C::NK; ++i) {
+      mbar_init(bar(C::B_KFULL + i), 4);
+      mbar_init(bar(C::B_KEMPTY + i), 1);
+    }
+    for (int i = 0; i < C::NV; ++i) {
+      mbar_init(bar(C::B_VFULL + i), 4);
+      mbar_init(bar(C::B_VEMPTY + i), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(C::B_Q + t), 128);
+      mbar_init(bar(C::B_SFULL + t), 1);
+      mbar_init(bar(C::B_PFULL + t), 128);
+      mbar_init(bar(C::B_ODONE + t), 1);
+    }
+    mbar_init(bar(C::B_DRAIN), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  // The kernel may start while the one before it in the stream finishes; what that
+  // one wrote is read, and tensor memory taken, from here on.
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (p.zero_tail) {
+    // Rows behind the last sequence, shared out over the grid.
+    const int end = min(max(p.cu_seqlens[p.B], 0), p.total);
+    for (int row = end + blockIdx.x; row < p.total; row += gridDim.x) {
+      uint4* o = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(row) * p.H * D);
+      for (int i = tid; i < p.H * (D / 8); i += C::NUM_THREADS) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int h = tid; h < p.H; h += C::NUM_THREADS) p.lse[static_cast<size_t>(h) * p.total + row] = -CUDART_INF_F;
+    }
+  }
+
+  // ---- this CTA's place: the tiles of all (sequence, row block) pairs counted, then
+  // the pair that holds the run's first tile
+  const int pairs = p.B * p.row_blocks;
+  long long* scan = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
+  auto pair_tiles = [&](int x) -> long long {
+    const int b = x / p.row_blocks, rb = x - b * p.row_blocks;
+    int tok0, n, len;
+    chunk_seq(p, b, tok0, n, len);
+    return static_cast<long long>(p.Hk) * chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
+  };
+  auto warp_scan = [&](long long v) {  // inclusive
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, v, off);
+      if (lane >= off) v += y;
+    }
+    return v;
+  };
+  long long own = 0;  // tiles of pair tid, where one pass takes all pairs; else of all of this thread's
+  for (int x = tid; x < pairs; x += C::NUM_THREADS) own += pair_tiles(x);
+  long long upto = warp_scan(own);
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const long long s = scan[i];
+    if (i < warp) upto += s;
+    total += s;
+  }
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));  // every one of them has a tile
+  if (tid == 0) p.merge[blockIdx.x * 8] = -1;
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const long long t_lo = chunk8::run_start(blockIdx.x, total, ctas), t_hi = chunk8::run_start(blockIdx.x + 1LL, total, ctas);
+  long long* found = scan + 16;  // first tile of the pair; the pair
+  if (pairs <= C::NUM_THREADS) {
+    if (t_lo >= upto - own && t_lo < upto) {
+      found[0] = upto - own;
+      found[1] = tid;
+    }
+  } else {
+    long long base = 0;
+    for (int x0 = 0; x0 < pairs && base <= t_lo; x0 += C::NUM_THREADS) {
+      const long long w = x0 + tid < pairs ? pair_tiles(x0 + tid) : 0;
+      long long sum = warp_scan(w);
+      __syncthreads();  // (the sums of the round before have been read)
+      if (lane == 31) scan[warp] = sum;
+      __syncthreads();
+      long long all = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const long long s = scan[i];
+        if (i < warp) sum += s;
+        all += s;
+      }
+      if (t_lo >= base + sum - w && t_lo < base + sum) {
+        found[0] = base + sum - w;
+        found[1] = x0 + tid;
+      }
+      base += all;
+    }
+  }
+  if (blockIdx.x == 0) {  // lengths out of range are reported once
+    for (int b = tid; b < p.B; b += C::NUM_THREADS) {
+      int tok0, n, len;
+      chunk_seq(p, b, tok0, n, len);
+      if (len != p.seqlens[b]) atomicOr(p.err, kDevErrPage);
+    }
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The next item of the CTA, as the copying warp publishes it; false at the end.
+  int items = 0;
+  auto take_item = [&](Item& it) -> bool {
+    const int s = items % C::NI;
+    bool ok = wait_bounded(bar(C::B_IFULL + s), (items / C::NI) & 1, abort_flag, p.err, p.timeout_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    const int4* src = reinterpret_cast<const int4*>(smem + C::OFF_ITEM + s * C::ITEM_INTS * 4);
+    const int4 a = src[0], b = src[1], c = src[2];
+    it.b = a.x, it.hk = a.y, it.rb = a.z, it.k0 = a.w;
+    it.tiles = b.x, it.n = b.y, it.len = b.z, it.tok0 = b.w;
+    it.cnt0 = c.x, it.cnt1 = c.y, it.slot = c.z;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::B_IEMPTY + s));
+    ++items;
+    return it.tiles > 0;
+  };
+
+  if (warp >= C::MMA_WARP) {
+    setmaxnreg_dec<C::REG_OTHER>();
+    if (warp == C::COPY_WARP) {
+      // ------------------------------------------------------------ items, copies
+      const int ppt = kKeys >> p.block_shift, page_bytes = D << p.block_shift;
+      struct Unit {
+        int b, hk, rb, k0, k1, nt, n, len, tok0;  // the item (tiles k0 .. k1 of nt)
+        int kt, tiles;                            // first tile of the unit, and how many
+        int page;                                 // this lane's page (of 32 / ppt tiles), -1: none
+        float ks, vs;
+      };
+      int x = static_cast<int>(found[1]);
+      long long x_start = found[0], t = t_lo;
+      int nt = 0, n = 0, len = 0, tok0 = 0, b = 0, rb = 0;
+      auto load_pair = [&]() {
+        b = x / p.row_blocks;
+        rb = x - b * p.row_blocks;
+        chunk_seq(p, b, tok0, n, len);
+        n = __shfl_sync(0xffffffffu, n, 0);  // the warp stays together even if a caller changes the lengths meanwhile
+        len = __shfl_sync(0xffffffffu, len, 0);
+        nt = chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
+      };
+      load_pair();
+      auto next_unit = [&](Unit& u) {
+        u.tiles = 0;
+        if (t >= t_hi) return;
+        while (t >= x_start + static_cast<long long>(p.Hk) * nt) {
+          x_start += static_cast<long long>(p.Hk) * nt;
+          if (++x >= pairs) {
+            t = t_hi;
+            return;
+          }
+          load_pair();
+        }
+        const long long at = t - x_start;
+        u.b = b, u.rb = rb, u.n = n, u.len = len, u.tok0 = tok0, u.nt = nt;
+        u.hk = static_cast<int>(at / nt);
+        u.kt = static_cast<int>(at - static_cast<long long>(u.hk) * nt);
+        const long long head_start = x_start + static_cast<long long>(u.hk) * nt;
+        u.k0 = static_cast<int>(max(t_lo - head_start, 0LL));
+        u.k1 = static_cast<int>(min(t_hi - head_start, static_cast<long long>(nt)));
+        u.tiles = min(u.k1 - u.kt, 32 / ppt);
+        t += u.tiles;
+        u.page = -1;
+        if (lane < u.tiles * ppt && u.kt * ppt + lane < cache8::pages_of(len, p.block_shift))
+          u.page = p.table[static_cast<size_t>(b) * p.table_cols + u.kt * ppt + lane];
+      };
+      auto load_scales = [&](Unit& u) {
+        const bool token = lane < u.tiles * ppt && u.kt * ppt + lane < cache8::pages_of(u.len, p.block_shift);
+        u.ks = u.vs = 0.f;
+        if (token && u.page >= 0 && u.page < p.num_blocks) {
+          u.ks = p.k_scale[static_cast<size_t>(u.page) * p.Hk + u.hk];
+          u.vs = p.v_scale[static_cast<size_t>(u.page) * p.Hk + u.hk];
+        } else {
+          if (token) atomicOr(p.err, kDevErrPage);
+          u.page = -1;
+        }
+      };
+      Unit cur, next;
+      next_unit(cur);
+      if (cur.tiles > 0) load_scales(cur);
+      int copies = 0, published = 0;
+      bool ok = true;
+      auto publish = [&](const Unit& u) {
+        const int s = published % C::NI;
+        if (published >= C::NI)
+          ok = wait_bounded(bar(C::B_IEMPTY + s), (published / C::NI - 1) & 1, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) {
+          int4* dst = reinterpret_cast<int4*>(smem + C::OFF_ITEM + s * C::ITEM_INTS * 4);
+          int slot = -1, cnt0 = 0, cnt1 = 0;
+          if (u.tiles > 0) {
+            const bool whole = u.k0 == 0 && u.k1 == u.nt;
+            if (!whole) slot = 2 * blockIdx.x + (u.k0 == 0 ? 1 : 0);
+            const int first = u.rb * kRows;
+            cnt0 = max(min(u.k1, chunk8::row_tiles(u.len, u.n, p.G, first, kHalf, p.causal)) - u.k0, 0);
+            cnt1 = max(min(u.k1, chunk8::row_tiles(u.len, u.n, p.G, first + kHalf, kHalf, p.causal)) - u.k0, 0);
+            if (!whole && u.k0 == 0) {
+              // begins here and ends in another CTA's run: joined by the second kernel
+              const long long last = t_hi - 1 + (u.nt - u.k1);
+              int* m = p.merge + blockIdx.x * 8;
+              m[1] = u.tok0, m[2] = u.n, m[3] = u.hk, m[4] = u.rb;
+              m[0] = chunk8::run_of(last, total, ctas);
+            }
+          }
+          dst[0] = make_int4(u.b, u.hk, u.rb, u.k0);
+          dst[1] = make_int4(u.tiles > 0 ? u.k1 - u.k0 : 0, u.n, u.len, u.tok0);
+          dst[2] = make_int4(cnt0, cnt1, slot, 0);
+          mbar_arrive(bar(C::B_IFULL + s));
+        }
+        ++published;
+      };
+      while (ok && cur.tiles > 0) {
+        if (cur.kt == cur.k0) publish(cur);
+        next_unit(next);
+        for (int i = 0; ok && i < cur.tiles; ++i) {
+          const int n_pages = min(ppt, cache8::pages_of(cur.len, p.block_shift) - (cur.kt + i) * ppt);
+          const int from = (i * ppt + lane) & 31;
+          const int page = __shfl_sync(0xffffffffu, cur.page, from);
+          const float ks = __shfl_sync(0xffffffffu, cur.ks, from), vs = __shfl_sync(0xffffffffu, cur.vs, from);
+          const bool mine = lane < n_pages && page >= 0;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * page_bytes;
+          const size_t at = mine ? (static_cast<size_t>(page) * p.Hk + cur.hk) * page_bytes : 0;
+#pragma unroll
+          for (int w = 0; w < 2; ++w, ++copies) {
+            const int st = copies % C::NST;
+            if (copies >= C::NST)
+              ok = wait_bounded(bar(C::B_CEMPTY + st), (copies / C::NST - 1) & 1, abort_flag, p.err, p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane < C::MAX_PPT)
+              reinterpret_cast<uint2*>(smem + C::OFF_SC)[st * C::MAX_PPT + lane] =
+                  mine ? scale_factors(w ? vs : ks) : make_uint2(0u, kOne2);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::B_CFULL + st), bytes);
+            __syncwarp();
+            if (mine)
+              bulk_load(sb + C::OFF_C + st * C::CODE_BYTES + lane * page_bytes, (w ? p.v_codes : p.k_codes) + at, page_bytes,
+                        bar(C::B_CFULL + st));
+          }
+          if (i == 0 && next.tiles > 0) load_scales(next);
+        }
+        cur = next;
+      }
+      if (ok) {  // no more items
+        cur.tiles = 0;
+        publish(cur);
+      }
+      // Every copy issued lands before the CTA may exit, whoever aborted.
+      for (int s = 0; s < C::NST && s < copies; ++s)
+        wait_drain(bar(C::B_CFULL + s), ((copies - 1 - s) / C::NST) & 1, p.err, p.timeout_ns);
+    } else if (warp == C::MMA_WARP) {
+      // ------------------------------------------------------------ MMA
+      constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
+      const uint64_t dQ0 = sdesc_sw128(sb + C::OFF_Q, 16, 1024);
+      const uint64_t dK0 = sdesc_sw128(sb + C::OFF_K, 16, 1024);
+      const uint64_t dV0 = sdesc_sw128(sb + C::OFF_V, C::BLK_BYTES, 1024);
+      auto issue_s = [&](int t, int ks) {
+        const uint64_t dQ = sdesc_add(dQ0, t * C::TILE_BYTES), dK = sdesc_add(dK0, ks * C::TILE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t koff = (kk / 4) * C::BLK_BYTES + (kk % 4) * 32;
+          mma_ss(tmem + C::S_COL(t), sdesc_add(dQ, koff), sdesc_add(dK, koff), idesc_s, kk > 0);
+        }
+      };
+      auto issue_pv = [&](int t, int vs, bool acc) {
+        const uint64_t dV = sdesc_add(dV0, vs * C::TILE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_ts(tmem + C::O_COL(t), tmem + C::S_COL(t) + kk * 8, sdesc_add(dV, kk * 2048), idesc_o,
+                 (acc || kk > 0) ? 1u : 0u);
+      };
+      bool ok = true;
+      auto wait = [&](int i, int phase) {
+        ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
+        return ok;
+      };
+      int tile = 0;                          // K and V tiles so far
+      int nq[2] = {0, 0}, np[2] = {0, 0};    // items and P tiles of each row tile so far
+      Item it;
+      while (ok && take_item(it)) {
+        if (lane == 0) {
+          const int cnt[2] = {it.cnt0, it.cnt1};
+          wait(C::B_KFULL + tile % C::NK, tile / C::NK);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (ok && cnt[t] > 0 && wait(C::B_Q + t, nq[t]++)) {
+              tc_fence_after();
+              issue_s(t, tile % C::NK);
+              tc_commit(bar(C::B_SFULL + t));
+            }
+          }
+          if (ok) tc_commit(bar(C::B_KEMPTY + tile % C::NK));
+          for (int j = 0; ok && j < it.tiles; ++j, ++tile) {
+            const int vs = tile % C::NV, ks1 = (tile + 1) % C::NK;
+            const bool more = j + 1 < it.tiles;
+            wait(C::B_VFULL + vs, tile / C::NV);
+            if (more) wait(C::B_KFULL + ks1, (tile + 1) / C::NK);
+            if (!ok) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (j < cnt[t]) {
+                if (!wait(C::B_PFULL + t, np[t]++)) break;
+                tc_fence_after();
+                issue_pv(t, vs, j > 0);
+                if (j + 1 == cnt[t]) tc_commit(bar(C::B_ODONE + t));
+              }
+              if (j + 1 < cnt[t]) {
+                issue_s(t, ks1);
+                tc_commit(bar(C::B_SFULL + t));
+              }
+            }
+            if (!ok) break;
+            tc_commit(bar(C::B_VEMPTY + vs));
+            if (more) tc_commit(bar(C::B_KEMPTY + ks1));
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (lane == 0) {  // every MMA issued so far must finish before tensor memory is released
+        tc_commit(bar(C::B_DRAIN));
+        wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
+      }
+    }
+  } else if (warp >= C::CONVERT_WARP) {
+    // ---------------------------------------------------------------- conversion
+    setmaxnreg_dec<C::REG_CONVERT>();
+    // A thread's 16-byte chunk of codes becomes two chunks of bf16.  The chunks of a
+    // quarter-warp lie in two rows, at d = 128 in the two halves of them: neither its
+    // reads nor its swizzled writes meet in a bank.
+    const int cw = warp - C::CONVERT_WARP;
+    int row0, chunk;  // of the first pass; a pass is ROWS rows
+    constexpr int CPR = D / 16, ROWS = 128 / CPR, PASSES = kKeys / ROWS;
+    if (D == 128) {
+      const int rb = (lane >> 2) & 1;
+      row0 = cw * 4 + ((lane >> 4) & 1) * 2 + rb;
+      chunk = (lane & 3) + 4 * (((lane >> 3) & 1) ^ rb);
+    } else {
+      row0 = cw * 8 + (lane >> 2);
+      chunk = lane & 3;
+    }
+    int copies = 0, tile = 0;
+    bool ok = true;
+    auto wait = [&](int i, int phase) {
+      ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    Item it;
+    while (ok && take_item(it)) {
+      for (int kt = it.k0; ok && kt < it.k0 + it.tiles; ++kt, ++tile) {
+        const int held = cache8::tokens_from(it.len, kt, kKeys, 0);  // tokens of the tile, if fewer than its rows
+#pragma unroll 1
+        for (int w = 0; w < 2; ++w, ++copies) {
+          const int st = copies % C::NST;
+          if (!wait(C::B_CFULL + st, copies / C::NST)) break;
+          const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES;
+          const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_SC) + st * C::MAX_PPT;
+          const int slot = tile % C::NK;
+          if (tile >= C::NK && !wait((w ? C::B_VEMPTY : C::B_KEMPTY) + slot, tile / C::NK - 1)) break;
+          uint8_t* out = smem + (w ? C::OFF_V : C::OFF_K) + slot * C::TILE_BYTES + (2 * chunk / 8) * C::BLK_BYTES;
+#pragma unroll
+          for (int i = 0; i < PASSES; ++i) {
+            const int row = row0 + i * ROWS;
+            uint4 c = *reinterpret_cast<const uint4*>(codes + row * D + chunk * 16);
+            if (row >= held) c = make_uint4(0u, 0u, 0u, 0u);  // slots without a token may hold anything
+            const uint2 f = factors[row >> p.block_shift];
+            const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              widen4(in[k], v[2 * k], v[2 * k + 1]);
+              v[2 * k] = mul_bf16x2(v[2 * k], f.x);
+              v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f.x);
+            }
+            if (f.y != kOne2) {  // a scale above 2^7: the factor does not fit one bf16 number
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = mul_bf16x2(v[k], f.y);
+            }
+            uint8_t* at = out + row * 128;
+            const int c0 = 2 * (chunk % 4);
+            *reinterpret_cast<uint4*>(at + ((c0 ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(at + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::B_CEMPTY + st));
+            mbar_arrive(bar((w ? C::B_VFULL : C::B_KFULL) + slot));
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax
+    setmaxnreg_inc<C::REG_SOFTMAX>();
+    const int t = warp / 4, wq = warp % 4, r = wq * 32 + lane;
+    const float c = p.scale_log2;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t tS = lane_addr + C::S_COL(t), tO = lane_addr + C::O_COL(t);
+    uint8_t* q_smem = smem + C::OFF_Q + t * C::TILE_BYTES;
+    // A warp moves its 32 rows between memory and their swizzled places 16 bytes a
+    // lane, RPP rows at a time.
+    constexpr int CH = D / 8, RPP = 32 / CH;
+    const int my_chunk = lane % CH, my_row = wq * 32 + lane / CH;
+    auto place = [&](int row, int ch) { return q_smem + (ch / 8) * C::BLK_BYTES + row * 128 + (((ch % 8) ^ (row & 7)) << 4); };
+    int np = 0, no = 0;  // tiles and items of this row tile so far
+    bool ok = true;
+    auto wait = [&](int i, int phase) {
+      ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    Item it;
+    while (ok && take_item(it)) {
+      const int cnt = t ? it.cnt1 : it.cnt0;
+      const int first = it.rb * kRows + t * kHalf, rows = it.n * p.G;
+      if (first >= rows) continue;
+      const int f = first + r;
+      const bool exists = f < rows;
+      const int tok = f / p.G, g = f - tok * p.G;
+      float m_ref = -CUDART_INF_F, l = 0.f;
+      bool far = false;  // (of the warp) some reference so large that c·m_ref is off by too much: subtracted first
+      if (cnt > 0) {
+        // ---- Q, its dimensions in the order of the converted codes
+#pragma unroll
+        for (int i0 = 0; i0 < 32 / RPP; i0 += 8) {
+          uint4 x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int from = (i0 + i) * RPP + lane / CH;
+            const int qt = __shfl_sync(0xffffffffu, tok, from), qg = __shfl_sync(0xffffffffu, g, from);
+            x[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (first + wq * 32 + from < rows)
+              x[i] = *reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(it.tok0 + qt) * p.ldq +
+                                                     static_cast<size_t>(it.hk * p.G + qg) * D + 8 * my_chunk);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 y = make_uint4(__byte_perm(x[i].x, x[i].y, 0x5410), __byte_perm(x[i].x, x[i].y, 0x7632),
+                                       __byte_perm(x[i].z, x[i].w, 0x5410), __byte_perm(x[i].z, x[i].w, 0x7632));
+            *reinterpret_cast<uint4*>(place(my_row + (i0 + i) * RPP, my_chunk)) = y;
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::B_Q + t));
+        // Keys the row sees, and the warpgroup's first row (which sees the fewest).
+        const int sees = exists ? chunk8::visible(it.len, it.n, tok, p.causal) : 0;
+        const int all_see = chunk8::visible(it.len, it.n, first / p.G, p.causal);
+        for (int j = 0; j < cnt; ++j, ++np) {
+          if (!wait(C::B_SFULL + t, np)) break;
+          tc_fence_after();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) tmem_ld32(tS + ch * 32, s[ch]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) reg_fence(s[ch]);
+          const int kv0 = (it.k0 + j) * kKeys;
+          if (all_see - kv0 < kKeys) {
+            const int end = sees - kv0;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (ch * 32 + i >= end) s[ch][i] = __float_as_uint(-CUDART_INF_F);
+          }
+          auto row_max = [&]() -> float {
+            float mx[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = -CUDART_INF_F;
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                mx[i & 3] = fmax3(mx[i & 3], __uint_as_float(s[ch][2 * i]), __uint_as_float(s[ch][2 * i + 1]));
+            return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          };
+          // P = 2^(c·s − c·m_ref) as bf16 over S; returns the tile's row sum.
+          auto p_pass = [&]() -> float {
+            const float mc = (far || m_ref == -CUDART_INF_F) ? 0.f : m_ref * c;
+            const uint64_t c2 = f2_pack(c, c), nmc2 = f2_pack(-mc, -mc);
+            uint64_t ls2[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ls2[k] = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float x0, x1;
+                f2_unpack(ffma2(f2_pack(__uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1])), c2, nmc2),
+                          x0, x1);
+                const float p0 = ex2_approx(x0);
+                const float p1 = ex2_approx(x1);
+                ls2[e & 3] = fadd2(ls2[e & 3], f2_pack(p0, p1));
+                pk[e] = pack_bf16x2(p0, p1);
+              }
+              tmem_st16(tS + ch * 16, pk);
+            }
+            float ls[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f2_unpack(ls2[k], ls[2 * k], ls[2 * k + 1]);
+            return ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+          };
+          // With scores so large, c·s − c·m_ref as one FMA would leave the rounding of
+          // c·m_ref, up to 2^-24 of it, in the exponent.
+          auto subtract = [&](float by) {
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[ch][i] = __float_as_uint(__uint_as_float(s[ch][i]) - by);
+          };
+          auto set_far = [&]() {
+            far = __any_sync(0xffffffffu, m_ref != -CUDART_INF_F && !(fabsf(m_ref * c) < 0x1p20f));
+          };
+          float base = 0.f;  // what has been subtracted from s
+          if (j == 0) {
+            m_ref = row_max();
+            set_far();
+          }
+          if (far) {
+            base = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+            subtract(base);
+          }
+          float lt = p_pass();
+          if (__any_sync(0xffffffffu, !(lt < 0x1p40f))) {
+            const float m_new = fmaxf(m_ref, base + row_max());
+            const float alpha = (m_ref == -CUDART_INF_F) ? 0.f : ex2_approx((m_ref - m_new) * c);
+            m_ref = m_new;
+            l *= alpha;
+            set_far();
+            if (far) subtract(m_ref == -CUDART_INF_F ? 0.f : m_ref - base);
+            else if (base != 0.f) subtract(-base);
+#pragma unroll 1
+            for (int ch = 0; j > 0 && ch < D / 16; ++ch) {
+              uint32_t o[16];
+              tmem_ld16(tO + ch * 16, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + ch * 16, o);
+            }
+            tmem_wait_st();
+            lt = p_pass();
+          }
+          l += lt;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(C::B_PFULL + t));
+        }
+        if (!ok || !wait(C::B_ODONE + t, no++)) break;
+        tc_fence_after();
+      }
+      const size_t part = static_cast<size_t>(it.slot < 0 ? 0 : it.slot) * kRows + t * kHalf + r;
+      if (it.slot < 0) {
+        // ---- O / l, staged over Q (which no MMA reads any more), out by whole rows
+        const float inv_l = l > 0.f ? 1.0f / l : 0.f;
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          tmem_ld32(tO + cb * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {  // a 16-byte chunk; its dimensions change places again
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t* q4 = o + 8 * u + 4 * e;
+              w[2 * e] = pack_bf16x2(__uint_as_float(q4[0]) * inv_l, __uint_as_float(q4[2]) * inv_l);
+              w[2 * e + 1] = pack_bf16x2(__uint_as_float(q4[1]) * inv_l, __uint_as_float(q4[3]) * inv_l);
+            }
+            *reinterpret_cast<uint4*>(place(r, cb * 4 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32 / RPP; ++i) {
+          const int from = i * RPP + lane / CH;
+          const int qt = __shfl_sync(0xffffffffu, tok, from), qg = __shfl_sync(0xffffffffu, g, from);
+          const uint4 y = *reinterpret_cast<const uint4*>(place(my_row + i * RPP, my_chunk));
+          if (first + wq * 32 + from < rows)
+            *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(it.tok0 + qt) * p.H + it.hk * p.G + qg) * D + 8 * my_chunk) = y;
+        }
+        __syncwarp();
+        if (exists)
+          p.lse[static_cast<size_t>(it.hk * p.G + g) * p.total + it.tok0 + tok] =
+              l > 0.f ? (m_ref * c + log2f(l)) * kLn2 : -CUDART_INF_F;
+      } else if (exists) {
+        reinterpret_cast<float2*>(p.ml_part)[part] = make_float2(l > 0.f ? m_ref * c : -CUDART_INF_F, l);
+      }
+      if (it.slot >= 0 && cnt > 0) {
+        // ---- a partial: four dimensions of 32 rows side by side
+        float4* dst = reinterpret_cast<float4*>(p.o_part) + static_cast<size_t>(it.slot) * (kRows * D / 4) + t * kHalf + r;
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          tmem_ld32(tO + cb * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (exists)
+              dst[(cb * 8 + u) * kRows] = make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 2]),
+                                                      __uint_as_float(o[4 * u + 1]), __uint_as_float(o[4 * u + 3]));
+        }
+        tc_fence_before();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the partials of the item that begins in CTA blockIdx.x's run and ends in
+// another's, in the order of the keys.  A warp takes 8 rows by 4 groups of four
+// dimensions: whole sectors of the partials and of O.
+constexpr int kMergeThreads = 256, kMergeRows = 32;
+
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) fa_chunk8_merge_kernel(const Chunk8Params p) {
+  grid_dependency_wait();
+  const int c0 = blockIdx.x;
+  const int* m = p.merge + c0 * 8;
+  const int c1 = m[0];
+  if (c1 < 0) return;
+  const int tok0 = m[1], n = m[2], hk = m[3], rb = m[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float2* ml = reinterpret_cast<const float2*>(p.ml_part);
+  const float4* part = reinterpret_cast<const float4*>(p.o_part);
+  auto slot = [&](int c) { return static_cast<size_t>(2 * c + (c == c0 ? 1 : 0)); };
+  for (int w = warp; w < (kMergeRows / 8) * (D / 16); w += kMergeThreads / 32) {
+    const int row = blockIdx.y * kMergeRows + (w % (kMergeRows / 8)) * 8 + lane % 8;
+    const int d4 = (w / (kMergeRows / 8)) * 4 + lane / 8;
+    const int f = rb * kRows + row;
+    if (f >= n * p.G) continue;
+    float top = -CUDART_INF_F;
+    for (int c = c0; c <= c1; ++c) top = fmaxf(top, ml[slot(c) * kRows + row].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float2 s = ml[slot(c) * kRows + row];
+      if (s.x == -CUDART_INF_F) continue;  // the row sees none of its keys
+      const float wt = ex2_approx(s.x - top);
+      const float4 v = part[(slot(c) * (D / 4) + d4) * kRows + row];
+      l = fmaf(wt, s.y, l);
+      o.x = fmaf(wt, v.x, o.x), o.y = fmaf(wt, v.y, o.y);
+      o.z = fmaf(wt, v.z, o.z), o.w = fmaf(wt, v.w, o.w);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int tok = f / p.G, h = hk * p.G + f - tok * p.G;
+    *reinterpret_cast<uint2*>(p.o + (static_cast<size_t>(tok0 + tok) * p.H + h) * D + 4 * d4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (d4 == 0)
+      p.lse[static_cast<size_t>(h) * p.total + tok0 + tok] = l > 0.f ? (top + log2f(l)) * kLn2 : -CUDART_INF_F;
+  }
+}
+
+template <int D>
+cudaError_t launch_chunk(const Chunk8Params& p, int ctas, bool merge, cudaStream_t s) {
+  using C = ChunkCfg<D>;
+  static SmemLimit smem_limit;
+  cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_chunk8_kernel<D>), C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  // The softmax warps' larger share of registers comes out of what the CTA was
+  // launched with: with fewer the kernel would wait for it without end.
+  static const int launch_regs = [] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(fa_chunk8_kernel<D>)) == cudaSuccess ? a.numRegs : 0;
+  }();
+  if (launch_regs != 128) return cudaErrorInvalidConfiguration;
+  e = launch_kernel(fa_chunk8_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(C::NUM_THREADS), C::SMEM_BYTES, s, true, p);
+  if (e != cudaSuccess || !merge) return e;
+  return launch_kernel(fa_chunk8_merge_kernel<D>, dim3(static_cast<unsigned>(ctas), kRows / kMergeRows),
+                       dim3(kMergeThreads), 0, s, true, p);
+}
+
+}  // namespace
+
+cudaError_t launch_cache8_chunk(int d, const Chunk8Params& p, int ctas, bool merge, cudaStream_t s) {
+  return d == 64 ? launch_chunk<64>(p, ctas, merge, s) : launch_chunk<128>(p, ctas, merge, s);
+}
+
+}  // namespace fa

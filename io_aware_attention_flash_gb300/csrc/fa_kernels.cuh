@@ -194,6 +194,45 @@ struct Cache8StoreParams {
   uint32_t* err;
 };
 
+// Rotary positions (fa_rotary.cu).
+struct RotaryParams {
+  const uint64_t* turns;  // [pairs] frequency as a fraction of a turn, 64-bit fixed point
+  const int* axis;        // [pairs] position axis of each pair (not read where there is one axis)
+  const int* positions;   // [axes, total], or nullptr in the append: a token's place in its sequence
+  int pairs, axes, interleaved, inverse;
+};
+// Rows to turn: bf16 [total, heads, d], those of src ld elements apart (src1 may have no heads).
+struct TurnRows {
+  const uint16_t *src0, *src1;
+  long long ld0, ld1;
+  uint16_t *dst0, *dst1;
+  int heads0, heads1;
+};
+
+// Attention of a chunk of new tokens over the cache (fa_chunk8.cu).
+struct Chunk8Params {
+  const uint16_t* q;      // bf16 [total, H, d], rows ldq elements apart
+  long long ldq;
+  uint16_t* o;            // bf16 [total, H, d]
+  float* lse;             // fp32 [H, total]
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  const float* k_scale;
+  const float* v_scale;
+  const int* table;
+  const int* cu_seqlens;  // [B + 1] new tokens' rows
+  const int* seqlens;     // [B] cached tokens, the new ones among them
+  float* o_part;          // fp32 [2 · CTAs][d / 4][256 rows][4]
+  float* ml_part;         // fp32 [2 · CTAs][256 rows][2]
+  int* merge;             // [CTAs][8]: the item that begins in a CTA's run and ends in another's
+  int B, total, H, Hk, G, num_blocks, table_cols, block_shift, max_new, max_seqlen;
+  int row_blocks;         // of a sequence, at most
+  int causal, zero_tail;
+  float scale_log2;
+  uint32_t* err;
+  uint64_t timeout_ns;
+};
+
 struct Cache8DecodeParams {
   const uint16_t* q;      // bf16 [B, Nq, H, d]
   uint16_t* o;
@@ -306,6 +345,10 @@ cudaError_t launch_cache8_store(int d, int block, const Cache8StoreParams& p, cu
 void cache8_plan(int d, int rows_total, int* groups, int* rows, int* tokens);
 cudaError_t launch_cache8_decode(int d, const CUtensorMap& tk, const CUtensorMap& tv, const Cache8DecodeParams& p,
                                  int ctas, cudaStream_t s);
+cudaError_t launch_rotary(int d, const RotaryParams& r, const TurnRows& x, int total, cudaStream_t s);
+cudaError_t launch_cache8_append(int d, int block, const Cache8StoreParams& p, const RotaryParams& r, const TurnRows& x,
+                                 int zero_tail, cudaStream_t s);
+cudaError_t launch_cache8_chunk(int d, const Chunk8Params& p, int ctas, bool merge, cudaStream_t s);
 cudaError_t launch_wait_timeout_selftest(uint32_t* err, uint64_t limit_ns, cudaStream_t s);
 cudaError_t run_microbench(int which, int iters, uint32_t* err, double* result, cudaStream_t s);
 

@@ -1,0 +1,405 @@
+// Rotary positions for sm_103a: queries and keys turned by their tokens'
+// positions, and the append to the 8-bit paged cache that turns the keys (and
+// the call's queries) on the way.
+//
+// Pair j of a head's dimensions, (a, b), becomes (a cos t - b sin t, b cos t +
+// a sin t), t = position · frequency_j; a token may have several positions
+// (time, height, width), and each pair belongs to one of them.  The inverse, which
+// is also the gradient (the turn is orthogonal), takes -t.
+//
+// Angles.  A frequency is kept as a fraction of a turn in 64-bit fixed point, F =
+// round(frequency / 2 pi · 2^64), so the angle of an integer position is the low 64
+// bits of position · F, whole turns falling off the top: exact but for F's own
+// rounding, 2^31 · 2^-65 turns at the furthest position.  Its upper 32 bits as a
+// signed fraction go to sincospif, which needs no reduction of its argument.  One
+// sine and cosine serves a token's pair in all heads.
+//
+// Both kernels are bound by DRAM: each element is read once and written once.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include "e4m3.cuh"
+#include "fa_kernels.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+// Cosine and sine of pair j at position pos.
+__device__ __forceinline__ float2 cos_sin(const RotaryParams& r, int j, int pos) {
+  const uint64_t turn = r.turns[j] * static_cast<uint64_t>(static_cast<long long>(pos));
+  float s, c;
+  sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &s, &c);
+  return make_float2(c, r.inverse ? -s : s);
+}
+
+// Axis of pair j, within the axes there are.
+__device__ __forceinline__ int axis_of(const RotaryParams& r, int j) {
+  return r.axes == 1 ? 0 : min(max(r.axis[j], 0), r.axes - 1);
+}
+// Position of token `row` on the axis of pair j.
+__device__ __forceinline__ int position_of(const RotaryParams& r, int j, int row, int total) {
+  return r.positions[static_cast<size_t>(axis_of(r, j)) * total + row];
+}
+
+// A head's dimensions are taken in units of two 16-byte chunks that hold eight
+// whole pairs: unit u is chunks u and u + pairs / 8 where a pair has one element in
+// each half, chunks 2u and 2u + 1 where pairs are neighbours and behind the turned
+// dimensions.
+template <bool IL>
+__device__ __forceinline__ void unit_chunks(int u, int pairs, int& c0, int& c1) {
+  const bool halves = !IL && 8 * u < pairs;
+  c0 = halves ? u : 2 * u;
+  c1 = halves ? u + pairs / 8 : 2 * u + 1;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& x, float* v) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = bf16lo_to_f32(w[i]);
+    v[2 * i + 1] = bf16hi_to_f32(w[i]);
+  }
+}
+
+// The unit's sixteen elements in 32 bits, turned: y[0..7] its first chunk.
+template <bool IL>
+__device__ __forceinline__ void turn_unit(const uint4& x0, const uint4& x1, const float2 (&cs)[8], float (&y)[16]) {
+  unpack8(x0, y);
+  unpack8(x1, y + 8);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int i = IL ? 2 * e : e, j = IL ? 2 * e + 1 : e + 8;
+    const float a = y[i], b = y[j];
+    y[i] = fmaf(a, cs[e].x, -(b * cs[e].y));
+    y[j] = fmaf(b, cs[e].x, a * cs[e].y);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Rows [tok0, tok0 + n) of one or two tensors, turned by the angles cs[token][pair].
+// A thread keeps its unit of the head and goes through the heads of one token after
+// another, two units in flight.
+template <int D, bool IL, int NT>
+__device__ __forceinline__ void turn_rows(const TurnRows& x, int tok0, int n, const float2* cs, int pairs) {
+  constexpr int U = D / 16, SWEEP = NT / U;
+  const int u = threadIdx.x % U, heads = x.heads0 + x.heads1;
+  const bool turned = 8 * u < pairs;
+  int c0, c1;
+  unit_chunks<IL>(u, pairs, c0, c1);
+  int tok = 0, h = threadIdx.x / U;
+  auto settle = [&]() {
+    while (h >= heads && tok < n) {
+      h -= heads;
+      ++tok;
+    }
+  };
+  struct Unit {
+    uint4 a, b;
+    uint16_t* dst;
+    int tok;
+  };
+  auto load = [&](Unit& w) -> bool {
+    if (tok >= n) return false;
+    const bool first = h < x.heads0;
+    const int head = first ? h : h - x.heads0;
+    const long long row = tok0 + tok;
+    const uint16_t* src = (first ? x.src0 + row * x.ld0 : x.src1 + row * x.ld1) + head * D;
+    w.dst = (first ? x.dst0 + row * x.heads0 * D : x.dst1 + row * x.heads1 * D) + head * D;
+    w.a = *reinterpret_cast<const uint4*>(src + 8 * c0);
+    w.b = *reinterpret_cast<const uint4*>(src + 8 * c1);
+    w.tok = tok;
+    h += SWEEP;
+    settle();
+    return true;
+  };
+  auto finish = [&](const Unit& w) {
+    uint4 a = w.a, b = w.b;
+    if (turned) {
+      float2 c[8];
+      float y[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) c[e] = cs[w.tok * pairs + 8 * u + e];
+      turn_unit<IL>(a, b, c, y);
+      a = pack8(y);
+      b = pack8(y + 8);
+    }
+    *reinterpret_cast<uint4*>(w.dst + 8 * c0) = a;
+    *reinterpret_cast<uint4*>(w.dst + 8 * c1) = b;
+  };
+  settle();
+  Unit w0, w1;
+  while (load(w0)) {
+    const bool more = load(w1);
+    finish(w0);
+    if (more) finish(w1);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// Queries and keys of a packed batch
+// ----------------------------------------------------------------------------
+constexpr int kTurnThreads = 256, kTurnTokens = 4;  // a block's tokens: one angle a thread at 64 pairs
+
+template <int D, bool IL>
+__global__ void __launch_bounds__(kTurnThreads) fa_rotary_kernel(const RotaryParams r, const TurnRows x, int total) {
+  __shared__ float2 cs[kTurnTokens * (D / 2)];
+  grid_dependency_wait();  // scheduled while the kernel before it in the stream finishes
+  const int tok0 = blockIdx.x * kTurnTokens;
+  const int n = min(kTurnTokens, total - tok0);
+  for (int i = threadIdx.x; i < n * r.pairs; i += kTurnThreads) {
+    const int t = i / r.pairs, j = i - t * r.pairs;
+    cs[i] = cos_sin(r, j, position_of(r, j, tok0 + t, total));
+  }
+  __syncthreads();
+  turn_rows<D, IL, kTurnThreads>(x, tok0, n, cs, r.pairs);
+}
+
+// ----------------------------------------------------------------------------
+// Append to the cache
+// ----------------------------------------------------------------------------
+// The first blocks take a page's new tokens and up to HG heads of K or of V; the
+// others turn the queries.  A thread owns one or two units (token, two chunks) of
+// the page in every head of its block, so a unit's eight sines and cosines are
+// formed once; the input stays in registers between the largest magnitude and the
+// rounding.  Keys are turned in 32 bits and rounded once, to their codes.
+template <int D, int BLOCK>
+struct AppendCfg {
+  static constexpr int U = D / 16, UNITS = BLOCK * U;
+  static constexpr int NT = UNITS < 128 ? 128 : UNITS > 512 ? 512 : UNITS;
+  static constexpr int NU = UNITS <= NT ? 1 : UNITS / NT;
+  static constexpr int HG = 4 / NU;        // heads of a block
+  static constexpr int TOKENS = NT / 64;   // queries' tokens of a block
+};
+
+template <int D, int BLOCK, bool IL>
+__global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT) fa_cache8_append_kernel(const Cache8StoreParams p,
+                                                                                   const RotaryParams r,
+                                                                                   const TurnRows x, int store_blocks,
+                                                                                   int zero_tail) {
+  using C = AppendCfg<D, BLOCK>;
+  constexpr int NT = C::NT, NU = C::NU, HG = C::HG, U = C::U;
+  __shared__ float2 cs[C::TOKENS * (D / 2)];
+  __shared__ int where[C::TOKENS];
+  __shared__ uint32_t warp_max[HG][NT / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();  // scheduled while the kernel before it in the stream finishes
+  if (static_cast<int>(blockIdx.x) >= store_blocks) {
+    // ---- queries
+    const int end = min(max(p.cu_seqlens[p.B], 0), p.total);
+    const int tok0 = (static_cast<int>(blockIdx.x) - store_blocks) * C::TOKENS;
+    const int n = min(C::TOKENS, end - tok0);  // of them before the end of the last sequence
+    if (!r.positions && static_cast<int>(threadIdx.x) < n) {
+      // the token's sequence: the last one that begins at or before it
+      const int row = tok0 + threadIdx.x;
+      int lo = 0, hi = p.B - 1;
+      while (lo < hi) {
+        const int mid = lo + (hi - lo + 1) / 2;
+        if (p.cu_seqlens[mid] <= row) lo = mid;
+        else hi = mid - 1;
+      }
+      where[threadIdx.x] = static_cast<int>(static_cast<uint32_t>(p.start[lo]) + static_cast<uint32_t>(row) -
+                                            static_cast<uint32_t>(p.cu_seqlens[lo]));
+    }
+    if (!r.positions) __syncthreads();
+    for (int i = threadIdx.x; i < n * r.pairs; i += NT) {
+      const int t = i / r.pairs, j = i - t * r.pairs;
+      cs[i] = cos_sin(r, j, r.positions ? position_of(r, j, tok0 + t, p.total) : where[t]);
+    }
+    __syncthreads();
+    turn_rows<D, IL, NT>(x, tok0, n, cs, r.pairs);
+    if (zero_tail) {
+      for (int t = max(n, 0); t < C::TOKENS && tok0 + t < p.total; ++t) {
+        uint4* row = reinterpret_cast<uint4*>(x.dst0 + static_cast<long long>(tok0 + t) * x.heads0 * D);
+        for (int i = threadIdx.x; i < x.heads0 * (D / 8); i += NT) row[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+    return;
+  }
+  // ---- keys or values of one page
+  const int groups = (p.Hk + HG - 1) / HG;
+  const int id = blockIdx.x, at = id / (2 * groups), g = id - at * 2 * groups;
+  const bool is_v = g >= groups;
+  const int h0 = (is_v ? g - groups : g) * HG, heads = min(HG, p.Hk - h0);
+  const int b = at / p.blocks, nth = at - b * p.blocks;
+  const int first = min(max(p.cu_seqlens[b], 0), p.total);
+  const int count = min(max(p.cu_seqlens[b + 1], first), p.total) - first;
+  const int start = p.start[b];
+  const long long end = static_cast<long long>(start) + min(count, p.max_new);
+  const long long blk = static_cast<long long>(start) / BLOCK + nth;
+  const long long base = blk * BLOCK;
+  if (start < 0 || count == 0 || base >= end) {
+    if (start < 0 && count > 0 && threadIdx.x == 0) atomicOr(p.err, kDevErrPage);
+    return;
+  }
+  const int page = blk < p.table_cols ? p.table[static_cast<size_t>(b) * p.table_cols + blk] : -1;
+  const int old = static_cast<int>(max(0LL, start - base));  // tokens [0, old) are held, [old, hi) are new
+  const int hi = static_cast<int>(min(end - base, static_cast<long long>(BLOCK)));
+  const int src = first + static_cast<int>(base - start);  // input row of slot 0
+  const long long ld = is_v ? p.ldv : p.ldk;
+  const int u = threadIdx.x % U;
+  int c0, c1;
+  if (is_v) c0 = 2 * u, c1 = 2 * u + 1;
+  else unit_chunks<IL>(u, r.pairs, c0, c1);
+  const bool turned = !is_v && 8 * u < r.pairs;
+  int tok[NU];
+  bool fresh[NU];
+#pragma unroll
+  for (int n = 0; n < NU; ++n) {
+    tok[n] = (threadIdx.x + n * NT) / U;
+    fresh[n] = tok[n] >= old && tok[n] < hi;
+  }
+  uint4 raw[HG][NU][2];
+#pragma unroll
+  for (int h = 0; h < HG; ++h)
+#pragma unroll
+    for (int n = 0; n < NU; ++n) {
+      raw[h][n][0] = raw[h][n][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (fresh[n] && h < heads) {
+        const uint16_t* row = (is_v ? p.v : p.k) + (static_cast<long long>(src) + tok[n]) * ld + (h0 + h) * D;
+        raw[h][n][0] = *reinterpret_cast<const uint4*>(row + 8 * c0);
+        raw[h][n][1] = *reinterpret_cast<const uint4*>(row + 8 * c1);
+      }
+    }
+  const bool live = page >= 0 && page < p.num_blocks;
+  if (!live) {
+    if (threadIdx.x == 0) atomicOr(p.err, kDevErrPage);
+    return;
+  }
+  float2 angle[NU][8];
+#pragma unroll
+  for (int n = 0; n < NU; ++n)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      angle[n][e] = make_float2(1.f, 0.f);
+      if (turned && fresh[n]) {
+        const int j = 8 * u + e;
+        angle[n][e] = cos_sin(r, j, r.positions ? position_of(r, j, src + tok[n], p.total)
+                                                : static_cast<int>(base + tok[n]));
+      }
+    }
+  const size_t ph = static_cast<size_t>(page) * p.Hk + h0;
+  float* scale = (is_v ? p.v_scale : p.k_scale) + ph;
+  auto values = [&](int h, int n, float (&y)[16]) {
+    if (turned) {
+      turn_unit<IL>(raw[h][n][0], raw[h][n][1], angle[n], y);
+    } else {
+      unpack8(raw[h][n][0], y);
+      unpack8(raw[h][n][1], y + 8);
+    }
+  };
+  float held[HG];
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    held[h] = old > 0 && h < heads ? scale[h] : 0.f;
+    // Infinities and NaN do not set the scale: the maximum passes over NaN; where it
+    // is infinite, once more without.
+    auto largest = [&](bool finite) {
+      float top = 0.f;
+#pragma unroll
+      for (int n = 0; n < NU; ++n) {
+        float y[16];
+        values(h, n, y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float a = fabsf(y[i]);
+          top = fmaxf(top, finite && !(a < CUDART_INF_F) ? 0.f : a);
+        }
+      }
+      return top;
+    };
+    float top = largest(false);
+    if (top == CUDART_INF_F) top = largest(true);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    if (lane == 0) warp_max[h][warp] = m;
+  }
+  __syncthreads();  // (every thread has read the scales held before one of them writes the new ones)
+#pragma unroll
+  for (int h = 0; h < HG; ++h) {
+    if (h >= heads) break;
+    const uint32_t amax = __reduce_max_sync(0xffffffffu, lane < NT / 32 ? warp_max[h][lane] : 0u);
+    const float s = fmaxf(exp2_int(scale_exponent_f32(amax, kScaleFloor)), held[h]);
+    const float inv = exp2_int(127 - static_cast<int>((__float_as_uint(s) >> 23) & 255u));  // 1 / s, a power of two
+    const bool again = s > held[h];
+    if (threadIdx.x == 0 && again) scale[h] = s;
+    uint8_t* out = (is_v ? p.v_codes : p.k_codes) + (ph + h) * (BLOCK * D);
+#pragma unroll
+    for (int n = 0; n < NU; ++n) {
+      uint2* a = reinterpret_cast<uint2*>(out + tok[n] * D + 8 * c0);
+      uint2* z = reinterpret_cast<uint2*>(out + tok[n] * D + 8 * c1);
+      if (fresh[n]) {
+        float y[16];
+        values(h, n, y);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) y[i] *= inv;
+        *a = make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+        *z = make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11]), pack_e4m3x4(y[12], y[13], y[14], y[15]));
+      } else if (tok[n] < old && again) {
+        // tokens held at a smaller scale are rounded again
+        const float f = held[h] * inv;
+        const uint2 code[2] = {*a, *z};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float v[4], w[4];
+          unpack_e4m3x4(code[k].x, v);
+          unpack_e4m3x4(code[k].y, w);
+          *(k ? z : a) = make_uint2(pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
+                                    pack_e4m3x4(w[0] * f, w[1] * f, w[2] * f, w[3] * f));
+        }
+      }
+    }
+  }
+}
+
+template <int D, int BLOCK, bool IL>
+cudaError_t launch_append(const Cache8StoreParams& p, const RotaryParams& r, const TurnRows& x, int zero_tail,
+                          cudaStream_t s) {
+  using C = AppendCfg<D, BLOCK>;
+  const long long groups = (p.Hk + C::HG - 1) / C::HG;
+  const long long store = static_cast<long long>(p.B) * p.blocks * 2 * groups;
+  const long long turn = (p.total + C::TOKENS - 1) / C::TOKENS;
+  if (store + turn > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return launch_kernel(fa_cache8_append_kernel<D, BLOCK, IL>, dim3(static_cast<unsigned>(store + turn)), dim3(C::NT), 0, s,
+                       true, p, r, x, static_cast<int>(store), zero_tail);
+}
+
+template <int D, int BLOCK>
+cudaError_t launch_append_il(const Cache8StoreParams& p, const RotaryParams& r, const TurnRows& x, int zero_tail,
+                             cudaStream_t s) {
+  return r.interleaved ? launch_append<D, BLOCK, true>(p, r, x, zero_tail, s)
+                       : launch_append<D, BLOCK, false>(p, r, x, zero_tail, s);
+}
+
+template <int D>
+cudaError_t launch_append_d(int block, const Cache8StoreParams& p, const RotaryParams& r, const TurnRows& x,
+                            int zero_tail, cudaStream_t s) {
+  if (block == 16) return launch_append_il<D, 16>(p, r, x, zero_tail, s);
+  if (block == 32) return launch_append_il<D, 32>(p, r, x, zero_tail, s);
+  if (block == 64) return launch_append_il<D, 64>(p, r, x, zero_tail, s);
+  return launch_append_il<D, 128>(p, r, x, zero_tail, s);
+}
+
+template <int D>
+cudaError_t launch_rotary_d(const RotaryParams& r, const TurnRows& x, int total, cudaStream_t s) {
+  const dim3 grid((total + kTurnTokens - 1) / kTurnTokens), block(kTurnThreads);
+  return r.interleaved ? launch_kernel(fa_rotary_kernel<D, true>, grid, block, 0, s, true, r, x, total)
+                       : launch_kernel(fa_rotary_kernel<D, false>, grid, block, 0, s, true, r, x, total);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(int d, const RotaryParams& r, const TurnRows& x, int total, cudaStream_t s) {
+  return d == 64 ? launch_rotary_d<64>(r, x, total, s) : launch_rotary_d<128>(r, x, total, s);
+}
+
+cudaError_t launch_cache8_append(int d, int block, const Cache8StoreParams& p, const RotaryParams& r, const TurnRows& x,
+                                 int zero_tail, cudaStream_t s) {
+  return d == 64 ? launch_append_d<64>(block, p, r, x, zero_tail, s) : launch_append_d<128>(block, p, r, x, zero_tail, s);
+}
+
+}  // namespace fa

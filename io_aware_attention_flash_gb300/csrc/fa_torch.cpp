@@ -1,4 +1,4 @@
-// Calls of the grouped-head and 8-bit cache entry points from PyTorch without
+// Calls of the grouped-head, 8-bit cache and rotary entry points from PyTorch without
 // the interpreter in between: what the Python helpers of the same names do
 // (check the tensors, allocate the outputs and the workspace, call the C ABI on
 // the current stream), for the plain case in which all arguments are in order.
@@ -399,10 +399,258 @@ PyObject* py_decode_cache8(PyObject*, PyObject* const* args, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// ----------------------------------------------------------------------------
+// Rotary positions
+// ----------------------------------------------------------------------------
+struct Turn {
+  const Tensor *turns, *axis;
+  int pairs, axes;
+  bool interleaved;
+};
+
+bool turn_tensors(const Tensor& turns, const Tensor& axis, int axes, int64_t d, int dev, Turn* r) {
+  if (turns.dim() != 1) return false;
+  const int64_t pairs = turns.size(0);
+  r->turns = &turns, r->axis = &axis, r->axes = axes, r->pairs = static_cast<int>(pairs);
+  return pairs > 0 && pairs % 8 == 0 && 2 * pairs <= d && axes >= 1 && axes <= pairs &&
+         dense(turns, at::kLong, {pairs}, dev) && dense(axis, at::kInt, {pairs}, dev);
+}
+
+bool turn_args(PyObject* rotary, int64_t d, int dev, Turn* r) {
+  if (!PyTuple_Check(rotary) || PyTuple_GET_SIZE(rotary) != 4) return false;
+  const Tensor *turns = tensor(PyTuple_GET_ITEM(rotary, 0)), *axis = tensor(PyTuple_GET_ITEM(rotary, 1));
+  int axes = 0;
+  const int il = PyObject_IsTrue(PyTuple_GET_ITEM(rotary, 3));
+  if (il < 0) PyErr_Clear();
+  if (il < 0 || !turns || !axis || !to_int(PyTuple_GET_ITEM(rotary, 2), &axes)) return false;
+  r->interleaved = il != 0;
+  return turn_tensors(*turns, *axis, axes, d, dev, r);
+}
+
+// positions: int32 [axes, T], or [T] with one axis.
+bool positions_ok(const Tensor& t, int axes, int64_t T, int dev) {
+  return (axes == 1 && t.dim() == 1) ? dense(t, at::kInt, {T}, dev) : dense(t, at::kInt, {axes, T}, dev);
+}
+
+struct Rows {
+  int dev, T, H, Hk, d;
+  int64_t ldq, ldk;
+};
+
+bool check_rows(const Tensor& q, const Tensor& k, Rows* r) {
+  if (!q.is_cuda() || q.dim() != 3 || k.dim() != 3) return false;
+  r->dev = q.get_device();
+  const int64_t T = q.size(0), H = q.size(1), d = q.size(2), Hk = k.size(1);
+  if (!fits(T) || !fits(H) || !fits(d) || !fits(Hk)) return false;
+  r->T = static_cast<int>(T), r->H = static_cast<int>(H), r->d = static_cast<int>(d), r->Hk = static_cast<int>(Hk);
+  r->ldq = rows_stride(q, T, H, d, r->dev);
+  r->ldk = rows_stride(k, T, Hk, d, r->dev);
+  return r->ldq > 0 && r->ldk > 0;
+}
+
+const uint64_t* turns_ptr(const Turn& t) { return static_cast<const uint64_t*>(t.turns->data_ptr()); }
+const int* ints(const Tensor& t) { return static_cast<const int*>(t.data_ptr()); }
+
+fa_status turn(const Rows& r, const Turn& t, const Tensor& q, const Tensor& k, const Tensor& positions, bool inverse,
+               Tensor* q_out, Tensor* k_out) {
+  const auto opt = q.options().requires_grad(false);
+  *q_out = at::empty({r.T, r.H, r.d}, opt);
+  *k_out = at::empty({r.T, r.Hk, r.d}, opt);
+  return fa_rotary(q.data_ptr(), k.data_ptr(), q_out->data_ptr(), k_out->data_ptr(), ints(positions), turns_ptr(t),
+                   ints(*t.axis), r.T, r.H, r.Hk, r.d, t.pairs, t.axes, t.interleaved, inverse, r.ldq, r.ldk,
+                   stream_of(r.dev));
+}
+
+// (q, k, positions, rotary) of `args`.
+bool rotary_args(PyObject* const* args, const Tensor* (&t)[3], Rows* r, Turn* turn) {
+  if (recording()) return false;
+  for (int i = 0; i < 3; ++i)
+    if (!(t[i] = tensor(args[i]))) return false;
+  return check_rows(*t[0], *t[1], r) && turn_args(args[3], r->d, r->dev, turn) &&
+         positions_ok(*t[2], turn->axes, r->T, r->dev);
+}
+
+// (q, k, positions, rotary, inverse) -> (q', k')
+PyObject* py_rotary(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    const Tensor* t[3];
+    Rows r;
+    Turn plan;
+    if (n == 5 && rotary_args(args, t, &r, &plan)) {
+      const bool inverse = args[4] == Py_True;
+      Tensor q, k;
+      fa_status st;
+      {
+        WithoutLock unlocked;
+        st = turn(r, plan, *t[0], *t[1], *t[2], inverse, &q, &k);
+      }
+      if (st == FA_OK) return pair(std::move(q), std::move(k));
+    }
+  } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
+  }
+  Py_RETURN_NONE;
+}
+
+// The autograd function; differentiable once, like its Python counterpart.
+struct RotaryEmbedding : torch::autograd::Function<RotaryEmbedding> {
+  static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx, const Tensor& q, const Tensor& k,
+                                                const Tensor& positions, const Tensor& turns, const Tensor& axis,
+                                                int64_t axes, bool interleaved) {
+    Rows r;
+    Turn t;
+    t.interleaved = interleaved;
+    TORCH_CHECK(check_rows(q, k, &r) && turn_tensors(turns, axis, static_cast<int>(axes), r.d, r.dev, &t) &&
+                    positions_ok(positions, t.axes, r.T, r.dev),
+                "rotary_embedding: arguments out of order");
+    torch::autograd::variable_list out(2);
+    const fa_status st = turn(r, t, q, k, positions, false, &out[0], &out[1]);
+    TORCH_CHECK(st == FA_OK, "fa_rotary failed: ", fa_status_string(st), " ", fa_last_error_detail());
+    ctx->save_for_backward({positions, turns, axis});
+    ctx->saved_data["axes"] = axes;
+    ctx->saved_data["interleaved"] = interleaved;
+    return out;
+  }
+
+  static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx,
+                                                 torch::autograd::variable_list grads) {
+    const auto s = ctx->get_saved_variables();
+    const Tensor dq = grads[0].contiguous(), dk = grads[1].contiguous();
+    Rows r;
+    Turn t;
+    t.interleaved = ctx->saved_data["interleaved"].toBool();
+    // (what was saved comes back through hooks that the user may have set)
+    TORCH_CHECK(check_rows(dq, dk, &r), "rotary_embedding: gradients must be bfloat16 tensors of q's and k's shapes on their device");
+    TORCH_CHECK(turn_tensors(s[1], s[2], static_cast<int>(ctx->saved_data["axes"].toInt()), r.d, r.dev, &t) &&
+                    positions_ok(s[0], t.axes, r.T, r.dev),
+                "rotary_embedding: saved tensors out of order");
+    const bool again = at::GradMode::is_enabled();
+    torch::autograd::variable_list out(7);
+    {
+      at::AutoGradMode no_grad(false);
+      const fa_status st = turn(r, t, dq, dk, s[0], true, &out[0], &out[1]);
+      TORCH_CHECK(st == FA_OK, "fa_rotary failed: ", fa_status_string(st), " ", fa_last_error_detail());
+    }
+    if (again) {  // the gradients are wanted for differentiation: that, not this, is the error
+      torch::autograd::variable_list two(out.begin(), out.begin() + 2);
+      for (auto& x : two) x = x.requires_grad_(true);
+      auto err = std::make_shared<torch::autograd::DelayedError>("rotary_embedding is differentiable once", 2);
+      two = (*err)(std::move(two));
+      for (int i = 0; i < 2; ++i) out[i] = two[i];
+    }
+    return out;
+  }
+};
+
+PyObject* py_rotary_embedding(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    const Tensor* t[3];
+    Rows r;
+    Turn plan;
+    if (n == 4 && rotary_args(args, t, &r, &plan)) {
+      torch::autograd::variable_list out;
+      {
+        WithoutLock unlocked;
+        out = RotaryEmbedding::apply(*t[0], *t[1], *t[2], *plan.turns, *plan.axis, static_cast<int64_t>(plan.axes),
+                                     plan.interleaved);
+      }
+      return pair(std::move(out[0]), std::move(out[1]));
+    }
+  } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
+  }
+  Py_RETURN_NONE;
+}
+
+// (q, k, v, cache, block_table, cu_seqlens, start, max_new, rotary, positions) -> q'
+PyObject* py_cache8_store_rotary(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    if (n != 10 || recording()) Py_RETURN_NONE;
+    const Tensor *q = tensor(args[0]), *k = tensor(args[1]), *v = tensor(args[2]), *table = tensor(args[4]),
+                 *cu = tensor(args[5]), *start = tensor(args[6]);
+    const Tensor* positions = args[9] == Py_None ? nullptr : tensor(args[9]);
+    Cache c;
+    Rows r;
+    Turn t;
+    int max_new = 0;
+    if (!q || !k || !v || !table || !cu || !start || (args[9] != Py_None && !positions) || !check_rows(*q, *k, &r) ||
+        !cache_args(args[3], r.dev, &c) || c.Hk != r.Hk || c.d != r.d || !to_int(args[7], &max_new) ||
+        !turn_args(args[8], r.d, r.dev, &t) || (positions && !positions_ok(*positions, t.axes, r.T, r.dev)))
+      Py_RETURN_NONE;
+    const int64_t B = start->numel(), ldv = rows_stride(*v, r.T, r.Hk, r.d, r.dev);
+    if (ldv < 0 || !fits(B) || table->dim() != 2 || !fits(table->size(1)) ||
+        !dense(*table, at::kInt, {B, table->size(1)}, r.dev) || !dense(*cu, at::kInt, {B + 1}, r.dev) ||
+        !dense(*start, at::kInt, {B}, r.dev))
+      Py_RETURN_NONE;
+    Tensor out;
+    fa_status st;
+    {
+      WithoutLock unlocked;
+      out = at::empty({r.T, r.H, r.d}, q->options().requires_grad(false));
+      st = fa_cache8_store_rotary(
+          q->data_ptr(), k->data_ptr(), v->data_ptr(), out.data_ptr(), c.t[0]->data_ptr(), c.t[1]->data_ptr(),
+          static_cast<float*>(c.t[2]->data_ptr()), static_cast<float*>(c.t[3]->data_ptr()), ints(*table), ints(*cu),
+          ints(*start), positions ? ints(*positions) : nullptr, turns_ptr(t), ints(*t.axis), static_cast<int>(B), max_new,
+          r.T, c.num_blocks, static_cast<int>(table->size(1)), r.H, r.Hk, c.block, r.d, t.pairs, t.axes, t.interleaved,
+          r.ldq, r.ldk, ldv, 1, stream_of(r.dev));
+    }
+    if (st == FA_OK) return THPVariable_Wrap(std::move(out));
+  } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
+  }
+  Py_RETURN_NONE;
+}
+
+// (q, cache, block_table, cu_seqlens, seqlens, max_new, max_seqlen, causal, scale) -> (o, lse)
+PyObject* py_chunk_cache8(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  try {
+    if (n != 9 || recording()) Py_RETURN_NONE;
+    const Tensor *q = tensor(args[0]), *table = tensor(args[2]), *cu = tensor(args[3]), *lens = tensor(args[4]);
+    Cache c;
+    int max_new = 0, max_seqlen = 0;
+    float scale = 0.f;
+    if (!q || !table || !cu || !lens || !q->is_cuda() || q->dim() != 3) Py_RETURN_NONE;
+    const int dev = q->get_device();
+    const int64_t T = q->size(0), H = q->size(1), d = q->size(2), B = lens->numel();
+    const int64_t ldq = rows_stride(*q, T, H, d, dev);
+    const int causal = PyObject_IsTrue(args[7]);
+    if (causal < 0) PyErr_Clear();
+    if (causal < 0 || ldq <= 0 || !cache_args(args[1], dev, &c) || !to_int(args[5], &max_new) ||
+        !to_int(args[6], &max_seqlen) || !to_scale(args[8], d, &scale))
+      Py_RETURN_NONE;
+    if (!fits(T) || !fits(H) || !fits(B) || d != c.d || table->dim() != 2 || !fits(table->size(1)) ||
+        !dense(*table, at::kInt, {B, table->size(1)}, dev) || !dense(*cu, at::kInt, {B + 1}, dev) ||
+        !dense(*lens, at::kInt, {B}, dev))
+      Py_RETURN_NONE;
+    const int b = static_cast<int>(B), t = static_cast<int>(T), h = static_cast<int>(H);
+    const size_t bytes = fa_chunk_cache8_workspace_bytes(b, max_new, t, h, c.Hk, max_seqlen, c.d);
+    if (bytes == 0) Py_RETURN_NONE;
+    Tensor o, lse;
+    fa_status st;
+    {
+      WithoutLock unlocked;
+      const auto opt = q->options().requires_grad(false);
+      o = at::empty({T, H, d}, opt);
+      lse = at::empty({H, T}, opt.dtype(at::kFloat));
+      Tensor ws = at::empty({static_cast<int64_t>(bytes)}, opt.dtype(at::kByte));
+      st = fa_fwd_chunk_cache8(
+          q->data_ptr(), c.t[0]->data_ptr(), c.t[1]->data_ptr(), static_cast<const float*>(c.t[2]->data_ptr()),
+          static_cast<const float*>(c.t[3]->data_ptr()), ints(*table), ints(*cu), ints(*lens), o.data_ptr(),
+          static_cast<float*>(lse.data_ptr()), ws.data_ptr(), bytes, b, max_new, t, h, c.Hk, c.num_blocks,
+          static_cast<int>(table->size(1)), c.block, max_seqlen, c.d, ldq, scale, causal, 1, stream_of(dev));
+    }
+    if (st == FA_OK) return pair(std::move(o), std::move(lse));
+  } catch (...) {
+    PyErr_Clear();  // an exception that came out of Python
+  }
+  Py_RETURN_NONE;
+}
+
 #define FA_METHOD(name) \
   { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_##name)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {FA_METHOD(forward_grouped), FA_METHOD(backward_grouped), FA_METHOD(flash_attention_grouped),
-                         FA_METHOD(cache8_store), FA_METHOD(decode_cache8), {nullptr, nullptr, 0, nullptr}};
+                         FA_METHOD(cache8_store), FA_METHOD(decode_cache8), FA_METHOD(rotary), FA_METHOD(rotary_embedding),
+                         FA_METHOD(cache8_store_rotary), FA_METHOD(chunk_cache8), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
