@@ -327,10 +327,12 @@ FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void
  *               their results unspecified);  max_seqlen  at least every length
  * causal != 0: new token i of n sees the keys j <= seqlens[b] − n + i; otherwise all.
  * A row that sees no key gets o = 0, lse = −infinity.  zero_tail as in
- * fa_fwd_grouped.  Keys and values are code · scale exactly; products, sums and
- * rounding of the probabilities (to bf16) are those of fa_fwd_grouped.  What slots
- * behind a sequence's last token hold does not matter; queries and stored tokens
- * must be finite (a stored NaN reads as ±480 scales), scales powers of two.  A page
+ * fa_fwd_grouped.  Scores and sums are fp32, which the scores have to fit.  A query
+ * element enters its product with the codes as the sum of two e4m3 terms, off by at
+ * most 2^-17 of its row's largest (rows below 2^-118: of 2^-118); a probability is
+ * rounded to bf16, values are exact.  What slots behind a sequence's last token hold
+ * does not matter; queries and stored tokens must be finite (a value stored as NaN
+ * reads as ±480 scales), scales powers of two.  A page
  * index out of range reads as a page of zeros, a length outside [0, min(max_seqlen,
  * table_cols · block)] as the nearer end of that range, and both are reported by
  * fa_get_device_error as FA_ERR_PAGE.  Results do not depend on the order in which

@@ -413,18 +413,20 @@ fa_status check_cache8(int B, int num_blocks, int table_cols, int Hk, int block,
 }
 
 // Pages [num_blocks, Hk, block, d] of 1-byte codes, one (page, head) a copy, as
-// rows of 128 bytes (d = 64: two tokens a row), swizzled.
-fa_status make_map_codes(CUtensorMap* map, const void* ptr, int d, int block, int Hk, int num_blocks) {
+// rows of `width` bytes (128: at d = 64 two tokens a row; or d), swizzled over them.
+fa_status make_map_codes(CUtensorMap* map, const void* ptr, int d, int block, int Hk, int num_blocks, int width = 128) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return cuda_fail("cuTensorMapEncodeTiled entry point not found", cudaErrorSymbolNotFound);
-  const int rows = block * d / 128;
-  const cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(Hk),
+  const int rows = block * d / width;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(Hk),
                               static_cast<cuuint64_t>(num_blocks)};
-  const cuuint64_t strides[3] = {128, static_cast<cuuint64_t>(block) * d, static_cast<cuuint64_t>(Hk) * block * d};
-  const cuuint32_t box[4] = {128, static_cast<cuuint32_t>(rows), 1, 1};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(block) * d,
+                                 static_cast<cuuint64_t>(Hk) * block * d};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(rows), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     snprintf(t_detail, sizeof(t_detail), "cuTensorMapEncodeTiled (cache pages) failed (CUresult %d)",
              static_cast<int>(r));
@@ -924,7 +926,6 @@ FA_API fa_status fa_fwd_chunk_cache8(const void* q, const void* k_codes, const v
   p.ldq = ldq;
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
-  p.k_codes = static_cast<const uint8_t*>(k_codes);
   p.v_codes = static_cast<const uint8_t*>(v_codes);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
@@ -951,7 +952,9 @@ FA_API fa_status fa_fwd_chunk_cache8(const void* q, const void* k_codes, const v
   p.timeout_ns = kWaitLimitNs;
   // An item of one tile is whole: nothing to join.
   const bool merge = max_seqlen > fa::chunk8::kKeys;
-  const cudaError_t e = fa::launch_cache8_chunk(d, p, w.ctas, merge, static_cast<cudaStream_t>(stream));
+  CUtensorMap tk;
+  FA_TRY(make_map_codes(&tk, k_codes, d, block, Hk, num_blocks, d));
+  const cudaError_t e = fa::launch_cache8_chunk(d, tk, p, w.ctas, merge, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail("chunk attention launch", e);
 }
 

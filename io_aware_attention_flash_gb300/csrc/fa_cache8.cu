@@ -305,23 +305,6 @@ __device__ __forceinline__ float rows_sum(const float (&y)[RP], int lane) {
   return v[0];
 }
 
-// D(tmem) (+)= A(smem) B(smem), e4m3 inputs, fp32 accumulate, K = 32 a step.
-__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                         uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Instruction descriptor, kind::f8f6f4: e4m3 A and B (formats 0), both of them
-// K-major or both MN-major, fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool mn_major) {
-  return (1u << 4) | ((mn_major ? 3u : 0u) << 15) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-
 template <int D, int RP>
 struct Dec8Cfg {
   static constexpr int WG = RP >= 8 ? 2 : 1;                 // warpgroups that share the rows
@@ -361,27 +344,6 @@ struct Dec8Cfg {
   static_assert(OFF_Q % 1024 == 0 && OFF_P % 512 == 0, "swizzle atoms");
   static_assert(D == 128 || RP * 64 * 4 <= 2 * P_BYTES, "O of the second tokens fits over P");
 };
-
-// Byte `byte` of row `row` in a tile of W-byte rows swizzled over W bytes (the
-// 16-byte chunk's index exclusive-or the address bits above the 128-byte line).
-template <int W>
-__device__ __forceinline__ uint32_t swz(int row, int byte) {
-  constexpr int MASK = W / 16 - 1;
-  const int line = row / (128 / W);
-  return row * W + ((((byte >> 4) ^ line) & MASK) << 4) + (byte & 15);
-}
-// Descriptor of an operand in W-byte rows swizzled over W bytes (16: not
-// swizzled), 8 rows an atom.  K-major: rows are M or N.  MN-major: rows are K,
-// lbo the distance to the next W bytes of M.
-template <int W>
-__device__ __forceinline__ uint64_t sdesc8(uint32_t saddr, uint32_t lbo) {
-  constexpr uint64_t mode = W == 128 ? 2 : W == 64 ? 4 : W == 32 ? 6 : 0;
-  // Without a swizzle the two distances change places in MN-major.
-  constexpr uint32_t next8 = 8 * W;
-  const uint32_t lead = W == 16 ? next8 : lbo, stride = W == 16 ? lbo : next8;
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (mode << 61);
-}
 
 // 8 or 16 columns of this warp's TMEM lanes.
 template <int N>

@@ -10,17 +10,18 @@
 // share leaves partials (m, l, O), which a second kernel joins in the order of the
 // keys, so results do not depend on timing.
 //
-// Keys and values leave the cache as codes (half the bytes of bf16 through L2 and
-// shared memory) and are made bf16 in shared memory on the way to the tensor core:
-// an e4m3 value times its page's power of two is a bf16 number, so nothing is
-// rounded, and the products are those of the forward kernel.  (Straight from the
-// codes, as the cache's decode does it, Q and P need two e4m3 terms each: as many
-// tensor operations, and the second term of P costs the softmax as many instructions
-// as this conversion costs warps of its own.)
+// Keys go to the tensor core as the codes they are stored as: a query row, scaled by
+// a power of two, is the sum of two e4m3 terms, so S takes two products at twice
+// bf16's rate; the page's scale is a factor of 16 columns or more in the softmax.
+// Values are made bf16 in shared memory by warps of their own (an e4m3 value times a
+// power of two is a bf16 number: nothing is rounded), since P in two e4m3 terms would
+// cost the softmax warps more instructions than the conversion costs those.  With
+// both keys and values made bf16, 8192 rows over 32768 keys took 1230 us against
+// 750 without any conversion: the issue slots of an SM hold the softmax and one.
 //
 // Warp roles (16 warps):
 //   0-3, 4-7   softmax, one warpgroup a row tile; thread r owns row r of it
-//   8-11       conversion of a K, then a V tile
+//   8-11       conversion of V tiles
 //   12         tcgen05.mma issue
 //   13         items and copies: publishes the CTA's next item, copies the codes of
 //              its pages (lane i: page i of the tile) with their scales
@@ -33,6 +34,7 @@
 
 #include "cache8_tiles.h"
 #include "chunk8_items.h"
+#include "e4m3.cuh"
 #include "fa_kernels.cuh"
 #include "ptx.cuh"
 
@@ -45,31 +47,34 @@ using chunk8::kRows;
 
 template <int D>
 struct ChunkCfg {
-  static constexpr int KB = D / 64;                     // 128-byte swizzle blocks per row
+  static constexpr int KB = D / 64;                     // 128-byte swizzle blocks of a bf16 row
   static constexpr int BLK_BYTES = kTile * 128;         // one 128-row x 64-col block
   static constexpr int TILE_BYTES = KB * BLK_BYTES;     // one 128 x D tile of bf16
   static constexpr int CODE_BYTES = kKeys * D;          // the same of codes
-  static constexpr int NK = D == 128 ? 2 : 3;           // K, V ring depth
-  static constexpr int NV = NK;
-  static constexpr int NST = D == 128 ? 2 : 6;          // code ring: K, V, K, V, ...
+  static constexpr int NK = D == 128 ? 3 : 6;           // ring of K's codes
+  static constexpr int NC = NK;                         // ring of V's codes
+  static constexpr int NV = D == 128 ? 2 : 3;           // ring of V in bf16
+  static constexpr int NSC = NK + 1;                    // ring of K's scales
   static constexpr int NI = 4;                          // published items
   static constexpr int MAX_PPT = kKeys / 16;            // pages of a tile, at most
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + 2 * TILE_BYTES;
-  static constexpr int OFF_V = OFF_K + NK * TILE_BYTES;
-  static constexpr int OFF_C = OFF_V + NV * TILE_BYTES;
-  static constexpr int OFF_SC = OFF_C + NST * CODE_BYTES;          // [NST][pages] two factors, bf16 pairs
+  static constexpr int OFF_Q = 0;                       // two row tiles, each its first terms, then its second
+  static constexpr int OFF_V = OFF_Q + 2 * TILE_BYTES;
+  static constexpr int OFF_K = OFF_V + NV * TILE_BYTES;
+  static constexpr int OFF_C = OFF_K + NK * CODE_BYTES;
+  static constexpr int OFF_KS = OFF_C + NC * CODE_BYTES;           // [NSC][pages] K's scales
+  static constexpr int OFF_VF = OFF_KS + NSC * MAX_PPT * 4;        // [NC][pages] V's two factors, bf16 pairs
   static constexpr int ITEM_INTS = 12;
-  static constexpr int OFF_ITEM = OFF_SC + NST * MAX_PPT * 8;
+  static constexpr int OFF_ITEM = OFF_VF + NC * MAX_PPT * 8;
   static constexpr int OFF_SCAN = OFF_ITEM + NI * ITEM_INTS * 4;   // [16] sums of a scan, then its find
   static constexpr int OFF_BAR = OFF_SCAN + 18 * 8;
   static constexpr int B_IFULL = 0;
   static constexpr int B_IEMPTY = B_IFULL + NI;
-  static constexpr int B_CFULL = B_IEMPTY + NI;
-  static constexpr int B_CEMPTY = B_CFULL + NST;
-  static constexpr int B_KFULL = B_CEMPTY + NST;
+  static constexpr int B_KFULL = B_IEMPTY + NI;
   static constexpr int B_KEMPTY = B_KFULL + NK;
-  static constexpr int B_VFULL = B_KEMPTY + NK;
+  static constexpr int B_SCFULL = B_KEMPTY + NK;
+  static constexpr int B_CFULL = B_SCFULL + NSC;
+  static constexpr int B_CEMPTY = B_CFULL + NC;
+  static constexpr int B_VFULL = B_CEMPTY + NC;
   static constexpr int B_VEMPTY = B_VFULL + NV;
   static constexpr int B_Q = B_VEMPTY + NV;
   static constexpr int B_SFULL = B_Q + 2;
@@ -83,12 +88,14 @@ struct ChunkCfg {
   static constexpr int NUM_THREADS = 512;
   static constexpr int READERS = 13;                    // warps that take an item: all but the copying one and two idle
   // Registers a thread after the split; launched with 128.
-  static constexpr int REG_SOFTMAX = 192, REG_CONVERT = 72, REG_OTHER = 56;
+  static constexpr int REG_SOFTMAX = 184, REG_CONVERT = 80, REG_OTHER = 64;
   static_assert(2 * REG_SOFTMAX + REG_CONVERT + REG_OTHER == 4 * 128, "the split takes what the launch gives");
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t S_COL(int t) { return t * 128; }
   __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256 + t * D; }
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(OFF_K % 1024 == 0 && OFF_C % 1024 == 0 && CODE_BYTES % 1024 == 0, "swizzle atoms");
+  static_assert(OFF_ITEM % 16 == 0 && OFF_KS % 16 == 0 && OFF_SCAN % 8 == 0, "vector accesses");
 };
 
 // What the roles know of an item.
@@ -112,8 +119,8 @@ __device__ __forceinline__ void chunk_seq(const Chunk8Params& p, int b, int& tok
 
 // Four codes to bf16 by their bits: sign, and exponent and mantissa four places
 // down, which reads as the value times 2^-120 (a subnormal code as a subnormal).
-// The first word holds elements 0 and 2, the second 1 and 3: Q's and O's dimensions
-// change places to match, which costs nothing.
+// The first word holds elements 0 and 2, the second 1 and 3: O's dimensions change
+// places again at the end.
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t& even, uint32_t& odd) {
   odd = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
   even = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
@@ -124,15 +131,20 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 constexpr uint32_t kOne2 = 0x3f803f80u;
-// 2^(e + 120) as two bf16 factors, each a pair; e the exponent of a page's scale.
+// V is kept 2^-kVShift times its value, so that O, up to 2^40 times the largest value
+// while it is summed, does not leave fp32; the least of a value's codes, 2^-9 · 2^-64,
+// stays a normal bf16 number.
+constexpr int kVShift = 48;
+// 2^(e + 120 - kVShift) as two bf16 factors, each a pair; e the exponent of a page's scale.
 __device__ __forceinline__ uint2 scale_factors(float scale) {
-  const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127;
-  const int a = max(min(e + 120, 127), -126), b = max(e - 7, 0);
+  const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127 + 120 - kVShift;
+  const int a = max(min(e, 127), -126), b = max(e - 127, 0);
   return make_uint2(static_cast<uint32_t>(a + 127) * 0x00800080u, static_cast<uint32_t>(b + 127) * 0x00800080u);
 }
 
 template <int D>
-__global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(const Chunk8Params p) {
+__global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                                              const Chunk8Params p) {
   using C = ChunkCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_base = smem_u32(smem_raw);
@@ -149,13 +161,14 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       mbar_init(bar(C::B_IFULL + i), 1);
       mbar_init(bar(C::B_IEMPTY + i), C::READERS);
     }
-    for (int i = 0; i < C::NST; ++i) {
+    for (int i = 0; i < C::NK; ++i) {
+      mbar_init(bar(C::B_KFULL + i), 1);
+      mbar_init(bar(C::B_KEMPTY + i), 1);
+    }
+    for (int i = 0; i < C::NSC; ++i) mbar_init(bar(C::B_SCFULL + i), 1);
+    for (int i = 0; i < C::NC; ++i) {
       mbar_init(bar(C::B_CFULL + i), 1);
       mbar_init(bar(C::B_CEMPTY + i), 4);
-    }
-    for (int i = 0; i < C::NK; ++i) {
-      mbar_init(bar(C::B_KFULL + i), 4);
-      mbar_init(bar(C::B_KEMPTY + i), 1);
     }
     for (int i = 0; i < C::NV; ++i) {
       mbar_init(bar(C::B_VFULL + i), 4);
@@ -170,6 +183,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     mbar_init(bar(C::B_DRAIN), 1);
     *abort_flag = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&tmK);
   }
   // The kernel may start while the one before it in the stream finishes; what that
   // one wrote is read, and tensor memory taken, from here on.
@@ -343,7 +357,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       Unit cur, next;
       next_unit(cur);
       if (cur.tiles > 0) load_scales(cur);
-      int copies = 0, published = 0;
+      int tile = 0, v_tiles = 0, published = 0;  // (tile: K tiles issued)
       bool ok = true;
       auto publish = [&](const Unit& u) {
         const int s = published % C::NI;
@@ -384,25 +398,42 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           const int page = __shfl_sync(0xffffffffu, cur.page, from);
           const float ks = __shfl_sync(0xffffffffu, cur.ks, from), vs = __shfl_sync(0xffffffffu, cur.vs, from);
           const bool mine = lane < n_pages && page >= 0;
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * page_bytes;
-          const size_t at = mine ? (static_cast<size_t>(page) * p.Hk + cur.hk) * page_bytes : 0;
-#pragma unroll
-          for (int w = 0; w < 2; ++w, ++copies) {
-            const int st = copies % C::NST;
-            if (copies >= C::NST)
-              ok = wait_bounded(bar(C::B_CEMPTY + st), (copies / C::NST - 1) & 1, abort_flag, p.err, p.timeout_ns);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (lane < C::MAX_PPT)
-              reinterpret_cast<uint2*>(smem + C::OFF_SC)[st * C::MAX_PPT + lane] =
-                  mine ? scale_factors(w ? vs : ks) : make_uint2(0u, kOne2);
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bar(C::B_CFULL + st), bytes);
-            __syncwarp();
-            if (mine)
-              bulk_load(sb + C::OFF_C + st * C::CODE_BYTES + lane * page_bytes, (w ? p.v_codes : p.k_codes) + at, page_bytes,
-                        bar(C::B_CFULL + st));
+          // ---- K: a page out of range reads as zeros (the copy's fill)
+          const int ks_slot = tile % C::NK;
+          if (tile >= C::NK)
+            ok = wait_bounded(bar(C::B_KEMPTY + ks_slot), (tile / C::NK - 1) & 1, abort_flag, p.err, p.timeout_ns);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane < C::MAX_PPT)
+            reinterpret_cast<float*>(smem + C::OFF_KS)[tile % C::NSC * C::MAX_PPT + lane] = mine ? ks : 1.f;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::B_SCFULL + tile % C::NSC));
+            mbar_arrive_expect_tx(bar(C::B_KFULL + ks_slot), max(n_pages, 0) * page_bytes);
           }
+          __syncwarp();
+          if (lane < n_pages)
+            tma_load_4d(sb + C::OFF_K + ks_slot * C::CODE_BYTES + lane * page_bytes, &tmK, bar(C::B_KFULL + ks_slot), 0, 0,
+                        cur.hk, page >= 0 ? page : p.num_blocks);
+          // ---- V
+          const int st = tile % C::NC;
+          if (tile >= C::NC)
+            ok = wait_bounded(bar(C::B_CEMPTY + st), (tile / C::NC - 1) & 1, abort_flag, p.err, p.timeout_ns);
+          ++tile;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * page_bytes;
+          if (lane < C::MAX_PPT)
+            reinterpret_cast<uint2*>(smem + C::OFF_VF)[st * C::MAX_PPT + lane] =
+                mine ? scale_factors(vs) : make_uint2(0u, kOne2);
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::B_CFULL + st), bytes);
+          __syncwarp();
+          if (mine)
+            bulk_load(sb + C::OFF_C + st * C::CODE_BYTES + lane * page_bytes,
+                      p.v_codes + (static_cast<size_t>(page) * p.Hk + cur.hk) * page_bytes, page_bytes,
+                      bar(C::B_CFULL + st));
+          ++v_tiles;
           if (i == 0 && next.tiles > 0) load_scales(next);
         }
         cur = next;
@@ -412,22 +443,25 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         publish(cur);
       }
       // Every copy issued lands before the CTA may exit, whoever aborted.
-      for (int s = 0; s < C::NST && s < copies; ++s)
-        wait_drain(bar(C::B_CFULL + s), ((copies - 1 - s) / C::NST) & 1, p.err, p.timeout_ns);
+      for (int s = 0; s < C::NK && s < tile; ++s)
+        wait_drain(bar(C::B_KFULL + s), ((tile - 1 - s) / C::NK) & 1, p.err, p.timeout_ns);
+      for (int s = 0; s < C::NC && s < v_tiles; ++s)
+        wait_drain(bar(C::B_CFULL + s), ((v_tiles - 1 - s) / C::NC) & 1, p.err, p.timeout_ns);
     } else if (warp == C::MMA_WARP) {
       // ------------------------------------------------------------ MMA
-      constexpr uint32_t idesc_s = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_s = idesc_e4m3(128, 128, false);
       constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
-      const uint64_t dQ0 = sdesc_sw128(sb + C::OFF_Q, 16, 1024);
-      const uint64_t dK0 = sdesc_sw128(sb + C::OFF_K, 16, 1024);
+      const uint64_t dQ0 = sdesc8<D>(sb + C::OFF_Q, 16);
+      const uint64_t dK0 = sdesc8<D>(sb + C::OFF_K, 16);
       const uint64_t dV0 = sdesc_sw128(sb + C::OFF_V, C::BLK_BYTES, 1024);
       auto issue_s = [&](int t, int ks) {
-        const uint64_t dQ = sdesc_add(dQ0, t * C::TILE_BYTES), dK = sdesc_add(dK0, ks * C::TILE_BYTES);
+        const uint64_t dQ = sdesc_add(dQ0, t * C::TILE_BYTES), dK = sdesc_add(dK0, ks * C::CODE_BYTES);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t koff = (kk / 4) * C::BLK_BYTES + (kk % 4) * 32;
-          mma_ss(tmem + C::S_COL(t), sdesc_add(dQ, koff), sdesc_add(dK, koff), idesc_s, kk > 0);
-        }
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_e4m3(tmem + C::S_COL(t), sdesc_add(dQ, term * C::CODE_BYTES + kk * 32), sdesc_add(dK, kk * 32), idesc_s,
+                     term + kk > 0);
       };
       auto issue_pv = [&](int t, int vs, bool acc) {
         const uint64_t dV = sdesc_add(dV0, vs * C::TILE_BYTES);
@@ -496,7 +530,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     // reads nor its swizzled writes meet in a bank.
     const int cw = warp - C::CONVERT_WARP;
     int row0, chunk;  // of the first pass; a pass is ROWS rows
-    constexpr int CPR = D / 16, ROWS = 128 / CPR, PASSES = kKeys / ROWS;
+    constexpr int CPR = D / 16, ROWS = 128 / CPR, PASSES = kKeys / ROWS, BATCH = 4;
     if (D == 128) {
       const int rb = (lane >> 2) & 1;
       row0 = cw * 4 + ((lane >> 4) & 1) * 2 + rb;
@@ -505,7 +539,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       row0 = cw * 8 + (lane >> 2);
       chunk = lane & 3;
     }
-    int copies = 0, tile = 0;
+    const uint32_t in0 = row0 * D + chunk * 16;
+    const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES + row0 * 128;
+    // (a pass is a multiple of 8 rows: the swizzle stays)
+    const uint32_t at0 = out0 + ((c0 ^ (row0 & 7)) << 4), at1 = out0 + (((c0 + 1) ^ (row0 & 7)) << 4);
+    int tile = 0;
     bool ok = true;
     auto wait = [&](int i, int phase) {
       ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
@@ -514,24 +552,25 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     };
     Item it;
     while (ok && take_item(it)) {
-      for (int kt = it.k0; ok && kt < it.k0 + it.tiles; ++kt, ++tile) {
+      for (int kt = it.k0; kt < it.k0 + it.tiles; ++kt, ++tile) {
         const int held = cache8::tokens_from(it.len, kt, kKeys, 0);  // tokens of the tile, if fewer than its rows
-#pragma unroll 1
-        for (int w = 0; w < 2; ++w, ++copies) {
-          const int st = copies % C::NST;
-          if (!wait(C::B_CFULL + st, copies / C::NST)) break;
-          const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES;
-          const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_SC) + st * C::MAX_PPT;
-          const int slot = tile % C::NK;
-          if (tile >= C::NK && !wait((w ? C::B_VEMPTY : C::B_KEMPTY) + slot, tile / C::NK - 1)) break;
-          uint8_t* out = smem + (w ? C::OFF_V : C::OFF_K) + slot * C::TILE_BYTES + (2 * chunk / 8) * C::BLK_BYTES;
+        const int st = tile % C::NC, slot = tile % C::NV;
+        if (!wait(C::B_CFULL + st, tile / C::NC)) break;
+        if (tile >= C::NV && !wait(C::B_VEMPTY + slot, tile / C::NV - 1)) break;
+        const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES + in0;
+        const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_VF) + st * C::MAX_PPT;
+        uint8_t* out = smem + C::OFF_V + slot * C::TILE_BYTES;
+        uint4 c[BATCH];
 #pragma unroll
-          for (int i = 0; i < PASSES; ++i) {
-            const int row = row0 + i * ROWS;
-            uint4 c = *reinterpret_cast<const uint4*>(codes + row * D + chunk * 16);
-            if (row >= held) c = make_uint4(0u, 0u, 0u, 0u);  // slots without a token may hold anything
+        for (int i0 = 0; i0 < PASSES; i0 += BATCH) {
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) c[i] = *reinterpret_cast<const uint4*>(codes + (i0 + i) * ROWS * D);
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int row = row0 + (i0 + i) * ROWS;
+            if (row >= held) c[i] = make_uint4(0u, 0u, 0u, 0u);  // slots without a token may hold anything
             const uint2 f = factors[row >> p.block_shift];
-            const uint32_t in[4] = {c.x, c.y, c.z, c.w};
+            const uint32_t in[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
             uint32_t v[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -539,21 +578,19 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
               v[2 * k] = mul_bf16x2(v[2 * k], f.x);
               v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f.x);
             }
-            if (f.y != kOne2) {  // a scale above 2^7: the factor does not fit one bf16 number
+            if (f.y != kOne2) {  // a scale above 2^55: the factor does not fit one bf16 number
 #pragma unroll
               for (int k = 0; k < 8; ++k) v[k] = mul_bf16x2(v[k], f.y);
             }
-            uint8_t* at = out + row * 128;
-            const int c0 = 2 * (chunk % 4);
-            *reinterpret_cast<uint4*>(at + ((c0 ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(at + (((c0 + 1) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<uint4*>(out + at0 + (i0 + i) * ROWS * 128) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(out + at1 + (i0 + i) * ROWS * 128) = make_uint4(v[4], v[5], v[6], v[7]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(C::B_CEMPTY + st));
-            mbar_arrive(bar((w ? C::B_VFULL : C::B_KFULL) + slot));
-          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(C::B_CEMPTY + st));
+          mbar_arrive(bar(C::B_VFULL + slot));
         }
       }
     }
@@ -561,7 +598,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     // ---------------------------------------------------------------- softmax
     setmaxnreg_inc<C::REG_SOFTMAX>();
     const int t = warp / 4, wq = warp % 4, r = wq * 32 + lane;
-    const float c = p.scale_log2;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t tS = lane_addr + C::S_COL(t), tO = lane_addr + C::O_COL(t);
     uint8_t* q_smem = smem + C::OFF_Q + t * C::TILE_BYTES;
@@ -571,6 +607,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     const int my_chunk = lane % CH, my_row = wq * 32 + lane / CH;
     auto place = [&](int row, int ch) { return q_smem + (ch / 8) * C::BLK_BYTES + row * 128 + (((ch % 8) ^ (row & 7)) << 4); };
     int np = 0, no = 0;  // tiles and items of this row tile so far
+    int tile0 = 0;       // tiles of the items before
     bool ok = true;
     auto wait = [&](int i, int phase) {
       ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
@@ -581,14 +618,19 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     while (ok && take_item(it)) {
       const int cnt = t ? it.cnt1 : it.cnt0;
       const int first = it.rb * kRows + t * kHalf, rows = it.n * p.G;
+      const int first_tile = tile0;
+      tile0 += it.tiles;
       if (first >= rows) continue;
       const int f = first + r;
       const bool exists = f < rows;
       const int tok = f / p.G, g = f - tok * p.G;
       float m_ref = -CUDART_INF_F, l = 0.f;
-      bool far = false;  // (of the warp) some reference so large that c·m_ref is off by too much: subtracted first
+      // (of the warp) some reference so large that a product's rounding, 2^-24 of it,
+      // counts in the exponent
+      bool far = false;
       if (cnt > 0) {
-        // ---- Q, its dimensions in the order of the converted codes
+        // ---- Q: each row scaled by a power of two, as two e4m3 terms
+        int my_e = 0;  // the exponent of this thread's row
 #pragma unroll
         for (int i0 = 0; i0 < 32 / RPP; i0 += 8) {
           uint4 x[8];
@@ -603,11 +645,35 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           }
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 y = make_uint4(__byte_perm(x[i].x, x[i].y, 0x5410), __byte_perm(x[i].x, x[i].y, 0x7632),
-                                       __byte_perm(x[i].z, x[i].w, 0x5410), __byte_perm(x[i].z, x[i].w, 0x7632));
-            *reinterpret_cast<uint4*>(place(my_row + (i0 + i) * RPP, my_chunk)) = y;
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) top = __vmaxu2(top, w[u] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+            for (int off = CH / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+            // smallest power of two s with max <= 448 s, for any finite row: 2^120 at
+            // most, at least 2^-126 (fp32's smallest that is not subnormal)
+            const int e = min(scale_exponent(top, -126), 120);
+            const int of_row = __shfl_sync(0xffffffffu, e, lane % RPP * CH);
+            if (lane / RPP == i0 + i) my_e = of_row;
+            const float inv = exp2_int(-e);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float v[4] = {bf16lo_to_f32(w[2 * u]) * inv, bf16hi_to_f32(w[2 * u]) * inv,
+                                  bf16lo_to_f32(w[2 * u + 1]) * inv, bf16hi_to_f32(w[2 * u + 1]) * inv};
+              float h[4];
+              hi[u] = pack_e4m3x4(v[0], v[1], v[2], v[3]);
+              unpack_e4m3x4(hi[u], h);
+              lo[u] = pack_e4m3x4(v[0] - h[0], v[1] - h[1], v[2] - h[2], v[3] - h[3]);
+            }
+            uint8_t* at = q_smem + swz<D>(my_row + (i0 + i) * RPP, 8 * my_chunk);
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + C::CODE_BYTES) = make_uint2(lo[0], lo[1]);
           }
         }
+        const float c_row = exp2_int(my_e) * p.scale_log2;
         fence_proxy_async_smem();
         mbar_arrive(bar(C::B_Q + t));
         // Keys the row sees, and the warpgroup's first row (which sees the fewest).
@@ -622,6 +688,14 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           tmem_wait_ld();
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) reg_fence(s[ch]);
+          // the columns' factors: K's scale of each 16 keys, the row's and the softmax's
+          // (not below fp32's least normal number: a masked column stays -infinity)
+          const int sc = (first_tile + j) % C::NSC;
+          if (!wait(C::B_SCFULL + sc, (first_tile + j) / C::NSC)) break;
+          const float* k_scale = reinterpret_cast<const float*>(smem + C::OFF_KS) + sc * C::MAX_PPT;
+          float cf[8];
+#pragma unroll
+          for (int g16 = 0; g16 < 8; ++g16) cf[g16] = fmaxf(k_scale[(16 * g16) >> p.block_shift] * c_row, 0x1p-126f);
           const int kv0 = (it.k0 + j) * kKeys;
           if (all_see - kv0 < kKeys) {
             const int end = sees - kv0;
@@ -631,21 +705,23 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
               for (int i = 0; i < 32; ++i)
                 if (ch * 32 + i >= end) s[ch][i] = __float_as_uint(-CUDART_INF_F);
           }
+          // The largest y = s · factor of the row.
           auto row_max = [&]() -> float {
-            float mx[4];
+            float m = -CUDART_INF_F;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mx[k] = -CUDART_INF_F;
+            for (int g16 = 0; g16 < 8; ++g16) {
+              const uint32_t* x = s[g16 / 2] + 16 * (g16 % 2);
+              float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                mx[i & 3] = fmax3(mx[i & 3], __uint_as_float(s[ch][2 * i]), __uint_as_float(s[ch][2 * i + 1]));
-            return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              for (int i = 1; i < 8; ++i) mx[i & 1] = fmax3(mx[i & 1], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+              m = fmaxf(m, fmaxf(mx[0], mx[1]) * cf[g16]);
+            }
+            return m;
           };
-          // P = 2^(c·s − c·m_ref) as bf16 over S; returns the tile's row sum.
+          // P = 2^(y − m_ref) as bf16 over S; returns the tile's row sum.
           auto p_pass = [&]() -> float {
-            const float mc = (far || m_ref == -CUDART_INF_F) ? 0.f : m_ref * c;
-            const uint64_t c2 = f2_pack(c, c), nmc2 = f2_pack(-mc, -mc);
+            const float m = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+            const uint64_t nm2 = f2_pack(-m, -m);
             uint64_t ls2[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) ls2[k] = f2_pack(0.f, 0.f);
@@ -654,8 +730,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
               uint32_t pk[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
+                const float f = cf[2 * ch + e / 8];
                 float x0, x1;
-                f2_unpack(ffma2(f2_pack(__uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1])), c2, nmc2),
+                f2_unpack(ffma2(f2_pack(__uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1])), f2_pack(f, f),
+                                nm2),
                           x0, x1);
                 const float p0 = ex2_approx(x0);
                 const float p1 = ex2_approx(x1);
@@ -669,35 +747,32 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             for (int k = 0; k < 4; ++k) f2_unpack(ls2[k], ls[2 * k], ls[2 * k + 1]);
             return ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
           };
-          // With scores so large, c·s − c·m_ref as one FMA would leave the rounding of
-          // c·m_ref, up to 2^-24 of it, in the exponent.
-          auto subtract = [&](float by) {
+          auto set_far = [&]() {
+            far = __any_sync(0xffffffffu, m_ref != -CUDART_INF_F && !(fabsf(m_ref) < 0x1p20f));
+          };
+          // Far references: y is formed before the reference is taken off, so that the
+          // largest of the row comes to 0 exactly.
+          auto form_y = [&]() {
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
-              for (int i = 0; i < 32; ++i) s[ch][i] = __float_as_uint(__uint_as_float(s[ch][i]) - by);
+              for (int i = 0; i < 32; ++i) s[ch][i] = __float_as_uint(__uint_as_float(s[ch][i]) * cf[2 * ch + i / 16]);
+#pragma unroll
+            for (int g16 = 0; g16 < 8; ++g16) cf[g16] = 1.f;
           };
-          auto set_far = [&]() {
-            far = __any_sync(0xffffffffu, m_ref != -CUDART_INF_F && !(fabsf(m_ref * c) < 0x1p20f));
-          };
-          float base = 0.f;  // what has been subtracted from s
           if (j == 0) {
             m_ref = row_max();
             set_far();
           }
-          if (far) {
-            base = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-            subtract(base);
-          }
+          if (far) form_y();
           float lt = p_pass();
           if (__any_sync(0xffffffffu, !(lt < 0x1p40f))) {
-            const float m_new = fmaxf(m_ref, base + row_max());
-            const float alpha = (m_ref == -CUDART_INF_F) ? 0.f : ex2_approx((m_ref - m_new) * c);
+            const float m_new = fmaxf(m_ref, row_max());
+            const float alpha = (m_ref == -CUDART_INF_F) ? 0.f : ex2_approx(m_ref - m_new);
             m_ref = m_new;
             l *= alpha;
             set_far();
-            if (far) subtract(m_ref == -CUDART_INF_F ? 0.f : m_ref - base);
-            else if (base != 0.f) subtract(-base);
+            if (far) form_y();
 #pragma unroll 1
             for (int ch = 0; j > 0 && ch < D / 16; ++ch) {
               uint32_t o[16];
@@ -722,7 +797,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       const size_t part = static_cast<size_t>(it.slot < 0 ? 0 : it.slot) * kRows + t * kHalf + r;
       if (it.slot < 0) {
         // ---- O / l, staged over Q (which no MMA reads any more), out by whole rows
-        const float inv_l = l > 0.f ? 1.0f / l : 0.f;
+        const float inv_l = l > 0.f ? exp2_int(kVShift) / l : 0.f;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t o[32];
@@ -754,9 +829,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         __syncwarp();
         if (exists)
           p.lse[static_cast<size_t>(it.hk * p.G + g) * p.total + it.tok0 + tok] =
-              l > 0.f ? (m_ref * c + log2f(l)) * kLn2 : -CUDART_INF_F;
+              l > 0.f ? (m_ref + log2f(l)) * kLn2 : -CUDART_INF_F;
       } else if (exists) {
-        reinterpret_cast<float2*>(p.ml_part)[part] = make_float2(l > 0.f ? m_ref * c : -CUDART_INF_F, l);
+        reinterpret_cast<float2*>(p.ml_part)[part] = make_float2(l > 0.f ? m_ref : -CUDART_INF_F, l);
       }
       if (it.slot >= 0 && cnt > 0) {
         // ---- a partial: four dimensions of 32 rows side by side
@@ -822,7 +897,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk8_merge_kernel(const Ch
       o.x = fmaf(wt, v.x, o.x), o.y = fmaf(wt, v.y, o.y);
       o.z = fmaf(wt, v.z, o.z), o.w = fmaf(wt, v.w, o.w);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? exp2_int(kVShift) / l : 0.f;
     const int tok = f / p.G, h = hk * p.G + f - tok * p.G;
     *reinterpret_cast<uint2*>(p.o + (static_cast<size_t>(tok0 + tok) * p.H + h) * D + 4 * d4) =
         make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -832,7 +907,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_chunk8_merge_kernel(const Ch
 }
 
 template <int D>
-cudaError_t launch_chunk(const Chunk8Params& p, int ctas, bool merge, cudaStream_t s) {
+cudaError_t launch_chunk(const CUtensorMap& tk, const Chunk8Params& p, int ctas, bool merge, cudaStream_t s) {
   using C = ChunkCfg<D>;
   static SmemLimit smem_limit;
   cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_chunk8_kernel<D>), C::SMEM_BYTES);
@@ -844,7 +919,7 @@ cudaError_t launch_chunk(const Chunk8Params& p, int ctas, bool merge, cudaStream
     return cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(fa_chunk8_kernel<D>)) == cudaSuccess ? a.numRegs : 0;
   }();
   if (launch_regs != 128) return cudaErrorInvalidConfiguration;
-  e = launch_kernel(fa_chunk8_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(C::NUM_THREADS), C::SMEM_BYTES, s, true, p);
+  e = launch_kernel(fa_chunk8_kernel<D>, dim3(static_cast<unsigned>(ctas)), dim3(C::NUM_THREADS), C::SMEM_BYTES, s, true, tk, p);
   if (e != cudaSuccess || !merge) return e;
   return launch_kernel(fa_chunk8_merge_kernel<D>, dim3(static_cast<unsigned>(ctas), kRows / kMergeRows),
                        dim3(kMergeThreads), 0, s, true, p);
@@ -852,8 +927,9 @@ cudaError_t launch_chunk(const Chunk8Params& p, int ctas, bool merge, cudaStream
 
 }  // namespace
 
-cudaError_t launch_cache8_chunk(int d, const Chunk8Params& p, int ctas, bool merge, cudaStream_t s) {
-  return d == 64 ? launch_chunk<64>(p, ctas, merge, s) : launch_chunk<128>(p, ctas, merge, s);
+cudaError_t launch_cache8_chunk(int d, const CUtensorMap& tk, const Chunk8Params& p, int ctas, bool merge,
+                                cudaStream_t s) {
+  return d == 64 ? launch_chunk<64>(tk, p, ctas, merge, s) : launch_chunk<128>(tk, p, ctas, merge, s);
 }
 
 }  // namespace fa

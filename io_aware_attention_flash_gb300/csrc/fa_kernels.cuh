@@ -215,8 +215,7 @@ struct Chunk8Params {
   long long ldq;
   uint16_t* o;            // bf16 [total, H, d]
   float* lse;             // fp32 [H, total]
-  const uint8_t* k_codes;
-  const uint8_t* v_codes;
+  const uint8_t* v_codes; // (K's: by tensor map)
   const float* k_scale;
   const float* v_scale;
   const int* table;
@@ -348,7 +347,8 @@ cudaError_t launch_cache8_decode(int d, const CUtensorMap& tk, const CUtensorMap
 cudaError_t launch_rotary(int d, const RotaryParams& r, const TurnRows& x, int total, cudaStream_t s);
 cudaError_t launch_cache8_append(int d, int block, const Cache8StoreParams& p, const RotaryParams& r, const TurnRows& x,
                                  int zero_tail, cudaStream_t s);
-cudaError_t launch_cache8_chunk(int d, const Chunk8Params& p, int ctas, bool merge, cudaStream_t s);
+cudaError_t launch_cache8_chunk(int d, const CUtensorMap& tk, const Chunk8Params& p, int ctas, bool merge,
+                                cudaStream_t s);
 cudaError_t launch_wait_timeout_selftest(uint32_t* err, uint64_t limit_ns, cudaStream_t s);
 cudaError_t run_microbench(int which, int iters, uint32_t* err, double* result, cudaStream_t s);
 

@@ -4,8 +4,10 @@ in 64 bits on the stored values.
 Tolerances, element by element.  Keys and values are code times a power of two,
 exact in bf16.  A probability is rounded to bf16, by at most 2^-8 of it, and the
 output by 2^-8 of itself, which is at most sum P |v|: 2^-7 sum P |v| together.  A
-score is a sum of d products in fp32, off by at most d 2^-24 scale sum |q| |k| = E;
-that moves the LSE by E and each P by 2 E of itself.  The fp32 sums over the keys add
+score is a sum of d products in fp32, off by at most d 2^-24 scale sum |q| |k|, of
+queries in two e4m3 terms, each element off by at most 2^-17 of its row's largest:
+another scale 2^-17 max |q| sum |k|.  The two together, E, move the LSE by E and each
+P by 2 E of itself.  The fp32 sums over the keys add
 2^-14 of sum P |v| and the exponentials 2^-20: both within 2^-7 * 2^-5.  LSE: 1e-4 + E.
 """
 import numpy as np
@@ -45,7 +47,8 @@ def check(o, lse, q, cache, table, new, lens, scale, causal):
             x = qs[live, h]
             s = scale * x @ k.T
             s = s.masked_fill(torch.arange(L, device="cuda") >= seen[live][:, None], -np.inf)
-            e = d * 2.0 ** -24 * scale * float((x.abs() @ k.abs().T).max())
+            e = scale * (d * 2.0 ** -24 * float((x.abs() @ k.abs().T).max())
+                         + 2.0 ** -17 * float(x.abs().max() * k.abs().sum(1).max()))
             p = torch.softmax(s, 1)
             bound = (2.0 ** -7 * (1 + 2.0 ** -5) + 2 * e) * (p @ v.abs())
             assert ((got[live, h] - p @ v).abs() <= bound).all(), (b, h)
@@ -184,6 +187,38 @@ def test_every_code_and_scale(d):
             # lse = (score · log2 e + log2 1) ln 2 in fp32: three roundings of 2^-24
             assert ((lse[0].double() - want).abs() <= 2.0 ** -22 * want.abs()).all(), (e, dim)
     assert_no_device_error(fa)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_exp,k_exp", [(110, -60), (125, -70), (-100, 60), (-115, 90), (-60, 30), (0, 119)])
+def test_queries_of_any_size(q_exp, k_exp, d):
+    """Queries up to bf16's largest and down to its smallest normal numbers, keys over
+    the range of their scales, with a softmax scale that makes the scores of order 1."""
+    fa = require_gpu()
+    cache = random_cache(fa, 20, 2, 16, d, seed=40)
+    cache.k_scale.fill_(2.0 ** k_exp)
+    q = (torch.randn(21, 8, d, generator=torch.Generator().manual_seed(41)) * 2.0 ** (q_exp // 2) * 2.0 ** (q_exp - q_exp // 2)).bfloat16().cuda()
+    assert torch.isfinite(q).all()
+    table, scale = torch.arange(19, dtype=torch.int32)[None], d ** -0.5 * 2.0 ** -(q_exp + k_exp) / 8
+    o, lse = fa.attention_chunk_cache8(q, cache, table.cuda(), i32([0, 21]), i32([300]), 21, 300, True, scale)
+    assert_no_device_error(fa)
+    check(o, lse, q, cache, table, [21], [300], scale, True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_under_rising_scores(d):
+    """Values up to bf16's largest while the scores climb past their first tile's by
+    far: what is summed before the last division must not leave fp32."""
+    fa = require_gpu()
+    cache = random_cache(fa, 40, 1, 16, d, seed=42)
+    cache.v.copy_((cache.v.float() / 2).to(torch.float8_e4m3fn))
+    cache.v_scale.fill_(2.0 ** 119)
+    cache.k_scale.copy_(2.0 ** (torch.arange(40, device="cuda") // 5 - 2.0)[:, None])
+    q = torch.randn(9, 4, d, generator=torch.Generator().manual_seed(43)).bfloat16().cuda()
+    table = torch.arange(40, dtype=torch.int32)[None]
+    o, lse = fa.attention_chunk_cache8(q, cache, table.cuda(), i32([0, 9]), i32([640]), 9, 640, False)
+    assert_no_device_error(fa)
+    check(o, lse, q, cache, table, [9], [640], d ** -0.5, False)
 
 
 def test_indexes_out_of_range():
