@@ -21,10 +21,11 @@
 //
 // Warp roles (16 warps):
 //   0-3, 4-7   softmax, one warpgroup a row tile; thread r owns row r of it
-//   8-11       conversion of V tiles
-//   12         tcgen05.mma issue
-//   13         items and copies: publishes the CTA's next item, copies the codes of
+//   8          items and copies: publishes the CTA's next item, copies the codes of
 //              its pages (lane i: page i of the tile) with their scales
+//   12         tcgen05.mma issue
+//   others     conversion of V tiles: none on the scheduler (warp mod 4) that the MMA
+//              warp shares
 // The softmax is the forward kernel's: the reference of a row is the maximum of its
 // first tile and moves only where a tile's row sum reaches 2^40.
 #include <cstdint>
@@ -84,12 +85,12 @@ struct ChunkCfg {
   static constexpr int NBAR = B_DRAIN + 1;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // slack to align the base to 1024
-  static constexpr int CONVERT_WARP = 8, MMA_WARP = 12, COPY_WARP = 13;
+  static constexpr int COPY_WARP = 8, MMA_WARP = 12, CONVERT_WARPS = 6;
   static constexpr int NUM_THREADS = 512;
-  static constexpr int READERS = 13;                    // warps that take an item: all but the copying one and two idle
+  static constexpr int READERS = 15;                    // warps that take an item: all but the copying one
   // Registers a thread after the split; launched with 128.
-  static constexpr int REG_SOFTMAX = 184, REG_CONVERT = 80, REG_OTHER = 64;
-  static_assert(2 * REG_SOFTMAX + REG_CONVERT + REG_OTHER == 4 * 128, "the split takes what the launch gives");
+  static constexpr int REG_SOFTMAX = 184, REG_OTHER = 72;
+  static_assert(2 * REG_SOFTMAX + 2 * REG_OTHER == 4 * 128, "the split takes what the launch gives");
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t S_COL(int t) { return t * 128; }
   __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256 + t * D; }
@@ -168,10 +169,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     for (int i = 0; i < C::NSC; ++i) mbar_init(bar(C::B_SCFULL + i), 1);
     for (int i = 0; i < C::NC; ++i) {
       mbar_init(bar(C::B_CFULL + i), 1);
-      mbar_init(bar(C::B_CEMPTY + i), 4);
+      mbar_init(bar(C::B_CEMPTY + i), C::CONVERT_WARPS);
     }
     for (int i = 0; i < C::NV; ++i) {
-      mbar_init(bar(C::B_VFULL + i), 4);
+      mbar_init(bar(C::B_VFULL + i), C::CONVERT_WARPS);
       mbar_init(bar(C::B_VEMPTY + i), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     return it.tiles > 0;
   };
 
-  if (warp >= C::MMA_WARP) {
+  if (warp >= 8) {
     setmaxnreg_dec<C::REG_OTHER>();
     if (warp == C::COPY_WARP) {
       // ------------------------------------------------------------ items, copies
@@ -449,6 +450,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         wait_drain(bar(C::B_CFULL + s), ((v_tiles - 1 - s) / C::NC) & 1, p.err, p.timeout_ns);
     } else if (warp == C::MMA_WARP) {
       // ------------------------------------------------------------ MMA
+      // The tensor core's queue holds some 190 cycles of products, and a wait for what
+      // is there already, or a commit, costs this thread 50 to 100: each stands between
+      // two batches of products, none beside another where that can be had.  (All waits
+      // of a tile before its products: 880 us on 8192 rows over 32768 keys; a thread for
+      // each row tile, whose products then alternate on the tensor core: 1064.)
       constexpr uint32_t idesc_s = idesc_e4m3(128, 128, false);
       constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
       const uint64_t dQ0 = sdesc8<D>(sb + C::OFF_Q, 16);
@@ -491,28 +497,30 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             }
           }
           if (ok) tc_commit(bar(C::B_KEMPTY + tile % C::NK));
+          wait(C::B_VFULL + tile % C::NV, tile / C::NV);
           for (int j = 0; ok && j < it.tiles; ++j, ++tile) {
             const int vs = tile % C::NV, ks1 = (tile + 1) % C::NK;
             const bool more = j + 1 < it.tiles;
-            wait(C::B_VFULL + vs, tile / C::NV);
-            if (more) wait(C::B_KFULL + ks1, (tile + 1) / C::NK);
-            if (!ok) break;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              if (j < cnt[t]) {
-                if (!wait(C::B_PFULL + t, np[t]++)) break;
+              if (j < cnt[t] && wait(C::B_PFULL + t, np[t]++)) {
                 tc_fence_after();
                 issue_pv(t, vs, j > 0);
                 if (j + 1 == cnt[t]) tc_commit(bar(C::B_ODONE + t));
+              }
+              if (!ok) break;
+              if (t == 0) {
+                if (more && !wait(C::B_KFULL + ks1, (tile + 1) / C::NK)) break;
+              } else {
+                tc_commit(bar(C::B_VEMPTY + vs));
+                if (more && !wait(C::B_VFULL + (tile + 1) % C::NV, (tile + 1) / C::NV)) break;
               }
               if (j + 1 < cnt[t]) {
                 issue_s(t, ks1);
                 tc_commit(bar(C::B_SFULL + t));
               }
             }
-            if (!ok) break;
-            tc_commit(bar(C::B_VEMPTY + vs));
-            if (more) tc_commit(bar(C::B_KEMPTY + ks1));
+            if (ok && more) tc_commit(bar(C::B_KEMPTY + ks1));
           }
         }
         ok = __all_sync(0xffffffffu, ok);
@@ -521,28 +529,26 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         tc_commit(bar(C::B_DRAIN));
         wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
       }
-    }
-  } else if (warp >= C::CONVERT_WARP) {
+    } else {
     // ---------------------------------------------------------------- conversion
-    setmaxnreg_dec<C::REG_CONVERT>();
-    // A thread's 16-byte chunk of codes becomes two chunks of bf16.  The chunks of a
+    // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32
+    // chunks of consecutive rows, every sixth group of them.  The chunks of a
     // quarter-warp lie in two rows, at d = 128 in the two halves of them: neither its
     // reads nor its swizzled writes meet in a bank.
-    const int cw = warp - C::CONVERT_WARP;
-    int row0, chunk;  // of the first pass; a pass is ROWS rows
-    constexpr int CPR = D / 16, ROWS = 128 / CPR, PASSES = kKeys / ROWS, BATCH = 4;
+    const int cw = warp < C::MMA_WARP ? warp - 9 : warp - 10;
+    constexpr int CPR = D / 16, ROWS = 32 / CPR, GROUPS = kKeys / ROWS;
+    int row0, chunk;  // within a group
     if (D == 128) {
       const int rb = (lane >> 2) & 1;
-      row0 = cw * 4 + ((lane >> 4) & 1) * 2 + rb;
+      row0 = ((lane >> 4) & 1) * 2 + rb;
       chunk = (lane & 3) + 4 * (((lane >> 3) & 1) ^ rb);
     } else {
-      row0 = cw * 8 + (lane >> 2);
+      row0 = lane >> 2;
       chunk = lane & 3;
     }
     const uint32_t in0 = row0 * D + chunk * 16;
-    const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES + row0 * 128;
-    // (a pass is a multiple of 8 rows: the swizzle stays)
-    const uint32_t at0 = out0 + ((c0 ^ (row0 & 7)) << 4), at1 = out0 + (((c0 + 1) ^ (row0 & 7)) << 4);
+    const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES;
+    auto place = [&](int row, int half) -> uint32_t { return out0 + row * 128 + (((c0 + half) ^ (row & 7)) << 4); };
     int tile = 0;
     bool ok = true;
     auto wait = [&](int i, int phase) {
@@ -560,30 +566,40 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES + in0;
         const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_VF) + st * C::MAX_PPT;
         uint8_t* out = smem + C::OFF_V + slot * C::TILE_BYTES;
-        uint4 c[BATCH];
+        // (rolled: beside the softmax's code an unrolled loop costs instruction fetches)
+        uint4 next = *reinterpret_cast<const uint4*>(codes + cw * ROWS * D);
+#pragma unroll 1
+        for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
+          const uint4 now = next;
+          const int row = g * ROWS + row0;
+          const uint32_t f = factors[row >> p.block_shift].x;
+          if (g + C::CONVERT_WARPS < GROUPS)
+            next = *reinterpret_cast<const uint4*>(codes + (g + C::CONVERT_WARPS) * ROWS * D);
+          const uint32_t in[4] = {now.x, now.y, now.z, now.w};
+          uint32_t v[8];
 #pragma unroll
-        for (int i0 = 0; i0 < PASSES; i0 += BATCH) {
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) c[i] = *reinterpret_cast<const uint4*>(codes + (i0 + i) * ROWS * D);
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const int row = row0 + (i0 + i) * ROWS;
-            if (row >= held) c[i] = make_uint4(0u, 0u, 0u, 0u);  // slots without a token may hold anything
-            const uint2 f = factors[row >> p.block_shift];
-            const uint32_t in[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-            uint32_t v[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              widen4(in[k], v[2 * k], v[2 * k + 1]);
-              v[2 * k] = mul_bf16x2(v[2 * k], f.x);
-              v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f.x);
+          for (int k = 0; k < 4; ++k) {
+            widen4(in[k], v[2 * k], v[2 * k + 1]);
+            v[2 * k] = mul_bf16x2(v[2 * k], f);
+            v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f);
+          }
+          *reinterpret_cast<uint4*>(out + place(row, 0)) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(out + place(row, 1)) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
+        // Seldom: slots without a token, which may hold anything, become 0; a scale above
+        // 2^55, whose factor does not fit one bf16 number, is a second one.
+        if (held < kKeys || __any_sync(0xffffffffu, factors[lane % C::MAX_PPT].y != kOne2)) {
+#pragma unroll 1
+          for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
+            const int row = g * ROWS + row0;
+            const uint32_t f = factors[row >> p.block_shift].y;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              uint4* at = reinterpret_cast<uint4*>(out + place(row, half));
+              const uint4 x = *at;
+              *at = row >= held ? make_uint4(0u, 0u, 0u, 0u)
+                                : make_uint4(mul_bf16x2(x.x, f), mul_bf16x2(x.y, f), mul_bf16x2(x.z, f), mul_bf16x2(x.w, f));
             }
-            if (f.y != kOne2) {  // a scale above 2^55: the factor does not fit one bf16 number
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[k] = mul_bf16x2(v[k], f.y);
-            }
-            *reinterpret_cast<uint4*>(out + at0 + (i0 + i) * ROWS * 128) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(out + at1 + (i0 + i) * ROWS * 128) = make_uint4(v[4], v[5], v[6], v[7]);
           }
         }
         fence_proxy_async_smem();
@@ -593,6 +609,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           mbar_arrive(bar(C::B_VFULL + slot));
         }
       }
+    }
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -630,22 +647,32 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       bool far = false;
       if (cnt > 0) {
         // ---- Q: each row scaled by a power of two, as two e4m3 terms
+        // (rolled, a batch of loads ahead: run through once an item, unrolled code cost
+        // 10,000 to 17,000 cycles an item in instruction fetches)
         int my_e = 0;  // the exponent of this thread's row
+        constexpr int NB = 4;
+        uint4 x[NB];
+        auto load_rows = [&](int i0) {
 #pragma unroll
-        for (int i0 = 0; i0 < 32 / RPP; i0 += 8) {
-          uint4 x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < NB; ++i) {
             const int from = (i0 + i) * RPP + lane / CH;
-            const int qt = __shfl_sync(0xffffffffu, tok, from), qg = __shfl_sync(0xffffffffu, g, from);
+            const int qt = __shfl_sync(0xffffffffu, tok, from & 31), qg = __shfl_sync(0xffffffffu, g, from & 31);
             x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (first + wq * 32 + from < rows)
+            if (from < 32 && first + wq * 32 + from < rows)
               x[i] = *reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(it.tok0 + qt) * p.ldq +
                                                      static_cast<size_t>(it.hk * p.G + qg) * D + 8 * my_chunk);
           }
+        };
+        load_rows(0);
+#pragma unroll 1
+        for (int i0 = 0; i0 < 32 / RPP; i0 += NB) {
+          uint4 now[NB];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          for (int i = 0; i < NB; ++i) now[i] = x[i];
+          load_rows(i0 + NB);
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
             uint32_t top = 0;
 #pragma unroll
             for (int u = 0; u < 4; ++u) top = __vmaxu2(top, w[u] & 0x7fff7fffu);
@@ -680,14 +707,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         const int sees = exists ? chunk8::visible(it.len, it.n, tok, p.causal) : 0;
         const int all_see = chunk8::visible(it.len, it.n, first / p.G, p.causal);
         for (int j = 0; j < cnt; ++j, ++np) {
-          if (!wait(C::B_SFULL + t, np)) break;
-          tc_fence_after();
-          uint32_t s[4][32];
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) tmem_ld32(tS + ch * 32, s[ch]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) reg_fence(s[ch]);
           // the columns' factors: K's scale of each 16 keys, the row's and the softmax's
           // (not below fp32's least normal number: a masked column stays -infinity)
           const int sc = (first_tile + j) % C::NSC;
@@ -696,6 +715,14 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           float cf[8];
 #pragma unroll
           for (int g16 = 0; g16 < 8; ++g16) cf[g16] = fmaxf(k_scale[(16 * g16) >> p.block_shift] * c_row, 0x1p-126f);
+          if (!wait(C::B_SFULL + t, np)) break;
+          tc_fence_after();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) tmem_ld32(tS + ch * 32, s[ch]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) reg_fence(s[ch]);
           const int kv0 = (it.k0 + j) * kKeys;
           if (all_see - kv0 < kKeys) {
             const int end = sees - kv0;
@@ -722,6 +749,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           auto p_pass = [&]() -> float {
             const float m = m_ref == -CUDART_INF_F ? 0.f : m_ref;
             const uint64_t nm2 = f2_pack(-m, -m);
+            uint64_t cf2[8];
+#pragma unroll
+            for (int g16 = 0; g16 < 8; ++g16) cf2[g16] = f2_pack(cf[g16], cf[g16]);
             uint64_t ls2[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) ls2[k] = f2_pack(0.f, 0.f);
@@ -730,10 +760,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
               uint32_t pk[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const float f = cf[2 * ch + e / 8];
                 float x0, x1;
-                f2_unpack(ffma2(f2_pack(__uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1])), f2_pack(f, f),
-                                nm2),
+                f2_unpack(ffma2(f2_pack(__uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1])),
+                                cf2[2 * ch + e / 8], nm2),
                           x0, x1);
                 const float p0 = ex2_approx(x0);
                 const float p1 = ex2_approx(x1);
@@ -764,15 +793,17 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             m_ref = row_max();
             set_far();
           }
-          if (far) form_y();
-          float lt = p_pass();
-          if (__any_sync(0xffffffffu, !(lt < 0x1p40f))) {
+          float lt;
+#pragma unroll 1
+          for (bool moved = false;; moved = true) {  // (one copy of the pass in the code)
+            if (far) form_y();
+            lt = p_pass();
+            if (moved || !__any_sync(0xffffffffu, !(lt < 0x1p40f))) break;
             const float m_new = fmaxf(m_ref, row_max());
             const float alpha = (m_ref == -CUDART_INF_F) ? 0.f : ex2_approx(m_ref - m_new);
             m_ref = m_new;
             l *= alpha;
             set_far();
-            if (far) form_y();
 #pragma unroll 1
             for (int ch = 0; j > 0 && ch < D / 16; ++ch) {
               uint32_t o[16];
@@ -784,7 +815,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
               tmem_st16(tO + ch * 16, o);
             }
             tmem_wait_st();
-            lt = p_pass();
           }
           l += lt;
           tmem_wait_st();
@@ -818,7 +848,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         }
         tc_fence_before();
         __syncwarp();
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < 32 / RPP; ++i) {
           const int from = i * RPP + lane / CH;
           const int qt = __shfl_sync(0xffffffffu, tok, from), qg = __shfl_sync(0xffffffffu, g, from);
