@@ -6,7 +6,7 @@
 // rows, token by token (row f: token f / G, head f mod G of the group).  An item is
 // kRows of them over one key/value head; its tiles are the runs of kKeys keys that
 // its last row sees, at least one.  The items in the order (sequence, row block,
-// key/value head), tile after tile, are cut into runs of equal length, one a CTA.
+// key/value head), tile after tile, are cut into runs of equal cost, one a CTA.
 #pragma once
 
 #ifdef __CUDACC__
@@ -38,10 +38,17 @@ FA_CHUNK_FN int row_tiles(int len, int n, int G, int first, int count, bool caus
   return tiles(visible(len, n, last / G, causal));
 }
 
-// Run c of `ctas` over `total` tiles begins at run_start(c); tile t lies in run run_of(t).
+// A run is counted in units: one for each tile, and `extra` before an item's first,
+// as many as its fixed cost is tiles' time (kItemCost; less where a CTA has fewer tiles
+// than that: with little work every tile had better have a CTA of its own).
+constexpr int kItemCost = 3;
+FA_CHUNK_FN int extra_units(long long all_tiles, long long ctas) {
+  return all_tiles / ctas <= kItemCost ? static_cast<int>(all_tiles / ctas) - 1 : kItemCost;
+}
+// Run c of `ctas` over `total` units begins at run_start(c); unit u lies in run run_of(u).
 FA_CHUNK_FN long long run_start(long long c, long long total, long long ctas) { return c * total / ctas; }
-FA_CHUNK_FN int run_of(long long t, long long total, long long ctas) {
-  return static_cast<int>(((t + 1) * ctas + total - 1) / total - 1);
+FA_CHUNK_FN int run_of(long long u, long long total, long long ctas) {
+  return static_cast<int>(((u + 1) * ctas + total - 1) / total - 1);
 }
 
 }  // namespace chunk8

@@ -90,13 +90,12 @@ __device__ __forceinline__ uint32_t swz(int row, int byte) {
   return row * W + ((((byte >> 4) ^ line) & MASK) << 4) + (byte & 15);
 }
 // Descriptor of an operand in W-byte rows swizzled over W bytes (16: not
-// swizzled), 8 rows an atom.  K-major: rows are M or N.  MN-major: rows are K,
-// lbo the distance to the next W bytes of M.
+// swizzled), 8 rows an atom, the next 8 `next8` bytes on.  K-major: rows are M or N.
+// MN-major: rows are K, lbo the distance to the next W bytes of M.
 template <int W>
-__device__ __forceinline__ uint64_t sdesc8(uint32_t saddr, uint32_t lbo) {
+__device__ __forceinline__ uint64_t sdesc8(uint32_t saddr, uint32_t lbo, uint32_t next8 = 8 * W) {
   constexpr uint64_t mode = W == 128 ? 2 : W == 64 ? 4 : W == 32 ? 6 : 0;
   // Without a swizzle the two distances change places in MN-major.
-  constexpr uint32_t next8 = 8 * W;
   const uint32_t lead = W == 16 ? next8 : lbo, stride = W == 16 ? lbo : next8;
   return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>((stride >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (mode << 61);

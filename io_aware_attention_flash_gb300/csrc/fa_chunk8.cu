@@ -58,7 +58,7 @@ struct ChunkCfg {
   static constexpr int NSC = NK + 1;                    // ring of K's scales
   static constexpr int NI = 4;                          // published items
   static constexpr int MAX_PPT = kKeys / 16;            // pages of a tile, at most
-  static constexpr int OFF_Q = 0;                       // two row tiles, each its first terms, then its second
+  static constexpr int OFF_Q = 0;                       // two row tiles: of each 8 rows the first terms, then the second
   static constexpr int OFF_V = OFF_Q + 2 * TILE_BYTES;
   static constexpr int OFF_K = OFF_V + NV * TILE_BYTES;
   static constexpr int OFF_C = OFF_K + NK * CODE_BYTES;
@@ -66,8 +66,8 @@ struct ChunkCfg {
   static constexpr int OFF_VF = OFF_KS + NSC * MAX_PPT * 4;        // [NC][pages] V's two factors, bf16 pairs
   static constexpr int ITEM_INTS = 12;
   static constexpr int OFF_ITEM = OFF_VF + NC * MAX_PPT * 8;
-  static constexpr int OFF_SCAN = OFF_ITEM + NI * ITEM_INTS * 4;   // [16] sums of a scan, then its find
-  static constexpr int OFF_BAR = OFF_SCAN + 18 * 8;
+  static constexpr int OFF_SCAN = OFF_ITEM + NI * ITEM_INTS * 4;   // [2][16] sums, then what is found
+  static constexpr int OFF_BAR = OFF_SCAN + 34 * 8;
   static constexpr int B_IFULL = 0;
   static constexpr int B_IEMPTY = B_IFULL + NI;
   static constexpr int B_KFULL = B_IEMPTY + NI;
@@ -82,7 +82,8 @@ struct ChunkCfg {
   static constexpr int B_PFULL = B_SFULL + 2;
   static constexpr int B_ODONE = B_PFULL + 2;
   static constexpr int B_DRAIN = B_ODONE + 2;
-  static constexpr int NBAR = B_DRAIN + 1;
+  static constexpr int B_RAW = B_DRAIN + 1;             // [8]: a softmax warp's rows of Q have landed
+  static constexpr int NBAR = B_RAW + 8;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // slack to align the base to 1024
   static constexpr int COPY_WARP = 8, MMA_WARP = 12, CONVERT_WARPS = 6;
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       mbar_init(bar(C::B_ODONE + t), 1);
     }
     mbar_init(bar(C::B_DRAIN), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(bar(C::B_RAW + i), 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
@@ -201,15 +203,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     }
   }
 
-  // ---- this CTA's place: the tiles of all (sequence, row block) pairs counted, then
-  // the pair that holds the run's first tile
+  // ---- this CTA's place: the tiles and items of all (sequence, row block) pairs
+  // counted, then the pair that holds the run's first unit
   const int pairs = p.B * p.row_blocks;
   long long* scan = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
-  auto pair_tiles = [&](int x) -> long long {
+  auto pair_tiles = [&](int x) -> int {
     const int b = x / p.row_blocks, rb = x - b * p.row_blocks;
     int tok0, n, len;
     chunk_seq(p, b, tok0, n, len);
-    return static_cast<long long>(p.Hk) * chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
+    return chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
   };
   auto warp_scan = [&](long long v) {  // inclusive
 #pragma unroll
@@ -219,44 +221,49 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     }
     return v;
   };
-  long long own = 0;  // tiles of pair tid, where one pass takes all pairs; else of all of this thread's
-  for (int x = tid; x < pairs; x += C::NUM_THREADS) own += pair_tiles(x);
-  long long upto = warp_scan(own);
-  if (lane == 31) scan[warp] = upto;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const long long s = scan[i];
-    if (i < warp) upto += s;
-    total += s;
+  int one = 0;  // tiles of pair tid, if one pass takes all pairs
+  long long tiles_sum = 0, items_sum = 0;
+  for (int x = tid; x < pairs; x += C::NUM_THREADS) {
+    one = pair_tiles(x);
+    tiles_sum += one;
+    items_sum += one > 0;
   }
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));  // every one of them has a tile
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    tiles_sum += __shfl_xor_sync(0xffffffffu, tiles_sum, off);
+    items_sum += __shfl_xor_sync(0xffffffffu, items_sum, off);
+  }
+  if (lane == 0) scan[warp] = tiles_sum, scan[16 + warp] = items_sum;
+  __syncthreads();
+  tiles_sum = items_sum = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) tiles_sum += scan[i], items_sum += scan[16 + i];
+  tiles_sum *= p.Hk, items_sum *= p.Hk;
+  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), tiles_sum));
   if (tid == 0) p.merge[blockIdx.x * 8] = -1;
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const long long t_lo = chunk8::run_start(blockIdx.x, total, ctas), t_hi = chunk8::run_start(blockIdx.x + 1LL, total, ctas);
-  long long* found = scan + 16;  // first tile of the pair; the pair
-  if (pairs <= C::NUM_THREADS) {
-    if (t_lo >= upto - own && t_lo < upto) {
-      found[0] = upto - own;
-      found[1] = tid;
-    }
-  } else {
+  const int extra = chunk8::extra_units(tiles_sum, ctas);
+  const long long total = tiles_sum + extra * items_sum;
+  auto pair_units = [&](int tiles) -> long long { return tiles > 0 ? static_cast<long long>(p.Hk) * (tiles + extra) : 0; };
+  const long long u_lo = chunk8::run_start(blockIdx.x, total, ctas), u_hi = chunk8::run_start(blockIdx.x + 1LL, total, ctas);
+  long long* found = scan + 32;  // first unit of the pair; the pair
+  {
     long long base = 0;
-    for (int x0 = 0; x0 < pairs && base <= t_lo; x0 += C::NUM_THREADS) {
-      const long long w = x0 + tid < pairs ? pair_tiles(x0 + tid) : 0;
+    for (int x0 = 0; x0 < pairs && base <= u_lo; x0 += C::NUM_THREADS) {
+      if (pairs > C::NUM_THREADS) one = x0 + tid < pairs ? pair_tiles(x0 + tid) : 0;
+      const long long w = pair_units(one);
       long long sum = warp_scan(w);
-      __syncthreads();  // (the sums of the round before have been read)
+      __syncthreads();  // (the sums before have been read)
       if (lane == 31) scan[warp] = sum;
       __syncthreads();
       long long all = 0;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const long long s = scan[i];
-        if (i < warp) sum += s;
-        all += s;
+        const long long v = scan[i];
+        if (i < warp) sum += v;
+        all += v;
       }
-      if (t_lo >= base + sum - w && t_lo < base + sum) {
+      if (u_lo >= base + sum - w && u_lo < base + sum) {
         found[0] = base + sum - w;
         found[1] = x0 + tid;
       }
@@ -305,11 +312,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       struct Unit {
         int b, hk, rb, k0, k1, nt, n, len, tok0;  // the item (tiles k0 .. k1 of nt)
         int kt, tiles;                            // first tile of the unit, and how many
+        long long last;                           // the item's last unit
         int page;                                 // this lane's page (of 32 / ppt tiles), -1: none
         float ks, vs;
       };
       int x = static_cast<int>(found[1]);
-      long long x_start = found[0], t = t_lo;
+      long long x_start = found[0], at = u_lo;  // first unit of the pair; the next unit
       int nt = 0, n = 0, len = 0, tok0 = 0, b = 0, rb = 0;
       auto load_pair = [&]() {
         b = x / p.row_blocks;
@@ -322,24 +330,26 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       load_pair();
       auto next_unit = [&](Unit& u) {
         u.tiles = 0;
-        if (t >= t_hi) return;
-        while (t >= x_start + static_cast<long long>(p.Hk) * nt) {
-          x_start += static_cast<long long>(p.Hk) * nt;
-          if (++x >= pairs) {
-            t = t_hi;
-            return;
+        while (u.tiles <= 0) {
+          if (at >= u_hi) return;
+          while (at >= x_start + pair_units(nt)) {
+            x_start += pair_units(nt);
+            if (++x >= pairs) {
+              at = u_hi;
+              return;
+            }
+            load_pair();
           }
-          load_pair();
+          const int hk = static_cast<int>((at - x_start) / (nt + extra));
+          const long long item = x_start + static_cast<long long>(hk) * (nt + extra), first = item + extra;
+          u.b = b, u.rb = rb, u.n = n, u.len = len, u.tok0 = tok0, u.nt = nt, u.hk = hk;
+          u.kt = static_cast<int>(max(at - first, 0LL));
+          u.k0 = static_cast<int>(max(u_lo - first, 0LL));
+          u.k1 = static_cast<int>(min(u_hi - first, static_cast<long long>(nt)));
+          u.tiles = min(u.k1 - u.kt, 32 / ppt);  // (none: the run ends before the item's first tile)
+          u.last = first + nt - 1;
+          at = u.tiles > 0 ? first + u.kt + u.tiles : u_hi;
         }
-        const long long at = t - x_start;
-        u.b = b, u.rb = rb, u.n = n, u.len = len, u.tok0 = tok0, u.nt = nt;
-        u.hk = static_cast<int>(at / nt);
-        u.kt = static_cast<int>(at - static_cast<long long>(u.hk) * nt);
-        const long long head_start = x_start + static_cast<long long>(u.hk) * nt;
-        u.k0 = static_cast<int>(max(t_lo - head_start, 0LL));
-        u.k1 = static_cast<int>(min(t_hi - head_start, static_cast<long long>(nt)));
-        u.tiles = min(u.k1 - u.kt, 32 / ppt);
-        t += u.tiles;
         u.page = -1;
         if (lane < u.tiles * ppt && u.kt * ppt + lane < cache8::pages_of(len, p.block_shift))
           u.page = p.table[static_cast<size_t>(b) * p.table_cols + u.kt * ppt + lane];
@@ -377,10 +387,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             cnt1 = max(min(u.k1, chunk8::row_tiles(u.len, u.n, p.G, first + kHalf, kHalf, p.causal)) - u.k0, 0);
             if (!whole && u.k0 == 0) {
               // begins here and ends in another CTA's run: joined by the second kernel
-              const long long last = t_hi - 1 + (u.nt - u.k1);
               int* m = p.merge + blockIdx.x * 8;
               m[1] = u.tok0, m[2] = u.n, m[3] = u.hk, m[4] = u.rb;
-              m[0] = chunk8::run_of(last, total, ctas);
+              m[0] = chunk8::run_of(u.last, total, ctas);
             }
           }
           dst[0] = make_int4(u.b, u.hk, u.rb, u.k0);
@@ -457,7 +466,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       // each row tile, whose products then alternate on the tensor core: 1064.)
       constexpr uint32_t idesc_s = idesc_e4m3(128, 128, false);
       constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
-      const uint64_t dQ0 = sdesc8<D>(sb + C::OFF_Q, 16);
+      const uint64_t dQ0 = sdesc8<D>(sb + C::OFF_Q, 16, 16 * D);
       const uint64_t dK0 = sdesc8<D>(sb + C::OFF_K, 16);
       const uint64_t dV0 = sdesc_sw128(sb + C::OFF_V, C::BLK_BYTES, 1024);
       auto issue_s = [&](int t, int ks) {
@@ -466,7 +475,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         for (int term = 0; term < 2; ++term)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_e4m3(tmem + C::S_COL(t), sdesc_add(dQ, term * C::CODE_BYTES + kk * 32), sdesc_add(dK, kk * 32), idesc_s,
+            mma_e4m3(tmem + C::S_COL(t), sdesc_add(dQ, term * 8 * D + kk * 32), sdesc_add(dK, kk * 32), idesc_s,
                      term + kk > 0);
       };
       auto issue_pv = [&](int t, int vs, bool acc) {
@@ -618,12 +627,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t tS = lane_addr + C::S_COL(t), tO = lane_addr + C::O_COL(t);
     uint8_t* q_smem = smem + C::OFF_Q + t * C::TILE_BYTES;
-    // A warp moves its 32 rows between memory and their swizzled places 16 bytes a
-    // lane, RPP rows at a time.
+    // A warp moves its 32 rows 16 bytes a lane, RPP rows at a time.
     constexpr int CH = D / 8, RPP = 32 / CH;
     const int my_chunk = lane % CH, my_row = wq * 32 + lane / CH;
-    auto place = [&](int row, int ch) { return q_smem + (ch / 8) * C::BLK_BYTES + row * 128 + (((ch % 8) ^ (row & 7)) << 4); };
-    int np = 0, no = 0;  // tiles and items of this row tile so far
+    auto place = [&](int row, int ch) { return q_smem + row * (2 * D) + ((ch ^ (row & 7)) << 4); };  // (within the warp's own rows)
+    int np = 0, no = 0, n_raw = 0;  // tiles and items of this row tile so far; of the warp's rows of Q
     int tile0 = 0;       // tiles of the items before
     bool ok = true;
     auto wait = [&](int i, int phase) {
@@ -646,33 +654,43 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       // counts in the exponent
       bool far = false;
       if (cnt > 0) {
-        // ---- Q: each row scaled by a power of two, as two e4m3 terms
-        // (rolled, a batch of loads ahead: run through once an item, unrolled code cost
-        // 10,000 to 17,000 cycles an item in instruction fetches)
-        int my_e = 0;  // the exponent of this thread's row
-        constexpr int NB = 4;
-        uint4 x[NB];
-        auto load_rows = [&](int i0) {
-#pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const int from = (i0 + i) * RPP + lane / CH;
-            const int qt = __shfl_sync(0xffffffffu, tok, from & 31), qg = __shfl_sync(0xffffffffu, g, from & 31);
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (from < 32 && first + wq * 32 + from < rows)
-              x[i] = *reinterpret_cast<const uint4*>(p.q + static_cast<size_t>(it.tok0 + qt) * p.ldq +
-                                                     static_cast<size_t>(it.hk * p.G + qg) * D + 8 * my_chunk);
+        // ---- Q: the warp's rows, all in flight at once, then each row scaled by a power
+        // of two, as two e4m3 terms, in place: 8 rows' terms take the room of the rows.
+        // (Loaded through registers in four batches, each as long as a miss: 5 us an item.)
+        {
+          const int from = first + wq * 32, count = max(min(rows - from, 32), 0);
+          const int tok_a = from / p.G, toks = count > 0 ? (from + count - 1) / p.G - tok_a + 1 : 0;
+          fence_proxy_async_smem();  // (the staging of O has been read)
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::B_RAW + warp), count * (2 * D));
+          __syncwarp();
+          for (int i = lane; i < toks; i += 32) {
+            const int f0 = max((tok_a + i) * p.G, from), f1 = min((tok_a + i + 1) * p.G, from + count);
+            bulk_load(sb + C::OFF_Q + t * C::TILE_BYTES + (f0 - first) * (2 * D),
+                      p.q + static_cast<size_t>(it.tok0 + tok_a + i) * p.ldq +
+                          (static_cast<size_t>(it.hk) * p.G + f0 - (tok_a + i) * p.G) * D,
+                      (f1 - f0) * (2 * D), bar(C::B_RAW + warp));
           }
-        };
-        load_rows(0);
+          ++n_raw;
+          if (!wait(C::B_RAW + warp, n_raw - 1)) break;
+        }
+        // (rolled: run through once an item, unrolled code is all instruction fetches)
+        int my_e = 0;  // the exponent of this thread's row
 #pragma unroll 1
-        for (int i0 = 0; i0 < 32 / RPP; i0 += NB) {
-          uint4 now[NB];
-#pragma unroll
-          for (int i = 0; i < NB; ++i) now[i] = x[i];
-          load_rows(i0 + NB);
+        for (int r8 = 0; r8 < 32; r8 += 8) {
+          constexpr int NB = 8 / RPP;
+          uint8_t* rows8 = q_smem + (wq * 32 + r8) * (2 * D);
+          uint4 x[NB];
 #pragma unroll
           for (int i = 0; i < NB; ++i) {
-            const uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+            const int row = i * RPP + lane / CH;
+            x[i] = *reinterpret_cast<const uint4*>(rows8 + row * (2 * D) + 16 * my_chunk);
+            if (first + wq * 32 + r8 + row >= rows) x[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
             uint32_t top = 0;
 #pragma unroll
             for (int u = 0; u < 4; ++u) top = __vmaxu2(top, w[u] & 0x7fff7fffu);
@@ -683,7 +701,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             // most, at least 2^-126 (fp32's smallest that is not subnormal)
             const int e = min(scale_exponent(top, -126), 120);
             const int of_row = __shfl_sync(0xffffffffu, e, lane % RPP * CH);
-            if (lane / RPP == i0 + i) my_e = of_row;
+            if (lane / RPP == r8 / RPP + i) my_e = of_row;
             const float inv = exp2_int(-e);
             uint32_t hi[2], lo[2];
 #pragma unroll
@@ -695,9 +713,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
               unpack_e4m3x4(hi[u], h);
               lo[u] = pack_e4m3x4(v[0] - h[0], v[1] - h[1], v[2] - h[2], v[3] - h[3]);
             }
-            uint8_t* at = q_smem + swz<D>(my_row + (i0 + i) * RPP, 8 * my_chunk);
+            uint8_t* at = rows8 + swz<D>(i * RPP + lane / CH, 8 * my_chunk);
             *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(at + C::CODE_BYTES) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(at + 8 * D) = make_uint2(lo[0], lo[1]);
           }
         }
         const float c_row = exp2_int(my_e) * p.scale_log2;
@@ -881,6 +899,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         tc_fence_before();
       }
     }
+    // A copy issued lands before the CTA may exit, whoever aborted.
+    if (n_raw > 0) wait_drain(bar(C::B_RAW + warp), (n_raw - 1) & 1, p.err, p.timeout_ns);
   }
 
   tc_fence_before();

@@ -21,7 +21,9 @@ int main(int argc, char** argv) {
       std::printf("%%d %%d %%d\\n", row_tiles(len, n, G, rb * kRows, kRows, causal), row_tiles(len, n, G, rb * kRows, kHalf, causal),
                   row_tiles(len, n, G, rb * kRows + kHalf, kHalf, causal));
     std::printf("%%d %%d\\n", visible(len, n, 0, causal), visible(len, n, n - 1, causal));
-  } else {  // total ctas: the runs' beginnings, and the run of each run's first and last tile
+  } else if (argc == 4) {  // tiles ctas 0: the units before an item's first tile
+    std::printf("%%d\n", extra_units(std::atoll(argv[1]), std::atoll(argv[2])));
+  } else {  // total ctas: the runs' beginnings, and the run of each run's first and last unit
     const long long total = std::atoll(argv[1]), ctas = std::atoll(argv[2]);
     for (long long c = 0; c < ctas; ++c)
       std::printf("%%lld %%d %%d\\n", run_start(c, total, ctas), run_of(run_start(c, total, ctas), total, ctas),
@@ -72,3 +74,10 @@ def test_runs_are_even_and_found_again(program, total):
     starts = [row[0] for row in out] + [total]
     assert starts[0] == 0 and all(total // ctas <= b - a <= -(-total // ctas) for a, b in zip(starts, starts[1:]))
     assert [row[1:] for row in out] == [[c, c] for c in range(ctas)]
+
+
+@pytest.mark.parametrize("tiles,ctas", [(1, 1), (7, 7), (152, 152), (303, 152), (304, 152), (455, 152), (456, 152), (10 ** 9, 152)])
+def test_units_before_an_item(program, tiles, ctas):
+    """No more than a CTA has tiles, so that no run is all fixed cost where work is scarce."""
+    (extra,), = program(tiles, ctas, 0)
+    assert 0 <= extra <= 3 and extra < tiles / ctas and (extra == 3 or extra == tiles // ctas - 1)
