@@ -466,6 +466,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       // each row tile, whose products then alternate on the tensor core: 1064.)
       constexpr uint32_t idesc_s = idesc_e4m3(128, 128, false);
       constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint64_t dQ0 = sdesc8<D>(sb + C::OFF_Q, 16, 16 * D);
       const uint64_t dK0 = sdesc8<D>(sb + C::OFF_K, 16);
       const uint64_t dV0 = sdesc_sw128(sb + C::OFF_V, C::BLK_BYTES, 1024);
@@ -475,69 +476,72 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         for (int term = 0; term < 2; ++term)
 #pragma unroll
           for (int kk = 0; kk < D / 32; ++kk)
-            mma_e4m3(tmem + C::S_COL(t), sdesc_add(dQ, term * 8 * D + kk * 32), sdesc_add(dK, kk * 32), idesc_s,
+            mma_e4m3(tm + C::S_COL(t), sdesc_add(dQ, term * 8 * D + kk * 32), sdesc_add(dK, kk * 32), idesc_s,
                      term + kk > 0);
       };
       auto issue_pv = [&](int t, int vs, bool acc) {
         const uint64_t dV = sdesc_add(dV0, vs * C::TILE_BYTES);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(tmem + C::O_COL(t), tmem + C::S_COL(t) + kk * 8, sdesc_add(dV, kk * 2048), idesc_o,
+          mma_ts(tm + C::O_COL(t), tm + C::S_COL(t) + kk * 8, sdesc_add(dV, kk * 2048), idesc_o,
                  (acc || kk > 0) ? 1u : 0u);
       };
       bool ok = true;
-      auto wait = [&](int i, int phase) {
+      auto wait = [&](int i, int phase) {  // (the whole warp, which stays together)
         ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
         return ok;
       };
       int tile = 0;                          // K and V tiles so far
       int nq[2] = {0, 0}, np[2] = {0, 0};    // items and P tiles of each row tile so far
       Item it;
       while (ok && take_item(it)) {
-        if (lane == 0) {
-          const int cnt[2] = {it.cnt0, it.cnt1};
-          wait(C::B_KFULL + tile % C::NK, tile / C::NK);
+        const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+        const int cnt[2] = {__shfl_sync(0xffffffffu, it.cnt0, 0), __shfl_sync(0xffffffffu, it.cnt1, 0)};
+        if (!wait(C::B_KFULL + tile % C::NK, tile / C::NK)) break;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (ok && cnt[t] > 0 && wait(C::B_Q + t, nq[t]++)) {
-              tc_fence_after();
+        for (int t = 0; t < 2; ++t) {
+          if (cnt[t] > 0 && wait(C::B_Q + t, nq[t]++)) {
+            tc_fence_after();
+            if (elect_one()) {
               issue_s(t, tile % C::NK);
               tc_commit(bar(C::B_SFULL + t));
             }
           }
-          if (ok) tc_commit(bar(C::B_KEMPTY + tile % C::NK));
-          wait(C::B_VFULL + tile % C::NV, tile / C::NV);
-          for (int j = 0; ok && j < it.tiles; ++j, ++tile) {
-            const int vs = tile % C::NV, ks1 = (tile + 1) % C::NK;
-            const bool more = j + 1 < it.tiles;
+        }
+        if (!ok) break;
+        if (elect_one()) tc_commit(bar(C::B_KEMPTY + tile % C::NK));
+        wait(C::B_VFULL + tile % C::NV, tile / C::NV);
+        for (int j = 0; ok && j < tiles; ++j, ++tile) {
+          const int vs = tile % C::NV, ks1 = (tile + 1) % C::NK;
+          const bool more = j + 1 < tiles;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (j < cnt[t] && wait(C::B_PFULL + t, np[t]++)) {
-                tc_fence_after();
+          for (int t = 0; t < 2; ++t) {
+            if (j < cnt[t] && wait(C::B_PFULL + t, np[t]++)) {
+              tc_fence_after();
+              if (elect_one()) {
                 issue_pv(t, vs, j > 0);
                 if (j + 1 == cnt[t]) tc_commit(bar(C::B_ODONE + t));
               }
-              if (!ok) break;
-              if (t == 0) {
-                if (more && !wait(C::B_KFULL + ks1, (tile + 1) / C::NK)) break;
-              } else {
-                tc_commit(bar(C::B_VEMPTY + vs));
-                if (more && !wait(C::B_VFULL + (tile + 1) % C::NV, (tile + 1) / C::NV)) break;
-              }
-              if (j + 1 < cnt[t]) {
-                issue_s(t, ks1);
-                tc_commit(bar(C::B_SFULL + t));
-              }
             }
-            if (ok && more) tc_commit(bar(C::B_KEMPTY + ks1));
+            if (!ok) break;
+            if (t == 0) {
+              if (more && !wait(C::B_KFULL + ks1, (tile + 1) / C::NK)) break;
+            } else {
+              if (elect_one()) tc_commit(bar(C::B_VEMPTY + vs));
+              if (more && !wait(C::B_VFULL + (tile + 1) % C::NV, (tile + 1) / C::NV)) break;
+            }
+            if (j + 1 < cnt[t] && elect_one()) {
+              issue_s(t, ks1);
+              tc_commit(bar(C::B_SFULL + t));
+            }
           }
+          if (ok && more && elect_one()) tc_commit(bar(C::B_KEMPTY + ks1));
         }
-        ok = __all_sync(0xffffffffu, ok);
       }
-      if (lane == 0) {  // every MMA issued so far must finish before tensor memory is released
-        tc_commit(bar(C::B_DRAIN));
-        wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
-      }
+      // every MMA issued so far must finish before tensor memory is released
+      if (elect_one()) tc_commit(bar(C::B_DRAIN));
+      wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
     } else {
     // ---------------------------------------------------------------- conversion
     // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32

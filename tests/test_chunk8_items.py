@@ -22,7 +22,7 @@ int main(int argc, char** argv) {
                   row_tiles(len, n, G, rb * kRows + kHalf, kHalf, causal));
     std::printf("%%d %%d\\n", visible(len, n, 0, causal), visible(len, n, n - 1, causal));
   } else if (argc == 4) {  // tiles ctas 0: the units before an item's first tile
-    std::printf("%%d\n", extra_units(std::atoll(argv[1]), std::atoll(argv[2])));
+    std::printf("%%d\\n", extra_units(std::atoll(argv[1]), std::atoll(argv[2])));
   } else {  // total ctas: the runs' beginnings, and the run of each run's first and last unit
     const long long total = std::atoll(argv[1]), ctas = std::atoll(argv[2]);
     for (long long c = 0; c < ctas; ++c)
