@@ -55,10 +55,7 @@ struct ChunkCfg {
   static constexpr int NK = D == 128 ? 3 : 6;           // ring of K's codes
   static constexpr int NC = NK;                         // ring of V's codes
   static constexpr int NV = D == 128 ? 2 : 3;           // ring of V in bf16
-  // Ring of K's scales: a slot is written again once S of the tile NK before has been
-  // formed, by when the softmax has taken the tile one further back (at d = 64, where S
-  // runs a tile ahead, two).
-  static constexpr int NSC = NK + (D == 64 ? 2 : 1);
+  static constexpr int NSC = NK + 1;                    // ring of K's scales
   static constexpr int NI = 4;                          // published items
   static constexpr int MAX_PPT = kKeys / 16;            // pages of a tile, at most
   static constexpr int OFF_Q = 0;                       // two row tiles: of each 8 rows the first terms, then the second
@@ -86,8 +83,7 @@ struct ChunkCfg {
   static constexpr int B_ODONE = B_PFULL + 2;
   static constexpr int B_DRAIN = B_ODONE + 2;
   static constexpr int B_RAW = B_DRAIN + 1;             // [8]: a softmax warp's rows of Q have landed
-  static constexpr int B_SREAD = B_RAW + 8;             // (OWN_P) S has been read
-  static constexpr int NBAR = B_SREAD + 2;
+  static constexpr int NBAR = B_RAW + 8;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // slack to align the base to 1024
   static constexpr int COPY_WARP = 8, MMA_WARP = 12, CONVERT_WARPS = 6;
@@ -99,11 +95,6 @@ struct ChunkCfg {
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t S_COL(int t) { return t * 128; }
   __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256 + t * D; }
-  // At d = 128 S and O fill tensor memory and P takes S's place; S of the next tile has
-  // to wait for P V.  At d = 64 P has columns of its own, and S of the next tile is
-  // formed as soon as the softmax has read this one's.
-  static constexpr bool OWN_P = D == 64;
-  __host__ __device__ static constexpr uint32_t P_COL(int t) { return OWN_P ? 384 + t * 64 : S_COL(t); }
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(OFF_K % 1024 == 0 && OFF_C % 1024 == 0 && CODE_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(OFF_ITEM % 16 == 0 && OFF_KS % 16 == 0 && OFF_SCAN % 8 == 0, "vector accesses");
@@ -190,7 +181,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       mbar_init(bar(C::B_SFULL + t), 1);
       mbar_init(bar(C::B_PFULL + t), 128);
       mbar_init(bar(C::B_ODONE + t), 1);
-      mbar_init(bar(C::B_SREAD + t), 128);
     }
     mbar_init(bar(C::B_DRAIN), 1);
     for (int i = 0; i < 8; ++i) mbar_init(bar(C::B_RAW + i), 1);
@@ -493,7 +483,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         const uint64_t dV = sdesc_add(dV0, vs * C::TILE_BYTES);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(tm + C::O_COL(t), tm + C::P_COL(t) + kk * 8, sdesc_add(dV, kk * 2048), idesc_o,
+          mma_ts(tm + C::O_COL(t), tm + C::S_COL(t) + kk * 8, sdesc_add(dV, kk * 2048), idesc_o,
                  (acc || kk > 0) ? 1u : 0u);
       };
       bool ok = true;
@@ -504,12 +494,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       };
       int tile = 0;                          // K and V tiles so far
       int nq[2] = {0, 0}, np[2] = {0, 0};    // items and P tiles of each row tile so far
-      int ns[2] = {0, 0};                    // (OWN_P) S tiles that have been read
       Item it;
       while (ok && take_item(it)) {
         const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
         const int cnt[2] = {__shfl_sync(0xffffffffu, it.cnt0, 0), __shfl_sync(0xffffffffu, it.cnt1, 0)};
-        const int tile0 = tile;
         if (!wait(C::B_KFULL + tile % C::NK, tile / C::NK)) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -523,48 +511,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         }
         if (!ok) break;
         if (elect_one()) tc_commit(bar(C::B_KEMPTY + tile % C::NK));
-        if constexpr (C::OWN_P) {
-          // S of tile 1, then, tile by tile, P V and the S of the tile after the next
-          auto next_s = [&](int t, int j) {  // S of tile j of the item, once S of tile j - 1 has been read
-            const int x = tile0 + j;
-            if (t == 0 && !wait(C::B_KFULL + x % C::NK, x / C::NK)) return;
-            if (j < cnt[t] && wait(C::B_SREAD + t, ns[t]++)) {
-              tc_fence_after();
-              if (elect_one()) {
-                issue_s(t, x % C::NK);
-                tc_commit(bar(C::B_SFULL + t));
-              }
-            }
-            if (ok && t == 1 && elect_one()) tc_commit(bar(C::B_KEMPTY + x % C::NK));
-          };
-          if (tiles > 1) {
-            next_s(0, 1);
-            if (ok) next_s(1, 1);
-          }
-          for (int j = 0; ok && j < tiles; ++j) {
-            const int x = tile0 + j;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (t == 0 && !wait(C::B_VFULL + x % C::NV, x / C::NV)) break;
-              if (j < cnt[t] && wait(C::B_PFULL + t, np[t]++)) {
-                tc_fence_after();
-                if (elect_one()) {
-                  issue_pv(t, x % C::NV, j > 0);
-                  tc_commit(bar(C::B_ODONE + t));
-                }
-              }
-              if (!ok) break;
-              if (t == 1 && elect_one()) tc_commit(bar(C::B_VEMPTY + x % C::NV));
-              if (j + 2 < tiles) next_s(t, j + 2);
-              if (!ok) break;
-            }
-          }
-          // (S of an item's last tile is read before its P is there)
-          for (int t = 0; ok && t < 2; ++t)
-            if (cnt[t] > 0) wait(C::B_SREAD + t, ns[t]++);
-          tile = tile0 + tiles;
-          continue;
-        }
         wait(C::B_VFULL + tile % C::NV, tile / C::NV);
         for (int j = 0; ok && j < tiles; ++j, ++tile) {
           const int vs = tile % C::NV, ks1 = (tile + 1) % C::NK;
@@ -683,13 +629,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     setmaxnreg_inc<C::REG_SOFTMAX>();
     const int t = warp / 4, wq = warp % 4, r = wq * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const uint32_t tS = lane_addr + C::S_COL(t), tP = lane_addr + C::P_COL(t), tO = lane_addr + C::O_COL(t);
+    const uint32_t tS = lane_addr + C::S_COL(t), tO = lane_addr + C::O_COL(t);
     uint8_t* q_smem = smem + C::OFF_Q + t * C::TILE_BYTES;
     // A warp moves its 32 rows 16 bytes a lane, RPP rows at a time.
     constexpr int CH = D / 8, RPP = 32 / CH;
     const int my_chunk = lane % CH, my_row = wq * 32 + lane / CH;
     auto place = [&](int row, int ch) { return q_smem + row * (2 * D) + ((ch ^ (row & 7)) << 4); };  // (within the warp's own rows)
-    int np = 0, no = 0, n_raw = 0;  // tiles, O waited for (a tile or an item), rows of Q so far
+    int np = 0, no = 0, n_raw = 0;  // tiles and items of this row tile so far; of the warp's rows of Q
     int tile0 = 0;       // tiles of the items before
     bool ok = true;
     auto wait = [&](int i, int phase) {
@@ -799,11 +745,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           tmem_wait_ld();
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) reg_fence(s[ch]);
-          if (C::OWN_P) {
-            tc_fence_before();
-            mbar_arrive(bar(C::B_SREAD + t));
-          }
-          bool p_free = !C::OWN_P || j == 0;  // P V of the tile before has read P (else: S of this one is behind it)
           const int kv0 = (it.k0 + j) * kKeys;
           if (all_see - kv0 < kKeys) {
             const int end = sees - kv0;
@@ -850,12 +791,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
                 ls2[e & 3] = fadd2(ls2[e & 3], f2_pack(p0, p1));
                 pk[e] = pack_bf16x2(p0, p1);
               }
-              if (C::OWN_P && ch == 0 && !p_free) {
-                wait(C::B_ODONE + t, no++);
-                tc_fence_after();
-                p_free = true;
-              }
-              tmem_st16(tP + ch * 16, pk);
+              tmem_st16(tS + ch * 16, pk);
             }
             float ls[8];
 #pragma unroll
