@@ -55,6 +55,23 @@ __device__ __forceinline__ void unit_chunks(int u, int pairs, int& c0, int& c1) 
   c1 = halves ? u + pairs / 8 : 2 * u + 1;
 }
 
+// Where the angle of a token's pair lies in shared memory: two pairs of each unit beside
+// the same two of the next, so that the units' 16-byte reads meet in no bank.  (A unit's
+// eight one after another: four-way conflicts, which held the queries' turn at 57 us
+// for 380 MB.)
+__device__ __forceinline__ int angle_at(int t, int j, int pairs) {
+  return ((t * 4 + ((j >> 1) & 3)) * (pairs / 8) + (j >> 3)) * 2 + (j & 1);
+}
+// The eight of unit u.
+__device__ __forceinline__ void load_angles(const float2* cs, int t, int u, int pairs, float2 (&c)[8]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float4 v = reinterpret_cast<const float4*>(cs)[(t * 4 + e) * (pairs / 8) + u];
+    c[2 * e] = make_float2(v.x, v.y);
+    c[2 * e + 1] = make_float2(v.z, v.w);
+  }
+}
+
 __device__ __forceinline__ void unpack8(const uint4& x, float* v) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -82,11 +99,13 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
-// Rows [tok0, tok0 + n) of one or two tensors, turned by the angles cs[token][pair].
-// A thread keeps its unit of the head and goes through the heads of one token after
+// Rows [tok0, tok0 + n) of one or two tensors, turned by the angles cs[token][pair],
+// which `angles` forms (for the whole block) while the first rows are on their way.  A
+// thread keeps its unit of the head and goes through the heads of one token after
 // another, two units in flight.
-template <int D, bool IL, int NT>
-__device__ __forceinline__ void turn_rows(const TurnRows& x, int tok0, int n, const float2* cs, int pairs) {
+template <int D, bool IL, int NT, typename Angles>
+__device__ __forceinline__ void turn_rows(const TurnRows& x, int tok0, int n, const float2* cs, int pairs,
+                                          Angles angles) {
   constexpr int U = D / 16, SWEEP = NT / U;
   const int u = threadIdx.x % U, heads = x.heads0 + x.heads1;
   const bool turned = 8 * u < pairs;
@@ -123,8 +142,7 @@ __device__ __forceinline__ void turn_rows(const TurnRows& x, int tok0, int n, co
     if (turned) {
       float2 c[8];
       float y[16];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = cs[w.tok * pairs + 8 * u + e];
+      load_angles(cs, w.tok, u, pairs, c);
       turn_unit<IL>(a, b, c, y);
       a = pack8(y);
       b = pack8(y + 8);
@@ -134,10 +152,13 @@ __device__ __forceinline__ void turn_rows(const TurnRows& x, int tok0, int n, co
   };
   settle();
   Unit w0, w1;
-  while (load(w0)) {
-    const bool more = load(w1);
+  bool one = load(w0), two = load(w1);
+  angles();
+  while (one) {
     finish(w0);
-    if (more) finish(w1);
+    if (two) finish(w1);
+    one = load(w0);
+    two = load(w1);
   }
 }
 
@@ -148,45 +169,49 @@ constexpr int kTurnThreads = 256, kTurnTokens = 4;  // a block's tokens: one ang
 
 template <int D, bool IL>
 __global__ void __launch_bounds__(kTurnThreads) fa_rotary_kernel(const RotaryParams r, const TurnRows x, int total) {
-  __shared__ float2 cs[kTurnTokens * (D / 2)];
+  __shared__ __align__(16) float2 cs[kTurnTokens * (D / 2)];
   grid_dependency_wait();  // scheduled while the kernel before it in the stream finishes
   const int tok0 = blockIdx.x * kTurnTokens;
   const int n = min(kTurnTokens, total - tok0);
-  for (int i = threadIdx.x; i < n * r.pairs; i += kTurnThreads) {
-    const int t = i / r.pairs, j = i - t * r.pairs;
-    cs[i] = cos_sin(r, j, position_of(r, j, tok0 + t, total));
-  }
-  __syncthreads();
-  turn_rows<D, IL, kTurnThreads>(x, tok0, n, cs, r.pairs);
+  turn_rows<D, IL, kTurnThreads>(x, tok0, n, cs, r.pairs, [&]() {
+    for (int i = threadIdx.x; i < n * r.pairs; i += kTurnThreads) {
+      const int t = i / r.pairs, j = i - t * r.pairs;
+      cs[angle_at(t, j, r.pairs)] = cos_sin(r, j, position_of(r, j, tok0 + t, total));
+    }
+    __syncthreads();
+  });
 }
 
 // ----------------------------------------------------------------------------
 // Append to the cache
 // ----------------------------------------------------------------------------
-// The first blocks take a page's new tokens and up to HG heads of K or of V; the
-// others turn the queries.  A thread owns one or two units (token, two chunks) of
-// the page in every head of its block, so a unit's eight sines and cosines are
-// formed once; the input stays in registers between the largest magnitude and the
-// rounding.  Keys are turned in 32 bits and rounded once, to their codes.
+// The first blocks take a page's new tokens in some heads of K or of V, a group of
+// threads (a warp up to 64 units) each (page, head); the others turn the queries.  A
+// thread owns NU units, which stay in registers between the largest magnitude and the
+// rounding and are on their way while the block's groups form the angles together.
+// Keys are turned in 32 bits and rounded once, to their codes; values go the way of
+// the plain store.
 template <int D, int BLOCK>
 struct AppendCfg {
   static constexpr int U = D / 16, UNITS = BLOCK * U;
-  static constexpr int NT = UNITS < 128 ? 128 : UNITS > 512 ? 512 : UNITS;
-  static constexpr int NU = UNITS <= NT ? 1 : UNITS / NT;
-  static constexpr int HG = 4 / NU;        // heads of a block
-  static constexpr int TOKENS = NT / 64;   // queries' tokens of a block
+  static constexpr int NU = UNITS < 128 ? UNITS / 32 : 4;  // units of a thread
+  static constexpr int TG = UNITS / NU;                    // threads of a group
+  static constexpr int NT = 256;
+  static constexpr int HEADS = NT / TG;                    // heads of a block
+  static constexpr int TOKENS = NT / 64;                   // queries' tokens of a block
+  static constexpr int SMEM = (BLOCK > TOKENS ? BLOCK : TOKENS) * (D / 2) * 8;
 };
 
 template <int D, int BLOCK, bool IL>
-__global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT) fa_cache8_append_kernel(const Cache8StoreParams p,
-                                                                                   const RotaryParams r,
-                                                                                   const TurnRows x, int store_blocks,
-                                                                                   int zero_tail) {
+__global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT, 4)
+    fa_cache8_append_kernel(const Cache8StoreParams p, const RotaryParams r, const TurnRows x, int store_blocks,
+                            int zero_tail) {
   using C = AppendCfg<D, BLOCK>;
-  constexpr int NT = C::NT, NU = C::NU, HG = C::HG, U = C::U;
-  __shared__ float2 cs[C::TOKENS * (D / 2)];
-  __shared__ int where[C::TOKENS];
-  __shared__ uint32_t warp_max[HG][NT / 32];
+  constexpr int NT = C::NT, NU = C::NU, TG = C::TG, U = C::U, WG = TG / 32;
+  static_assert(TG % 32 == 0 && TG <= NT, "a warp is of one group");
+  extern __shared__ __align__(16) float2 cs[];  // cosine, sine (angle_at)
+  __shared__ int place[C::TOKENS];
+  __shared__ uint32_t warp_max[NT / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();  // scheduled while the kernel before it in the stream finishes
   if (static_cast<int>(blockIdx.x) >= store_blocks) {
@@ -194,25 +219,26 @@ __global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT) fa_cache8_append_kern
     const int end = min(max(p.cu_seqlens[p.B], 0), p.total);
     const int tok0 = (static_cast<int>(blockIdx.x) - store_blocks) * C::TOKENS;
     const int n = min(C::TOKENS, end - tok0);  // of them before the end of the last sequence
-    if (!r.positions && static_cast<int>(threadIdx.x) < n) {
-      // the token's sequence: the last one that begins at or before it
-      const int row = tok0 + threadIdx.x;
-      int lo = 0, hi = p.B - 1;
-      while (lo < hi) {
-        const int mid = lo + (hi - lo + 1) / 2;
-        if (p.cu_seqlens[mid] <= row) lo = mid;
-        else hi = mid - 1;
+    turn_rows<D, IL, NT>(x, tok0, n, cs, r.pairs, [&]() {
+      if (!r.positions) {  // a token's place: that of its row behind its sequence's first
+        if (threadIdx.x < C::TOKENS) place[threadIdx.x] = 0;
+        __syncthreads();
+        for (int b = threadIdx.x; b < p.B; b += NT) {
+          const int first = p.cu_seqlens[b], behind = p.cu_seqlens[b + 1], start = p.start[b];
+#pragma unroll
+          for (int t = 0; t < C::TOKENS; ++t)
+            if (first <= tok0 + t && tok0 + t < behind)
+              place[t] = static_cast<int>(static_cast<uint32_t>(start) + static_cast<uint32_t>(tok0 + t) -
+                                          static_cast<uint32_t>(first));
+        }
+        __syncthreads();
       }
-      where[threadIdx.x] = static_cast<int>(static_cast<uint32_t>(p.start[lo]) + static_cast<uint32_t>(row) -
-                                            static_cast<uint32_t>(p.cu_seqlens[lo]));
-    }
-    if (!r.positions) __syncthreads();
-    for (int i = threadIdx.x; i < n * r.pairs; i += NT) {
-      const int t = i / r.pairs, j = i - t * r.pairs;
-      cs[i] = cos_sin(r, j, r.positions ? position_of(r, j, tok0 + t, p.total) : where[t]);
-    }
-    __syncthreads();
-    turn_rows<D, IL, NT>(x, tok0, n, cs, r.pairs);
+      for (int i = threadIdx.x; i < n * r.pairs; i += NT) {
+        const int t = i / r.pairs, j = i - t * r.pairs;
+        cs[angle_at(t, j, r.pairs)] = cos_sin(r, j, r.positions ? position_of(r, j, tok0 + t, p.total) : place[t]);
+      }
+      __syncthreads();
+    });
     if (zero_tail) {
       for (int t = max(n, 0); t < C::TOKENS && tok0 + t < p.total; ++t) {
         uint4* row = reinterpret_cast<uint4*>(x.dst0 + static_cast<long long>(tok0 + t) * x.heads0 * D);
@@ -222,10 +248,12 @@ __global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT) fa_cache8_append_kern
     return;
   }
   // ---- keys or values of one page
-  const int groups = (p.Hk + HG - 1) / HG;
+  const int groups = (p.Hk + C::HEADS - 1) / C::HEADS;
   const int id = blockIdx.x, at = id / (2 * groups), g = id - at * 2 * groups;
   const bool is_v = g >= groups;
-  const int h0 = (is_v ? g - groups : g) * HG, heads = min(HG, p.Hk - h0);
+  const int group = threadIdx.x / TG, tid = threadIdx.x % TG;
+  const int head = (is_v ? g - groups : g) * C::HEADS + group;
+  const bool has_head = head < p.Hk;
   const int b = at / p.blocks, nth = at - b * p.blocks;
   const int first = min(max(p.cu_seqlens[b], 0), p.total);
   const int count = min(max(p.cu_seqlens[b + 1], first), p.total) - first;
@@ -242,7 +270,7 @@ __global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT) fa_cache8_append_kern
   const int hi = static_cast<int>(min(end - base, static_cast<long long>(BLOCK)));
   const int src = first + static_cast<int>(base - start);  // input row of slot 0
   const long long ld = is_v ? p.ldv : p.ldk;
-  const int u = threadIdx.x % U;
+  const int u = tid % U;
   int c0, c1;
   if (is_v) c0 = 2 * u, c1 = 2 * u + 1;
   else unit_chunks<IL>(u, r.pairs, c0, c1);
@@ -251,106 +279,116 @@ __global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT) fa_cache8_append_kern
   bool fresh[NU];
 #pragma unroll
   for (int n = 0; n < NU; ++n) {
-    tok[n] = (threadIdx.x + n * NT) / U;
+    tok[n] = (tid + n * TG) / U;
     fresh[n] = tok[n] >= old && tok[n] < hi;
   }
-  uint4 raw[HG][NU][2];
+  uint4 raw[NU][2];
+  const uint16_t* in = (is_v ? p.v : p.k) + static_cast<long long>(src) * ld + head * D;
 #pragma unroll
-  for (int h = 0; h < HG; ++h)
-#pragma unroll
-    for (int n = 0; n < NU; ++n) {
-      raw[h][n][0] = raw[h][n][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (fresh[n] && h < heads) {
-        const uint16_t* row = (is_v ? p.v : p.k) + (static_cast<long long>(src) + tok[n]) * ld + (h0 + h) * D;
-        raw[h][n][0] = *reinterpret_cast<const uint4*>(row + 8 * c0);
-        raw[h][n][1] = *reinterpret_cast<const uint4*>(row + 8 * c1);
-      }
+  for (int n = 0; n < NU; ++n) {
+    raw[n][0] = raw[n][1] = make_uint4(0u, 0u, 0u, 0u);
+    fresh[n] &= has_head;
+    if (fresh[n]) {
+      raw[n][0] = *reinterpret_cast<const uint4*>(in + tok[n] * ld + 8 * c0);
+      raw[n][1] = *reinterpret_cast<const uint4*>(in + tok[n] * ld + 8 * c1);
     }
+  }
+  if (!is_v) {
+    for (int i = threadIdx.x; i < (hi - old) * r.pairs; i += NT) {
+      const int t = i / r.pairs, j = i - t * r.pairs;
+      cs[angle_at(old + t, j, r.pairs)] =
+          cos_sin(r, j, r.positions ? position_of(r, j, src + old + t, p.total) : static_cast<int>(base + old + t));
+    }
+    __syncthreads();
+  }
   const bool live = page >= 0 && page < p.num_blocks;
   if (!live) {
     if (threadIdx.x == 0) atomicOr(p.err, kDevErrPage);
     return;
   }
-  float2 angle[NU][8];
-#pragma unroll
-  for (int n = 0; n < NU; ++n)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      angle[n][e] = make_float2(1.f, 0.f);
-      if (turned && fresh[n]) {
-        const int j = 8 * u + e;
-        angle[n][e] = cos_sin(r, j, r.positions ? position_of(r, j, src + tok[n], p.total)
-                                                : static_cast<int>(base + tok[n]));
-      }
-    }
-  const size_t ph = static_cast<size_t>(page) * p.Hk + h0;
+  const size_t ph = static_cast<size_t>(page) * p.Hk + (has_head ? head : 0);
   float* scale = (is_v ? p.v_scale : p.k_scale) + ph;
-  auto values = [&](int h, int n, float (&y)[16]) {
-    if (turned) {
-      turn_unit<IL>(raw[h][n][0], raw[h][n][1], angle[n], y);
+  const float held = old > 0 ? *scale : 0.f;
+  auto values = [&](int n, float (&y)[16]) {
+    if (turned && fresh[n]) {
+      float2 c[8];
+      load_angles(cs, tok[n], u, r.pairs, c);
+      turn_unit<IL>(raw[n][0], raw[n][1], c, y);
     } else {
-      unpack8(raw[h][n][0], y);
-      unpack8(raw[h][n][1], y + 8);
+      unpack8(raw[n][0], y);
+      unpack8(raw[n][1], y + 8);
     }
   };
-  float held[HG];
-#pragma unroll
-  for (int h = 0; h < HG; ++h) {
-    held[h] = old > 0 && h < heads ? scale[h] : 0.f;
-    // Infinities and NaN do not set the scale: the maximum passes over NaN; where it
-    // is infinite, once more without.
-    auto largest = [&](bool finite) {
-      float top = 0.f;
+  // The largest magnitude, as fp32 bits.  Infinities and NaN do not set the scale: the
+  // maximum passes over NaN; where it is infinite, once more without.
+  auto largest = [&](bool finite) -> uint32_t {
+    if (is_v) {
+      uint32_t top = 0;
 #pragma unroll
       for (int n = 0; n < NU; ++n) {
-        float y[16];
-        values(h, n, y);
+        const uint32_t w[8] = {raw[n][0].x, raw[n][0].y, raw[n][0].z, raw[n][0].w,
+                               raw[n][1].x, raw[n][1].y, raw[n][1].z, raw[n][1].w};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = fabsf(y[i]);
-          top = fmaxf(top, finite && !(a < CUDART_INF_F) ? 0.f : a);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t m = w[i] & 0x7fff7fffu;
+          top = max_bf16x2(top, finite ? m & ~__vcmpgeu2(m, 0x7f807f80u) : m);
         }
       }
-      return top;
-    };
-    float top = largest(false);
-    if (top == CUDART_INF_F) top = largest(true);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-    if (lane == 0) warp_max[h][warp] = m;
-  }
-  __syncthreads();  // (every thread has read the scales held before one of them writes the new ones)
-#pragma unroll
-  for (int h = 0; h < HG; ++h) {
-    if (h >= heads) break;
-    const uint32_t amax = __reduce_max_sync(0xffffffffu, lane < NT / 32 ? warp_max[h][lane] : 0u);
-    const float s = fmaxf(exp2_int(scale_exponent_f32(amax, kScaleFloor)), held[h]);
-    const float inv = exp2_int(127 - static_cast<int>((__float_as_uint(s) >> 23) & 255u));  // 1 / s, a power of two
-    const bool again = s > held[h];
-    if (threadIdx.x == 0 && again) scale[h] = s;
-    uint8_t* out = (is_v ? p.v_codes : p.k_codes) + (ph + h) * (BLOCK * D);
+      return max(top & 0xffffu, top >> 16) << 16;
+    }
+    float top = 0.f;
 #pragma unroll
     for (int n = 0; n < NU; ++n) {
-      uint2* a = reinterpret_cast<uint2*>(out + tok[n] * D + 8 * c0);
-      uint2* z = reinterpret_cast<uint2*>(out + tok[n] * D + 8 * c1);
-      if (fresh[n]) {
-        float y[16];
-        values(h, n, y);
+      float y[16];
+      values(n, y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] *= inv;
-        *a = make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
-        *z = make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11]), pack_e4m3x4(y[12], y[13], y[14], y[15]));
-      } else if (tok[n] < old && again) {
-        // tokens held at a smaller scale are rounded again
-        const float f = held[h] * inv;
-        const uint2 code[2] = {*a, *z};
+      for (int i = 0; i < 16; ++i) {
+        const float a = fabsf(y[i]);
+        top = fmaxf(top, finite && !(a < CUDART_INF_F) ? 0.f : a);
+      }
+    }
+    return __float_as_uint(top);
+  };
+  uint32_t amax = largest(false);
+  if (amax >= 0x7f800000u) amax = largest(true);
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if (TG > 32) {  // (and every thread has read the scale held before one of them writes the new one)
+    if (lane == 0) warp_max[warp] = amax;
+    __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float v[4], w[4];
-          unpack_e4m3x4(code[k].x, v);
-          unpack_e4m3x4(code[k].y, w);
-          *(k ? z : a) = make_uint2(pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
-                                    pack_e4m3x4(w[0] * f, w[1] * f, w[2] * f, w[3] * f));
-        }
+    for (int w = 0; w < WG; ++w) amax = max(amax, warp_max[group * WG + w]);
+  } else {
+    __syncwarp();
+  }
+  if (!has_head) return;
+  const float s = fmaxf(exp2_int(scale_exponent_f32(amax, kScaleFloor)), held);
+  const float inv = exp2_int(127 - static_cast<int>((__float_as_uint(s) >> 23) & 255u));  // 1 / s, a power of two
+  const uint64_t inv2 = f2_pack(inv, inv);
+  const bool again = s > held;
+  if (tid == 0 && again) *scale = s;
+  uint8_t* out = (is_v ? p.v_codes : p.k_codes) + ph * (BLOCK * D);
+#pragma unroll
+  for (int n = 0; n < NU; ++n) {
+    uint2* a = reinterpret_cast<uint2*>(out + tok[n] * D + 8 * c0);
+    uint2* z = reinterpret_cast<uint2*>(out + tok[n] * D + 8 * c1);
+    if (fresh[n]) {
+      float y[16];
+      values(n, y);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) f2_unpack(fmul2(f2_pack(y[i], y[i + 1]), inv2), y[i], y[i + 1]);
+      *a = make_uint2(pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
+      *z = make_uint2(pack_e4m3x4(y[8], y[9], y[10], y[11]), pack_e4m3x4(y[12], y[13], y[14], y[15]));
+    } else if (tok[n] < old && again) {
+      // tokens held at a smaller scale are rounded again
+      const float f = held * inv;
+      const uint2 code[2] = {*a, *z};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float v[4], w[4];
+        unpack_e4m3x4(code[k].x, v);
+        unpack_e4m3x4(code[k].y, w);
+        *(k ? z : a) = make_uint2(pack_e4m3x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f),
+                                  pack_e4m3x4(w[0] * f, w[1] * f, w[2] * f, w[3] * f));
       }
     }
   }
@@ -360,11 +398,14 @@ template <int D, int BLOCK, bool IL>
 cudaError_t launch_append(const Cache8StoreParams& p, const RotaryParams& r, const TurnRows& x, int zero_tail,
                           cudaStream_t s) {
   using C = AppendCfg<D, BLOCK>;
-  const long long groups = (p.Hk + C::HG - 1) / C::HG;
+  static SmemLimit smem_limit;
+  const cudaError_t e = smem_limit.ensure(reinterpret_cast<const void*>(fa_cache8_append_kernel<D, BLOCK, IL>), C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long groups = (p.Hk + C::HEADS - 1) / C::HEADS;
   const long long store = static_cast<long long>(p.B) * p.blocks * 2 * groups;
   const long long turn = (p.total + C::TOKENS - 1) / C::TOKENS;
   if (store + turn > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return launch_kernel(fa_cache8_append_kernel<D, BLOCK, IL>, dim3(static_cast<unsigned>(store + turn)), dim3(C::NT), 0, s,
+  return launch_kernel(fa_cache8_append_kernel<D, BLOCK, IL>, dim3(static_cast<unsigned>(store + turn)), dim3(C::NT), C::SMEM, s,
                        true, p, r, x, static_cast<int>(store), zero_tail);
 }
 
