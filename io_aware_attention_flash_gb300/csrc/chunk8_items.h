@@ -7,6 +7,9 @@
 // kRows of them over one key/value head; its tiles are the runs of kKeys keys that
 // its last row sees, at least one.  The items in the order (sequence, row block,
 // key/value head), tile after tile, are cut into runs of equal cost, one a CTA.
+//
+// A CTA takes rows as two halves.  Where an item has rows for one half only, both take
+// the same rows and every other tile each (`dual`).
 #pragma once
 
 #ifdef __CUDACC__
@@ -38,17 +41,38 @@ FA_CHUNK_FN int row_tiles(int len, int n, int G, int first, int count, bool caus
   return tiles(visible(len, n, last / G, causal));
 }
 
-// A run is counted in units: one for each tile, and `extra` before an item's first,
-// as many as its fixed cost is tiles' time (kItemCost; less where a CTA has fewer tiles
-// than that: with little work every tile had better have a CTA of its own).
-constexpr int kItemCost = 3;
-FA_CHUNK_FN int extra_units(long long all_tiles, long long ctas) {
-  return all_tiles / ctas <= kItemCost ? static_cast<int>(all_tiles / ctas) - 1 : kItemCost;
+// Rows of row block rb fit in one half.
+FA_CHUNK_FN bool dual(int n, int G, int rb) { return n * G - rb * kRows <= kHalf; }
+
+// Runs are counted in units: two for a tile of a dual item, three for another's (its
+// halves' products, of which a dual item's tile is one), and `extra` before an item's
+// first, as many as its fixed cost is (kItemCost; less where a CTA has little more than
+// a tile: every one had better have a CTA of its own).  Measured: a tile takes 1.2 us of
+// a dual item, 1.9 of another; an item 6.
+constexpr int kMostUnits = 3, kItemCost = 10;
+FA_CHUNK_FN int tile_units(bool dual) { return dual ? 2 : kMostUnits; }
+// CTAs that have a run each, of `most`: a run has as many units as a tile and more, so
+// that a tile begins in every run between an item's first and last.  all: the units of
+// all tiles.
+FA_CHUNK_FN int runs(long long all, int most) {
+  const long long r = all / kMostUnits;
+  return r >= most ? most : r > 0 ? static_cast<int>(r) : all > 0;
+}
+// Units before an item's first.
+FA_CHUNK_FN int extra_units(long long all, int ctas) {
+  const long long each = all / ctas - kMostUnits;
+  return each < 0 ? 0 : each < kItemCost ? static_cast<int>(each) : kItemCost;
 }
 // Run c of `ctas` over `total` units begins at run_start(c); unit u lies in run run_of(u).
+// A tile is in the run that has its first unit.
 FA_CHUNK_FN long long run_start(long long c, long long total, long long ctas) { return c * total / ctas; }
 FA_CHUNK_FN int run_of(long long u, long long total, long long ctas) {
   return static_cast<int>(((u + 1) * ctas + total - 1) / total - 1);
+}
+// Tiles of an item that begin before `units` units from its first one's.
+FA_CHUNK_FN int tiles_before(long long units, int per_tile, int tiles) {
+  const long long t = units <= 0 ? 0 : (units + per_tile - 1) / per_tile;
+  return t < tiles ? static_cast<int>(t) : tiles;
 }
 
 }  // namespace chunk8

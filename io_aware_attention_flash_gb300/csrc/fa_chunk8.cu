@@ -55,7 +55,10 @@ struct ChunkCfg {
   static constexpr int NK = D == 128 ? 3 : 6;           // ring of K's codes
   static constexpr int NC = NK;                         // ring of V's codes
   static constexpr int NV = D == 128 ? 2 : 3;           // ring of V in bf16
-  static constexpr int NSC = NK + 1;                    // ring of K's scales
+  // Ring of K's scales.  A slot is written again once the S of NK tiles before has been
+  // formed.  By then P of three tiles further back is there (of a dual item, whose halves
+  // take turns; else of one), and with it the scales have been read.
+  static constexpr int NSC = NK + 3;
   static constexpr int NI = 4;                          // published items
   static constexpr int MAX_PPT = kKeys / 16;            // pages of a tile, at most
   static constexpr int OFF_Q = 0;                       // two row tiles: of each 8 rows the first terms, then the second
@@ -83,12 +86,13 @@ struct ChunkCfg {
   static constexpr int B_ODONE = B_PFULL + 2;
   static constexpr int B_DRAIN = B_ODONE + 2;
   static constexpr int B_RAW = B_DRAIN + 1;             // [8]: a softmax warp's rows of Q have landed
-  static constexpr int NBAR = B_RAW + 8;
+  static constexpr int B_JOIN = B_RAW + 8;              // a dual item's second half is there, and has been read
+  static constexpr int NBAR = B_JOIN + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // slack to align the base to 1024
-  static constexpr int COPY_WARP = 8, MMA_WARP = 12, CONVERT_WARPS = 6;
+  static constexpr int COPY_WARP = 15, MMA_WARP = 12, CONVERT_WARPS = 5;
   static constexpr int NUM_THREADS = 512;
-  static constexpr int READERS = 15;                    // warps that take an item: all but the copying one
+  static constexpr int READERS = 14;                    // warps that take an item: all but the copying one
   // Registers a thread after the split; launched with 128.
   static constexpr int REG_SOFTMAX = 192, REG_OTHER = 64;
   static_assert(2 * REG_SOFTMAX + 2 * REG_OTHER == 4 * 128, "the split takes what the launch gives");
@@ -100,15 +104,37 @@ struct ChunkCfg {
   static_assert(OFF_ITEM % 16 == 0 && OFF_KS % 16 == 0 && OFF_SCAN % 8 == 0, "vector accesses");
 };
 
+// Tiles from one that is copied to the one that is brought to L2.
+constexpr int kAhead = 6;
+
 // What the roles know of an item.
 struct Item {
   int b, hk, rb, k0, tiles, n, len, tok0, cnt0, cnt1, slot;  // slot: of the partial, -1: the item is whole
+  bool dual;
+};
+
+// A place in a ring of N slots that is gone through in order, and its phase there.
+template <int N>
+struct Ring {
+  int i = 0, phase = 0;
+  __device__ __forceinline__ void step(int n = 1) {  // n <= N
+    i += n;
+    if (i >= N) {
+      i -= N;
+      phase ^= 1;
+    }
+  }
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
+}
+
+// Has a stretch of global memory brought to L2.
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 // New tokens and cached tokens of sequence b, within what the buffers hold.
@@ -181,6 +207,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       mbar_init(bar(C::B_SFULL + t), 1);
       mbar_init(bar(C::B_PFULL + t), 128);
       mbar_init(bar(C::B_ODONE + t), 1);
+      mbar_init(bar(C::B_JOIN + t), 128);
     }
     mbar_init(bar(C::B_DRAIN), 1);
     for (int i = 0; i < 8; ++i) mbar_init(bar(C::B_RAW + i), 1);
@@ -207,11 +234,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
   // counted, then the pair that holds the run's first unit
   const int pairs = p.B * p.row_blocks;
   long long* scan = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
-  auto pair_tiles = [&](int x) -> int {
+  auto pair_tiles = [&](int x, int& tiles) -> int {  // units of a tile
     const int b = x / p.row_blocks, rb = x - b * p.row_blocks;
     int tok0, n, len;
     chunk_seq(p, b, tok0, n, len);
-    return chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
+    tiles = chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
+    return chunk8::tile_units(chunk8::dual(n, p.G, rb));
   };
   auto warp_scan = [&](long long v) {  // inclusive
 #pragma unroll
@@ -221,36 +249,47 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     }
     return v;
   };
-  int one = 0;  // tiles of pair tid, if one pass takes all pairs
-  long long tiles_sum = 0, items_sum = 0;
+  int one = 0;  // units of pair tid's tiles, if one pass takes all pairs
+  long long units_sum = 0, items_sum = 0;
   for (int x = tid; x < pairs; x += C::NUM_THREADS) {
-    one = pair_tiles(x);
-    tiles_sum += one;
+    int tiles;
+    const int w = pair_tiles(x, tiles);
+    one = w * tiles;
+    units_sum += one;
     items_sum += one > 0;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    tiles_sum += __shfl_xor_sync(0xffffffffu, tiles_sum, off);
+    units_sum += __shfl_xor_sync(0xffffffffu, units_sum, off);
     items_sum += __shfl_xor_sync(0xffffffffu, items_sum, off);
   }
-  if (lane == 0) scan[warp] = tiles_sum, scan[16 + warp] = items_sum;
+  if (lane == 0) scan[warp] = units_sum, scan[16 + warp] = items_sum;
   __syncthreads();
-  tiles_sum = items_sum = 0;
+  units_sum = items_sum = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) tiles_sum += scan[i], items_sum += scan[16 + i];
-  tiles_sum *= p.Hk, items_sum *= p.Hk;
-  const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), tiles_sum));
+  for (int i = 0; i < 16; ++i) units_sum += scan[i], items_sum += scan[16 + i];
+  units_sum *= p.Hk, items_sum *= p.Hk;
+  const int ctas = chunk8::runs(units_sum, static_cast<int>(gridDim.x));
   if (tid == 0) p.merge[blockIdx.x * 8] = -1;
   if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const int extra = chunk8::extra_units(tiles_sum, ctas);
-  const long long total = tiles_sum + extra * items_sum;
-  auto pair_units = [&](int tiles) -> long long { return tiles > 0 ? static_cast<long long>(p.Hk) * (tiles + extra) : 0; };
+  const int extra = chunk8::extra_units(units_sum, ctas);
+  const long long total = units_sum + extra * items_sum;
+  auto pair_units = [&](int tile_units) -> long long {
+    return tile_units > 0 ? static_cast<long long>(p.Hk) * (tile_units + extra) : 0;
+  };
   const long long u_lo = chunk8::run_start(blockIdx.x, total, ctas), u_hi = chunk8::run_start(blockIdx.x + 1LL, total, ctas);
   long long* found = scan + 32;  // first unit of the pair; the pair
   {
     long long base = 0;
     for (int x0 = 0; x0 < pairs && base <= u_lo; x0 += C::NUM_THREADS) {
-      if (pairs > C::NUM_THREADS) one = x0 + tid < pairs ? pair_tiles(x0 + tid) : 0;
+      if (pairs > C::NUM_THREADS) {
+        one = 0;
+        if (x0 + tid < pairs) {
+          int tiles;
+          one = pair_tiles(x0 + tid, tiles);
+          one *= tiles;
+        }
+      }
       const long long w = pair_units(one);
       long long sum = warp_scan(w);
       __syncthreads();  // (the sums before have been read)
@@ -297,7 +336,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     const int4 a = src[0], b = src[1], c = src[2];
     it.b = a.x, it.hk = a.y, it.rb = a.z, it.k0 = a.w;
     it.tiles = b.x, it.n = b.y, it.len = b.z, it.tok0 = b.w;
-    it.cnt0 = c.x, it.cnt1 = c.y, it.slot = c.z;
+    it.cnt0 = c.x, it.cnt1 = c.y, it.slot = c.z, it.dual = c.w != 0;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(C::B_IEMPTY + s));
     ++items;
@@ -311,14 +350,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       const int ppt = kKeys >> p.block_shift, page_bytes = D << p.block_shift;
       struct Unit {
         int b, hk, rb, k0, k1, nt, n, len, tok0;  // the item (tiles k0 .. k1 of nt)
+        bool dual;
         int kt, tiles;                            // first tile of the unit, and how many
-        long long last;                           // the item's last unit
+        long long last;                           // the first unit of the item's last tile
         int page;                                 // this lane's page (of 32 / ppt tiles), -1: none
         float ks, vs;
       };
       int x = static_cast<int>(found[1]);
       long long x_start = found[0], at = u_lo;  // first unit of the pair; the next unit
-      int nt = 0, n = 0, len = 0, tok0 = 0, b = 0, rb = 0;
+      int nt = 0, w = 0, n = 0, len = 0, tok0 = 0, b = 0, rb = 0;  // (w: units of a tile)
       auto load_pair = [&]() {
         b = x / p.row_blocks;
         rb = x - b * p.row_blocks;
@@ -326,29 +366,32 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         n = __shfl_sync(0xffffffffu, n, 0);  // the warp stays together even if a caller changes the lengths meanwhile
         len = __shfl_sync(0xffffffffu, len, 0);
         nt = chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
+        w = chunk8::tile_units(chunk8::dual(n, p.G, rb));
       };
       load_pair();
       auto next_unit = [&](Unit& u) {
         u.tiles = 0;
         while (u.tiles <= 0) {
           if (at >= u_hi) return;
-          while (at >= x_start + pair_units(nt)) {
-            x_start += pair_units(nt);
+          while (at >= x_start + pair_units(nt * w)) {
+            x_start += pair_units(nt * w);
             if (++x >= pairs) {
               at = u_hi;
               return;
             }
             load_pair();
           }
-          const int hk = static_cast<int>((at - x_start) / (nt + extra));
-          const long long item = x_start + static_cast<long long>(hk) * (nt + extra), first = item + extra;
-          u.b = b, u.rb = rb, u.n = n, u.len = len, u.tok0 = tok0, u.nt = nt, u.hk = hk;
-          u.kt = static_cast<int>(max(at - first, 0LL));
-          u.k0 = static_cast<int>(max(u_lo - first, 0LL));
-          u.k1 = static_cast<int>(min(u_hi - first, static_cast<long long>(nt)));
-          u.tiles = min(u.k1 - u.kt, 32 / ppt);  // (none: the run ends before the item's first tile)
-          u.last = first + nt - 1;
-          at = u.tiles > 0 ? first + u.kt + u.tiles : u_hi;
+          const int units = nt * w + extra;  // of an item
+          const int hk = static_cast<int>((at - x_start) / units);
+          const long long first = x_start + static_cast<long long>(hk) * units + extra;
+          u.b = b, u.rb = rb, u.n = n, u.len = len, u.tok0 = tok0, u.nt = nt, u.hk = hk, u.dual = chunk8::dual(n, p.G, rb);
+          u.kt = chunk8::tiles_before(at - first, w, nt);
+          u.k0 = chunk8::tiles_before(u_lo - first, w, nt);
+          u.k1 = chunk8::tiles_before(u_hi - first, w, nt);
+          u.tiles = min(u.k1 - u.kt, 32 / ppt);
+          u.last = first + static_cast<long long>(nt - 1) * w;
+          // (no tile of it begins in what is left of the run: on to the next item, or the end)
+          at = u.tiles > 0 ? first + static_cast<long long>(u.kt + u.tiles) * w : first + static_cast<long long>(nt) * w;
         }
         u.page = -1;
         if (lane < u.tiles * ppt && u.kt * ppt + lane < cache8::pages_of(len, p.block_shift))
@@ -383,8 +426,13 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             const bool whole = u.k0 == 0 && u.k1 == u.nt;
             if (!whole) slot = 2 * blockIdx.x + (u.k0 == 0 ? 1 : 0);
             const int first = u.rb * kRows;
-            cnt0 = max(min(u.k1, chunk8::row_tiles(u.len, u.n, p.G, first, kHalf, p.causal)) - u.k0, 0);
-            cnt1 = max(min(u.k1, chunk8::row_tiles(u.len, u.n, p.G, first + kHalf, kHalf, p.causal)) - u.k0, 0);
+            if (u.dual) {
+              cnt0 = (u.k1 - u.k0 + 1) / 2;
+              cnt1 = (u.k1 - u.k0) / 2;
+            } else {
+              cnt0 = max(min(u.k1, chunk8::row_tiles(u.len, u.n, p.G, first, kHalf, p.causal)) - u.k0, 0);
+              cnt1 = max(min(u.k1, chunk8::row_tiles(u.len, u.n, p.G, first + kHalf, kHalf, p.causal)) - u.k0, 0);
+            }
             if (!whole && u.k0 == 0) {
               // begins here and ends in another CTA's run: joined by the second kernel
               int* m = p.merge + blockIdx.x * 8;
@@ -394,10 +442,21 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           }
           dst[0] = make_int4(u.b, u.hk, u.rb, u.k0);
           dst[1] = make_int4(u.tiles > 0 ? u.k1 - u.k0 : 0, u.n, u.len, u.tok0);
-          dst[2] = make_int4(cnt0, cnt1, slot, 0);
+          dst[2] = make_int4(cnt0, cnt1, slot, u.tiles > 0 && u.dual);
           mbar_arrive(bar(C::B_IFULL + s));
         }
         ++published;
+      };
+      // The pages of the tile `ahead` further on are brought to L2: a page's way from DRAM
+      // is longer than the tiles in flight take, where a CTA's tiles are few rows' work.
+      const int ahead = min(kAhead, 32 / ppt);
+      auto prefetch = [&](const Unit& u, int i) {
+        const int page = __shfl_sync(0xffffffffu, u.page, (i * ppt + lane) & 31);
+        if (lane < ppt && page >= 0) {
+          const size_t at = (static_cast<size_t>(page) * p.Hk + u.hk) * page_bytes;
+          bulk_prefetch(p.k_codes + at, page_bytes);
+          bulk_prefetch(p.v_codes + at, page_bytes);
+        }
       };
       while (ok && cur.tiles > 0) {
         if (cur.kt == cur.k0) publish(cur);
@@ -445,6 +504,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
                       bar(C::B_CFULL + st));
           ++v_tiles;
           if (i == 0 && next.tiles > 0) load_scales(next);
+          const int far = i + ahead;
+          (void)far;
         }
         cur = next;
       }
@@ -492,57 +553,92 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         ok = __all_sync(0xffffffffu, ok);
         return ok;
       };
-      int tile = 0;                          // K and V tiles so far
-      int nq[2] = {0, 0}, np[2] = {0, 0};    // items and P tiles of each row tile so far
+      Ring<C::NK> kr;                        // the next tile of K, of V
+      Ring<C::NV> vr;
+      int nq[2] = {0, 0}, np[2] = {0, 0};    // items and P tiles of each half so far
+      auto wait_k = [&]() { return wait(C::B_KFULL + kr.i, kr.phase); };
+      auto wait_v = [&]() { return wait(C::B_VFULL + vr.i, vr.phase); };
+      auto take_s = [&](int t, bool free_k) {  // S of half t over the K that is next
+        tc_fence_after();
+        if (elect_one()) {
+          issue_s(t, kr.i);
+          tc_commit(bar(C::B_SFULL + t));
+          if (free_k) tc_commit(bar(C::B_KEMPTY + kr.i));
+        }
+      };
       Item it;
       while (ok && take_item(it)) {
         const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
         const int cnt[2] = {__shfl_sync(0xffffffffu, it.cnt0, 0), __shfl_sync(0xffffffffu, it.cnt1, 0)};
-        if (!wait(C::B_KFULL + tile % C::NK, tile / C::NK)) break;
+        if (__shfl_sync(0xffffffffu, it.dual ? 1 : 0, 0) != 0) {
+          // The halves take the tiles in turn: K and V of each are free after its half.
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (cnt[t] > 0 && wait(C::B_Q + t, nq[t]++)) {
-            tc_fence_after();
-            if (elect_one()) {
-              issue_s(t, tile % C::NK);
-              tc_commit(bar(C::B_SFULL + t));
+          for (int t = 0; t < 2; ++t) {
+            if (cnt[t] == 0) break;
+            if (!wait_k() || !wait(C::B_Q + t, nq[t]++)) break;
+            take_s(t, true);
+            kr.step();
+          }
+          for (int j = 0; ok && j < cnt[0]; ++j) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (j >= cnt[t]) break;
+              if (!wait_v() || !wait(C::B_PFULL + t, np[t]++)) break;
+              tc_fence_after();
+              if (elect_one()) {
+                issue_pv(t, vr.i, j > 0);
+                if (j + 1 == cnt[t]) tc_commit(bar(C::B_ODONE + t));
+                tc_commit(bar(C::B_VEMPTY + vr.i));
+              }
+              vr.step();
+              if (j + 1 < cnt[t]) {
+                if (!wait_k()) break;
+                take_s(t, true);
+                kr.step();
+              }
             }
           }
+          continue;
         }
+        if (!wait_k()) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (cnt[t] > 0 && wait(C::B_Q + t, nq[t]++)) take_s(t, false);
         if (!ok) break;
-        if (elect_one()) tc_commit(bar(C::B_KEMPTY + tile % C::NK));
-        wait(C::B_VFULL + tile % C::NV, tile / C::NV);
-        for (int j = 0; ok && j < tiles; ++j, ++tile) {
-          const int vs = tile % C::NV, ks1 = (tile + 1) % C::NK;
+        if (elect_one()) tc_commit(bar(C::B_KEMPTY + kr.i));
+        kr.step();
+        wait_v();
+        for (int j = 0; ok && j < tiles; ++j) {
           const bool more = j + 1 < tiles;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (j < cnt[t] && wait(C::B_PFULL + t, np[t]++)) {
               tc_fence_after();
               if (elect_one()) {
-                issue_pv(t, vs, j > 0);
+                issue_pv(t, vr.i, j > 0);
                 if (j + 1 == cnt[t]) tc_commit(bar(C::B_ODONE + t));
               }
             }
             if (!ok) break;
             if (t == 0) {
-              if (more && !wait(C::B_KFULL + ks1, (tile + 1) / C::NK)) break;
+              if (more && !wait_k()) break;
             } else {
-              if (elect_one()) tc_commit(bar(C::B_VEMPTY + vs));
-              if (more && !wait(C::B_VFULL + (tile + 1) % C::NV, (tile + 1) / C::NV)) break;
+              if (elect_one()) tc_commit(bar(C::B_VEMPTY + vr.i));
+              vr.step();
+              if (more && !wait_v()) break;
             }
-            if (j + 1 < cnt[t] && elect_one()) {
-              issue_s(t, ks1);
-              tc_commit(bar(C::B_SFULL + t));
-            }
+            if (j + 1 < cnt[t]) take_s(t, false);
           }
-          if (ok && more && elect_one()) tc_commit(bar(C::B_KEMPTY + ks1));
+          if (ok && more) {
+            if (elect_one()) tc_commit(bar(C::B_KEMPTY + kr.i));
+            kr.step();
+          }
         }
       }
       // every MMA issued so far must finish before tensor memory is released
       if (elect_one()) tc_commit(bar(C::B_DRAIN));
       wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
-    } else {
+    } else if (warp != 8) {
     // ---------------------------------------------------------------- conversion
     // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32
     // chunks of consecutive rows, every sixth group of them.  The chunks of a
@@ -563,6 +659,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES;
     auto place = [&](int row, int half) -> uint32_t { return out0 + row * 128 + (((c0 + half) ^ (row & 7)) << 4); };
     int tile = 0;
+    Ring<C::NC> cr;
+    Ring<C::NV> vr;
     bool ok = true;
     auto wait = [&](int i, int phase) {
       ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
@@ -573,9 +671,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     while (ok && take_item(it)) {
       for (int kt = it.k0; kt < it.k0 + it.tiles; ++kt, ++tile) {
         const int held = cache8::tokens_from(it.len, kt, kKeys, 0);  // tokens of the tile, if fewer than its rows
-        const int st = tile % C::NC, slot = tile % C::NV;
-        if (!wait(C::B_CFULL + st, tile / C::NC)) break;
-        if (tile >= C::NV && !wait(C::B_VEMPTY + slot, tile / C::NV - 1)) break;
+        const int st = cr.i, slot = vr.i;
+        if (!wait(C::B_CFULL + st, cr.phase)) break;
+        if (tile >= C::NV && !wait(C::B_VEMPTY + slot, vr.phase ^ 1)) break;
         const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES + in0;
         const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_VF) + st * C::MAX_PPT;
         uint8_t* out = smem + C::OFF_V + slot * C::TILE_BYTES;
@@ -621,6 +719,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           mbar_arrive(bar(C::B_CEMPTY + st));
           mbar_arrive(bar(C::B_VFULL + slot));
         }
+        cr.step();
+        vr.step();
       }
     }
     }
@@ -635,7 +735,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     constexpr int CH = D / 8, RPP = 32 / CH;
     const int my_chunk = lane % CH, my_row = wq * 32 + lane / CH;
     auto place = [&](int row, int ch) { return q_smem + row * (2 * D) + ((ch ^ (row & 7)) << 4); };  // (within the warp's own rows)
-    int np = 0, no = 0, n_raw = 0;  // tiles and items of this row tile so far; of the warp's rows of Q
+    int np = 0, no = 0, n_raw = 0, n_join = 0;  // tiles and items of this half, rows of Q and joins so far
     int tile0 = 0;       // tiles of the items before
     bool ok = true;
     auto wait = [&](int i, int phase) {
@@ -643,16 +743,23 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       ok = __all_sync(0xffffffffu, ok);
       return ok;
     };
-    Item it;
-    while (ok && take_item(it)) {
-      const int cnt = t ? it.cnt1 : it.cnt0;
-      const int first = it.rb * kRows + t * kHalf, rows = it.n * p.G;
+    // An item's fields are read from shared memory where they are needed, which saves the
+    // tile loop their registers.
+    uint32_t item = 0;
+    enum { kHk = 1, kRb, kK0, kTiles, kN, kLen, kTok0, kCnt0, kCnt1, kSlot, kDual };
+    auto field = [&](int i) {
+      int v;
+      asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(item + 4 * i));
+      return v;
+    };
+    // This half's rows of the item: the first, and behind the last.
+    auto first_row = [&]() { return field(kRb) * kRows + (field(kDual) ? 0 : t * kHalf); };
+    auto all_rows = [&]() { return field(kN) * p.G; };
+    auto take = [&]() {
+      const int cnt = field(kCnt0 + t);
       const int first_tile = tile0;
-      tile0 += it.tiles;
-      if (first >= rows) continue;
-      const int f = first + r;
-      const bool exists = f < rows;
-      const int tok = f / p.G, g = f - tok * p.G;
+      tile0 += field(kTiles);
+      if (first_row() >= all_rows()) return;
       float m_ref = -CUDART_INF_F, l = 0.f;
       // (of the warp) some reference so large that a product's rounding, 2^-24 of it,
       // counts in the exponent
@@ -661,6 +768,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         // ---- Q: the warp's rows, all in flight at once, then each row scaled by a power
         // of two, as two e4m3 terms, in place: 8 rows' terms take the room of the rows.
         // (Loaded through registers in four batches, each as long as a miss: 5 us an item.)
+        const int first = first_row(), rows = all_rows();
         {
           const int from = first + wq * 32, count = max(min(rows - from, 32), 0);
           const int tok_a = from / p.G, toks = count > 0 ? (from + count - 1) / p.G - tok_a + 1 : 0;
@@ -671,12 +779,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           for (int i = lane; i < toks; i += 32) {
             const int f0 = max((tok_a + i) * p.G, from), f1 = min((tok_a + i + 1) * p.G, from + count);
             bulk_load(sb + C::OFF_Q + t * C::TILE_BYTES + (f0 - first) * (2 * D),
-                      p.q + static_cast<size_t>(it.tok0 + tok_a + i) * p.ldq +
-                          (static_cast<size_t>(it.hk) * p.G + f0 - (tok_a + i) * p.G) * D,
+                      p.q + static_cast<size_t>(field(kTok0) + tok_a + i) * p.ldq +
+                          (static_cast<size_t>(field(kHk)) * p.G + f0 - (tok_a + i) * p.G) * D,
                       (f1 - f0) * (2 * D), bar(C::B_RAW + warp));
           }
           ++n_raw;
-          if (!wait(C::B_RAW + warp, n_raw - 1)) break;
+          if (!wait(C::B_RAW + warp, n_raw - 1)) return;
         }
         // (rolled: run through once an item, unrolled code is all instruction fetches)
         int my_e = 0;  // the exponent of this thread's row
@@ -725,14 +833,20 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         const float c_row = exp2_int(my_e) * p.scale_log2;
         fence_proxy_async_smem();
         mbar_arrive(bar(C::B_Q + t));
-        // Keys the row sees, and the warpgroup's first row (which sees the fewest).
-        const int sees = exists ? chunk8::visible(it.len, it.n, tok, p.causal) : 0;
-        const int all_see = chunk8::visible(it.len, it.n, first / p.G, p.causal);
+        // This half's tiles: every one, or every other.  Keys, from the next tile's first, that
+        // the row sees, and that the half's first row does (which sees the fewest).
+        const int stride = field(kDual) ? 2 : 1, at = field(kDual) ? t : 0;
+        const int kv0 = (field(kK0) + at) * kKeys;  // (of a first tile behind the last: not used)
+        int sees = (first + r < rows ? chunk8::visible(field(kLen), field(kN), (first + r) / p.G, p.causal) : 0) - kv0;
+        int all_see = chunk8::visible(field(kLen), field(kN), first / p.G, p.causal) - kv0;
+        Ring<C::NSC> scr;  // the next tile's place among K's scales
+        scr.i = (first_tile + at) % C::NSC, scr.phase = (first_tile + at) / C::NSC & 1;
         for (int j = 0; j < cnt; ++j, ++np) {
           // the columns' factors: K's scale of each 16 keys, the row's and the softmax's
           // (not below fp32's least normal number: a masked column stays -infinity)
-          const int sc = (first_tile + j) % C::NSC;
-          if (!wait(C::B_SCFULL + sc, (first_tile + j) / C::NSC)) break;
+          const int sc = scr.i;
+          if (!wait(C::B_SCFULL + sc, scr.phase)) break;
+          scr.step(stride);
           const float* k_scale = reinterpret_cast<const float*>(smem + C::OFF_KS) + sc * C::MAX_PPT;
           float cf[8];
 #pragma unroll
@@ -745,14 +859,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           tmem_wait_ld();
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) reg_fence(s[ch]);
-          const int kv0 = (it.k0 + j) * kKeys;
-          if (all_see - kv0 < kKeys) {
-            const int end = sees - kv0;
+          if (all_see < kKeys) {
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (ch * 32 + i >= end) s[ch][i] = __float_as_uint(-CUDART_INF_F);
+                if (ch * 32 + i >= sees) s[ch][i] = __float_as_uint(-CUDART_INF_F);
           }
           // The largest y = s · factor of the row.
           auto row_max = [&]() -> float {
@@ -839,23 +951,72 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             tmem_wait_st();
           }
           l += lt;
+          sees -= stride * kKeys;
+          all_see -= stride * kKeys;
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(bar(C::B_PFULL + t));
         }
-        if (!ok || !wait(C::B_ODONE + t, no++)) break;
+        if (!ok || !wait(C::B_ODONE + t, no++)) return;
         tc_fence_after();
       }
-      const size_t part = static_cast<size_t>(it.slot < 0 ? 0 : it.slot) * kRows + t * kHalf + r;
-      if (it.slot < 0) {
+      // ---- a dual item: the first half's warps, which have the same lanes of tensor memory,
+      // take the second half's O with their own; m and l go through its columns of S
+      const bool join = field(kDual) && field(kCnt1) > 0;
+      float join0 = 1.f, join1 = 0.f;  // factors of the halves' O
+      if (join) {
+        uint32_t ml[16];
+        const uint32_t tM = lane_addr + C::S_COL(1);
+        if (t == 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) ml[i] = __float_as_uint(i == 0 ? m_ref : l);
+          tmem_st16(tM, ml);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(C::B_JOIN));
+          if (wait(C::B_JOIN + 1, n_join++)) tc_fence_after();
+          return;
+        }
+        if (!wait(C::B_JOIN, n_join++)) return;
+        tc_fence_after();
+        tmem_ld16(tM, ml);
+        tmem_wait_ld();
+        reg_fence(ml);
+        const float m1 = __uint_as_float(ml[0]), m = fmaxf(m_ref, m1);
+        join0 = m_ref == -CUDART_INF_F ? 0.f : ex2_approx(m_ref - m);
+        join1 = m1 == -CUDART_INF_F ? 0.f : ex2_approx(m1 - m);
+        l = fmaf(__uint_as_float(ml[1]), join1, l * join0);
+        m_ref = m;
+      } else if (field(kDual) && t == 1) {
+        return;
+      }
+      const int first = first_row(), rows = all_rows(), hk = field(kHk), tok0 = field(kTok0), slot = field(kSlot);
+      const bool exists = first + r < rows;
+      const int tok = (first + r) / p.G, g = first + r - tok * p.G;
+      auto load_o = [&](int c0, uint32_t (&o)[32]) {  // 32 columns of O
+        tmem_ld32(tO + c0, o);
+        if (join) {
+          uint32_t o1[32];
+          tmem_ld32(lane_addr + C::O_COL(1) + c0, o1);
+          tmem_wait_ld();
+          reg_fence(o);
+          reg_fence(o1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), join0, __uint_as_float(o1[i]) * join1));
+        } else {
+          tmem_wait_ld();
+          reg_fence(o);
+        }
+      };
+      const size_t part = static_cast<size_t>(slot < 0 ? 0 : slot) * kRows + t * kHalf + r;
+      if (slot < 0) {
         // ---- O / l, staged over Q (which no MMA reads any more), out by whole rows
         const float inv_l = l > 0.f ? exp2_int(kVShift) / l : 0.f;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t o[32];
-          tmem_ld32(tO + cb * 32, o);
-          tmem_wait_ld();
-          reg_fence(o);
+          load_o(cb * 32, o);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {  // a 16-byte chunk; its dimensions change places again
             uint32_t w[4];
@@ -876,24 +1037,22 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           const int qt = __shfl_sync(0xffffffffu, tok, from), qg = __shfl_sync(0xffffffffu, g, from);
           const uint4 y = *reinterpret_cast<const uint4*>(place(my_row + i * RPP, my_chunk));
           if (first + wq * 32 + from < rows)
-            *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(it.tok0 + qt) * p.H + it.hk * p.G + qg) * D + 8 * my_chunk) = y;
+            *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(tok0 + qt) * p.H + hk * p.G + qg) * D + 8 * my_chunk) = y;
         }
         __syncwarp();
         if (exists)
-          p.lse[static_cast<size_t>(it.hk * p.G + g) * p.total + it.tok0 + tok] =
+          p.lse[static_cast<size_t>(hk * p.G + g) * p.total + tok0 + tok] =
               l > 0.f ? (m_ref + log2f(l)) * kLn2 : -CUDART_INF_F;
       } else if (exists) {
         reinterpret_cast<float2*>(p.ml_part)[part] = make_float2(l > 0.f ? m_ref : -CUDART_INF_F, l);
       }
-      if (it.slot >= 0 && cnt > 0) {
+      if (slot >= 0 && cnt > 0) {
         // ---- a partial: four dimensions of 32 rows side by side
-        float4* dst = reinterpret_cast<float4*>(p.o_part) + static_cast<size_t>(it.slot) * (kRows * D / 4) + t * kHalf + r;
+        float4* dst = reinterpret_cast<float4*>(p.o_part) + static_cast<size_t>(slot) * (kRows * D / 4) + t * kHalf + r;
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t o[32];
-          tmem_ld32(tO + cb * 32, o);
-          tmem_wait_ld();
-          reg_fence(o);
+          load_o(cb * 32, o);
 #pragma unroll
           for (int u = 0; u < 8; ++u)
             if (exists)
@@ -902,6 +1061,21 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         }
         tc_fence_before();
       }
+      if (join) {
+        tc_fence_before();
+        mbar_arrive(bar(C::B_JOIN + 1));
+      }
+    };
+    while (ok) {
+      const int i = items % C::NI;
+      if (!wait(C::B_IFULL + i, items / C::NI)) break;
+      item = sb + C::OFF_ITEM + i * C::ITEM_INTS * 4;
+      const bool any = field(kTiles) > 0;
+      if (any) take();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_IEMPTY + i));
+      ++items;
+      if (!any) break;
     }
     // A copy issued lands before the CTA may exit, whoever aborted.
     if (n_raw > 0) wait_drain(bar(C::B_RAW + warp), (n_raw - 1) & 1, p.err, p.timeout_ns);

@@ -21,8 +21,30 @@ int main(int argc, char** argv) {
       std::printf("%%d %%d %%d\\n", row_tiles(len, n, G, rb * kRows, kRows, causal), row_tiles(len, n, G, rb * kRows, kHalf, causal),
                   row_tiles(len, n, G, rb * kRows + kHalf, kHalf, causal));
     std::printf("%%d %%d\\n", visible(len, n, 0, causal), visible(len, n, n - 1, causal));
-  } else if (argc == 4) {  // tiles ctas 0: the units before an item's first tile
-    std::printf("%%d\\n", extra_units(std::atoll(argv[1]), std::atoll(argv[2])));
+  } else if (argc == 4) {  // most, "cut", items as nt:w,...: every CTA's tiles of every item it has any of
+    const int most = std::atoi(argv[1]);
+    int nt[4096], w[4096], n = 0;
+    long long all = 0;
+    for (char* q = argv[3]; *q; ++n) {
+      nt[n] = std::strtol(q, &q, 10);
+      w[n] = std::strtol(q + 1, &q, 10);
+      all += static_cast<long long>(nt[n]) * w[n];
+      if (*q == ',') ++q;
+    }
+    const int ctas = runs(all, most), extra = extra_units(all, ctas);
+    const long long total = all + static_cast<long long>(extra) * n;
+    std::printf("%%d %%d %%lld\\n", ctas, extra, total);
+    for (int c = 0; c < ctas; ++c) {
+      const long long lo = run_start(c, total, ctas), hi = run_start(c + 1, total, ctas);
+      long long first = 0;
+      for (int i = 0; i < n; ++i) {
+        first += extra;
+        const int k0 = tiles_before(lo - first, w[i], nt[i]), k1 = tiles_before(hi - first, w[i], nt[i]);
+        if (k1 > k0) std::printf("%%d %%d %%d %%d %%d %%d\\n", c, i, k0, k1, run_of(first, total, ctas),
+                                 run_of(first + static_cast<long long>(nt[i] - 1) * w[i], total, ctas));
+        first += static_cast<long long>(nt[i]) * w[i];
+      }
+    }
   } else {  // total ctas: the runs' beginnings, and the run of each run's first and last unit
     const long long total = std::atoll(argv[1]), ctas = std::atoll(argv[2]);
     for (long long c = 0; c < ctas; ++c)
@@ -76,8 +98,27 @@ def test_runs_are_even_and_found_again(program, total):
     assert [row[1:] for row in out] == [[c, c] for c in range(ctas)]
 
 
-@pytest.mark.parametrize("tiles,ctas", [(1, 1), (7, 7), (152, 152), (303, 152), (304, 152), (455, 152), (456, 152), (10 ** 9, 152)])
-def test_units_before_an_item(program, tiles, ctas):
-    """No more than a CTA has tiles, so that no run is all fixed cost where work is scarce."""
-    (extra,), = program(tiles, ctas, 0)
-    assert 0 <= extra <= 3 and extra < tiles / ctas and (extra == 3 or extra == tiles // ctas - 1)
+@pytest.mark.parametrize("most", [1, 3, 152])
+@pytest.mark.parametrize("items", [[(1, 2)], [(1, 3)], [(7, 2)], [(7, 3)], [(3, 3), (1, 2), (2, 3), (5, 2)], [(1, 2)] * 300,
+                                   [(256, 2)] * 32, [(1 + i % 9, 2 + i % 2) for i in range(500)], [(250, 3)] * 256, [(2, 3), (1, 2)] * 40])
+def test_every_tile_is_in_one_run(program, items, most):
+    """And the CTAs between an item's first and last all have tiles of it, which the join relies on."""
+    out = program(most, "cut", ",".join(f"{n}:{w}" for n, w in items))
+    (ctas, extra, total), rows = out[0], out[1:]
+    assert 1 <= ctas <= most and 0 <= extra <= 10
+    seen = {}
+    for c, i, k0, k1, c0, c1 in rows:
+        assert k0 == seen.get(i, (0, 0))[0]
+        parts = seen.get(i, (0, []))[1] if i in seen else []
+        seen[i] = (k1, parts + [c])
+        assert c0 <= c <= c1
+        seen[i] = (k1, parts + [c])
+        assert (k0 == 0) == (c == c0) and (k1 == items[i][0]) == (c == c1)
+    assert len(seen) == len(items)
+    for i, (end, parts) in seen.items():
+        assert end == items[i][0] and parts == list(range(parts[0], parts[-1] + 1))
+    if most == 152 and len(items) > 200:  # and the runs are even, whole tiles and an item's cost apart
+        cost = {}
+        for c, i, k0, k1, _, _ in rows:
+            cost[c] = cost.get(c, 0) + (k1 - k0) * items[i][1] + (extra if k0 == 0 else 0)
+        assert max(cost.values()) <= total / ctas + extra + 3
