@@ -81,6 +81,32 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool mn_major) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Two floats to f16, the first in the low half; two f16 to two e4m3 codes (saturating)
+// and back (exact); a difference.
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4_of_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+      "mov.b32 %0, {l, h};}"
+      : "=r"(r)
+      : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void f16_of_e4m3x4(uint32_t code4, uint32_t& a, uint32_t& b) {
+  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
+      : "=r"(a), "=r"(b)
+      : "r"(code4));
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Byte `byte` of row `row` in a tile of W-byte rows swizzled over W bytes (the
 // 16-byte chunk's index exclusive-or the address bits above the 128-byte line).
 template <int W>

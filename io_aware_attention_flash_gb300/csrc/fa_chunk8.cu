@@ -21,8 +21,10 @@
 //
 // Warp roles (16 warps):
 //   0-3, 4-7   softmax, one warpgroup a row tile; thread r owns row r of it
-//   8          items and copies: publishes the CTA's next item, copies the codes of
-//              its pages (lane i: page i of the tile) with their scales
+//   15         items and K: publishes the CTA's next item, copies the codes of its pages
+//              (lane i: page i of the tile) and their scales
+//   8          the same of V (one warp for both could not issue the copies of 16-token
+//              pages as fast as they land)
 //   12         tcgen05.mma issue
 //   others     conversion of V tiles: none on the scheduler (warp mod 4) that the MMA
 //              warp shares
@@ -90,9 +92,9 @@ struct ChunkCfg {
   static constexpr int NBAR = B_JOIN + 2;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;          // slack to align the base to 1024
-  static constexpr int COPY_WARP = 15, MMA_WARP = 12, CONVERT_WARPS = 5;
+  static constexpr int COPY_WARP = 15, V_WARP = 8, MMA_WARP = 12, CONVERT_WARPS = 5;
   static constexpr int NUM_THREADS = 512;
-  static constexpr int READERS = 14;                    // warps that take an item: all but the copying one
+  static constexpr int READERS = 15;                    // warps that take an item: all but the one that publishes it
   // Registers a thread after the split; launched with 128.
   static constexpr int REG_SOFTMAX = 192, REG_OTHER = 64;
   static_assert(2 * REG_SOFTMAX + 2 * REG_OTHER == 4 * 128, "the split takes what the launch gives");
@@ -103,9 +105,6 @@ struct ChunkCfg {
   static_assert(OFF_K % 1024 == 0 && OFF_C % 1024 == 0 && CODE_BYTES % 1024 == 0, "swizzle atoms");
   static_assert(OFF_ITEM % 16 == 0 && OFF_KS % 16 == 0 && OFF_SCAN % 8 == 0, "vector accesses");
 };
-
-// Tiles from one that is copied to the one that is brought to L2.
-constexpr int kAhead = 6;
 
 // What the roles know of an item.
 struct Item {
@@ -130,11 +129,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
-}
-
-// Has a stretch of global memory brought to L2.
-__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 // New tokens and cached tokens of sequence b, within what the buffers hold.
@@ -354,7 +348,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         int kt, tiles;                            // first tile of the unit, and how many
         long long last;                           // the first unit of the item's last tile
         int page;                                 // this lane's page (of 32 / ppt tiles), -1: none
-        float ks, vs;
+        float ks;
       };
       int x = static_cast<int>(found[1]);
       long long x_start = found[0], at = u_lo;  // first unit of the pair; the next unit
@@ -399,10 +393,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       };
       auto load_scales = [&](Unit& u) {
         const bool token = lane < u.tiles * ppt && u.kt * ppt + lane < cache8::pages_of(u.len, p.block_shift);
-        u.ks = u.vs = 0.f;
+        u.ks = 0.f;
         if (token && u.page >= 0 && u.page < p.num_blocks) {
           u.ks = p.k_scale[static_cast<size_t>(u.page) * p.Hk + u.hk];
-          u.vs = p.v_scale[static_cast<size_t>(u.page) * p.Hk + u.hk];
         } else {
           if (token) atomicOr(p.err, kDevErrPage);
           u.page = -1;
@@ -411,7 +404,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       Unit cur, next;
       next_unit(cur);
       if (cur.tiles > 0) load_scales(cur);
-      int tile = 0, v_tiles = 0, published = 0;  // (tile: K tiles issued)
+      int tile = 0, published = 0;  // tiles issued, items
       bool ok = true;
       auto publish = [&](const Unit& u) {
         const int s = published % C::NI;
@@ -447,17 +440,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         }
         ++published;
       };
-      // The pages of the tile `ahead` further on are brought to L2: a page's way from DRAM
-      // is longer than the tiles in flight take, where a CTA's tiles are few rows' work.
-      const int ahead = min(kAhead, 32 / ppt);
-      auto prefetch = [&](const Unit& u, int i) {
-        const int page = __shfl_sync(0xffffffffu, u.page, (i * ppt + lane) & 31);
-        if (lane < ppt && page >= 0) {
-          const size_t at = (static_cast<size_t>(page) * p.Hk + u.hk) * page_bytes;
-          bulk_prefetch(p.k_codes + at, page_bytes);
-          bulk_prefetch(p.v_codes + at, page_bytes);
-        }
-      };
       while (ok && cur.tiles > 0) {
         if (cur.kt == cur.k0) publish(cur);
         next_unit(next);
@@ -465,9 +447,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           const int n_pages = min(ppt, cache8::pages_of(cur.len, p.block_shift) - (cur.kt + i) * ppt);
           const int from = (i * ppt + lane) & 31;
           const int page = __shfl_sync(0xffffffffu, cur.page, from);
-          const float ks = __shfl_sync(0xffffffffu, cur.ks, from), vs = __shfl_sync(0xffffffffu, cur.vs, from);
+          const float ks = __shfl_sync(0xffffffffu, cur.ks, from);
           const bool mine = lane < n_pages && page >= 0;
-          // ---- K: a page out of range reads as zeros (the copy's fill)
+          // a page out of range reads as zeros (the copy's fill)
           const int ks_slot = tile % C::NK;
           if (tile >= C::NK)
             ok = wait_bounded(bar(C::B_KEMPTY + ks_slot), (tile / C::NK - 1) & 1, abort_flag, p.err, p.timeout_ns);
@@ -484,28 +466,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           if (lane < n_pages)
             tma_load_4d(sb + C::OFF_K + ks_slot * C::CODE_BYTES + lane * page_bytes, &tmK, bar(C::B_KFULL + ks_slot), 0, 0,
                         cur.hk, page >= 0 ? page : p.num_blocks);
-          // ---- V
-          const int st = tile % C::NC;
-          if (tile >= C::NC)
-            ok = wait_bounded(bar(C::B_CEMPTY + st), (tile / C::NC - 1) & 1, abort_flag, p.err, p.timeout_ns);
           ++tile;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * page_bytes;
-          if (lane < C::MAX_PPT)
-            reinterpret_cast<uint2*>(smem + C::OFF_VF)[st * C::MAX_PPT + lane] =
-                mine ? scale_factors(vs) : make_uint2(0u, kOne2);
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(bar(C::B_CFULL + st), bytes);
-          __syncwarp();
-          if (mine)
-            bulk_load(sb + C::OFF_C + st * C::CODE_BYTES + lane * page_bytes,
-                      p.v_codes + (static_cast<size_t>(page) * p.Hk + cur.hk) * page_bytes, page_bytes,
-                      bar(C::B_CFULL + st));
-          ++v_tiles;
           if (i == 0 && next.tiles > 0) load_scales(next);
-          const int far = i + ahead;
-          (void)far;
         }
         cur = next;
       }
@@ -516,8 +478,58 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       // Every copy issued lands before the CTA may exit, whoever aborted.
       for (int s = 0; s < C::NK && s < tile; ++s)
         wait_drain(bar(C::B_KFULL + s), ((tile - 1 - s) / C::NK) & 1, p.err, p.timeout_ns);
-      for (int s = 0; s < C::NC && s < v_tiles; ++s)
-        wait_drain(bar(C::B_CFULL + s), ((v_tiles - 1 - s) / C::NC) & 1, p.err, p.timeout_ns);
+    } else if (warp == C::V_WARP) {
+      // ------------------------------------------------------------ copies of V
+      const int ppt = kKeys >> p.block_shift, page_bytes = D << p.block_shift, window = 32 / ppt;  // tiles of 32 pages
+      Ring<C::NC> cr;
+      int tile = 0;
+      bool ok = true;
+      Item it;
+      while (ok && take_item(it)) {
+        const int pages = cache8::pages_of(it.len, p.block_shift), end = it.k0 + it.tiles;
+        auto load_pages = [&](int kt) {  // lane i: page i of the window at tile kt, -1: none
+          return kt + lane / ppt < end && kt * ppt + lane < pages
+                     ? p.table[static_cast<size_t>(it.b) * p.table_cols + kt * ppt + lane]
+                     : -1;
+        };
+        auto load_scales = [&](int& page) {  // (a page out of range is reported with K's)
+          if (page < 0 || page >= p.num_blocks) page = -1;
+          return page >= 0 ? p.v_scale[static_cast<size_t>(page) * p.Hk + it.hk] : 0.f;
+        };
+        int cur = load_pages(it.k0);
+        float scale = load_scales(cur);
+        for (int k0 = it.k0; ok && k0 < end; k0 += window) {
+          int next = load_pages(min(k0 + window, end));
+          float next_scale = 0.f;
+          for (int i = 0; i < window && k0 + i < end; ++i, ++tile) {
+            const int from = (i * ppt + lane) & 31;
+            const int page = __shfl_sync(0xffffffffu, cur, from);
+            const float vs = __shfl_sync(0xffffffffu, scale, from);
+            const bool mine = lane < ppt && page >= 0;  // (a page out of range reads as zeros: its factor is 0)
+            if (tile >= C::NC) ok = wait_bounded(bar(C::B_CEMPTY + cr.i), cr.phase ^ 1, abort_flag, p.err, p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * page_bytes;
+            if (lane < C::MAX_PPT)
+              reinterpret_cast<uint2*>(smem + C::OFF_VF)[cr.i * C::MAX_PPT + lane] =
+                  mine ? scale_factors(vs) : make_uint2(0u, kOne2);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::B_CFULL + cr.i), bytes);
+            __syncwarp();
+            if (mine)
+              bulk_load(sb + C::OFF_C + cr.i * C::CODE_BYTES + lane * page_bytes,
+                        p.v_codes + (static_cast<size_t>(page) * p.Hk + it.hk) * page_bytes, page_bytes,
+                        bar(C::B_CFULL + cr.i));
+            cr.step();
+            if (i == 0) next_scale = load_scales(next);
+          }
+          cur = next;
+          scale = next_scale;
+        }
+      }
+      // Every copy issued lands before the CTA may exit, whoever aborted.
+      for (int s = 0; s < C::NC && s < tile; ++s)
+        wait_drain(bar(C::B_CFULL + s), ((tile - 1 - s) / C::NC) & 1, p.err, p.timeout_ns);
     } else if (warp == C::MMA_WARP) {
       // ------------------------------------------------------------ MMA
       // The tensor core's queue holds some 190 cycles of products, and a wait for what
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       // every MMA issued so far must finish before tensor memory is released
       if (elect_one()) tc_commit(bar(C::B_DRAIN));
       wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
-    } else if (warp != 8) {
+    } else {
     // ---------------------------------------------------------------- conversion
     // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32
     // chunks of consecutive rows, every sixth group of them.  The chunks of a
@@ -733,8 +745,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     uint8_t* q_smem = smem + C::OFF_Q + t * C::TILE_BYTES;
     // A warp moves its 32 rows 16 bytes a lane, RPP rows at a time.
     constexpr int CH = D / 8, RPP = 32 / CH;
-    const int my_chunk = lane % CH, my_row = wq * 32 + lane / CH;
-    auto place = [&](int row, int ch) { return q_smem + row * (2 * D) + ((ch ^ (row & 7)) << 4); };  // (within the warp's own rows)
+    const int my_chunk = lane % CH;
     int np = 0, no = 0, n_raw = 0, n_join = 0;  // tiles and items of this half, rows of Q and joins so far
     int tile0 = 0;       // tiles of the items before
     bool ok = true;
@@ -755,6 +766,25 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     // This half's rows of the item: the first, and behind the last.
     auto first_row = [&]() { return field(kRb) * kRows + (field(kDual) ? 0 : t * kHalf); };
     auto all_rows = [&]() { return field(kN) * p.G; };
+    // The warp's rows of Q of an item, all in flight at once.  (Loaded through registers in
+    // four batches, each as long as a miss: 5 us an item.)
+    auto load_q = [&]() {
+      const int first = first_row(), from = first + wq * 32, count = max(min(all_rows() - from, 32), 0);
+      const int tok_a = from / p.G, toks = count > 0 ? (from + count - 1) / p.G - tok_a + 1 : 0;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(bar(C::B_RAW + warp), count * (2 * D));
+      __syncwarp();
+      for (int i = lane; i < toks; i += 32) {
+        const int f0 = max((tok_a + i) * p.G, from), f1 = min((tok_a + i + 1) * p.G, from + count);
+        bulk_load(sb + C::OFF_Q + t * C::TILE_BYTES + (f0 - first) * (2 * D),
+                  p.q + static_cast<size_t>(field(kTok0) + tok_a + i) * p.ldq +
+                      (static_cast<size_t>(field(kHk)) * p.G + f0 - (tok_a + i) * p.G) * D,
+                  (f1 - f0) * (2 * D), bar(C::B_RAW + warp));
+      }
+      ++n_raw;
+    };
+    bool q_ahead = false;  // the next item's are on their way already
     auto take = [&]() {
       const int cnt = field(kCnt0 + t);
       const int first_tile = tile0;
@@ -765,27 +795,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       // counts in the exponent
       bool far = false;
       if (cnt > 0) {
-        // ---- Q: the warp's rows, all in flight at once, then each row scaled by a power
-        // of two, as two e4m3 terms, in place: 8 rows' terms take the room of the rows.
-        // (Loaded through registers in four batches, each as long as a miss: 5 us an item.)
+        // ---- Q: each row scaled by a power of two, as two e4m3 terms, in place: 8 rows'
+        // terms take the room of the rows
+        if (!q_ahead) load_q();
+        q_ahead = false;
+        if (!wait(C::B_RAW + warp, n_raw - 1)) return;
         const int first = first_row(), rows = all_rows();
-        {
-          const int from = first + wq * 32, count = max(min(rows - from, 32), 0);
-          const int tok_a = from / p.G, toks = count > 0 ? (from + count - 1) / p.G - tok_a + 1 : 0;
-          fence_proxy_async_smem();  // (the staging of O has been read)
-          __syncwarp();
-          if (lane == 0) mbar_arrive_expect_tx(bar(C::B_RAW + warp), count * (2 * D));
-          __syncwarp();
-          for (int i = lane; i < toks; i += 32) {
-            const int f0 = max((tok_a + i) * p.G, from), f1 = min((tok_a + i + 1) * p.G, from + count);
-            bulk_load(sb + C::OFF_Q + t * C::TILE_BYTES + (f0 - first) * (2 * D),
-                      p.q + static_cast<size_t>(field(kTok0) + tok_a + i) * p.ldq +
-                          (static_cast<size_t>(field(kHk)) * p.G + f0 - (tok_a + i) * p.G) * D,
-                      (f1 - f0) * (2 * D), bar(C::B_RAW + warp));
-          }
-          ++n_raw;
-          if (!wait(C::B_RAW + warp, n_raw - 1)) return;
-        }
         // (rolled: run through once an item, unrolled code is all instruction fetches)
         int my_e = 0;  // the exponent of this thread's row
 #pragma unroll 1
@@ -815,15 +830,21 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             const int of_row = __shfl_sync(0xffffffffu, e, lane % RPP * CH);
             if (lane / RPP == r8 / RPP + i) my_e = of_row;
             const float inv = exp2_int(-e);
+            // (through f16, which holds the scaled values exactly down to 2^-14)
+            const uint64_t inv2 = f2_pack(inv, inv);
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const float v[4] = {bf16lo_to_f32(w[2 * u]) * inv, bf16hi_to_f32(w[2 * u]) * inv,
-                                  bf16lo_to_f32(w[2 * u + 1]) * inv, bf16hi_to_f32(w[2 * u + 1]) * inv};
-              float h[4];
-              hi[u] = pack_e4m3x4(v[0], v[1], v[2], v[3]);
-              unpack_e4m3x4(hi[u], h);
-              lo[u] = pack_e4m3x4(v[0] - h[0], v[1] - h[1], v[2] - h[2], v[3] - h[3]);
+              uint32_t h[2], back[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float a, b;
+                f2_unpack(fmul2(f2_pack(bf16lo_to_f32(w[2 * u + k]), bf16hi_to_f32(w[2 * u + k])), inv2), a, b);
+                h[k] = pack_f16x2(a, b);
+              }
+              hi[u] = e4m3x4_of_f16(h[0], h[1]);
+              f16_of_e4m3x4(hi[u], back[0], back[1]);
+              lo[u] = e4m3x4_of_f16(sub_f16x2(h[0], back[0]), sub_f16x2(h[1], back[1]));
             }
             uint8_t* at = rows8 + swz<D>(i * RPP + lane / CH, 8 * my_chunk);
             *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
@@ -957,6 +978,17 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           tc_fence_before();
           mbar_arrive(bar(C::B_PFULL + t));
         }
+        // Q's place is free: the next item's, if that is known
+        if (const int i = (items + 1) % C::NI;
+            ok && __all_sync(0xffffffffu, mbar_test_wait(bar(C::B_IFULL + i), (items + 1) / C::NI & 1))) {
+          const uint32_t now = item;
+          item = sb + C::OFF_ITEM + i * C::ITEM_INTS * 4;
+          if (field(kTiles) > 0 && field(kCnt0 + t) > 0 && first_row() < all_rows()) {
+            load_q();
+            q_ahead = true;
+          }
+          item = now;
+        }
         if (!ok || !wait(C::B_ODONE + t, no++)) return;
         tc_fence_after();
       }
@@ -1011,8 +1043,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       };
       const size_t part = static_cast<size_t>(slot < 0 ? 0 : slot) * kRows + t * kHalf + r;
       if (slot < 0) {
-        // ---- O / l, staged over Q (which no MMA reads any more), out by whole rows
+        // ---- O / l, row by row (staged for whole lines it would take Q's place, which the
+        // next item's rows are on their way to)
         const float inv_l = l > 0.f ? exp2_int(kVShift) / l : 0.f;
+        uint4* dst = reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(tok0 + tok) * p.H + hk * p.G + g) * D);
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
           uint32_t o[32];
@@ -1026,20 +1060,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
               w[2 * e] = pack_bf16x2(__uint_as_float(q4[0]) * inv_l, __uint_as_float(q4[2]) * inv_l);
               w[2 * e + 1] = pack_bf16x2(__uint_as_float(q4[1]) * inv_l, __uint_as_float(q4[3]) * inv_l);
             }
-            *reinterpret_cast<uint4*>(place(r, cb * 4 + u)) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (exists) dst[cb * 4 + u] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
         tc_fence_before();
-        __syncwarp();
-#pragma unroll 2
-        for (int i = 0; i < 32 / RPP; ++i) {
-          const int from = i * RPP + lane / CH;
-          const int qt = __shfl_sync(0xffffffffu, tok, from), qg = __shfl_sync(0xffffffffu, g, from);
-          const uint4 y = *reinterpret_cast<const uint4*>(place(my_row + i * RPP, my_chunk));
-          if (first + wq * 32 + from < rows)
-            *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(tok0 + qt) * p.H + hk * p.G + qg) * D + 8 * my_chunk) = y;
-        }
-        __syncwarp();
         if (exists)
           p.lse[static_cast<size_t>(hk * p.G + g) * p.total + tok0 + tok] =
               l > 0.f ? (m_ref + log2f(l)) * kLn2 : -CUDART_INF_F;
