@@ -746,7 +746,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     // A warp moves its 32 rows 16 bytes a lane, RPP rows at a time.
     constexpr int CH = D / 8, RPP = 32 / CH;
     const int my_chunk = lane % CH;
-    int np = 0, no = 0, n_raw = 0, n_join = 0;  // tiles and items of this half, rows of Q and joins so far
+    // Phases of what this half waits for once a tile, an item, a load of Q, a join: one
+    // register (the tile loop has none to spare).
+    uint32_t phases = 0;
+    enum { kTile = 1, kItem = 2, kRaw = 4, kJoin = 8, kRawAhead = 16, kRawEver = 32 };
+    auto phase = [&](uint32_t of) { return (phases & of) ? 1 : 0; };
     int tile0 = 0;       // tiles of the items before
     bool ok = true;
     auto wait = [&](int i, int phase) {
@@ -782,9 +786,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
                       (static_cast<size_t>(field(kHk)) * p.G + f0 - (tok_a + i) * p.G) * D,
                   (f1 - f0) * (2 * D), bar(C::B_RAW + warp));
       }
-      ++n_raw;
+      phases |= kRawEver;
     };
-    bool q_ahead = false;  // the next item's are on their way already
     auto take = [&]() {
       const int cnt = field(kCnt0 + t);
       const int first_tile = tile0;
@@ -797,9 +800,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       if (cnt > 0) {
         // ---- Q: each row scaled by a power of two, as two e4m3 terms, in place: 8 rows'
         // terms take the room of the rows
-        if (!q_ahead) load_q();
-        q_ahead = false;
-        if (!wait(C::B_RAW + warp, n_raw - 1)) return;
+        if (!(phases & kRawAhead)) load_q();  // (else they are on their way already)
+        phases &= ~kRawAhead;
+        const bool landed = wait(C::B_RAW + warp, phase(kRaw));
+        phases ^= kRaw;
+        if (!landed) return;
         const int first = first_row(), rows = all_rows();
         // (rolled: run through once an item, unrolled code is all instruction fetches)
         int my_e = 0;  // the exponent of this thread's row
@@ -862,17 +867,22 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         int all_see = chunk8::visible(field(kLen), field(kN), first / p.G, p.causal) - kv0;
         Ring<C::NSC> scr;  // the next tile's place among K's scales
         scr.i = (first_tile + at) % C::NSC, scr.phase = (first_tile + at) / C::NSC & 1;
-        for (int j = 0; j < cnt; ++j, ++np) {
+        for (int j = 0; j < cnt; ++j) {
           // the columns' factors: K's scale of each 16 keys, the row's and the softmax's
           // (not below fp32's least normal number: a masked column stays -infinity)
           const int sc = scr.i;
           if (!wait(C::B_SCFULL + sc, scr.phase)) break;
           scr.step(stride);
-          const float* k_scale = reinterpret_cast<const float*>(smem + C::OFF_KS) + sc * C::MAX_PPT;
+          const uint32_t k_scale = sb + C::OFF_KS + sc * (C::MAX_PPT * 4);
           float cf[8];
 #pragma unroll
-          for (int g16 = 0; g16 < 8; ++g16) cf[g16] = fmaxf(k_scale[(16 * g16) >> p.block_shift] * c_row, 0x1p-126f);
-          if (!wait(C::B_SFULL + t, np)) break;
+          for (int g16 = 0; g16 < 8; ++g16) {
+            float v;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(k_scale + (((16 * g16) >> p.block_shift) << 2)));
+            cf[g16] = fmaxf(v * c_row, 0x1p-126f);
+          }
+          if (!wait(C::B_SFULL + t, phase(kTile))) break;
+          phases ^= kTile;
           tc_fence_after();
           uint32_t s[4][32];
 #pragma unroll
@@ -985,11 +995,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           item = sb + C::OFF_ITEM + i * C::ITEM_INTS * 4;
           if (field(kTiles) > 0 && field(kCnt0 + t) > 0 && first_row() < all_rows()) {
             load_q();
-            q_ahead = true;
+            phases |= kRawAhead;
           }
           item = now;
         }
-        if (!ok || !wait(C::B_ODONE + t, no++)) return;
+        if (!ok || !wait(C::B_ODONE + t, phase(kItem))) return;
+        phases ^= kItem;
         tc_fence_after();
       }
       // ---- a dual item: the first half's warps, which have the same lanes of tensor memory,
@@ -1006,10 +1017,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(bar(C::B_JOIN));
-          if (wait(C::B_JOIN + 1, n_join++)) tc_fence_after();
+          if (wait(C::B_JOIN + 1, phase(kJoin))) tc_fence_after();
+          phases ^= kJoin;
           return;
         }
-        if (!wait(C::B_JOIN, n_join++)) return;
+        if (!wait(C::B_JOIN, phase(kJoin))) return;
+        phases ^= kJoin;
         tc_fence_after();
         tmem_ld16(tM, ml);
         tmem_wait_ld();
@@ -1102,7 +1115,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       if (!any) break;
     }
     // A copy issued lands before the CTA may exit, whoever aborted.
-    if (n_raw > 0) wait_drain(bar(C::B_RAW + warp), (n_raw - 1) & 1, p.err, p.timeout_ns);
+    if (phases & kRawEver) wait_drain(bar(C::B_RAW + warp), phase(kRaw) ^ ((phases & kRawAhead) ? 0 : 1), p.err, p.timeout_ns);
   }
 
   tc_fence_before();
