@@ -415,7 +415,9 @@ class _RotaryEmbedding(torch.autograd.Function):
 
 
 def rotary_embedding(q, k, positions, rotary: Rotary):
-    """Autograd-aware rotary_forward, differentiable once."""
+    """Autograd-aware rotary_forward, differentiable once; captured into a CUDA graph
+    as flash_attention_grouped is.  positions may not change before the backward
+    pass.  torch.jit.trace and make_fx are refused."""
     out = _binding.native().rotary_embedding(q, k, positions, rotary)
     if out is not None:
         return out

@@ -48,8 +48,8 @@ FA_CHUNK_FN bool dual(int n, int G, int rb) { return n * G - rb * kRows <= kHalf
 // halves' products, of which a dual item's tile is one), and `extra` before an item's
 // first, as many as its fixed cost is (kItemCost; less where a CTA has little more than
 // a tile: every one had better have a CTA of its own).  Measured: a tile takes 1.2 us of
-// a dual item, 1.7 of another; an item 6 to 9.  Sixteen sequences of 64 to 1,000 new
-// tokens take 259 us with a cost of 10, 240 with 14, 231 with 18, 233 with 22, 242 with
+// a dual item, 1.7 of another; an item 6 to 9.  Sixteen sequences of 1 to 512 new
+// tokens over 100 to 8,192 take 259 us with a cost of 10, 240 with 14, 231 with 18, 233 with 22, 242 with
 // 26; one long document takes the same with all.
 constexpr int kMostUnits = 3, kItemCost = 18;
 FA_CHUNK_FN int tile_units(bool dual) { return dual ? 2 : kMostUnits; }

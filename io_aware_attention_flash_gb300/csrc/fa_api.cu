@@ -510,7 +510,7 @@ fa_status chunk_plan(int B, int max_new, int total, int H, int Hk, int max_seqle
   if (static_cast<long long>(total) * H > 0x7fffffffLL) return FA_ERR_SHAPE;
   const long long rows = static_cast<long long>(max_new < total ? max_new : total) * (H / Hk);
   const long long blocks = (rows + fa::chunk8::kRows - 1) / fa::chunk8::kRows;
-  if (blocks * B > 0x7fffffffLL) return FA_ERR_SHAPE;
+  if (blocks * B > 0x3fffffffLL) return FA_ERR_SHAPE;  // (counted with 32 bits, in steps of a CTA)
   const long long tiles = (static_cast<long long>(max_seqlen) + fa::chunk8::kKeys - 1) / fa::chunk8::kKeys;
   const long long most = kChunkCtas / tiles / Hk < blocks * B ? kChunkCtas : blocks * B * Hk * tiles;
   w->row_blocks = static_cast<int>(blocks);

@@ -653,7 +653,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     } else {
     // ---------------------------------------------------------------- conversion
     // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32
-    // chunks of consecutive rows, every sixth group of them.  The chunks of a
+    // chunks of consecutive rows, every fifth group of them.  The chunks of a
     // quarter-warp lie in two rows, at d = 128 in the two halves of them: neither its
     // reads nor its swizzled writes meet in a bank.
     const int cw = warp < C::MMA_WARP ? warp - 9 : warp - 10;
@@ -834,7 +834,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
             const int e = min(scale_exponent(top, -126), 120);
             const int of_row = __shfl_sync(0xffffffffu, e, lane % RPP * CH);
             if (lane / RPP == r8 / RPP + i) my_e = of_row;
-            const float inv = exp2_int(-e);
+            // (infinities, which e4m3 has not, make the row NaN as a whole)
+            const float inv = top < 0x7f80u ? exp2_int(-e) : CUDART_NAN_F;
             // (through f16, which holds the scaled values exactly down to 2^-14)
             const uint64_t inv2 = f2_pack(inv, inv);
             uint32_t hi[2], lo[2];
@@ -1058,7 +1059,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       if (slot < 0) {
         // ---- O / l, row by row (staged for whole lines it would take Q's place, which the
         // next item's rows are on their way to)
-        const float inv_l = l > 0.f ? exp2_int(kVShift) / l : 0.f;
+        const float inv_l = l == 0.f ? 0.f : exp2_int(kVShift) / l;
         uint4* dst = reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(tok0 + tok) * p.H + hk * p.G + g) * D);
 #pragma unroll 1
         for (int cb = 0; cb < D / 32; ++cb) {
@@ -1079,9 +1080,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         tc_fence_before();
         if (exists)
           p.lse[static_cast<size_t>(hk * p.G + g) * p.total + tok0 + tok] =
-              l > 0.f ? (m_ref + log2f(l)) * kLn2 : -CUDART_INF_F;
+              l == 0.f ? -CUDART_INF_F : (m_ref + log2f(l)) * kLn2;
       } else if (exists) {
-        reinterpret_cast<float2*>(p.ml_part)[part] = make_float2(l > 0.f ? m_ref : -CUDART_INF_F, l);
+        reinterpret_cast<float2*>(p.ml_part)[part] = make_float2(l == 0.f ? -CUDART_INF_F : l > 0.f ? m_ref : l, l);  // (NaN: both)
       }
       if (slot >= 0 && cnt > 0) {
         // ---- a partial: four dimensions of 32 rows side by side
@@ -1169,7 +1170,7 @@ __global__ void __launch_bounds__(4 * D) fa_chunk8_merge_kernel(const Chunk8Para
     const float t = weights[i * kMergeRows + r];
     const float wt = t == -CUDART_INF_F ? 0.f : ex2_approx(t - top);
     weights[i * kMergeRows + r] = wt;
-    if (wt > 0.f) l = fmaf(wt, ml[slot(i) * kRows + row].y, l);
+    if (wt != 0.f) l = fmaf(wt, ml[slot(i) * kRows + row].y, l);
   }
   red[d4][r] = l;
   __syncthreads();
@@ -1183,16 +1184,16 @@ __global__ void __launch_bounds__(4 * D) fa_chunk8_merge_kernel(const Chunk8Para
     const float wt = weights[i * kMergeRows + r];
     const float4 v = part[(slot(i) * (D / 4) + d4) * kRows + row];
     // what a row that sees none of the keys has in its place is not defined
-    const float4 u = wt > 0.f ? v : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 u = wt != 0.f ? v : make_float4(0.f, 0.f, 0.f, 0.f);
     o.x = fmaf(wt, u.x, o.x), o.y = fmaf(wt, u.y, o.y);
     o.z = fmaf(wt, u.z, o.z), o.w = fmaf(wt, u.w, o.w);
   }
-  const float inv = l > 0.f ? exp2_int(kVShift) / l : 0.f;
+  const float inv = l == 0.f ? 0.f : exp2_int(kVShift) / l;
   const int tok = f / p.G, h = hk * p.G + f - tok * p.G;
   *reinterpret_cast<uint2*>(p.o + (static_cast<size_t>(tok0 + tok) * p.H + h) * D + 4 * d4) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
   if (d4 == 0)
-    p.lse[static_cast<size_t>(h) * p.total + tok0 + tok] = l > 0.f ? (top + log2f(l)) * kLn2 : -CUDART_INF_F;
+    p.lse[static_cast<size_t>(h) * p.total + tok0 + tok] = l == 0.f ? -CUDART_INF_F : (top + log2f(l)) * kLn2;
 }
 
 template <int D>

@@ -403,7 +403,7 @@ cudaError_t launch_append(const Cache8StoreParams& p, const RotaryParams& r, con
   if (e != cudaSuccess) return e;
   const long long groups = (p.Hk + C::HEADS - 1) / C::HEADS;
   const long long store = static_cast<long long>(p.B) * p.blocks * 2 * groups;
-  const long long turn = (p.total + C::TOKENS - 1) / C::TOKENS;
+  const long long turn = (p.total - 1) / C::TOKENS + 1;
   if (store + turn > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return launch_kernel(fa_cache8_append_kernel<D, BLOCK, IL>, dim3(static_cast<unsigned>(store + turn)), dim3(C::NT), C::SMEM, s,
                        true, p, r, x, static_cast<int>(store), zero_tail);
@@ -427,7 +427,7 @@ cudaError_t launch_append_d(int block, const Cache8StoreParams& p, const RotaryP
 
 template <int D>
 cudaError_t launch_rotary_d(const RotaryParams& r, const TurnRows& x, int total, cudaStream_t s) {
-  const dim3 grid((total + kTurnTokens - 1) / kTurnTokens), block(kTurnThreads);
+  const dim3 grid((total - 1) / kTurnTokens + 1), block(kTurnThreads);
   return r.interleaved ? launch_kernel(fa_rotary_kernel<D, true>, grid, block, 0, s, true, r, x, total)
                        : launch_kernel(fa_rotary_kernel<D, false>, grid, block, 0, s, true, r, x, total);
 }

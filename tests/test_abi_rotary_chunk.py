@@ -59,7 +59,8 @@ def test_append(lib, bad, status):
     (dict(d=32), HEAD_DIM), (dict(block=8), SHAPE), (dict(H=5), SHAPE), (dict(Hk=3), SHAPE), (dict(B=0), SHAPE), (dict(max_new=0), SHAPE),
     (dict(total=0), SHAPE), (dict(max_seqlen=0), SHAPE), (dict(ldq=192), SHAPE), (dict(scale=0.0), SCALE), (dict(scale=-1.0), SCALE),
     (dict(scale=math.nan), SCALE), (dict(scale=math.inf), SCALE), (dict(nbytes=16), WORKSPACE), (dict(ws=None), NULL), (dict(cu=None), NULL),
-    (dict(q=P + 8), ALIGN), (dict(ws=P + 8), ALIGN), (dict(total=2 ** 29, H=8), SHAPE), (dict(B=2 ** 30, max_new=2 ** 20, total=2 ** 20), SHAPE)])
+    (dict(q=P + 8), ALIGN), (dict(ws=P + 8), ALIGN), (dict(total=2 ** 29, H=8), SHAPE), (dict(B=2 ** 30, max_new=2 ** 20, total=2 ** 20), SHAPE),
+    (dict(B=2 ** 23 + 1, max_new=2 ** 14, total=2 ** 14), SHAPE)])
 def test_chunk(lib, bad, status):
     assert chunk(lib, **bad) == status
 
