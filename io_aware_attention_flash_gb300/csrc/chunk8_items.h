@@ -47,10 +47,11 @@ FA_CHUNK_FN bool dual(int n, int G, int rb) { return n * G - rb * kRows <= kHalf
 // Runs are counted in units: two for a tile of a dual item, three for another's (its
 // halves' products, of which a dual item's tile is one), and `extra` before an item's
 // first, as many as its fixed cost is (kItemCost; less where a CTA has little more than
-// a tile: every one had better have a CTA of its own).  Measured: a tile takes 1.2 us of
-// a dual item, 1.7 of another; an item 6 to 9.  Sixteen sequences of 1 to 512 new
-// tokens over 100 to 8,192 take 259 us with a cost of 10, 240 with 14, 231 with 18, 233 with 22, 242 with
-// 26; one long document takes the same with all.
+// a tile: every one had better have a CTA of its own).  Measured: a tile takes 1.6 us, of
+// a dual item 1.1, an item 8 (at d = 64: 1.5, 0.8 and 6).  Sixteen sequences of 1 to 512
+// new tokens over 100 to 8,192 take 223 us with a cost of 14, 213 with 18, 219 with 22,
+// 227 with 26 (before the tile pass was shortened 259 with 10, 240 with 14, 231 with 18);
+// one long document takes the same with all.
 constexpr int kMostUnits = 3, kItemCost = 18;
 FA_CHUNK_FN int tile_units(bool dual) { return dual ? 2 : kMostUnits; }
 // CTAs that have a run each, of `most`: a run has as many units as a tile and more, so
