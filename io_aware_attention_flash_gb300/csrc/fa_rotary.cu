@@ -10,8 +10,10 @@
 // Angles.  A frequency is kept as a fraction of a turn in 64-bit fixed point, F =
 // round(frequency / 2 pi · 2^64), so the angle of an integer position is the low 64
 // bits of position · F, whole turns falling off the top: exact but for F's own
-// rounding, 2^31 · 2^-65 turns at the furthest position.  Its upper 32 bits as a
-// signed fraction go to sincospif, which needs no reduction of its argument.  One
+// rounding, 2^31 · 2^-65 turns at the furthest position.  Of its upper 32 bits what
+// lies beside the nearest quarter goes to sincospif, so that the fraction's rounding to
+// fp32 costs the angle 2^-25 at most, no more than the sine's and the cosine's own (a
+// fraction of the whole turn: 2^-23, and some more keys get a neighbouring code).  One
 // sine and cosine serves a token's pair in all heads.
 //
 // Both kernels are bound by DRAM: each element is read once and written once.
@@ -30,8 +32,16 @@ namespace {
 // Cosine and sine of pair j at position pos.
 __device__ __forceinline__ float2 cos_sin(const RotaryParams& r, int j, int pos) {
   const uint64_t turn = r.turns[j] * static_cast<uint64_t>(static_cast<long long>(pos));
+  // the nearest quarter of the turn, and the rest, an eighth at most either way
+  const uint32_t t = static_cast<uint32_t>(turn >> 32), quarter = (t + (1u << 29)) >> 30;
   float s, c;
-  sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &s, &c);
+  sincospif(static_cast<float>(static_cast<int>(t - (quarter << 30))) * 0x1p-31f, &s, &c);
+  if (quarter & 1) {
+    const float x = c;
+    c = -s;
+    s = x;
+  }
+  if (quarter & 2) c = -c, s = -s;
   return make_float2(c, r.inverse ? -s : s);
 }
 
