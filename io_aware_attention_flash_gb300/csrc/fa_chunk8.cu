@@ -654,90 +654,90 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       if (elect_one()) tc_commit(bar(C::B_DRAIN));
       wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
     } else {
-    // ---------------------------------------------------------------- conversion
-    // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32
-    // chunks of consecutive rows, every fifth group of them.  The chunks of a
-    // quarter-warp lie in two rows, at d = 128 in the two halves of them: neither its
-    // reads nor its swizzled writes meet in a bank.
-    const int cw = warp < C::MMA_WARP ? warp - 9 : warp - 10;
-    constexpr int CPR = D / 16, ROWS = 32 / CPR, GROUPS = kKeys / ROWS;
-    int row0, chunk;  // within a group
-    if (D == 128) {
-      const int rb = (lane >> 2) & 1;
-      row0 = ((lane >> 4) & 1) * 2 + rb;
-      chunk = (lane & 3) + 4 * (((lane >> 3) & 1) ^ rb);
-    } else {
-      row0 = lane >> 2;
-      chunk = lane & 3;
-    }
-    const uint32_t in0 = row0 * D + chunk * 16;
-    const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES;
-    auto place = [&](int row, int half) -> uint32_t { return out0 + row * 128 + (((c0 + half) ^ (row & 7)) << 4); };
-    int tile = 0;
-    Ring<C::NC> cr;
-    Ring<C::NV> vr;
-    bool ok = true;
-    auto wait = [&](int i, int phase) {
-      ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      return ok;
-    };
-    Item it;
-    while (ok && take_item(it)) {
-      for (int kt = it.k0; kt < it.k0 + it.tiles; ++kt, ++tile) {
-        const int held = cache8::tokens_from(it.len, kt, kKeys, 0);  // tokens of the tile, if fewer than its rows
-        const int st = cr.i, slot = vr.i;
-        if (!wait(C::B_CFULL + st, cr.phase)) break;
-        if (tile >= C::NV && !wait(C::B_VEMPTY + slot, vr.phase ^ 1)) break;
-        const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES + in0;
-        const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_VF) + st * C::MAX_PPT;
-        uint8_t* out = smem + C::OFF_V + slot * C::TILE_BYTES;
-        // (rolled: beside the softmax's code an unrolled loop costs instruction fetches)
-        uint4 next = *reinterpret_cast<const uint4*>(codes + cw * ROWS * D);
-#pragma unroll 1
-        for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
-          const uint4 now = next;
-          const int row = g * ROWS + row0;
-          const uint32_t f = factors[row >> p.block_shift].x;
-          if (g + C::CONVERT_WARPS < GROUPS)
-            next = *reinterpret_cast<const uint4*>(codes + (g + C::CONVERT_WARPS) * ROWS * D);
-          const uint32_t in[4] = {now.x, now.y, now.z, now.w};
-          uint32_t v[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            widen4(in[k], v[2 * k], v[2 * k + 1]);
-            v[2 * k] = mul_bf16x2(v[2 * k], f);
-            v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f);
-          }
-          *reinterpret_cast<uint4*>(out + place(row, 0)) = make_uint4(v[0], v[1], v[2], v[3]);
-          *reinterpret_cast<uint4*>(out + place(row, 1)) = make_uint4(v[4], v[5], v[6], v[7]);
-        }
-        // Seldom: slots without a token, which may hold anything, become 0; a scale above
-        // 2^55, whose factor does not fit one bf16 number, is a second one.
-        if (held < kKeys || __any_sync(0xffffffffu, factors[lane % C::MAX_PPT].y != kOne2)) {
+      // ---------------------------------------------------------------- conversion
+      // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32
+      // chunks of consecutive rows, every fifth group of them.  The chunks of a
+      // quarter-warp lie in two rows, at d = 128 in the two halves of them: neither its
+      // reads nor its swizzled writes meet in a bank.
+      const int cw = warp < C::MMA_WARP ? warp - 9 : warp - 10;
+      constexpr int CPR = D / 16, ROWS = 32 / CPR, GROUPS = kKeys / ROWS;
+      int row0, chunk;  // within a group
+      if (D == 128) {
+        const int rb = (lane >> 2) & 1;
+        row0 = ((lane >> 4) & 1) * 2 + rb;
+        chunk = (lane & 3) + 4 * (((lane >> 3) & 1) ^ rb);
+      } else {
+        row0 = lane >> 2;
+        chunk = lane & 3;
+      }
+      const uint32_t in0 = row0 * D + chunk * 16;
+      const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES;
+      auto place = [&](int row, int half) -> uint32_t { return out0 + row * 128 + (((c0 + half) ^ (row & 7)) << 4); };
+      int tile = 0;
+      Ring<C::NC> cr;
+      Ring<C::NV> vr;
+      bool ok = true;
+      auto wait = [&](int i, int phase) {
+        ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+      };
+      Item it;
+      while (ok && take_item(it)) {
+        for (int kt = it.k0; kt < it.k0 + it.tiles; ++kt, ++tile) {
+          const int held = cache8::tokens_from(it.len, kt, kKeys, 0);  // tokens of the tile, if fewer than its rows
+          const int st = cr.i, slot = vr.i;
+          if (!wait(C::B_CFULL + st, cr.phase)) break;
+          if (tile >= C::NV && !wait(C::B_VEMPTY + slot, vr.phase ^ 1)) break;
+          const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES + in0;
+          const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_VF) + st * C::MAX_PPT;
+          uint8_t* out = smem + C::OFF_V + slot * C::TILE_BYTES;
+          // (rolled: beside the softmax's code an unrolled loop costs instruction fetches)
+          uint4 next = *reinterpret_cast<const uint4*>(codes + cw * ROWS * D);
 #pragma unroll 1
           for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
+            const uint4 now = next;
             const int row = g * ROWS + row0;
-            const uint32_t f = factors[row >> p.block_shift].y;
+            const uint32_t f = factors[row >> p.block_shift].x;
+            if (g + C::CONVERT_WARPS < GROUPS)
+              next = *reinterpret_cast<const uint4*>(codes + (g + C::CONVERT_WARPS) * ROWS * D);
+            const uint32_t in[4] = {now.x, now.y, now.z, now.w};
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              widen4(in[k], v[2 * k], v[2 * k + 1]);
+              v[2 * k] = mul_bf16x2(v[2 * k], f);
+              v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f);
+            }
+            *reinterpret_cast<uint4*>(out + place(row, 0)) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(out + place(row, 1)) = make_uint4(v[4], v[5], v[6], v[7]);
+          }
+          // Seldom: slots without a token, which may hold anything, become 0; a scale above
+          // 2^55, whose factor does not fit one bf16 number, is a second one.
+          if (held < kKeys || __any_sync(0xffffffffu, factors[lane % C::MAX_PPT].y != kOne2)) {
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              uint4* at = reinterpret_cast<uint4*>(out + place(row, half));
-              const uint4 x = *at;
-              *at = row >= held ? make_uint4(0u, 0u, 0u, 0u)
-                                : make_uint4(mul_bf16x2(x.x, f), mul_bf16x2(x.y, f), mul_bf16x2(x.z, f), mul_bf16x2(x.w, f));
+            for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
+              const int row = g * ROWS + row0;
+              const uint32_t f = factors[row >> p.block_shift].y;
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                uint4* at = reinterpret_cast<uint4*>(out + place(row, half));
+                const uint4 x = *at;
+                *at = row >= held ? make_uint4(0u, 0u, 0u, 0u)
+                                  : make_uint4(mul_bf16x2(x.x, f), mul_bf16x2(x.y, f), mul_bf16x2(x.z, f), mul_bf16x2(x.w, f));
+              }
             }
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::B_CEMPTY + st));
+            mbar_arrive(bar(C::B_VFULL + slot));
+          }
+          cr.step();
+          vr.step();
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(C::B_CEMPTY + st));
-          mbar_arrive(bar(C::B_VFULL + slot));
-        }
-        cr.step();
-        vr.step();
       }
-    }
     }
   } else {
     // ---------------------------------------------------------------- softmax
