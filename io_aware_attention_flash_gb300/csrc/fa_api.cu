@@ -860,7 +860,9 @@ FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void
   FA_TRY(check_rotary(turns, axis, pairs, axes, d));
   FA_TRY(check_heads(total, H, d));
   if (max_new <= 0) return FA_ERR_SHAPE;
-  if (static_cast<long long>(B) * ((static_cast<long long>(max_new) + block - 2) / block + 1) > 0x7fffffffLL) return FA_ERR_SHAPE;
+  // pages that a sequence's new tokens lie in, at most
+  const long long blocks = (static_cast<long long>(max_new < total ? max_new : total) + block - 2) / block + 1;
+  if (B * blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
   if (!q || !k || !v || !q_out || !k_codes || !v_codes || !k_scale || !v_scale || !block_table || !cu_seqlens || !start)
     return FA_ERR_NULL;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_codes) || !aligned16(v_codes))
@@ -887,7 +889,7 @@ FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void
   p.num_blocks = num_blocks;
   p.table_cols = table_cols;
   p.Hk = Hk;
-  p.blocks = static_cast<int>((static_cast<long long>(max_new) + block - 2) / block + 1);
+  p.blocks = static_cast<int>(blocks);
   const fa::RotaryParams r = rotary_params(positions, turns, axis, pairs, axes, interleaved, 0);
   const fa::TurnRows x{static_cast<const uint16_t*>(q), nullptr, ldq, 0, static_cast<uint16_t*>(q_out), nullptr, H, 0};
   const cudaError_t e =

@@ -401,3 +401,23 @@ def test_infinite_and_nan_queries_stay_in_their_rows(new, lens, d):
     o, lse = fa.attention_chunk_cache8(q[:20], cache, table.cuda()[:1], i32([0, 20]), i32([0]), 20, 10, True)
     torch.cuda.synchronize()
     assert not o.any() and (lse == -np.inf).all()
+
+
+def test_capacities_far_above_what_is_there():
+    """max_new and max_seqlen are upper limits: the largest int gives what the tight ones do."""
+    fa = require_gpu()
+    x, cu, start = draw(torch.Generator().manual_seed(12), 150, 12, 64), i32([0, 30, 150]), i32([0, 33])
+    table, plan = i32([[0, 1, 2, 3, 4], [5, 6, 7, 8, 9]]), plan_of(fa, 32)
+    first = random_cache(fa, 10, 2, 32, 64, seed=13)
+    got = []
+    for max_new, max_seqlen in ((120, 153), (2 ** 31 - 1, 2 ** 31 - 1)):
+        cache = fa.Cache8(*[t.clone() for t in first])
+        q = fa.cache8_store_rotary(x[:, :8], x[:, 8:10], x[:, 10:], cache, table, cu, start, max_new, plan)
+        got.append([q, *cache, *fa.attention_chunk_cache8(q, cache, table, cu, i32([30, 153]), max_new, max_seqlen, True)])
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    o = [g.pop(-2) for g in got]  # (tiles may be shared out otherwise: two of the formula's tolerances)
+    lse = [g.pop(-1) for g in got]
+    assert_same(*got)
+    vmax = float((got[0][2].float() * got[0][4][..., None, None]).abs().max())
+    assert float((o[0] - o[1]).abs().max()) <= 2.0 ** -6 * vmax and float((lse[0] - lse[1]).abs().max()) <= 2e-4
