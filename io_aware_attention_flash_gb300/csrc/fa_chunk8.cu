@@ -337,7 +337,408 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     return it.tiles > 0;
   };
 
-  if (warp >= 8) {
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    // (Ahead of the other roles: where its code lies among theirs decides how often its
+    // instructions are fetched again.  Behind them d = 64 takes 3 % longer over drawn sizes,
+    // 197 against 182 us on pieces of prompts of 64 heads; d = 128 1 % less.)
+    setmaxnreg_inc<C::REG_SOFTMAX>();
+    const int t = warp / 4, wq = warp % 4, r = wq * 32 + lane;
+    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+    const uint32_t tS = lane_addr + C::S_COL(t), tO = lane_addr + C::O_COL(t);
+    uint8_t* q_smem = smem + C::OFF_Q + t * C::TILE_BYTES;
+    // A warp moves its 32 rows 16 bytes a lane, RPP rows at a time.
+    constexpr int CH = D / 8, RPP = 32 / CH;
+    const int my_chunk = lane % CH;
+    // Phases of what this half waits for once a tile, an item, a load of Q, a join: one
+    // register (the tile loop has none to spare).
+    uint32_t phases = 0;
+    enum { kTile = 1, kItem = 2, kRaw = 4, kJoin = 8, kRawAhead = 16, kRawEver = 32 };
+    auto phase = [&](uint32_t of) { return (phases & of) ? 1 : 0; };
+    int tile0 = 0;       // tiles of the items before
+    bool ok = true;
+    auto wait = [&](int i, int phase) {
+      ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      return ok;
+    };
+    // An item's fields are read from shared memory where they are needed, which saves the
+    // tile loop their registers.
+    uint32_t item = 0;
+    enum { kHk = 1, kRb, kK0, kTiles, kN, kLen, kTok0, kCnt0, kCnt1, kSlot, kDual };
+    auto field = [&](int i) {
+      int v;
+      asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(item + 4 * i));
+      return v;
+    };
+    // This half's rows of the item: the first, and behind the last.
+    auto first_row = [&]() { return field(kRb) * kRows + (field(kDual) ? 0 : t * kHalf); };
+    auto all_rows = [&]() { return field(kN) * p.G; };
+    // The warp's rows of Q of an item, all in flight at once.  (Loaded through registers in
+    // four batches, each as long as a miss: 5 us an item.)
+    auto load_q = [&]() {
+      const int first = first_row(), from = first + wq * 32, count = max(min(all_rows() - from, 32), 0);
+      const int tok_a = from / p.G, toks = count > 0 ? (from + count - 1) / p.G - tok_a + 1 : 0;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(bar(C::B_RAW + warp), count * (2 * D));
+      __syncwarp();
+      for (int i = lane; i < toks; i += 32) {
+        const int f0 = max((tok_a + i) * p.G, from), f1 = min((tok_a + i + 1) * p.G, from + count);
+        bulk_load(sb + C::OFF_Q + t * C::TILE_BYTES + (f0 - first) * (2 * D),
+                  p.q + static_cast<size_t>(field(kTok0) + tok_a + i) * p.ldq +
+                      (static_cast<size_t>(field(kHk)) * p.G + f0 - (tok_a + i) * p.G) * D,
+                  (f1 - f0) * (2 * D), bar(C::B_RAW + warp));
+      }
+      phases |= kRawEver;
+    };
+    auto take = [&]() {
+      const int cnt = field(kCnt0 + t);
+      const int first_tile = tile0;
+      tile0 += field(kTiles);
+      if (first_row() >= all_rows()) return;
+      float m_ref = -CUDART_INF_F, l = 0.f;
+      // (of the warp) some reference so large that a product's rounding, 2^-24 of it,
+      // counts in the exponent
+      bool far = false;
+      if (cnt > 0) {
+        // ---- Q: each row scaled by a power of two, as two e4m3 terms, in place: 8 rows'
+        // terms take the room of the rows
+        if (!(phases & kRawAhead)) load_q();  // (else they are on their way already)
+        phases &= ~kRawAhead;
+        const bool landed = wait(C::B_RAW + warp, phase(kRaw));
+        phases ^= kRaw;
+        if (!landed) return;
+        const int first = first_row(), rows = all_rows();
+        // (rolled: run through once an item, unrolled code is all instruction fetches)
+        int my_e = 0;  // the exponent of this thread's row
+#pragma unroll 1
+        for (int r8 = 0; r8 < 32; r8 += 8) {
+          constexpr int NB = 8 / RPP;
+          uint8_t* rows8 = q_smem + (wq * 32 + r8) * (2 * D);
+          uint4 x[NB];
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const int row = i * RPP + lane / CH;
+            x[i] = *reinterpret_cast<const uint4*>(rows8 + row * (2 * D) + 16 * my_chunk);
+            if (first + wq * 32 + r8 + row >= rows) x[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t top = 0;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) top = __vmaxu2(top, w[u] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+            for (int off = CH / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+            // smallest power of two s with max <= 448 s, for any finite row: 2^120 at
+            // most, at least 2^-126 (fp32's smallest that is not subnormal)
+            const int e = min(scale_exponent(top, -126), 120);
+            const int of_row = __shfl_sync(0xffffffffu, e, lane % RPP * CH);
+            if (lane / RPP == r8 / RPP + i) my_e = of_row;
+            // (infinities, which e4m3 has not, make the row NaN as a whole)
+            const float inv = top < 0x7f80u ? exp2_int(-e) : CUDART_NAN_F;
+            // (through f16, which holds the scaled values exactly down to 2^-14)
+            const uint64_t inv2 = f2_pack(inv, inv);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t h[2], back[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float a, b;
+                f2_unpack(fmul2(f2_pack(bf16lo_to_f32(w[2 * u + k]), bf16hi_to_f32(w[2 * u + k])), inv2), a, b);
+                h[k] = pack_f16x2(a, b);
+              }
+              hi[u] = e4m3x4_of_f16(h[0], h[1]);
+              f16_of_e4m3x4(hi[u], back[0], back[1]);
+              lo[u] = e4m3x4_of_f16(sub_f16x2(h[0], back[0]), sub_f16x2(h[1], back[1]));
+            }
+            uint8_t* at = rows8 + swz<D>(i * RPP + lane / CH, 8 * my_chunk);
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + 8 * D) = make_uint2(lo[0], lo[1]);
+          }
+        }
+        const float c_row = exp2_int(my_e) * p.scale_log2;
+        fence_proxy_async_smem();
+        mbar_arrive(bar(C::B_Q + t));
+        // This half's tiles: every one, or every other.  Keys, from the next tile's first, that
+        // the row sees, and that the half's first row does (which sees the fewest).
+        const int stride = field(kDual) ? 2 : 1, at = field(kDual) ? t : 0;
+        const int kv0 = (field(kK0) + at) * kKeys;  // (of a first tile behind the last: not used)
+        int sees = (first + r < rows ? chunk8::visible(field(kLen), field(kN), (first + r) / p.G, p.causal) : 0) - kv0;
+        int all_see = chunk8::visible(field(kLen), field(kN), first / p.G, p.causal) - kv0;
+        Ring<C::NSC> scr;  // the next tile's place among K's scales
+        scr.i = (first_tile + at) % C::NSC, scr.phase = (first_tile + at) / C::NSC & 1;
+        for (int j = 0; j < cnt; ++j) {
+          // the columns' factors: K's scale of each 16 keys, the row's and the softmax's
+          // (not below fp32's least normal number: a masked column stays -infinity)
+          const int sc = scr.i;
+          if (!wait(C::B_SCFULL + sc, scr.phase)) break;
+          scr.step(stride);
+          const uint32_t k_scale = sb + C::OFF_KS + sc * (C::MAX_PPT * 4);
+          float cf[8];
+#pragma unroll
+          for (int g16 = 0; g16 < 8; ++g16) {
+            float v;
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(k_scale + (((16 * g16) >> p.block_shift) << 2)));
+            cf[g16] = fmaxf(v * c_row, 0x1p-126f);
+          }
+          if (!wait(C::B_SFULL + t, phase(kTile))) break;
+          phases ^= kTile;
+          tc_fence_after();
+          // The first tile, whose largest score is the reference, and those that a row does not
+          // see all of, which are masked in place.  (Rolled, run through a few times an item: the
+          // same on the registers below is code that every tile jumps over, which its own
+          // instructions' fetch waits for.  239 against 213 us on 16 mixed sequences.)
+          if (j == 0 || all_see < kKeys) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t x[16];
+              tmem_ld16(tS + 16 * c, x);
+              tmem_wait_ld();
+              reg_fence(x);
+              if (all_see < 16 * c + 16) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (i >= sees - 16 * c) x[i] = __float_as_uint(-CUDART_INF_F);
+                tmem_st16(tS + 16 * c, x);
+              }
+              if (j == 0) {
+                float v, mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(k_scale + (((16 * c) >> p.block_shift) << 2)));
+#pragma unroll
+                for (int i = 1; i < 8; ++i) mx[i & 1] = fmax3(mx[i & 1], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                m_ref = fmaxf(m_ref, fmaxf(mx[0], mx[1]) * fmaxf(v * c_row, 0x1p-126f));
+              }
+            }
+            tmem_wait_st();
+          }
+          uint32_t s[4][32];
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) tmem_ld32(tS + ch * 32, s[ch]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) reg_fence(s[ch]);
+          // The largest y = s · factor of the row.
+          auto row_max = [&]() -> float {
+            float m = -CUDART_INF_F;
+#pragma unroll
+            for (int g16 = 0; g16 < 8; ++g16) {
+              const uint32_t* x = s[g16 / 2] + 16 * (g16 % 2);
+              float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+#pragma unroll
+              for (int i = 1; i < 8; ++i) mx[i & 1] = fmax3(mx[i & 1], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+              m = fmaxf(m, fmaxf(mx[0], mx[1]) * cf[g16]);
+            }
+            return m;
+          };
+          // P = 2^(y − m_ref) as bf16 over S; returns the tile's row sum.
+          auto p_pass = [&]() -> float {
+            const float m = m_ref == -CUDART_INF_F ? 0.f : m_ref;
+            const uint64_t nm2 = f2_pack(-m, -m);
+            uint64_t cf2[8];
+#pragma unroll
+            for (int g16 = 0; g16 < 8; ++g16) cf2[g16] = f2_pack(cf[g16], cf[g16]);
+            uint64_t ls2[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ls2[k] = f2_pack(0.f, 0.f);
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float x0, x1;
+                f2_unpack(ffma2(f2_pack(__uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1])),
+                                cf2[2 * ch + e / 8], nm2),
+                          x0, x1);
+                const float p0 = ex2_approx(x0);
+                const float p1 = ex2_approx(x1);
+                ls2[e & 3] = fadd2(ls2[e & 3], f2_pack(p0, p1));
+                pk[e] = pack_bf16x2(p0, p1);
+              }
+              tmem_st16(tS + ch * 16, pk);
+            }
+            float ls[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f2_unpack(ls2[k], ls[2 * k], ls[2 * k + 1]);
+            return ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
+          };
+          auto set_far = [&]() {
+            far = __any_sync(0xffffffffu, m_ref != -CUDART_INF_F && !(fabsf(m_ref) < 0x1p20f));
+          };
+          // Far references: y is formed before the reference is taken off, so that the
+          // largest of the row comes to 0 exactly.
+          auto form_y = [&]() {
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[ch][i] = __float_as_uint(__uint_as_float(s[ch][i]) * cf[2 * ch + i / 16]);
+#pragma unroll
+            for (int g16 = 0; g16 < 8; ++g16) cf[g16] = 1.f;
+          };
+          if (j == 0) set_far();
+          float lt;
+#pragma unroll 1
+          for (bool moved = false;; moved = true) {  // (one copy of the pass in the code)
+            if (far) form_y();
+            lt = p_pass();
+            if (moved || !__any_sync(0xffffffffu, !(lt < 0x1p40f))) break;
+            const float m_new = fmaxf(m_ref, row_max());
+            const float alpha = (m_ref == -CUDART_INF_F) ? 0.f : ex2_approx(m_ref - m_new);
+            m_ref = m_new;
+            l *= alpha;
+            set_far();
+#pragma unroll 1
+            for (int ch = 0; j > 0 && ch < D / 16; ++ch) {
+              uint32_t o[16];
+              tmem_ld16(tO + ch * 16, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + ch * 16, o);
+            }
+            tmem_wait_st();
+          }
+          l += lt;
+          sees -= stride * kKeys;
+          all_see -= stride * kKeys;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(C::B_PFULL + t));
+        }
+        // Q's place is free: the next item's, if that is known
+        if (const int i = (items + 1) % C::NI;
+            ok && __all_sync(0xffffffffu, mbar_test_wait(bar(C::B_IFULL + i), (items + 1) / C::NI & 1))) {
+          const uint32_t now = item;
+          item = sb + C::OFF_ITEM + i * C::ITEM_INTS * 4;
+          if (field(kTiles) > 0 && field(kCnt0 + t) > 0 && first_row() < all_rows()) {
+            load_q();
+            phases |= kRawAhead;
+          }
+          item = now;
+        }
+        if (!ok || !wait(C::B_ODONE + t, phase(kItem))) return;
+        phases ^= kItem;
+        tc_fence_after();
+      }
+      // ---- a dual item: the first half's warps, which have the same lanes of tensor memory,
+      // take the second half's O with their own; m and l go through its columns of S
+      const bool join = field(kDual) && field(kCnt1) > 0;
+      float join0 = 1.f, join1 = 0.f;  // factors of the halves' O
+      if (join) {
+        uint32_t ml[16];
+        const uint32_t tM = lane_addr + C::S_COL(1);
+        if (t == 1) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) ml[i] = __float_as_uint(i == 0 ? m_ref : l);
+          tmem_st16(tM, ml);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(bar(C::B_JOIN));
+          if (wait(C::B_JOIN + 1, phase(kJoin))) tc_fence_after();
+          phases ^= kJoin;
+          return;
+        }
+        if (!wait(C::B_JOIN, phase(kJoin))) return;
+        phases ^= kJoin;
+        tc_fence_after();
+        tmem_ld16(tM, ml);
+        tmem_wait_ld();
+        reg_fence(ml);
+        const float m1 = __uint_as_float(ml[0]), m = fmaxf(m_ref, m1);
+        join0 = m_ref == -CUDART_INF_F ? 0.f : ex2_approx(m_ref - m);
+        join1 = m1 == -CUDART_INF_F ? 0.f : ex2_approx(m1 - m);
+        l = fmaf(__uint_as_float(ml[1]), join1, l * join0);
+        m_ref = m;
+      } else if (field(kDual) && t == 1) {
+        return;
+      }
+      const int first = first_row(), rows = all_rows(), hk = field(kHk), tok0 = field(kTok0), slot = field(kSlot);
+      const bool exists = first + r < rows;
+      const int tok = (first + r) / p.G, g = first + r - tok * p.G;
+      auto load_o = [&](int c0, uint32_t (&o)[32]) {  // 32 columns of O
+        tmem_ld32(tO + c0, o);
+        if (join) {
+          uint32_t o1[32];
+          tmem_ld32(lane_addr + C::O_COL(1) + c0, o1);
+          tmem_wait_ld();
+          reg_fence(o);
+          reg_fence(o1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), join0, __uint_as_float(o1[i]) * join1));
+        } else {
+          tmem_wait_ld();
+          reg_fence(o);
+        }
+      };
+      const size_t part = static_cast<size_t>(slot < 0 ? 0 : slot) * kRows + t * kHalf + r;
+      if (slot < 0) {
+        // ---- O / l, row by row (staged for whole lines it would take Q's place, which the
+        // next item's rows are on their way to)
+        const float inv_l = l == 0.f ? 0.f : exp2_int(kVShift) / l;
+        uint4* dst = reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(tok0 + tok) * p.H + hk * p.G + g) * D);
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          load_o(cb * 32, o);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {  // a 16-byte chunk; its dimensions change places again
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t* q4 = o + 8 * u + 4 * e;
+              w[2 * e] = pack_bf16x2(__uint_as_float(q4[0]) * inv_l, __uint_as_float(q4[2]) * inv_l);
+              w[2 * e + 1] = pack_bf16x2(__uint_as_float(q4[1]) * inv_l, __uint_as_float(q4[3]) * inv_l);
+            }
+            if (exists) dst[cb * 4 + u] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        tc_fence_before();
+        if (exists)
+          p.lse[static_cast<size_t>(hk * p.G + g) * p.total + tok0 + tok] =
+              l == 0.f ? -CUDART_INF_F : (m_ref + log2f(l)) * kLn2;
+      } else if (exists) {
+        reinterpret_cast<float2*>(p.ml_part)[part] = make_float2(l == 0.f ? -CUDART_INF_F : l > 0.f ? m_ref : l, l);  // (NaN: both)
+      }
+      if (slot >= 0 && cnt > 0) {
+        // ---- a partial: four dimensions of 32 rows side by side
+        float4* dst = reinterpret_cast<float4*>(p.o_part) + static_cast<size_t>(slot) * (kRows * D / 4) + t * kHalf + r;
+#pragma unroll 1
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t o[32];
+          load_o(cb * 32, o);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (exists)
+              dst[(cb * 8 + u) * kRows] = make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 2]),
+                                                      __uint_as_float(o[4 * u + 1]), __uint_as_float(o[4 * u + 3]));
+        }
+        tc_fence_before();
+      }
+      if (join) {
+        tc_fence_before();
+        mbar_arrive(bar(C::B_JOIN + 1));
+      }
+    };
+    while (ok) {
+      const int i = items % C::NI;
+      if (!wait(C::B_IFULL + i, items / C::NI)) break;
+      item = sb + C::OFF_ITEM + i * C::ITEM_INTS * 4;
+      const bool any = field(kTiles) > 0;
+      if (any) take();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::B_IEMPTY + i));
+      ++items;
+      if (!any) break;
+    }
+    // A copy issued lands before the CTA may exit, whoever aborted.
+    if (phases & kRawEver) wait_drain(bar(C::B_RAW + warp), phase(kRaw) ^ ((phases & kRawAhead) ? 0 : 1), p.err, p.timeout_ns);
+  } else {
     setmaxnreg_dec<C::REG_OTHER>();
     if (warp == C::COPY_WARP) {
       // ------------------------------------------------------------ items, copies
@@ -739,404 +1140,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         }
       }
     }
-  } else {
-    // ---------------------------------------------------------------- softmax
-    setmaxnreg_inc<C::REG_SOFTMAX>();
-    const int t = warp / 4, wq = warp % 4, r = wq * 32 + lane;
-    const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-    const uint32_t tS = lane_addr + C::S_COL(t), tO = lane_addr + C::O_COL(t);
-    uint8_t* q_smem = smem + C::OFF_Q + t * C::TILE_BYTES;
-    // A warp moves its 32 rows 16 bytes a lane, RPP rows at a time.
-    constexpr int CH = D / 8, RPP = 32 / CH;
-    const int my_chunk = lane % CH;
-    // Phases of what this half waits for once a tile, an item, a load of Q, a join: one
-    // register (the tile loop has none to spare).
-    uint32_t phases = 0;
-    enum { kTile = 1, kItem = 2, kRaw = 4, kJoin = 8, kRawAhead = 16, kRawEver = 32 };
-    auto phase = [&](uint32_t of) { return (phases & of) ? 1 : 0; };
-    int tile0 = 0;       // tiles of the items before
-    bool ok = true;
-    auto wait = [&](int i, int phase) {
-      ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
-      ok = __all_sync(0xffffffffu, ok);
-      return ok;
-    };
-    // An item's fields are read from shared memory where they are needed, which saves the
-    // tile loop their registers.
-    uint32_t item = 0;
-    enum { kHk = 1, kRb, kK0, kTiles, kN, kLen, kTok0, kCnt0, kCnt1, kSlot, kDual };
-    auto field = [&](int i) {
-      int v;
-      asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(item + 4 * i));
-      return v;
-    };
-    // This half's rows of the item: the first, and behind the last.
-    auto first_row = [&]() { return field(kRb) * kRows + (field(kDual) ? 0 : t * kHalf); };
-    auto all_rows = [&]() { return field(kN) * p.G; };
-    // The warp's rows of Q of an item, all in flight at once.  (Loaded through registers in
-    // four batches, each as long as a miss: 5 us an item.)
-    auto load_q = [&]() {
-      const int first = first_row(), from = first + wq * 32, count = max(min(all_rows() - from, 32), 0);
-      const int tok_a = from / p.G, toks = count > 0 ? (from + count - 1) / p.G - tok_a + 1 : 0;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(bar(C::B_RAW + warp), count * (2 * D));
-      __syncwarp();
-      for (int i = lane; i < toks; i += 32) {
-        const int f0 = max((tok_a + i) * p.G, from), f1 = min((tok_a + i + 1) * p.G, from + count);
-        bulk_load(sb + C::OFF_Q + t * C::TILE_BYTES + (f0 - first) * (2 * D),
-                  p.q + static_cast<size_t>(field(kTok0) + tok_a + i) * p.ldq +
-                      (static_cast<size_t>(field(kHk)) * p.G + f0 - (tok_a + i) * p.G) * D,
-                  (f1 - f0) * (2 * D), bar(C::B_RAW + warp));
-      }
-      phases |= kRawEver;
-    };
-    auto take = [&]() {
-      const int cnt = field(kCnt0 + t);
-      const int first_tile = tile0;
-      tile0 += field(kTiles);
-      if (first_row() >= all_rows()) return;
-      float m_ref = -CUDART_INF_F, l = 0.f;
-      // (of the warp) some reference so large that a product's rounding, 2^-24 of it,
-      // counts in the exponent
-      bool far = false;
-      if (cnt > 0) {
-        // ---- Q: each row scaled by a power of two, as two e4m3 terms, in place: 8 rows'
-        // terms take the room of the rows
-        if (!(phases & kRawAhead)) load_q();  // (else they are on their way already)
-        phases &= ~kRawAhead;
-        const bool landed = wait(C::B_RAW + warp, phase(kRaw));
-        phases ^= kRaw;
-        if (!landed) return;
-        const int first = first_row(), rows = all_rows();
-        // (rolled: run through once an item, unrolled code is all instruction fetches)
-        int my_e = 0;  // the exponent of this thread's row
-#pragma unroll 1
-        for (int r8 = 0; r8 < 32; r8 += 8) {
-          constexpr int NB = 8 / RPP;
-          uint8_t* rows8 = q_smem + (wq * 32 + r8) * (2 * D);
-          uint4 x[NB];
-#pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const int row = i * RPP + lane / CH;
-            x[i] = *reinterpret_cast<const uint4*>(rows8 + row * (2 * D) + 16 * my_chunk);
-            if (first + wq * 32 + r8 + row >= rows) x[i] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t top = 0;
-#pragma unroll
-            for (int u = 0; u < 4; ++u) top = __vmaxu2(top, w[u] & 0x7fff7fffu);
-            top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-            for (int off = CH / 2; off > 0; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-            // smallest power of two s with max <= 448 s, for any finite row: 2^120 at
-            // most, at least 2^-126 (fp32's smallest that is not subnormal)
-            const int e = min(scale_exponent(top, -126), 120);
-            const int of_row = __shfl_sync(0xffffffffu, e, lane % RPP * CH);
-            if (lane / RPP == r8 / RPP + i) my_e = of_row;
-            // (infinities, which e4m3 has not, make the row NaN as a whole)
-            const float inv = top < 0x7f80u ? exp2_int(-e) : CUDART_NAN_F;
-            // (through f16, which holds the scaled values exactly down to 2^-14)
-            const uint64_t inv2 = f2_pack(inv, inv);
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t h[2], back[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float a, b;
-                f2_unpack(fmul2(f2_pack(bf16lo_to_f32(w[2 * u + k]), bf16hi_to_f32(w[2 * u + k])), inv2), a, b);
-                h[k] = pack_f16x2(a, b);
-              }
-              hi[u] = e4m3x4_of_f16(h[0], h[1]);
-              f16_of_e4m3x4(hi[u], back[0], back[1]);
-              lo[u] = e4m3x4_of_f16(sub_f16x2(h[0], back[0]), sub_f16x2(h[1], back[1]));
-            }
-            uint8_t* at = rows8 + swz<D>(i * RPP + lane / CH, 8 * my_chunk);
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(at + 8 * D) = make_uint2(lo[0], lo[1]);
-          }
-        }
-        const float c_row = exp2_int(my_e) * p.scale_log2;
-        fence_proxy_async_smem();
-        mbar_arrive(bar(C::B_Q + t));
-        // This half's tiles: every one, or every other.  Keys, from the next tile's first, that
-        // the row sees, and that the half's first row does (which sees the fewest).
-        const int stride = field(kDual) ? 2 : 1, at = field(kDual) ? t : 0;
-        const int kv0 = (field(kK0) + at) * kKeys;  // (of a first tile behind the last: not used)
-        int sees = (first + r < rows ? chunk8::visible(field(kLen), field(kN), (first + r) / p.G, p.causal) : 0) - kv0;
-        int all_see = chunk8::visible(field(kLen), field(kN), first / p.G, p.causal) - kv0;
-        Ring<C::NSC> scr;  // the next tile's place among K's scales
-        scr.i = (first_tile + at) % C::NSC, scr.phase = (first_tile + at) / C::NSC & 1;
-        for (int j = 0; j < cnt; ++j) {
-          // the columns' factors: K's scale of each 16 keys, the row's and the softmax's
-          // (not below fp32's least normal number: a masked column stays -infinity)
-          const int sc = scr.i;
-          if (!wait(C::B_SCFULL + sc, scr.phase)) break;
-          scr.step(stride);
-          const uint32_t k_scale = sb + C::OFF_KS + sc * (C::MAX_PPT * 4);
-          float cf[8];
-#pragma unroll
-          for (int g16 = 0; g16 < 8; ++g16) {
-            float v;
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(k_scale + (((16 * g16) >> p.block_shift) << 2)));
-            cf[g16] = fmaxf(v * c_row, 0x1p-126f);
-          }
-          if (!wait(C::B_SFULL + t, phase(kTile))) break;
-          phases ^= kTile;
-          tc_fence_after();
-          // The first tile, whose largest score is the reference, and those that a row does not
-          // see all of, which are masked in place.  (Rolled, run through a few times an item: the
-          // same on the registers below is code that every tile jumps over, which its own
-          // instructions' fetch waits for.  239 against 213 us on 16 mixed sequences.)
-          if (j == 0 || all_see < kKeys) {
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t x[16];
-              tmem_ld16(tS + 16 * c, x);
-              tmem_wait_ld();
-              reg_fence(x);
-              if (all_see < 16 * c + 16) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (i >= sees - 16 * c) x[i] = __float_as_uint(-CUDART_INF_F);
-                tmem_st16(tS + 16 * c, x);
-              }
-              if (j == 0) {
-                float v, mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(k_scale + (((16 * c) >> p.block_shift) << 2)));
-#pragma unroll
-                for (int i = 1; i < 8; ++i) mx[i & 1] = fmax3(mx[i & 1], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-                m_ref = fmaxf(m_ref, fmaxf(mx[0], mx[1]) * fmaxf(v * c_row, 0x1p-126f));
-              }
-            }
-            tmem_wait_st();
-          }
-          uint32_t s[4][32];
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) tmem_ld32(tS + ch * 32, s[ch]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int ch = 0; ch < 4; ++ch) reg_fence(s[ch]);
-          // The largest y = s · factor of the row.
-          auto row_max = [&]() -> float {
-            float m = -CUDART_INF_F;
-#pragma unroll
-            for (int g16 = 0; g16 < 8; ++g16) {
-              const uint32_t* x = s[g16 / 2] + 16 * (g16 % 2);
-              float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[1])};
-#pragma unroll
-              for (int i = 1; i < 8; ++i) mx[i & 1] = fmax3(mx[i & 1], __uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-              m = fmaxf(m, fmaxf(mx[0], mx[1]) * cf[g16]);
-            }
-            return m;
-          };
-          // P = 2^(y − m_ref) as bf16 over S; returns the tile's row sum.
-          auto p_pass = [&]() -> float {
-            const float m = m_ref == -CUDART_INF_F ? 0.f : m_ref;
-            const uint64_t nm2 = f2_pack(-m, -m);
-            uint64_t cf2[8];
-#pragma unroll
-            for (int g16 = 0; g16 < 8; ++g16) cf2[g16] = f2_pack(cf[g16], cf[g16]);
-            uint64_t ls2[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) ls2[k] = f2_pack(0.f, 0.f);
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float x0, x1;
-                f2_unpack(ffma2(f2_pack(__uint_as_float(s[ch][2 * e]), __uint_as_float(s[ch][2 * e + 1])),
-                                cf2[2 * ch + e / 8], nm2),
-                          x0, x1);
-                const float p0 = ex2_approx(x0);
-                const float p1 = ex2_approx(x1);
-                ls2[e & 3] = fadd2(ls2[e & 3], f2_pack(p0, p1));
-                pk[e] = pack_bf16x2(p0, p1);
-              }
-              tmem_st16(tS + ch * 16, pk);
-            }
-            float ls[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) f2_unpack(ls2[k], ls[2 * k], ls[2 * k + 1]);
-            return ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
-          };
-          auto set_far = [&]() {
-            far = __any_sync(0xffffffffu, m_ref != -CUDART_INF_F && !(fabsf(m_ref) < 0x1p20f));
-          };
-          // Far references: y is formed before the reference is taken off, so that the
-          // largest of the row comes to 0 exactly.
-          auto form_y = [&]() {
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) s[ch][i] = __float_as_uint(__uint_as_float(s[ch][i]) * cf[2 * ch + i / 16]);
-#pragma unroll
-            for (int g16 = 0; g16 < 8; ++g16) cf[g16] = 1.f;
-          };
-          if (j == 0) set_far();
-          float lt;
-#pragma unroll 1
-          for (bool moved = false;; moved = true) {  // (one copy of the pass in the code)
-            if (far) form_y();
-            lt = p_pass();
-            if (moved || !__any_sync(0xffffffffu, !(lt < 0x1p40f))) break;
-            const float m_new = fmaxf(m_ref, row_max());
-            const float alpha = (m_ref == -CUDART_INF_F) ? 0.f : ex2_approx(m_ref - m_new);
-            m_ref = m_new;
-            l *= alpha;
-            set_far();
-#pragma unroll 1
-            for (int ch = 0; j > 0 && ch < D / 16; ++ch) {
-              uint32_t o[16];
-              tmem_ld16(tO + ch * 16, o);
-              tmem_wait_ld();
-              reg_fence(o);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st16(tO + ch * 16, o);
-            }
-            tmem_wait_st();
-          }
-          l += lt;
-          sees -= stride * kKeys;
-          all_see -= stride * kKeys;
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(C::B_PFULL + t));
-        }
-        // Q's place is free: the next item's, if that is known
-        if (const int i = (items + 1) % C::NI;
-            ok && __all_sync(0xffffffffu, mbar_test_wait(bar(C::B_IFULL + i), (items + 1) / C::NI & 1))) {
-          const uint32_t now = item;
-          item = sb + C::OFF_ITEM + i * C::ITEM_INTS * 4;
-          if (field(kTiles) > 0 && field(kCnt0 + t) > 0 && first_row() < all_rows()) {
-            load_q();
-            phases |= kRawAhead;
-          }
-          item = now;
-        }
-        if (!ok || !wait(C::B_ODONE + t, phase(kItem))) return;
-        phases ^= kItem;
-        tc_fence_after();
-      }
-      // ---- a dual item: the first half's warps, which have the same lanes of tensor memory,
-      // take the second half's O with their own; m and l go through its columns of S
-      const bool join = field(kDual) && field(kCnt1) > 0;
-      float join0 = 1.f, join1 = 0.f;  // factors of the halves' O
-      if (join) {
-        uint32_t ml[16];
-        const uint32_t tM = lane_addr + C::S_COL(1);
-        if (t == 1) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) ml[i] = __float_as_uint(i == 0 ? m_ref : l);
-          tmem_st16(tM, ml);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(bar(C::B_JOIN));
-          if (wait(C::B_JOIN + 1, phase(kJoin))) tc_fence_after();
-          phases ^= kJoin;
-          return;
-        }
-        if (!wait(C::B_JOIN, phase(kJoin))) return;
-        phases ^= kJoin;
-        tc_fence_after();
-        tmem_ld16(tM, ml);
-        tmem_wait_ld();
-        reg_fence(ml);
-        const float m1 = __uint_as_float(ml[0]), m = fmaxf(m_ref, m1);
-        join0 = m_ref == -CUDART_INF_F ? 0.f : ex2_approx(m_ref - m);
-        join1 = m1 == -CUDART_INF_F ? 0.f : ex2_approx(m1 - m);
-        l = fmaf(__uint_as_float(ml[1]), join1, l * join0);
-        m_ref = m;
-      } else if (field(kDual) && t == 1) {
-        return;
-      }
-      const int first = first_row(), rows = all_rows(), hk = field(kHk), tok0 = field(kTok0), slot = field(kSlot);
-      const bool exists = first + r < rows;
-      const int tok = (first + r) / p.G, g = first + r - tok * p.G;
-      auto load_o = [&](int c0, uint32_t (&o)[32]) {  // 32 columns of O
-        tmem_ld32(tO + c0, o);
-        if (join) {
-          uint32_t o1[32];
-          tmem_ld32(lane_addr + C::O_COL(1) + c0, o1);
-          tmem_wait_ld();
-          reg_fence(o);
-          reg_fence(o1);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            o[i] = __float_as_uint(fmaf(__uint_as_float(o[i]), join0, __uint_as_float(o1[i]) * join1));
-        } else {
-          tmem_wait_ld();
-          reg_fence(o);
-        }
-      };
-      const size_t part = static_cast<size_t>(slot < 0 ? 0 : slot) * kRows + t * kHalf + r;
-      if (slot < 0) {
-        // ---- O / l, row by row (staged for whole lines it would take Q's place, which the
-        // next item's rows are on their way to)
-        const float inv_l = l == 0.f ? 0.f : exp2_int(kVShift) / l;
-        uint4* dst = reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(tok0 + tok) * p.H + hk * p.G + g) * D);
-#pragma unroll 1
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t o[32];
-          load_o(cb * 32, o);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {  // a 16-byte chunk; its dimensions change places again
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t* q4 = o + 8 * u + 4 * e;
-              w[2 * e] = pack_bf16x2(__uint_as_float(q4[0]) * inv_l, __uint_as_float(q4[2]) * inv_l);
-              w[2 * e + 1] = pack_bf16x2(__uint_as_float(q4[1]) * inv_l, __uint_as_float(q4[3]) * inv_l);
-            }
-            if (exists) dst[cb * 4 + u] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        tc_fence_before();
-        if (exists)
-          p.lse[static_cast<size_t>(hk * p.G + g) * p.total + tok0 + tok] =
-              l == 0.f ? -CUDART_INF_F : (m_ref + log2f(l)) * kLn2;
-      } else if (exists) {
-        reinterpret_cast<float2*>(p.ml_part)[part] = make_float2(l == 0.f ? -CUDART_INF_F : l > 0.f ? m_ref : l, l);  // (NaN: both)
-      }
-      if (slot >= 0 && cnt > 0) {
-        // ---- a partial: four dimensions of 32 rows side by side
-        float4* dst = reinterpret_cast<float4*>(p.o_part) + static_cast<size_t>(slot) * (kRows * D / 4) + t * kHalf + r;
-#pragma unroll 1
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t o[32];
-          load_o(cb * 32, o);
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            if (exists)
-              dst[(cb * 8 + u) * kRows] = make_float4(__uint_as_float(o[4 * u]), __uint_as_float(o[4 * u + 2]),
-                                                      __uint_as_float(o[4 * u + 1]), __uint_as_float(o[4 * u + 3]));
-        }
-        tc_fence_before();
-      }
-      if (join) {
-        tc_fence_before();
-        mbar_arrive(bar(C::B_JOIN + 1));
-      }
-    };
-    while (ok) {
-      const int i = items % C::NI;
-      if (!wait(C::B_IFULL + i, items / C::NI)) break;
-      item = sb + C::OFF_ITEM + i * C::ITEM_INTS * 4;
-      const bool any = field(kTiles) > 0;
-      if (any) take();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::B_IEMPTY + i));
-      ++items;
-      if (!any) break;
-    }
-    // A copy issued lands before the CTA may exit, whoever aborted.
-    if (phases & kRawEver) wait_drain(bar(C::B_RAW + warp), phase(kRaw) ^ ((phases & kRawAhead) ? 0 : 1), p.err, p.timeout_ns);
   }
 
   tc_fence_before();
