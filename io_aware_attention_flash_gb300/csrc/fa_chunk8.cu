@@ -98,6 +98,12 @@ struct ChunkCfg {
   // Registers a thread after the split; launched with 128.
   static constexpr int REG_SOFTMAX = 192, REG_OTHER = 64;
   static_assert(2 * REG_SOFTMAX + 2 * REG_OTHER == 4 * 128, "the split takes what the launch gives");
+  // How far the MMA warp's loops over the halves and the steps of P V are unrolled: at d = 64
+  // not at all, since the code that each scheduler fetches counts for more than the issue
+  // of these small products (2 to 3 % over drawn sizes each); at d = 128 rolled steps cost
+  // 703 -> 763 us on a long document, rolled halves 0.8 %.  Of dual items the halves' loop is
+  // rolled for both (1 % over drawn sizes).
+  static constexpr int HALF_UNROLL = D == 64 ? 1 : 2, PV_UNROLL = D == 64 ? 1 : kKeys / 16;
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t S_COL(int t) { return t * 128; }
   __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256 + t * D; }
@@ -955,10 +961,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       };
       auto issue_pv = [&](int t, int vs, bool acc) {
         const uint64_t dV = sdesc_add(dV0, vs * C::TILE_BYTES);
-        // (d = 64: rolled, since the code that each scheduler fetches counts for more than the
-        // issue of these small products: 203 against 195 us on pieces of prompts of 64 heads, 3 %
-        // over drawn sizes; at d = 128 it costs 703 -> 763 us on a long document)
-#pragma unroll(D == 64 ? 1 : kKeys / 16)
+#pragma unroll(C::PV_UNROLL)
         for (int kk = 0; kk < kKeys / 16; ++kk)
           mma_ts(tm + C::O_COL(t), tm + C::S_COL(t) + kk * 8, sdesc_add(dV, kk * 2048), idesc_o,
                  (acc || kk > 0) ? 1u : 0u);
@@ -971,7 +974,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       };
       Ring<C::NK> kr;                        // the next tile of K, of V
       Ring<C::NV> vr;
-      int nq[2] = {0, 0}, np[2] = {0, 0};    // items and P tiles of each half so far
+      uint32_t half_phases = 0;  // bit t: of half t's items, bit 2 + t: of its P tiles
+      auto wait_half = [&](int b, int t, int bit) {
+        const int ph = (half_phases >> (bit + t)) & 1;
+        half_phases ^= 1u << (bit + t);
+        return wait(b + t, ph);
+      };
       auto wait_k = [&]() { return wait(C::B_KFULL + kr.i, kr.phase); };
       auto wait_v = [&]() { return wait(C::B_VFULL + vr.i, vr.phase); };
       auto take_s = [&](int t, bool free_k) {  // S of half t over the K that is next
@@ -985,29 +993,30 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       Item it;
       while (ok && take_item(it)) {
         const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
-        const int cnt[2] = {__shfl_sync(0xffffffffu, it.cnt0, 0), __shfl_sync(0xffffffffu, it.cnt1, 0)};
+        const int cnt0 = __shfl_sync(0xffffffffu, it.cnt0, 0), cnt1 = __shfl_sync(0xffffffffu, it.cnt1, 0);
+        auto cnt = [&](int t) { return t ? cnt1 : cnt0; };
         if (__shfl_sync(0xffffffffu, it.dual ? 1 : 0, 0) != 0) {
           // The halves take the tiles in turn: K and V of each are free after its half.
-#pragma unroll
+#pragma unroll 1
           for (int t = 0; t < 2; ++t) {
-            if (cnt[t] == 0) break;
-            if (!wait_k() || !wait(C::B_Q + t, nq[t]++)) break;
+            if (cnt(t) == 0) break;
+            if (!wait_k() || !wait_half(C::B_Q, t, 0)) break;
             take_s(t, true);
             kr.step();
           }
-          for (int j = 0; ok && j < cnt[0]; ++j) {
-#pragma unroll
+          for (int j = 0; ok && j < cnt0; ++j) {
+#pragma unroll 1
             for (int t = 0; t < 2; ++t) {
-              if (j >= cnt[t]) break;
-              if (!wait_v() || !wait(C::B_PFULL + t, np[t]++)) break;
+              if (j >= cnt(t)) break;
+              if (!wait_v() || !wait_half(C::B_PFULL, t, 2)) break;
               tc_fence_after();
               if (elect_one()) {
                 issue_pv(t, vr.i, j > 0);
-                if (j + 1 == cnt[t]) tc_commit(bar(C::B_ODONE + t));
+                if (j + 1 == cnt(t)) tc_commit(bar(C::B_ODONE + t));
                 tc_commit(bar(C::B_VEMPTY + vr.i));
               }
               vr.step();
-              if (j + 1 < cnt[t]) {
+              if (j + 1 < cnt(t)) {
                 if (!wait_k()) break;
                 take_s(t, true);
                 kr.step();
@@ -1017,22 +1026,22 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           continue;
         }
         if (!wait_k()) break;
-#pragma unroll
+#pragma unroll(C::HALF_UNROLL)
         for (int t = 0; t < 2; ++t)
-          if (cnt[t] > 0 && wait(C::B_Q + t, nq[t]++)) take_s(t, false);
+          if (cnt(t) > 0 && wait_half(C::B_Q, t, 0)) take_s(t, false);
         if (!ok) break;
         if (elect_one()) tc_commit(bar(C::B_KEMPTY + kr.i));
         kr.step();
         wait_v();
         for (int j = 0; ok && j < tiles; ++j) {
           const bool more = j + 1 < tiles;
-#pragma unroll
+#pragma unroll(C::HALF_UNROLL)
           for (int t = 0; t < 2; ++t) {
-            if (j < cnt[t] && wait(C::B_PFULL + t, np[t]++)) {
+            if (j < cnt(t) && wait_half(C::B_PFULL, t, 2)) {
               tc_fence_after();
               if (elect_one()) {
                 issue_pv(t, vr.i, j > 0);
-                if (j + 1 == cnt[t]) tc_commit(bar(C::B_ODONE + t));
+                if (j + 1 == cnt(t)) tc_commit(bar(C::B_ODONE + t));
               }
             }
             if (!ok) break;
@@ -1043,7 +1052,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
               vr.step();
               if (more && !wait_v()) break;
             }
-            if (j + 1 < cnt[t]) take_s(t, false);
+            if (j + 1 < cnt(t)) take_s(t, false);
           }
           if (ok && more) {
             if (elect_one()) tc_commit(bar(C::B_KEMPTY + kr.i));
