@@ -53,7 +53,11 @@ FA_CHUNK_FN bool dual(int n, int G, int rb) { return n * G - rb * kRows <= kHalf
 // 227 with 26 (before the tile pass was shortened 259 with 10, 240 with 14, 231 with 18);
 // one long document takes the same with all.
 constexpr int kMostUnits = 3, kItemCost = 18;
-FA_CHUNK_FN int tile_units(bool dual) { return dual ? 2 : kMostUnits; }
+// Where every tile can have a CTA of its own, all count the same, so that it has (counted
+// as two, each third tile of few rows shared its CTA with another: 15 heads of one tile
+// took 16.1 us instead of 11.9, calls below 5 GFLOP 12 % longer on average).
+FA_CHUNK_FN bool few(long long tiles, int most) { return tiles <= most; }
+FA_CHUNK_FN int tile_units(bool dual, bool few) { return dual && !few ? 2 : kMostUnits; }
 // CTAs that have a run each, of `most`: a run has as many units as a tile and more, so
 // that a tile begins in every run between an item's first and last.  all: the units of
 // all tiles.

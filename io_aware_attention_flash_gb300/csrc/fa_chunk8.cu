@@ -78,8 +78,8 @@ struct ChunkCfg {
   static constexpr int OFF_VF = OFF_KS + NSC * MAX_PPT * 4;        // [NC][pages] V's two factors, bf16 pairs
   static constexpr int ITEM_INTS = 12;
   static constexpr int OFF_ITEM = OFF_VF + NC * MAX_PPT * 8;
-  static constexpr int OFF_SCAN = OFF_ITEM + NI * ITEM_INTS * 4;   // [2][16] sums, then what is found
-  static constexpr int OFF_BAR = OFF_SCAN + 34 * 8;
+  static constexpr int OFF_SCAN = OFF_ITEM + NI * ITEM_INTS * 4;   // [3][16] sums, then what is found
+  static constexpr int OFF_BAR = OFF_SCAN + 50 * 8;
   static constexpr int B_IFULL = 0;
   static constexpr int B_IEMPTY = B_IFULL + NI;
   static constexpr int B_KFULL = B_IEMPTY + NI;
@@ -241,12 +241,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
   // counted, then the pair that holds the run's first unit
   const int pairs = p.B * p.row_blocks;
   long long* scan = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
-  auto pair_tiles = [&](int x, int& tiles) -> int {  // units of a tile
+  auto pair_tiles = [&](int x, int& tiles) -> bool {  // whether they are a dual item's
     const int b = x / p.row_blocks, rb = x - b * p.row_blocks;
     int tok0, n, len;
     chunk_seq(p, b, tok0, n, len);
     tiles = chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
-    return chunk8::tile_units(chunk8::dual(n, p.G, rb));
+    return chunk8::dual(n, p.G, rb);
   };
   auto warp_scan = [&](long long v) {  // inclusive
 #pragma unroll
@@ -256,48 +256,49 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     }
     return v;
   };
-  int one = 0;  // units of pair tid's tiles, if one pass takes all pairs
-  long long units_sum = 0, items_sum = 0;
+  int one = 0;  // pair tid's tiles, if one pass takes all pairs
+  bool one_dual = false;
+  long long sums[3] = {0, 0, 0};  // tiles, those of dual items, items
   for (int x = tid; x < pairs; x += C::NUM_THREADS) {
-    int tiles;
-    const int w = pair_tiles(x, tiles);
-    one = w * tiles;
-    units_sum += one;
-    items_sum += one > 0;
+    one_dual = pair_tiles(x, one);
+    sums[0] += one;
+    sums[1] += one_dual ? one : 0;
+    sums[2] += one > 0;
   }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    units_sum += __shfl_xor_sync(0xffffffffu, units_sum, off);
-    items_sum += __shfl_xor_sync(0xffffffffu, items_sum, off);
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sums[k] += __shfl_xor_sync(0xffffffffu, sums[k], off);
+    if (lane == 0) scan[16 * k + warp] = sums[k];
   }
-  if (lane == 0) scan[warp] = units_sum, scan[16 + warp] = items_sum;
   __syncthreads();
-  units_sum = items_sum = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) units_sum += scan[i], items_sum += scan[16 + i];
-  units_sum *= p.Hk, items_sum *= p.Hk;
+  for (int k = 0; k < 3; ++k) {
+    sums[k] = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sums[k] += scan[16 * k + i];
+    sums[k] *= p.Hk;
+  }
+  const bool few = chunk8::few(sums[0], static_cast<int>(gridDim.x));
+  const long long units_sum = (sums[0] - sums[1]) * chunk8::tile_units(false, few) + sums[1] * chunk8::tile_units(true, few);
   const int ctas = chunk8::runs(units_sum, static_cast<int>(gridDim.x));
   if (tid == 0) p.merge[blockIdx.x * 8] = -1;
   if (static_cast<int>(blockIdx.x) >= ctas) return;
   const int extra = chunk8::extra_units(units_sum, ctas);
-  const long long total = units_sum + extra * items_sum;
+  const long long total = units_sum + extra * sums[2];
   auto pair_units = [&](int tile_units) -> long long {
     return tile_units > 0 ? static_cast<long long>(p.Hk) * (tile_units + extra) : 0;
   };
   const long long u_lo = chunk8::run_start(blockIdx.x, total, ctas), u_hi = chunk8::run_start(blockIdx.x + 1LL, total, ctas);
-  long long* found = scan + 32;  // first unit of the pair; the pair
+  long long* found = scan + 48;  // first unit of the pair; the pair
   {
     long long base = 0;
     for (int x0 = 0; x0 < pairs && base <= u_lo; x0 += C::NUM_THREADS) {
       if (pairs > C::NUM_THREADS) {
         one = 0;
-        if (x0 + tid < pairs) {
-          int tiles;
-          one = pair_tiles(x0 + tid, tiles);
-          one *= tiles;
-        }
+        if (x0 + tid < pairs) one_dual = pair_tiles(x0 + tid, one);
       }
-      const long long w = pair_units(one);
+      const long long w = pair_units(one * chunk8::tile_units(one_dual, few));
       long long sum = warp_scan(w);
       __syncthreads();  // (the sums before have been read)
       if (lane == 31) scan[warp] = sum;
@@ -774,7 +775,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         n = __shfl_sync(0xffffffffu, n, 0);  // the warp stays together even if a caller changes the lengths meanwhile
         len = __shfl_sync(0xffffffffu, len, 0);
         nt = chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
-        w = chunk8::tile_units(chunk8::dual(n, p.G, rb));
+        w = chunk8::tile_units(chunk8::dual(n, p.G, rb), few);
       };
       load_pair();
       auto next_unit = [&](Unit& u) {

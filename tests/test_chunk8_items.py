@@ -31,6 +31,12 @@ int main(int argc, char** argv) {
       all += static_cast<long long>(nt[n]) * w[n];
       if (*q == ',') ++q;
     }
+    long long tiles = 0;
+    for (int i = 0; i < n; ++i) tiles += nt[i];
+    if (few(tiles, most)) {  // all tiles count the same
+      all = 0;
+      for (int i = 0; i < n; ++i) all += static_cast<long long>(nt[i]) * (w[i] = tile_units(w[i] == 2, true));
+    }
     const int ctas = runs(all, most), extra = extra_units(all, ctas);
     const long long total = all + static_cast<long long>(extra) * n;
     std::printf("%%d %%d %%lld\\n", ctas, extra, total);
@@ -100,12 +106,14 @@ def test_runs_are_even_and_found_again(program, total):
 
 @pytest.mark.parametrize("most", [1, 3, 152])
 @pytest.mark.parametrize("items", [[(1, 2)], [(1, 3)], [(7, 2)], [(7, 3)], [(3, 3), (1, 2), (2, 3), (5, 2)], [(1, 2)] * 300,
-                                   [(256, 2)] * 32, [(1 + i % 9, 2 + i % 2) for i in range(500)], [(250, 3)] * 256, [(2, 3), (1, 2)] * 40])
+                                   [(256, 2)] * 32, [(1 + i % 9, 2 + i % 2) for i in range(500)], [(250, 3)] * 256, [(2, 3), (1, 2)] * 40, [(1, 2)] * 152, [(1, 2)] * 153])
 def test_every_tile_is_in_one_run(program, items, most):
     """And the CTAs between an item's first and last all have tiles of it, which the join relies on."""
     out = program(most, "cut", ",".join(f"{n}:{w}" for n, w in items))
     (ctas, extra, total), rows = out[0], out[1:]
     assert 1 <= ctas <= most and 0 <= extra <= 18
+    if sum(n for n, _ in items) <= most:  # a CTA for each tile
+        assert ctas == sum(n for n, _ in items) and all(k1 - k0 == 1 for _, _, k0, k1, _, _ in rows)
     seen = {}
     for c, i, k0, k1, c0, c1 in rows:
         assert k0 == seen.get(i, (0, 0))[0]
