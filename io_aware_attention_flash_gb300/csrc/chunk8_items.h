@@ -76,8 +76,16 @@ FA_CHUNK_FN long long run_start(long long c, long long total, long long ctas) { 
 FA_CHUNK_FN int run_of(long long u, long long total, long long ctas) {
   return static_cast<int>(((u + 1) * ctas + total - 1) / total - 1);
 }
+// Sequences of a few tiles at most, by the caller's limit, are not cut: an item counts as
+// one tile, and no partial results have to be joined.  Measured, d = 128, 16 sequences of 30
+// new tokens: 16.4 us whole and 21.8 cut at 250 keys, 18.1 and 23.9 at 380; 2 of 8: 15.6 and
+// 17.0 at 380, where a fourth tile would bring as much as it costs.
+constexpr int kWholeTiles = 3;
+FA_CHUNK_FN bool uncut(int max_seqlen) { return max_seqlen <= kWholeTiles * kKeys; }
+FA_CHUNK_FN int counted(int tiles, bool uncut) { return uncut && tiles > 0 ? 1 : tiles; }
 // Tiles of an item that begin before `units` units from its first one's.
-FA_CHUNK_FN int tiles_before(long long units, int per_tile, int tiles) {
+FA_CHUNK_FN int tiles_before(long long units, int per_tile, int tiles, bool uncut) {
+  if (uncut) return units <= 0 ? 0 : tiles;
   const long long t = units <= 0 ? 0 : (units + per_tile - 1) / per_tile;
   return t < tiles ? static_cast<int>(t) : tiles;
 }

@@ -953,8 +953,7 @@ FA_API fa_status fa_fwd_chunk_cache8(const void* q, const void* k_codes, const v
   p.zero_tail = zero_tail ? 1 : 0;
   p.scale_log2 = scale * fa::kLog2e;
   p.timeout_ns = kWaitLimitNs;
-  // An item of one tile is whole: nothing to join.
-  const bool merge = max_seqlen > fa::chunk8::kKeys;
+  const bool merge = !fa::chunk8::uncut(max_seqlen);  // otherwise there is nothing to join
   CUtensorMap tk;
   FA_TRY(make_map_codes(&tk, k_codes, d, block, Hk, num_blocks, d));
   const cudaError_t e = fa::launch_cache8_chunk(d, tk, p, w.ctas, merge, static_cast<cudaStream_t>(stream));

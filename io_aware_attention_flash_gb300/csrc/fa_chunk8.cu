@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
   // ---- this CTA's place: the tiles and items of all (sequence, row block) pairs
   // counted, then the pair that holds the run's first unit
   const int pairs = p.B * p.row_blocks;
+  const bool uncut = chunk8::uncut(p.max_seqlen);
   long long* scan = reinterpret_cast<long long*>(smem + C::OFF_SCAN);
   auto pair_tiles = [&](int x, int& tiles) -> bool {  // whether they are a dual item's
     const int b = x / p.row_blocks, rb = x - b * p.row_blocks;
@@ -261,6 +262,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
   long long sums[3] = {0, 0, 0};  // tiles, those of dual items, items
   for (int x = tid; x < pairs; x += C::NUM_THREADS) {
     one_dual = pair_tiles(x, one);
+    one = chunk8::counted(one, uncut);
     sums[0] += one;
     sums[1] += one_dual ? one : 0;
     sums[2] += one > 0;
@@ -297,6 +299,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       if (pairs > C::NUM_THREADS) {
         one = 0;
         if (x0 + tid < pairs) one_dual = pair_tiles(x0 + tid, one);
+        one = chunk8::counted(one, uncut);
       }
       const long long w = pair_units(one * chunk8::tile_units(one_dual, few));
       long long sum = warp_scan(w);
@@ -782,25 +785,25 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         u.tiles = 0;
         while (u.tiles <= 0) {
           if (at >= u_hi) return;
-          while (at >= x_start + pair_units(nt * w)) {
-            x_start += pair_units(nt * w);
+          while (at >= x_start + pair_units(chunk8::counted(nt, uncut) * w)) {
+            x_start += pair_units(chunk8::counted(nt, uncut) * w);
             if (++x >= pairs) {
               at = u_hi;
               return;
             }
             load_pair();
           }
-          const int units = nt * w + extra;  // of an item
+          const int own = chunk8::counted(nt, uncut) * w, units = own + extra;  // of an item
           const int hk = static_cast<int>((at - x_start) / units);
           const long long first = x_start + static_cast<long long>(hk) * units + extra;
           u.b = b, u.rb = rb, u.n = n, u.len = len, u.tok0 = tok0, u.nt = nt, u.hk = hk, u.dual = chunk8::dual(n, p.G, rb);
-          u.kt = chunk8::tiles_before(at - first, w, nt);
-          u.k0 = chunk8::tiles_before(u_lo - first, w, nt);
-          u.k1 = chunk8::tiles_before(u_hi - first, w, nt);
+          u.kt = chunk8::tiles_before(at - first, w, nt, uncut);
+          u.k0 = chunk8::tiles_before(u_lo - first, w, nt, uncut);
+          u.k1 = chunk8::tiles_before(u_hi - first, w, nt, uncut);
           u.tiles = min(u.k1 - u.kt, 32 / ppt);
           u.last = first + static_cast<long long>(nt - 1) * w;
           // (no tile of it begins in what is left of the run: on to the next item, or the end)
-          at = u.tiles > 0 ? first + static_cast<long long>(u.kt + u.tiles) * w : first + static_cast<long long>(nt) * w;
+          at = u.tiles > 0 && !uncut ? first + static_cast<long long>(u.kt + u.tiles) * w : first + own;
         }
         u.page = -1;
         if (lane < u.tiles * ppt && u.kt * ppt + lane < cache8::pages_of(len, p.block_shift))

@@ -45,7 +45,7 @@ int main(int argc, char** argv) {
       long long first = 0;
       for (int i = 0; i < n; ++i) {
         first += extra;
-        const int k0 = tiles_before(lo - first, w[i], nt[i]), k1 = tiles_before(hi - first, w[i], nt[i]);
+        const int k0 = tiles_before(lo - first, w[i], nt[i], false), k1 = tiles_before(hi - first, w[i], nt[i], false);
         if (k1 > k0) std::printf("%%d %%d %%d %%d %%d %%d\\n", c, i, k0, k1, run_of(first, total, ctas),
                                  run_of(first + static_cast<long long>(nt[i] - 1) * w[i], total, ctas));
         first += static_cast<long long>(nt[i]) * w[i];

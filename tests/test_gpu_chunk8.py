@@ -221,6 +221,18 @@ def test_large_values_under_rising_scores(d):
     check(o, lse, q, cache, table, [9], [640], d ** -0.5, False)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,block,B", [(64, 32, 5), (128, 16, 3), (64, 128, 130), (128, 64, 70)])
+def test_sequences_of_a_few_tiles(d, block, B, causal):
+    """Up to 384 keys, the limit under which no item is cut: fewer items than CTAs and
+    more, of one half and of both, and empty ones; and one key above the limit."""
+    fa = require_gpu()
+    for most in (384, 385):
+        lens = [(37 * i * i + 11) % (most - 1) + 1 for i in range(B - 2)] + [0, most]
+        new = [min(n, (53 * i + 1) % 200) for i, n in enumerate(lens)]
+        run(fa, 6, 2, d, block, new, lens, causal, seed=B + d)
+
+
 def test_indexes_out_of_range():
     """A page out of range reads as zeros, a length out of range is clamped; both are reported."""
     fa = require_gpu()
