@@ -76,7 +76,8 @@ enum {
   FA_ERR_WORKSPACE = 8,     /* workspace missing or smaller than required */
   FA_ERR_SCALE = 9,         /* scale not finite, or not positive where that is asked for */
   FA_ERR_NOT_DEVICE = 10,   /* q is not device memory (its device is the one launched on) */
-  FA_ERR_PAGE = 12,         /* a page table entry, length or start position out of range (device side) */
+  FA_ERR_PAGE = 12,         /* a page table entry, length, start position or number of new tokens
+                               out of range (device side) */
   FA_ERR_SCRATCH_LIMIT = 11 /* fa_bwd_noalloc: problem needs more than FA_NOALLOC_SCRATCH_BYTES */
 };
 
@@ -323,8 +324,9 @@ FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void
  *   cu_seqlens  device int32 [B + 1], non-decreasing, within [0, total]: sequence b's
  *               new tokens are rows cu_seqlens[b] .. cu_seqlens[b+1]−1
  *   seqlens     device int32 [B]: cached tokens, the new ones the last of them
- *   max_new     at least every number of new tokens (rows past it are not computed,
- *               their results unspecified);  max_seqlen  at least every length
+ *   max_new     at least every number of new tokens (of a sequence with more the first
+ *               max_new rows are computed, the results of the others unspecified);
+ *   max_seqlen  at least every length
  * causal != 0: new token i of n sees the keys j <= seqlens[b] − n + i; otherwise all.
  * A row that sees no key gets o = 0, lse = −infinity.  zero_tail as in
  * fa_fwd_grouped.  Scores and sums are fp32, which the scores have to fit.  A query
@@ -335,7 +337,8 @@ FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void
  * scales), scales powers of two.  A row of queries that holds an infinity or NaN gets
  * NaN for its results, no other row does.  A page index out of range reads as a page
  * of zeros, a length outside [0, min(max_seqlen, table_cols · block)] as the nearer
- * end of that range, and both are reported by fa_get_device_error as FA_ERR_PAGE.
+ * end of that range, and both are reported by fa_get_device_error as FA_ERR_PAGE, as
+ * is a sequence with more than max_new new tokens.
  * Results do not depend on the order in which CTAs run.  `workspace`: at least
  * fa_chunk_cache8_workspace_bytes() bytes (0 for arguments that the call rejects),
  * contents ignored; calls that may overlap need

@@ -317,8 +317,9 @@ def attention_chunk_cache8(q, cache: Cache8, block_table, cu_seqlens, seqlens, m
     cu_seqlens[b] .. cu_seqlens[b+1]-1 of q [T,H,d] are sequence b's newest
     tokens, any number of them (a prompt's next piece, a single token), seqlens
     int32 [B] its cached tokens with the new ones; max_new and max_seqlen at
-    least every number of new and of cached tokens.  causal: new token i of n
-    sees keys j <= seqlens[b] - n + i.  Returns (o [T,H,d] bf16, lse [H,T]
+    least every number of new and of cached tokens (more are reported by
+    fa_get_device_error).  causal: new token i of n sees keys
+    j <= seqlens[b] - n + i.  Returns (o [T,H,d] bf16, lse [H,T]
     fp32); rows that see no key, and rows behind the last sequence, get o = 0,
     lse = -inf."""
     if stream is None and workspace is None:

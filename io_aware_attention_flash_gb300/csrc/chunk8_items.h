@@ -29,6 +29,12 @@ FA_CHUNK_FN int visible(int len, int n, int i, bool causal) {
   const long long v = static_cast<long long>(len) - n + i + 1;
   return v < 0 ? 0 : v > len ? len : static_cast<int>(v);
 }
+// Where only the first `n` of `all` new tokens are computed: cached tokens that those can
+// see, the sequence as if it ended with them (the mask is counted from its end).
+FA_CHUNK_FN int reach(int len, int all, int n, bool causal) {
+  if (!causal || all <= n) return len;
+  return len < all - n ? 0 : len - (all - n);
+}
 FA_CHUNK_FN int tiles(int keys) {
   const int t = static_cast<int>((static_cast<unsigned>(keys) + kKeys - 1u) / kKeys);
   return t < 1 ? 1 : t;

@@ -144,12 +144,16 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// New tokens and cached tokens of sequence b, within what the buffers hold.
-__device__ __forceinline__ void chunk_seq(const Chunk8Params& p, int b, int& tok0, int& n, int& len) {
+// New tokens and cached tokens of sequence b, within what the buffers hold and the call
+// computes; whether that is all of them.
+__device__ __forceinline__ bool chunk_seq(const Chunk8Params& p, int b, int& tok0, int& n, int& len) {
   tok0 = min(max(p.cu_seqlens[b], 0), p.total);
-  n = min(min(max(p.cu_seqlens[b + 1], tok0), p.total) - tok0, p.max_new);
+  const int all = min(max(p.cu_seqlens[b + 1], tok0), p.total) - tok0, given = p.seqlens[b];
+  n = min(all, p.max_new);
   const long long cap = min(static_cast<long long>(p.table_cols) << p.block_shift, static_cast<long long>(p.max_seqlen));
-  len = static_cast<int>(min(max(static_cast<long long>(p.seqlens[b]), 0LL), cap));
+  const int held = static_cast<int>(min(max(static_cast<long long>(given), 0LL), cap));
+  len = chunk8::reach(held, all, n, p.causal);
+  return held == given && n == all;
 }
 
 // Four codes to bf16 by their bits: sign, and exponent and mantissa four places
@@ -320,11 +324,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       base += all;
     }
   }
-  if (blockIdx.x == 0) {  // lengths out of range are reported once
+  if (blockIdx.x == 0) {  // lengths out of range, and new tokens past max_new, are reported once
     for (int b = tid; b < p.B; b += C::NUM_THREADS) {
       int tok0, n, len;
-      chunk_seq(p, b, tok0, n, len);
-      if (len != p.seqlens[b]) atomicOr(p.err, kDevErrPage);
+      if (!chunk_seq(p, b, tok0, n, len)) atomicOr(p.err, kDevErrPage);
     }
   }
   if (warp == 0) {

@@ -1,0 +1,70 @@
+"""The chunk attention where a call's rows are not those of the tight case: more new
+tokens than max_new, rows in front of the first sequence, batches without a new token,
+many empty places of a batch, values stored as NaN.  Tolerances as in
+tests/test_gpu_chunk8.py, whose check of the formula is used."""
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_util import assert_no_device_error, gpu, require_gpu
+from tests.test_gpu_cache8 import make_table, random_cache
+from tests.test_gpu_chunk8 import ERR_PAGE, check, i32
+
+pytestmark = gpu
+
+
+def batch(fa, H, Hk, d, block, lens, T, seed):
+    cols = max(1, max(-(-n // block) for n in lens))
+    cache = random_cache(fa, len(lens) * cols, Hk, block, d, seed)
+    table = make_table(len(lens) * cols, len(lens), cols, seed)
+    q = torch.randn(T, H, d, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+    return cache, table, q
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,Hk,d,block,max_new", [(4, 2, 64, 16, 7), (8, 1, 128, 64, 33), (6, 2, 128, 32, 1), (16, 2, 64, 128, 100)])
+def test_more_new_tokens_than_max_new(H, Hk, d, block, max_new, causal):
+    """The first max_new rows of a sequence are those of the whole one, and that there
+    are more is reported; sequences within the limit, and rows behind the last, are as
+    ever.  Lengths below the number of new tokens too."""
+    fa = require_gpu()
+    new, lens = [max_new, max_new + 1, 150, 0, 1, 200, 180, max_new], [max_new, 400, 150, 9, 300, 160, 1000, 130]
+    cache, table, q = batch(fa, H, Hk, d, block, lens, sum(new) + 3, seed=max_new + d)
+    cu = np.cumsum([0] + new).tolist()
+    args = (q, cache, table.cuda(), i32(cu), i32(lens))
+    whole = fa.attention_chunk_cache8(*args, max(new), max(lens), causal)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    check(*whole, q, cache, table, new, lens, d ** -0.5, causal)
+    o, lse = fa.attention_chunk_cache8(*args, max_new, max(lens), causal)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == ERR_PAGE
+    for a, n in zip(cu, new):  # rows past the limit are unspecified
+        o[a + max_new:a + n], lse[:, a + max_new:a + n] = whole[0][a + max_new:a + n], whole[1][:, a + max_new:a + n]
+    check(o, lse, q, cache, table, new, lens, d ** -0.5, causal)
+    assert not o[cu[-1]:].any() and (lse[:, cu[-1]:] == -np.inf).all()
+
+
+def test_a_replayed_step_outgrows_max_new():
+    fa = require_gpu()
+    H, Hk, d, block = 8, 2, 128, 16
+    cache, table, q = batch(fa, H, Hk, d, block, [200, 300], 60, seed=4)
+    cu, lens = i32([0, 8, 16]), i32([100, 300])
+    f = lambda: fa.attention_chunk_cache8(q, cache, table.cuda(), cu, lens, 8, 300, True)  # noqa: E731
+    f()
+    graph = torch.cuda.CUDAGraph()
+    held = table.cuda()
+    with torch.cuda.graph(graph):
+        o, lse = fa.attention_chunk_cache8(q, cache, held, cu, lens, 8, 300, True)
+    for new, n, error in (([8, 8], [100, 300], 0), ([30, 5], [120, 300], ERR_PAGE), ([3, 8], [200, 8], 0)):
+        cu.copy_(torch.tensor(np.cumsum([0] + new), dtype=torch.int32))
+        lens.copy_(torch.tensor(n, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fa.fa_get_device_error() == error
+        whole = fa.attention_chunk_cache8(q, cache, held, cu, lens, 60, 300, True)
+        got = [t.clone() for t in (o, lse)]
+        for a, m in zip(np.cumsum([0] + new), new):
+            got[0][a + 8:a + m], got[1][:, a + 8:a + m] = whole[0][a + 8:a + m], whole[1][:, a + 8:a + m]
+        check(*got, q, cache, table, new, n, d ** -0.5, True)
+    assert_no_device_error(fa)
