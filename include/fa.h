@@ -329,7 +329,8 @@ FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void
  *   max_seqlen  at least every length
  * causal != 0: new token i of n sees the keys j <= seqlens[b] − n + i; otherwise all.
  * A row that sees no key gets o = 0, lse = −infinity.  zero_tail as in
- * fa_fwd_grouped.  Scores and sums are fp32, which the scores have to fit.  A query
+ * fa_fwd_grouped, of rows in front of the first sequence (cu_seqlens[0] > 0) as of
+ * those behind the last.  Scores and sums are fp32, which the scores have to fit.  A query
  * element enters its product with the codes as the sum of two e4m3 terms, off by at
  * most 2^-17 of its row's largest (rows below 2^-118: of 2^-118); a probability is
  * rounded to bf16, values are exact.  What slots behind a sequence's last token hold

@@ -232,9 +232,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
   grid_launch_dependents();
 
   if (p.zero_tail) {
-    // Rows behind the last sequence, shared out over the grid.
-    const int end = min(max(p.cu_seqlens[p.B], 0), p.total);
-    for (int row = end + blockIdx.x; row < p.total; row += gridDim.x) {
+    // Rows in front of the first sequence and behind the last, shared out over the grid.
+    const int front = min(max(p.cu_seqlens[0], 0), p.total), end = min(max(p.cu_seqlens[p.B], front), p.total);
+    for (int x = blockIdx.x; x < front + p.total - end; x += gridDim.x) {
+      const int row = x < front ? x : x - front + end;
       uint4* o = reinterpret_cast<uint4*>(p.o + static_cast<size_t>(row) * p.H * D);
       for (int i = tid; i < p.H * (D / 8); i += C::NUM_THREADS) o[i] = make_uint4(0u, 0u, 0u, 0u);
       for (int h = tid; h < p.H; h += C::NUM_THREADS) p.lse[static_cast<size_t>(h) * p.total + row] = -CUDART_INF_F;

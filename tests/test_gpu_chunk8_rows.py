@@ -68,3 +68,31 @@ def test_a_replayed_step_outgrows_max_new():
             got[0][a + 8:a + m], got[1][:, a + 8:a + m] = whole[0][a + 8:a + m], whole[1][:, a + 8:a + m]
         check(*got, q, cache, table, new, n, d ** -0.5, True)
     assert_no_device_error(fa)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_in_front_of_the_first_sequence(d):
+    """They belong to no sequence, as those behind the last: zeros from the call that
+    allocates, left as they were by the one that does not."""
+    fa = require_gpu()
+    H, Hk, block, new, lens = 4, 2, 16, [7, 0, 30], [90, 3, 30]
+    for first, tail in ((0, 4), (1, 0), (13, 4), (200, 1)):
+        cu = np.cumsum([first] + new).tolist()
+        T = cu[-1] + tail
+        cache, table, q = batch(fa, H, Hk, d, block, lens, T, seed=first + d)
+        q[:first] = q[cu[-1]:] = float("nan")
+        args = (q, cache, table.cuda(), i32(cu), i32(lens))
+        ws = torch.empty(fa.fa_chunk_cache8_workspace_bytes(3, 30, T, H, Hk, 90, d), dtype=torch.uint8, device="cuda")
+        for zero_tail in (True, False):
+            o, lse = torch.full((T, H, d), 3.0, device="cuda").bfloat16(), torch.full((H, T), 3.0, device="cuda")
+            fa.fa_fwd_chunk_cache8(*args, o, lse, ws, 30, 90, True, zero_tail=zero_tail)
+            torch.cuda.synchronize()
+            outside = torch.ones(T, dtype=torch.bool, device="cuda")
+            outside[first:cu[-1]] = False
+            assert (o[outside] == (0 if zero_tail else 3)).all() and (lse.T[outside] == (-np.inf if zero_tail else 3)).all()
+            check(o[first:], lse[:, first:], q[first:], cache, table, new, lens, d ** -0.5, True)
+    # a batch of rows, none of them a sequence's
+    o, lse = fa.attention_chunk_cache8(q, cache, table.cuda(), i32([5, 5, 5, 5]), i32([0, 3, 0]), 30, 90, True)
+    torch.cuda.synchronize()
+    assert not o.any() and (lse == -np.inf).all()
+    assert_no_device_error(fa)
