@@ -303,9 +303,10 @@ FA_API fa_status fa_rotary(const void* q, const void* k, void* q_out, void* k_ou
  * contiguous).  Arguments, pages and errors as fa_cache8_store; in addition
  *   positions   device int32 [axes, total], or NULL: a token's place in its
  *               sequence, start[b] + i, on every axis
- *   zero_tail   rows of q_out behind the last sequence: 0 leaves them as they were,
- *               otherwise they become 0
- * Queries are turned whether or not their token could be stored.
+ *   zero_tail   rows of q_out behind the last sequence or in front of the first
+ *               (cu_seqlens[0] > 0): 0 leaves them as they were, otherwise they
+ *               become 0
+ * A sequence's queries are turned whether or not their token could be stored.
  */
 FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void* v, void* q_out, void* k_codes,
                                         void* v_codes, float* k_scale, float* v_scale, const int* block_table,

@@ -431,8 +431,8 @@ def cache8_store_rotary(q, k, v, cache: Cache8, block_table, cu_seqlens, start, 
     """cache8_store with the positions on the way: the new tokens' keys [T,Hk,d]
     are turned and stored with the values, and the queries q [T,H,d] turned.
     positions: int32 [T] or [axes,T]; None: each token's place in its sequence,
-    start[b] + i, on every axis.  Returns q', zero in rows behind the last
-    sequence."""
+    start[b] + i, on every axis.  Returns q', zero in rows of no sequence (behind
+    the last, in front of the first)."""
     if stream is None:
         out = _binding.native().cache8_store_rotary(q, k, v, cache, block_table, cu_seqlens, start, max_new, rotary,
                                                     positions)

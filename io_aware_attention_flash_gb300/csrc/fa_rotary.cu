@@ -229,9 +229,11 @@ __global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT, 4)
   grid_dependency_wait();  // scheduled while the kernel before it in the stream finishes
   if (static_cast<int>(blockIdx.x) >= store_blocks) {
     // ---- queries
-    const int end = min(max(p.cu_seqlens[p.B], 0), p.total);
-    const int tok0 = (static_cast<int>(blockIdx.x) - store_blocks) * C::TOKENS;
-    const int n = min(C::TOKENS, end - tok0);  // of them before the end of the last sequence
+    // of the block's tokens those of sequences: not in front of the first, nor behind the last
+    const int front = min(max(p.cu_seqlens[0], 0), p.total), end = min(max(p.cu_seqlens[p.B], front), p.total);
+    const int all0 = (static_cast<int>(blockIdx.x) - store_blocks) * C::TOKENS, all = min(C::TOKENS, p.total - all0);
+    const int skip = min(max(front - all0, 0), all), tok0 = all0 + skip;
+    const int n = min(all - skip, end - tok0);
     turn_rows<D, IL, NT>(x, tok0, n, cs, r.pairs, [&]() {
       if (!r.positions) {  // a token's place: that of its row behind its sequence's first
         if (threadIdx.x < C::TOKENS) place[threadIdx.x] = 0;
@@ -253,8 +255,9 @@ __global__ void __launch_bounds__(AppendCfg<D, BLOCK>::NT, 4)
       __syncthreads();
     });
     if (zero_tail) {
-      for (int t = max(n, 0); t < C::TOKENS && tok0 + t < p.total; ++t) {
-        uint4* row = reinterpret_cast<uint4*>(x.dst0 + static_cast<long long>(tok0 + t) * x.heads0 * D);
+      for (int t = 0; t < all; ++t) {
+        if (t >= skip && t - skip < n) continue;
+        uint4* row = reinterpret_cast<uint4*>(x.dst0 + static_cast<long long>(all0 + t) * x.heads0 * D);
         for (int i = threadIdx.x; i < x.heads0 * (D / 8); i += NT) row[i] = make_uint4(0u, 0u, 0u, 0u);
       }
     }
