@@ -290,7 +290,16 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
   const long long units_sum = (sums[0] - sums[1]) * chunk8::tile_units(false, few) + sums[1] * chunk8::tile_units(true, few);
   const int ctas = chunk8::runs(units_sum, static_cast<int>(gridDim.x));
   if (tid == 0) p.merge[blockIdx.x * 8] = -1;
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  auto report = [&]() {  // lengths out of range, and new tokens past max_new: once
+    for (int b = tid; b < p.B; b += C::NUM_THREADS) {
+      int tok0, n, len;
+      if (!chunk_seq(p, b, tok0, n, len)) atomicOr(p.err, kDevErrPage);
+    }
+  };
+  if (static_cast<int>(blockIdx.x) >= ctas) {
+    if (blockIdx.x == 0) report();  // (there is no row to compute)
+    return;
+  }
   const int extra = chunk8::extra_units(units_sum, ctas);
   const long long total = units_sum + extra * sums[2];
   auto pair_units = [&](int tile_units) -> long long {
@@ -325,12 +334,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       base += all;
     }
   }
-  if (blockIdx.x == 0) {  // lengths out of range, and new tokens past max_new, are reported once
-    for (int b = tid; b < p.B; b += C::NUM_THREADS) {
-      int tok0, n, len;
-      if (!chunk_seq(p, b, tok0, n, len)) atomicOr(p.err, kDevErrPage);
-    }
-  }
+  if (blockIdx.x == 0) report();
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
     tmem_relinquish();

@@ -96,3 +96,13 @@ def test_rows_in_front_of_the_first_sequence(d):
     torch.cuda.synchronize()
     assert not o.any() and (lse == -np.inf).all()
     assert_no_device_error(fa)
+
+
+def test_lengths_are_reported_without_new_tokens():
+    fa = require_gpu()
+    cache, table, q = batch(fa, 2, 1, 64, 16, [40, 40], 5, seed=3)
+    for lens, error in (([40, 0], 0), ([41, 48], 0), ([40, 49], ERR_PAGE), ([-1, 3], ERR_PAGE), ([0, 2 ** 31 - 1], ERR_PAGE)):
+        o, lse = fa.attention_chunk_cache8(q, cache, table.cuda(), i32([0, 0, 0]), i32(lens), 5, 1000, True)
+        torch.cuda.synchronize()
+        assert fa.fa_get_device_error() == error
+        assert not o.any() and (lse == -np.inf).all()
