@@ -47,6 +47,22 @@ FA_CHUNK_FN int row_tiles(int len, int n, int G, int first, int count, bool caus
   return tiles(visible(len, n, last / G, causal));
 }
 
+// Row block rb is a sequence's last, or it has none.
+FA_CHUNK_FN bool last_block(int n, int G, int rb) { return n * G - rb * kRows <= kRows; }
+// Where the pairs (sequence, row block) that have rows are gone through in order: the row
+// block behind rb of its sequence, or of the next sequence with new tokens, which
+// next_with(b) finds from b on (`count` if there is none).  As many steps as there are
+// pairs with rows, whatever the largest sequence's row blocks are.
+template <typename NextWith>
+FA_CHUNK_FN void next_pair(int& b, int& rb, int n, int G, NextWith next_with) {
+  if (!last_block(n, G, rb)) {
+    ++rb;
+  } else {
+    b = next_with(b + 1);
+    rb = 0;
+  }
+}
+
 // Rows of row block rb fit in one half.
 FA_CHUNK_FN bool dual(int n, int G, int rb) { return n * G - rb * kRows <= kHalf; }
 

@@ -511,6 +511,9 @@ fa_status chunk_plan(int B, int max_new, int total, int H, int Hk, int max_seqle
   const long long rows = static_cast<long long>(max_new < total ? max_new : total) * (H / Hk);
   const long long blocks = (rows + fa::chunk8::kRows - 1) / fa::chunk8::kRows;
   if (blocks * B > 0x3fffffffLL) return FA_ERR_SHAPE;  // (counted with 32 bits, in steps of a CTA)
+  // (a warp that others wait for passes the places without new tokens 32 at a time, each
+  // step as long as a miss: two of the wait limit's four seconds for this many)
+  if (B > 1 << 26) return FA_ERR_SHAPE;
   const long long tiles = (static_cast<long long>(max_seqlen) + fa::chunk8::kKeys - 1) / fa::chunk8::kKeys;
   const long long most = kChunkCtas / tiles / Hk < blocks * B ? kChunkCtas : blocks * B * Hk * tiles;
   w->row_blocks = static_cast<int>(blocks);

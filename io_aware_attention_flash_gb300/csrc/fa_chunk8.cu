@@ -776,17 +776,26 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
         int page;                                 // this lane's page (of 32 / ppt tiles), -1: none
         float ks;
       };
-      int x = static_cast<int>(found[1]);
+      int b = static_cast<int>(found[1]) / p.row_blocks, rb = static_cast<int>(found[1]) - b * p.row_blocks;
       long long x_start = found[0], at = u_lo;  // first unit of the pair; the next unit
-      int nt = 0, w = 0, n = 0, len = 0, tok0 = 0, b = 0, rb = 0;  // (w: units of a tile)
+      int nt = 0, w = 0, n = 0, len = 0, tok0 = 0;  // (w: units of a tile)
       auto load_pair = [&]() {
-        b = x / p.row_blocks;
-        rb = x - b * p.row_blocks;
         chunk_seq(p, b, tok0, n, len);
         n = __shfl_sync(0xffffffffu, n, 0);  // the warp stays together even if a caller changes the lengths meanwhile
         len = __shfl_sync(0xffffffffu, len, 0);
         nt = chunk8::row_tiles(len, n, p.G, rb * kRows, kRows, p.causal);
         w = chunk8::tile_units(chunk8::dual(n, p.G, rb), few);
+      };
+      // The first sequence from `from` on that has new tokens, 32 at a time: the other roles
+      // wait for an item meanwhile, and a wait has a limit.
+      auto next_with = [&](int from) {
+        for (; from < p.B; from += 32) {
+          int first, rows = 0, held;
+          if (from + lane < p.B) chunk_seq(p, from + lane, first, rows, held);
+          const unsigned some = __ballot_sync(0xffffffffu, rows > 0);
+          if (some) return from + __ffs(some) - 1;
+        }
+        return p.B;
       };
       load_pair();
       auto next_unit = [&](Unit& u) {
@@ -795,7 +804,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           if (at >= u_hi) return;
           while (at >= x_start + pair_units(chunk8::counted(nt, uncut) * w)) {
             x_start += pair_units(chunk8::counted(nt, uncut) * w);
-            if (++x >= pairs) {
+            chunk8::next_pair(b, rb, n, p.G, next_with);
+            if (b >= p.B) {
               at = u_hi;
               return;
             }

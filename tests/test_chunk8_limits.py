@@ -20,6 +20,19 @@ int main(int argc, char** argv) {
   if (!std::strcmp(argv[1], "reach")) {  // len all n causal row...: keys that the rows see
     const int len = std::atoi(argv[2]), all = std::atoi(argv[3]), n = std::atoi(argv[4]), causal = std::atoi(argv[5]);
     for (int i = 6; i < argc; ++i) std::printf("%%d\\n", visible(reach(len, all, n, causal), n, std::atoi(argv[i]), causal));
+  } else if (!std::strcmp(argv[1], "last")) {  // n G row-block...: whether it is the last
+    for (int i = 4; i < argc; ++i) std::printf("%%d\\n", last_block(std::atoi(argv[2]), std::atoi(argv[3]), std::atoi(argv[i])));
+  } else if (!std::strcmp(argv[1], "walk")) {  // G, the sequences' new tokens: the pairs from the first with rows on
+    const int G = std::atoi(argv[2]), B = argc - 3;
+    auto next_with = [&](int b) {
+      while (b < B && std::atoi(argv[3 + b]) == 0) ++b;
+      return b;
+    };
+    int b = next_with(0), rb = 0;
+    while (b < B) {
+      std::printf("%%d %%d\\n", b, rb);
+      next_pair(b, rb, std::atoi(argv[3 + b]), G, next_with);
+    }
   }
 }
 """
@@ -54,3 +67,20 @@ def test_rows_below_max_new_see_what_they_see_of_the_whole(program, length, new,
     rows = sorted({0, n // 2, n - 1})
     want = [max(0, min(length, length - new + i + 1)) if causal else length for i in rows]
     assert [x[0] for x in program("reach", length, new, n, causal, *rows)] == want
+
+
+@pytest.mark.parametrize("G", [1, 3, 8, 256, 300])
+@pytest.mark.parametrize("new", [[1], [0, 0, 5, 0], [4096] + [1] * 50 + [0] * 200 + [256, 257, 0, 255], [0] * 3000 + [100000, 0, 0, 33],
+                                 [300, 0, 512, 85, 86]])
+def test_pairs_with_rows_are_gone_through_without_the_others(program, new, G):
+    """As many steps as there are such pairs: a copying warp that stepped over the empty
+    ones, the longest sequence's row blocks for each other sequence, could keep the CTA's
+    waits past their limit (2^25 pairs of two loads each and a division: seconds)."""
+    new = [min(n, (2 ** 31 - 1) // G) for n in new]
+    assert program("walk", G, *new) == [[b, rb] for b, n in enumerate(new) for rb in range(-(-n * G // 256))]
+
+
+@pytest.mark.parametrize("n,G", [(MOST, 1), (1, MOST), (MOST // 300, 300), (2 ** 23, 255)])
+def test_last_row_block_at_the_ends_of_int(program, n, G):
+    last = (n * G - 1) // 256
+    assert program("last", n, G, last - 1, last) == [[0], [1]]

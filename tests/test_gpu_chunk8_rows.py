@@ -106,3 +106,27 @@ def test_lengths_are_reported_without_new_tokens():
         torch.cuda.synchronize()
         assert fa.fa_get_device_error() == error
         assert not o.any() and (lse == -np.inf).all()
+
+
+@pytest.mark.parametrize("H,d,total,B", [(64, 64, 4096, 32768), (8, 128, 1024, 5000)])
+def test_many_places_without_new_tokens(H, d, total, B):
+    """A batch of many places, of which a few have a token, in a buffer of many rows: the
+    places between two of them times the row blocks that the buffer could hold (2^25 at
+    the most here) are passed within the waits' limit."""
+    fa = require_gpu()
+    at = {0: (1, 700), 1: (2, 90), B // 2: (3, 1000), B - 1: (1, 400)}
+    new, lens = [0] * B, [0] * B
+    for b, (n, L) in at.items():
+        new[b], lens[b] = n, L
+    block, cols = 128, 8
+    cache = random_cache(fa, len(at) * cols, 1, block, d, seed=d)
+    few = make_table(len(at) * cols, len(at), cols, d)
+    table = torch.full((B, cols), -5, dtype=torch.int32)
+    for row, b in enumerate(at):
+        table[b] = few[row]
+    q = torch.randn(total, H, d, generator=torch.Generator().manual_seed(d)).bfloat16().cuda()
+    o, lse = fa.attention_chunk_cache8(q, cache, table.cuda(), i32(np.cumsum([0] + new).tolist()), i32(lens), 2 ** 31 - 1, 1000, True)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    check(o, lse, q, cache, few, [n for n, _ in at.values()], [L for _, L in at.values()], d ** -0.5, True)
+    assert not o[7:].any() and (lse[:, 7:] == -np.inf).all()
