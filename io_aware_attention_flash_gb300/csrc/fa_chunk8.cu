@@ -364,9 +364,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    // (Ahead of the other roles: where its code lies among theirs decides how often its
-    // instructions are fetched again.  Behind them d = 64 takes 3 % longer over drawn sizes,
-    // 197 against 182 us on pieces of prompts of 64 heads; d = 128 1 % less.)
+    // (Ahead of the other roles, and the long code that runs once an item, the items' with
+    // K's copies, behind them: where the loops of a tile lie among one another decides how
+    // often their instructions are fetched again.  With that between the softmax and the rest 16
+    // mixed sequences take 218 to 249 us, by what it holds, instead of 214, a long document 736 to
+    // 768 instead of 731, pieces of prompts of 64 heads at d = 64 173 to 176 instead of 177;
+    // with the softmax behind all others d = 64 takes 3 % longer over drawn sizes.)
     setmaxnreg_inc<C::REG_SOFTMAX>();
     const int t = warp / 4, wq = warp % 4, r = wq * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -765,7 +768,270 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     if (phases & kRawEver) wait_drain(bar(C::B_RAW + warp), phase(kRaw) ^ ((phases & kRawAhead) ? 0 : 1), p.err, p.timeout_ns);
   } else {
     setmaxnreg_dec<C::REG_OTHER>();
-    if (warp == C::COPY_WARP) {
+    if (warp == C::MMA_WARP) {
+      // ------------------------------------------------------------ MMA
+      // The tensor core's queue holds some 190 cycles of products, and a wait for what
+      // is there already, or a commit, costs this thread 50 to 100: each stands between
+      // two batches of products, none beside another where that can be had.  (All waits
+      // of a tile before its products: 880 us on 8192 rows over 32768 keys; a thread for
+      // each row tile, whose products then alternate on the tensor core: 1064.)
+      constexpr uint32_t idesc_s = idesc_e4m3(128, 128, false);
+      constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const uint64_t dQ0 = sdesc8<D>(sb + C::OFF_Q, 16, 16 * D);
+      const uint64_t dK0 = sdesc8<D>(sb + C::OFF_K, 16);
+      const uint64_t dV0 = sdesc_sw128(sb + C::OFF_V, C::BLK_BYTES, 1024);
+      auto issue_s = [&](int t, int ks) {
+        const uint64_t dQ = sdesc_add(dQ0, t * C::TILE_BYTES), dK = sdesc_add(dK0, ks * C::CODE_BYTES);
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk)
+            mma_e4m3(tm + C::S_COL(t), sdesc_add(dQ, term * 8 * D + kk * 32), sdesc_add(dK, kk * 32), idesc_s,
+                     term + kk > 0);
+      };
+      auto issue_pv = [&](int t, int vs, bool acc) {
+        const uint64_t dV = sdesc_add(dV0, vs * C::TILE_BYTES);
+#pragma unroll(C::PV_UNROLL)
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_ts(tm + C::O_COL(t), tm + C::S_COL(t) + kk * 8, sdesc_add(dV, kk * 2048), idesc_o,
+                 (acc || kk > 0) ? 1u : 0u);
+      };
+      bool ok = true;
+      auto wait = [&](int i, int phase) {  // (the whole warp, which stays together)
+        ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+      };
+      Ring<C::NK> kr;                        // the next tile of K, of V
+      Ring<C::NV> vr;
+      uint32_t half_phases = 0;  // bit t: of half t's items, bit 2 + t: of its P tiles
+      auto wait_half = [&](int b, int t, int bit) {
+        const int ph = (half_phases >> (bit + t)) & 1;
+        half_phases ^= 1u << (bit + t);
+        return wait(b + t, ph);
+      };
+      auto wait_k = [&]() { return wait(C::B_KFULL + kr.i, kr.phase); };
+      auto wait_v = [&]() { return wait(C::B_VFULL + vr.i, vr.phase); };
+      auto take_s = [&](int t, bool free_k) {  // S of half t over the K that is next
+        tc_fence_after();
+        if (elect_one()) {
+          issue_s(t, kr.i);
+          tc_commit(bar(C::B_SFULL + t));
+          if (free_k) tc_commit(bar(C::B_KEMPTY + kr.i));
+        }
+      };
+      Item it;
+      while (ok && take_item(it)) {
+        const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
+        const int cnt0 = __shfl_sync(0xffffffffu, it.cnt0, 0), cnt1 = __shfl_sync(0xffffffffu, it.cnt1, 0);
+        auto cnt = [&](int t) { return t ? cnt1 : cnt0; };
+        if (__shfl_sync(0xffffffffu, it.dual ? 1 : 0, 0) != 0) {
+          // The halves take the tiles in turn: K and V of each are free after its half.
+#pragma unroll 1
+          for (int t = 0; t < 2; ++t) {
+            if (cnt(t) == 0) break;
+            if (!wait_k() || !wait_half(C::B_Q, t, 0)) break;
+            take_s(t, true);
+            kr.step();
+          }
+          for (int j = 0; ok && j < cnt0; ++j) {
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+              if (j >= cnt(t)) break;
+              if (!wait_v() || !wait_half(C::B_PFULL, t, 2)) break;
+              tc_fence_after();
+              if (elect_one()) {
+                issue_pv(t, vr.i, j > 0);
+                if (j + 1 == cnt(t)) tc_commit(bar(C::B_ODONE + t));
+                tc_commit(bar(C::B_VEMPTY + vr.i));
+              }
+              vr.step();
+              if (j + 1 < cnt(t)) {
+                if (!wait_k()) break;
+                take_s(t, true);
+                kr.step();
+              }
+            }
+          }
+          continue;
+        }
+        if (!wait_k()) break;
+#pragma unroll(C::HALF_UNROLL)
+        for (int t = 0; t < 2; ++t)
+          if (cnt(t) > 0 && wait_half(C::B_Q, t, 0)) take_s(t, false);
+        if (!ok) break;
+        if (elect_one()) tc_commit(bar(C::B_KEMPTY + kr.i));
+        kr.step();
+        wait_v();
+        for (int j = 0; ok && j < tiles; ++j) {
+          const bool more = j + 1 < tiles;
+#pragma unroll(C::HALF_UNROLL)
+          for (int t = 0; t < 2; ++t) {
+            if (j < cnt(t) && wait_half(C::B_PFULL, t, 2)) {
+              tc_fence_after();
+              if (elect_one()) {
+                issue_pv(t, vr.i, j > 0);
+                if (j + 1 == cnt(t)) tc_commit(bar(C::B_ODONE + t));
+              }
+            }
+            if (!ok) break;
+            if (t == 0) {
+              if (more && !wait_k()) break;
+            } else {
+              if (elect_one()) tc_commit(bar(C::B_VEMPTY + vr.i));
+              vr.step();
+              if (more && !wait_v()) break;
+            }
+            if (j + 1 < cnt(t)) take_s(t, false);
+          }
+          if (ok && more) {
+            if (elect_one()) tc_commit(bar(C::B_KEMPTY + kr.i));
+            kr.step();
+          }
+        }
+      }
+      // every MMA issued so far must finish before tensor memory is released
+      if (elect_one()) tc_commit(bar(C::B_DRAIN));
+      wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
+    } else if (warp != C::COPY_WARP && warp != C::V_WARP) {
+      // ---------------------------------------------------------------- conversion
+      // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32
+      // chunks of consecutive rows, every fifth group of them.  The chunks of a
+      // quarter-warp lie in two rows, at d = 128 in the two halves of them: neither its
+      // reads nor its swizzled writes meet in a bank.
+      const int cw = warp < C::MMA_WARP ? warp - 9 : warp - 10;
+      constexpr int CPR = D / 16, ROWS = 32 / CPR, GROUPS = kKeys / ROWS;
+      int row0, chunk;  // within a group
+      if (D == 128) {
+        const int rb = (lane >> 2) & 1;
+        row0 = ((lane >> 4) & 1) * 2 + rb;
+        chunk = (lane & 3) + 4 * (((lane >> 3) & 1) ^ rb);
+      } else {
+        row0 = lane >> 2;
+        chunk = lane & 3;
+      }
+      const uint32_t in0 = row0 * D + chunk * 16;
+      const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES;
+      auto place = [&](int row, int half) -> uint32_t { return out0 + row * 128 + (((c0 + half) ^ (row & 7)) << 4); };
+      int tile = 0;
+      Ring<C::NC> cr;
+      Ring<C::NV> vr;
+      bool ok = true;
+      auto wait = [&](int i, int phase) {
+        ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        return ok;
+      };
+      Item it;
+      while (ok && take_item(it)) {
+        for (int kt = it.k0; kt < it.k0 + it.tiles; ++kt, ++tile) {
+          const int held = cache8::tokens_from(it.len, kt, kKeys, 0);  // tokens of the tile, if fewer than its rows
+          const int st = cr.i, slot = vr.i;
+          if (!wait(C::B_CFULL + st, cr.phase)) break;
+          if (tile >= C::NV && !wait(C::B_VEMPTY + slot, vr.phase ^ 1)) break;
+          const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES + in0;
+          const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_VF) + st * C::MAX_PPT;
+          uint8_t* out = smem + C::OFF_V + slot * C::TILE_BYTES;
+          // (rolled: beside the softmax's code an unrolled loop costs instruction fetches)
+          uint4 next = *reinterpret_cast<const uint4*>(codes + cw * ROWS * D);
+#pragma unroll 1
+          for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
+            const uint4 now = next;
+            const int row = g * ROWS + row0;
+            const uint32_t f = factors[row >> p.block_shift].x;
+            if (g + C::CONVERT_WARPS < GROUPS)
+              next = *reinterpret_cast<const uint4*>(codes + (g + C::CONVERT_WARPS) * ROWS * D);
+            const uint32_t in[4] = {now.x, now.y, now.z, now.w};
+            uint32_t v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              widen4(in[k], v[2 * k], v[2 * k + 1]);
+              v[2 * k] = mul_bf16x2(v[2 * k], f);
+              v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f);
+            }
+            *reinterpret_cast<uint4*>(out + place(row, 0)) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(out + place(row, 1)) = make_uint4(v[4], v[5], v[6], v[7]);
+          }
+          // Seldom: slots without a token, which may hold anything, become 0; a scale above
+          // 2^55, whose factor does not fit one bf16 number, is a second one.
+          if (held < kKeys || __any_sync(0xffffffffu, factors[lane % C::MAX_PPT].y != kOne2)) {
+#pragma unroll 1
+            for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
+              const int row = g * ROWS + row0;
+              const uint32_t f = factors[row >> p.block_shift].y;
+#pragma unroll 1
+              for (int half = 0; half < 2; ++half) {
+                uint4* at = reinterpret_cast<uint4*>(out + place(row, half));
+                const uint4 x = *at;
+                *at = row >= held ? make_uint4(0u, 0u, 0u, 0u)
+                                  : make_uint4(mul_bf16x2(x.x, f), mul_bf16x2(x.y, f), mul_bf16x2(x.z, f), mul_bf16x2(x.w, f));
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(C::B_CEMPTY + st));
+            mbar_arrive(bar(C::B_VFULL + slot));
+          }
+          cr.step();
+          vr.step();
+        }
+      }
+    } else if (warp == C::V_WARP) {
+      // ------------------------------------------------------------ copies of V
+      const int ppt = kKeys >> p.block_shift, page_bytes = D << p.block_shift, window = 32 / ppt;  // tiles of 32 pages
+      Ring<C::NC> cr;
+      int tile = 0;
+      bool ok = true;
+      Item it;
+      while (ok && take_item(it)) {
+        const int pages = cache8::pages_of(it.len, p.block_shift), end = it.k0 + it.tiles;
+        auto load_pages = [&](int kt) {  // lane i: page i of the window at tile kt, -1: none
+          return kt + lane / ppt < end && kt * ppt + lane < pages
+                     ? p.table[static_cast<size_t>(it.b) * p.table_cols + kt * ppt + lane]
+                     : -1;
+        };
+        auto load_scales = [&](int& page) {  // (a page out of range is reported with K's)
+          if (page < 0 || page >= p.num_blocks) page = -1;
+          return page >= 0 ? p.v_scale[static_cast<size_t>(page) * p.Hk + it.hk] : 0.f;
+        };
+        int cur = load_pages(it.k0);
+        float scale = load_scales(cur);
+        for (int k0 = it.k0; ok && k0 < end; k0 += window) {
+          int next = load_pages(min(k0 + window, end));
+          float next_scale = 0.f;
+          for (int i = 0; i < window && k0 + i < end; ++i, ++tile) {
+            const int from = (i * ppt + lane) & 31;
+            const int page = __shfl_sync(0xffffffffu, cur, from);
+            const float vs = __shfl_sync(0xffffffffu, scale, from);
+            const bool mine = lane < ppt && page >= 0;  // (a page out of range reads as zeros: its factor is 0)
+            if (tile >= C::NC) ok = wait_bounded(bar(C::B_CEMPTY + cr.i), cr.phase ^ 1, abort_flag, p.err, p.timeout_ns);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * page_bytes;
+            if (lane < C::MAX_PPT)
+              reinterpret_cast<uint2*>(smem + C::OFF_VF)[cr.i * C::MAX_PPT + lane] =
+                  mine ? scale_factors(vs) : make_uint2(0u, kOne2);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(bar(C::B_CFULL + cr.i), bytes);
+            __syncwarp();
+            if (mine)
+              bulk_load(sb + C::OFF_C + cr.i * C::CODE_BYTES + lane * page_bytes,
+                        p.v_codes + (static_cast<size_t>(page) * p.Hk + it.hk) * page_bytes, page_bytes,
+                        bar(C::B_CFULL + cr.i));
+            cr.step();
+            if (i == 0) next_scale = load_scales(next);
+          }
+          cur = next;
+          scale = next_scale;
+        }
+      }
+      // Every copy issued lands before the CTA may exit, whoever aborted.
+      for (int s = 0; s < C::NC && s < tile; ++s)
+        wait_drain(bar(C::B_CFULL + s), ((tile - 1 - s) / C::NC) & 1, p.err, p.timeout_ns);
+    } else {
       // ------------------------------------------------------------ items, copies
       const int ppt = kKeys >> p.block_shift, page_bytes = D << p.block_shift;
       struct Unit {
@@ -914,269 +1180,6 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       // Every copy issued lands before the CTA may exit, whoever aborted.
       for (int s = 0; s < C::NK && s < tile; ++s)
         wait_drain(bar(C::B_KFULL + s), ((tile - 1 - s) / C::NK) & 1, p.err, p.timeout_ns);
-    } else if (warp == C::V_WARP) {
-      // ------------------------------------------------------------ copies of V
-      const int ppt = kKeys >> p.block_shift, page_bytes = D << p.block_shift, window = 32 / ppt;  // tiles of 32 pages
-      Ring<C::NC> cr;
-      int tile = 0;
-      bool ok = true;
-      Item it;
-      while (ok && take_item(it)) {
-        const int pages = cache8::pages_of(it.len, p.block_shift), end = it.k0 + it.tiles;
-        auto load_pages = [&](int kt) {  // lane i: page i of the window at tile kt, -1: none
-          return kt + lane / ppt < end && kt * ppt + lane < pages
-                     ? p.table[static_cast<size_t>(it.b) * p.table_cols + kt * ppt + lane]
-                     : -1;
-        };
-        auto load_scales = [&](int& page) {  // (a page out of range is reported with K's)
-          if (page < 0 || page >= p.num_blocks) page = -1;
-          return page >= 0 ? p.v_scale[static_cast<size_t>(page) * p.Hk + it.hk] : 0.f;
-        };
-        int cur = load_pages(it.k0);
-        float scale = load_scales(cur);
-        for (int k0 = it.k0; ok && k0 < end; k0 += window) {
-          int next = load_pages(min(k0 + window, end));
-          float next_scale = 0.f;
-          for (int i = 0; i < window && k0 + i < end; ++i, ++tile) {
-            const int from = (i * ppt + lane) & 31;
-            const int page = __shfl_sync(0xffffffffu, cur, from);
-            const float vs = __shfl_sync(0xffffffffu, scale, from);
-            const bool mine = lane < ppt && page >= 0;  // (a page out of range reads as zeros: its factor is 0)
-            if (tile >= C::NC) ok = wait_bounded(bar(C::B_CEMPTY + cr.i), cr.phase ^ 1, abort_flag, p.err, p.timeout_ns);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * page_bytes;
-            if (lane < C::MAX_PPT)
-              reinterpret_cast<uint2*>(smem + C::OFF_VF)[cr.i * C::MAX_PPT + lane] =
-                  mine ? scale_factors(vs) : make_uint2(0u, kOne2);
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(bar(C::B_CFULL + cr.i), bytes);
-            __syncwarp();
-            if (mine)
-              bulk_load(sb + C::OFF_C + cr.i * C::CODE_BYTES + lane * page_bytes,
-                        p.v_codes + (static_cast<size_t>(page) * p.Hk + it.hk) * page_bytes, page_bytes,
-                        bar(C::B_CFULL + cr.i));
-            cr.step();
-            if (i == 0) next_scale = load_scales(next);
-          }
-          cur = next;
-          scale = next_scale;
-        }
-      }
-      // Every copy issued lands before the CTA may exit, whoever aborted.
-      for (int s = 0; s < C::NC && s < tile; ++s)
-        wait_drain(bar(C::B_CFULL + s), ((tile - 1 - s) / C::NC) & 1, p.err, p.timeout_ns);
-    } else if (warp == C::MMA_WARP) {
-      // ------------------------------------------------------------ MMA
-      // The tensor core's queue holds some 190 cycles of products, and a wait for what
-      // is there already, or a commit, costs this thread 50 to 100: each stands between
-      // two batches of products, none beside another where that can be had.  (All waits
-      // of a tile before its products: 880 us on 8192 rows over 32768 keys; a thread for
-      // each row tile, whose products then alternate on the tensor core: 1064.)
-      constexpr uint32_t idesc_s = idesc_e4m3(128, 128, false);
-      constexpr uint32_t idesc_o = idesc_bf16(128, D, false, true);
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      const uint64_t dQ0 = sdesc8<D>(sb + C::OFF_Q, 16, 16 * D);
-      const uint64_t dK0 = sdesc8<D>(sb + C::OFF_K, 16);
-      const uint64_t dV0 = sdesc_sw128(sb + C::OFF_V, C::BLK_BYTES, 1024);
-      auto issue_s = [&](int t, int ks) {
-        const uint64_t dQ = sdesc_add(dQ0, t * C::TILE_BYTES), dK = sdesc_add(dK0, ks * C::CODE_BYTES);
-#pragma unroll
-        for (int term = 0; term < 2; ++term)
-#pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk)
-            mma_e4m3(tm + C::S_COL(t), sdesc_add(dQ, term * 8 * D + kk * 32), sdesc_add(dK, kk * 32), idesc_s,
-                     term + kk > 0);
-      };
-      auto issue_pv = [&](int t, int vs, bool acc) {
-        const uint64_t dV = sdesc_add(dV0, vs * C::TILE_BYTES);
-#pragma unroll(C::PV_UNROLL)
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          mma_ts(tm + C::O_COL(t), tm + C::S_COL(t) + kk * 8, sdesc_add(dV, kk * 2048), idesc_o,
-                 (acc || kk > 0) ? 1u : 0u);
-      };
-      bool ok = true;
-      auto wait = [&](int i, int phase) {  // (the whole warp, which stays together)
-        ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        return ok;
-      };
-      Ring<C::NK> kr;                        // the next tile of K, of V
-      Ring<C::NV> vr;
-      uint32_t half_phases = 0;  // bit t: of half t's items, bit 2 + t: of its P tiles
-      auto wait_half = [&](int b, int t, int bit) {
-        const int ph = (half_phases >> (bit + t)) & 1;
-        half_phases ^= 1u << (bit + t);
-        return wait(b + t, ph);
-      };
-      auto wait_k = [&]() { return wait(C::B_KFULL + kr.i, kr.phase); };
-      auto wait_v = [&]() { return wait(C::B_VFULL + vr.i, vr.phase); };
-      auto take_s = [&](int t, bool free_k) {  // S of half t over the K that is next
-        tc_fence_after();
-        if (elect_one()) {
-          issue_s(t, kr.i);
-          tc_commit(bar(C::B_SFULL + t));
-          if (free_k) tc_commit(bar(C::B_KEMPTY + kr.i));
-        }
-      };
-      Item it;
-      while (ok && take_item(it)) {
-        const int tiles = __shfl_sync(0xffffffffu, it.tiles, 0);
-        const int cnt0 = __shfl_sync(0xffffffffu, it.cnt0, 0), cnt1 = __shfl_sync(0xffffffffu, it.cnt1, 0);
-        auto cnt = [&](int t) { return t ? cnt1 : cnt0; };
-        if (__shfl_sync(0xffffffffu, it.dual ? 1 : 0, 0) != 0) {
-          // The halves take the tiles in turn: K and V of each are free after its half.
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t) {
-            if (cnt(t) == 0) break;
-            if (!wait_k() || !wait_half(C::B_Q, t, 0)) break;
-            take_s(t, true);
-            kr.step();
-          }
-          for (int j = 0; ok && j < cnt0; ++j) {
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-              if (j >= cnt(t)) break;
-              if (!wait_v() || !wait_half(C::B_PFULL, t, 2)) break;
-              tc_fence_after();
-              if (elect_one()) {
-                issue_pv(t, vr.i, j > 0);
-                if (j + 1 == cnt(t)) tc_commit(bar(C::B_ODONE + t));
-                tc_commit(bar(C::B_VEMPTY + vr.i));
-              }
-              vr.step();
-              if (j + 1 < cnt(t)) {
-                if (!wait_k()) break;
-                take_s(t, true);
-                kr.step();
-              }
-            }
-          }
-          continue;
-        }
-        if (!wait_k()) break;
-#pragma unroll(C::HALF_UNROLL)
-        for (int t = 0; t < 2; ++t)
-          if (cnt(t) > 0 && wait_half(C::B_Q, t, 0)) take_s(t, false);
-        if (!ok) break;
-        if (elect_one()) tc_commit(bar(C::B_KEMPTY + kr.i));
-        kr.step();
-        wait_v();
-        for (int j = 0; ok && j < tiles; ++j) {
-          const bool more = j + 1 < tiles;
-#pragma unroll(C::HALF_UNROLL)
-          for (int t = 0; t < 2; ++t) {
-            if (j < cnt(t) && wait_half(C::B_PFULL, t, 2)) {
-              tc_fence_after();
-              if (elect_one()) {
-                issue_pv(t, vr.i, j > 0);
-                if (j + 1 == cnt(t)) tc_commit(bar(C::B_ODONE + t));
-              }
-            }
-            if (!ok) break;
-            if (t == 0) {
-              if (more && !wait_k()) break;
-            } else {
-              if (elect_one()) tc_commit(bar(C::B_VEMPTY + vr.i));
-              vr.step();
-              if (more && !wait_v()) break;
-            }
-            if (j + 1 < cnt(t)) take_s(t, false);
-          }
-          if (ok && more) {
-            if (elect_one()) tc_commit(bar(C::B_KEMPTY + kr.i));
-            kr.step();
-          }
-        }
-      }
-      // every MMA issued so far must finish before tensor memory is released
-      if (elect_one()) tc_commit(bar(C::B_DRAIN));
-      wait_drain(bar(C::B_DRAIN), 0, p.err, p.timeout_ns);
-    } else {
-      // ---------------------------------------------------------------- conversion
-      // A thread's 16-byte chunk of codes becomes two chunks of bf16; a warp takes 32
-      // chunks of consecutive rows, every fifth group of them.  The chunks of a
-      // quarter-warp lie in two rows, at d = 128 in the two halves of them: neither its
-      // reads nor its swizzled writes meet in a bank.
-      const int cw = warp < C::MMA_WARP ? warp - 9 : warp - 10;
-      constexpr int CPR = D / 16, ROWS = 32 / CPR, GROUPS = kKeys / ROWS;
-      int row0, chunk;  // within a group
-      if (D == 128) {
-        const int rb = (lane >> 2) & 1;
-        row0 = ((lane >> 4) & 1) * 2 + rb;
-        chunk = (lane & 3) + 4 * (((lane >> 3) & 1) ^ rb);
-      } else {
-        row0 = lane >> 2;
-        chunk = lane & 3;
-      }
-      const uint32_t in0 = row0 * D + chunk * 16;
-      const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES;
-      auto place = [&](int row, int half) -> uint32_t { return out0 + row * 128 + (((c0 + half) ^ (row & 7)) << 4); };
-      int tile = 0;
-      Ring<C::NC> cr;
-      Ring<C::NV> vr;
-      bool ok = true;
-      auto wait = [&](int i, int phase) {
-        ok = ok && wait_bounded(bar(i), phase & 1, abort_flag, p.err, p.timeout_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        return ok;
-      };
-      Item it;
-      while (ok && take_item(it)) {
-        for (int kt = it.k0; kt < it.k0 + it.tiles; ++kt, ++tile) {
-          const int held = cache8::tokens_from(it.len, kt, kKeys, 0);  // tokens of the tile, if fewer than its rows
-          const int st = cr.i, slot = vr.i;
-          if (!wait(C::B_CFULL + st, cr.phase)) break;
-          if (tile >= C::NV && !wait(C::B_VEMPTY + slot, vr.phase ^ 1)) break;
-          const uint8_t* codes = smem + C::OFF_C + st * C::CODE_BYTES + in0;
-          const uint2* factors = reinterpret_cast<const uint2*>(smem + C::OFF_VF) + st * C::MAX_PPT;
-          uint8_t* out = smem + C::OFF_V + slot * C::TILE_BYTES;
-          // (rolled: beside the softmax's code an unrolled loop costs instruction fetches)
-          uint4 next = *reinterpret_cast<const uint4*>(codes + cw * ROWS * D);
-#pragma unroll 1
-          for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
-            const uint4 now = next;
-            const int row = g * ROWS + row0;
-            const uint32_t f = factors[row >> p.block_shift].x;
-            if (g + C::CONVERT_WARPS < GROUPS)
-              next = *reinterpret_cast<const uint4*>(codes + (g + C::CONVERT_WARPS) * ROWS * D);
-            const uint32_t in[4] = {now.x, now.y, now.z, now.w};
-            uint32_t v[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              widen4(in[k], v[2 * k], v[2 * k + 1]);
-              v[2 * k] = mul_bf16x2(v[2 * k], f);
-              v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f);
-            }
-            *reinterpret_cast<uint4*>(out + place(row, 0)) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(out + place(row, 1)) = make_uint4(v[4], v[5], v[6], v[7]);
-          }
-          // Seldom: slots without a token, which may hold anything, become 0; a scale above
-          // 2^55, whose factor does not fit one bf16 number, is a second one.
-          if (held < kKeys || __any_sync(0xffffffffu, factors[lane % C::MAX_PPT].y != kOne2)) {
-#pragma unroll 1
-            for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
-              const int row = g * ROWS + row0;
-              const uint32_t f = factors[row >> p.block_shift].y;
-#pragma unroll 1
-              for (int half = 0; half < 2; ++half) {
-                uint4* at = reinterpret_cast<uint4*>(out + place(row, half));
-                const uint4 x = *at;
-                *at = row >= held ? make_uint4(0u, 0u, 0u, 0u)
-                                  : make_uint4(mul_bf16x2(x.x, f), mul_bf16x2(x.y, f), mul_bf16x2(x.z, f), mul_bf16x2(x.w, f));
-              }
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(C::B_CEMPTY + st));
-            mbar_arrive(bar(C::B_VFULL + slot));
-          }
-          cr.step();
-          vr.step();
-        }
-      }
     }
   }
 
