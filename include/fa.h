@@ -335,9 +335,9 @@ FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void
  * element enters its product with the codes as the sum of two e4m3 terms, off by at
  * most 2^-17 of its row's largest (rows below 2^-118: of 2^-118); a probability is
  * rounded to bf16, values are exact.  What slots behind a sequence's last token hold
- * does not matter; stored tokens must be finite (a value stored as NaN reads as ±480
- * scales), scales powers of two.  A row of queries that holds an infinity or NaN gets
- * NaN for its results, no other row does.  A page index out of range reads as a page
+ * does not matter; scales must be powers of two.  A row of queries that holds an
+ * infinity or NaN, or that sees a key or value stored as NaN, gets NaN for its
+ * results, no other row does.  A page index out of range reads as a page
  * of zeros, a length outside [0, min(max_seqlen, table_cols · block)] as the nearer
  * end of that range, and both are reported by fa_get_device_error as FA_ERR_PAGE, as
  * is a sequence with more than max_new new tokens.

@@ -321,7 +321,8 @@ def attention_chunk_cache8(q, cache: Cache8, block_table, cu_seqlens, seqlens, m
     fa_get_device_error).  causal: new token i of n sees keys
     j <= seqlens[b] - n + i.  Returns (o [T,H,d] bf16, lse [H,T]
     fp32); rows that see no key, and rows of no sequence (behind the last, in
-    front of the first), get o = 0, lse = -inf."""
+    front of the first), get o = 0, lse = -inf; rows that see a key or value
+    stored as NaN get NaN."""
     if stream is None and workspace is None:
         out = _binding.native().chunk_cache8(q, cache, block_table, cu_seqlens, seqlens, max_new, max_seqlen, causal, scale)
         if out is not None:

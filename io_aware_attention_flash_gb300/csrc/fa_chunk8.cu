@@ -76,7 +76,7 @@ struct ChunkCfg {
   static constexpr int OFF_C = OFF_K + NK * CODE_BYTES;
   static constexpr int OFF_KS = OFF_C + NC * CODE_BYTES;           // [NSC][pages] K's scales
   static constexpr int OFF_VF = OFF_KS + NSC * MAX_PPT * 4;        // [NC][pages] V's two factors, bf16 pairs
-  static constexpr int ITEM_INTS = 12;
+  static constexpr int ITEM_INTS = 16;
   static constexpr int OFF_ITEM = OFF_VF + NC * MAX_PPT * 8;
   static constexpr int OFF_SCAN = OFF_ITEM + NI * ITEM_INTS * 4;   // [3][16] sums, then what is found
   static constexpr int OFF_BAR = OFF_SCAN + 50 * 8;
@@ -106,11 +106,12 @@ struct ChunkCfg {
   static constexpr int REG_SOFTMAX = 192, REG_OTHER = 64;
   static_assert(2 * REG_SOFTMAX + 2 * REG_OTHER == 4 * 128, "the split takes what the launch gives");
   // How far the MMA warp's loops over the halves and the steps of P V are unrolled: at d = 64
-  // not at all, since the code that each scheduler fetches counts for more than the issue
-  // of these small products (2 to 3 % over drawn sizes each); at d = 128 rolled steps cost
-  // 703 -> 763 us on a long document, rolled halves 0.8 %.  Of dual items the halves' loop is
-  // rolled for both (1 % over drawn sizes).
-  static constexpr int HALF_UNROLL = D == 64 ? 1 : 2, PV_UNROLL = D == 64 ? 1 : kKeys / 16;
+  // hardly, since the code that each scheduler fetches counts for more than the issue of
+  // these small products (pieces of prompts 176 us with steps in pairs, 181 one by one, 189
+  // unrolled, 204 with the halves unrolled); at d = 128 rolled steps cost 703 -> 763 us on a
+  // long document, rolled halves 0.8 %.  Of dual items the halves' loop is rolled for both (1 %
+  // over drawn sizes).
+  static constexpr int HALF_UNROLL = D == 64 ? 1 : 2, PV_UNROLL = D == 64 ? 2 : kKeys / 16;
   static constexpr uint32_t TMEM_COLS = 512;
   __host__ __device__ static constexpr uint32_t S_COL(int t) { return t * 128; }
   __host__ __device__ static constexpr uint32_t O_COL(int t) { return 256 + t * D; }
@@ -159,10 +160,19 @@ __device__ __forceinline__ bool chunk_seq(const Chunk8Params& p, int b, int& tok
 // Four codes to bf16 by their bits: sign, and exponent and mantissa four places
 // down, which reads as the value times 2^-120 (a subnormal code as a subnormal).
 // The first word holds elements 0 and 2, the second 1 and 3: O's dimensions change
-// places again at the end.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& even, uint32_t& odd) {
-  odd = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
-  even = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
+// places again at the end.  (The search for NaN is one instruction more a word; of all codes
+// again, byte by byte, it was five halves of one: 2 to 4 % of the attention.)
+// `top` keeps the largest magnitude (of each half's): NaN, 0x7f, comes out as 480, above all
+// numbers' bits.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& even, uint32_t& odd, uint32_t& top) {
+  const uint32_t o = (w >> 4) & 0x07f007f0u, e = (w << 4) & 0x07f007f0u;
+  odd = o | (w & 0x80008000u);
+  even = e | ((w << 8) & 0x80008000u);
+  top = __vimax3_u16x2(top, o, e);
+}
+__device__ __forceinline__ bool nan_among(uint32_t top) { return (top & 0xffffu) == 0x07f0u || (top >> 16) == 0x07f0u; }
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -170,6 +180,9 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 constexpr uint32_t kOne2 = 0x3f803f80u;
+// Bit 7 of each byte: whether that code of four is NaN.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return (w & 0x7f7f7f7fu) + 0x01010101u; }
+constexpr int kNoKey = 0x7fffffff;  // behind every key
 // V is kept 2^-kVShift times its value, so that O, up to 2^40 times the largest value
 // while it is summed, does not leave fp32; the least of a value's codes, 2^-9 · 2^-64,
 // stays a normal bf16 number.
@@ -393,7 +406,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     // An item's fields are read from shared memory where they are needed, which saves the
     // tile loop their registers.
     uint32_t item = 0;
-    enum { kHk = 1, kRb, kK0, kTiles, kN, kLen, kTok0, kCnt0, kCnt1, kSlot, kDual };
+    enum { kHk = 1, kRb, kK0, kTiles, kN, kLen, kTok0, kCnt0, kCnt1, kSlot, kDual, kNan };
     auto field = [&](int i) {
       int v;
       asm volatile("ld.shared.s32 %0, [%1];" : "=r"(v) : "r"(item + 4 * i));
@@ -688,6 +701,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       const int first = first_row(), rows = all_rows(), hk = field(kHk), tok0 = field(kTok0), slot = field(kSlot);
       const bool exists = first + r < rows;
       const int tok = (first + r) / p.G, g = first + r - tok * p.G;
+      // a row that sees a value stored as NaN (the products have taken it for a number)
+      if (const int key = field(kNan); key != kNoKey && chunk8::visible(field(kLen), field(kN), tok, p.causal) > key)
+        l = CUDART_NAN_F;
       auto load_o = [&](int c0, uint32_t (&o)[32]) {  // 32 columns of O
         tmem_ld32(tO + c0, o);
         if (join) {
@@ -914,6 +930,12 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       const uint32_t in0 = row0 * D + chunk * 16;
       const uint32_t c0 = 2 * (chunk % 4), out0 = (2 * chunk / 8) * C::BLK_BYTES;
       auto place = [&](int row, int half) -> uint32_t { return out0 + row * 128 + (((c0 + half) ^ (row & 7)) << 4); };
+      // From a group of the warp's to its next the chunk's place moves by STEP, and its row's
+      // last three bits, which the swizzle takes, change by a half where a group has four rows;
+      // the second chunk's place is the first's with another lowest bit.
+      constexpr uint32_t STEP = C::CONVERT_WARPS * ROWS * 128, FLIP = ROWS == 4 ? 64 : 0;
+      static_assert(C::CONVERT_WARPS % 2 == 1 && (ROWS == 4 || ROWS == 8), "rows mod 8 from group to group");
+      const uint32_t place0 = place(cw * ROWS + row0, 0);
       int tile = 0;
       Ring<C::NC> cr;
       Ring<C::NV> vr;
@@ -925,6 +947,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
       };
       Item it;
       while (ok && take_item(it)) {
+        int* first_nan = reinterpret_cast<int*>(smem + C::OFF_ITEM + (items - 1) % C::NI * (C::ITEM_INTS * 4)) + 12;
         for (int kt = it.k0; kt < it.k0 + it.tiles; ++kt, ++tile) {
           const int held = cache8::tokens_from(it.len, kt, kKeys, 0);  // tokens of the tile, if fewer than its rows
           const int st = cr.i, slot = vr.i;
@@ -935,31 +958,37 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           uint8_t* out = smem + C::OFF_V + slot * C::TILE_BYTES;
           // (rolled: beside the softmax's code an unrolled loop costs instruction fetches)
           uint4 next = *reinterpret_cast<const uint4*>(codes + cw * ROWS * D);
+          uint32_t top = 0, at = sb + C::OFF_V + slot * C::TILE_BYTES + place0;
 #pragma unroll 1
-          for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
+          for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS, at = (at + STEP) ^ FLIP) {
             const uint4 now = next;
-            const int row = g * ROWS + row0;
-            const uint32_t f = factors[row >> p.block_shift].x;
+            const uint32_t f = factors[g * ROWS >> p.block_shift].x;  // (a group lies in one page)
             if (g + C::CONVERT_WARPS < GROUPS)
               next = *reinterpret_cast<const uint4*>(codes + (g + C::CONVERT_WARPS) * ROWS * D);
             const uint32_t in[4] = {now.x, now.y, now.z, now.w};
             uint32_t v[8];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              widen4(in[k], v[2 * k], v[2 * k + 1]);
+              widen4(in[k], v[2 * k], v[2 * k + 1], top);
               v[2 * k] = mul_bf16x2(v[2 * k], f);
               v[2 * k + 1] = mul_bf16x2(v[2 * k + 1], f);
             }
-            *reinterpret_cast<uint4*>(out + place(row, 0)) = make_uint4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<uint4*>(out + place(row, 1)) = make_uint4(v[4], v[5], v[6], v[7]);
+            st_shared_v4(at, v[0], v[1], v[2], v[3]);
+            st_shared_v4(at ^ 16u, v[4], v[5], v[6], v[7]);
           }
           // Seldom: slots without a token, which may hold anything, become 0; a scale above
-          // 2^55, whose factor does not fit one bf16 number, is a second one.
-          if (held < kKeys || __any_sync(0xffffffffu, factors[lane % C::MAX_PPT].y != kOne2)) {
+          // 2^55, whose factor does not fit one bf16 number, is a second one; of tokens with a
+          // value stored as NaN the first is noted in the item (P of rows that do not see it is
+          // 0, which a NaN in the product would not leave so).
+          if (held < kKeys || __any_sync(0xffffffffu, factors[lane % C::MAX_PPT].y != kOne2 || nan_among(top))) {
 #pragma unroll 1
             for (int g = cw; g < GROUPS; g += C::CONVERT_WARPS) {
               const int row = g * ROWS + row0;
               const uint32_t f = factors[row >> p.block_shift].y;
+              const uint4 c = *reinterpret_cast<const uint4*>(codes + g * ROWS * D);
+              if (((nan_codes(c.x) | nan_codes(c.y) | nan_codes(c.z) | nan_codes(c.w)) & 0x80808080u) && row < held &&
+                  factors[row >> p.block_shift].x != 0)  // (of a page out of range: what was here before)
+                atomicMin(first_nan, kt * kKeys + row);
 #pragma unroll 1
               for (int half = 0; half < 2; ++half) {
                 uint4* at = reinterpret_cast<uint4*>(out + place(row, half));
@@ -1138,6 +1167,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
           dst[0] = make_int4(u.b, u.hk, u.rb, u.k0);
           dst[1] = make_int4(u.tiles > 0 ? u.k1 - u.k0 : 0, u.n, u.len, u.tok0);
           dst[2] = make_int4(cnt0, cnt1, slot, u.tiles > 0 && u.dual);
+          dst[3] = make_int4(kNoKey, 0, 0, 0);
           mbar_arrive(bar(C::B_IFULL + s));
         }
         ++published;

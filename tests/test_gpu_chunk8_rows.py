@@ -130,3 +130,73 @@ def test_many_places_without_new_tokens(H, d, total, B):
     assert_no_device_error(fa)
     check(o, lse, q, cache, few, [n for n, _ in at.values()], [L for _, L in at.values()], d ** -0.5, True)
     assert not o[7:].any() and (lse[:, 7:] == -np.inf).all()
+
+
+@pytest.mark.parametrize("what", ["v", "k"])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("H,Hk,d,block,new,lens", [
+    (8, 2, 128, 16, [40, 1, 300, 9], [700, 513, 300, 5000]), (4, 1, 64, 64, [33, 600, 2], [64, 1500, 9000]),
+    (2, 2, 64, 16, [130, 3], [130, 384]), (16, 1, 128, 128, [20, 100], [3000, 260])])
+def test_stored_nan_reaches_the_rows_that_see_it(H, Hk, d, block, new, lens, causal, what):
+    """A key or value stored as NaN makes the results of the rows that see it NaN, and no
+    others'; NaN codes behind a sequence's last token reach none."""
+    fa = require_gpu()
+    G, T = H // Hk, sum(new)
+    clean, table, q = batch(fa, H, Hk, d, block, lens, T, seed=H + d)
+    cache = fa.Cache8(*(t.clone() for t in clean))
+    for b, L in enumerate(lens):
+        if L % block:
+            for c in cache[:2]:
+                c.view(torch.uint8)[int(table[b, L // block]), :, L % block:] = 0x7F
+    bad = torch.zeros(T, H, dtype=torch.bool, device="cuda")
+    first = 0
+    for b, (n, L) in enumerate(zip(new, lens)):
+        # the last token, one inside the new ones, one long before them, by head
+        places = [(0, L - 1, d - 1, 0x7F), (Hk - 1, max(0, L - n) + n // 3, 5, 0xFF)]
+        if b == 1:
+            places = [(Hk - 1, L // 7, 0, 0x7F)] if Hk > 1 else []
+        for hk, at, dim, code in places:
+            getattr(cache, what).view(torch.uint8)[int(table[b, at // block]), hk, at % block, dim] = code
+            seen = L - n + np.arange(n) + 1 if causal else np.full(n, L)
+            for i in np.flatnonzero(seen > at):
+                bad[first + i, hk * G:(hk + 1) * G] = True
+        first += n
+    args = (table.cuda(), i32(np.cumsum([0] + new).tolist()), i32(lens), max(new), max(lens), causal)
+    o, lse = fa.attention_chunk_cache8(q, cache, *args)
+    want, want_lse = fa.attention_chunk_cache8(q, clean, *args)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    assert bad.any() and not bad.all()
+    assert torch.isnan(o[bad]).all() and torch.isnan(lse.T[bad]).all()
+    o, lse = torch.where(bad[..., None], want, o), torch.where(bad.T, want_lse, lse)
+    check(o, lse, q, clean, table, new, lens, d ** -0.5, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_pages_out_of_range_beside_stored_nan(d):
+    """What a page out of range leaves in its place from tiles before it counts as zeros,
+    a NaN too."""
+    fa = require_gpu()
+    block, cols = 16, 60
+    cache = random_cache(fa, cols + 1, 1, block, d, seed=d)
+    cache.v.view(torch.uint8)[cols] = 0x7F
+    table = torch.arange(cols, dtype=torch.int32)[None].repeat(3, 1)
+    q = torch.randn(12, 2, d, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    clean = fa.Cache8(*(t.clone() for t in cache))
+    for c in clean[:2]:
+        c.view(torch.uint8)[cols] = 0
+    sent, read = table.clone(), table.clone()
+    sent[0, ::2] = read[0, ::2] = cols          # sequence 0: every other page all NaN
+    sent[1, 1::3], read[1, 1::3] = cols + 1, cols  # sequence 1: out of range
+    new, lens = [4, 4, 4], [900, 950, 960]
+    args = (i32([0, 4, 8, 12]), i32(lens), 4, 960, True)
+    o, lse = fa.attention_chunk_cache8(q, cache, sent.cuda(), *args)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == ERR_PAGE
+    assert torch.isnan(o[:4]).all() and torch.isfinite(o[4:]).all()
+    want = fa.attention_chunk_cache8(q, clean, read.cuda(), *args)
+    torch.cuda.synchronize()
+    assert_no_device_error(fa)
+    o[:4], lse[:, :4] = want[0][:4], want[1][:, :4]
+    clean.k_scale[cols] = clean.v_scale[cols] = 1.0
+    check(o, lse, q, clean, read, new, lens, d ** -0.5, True)
