@@ -931,7 +931,6 @@ FA_API fa_status fa_fwd_chunk_cache8(const void* q, const void* k_codes, const v
   p.ldq = ldq;
   p.o = static_cast<uint16_t*>(o);
   p.lse = lse;
-  p.k_codes = static_cast<const uint8_t*>(k_codes);
   p.v_codes = static_cast<const uint8_t*>(v_codes);
   p.k_scale = k_scale;
   p.v_scale = v_scale;

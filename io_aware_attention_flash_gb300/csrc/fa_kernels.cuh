@@ -215,7 +215,6 @@ struct Chunk8Params {
   long long ldq;
   uint16_t* o;            // bf16 [total, H, d]
   float* lse;             // fp32 [H, total]
-  const uint8_t* k_codes; // (read by tensor map)
   const uint8_t* v_codes;
   const float* k_scale;
   const float* v_scale;
