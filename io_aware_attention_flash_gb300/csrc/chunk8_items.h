@@ -71,9 +71,10 @@ FA_CHUNK_FN bool dual(int n, int G, int rb) { return n * G - rb * kRows <= kHalf
 // first, as many as its fixed cost is (kItemCost; less where a CTA has little more than
 // a tile: every one had better have a CTA of its own).  Measured: a tile takes 1.6 us, of
 // a dual item 1.1, an item 8 (at d = 64: 1.5, 0.8 and 6).  Sixteen sequences of 1 to 512
-// new tokens over 100 to 8,192 take 223 us with a cost of 14, 213 with 18, 219 with 22,
+// new tokens over 100 to 8,192 took 223 us with a cost of 14, 213 with 18, 219 with 22,
 // 227 with 26 (before the tile pass was shortened 259 with 10, 240 with 14, 231 with 18);
-// one long document takes the same with all.
+// one long document took the same with all.  (One batch at d = 128: for d = 64, where an item
+// costs less, and for other mixes the same number is taken.)
 constexpr int kMostUnits = 3, kItemCost = 18;
 // Where every tile can have a CTA of its own, all count the same, so that it has (counted
 // as two, each third tile of few rows shared its CTA with another: 15 heads of one tile

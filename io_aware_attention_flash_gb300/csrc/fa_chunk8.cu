@@ -27,13 +27,13 @@
 //              pages as fast as they land)
 //   12         tcgen05.mma issue
 //   others     conversion of V tiles: none on the scheduler (warp mod 4) that the MMA
-//              warp shares
+//              warp shares.  They note an item's first token with a value stored as NaN
 // The softmax is the forward kernel's: the reference of a row is the maximum of its
 // first tile and moves only where a tile's row sum reaches 2^40.
 //
-// Measured: 2,048 new tokens of 32 heads (8 of keys) over 32,768 at d = 128 in 700 us,
-// 1520 TFLOP/s, 81 % of the large product's rate; 16 mixed sequences at 980, pieces of
-// prompts at d = 64 at 580 TFLOP/s; 4 x 12 tokens over 32,768 in 83 us (3.2 TB/s).  Bound by a
+// Measured, a call: 2,048 new tokens of 32 heads (8 of keys) over 32,768 at d = 128 in 743
+// us, 1430 TFLOP/s, 76 % of the large product's rate; 16 mixed sequences at 965, pieces of
+// prompts at d = 64 at 583 TFLOP/s; 4 x 12 tokens over 32,768 in 85 us (3.2 TB/s).  Bound by a
 // softmax warp's way through its tile, some 450 instructions at four cycles each (fixed
 // latencies, instruction fetch) with the hand-overs around it: without the conversion, the
 // exponentials and three quarters of the products the first takes 2 to 4 % less.
@@ -380,9 +380,10 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NUM_THREADS, 1) fa_chunk8_kernel(
     // (Ahead of the other roles, and the long code that runs once an item, the items' with
     // K's copies, behind them: where the loops of a tile lie among one another decides how
     // often their instructions are fetched again.  With that between the softmax and the rest 16
-    // mixed sequences take 218 to 249 us, by what it holds, instead of 214, a long document 736 to
-    // 768 instead of 731, pieces of prompts of 64 heads at d = 64 173 to 176 instead of 177;
-    // with the softmax behind all others d = 64 takes 3 % longer over drawn sizes.)
+    // mixed sequences take 218 to 271 us, by what it holds, instead of 214 to 222, a long
+    // document 736 to 769 instead of 731 to 743, pieces of prompts of 64 heads at d = 64 173 to
+    // 206 instead of 176; with the softmax behind all others d = 64 takes 3 % longer over drawn
+    // sizes.)
     setmaxnreg_inc<C::REG_SOFTMAX>();
     const int t = warp / 4, wq = warp % 4, r = wq * 32 + lane;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16);

@@ -14,12 +14,15 @@
 // lies beside the nearest quarter goes to sincospif, so that the fraction's rounding to
 // fp32 costs the angle 2^-25 at most, no more than the sine's and the cosine's own (a
 // fraction of the whole turn: 2^-23, and some more keys get a neighbouring code).  One
-// sine and cosine serves a token's pair in all heads.
+// sine and cosine serves a token's pair in all heads, of the append's keys in those that a
+// block takes.
 //
 // Both kernels are bound by DRAM: each element is read once and written once.  Measured:
 // 16,421 tokens of 32 + 8 heads of 128 turned in 50 us (6.7 TB/s, 99 % of the copy
-// rate), 16 prompts of up to 4,096 of them with 8 heads of values appended in 122 us (6.25
-// TB/s); 64 single tokens in 6 us, a launch of dependent loads.
+// rate), 16 prompts of up to 4,096 of them with 8 heads of values appended in 124 us (6.2
+// TB/s) to pages of 16 tokens; 64 single tokens in 5.3 us, a launch of dependent loads.
+// Larger pages have fewer heads a block (8, 4, 2, 1 at d = 128), so that the keys' angles
+// are formed more often: the same prompts take 130, 141 and 182 us with pages of 32, 64 and 128.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -199,7 +202,7 @@ __global__ void __launch_bounds__(kTurnThreads) fa_rotary_kernel(const RotaryPar
 // Append to the cache
 // ----------------------------------------------------------------------------
 // The first blocks take a page's new tokens in some heads of K or of V, a group of
-// threads (a warp up to 64 units) each (page, head); the others turn the queries.  A
+// threads (a warp up to 128 units) each (page, head); the others turn the queries.  A
 // thread owns NU units, which stay in registers between the largest magnitude and the
 // rounding and are on their way while the block's groups form the angles together.
 // Keys are turned in 32 bits and rounded once, to their codes; values go the way of
