@@ -340,7 +340,7 @@ FA_API fa_status fa_cache8_store_rotary(const void* q, const void* k, const void
  * results, no other row does.  A page index out of range reads as a page
  * of zeros, a length outside [0, min(max_seqlen, table_cols · block)] as the nearer
  * end of that range, and both are reported by fa_get_device_error as FA_ERR_PAGE, as
- * is a sequence with more than max_new new tokens.
+ * is a sequence with more than max_new new tokens.  B is at most 2^26.
  * Results do not depend on the order in which CTAs run.  `workspace`: at least
  * fa_chunk_cache8_workspace_bytes() bytes (0 for arguments that the call rejects),
  * contents ignored; calls that may overlap need

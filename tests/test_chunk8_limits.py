@@ -1,7 +1,6 @@
 """The chunk attention's arithmetic at its limits, from the header that the kernel is
 compiled with, on the host under the undefined-behaviour sanitiser."""
 import os
-import random
 import shutil
 import subprocess
 
